@@ -289,7 +289,7 @@ def _plain(s):
         d = _values(*_quantize(dy, kind, t), kind)
         dx = _scaled(d @ _stored_values(s["w_t"], kind).t(), t, s["w_t"]["tensor_scale"]).bfloat16()
         d = _values(*_quantize(dy.t(), kind, t), kind)
-        return dx, _scaled(d @ _stored_values(s["x_t"], kind).t(), t, s["x_t"]["tensor_scale"])
+        return dx, _scaled(d @ _stored_values(s["x_t"], kind).t(), t, s["x_t"]["tensor_scale"]).bfloat16()
     if op == "swiglu":
         gate, up = s["gate"].float(), s["up"].float()
         h = gate / (1 + torch.exp(-gate)) * up
@@ -331,7 +331,7 @@ def _framework(s):
     if op == "linear_bwd":
         dy = s["dy"]
         d, d_t = hg.fp4_quant_dual(dy, kind, hg.fp4_tensor_scale(dy) if kind == hg.FP4_NV else None)
-        return hg.fp4_gemm_scaled(d, stored(s["w_t"])), hg.fp4_gemm_scaled(d_t, stored(s["x_t"]), out_dtype=torch.float32)
+        return hg.fp4_gemm_scaled(d, stored(s["w_t"])), hg.fp4_gemm_scaled(d_t, stored(s["x_t"]))
     if op == "swiglu":
         h, kept = hg.fp8_swiglu_ckpt(s["gate"], s["up"])
         return [_shown(q) for q in (h, kept.gate, kept.up)]
@@ -363,7 +363,7 @@ def work(case):
         m, n, k, kind = case["m"], case["n"], case["k"], case["kind"]
         if op == "linear":
             return {"bytes": 2 * m * k + _fp4_bytes(n, k, kind) + 2 * m * n, "flops": 2 * m * n * k}
-        return {"bytes": 2 * m * n + _fp4_bytes(k, m, kind) + _fp4_bytes(k, n, kind) + 2 * m * k + 4 * n * k, "flops": 4 * m * n * k}
+        return {"bytes": 2 * m * n + _fp4_bytes(k, m, kind) + _fp4_bytes(k, n, kind) + 2 * m * k + 2 * n * k, "flops": 4 * m * n * k}
     n = case["rows"] * case["cols"]
     if op == "swiglu":
         return {"bytes": 4 * n + 3 * n + 3 * n // 128, "flops": 0}
