@@ -19,6 +19,8 @@ Tensor-level API (same names as the C entry points):
   fp8_quant_token_f32s / fp8_quant_block128_f32s / fp8_gemm_scaled_f32s
                                                         the FP32-scale variant
   fp8hg_get_device_error(stream=None)
+  fp4_* and fp8_swiglu_ckpt*                            4-bit tensors and SwiGLU with 8-bit
+                                                        checkpoints (see lowbit.py)
 
 Scale arrays are allocated with their column count rounded up to a multiple
 of four (the GEMM reads scale bytes four at a time); ``QTensor.scales()``
@@ -579,3 +581,20 @@ def fp8hg_get_device_error(stream=None) -> int:
 
 def fp8hg_status_str(status: int) -> str:
     return lib().fp8hg_status_str(int(status)).decode()
+
+
+_LOWBIT = ("FP4_MX", "FP4_NV", "Fp4Tensor", "SwigluCkpt", "alloc_fp4", "fp4_tensor_scale",
+           "fp4_quant", "fp4_quant_dual", "fp4_dequant", "fp4_gemm_scaled", "fp4_linear",
+           "fp4_linear_workspace", "fp8_swiglu_ckpt", "fp8_swiglu_ckpt_bwd",
+           "fp8_swiglu_ckpt_bwd_q")
+
+
+def __getattr__(name):
+    # lowbit.py's tensors need torch at import time, which this module does
+    # not; its names are loaded on first use
+    if name in _LOWBIT:
+        from . import lowbit
+        for n in _LOWBIT:
+            globals()[n] = getattr(lowbit, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libfp8hg.so")
-SOURCES = ["api.cu", "quant.cu", "quant_dual.cu", "gemm.cu", "gemm_f32s.cu"]
+SOURCES = ["api.cu", "quant.cu", "quant_dual.cu", "gemm.cu", "gemm_f32s.cu", "lowbit_api.cu",
+           "fp4_quant.cu", "gemm_fp4.cu", "swiglu.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -31,7 +32,7 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "fp8hg.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

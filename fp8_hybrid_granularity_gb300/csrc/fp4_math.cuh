@@ -1,0 +1,123 @@
+// Block scales and casts of the 4-bit formats (E2M1 values).
+//
+// As in quant_math.cuh the amax of a block is an integer maximum over BF16
+// patterns.  MX scales are read off its exponent field.  NV scales take two
+// correctly rounded divisions and one E4M3 cast per block; an element's
+// quotient x / d, d = s * t, is x * (1/d) followed by one residual step
+// (q + (x - q d) (1/d), two fused multiply-adds), which leaves the error of
+// the quotient below one FP32 rounding: with t a power of two d has four
+// significant bits and x eight, so x / d either equals a midpoint of two E2M1
+// values or is farther from it than that error, and the cast is the nearest
+// value of the exact quotient.  (A plain multiply by 1/d breaks such ties at
+// random.)
+#pragma once
+#include <cstdint>
+
+#include "quant_math.cuh"
+
+namespace fp8hg {
+
+// Eight floats -> eight E2M1 codes (nearest even, saturating), the first in
+// the low four bits.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// Eight codes -> their values.
+__device__ __forceinline__ void e2m1x8_values(uint32_t w, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ptx::f16x2_to_f32(h[i], v[2 * i], v[2 * i + 1]);
+}
+
+// A scale byte's value (NaN for the byte of a non-finite block).
+template <bool NV>
+__device__ __forceinline__ float fp4_scale_value(uint32_t byte) {
+    if constexpr (NV) {
+        float lo, hi;
+        ptx::f16x2_to_f32(ptx::cvt_f16x2_e4m3x2(static_cast<uint16_t>(byte)), lo, hi);
+        return lo;
+    } else {
+        return byte == 0xFFu ? __uint_as_float(0x7FC00000u) : pow2f(static_cast<int>(byte) - 127);
+    }
+}
+
+template <bool NV>
+struct Fp4Scale {
+    uint32_t byte;
+    float mul;       // MX: 2^-e; NV: 1 / d
+    float d;         // NV: s * t
+    bool nan, sat;   // a non-finite block; NV: the E4M3 scale saturated
+    __device__ __forceinline__ Fp4Scale(uint32_t amax_bits, float t) {
+        nan = amax_bits >= 0x7F80u;
+        sat = false;
+        d = 0.0f;
+        mul = 0.0f;
+        if constexpr (NV) {
+            const float q = __fdiv_rn(__fdiv_rn(__uint_as_float(amax_bits << 16), 6.0f), t);
+            byte = nan ? 0x7Fu : ptx::cvt_e4m3x2(q, 0.0f) & 0xFFu;
+            if (!nan && byte != 0u) {
+                d = __fmul_rn(fp4_scale_value<true>(byte), t);
+                mul = __frcp_rn(d);
+                sat = q > 448.0f;
+            }
+        } else {
+            const int ef = static_cast<int>(amax_bits >> 7);
+            const int e = ef == 0 ? -127 : clamp_exp(ef - 129);
+            byte = nan ? 0xFFu : static_cast<uint32_t>(e + 127);
+            if (!nan) mul = pow2f(-e);
+        }
+    }
+    // Eight BF16 values (four words) -> eight codes.  Non-finite block: 0.
+    __device__ __forceinline__ uint32_t cast8(const uint32_t *w) const {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+        if constexpr (NV) {
+            if (sat) {   // keeps the quotient finite; all such values saturate
+                const float m = 8.0f * d;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -m), m);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // the sign is x's own: the residual of -0 is +0
+                const float q = __fmul_rn(v[i], mul);
+                v[i] = copysignf(__fmaf_rn(__fmaf_rn(-q, d, v[i]), mul, q), v[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], mul);
+        }
+        const uint32_t c = cvt_e2m1x8(v);
+        return nan ? 0u : c;
+    }
+};
+
+// Byte offset of (row, block j) in a scale array with `tiles` tiles along k.
+__device__ __forceinline__ int64_t fp4_scale_offset(int64_t row, int64_t j, int64_t tiles) {
+    const int r = static_cast<int>(row & 127);
+    return ((row >> 7) * tiles + (j >> 2)) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (j & 3);
+}
+
+}  // namespace fp8hg

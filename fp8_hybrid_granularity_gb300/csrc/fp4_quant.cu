@@ -1,0 +1,444 @@
+// 4-bit quantizer kernels: BF16 -> E2M1 codes and block scales, the tensor
+// scale, and back to values.  All are bound by HBM: 2 bytes read and about
+// 0.53 (MX) or 0.56 (NV) written per element and direction.
+//
+//  k_fp4_rows    along the rows: a thread takes 16 elements (an NV block, or
+//                half an MX block, whose other half is in the next lane), so
+//                nothing is exchanged but one shuffle for MX and the packing
+//                of four scale bytes into a word.
+//  k_fp4_tile    along the columns, or in both directions from one read: a
+//                128 x 128 tile per CTA.
+//  k_fp4_amax, k_fp4_tensor_scale   the tensor's scale.
+//  k_fp4_dequant values from codes and scales.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fp4_math.cuh"
+#include "lowbit.h"
+
+namespace fp8hg {
+
+namespace {
+
+// Sixteen BF16 values from column c0 of a row as eight words, zeros past the
+// last column.
+template <bool VEC>
+__device__ __forceinline__ void load16(const uint16_t *row, int64_t c0, int64_t cols,
+                                       uint32_t (&w)[8]) {
+    if (VEC && c0 + 16 <= cols) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(row + c0);
+        const uint4 a = __ldg(p), b = __ldg(p + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t c = c0 + 2 * i;
+            const uint32_t lo = c < cols ? __ldg(row + c) : 0u;
+            const uint32_t hi = c + 1 < cols ? __ldg(row + c + 1) : 0u;
+            w[i] = lo | (hi << 16);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t abs_max16(const uint32_t (&w)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    return max(m & 0xFFFFu, m >> 16);
+}
+
+// The low `n` bytes of eight code bytes to p (8-byte aligned).
+__device__ __forceinline__ void store_codes(uint8_t *p, uint32_t lo, uint32_t hi, int64_t n) {
+    if (n >= 8) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+    } else {
+        const uint64_t v = (static_cast<uint64_t>(hi) << 32) | lo;
+        for (int i = 0; i < n; ++i) p[i] = static_cast<uint8_t>(v >> (8 * i));
+    }
+}
+
+// Four neighbouring blocks' scale bytes (one per LPB lanes) into one word, in
+// the first of the 4 * LPB lanes.
+template <int LPB>
+__device__ __forceinline__ uint32_t gather_scales(uint32_t byte, int lane) {
+    uint32_t v = byte << (8 * ((lane / LPB) & 3));
+    v |= __shfl_xor_sync(0xFFFFFFFFu, v, LPB);
+    v |= __shfl_xor_sync(0xFFFFFFFFu, v, 2 * LPB);
+    return v;
+}
+
+// ------------------------------------------------------------- along the rows
+// Block: `segs` segments of 16 elements (a multiple of 16) by some rows, a
+// thread each; the segments cover k padded to 256, so that the padding's
+// scale bytes are written too.
+template <bool NV, bool VEC>
+__global__ void __launch_bounds__(256)
+    k_fp4_rows(const uint16_t *__restrict__ x, int64_t rows, int64_t cols, int64_t ld_x,
+               const float *__restrict__ ts, uint8_t *__restrict__ q, int64_t ld_q,
+               uint8_t *__restrict__ s, int64_t tiles, int segs, int total_segs) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int seg = blockIdx.y * segs + tid % segs;
+    const int rpb = blockDim.x / segs;
+    const float t = NV && ts ? __ldg(ts) : 1.0f;
+    const int64_t c0 = static_cast<int64_t>(seg) * 16;
+    constexpr int LPB = NV ? 1 : 2;
+    // every lane of the warp stays in the loop for the shuffles
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < rows;
+         r0 += static_cast<int64_t>(gridDim.x) * rpb) {
+        const int64_t r = r0 + tid / segs;
+        const bool in = tid / segs < rpb && r < rows && seg < total_segs;
+        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (in && c0 < cols) load16<VEC>(x + r * ld_x, c0, cols, w);
+        uint32_t m = abs_max16(w);
+        if (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        const Fp4Scale<NV> sc(m, t);
+        const uint32_t word = gather_scales<LPB>(sc.byte, lane);
+        if (!in) continue;
+        if (c0 < cols) {
+            const uint32_t lo = sc.cast8(w), hi = sc.cast8(w + 4);
+            store_codes(q + r * ld_q + c0 / 2, lo, hi, (cols - c0 + 1) / 2);
+        }
+        if (lane % (4 * LPB) == 0)
+            *reinterpret_cast<uint32_t *>(s + fp4_scale_offset(r, seg / LPB, tiles)) = word;
+    }
+}
+
+// ------------------------------------------- along the columns, or both ways
+// A CTA takes a tile of 128 rows x 128 columns.  Each thread loads 16
+// neighbouring elements of four rows, quantizes them along the row at once
+// (ROWS) and leaves them in shared memory; then each thread takes two
+// neighbouring columns over 32 rows (conflict-free 4-byte reads).  Codes of
+// the columns go through shared memory so that a column's 64 bytes leave as
+// whole sectors.  Scale tiles (128 rows x 4 blocks) are assembled in shared
+// memory as well.
+constexpr int kTile = 128;
+
+template <bool NV, bool VEC, bool ROWS>
+__global__ void __launch_bounds__(256)
+    k_fp4_tile(const uint16_t *__restrict__ x, int64_t rows, int64_t cols, int64_t ld_x,
+               const float *__restrict__ ts, uint8_t *__restrict__ q, int64_t ld_q,
+               uint8_t *__restrict__ s, int64_t tiles, uint8_t *__restrict__ qt, int64_t ld_qt,
+               uint8_t *__restrict__ st, int64_t tiles_t) {
+    constexpr int NT = NV ? 2 : 1;          // scale tiles of 4 blocks per 128 elements
+    constexpr int LPB = NV ? 1 : 2;
+    __shared__ __align__(16) uint8_t tile[kTile * 256];
+    __shared__ __align__(16) uint8_t codes[kTile * 64];
+    __shared__ __align__(16) uint8_t scales[2][NT * 512];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile;
+    const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTile;
+    const float t = NV && ts ? __ldg(ts) : 1.0f;
+    {
+        const int seg = tid & 7;
+        const int64_t c0 = k0 + seg * 16;
+        uint32_t w[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = r0 + (tid >> 3) + i * 32;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[i][j] = 0;
+            if (r < rows && c0 < cols) load16<VEC>(x + r * ld_x, c0, cols, w[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int rr = (tid >> 3) + i * 32;
+            const int64_t r = r0 + rr;
+            // 16-byte pieces 2 seg and 2 seg + 1, swapped in the row's upper
+            // half so that eight lanes' writes fall into different banks
+            uint4 *row = reinterpret_cast<uint4 *>(tile + rr * 256);
+            row[(2 * seg) ^ (seg >> 2)] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+            row[(2 * seg + 1) ^ (seg >> 2)] = make_uint4(w[i][4], w[i][5], w[i][6], w[i][7]);
+            if constexpr (ROWS) {
+                uint32_t m = abs_max16(w[i]);
+                if (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                const Fp4Scale<NV> sc(m, t);
+                const uint32_t word = gather_scales<LPB>(sc.byte, lane);
+                if (lane % (4 * LPB) == 0)
+                    *reinterpret_cast<uint32_t *>(scales[0] + (seg / (4 * LPB)) * 512 +
+                                                  (rr & 31) * 16 + (rr >> 5) * 4) = word;
+                if (r < rows && c0 < cols) {
+                    const uint32_t lo = sc.cast8(w[i]), hi = sc.cast8(w[i] + 4);
+                    store_codes(q + r * ld_q + c0 / 2, lo, hi, (cols - c0 + 1) / 2);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    {
+        // columns 2p, 2p + 1, rows 32 b .. 32 b + 31
+        const int p = tid & 63, b = tid >> 6;
+        const int piece = (p >> 2) ^ (p >> 5);   // the 16-byte piece, as swapped above
+        const uint8_t *src = tile + b * 32 * 256 + piece * 16 + (p & 3) * 4;
+        uint32_t v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = *reinterpret_cast<const uint32_t *>(src + i * 256);
+        uint32_t m[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m[i >> 4] = __vmaxu2(m[i >> 4], v[i] & 0x7FFF7FFFu);
+        if (!NV) m[0] = m[1] = __vmaxu2(m[0], m[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t c[4];
+            const int col = 2 * p + h;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                const Fp4Scale<NV> sc(h ? m[part] >> 16 : m[part] & 0xFFFFu, t);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = part * 16 + half * 8 + 2 * i;
+                        w[i] = h ? __byte_perm(v[at], v[at + 1], 0x7632)
+                                 : __byte_perm(v[at], v[at + 1], 0x5410);
+                    }
+                    c[part * 2 + half] = sc.cast8(w);
+                }
+                // block index along the rows within the tile
+                if (NV || part == 0) {
+                    const int j = NV ? 2 * b + part : b;
+                    scales[1][(j >> 2) * 512 + (col & 31) * 16 + (col >> 5) * 4 + (j & 3)] =
+                        static_cast<uint8_t>(sc.byte);
+                }
+            }
+            *reinterpret_cast<uint4 *>(codes + col * 64 + ((b ^ (p & 3)) << 4)) =
+                make_uint4(c[0], c[1], c[2], c[3]);
+        }
+    }
+    __syncthreads();
+    // columns' codes: four lanes write one column's 64 bytes
+    {
+        const int64_t bytes = (rows + 1) / 2;   // of a whole column
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int idx = i * 256 + tid, col = idx >> 2, b = idx & 3;
+            const int64_t at = r0 / 2 + b * 16;
+            if (k0 + col >= cols || at >= bytes) continue;
+            const uint4 v = *reinterpret_cast<const uint4 *>(codes + col * 64 +
+                                                             ((b ^ ((col >> 1) & 3)) << 4));
+            uint8_t *d = qt + (k0 + col) * ld_qt + at;
+            if (at + 16 <= bytes) {
+                *reinterpret_cast<uint4 *>(d) = v;
+            } else {
+                store_codes(d, v.x, v.y, bytes - at);
+                if (bytes - at > 8) store_codes(d + 8, v.z, v.w, bytes - at - 8);
+            }
+        }
+    }
+    // scale tiles: 32 uint4 each; a tile of the padding along k has only zeros
+    // (this kernel's tile then lies past the tensor) and is written too
+    if (tid < 32 * NT) {
+        if (ROWS && r0 < rows)
+            reinterpret_cast<uint4 *>(s + ((r0 >> 7) * tiles + (k0 >> 7) * NT) * 512)[tid] =
+                reinterpret_cast<const uint4 *>(scales[0])[tid];
+    } else if (tid >= 64 && tid < 64 + 32 * NT) {
+        if (k0 < cols)
+            reinterpret_cast<uint4 *>(st + ((k0 >> 7) * tiles_t + (r0 >> 7) * NT) * 512)[tid - 64] =
+                reinterpret_cast<const uint4 *>(scales[1])[tid - 64];
+    }
+}
+
+// ------------------------------------------------------------- tensor scale
+constexpr int kAmaxBlocks = 608;
+
+// Largest finite |x| pattern per CTA.
+template <bool VEC>
+__global__ void __launch_bounds__(512)
+    k_fp4_amax(const uint16_t *__restrict__ x, int64_t rows, int64_t segs, int64_t cols,
+               int64_t ld_x, uint32_t *__restrict__ part) {
+    __shared__ uint32_t red[16];
+    uint32_t m = 0;
+    // segments of 16 elements, rows and segments walked together
+    const int64_t n = rows * segs, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    int64_t r = i / segs, c = i % segs;
+    const int64_t dr = step / segs, dc = step % segs;
+    for (; i < n; i += step) {
+        uint32_t w[8];
+        load16<VEC>(x + r * ld_x, c * 16, cols, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t a = w[j] & 0x7FFF7FFFu;
+            m = __vmaxu2(m, a & ~__vcmpgeu2(a, 0x7F807F80u));
+        }
+        r += dr;
+        c += dc;
+        if (c >= segs) c -= segs, ++r;
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        m = threadIdx.x < blockDim.x / 32 ? red[threadIdx.x] : 0u;
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (threadIdx.x == 0) part[blockIdx.x] = m;
+    }
+}
+
+__global__ void __launch_bounds__(32)
+    k_fp4_tensor_scale(const uint32_t *__restrict__ part, int n, float *__restrict__ scale) {
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < n; i += 32) m = max(m, part[i]);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (threadIdx.x == 0) {
+        // 2688 = 1.3125 * 2^11, a mantissa field of 40: the power of two goes
+        // up by one when the amax's mantissa is above that
+        const int ef = static_cast<int>(m >> 7), mf = static_cast<int>(m & 0x7F);
+        const int e = ef - 127 - 11 + (mf > 40 ? 1 : 0);
+        *scale = m == 0 ? 1.0f : pow2f(max(e, -100));
+    }
+}
+
+// ------------------------------------------------------------------- values
+template <bool NV, bool FP32>
+__global__ void __launch_bounds__(256)
+    k_fp4_dequant(const uint8_t *__restrict__ q, const uint8_t *__restrict__ s,
+                  const float *__restrict__ ts, int64_t rows, int64_t k, int64_t ld, int64_t tiles,
+                  void *__restrict__ out, int64_t ld_out, bool vec, int64_t segs) {
+    const float t = NV && ts ? __ldg(ts) : 1.0f;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        for (int64_t g = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; g < segs;
+             g += static_cast<int64_t>(gridDim.y) * blockDim.x) {
+            const int64_t c0 = g * 16;
+            const int64_t left = k - c0;
+            uint32_t w[2] = {0, 0};
+            const uint8_t *src = q + r * ld + c0 / 2;
+            if (left >= 16) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+                w[0] = v.x, w[1] = v.y;
+            } else {
+                for (int i = 0; i < (left + 1) / 2; ++i)
+                    w[i >> 2] |= static_cast<uint32_t>(__ldg(src + i)) << (8 * (i & 3));
+            }
+            const float sc = fp4_scale_value<NV>(__ldg(s + fp4_scale_offset(r, NV ? g : g >> 1, tiles)));
+            float v[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float u[8];
+                e2m1x8_values(w[h], u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[8 * h + i] = u[i] * sc;
+                    if (NV) v[8 * h + i] *= t;
+                }
+            }
+            if constexpr (FP32) {
+                float *d = static_cast<float *>(out) + r * ld_out + c0;
+                if (vec && left >= 16) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<float4 *>(d)[i] =
+                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < left) d[i] = v[i];
+                }
+            } else {
+                uint16_t *d = static_cast<uint16_t *>(out) + r * ld_out + c0;
+                uint32_t p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = ptx::cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+                if (vec && left >= 16) {
+                    reinterpret_cast<uint4 *>(d)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+                    reinterpret_cast<uint4 *>(d)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < left) d[i] = static_cast<uint16_t>(p[i >> 1] >> (16 * (i & 1)));
+                }
+            }
+        }
+    }
+}
+
+bool vec_ok(const void *p, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
+}
+
+template <bool NV>
+cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
+    const int64_t total = (a.cols + 255) / 256 * 16;      // segments, k padded to 256
+    const int64_t chunks = (total + 255) / 256;
+    const int segs = static_cast<int>((total / 16 + chunks - 1) / chunks * 16);
+    const int rpb = 256 / segs;
+    const int threads = (segs * rpb + 31) / 32 * 32;
+    const int64_t rblocks = (a.rows + rpb - 1) / rpb;
+    const dim3 grid(static_cast<unsigned>(rblocks < 0x7FFFFFFF ? rblocks : 0x7FFFFFFF),
+                    static_cast<unsigned>((total + segs - 1) / segs));
+    const int64_t tiles = fp4_scale_tiles(a.cols, a.kind);
+    if (vec_ok(a.x, a.ld_x))
+        k_fp4_rows<NV, true><<<grid, threads, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
+                                                           a.ld_q, a.s, tiles, segs,
+                                                           static_cast<int>(total));
+    else
+        k_fp4_rows<NV, false><<<grid, threads, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
+                                                            a.ld_q, a.s, tiles, segs,
+                                                            static_cast<int>(total));
+    return cudaGetLastError();
+}
+
+template <bool NV, bool VEC>
+cudaError_t quant_tile(const Fp4QuantArgs &a, cudaStream_t stream) {
+    // tiles cover both directions' padding to 256
+    const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256 * 2),
+                    static_cast<unsigned>((a.rows + 255) / 256 * 2));
+    const int64_t tiles = fp4_scale_tiles(a.cols, a.kind), tiles_t = fp4_scale_tiles(a.rows, a.kind);
+    if (a.q)
+        k_fp4_tile<NV, VEC, true><<<grid, 256, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
+                                                            a.ld_q, a.s, tiles, a.qt, a.ld_qt, a.st,
+                                                            tiles_t);
+    else
+        k_fp4_tile<NV, VEC, false><<<grid, 256, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts,
+                                                             a.q, a.ld_q, a.s, tiles, a.qt, a.ld_qt,
+                                                             a.st, tiles_t);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t fp4_tensor_scale_ws_bytes() { return kAmaxBlocks * sizeof(uint32_t); }
+
+cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x,
+                                    float *scale, void *ws, cudaStream_t stream) {
+    const int64_t segs = (cols + 15) / 16, n = rows * segs;
+    int64_t blocks = (n + 511) / 512;
+    if (blocks > kAmaxBlocks) blocks = kAmaxBlocks;
+    uint32_t *part = static_cast<uint32_t *>(ws);
+    if (n > 0) {
+        const unsigned g = static_cast<unsigned>(blocks);
+        if (vec_ok(x, ld_x)) k_fp4_amax<true><<<g, 512, 0, stream>>>(x, rows, segs, cols, ld_x, part);
+        else k_fp4_amax<false><<<g, 512, 0, stream>>>(x, rows, segs, cols, ld_x, part);
+    }
+    k_fp4_tensor_scale<<<1, 32, 0, stream>>>(part, static_cast<int>(blocks), scale);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, cudaStream_t stream) {
+    const bool nv = a.kind == FP4_NV;
+    if (!a.qt) return nv ? quant_rows<true>(a, stream) : quant_rows<false>(a, stream);
+    if (vec_ok(a.x, a.ld_x))
+        return nv ? quant_tile<true, true>(a, stream) : quant_tile<false, true>(a, stream);
+    return nv ? quant_tile<true, false>(a, stream) : quant_tile<false, false>(a, stream);
+}
+
+cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, int64_t ld_out, int fp32,
+                               cudaStream_t stream) {
+    const int64_t segs = (a.k + 15) / 16, tiles = fp4_scale_tiles(a.k, a.kind);
+    const int threads = segs < 256 ? static_cast<int>((segs + 31) / 32 * 32) : 256;
+    const int64_t cb = (segs + threads - 1) / threads;
+    const dim3 grid(static_cast<unsigned>(a.rows < 0x7FFFFFFF ? a.rows : 0x7FFFFFFF),
+                    static_cast<unsigned>(cb < 65535 ? cb : 65535));
+    const bool vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ld_out % (fp32 ? 4 : 8) == 0;
+    auto go = [&](auto kern) {
+        kern<<<grid, threads, 0, stream>>>(a.codes, a.scale, a.ts, a.rows, a.k, a.ld, tiles, out,
+                                           ld_out, vec, segs);
+        return cudaGetLastError();
+    };
+    if (a.kind == FP4_NV) return fp32 ? go(k_fp4_dequant<true, true>) : go(k_fp4_dequant<true, false>);
+    return fp32 ? go(k_fp4_dequant<false, true>) : go(k_fp4_dequant<false, false>);
+}
+
+}  // namespace fp8hg

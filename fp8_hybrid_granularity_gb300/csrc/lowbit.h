@@ -1,0 +1,90 @@
+// Launchers of the 4-bit operators and of the SwiGLU with 8-bit checkpoints,
+// shared between the C-ABI layer (lowbit_api.cu) and the kernel files.
+// Arguments are validated by the caller; these only configure and launch.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "internal.h"
+
+namespace fp8hg {
+
+enum { FP4_MX = 0, FP4_NV = 1 };
+
+// Tiles (128 rows x 4 blocks) along k of a scale array: k padded to 256.
+inline int64_t fp4_scale_tiles(int64_t k, int kind) {
+    return (k + 255) / 256 * (kind == FP4_NV ? 4 : 2);
+}
+inline int64_t fp4_row_tiles(int64_t rows) { return (rows + 127) / 128; }
+
+size_t fp4_tensor_scale_ws_bytes();
+cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x,
+                                    float *scale, void *ws, cudaStream_t stream);
+
+struct Fp4QuantArgs {
+    const uint16_t *x;
+    int64_t rows, cols, ld_x;
+    int kind;
+    const float *ts;
+    uint8_t *q;              // along the rows, or null
+    int64_t ld_q;
+    uint8_t *s;
+    uint8_t *qt;             // along the columns, or null
+    int64_t ld_qt;
+    uint8_t *st;
+};
+cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, cudaStream_t stream);
+
+struct Fp4Operand {
+    const uint8_t *codes, *scale;
+    const float *ts;
+    int64_t rows, k, ld;
+    int kind;
+};
+cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, int64_t ld_out, int fp32,
+                               cudaStream_t stream);
+
+struct Fp4GemmArgs {
+    Fp4Operand a, b;
+    void *c;
+    int64_t ldc;
+    int out_fp32, accumulate;
+    uint64_t wait_limit_ns;
+    int inject_fault;
+    unsigned int *err;
+};
+// 0 on success, 1 if a tensor map could not be encoded, cudaError_t + 2 on a
+// launch failure.
+int launch_fp4_gemm(const Fp4GemmArgs &g, cudaStream_t stream);
+
+struct SwigluFwdArgs {
+    const uint16_t *gate, *up;
+    int64_t rows, cols, ld_in;
+    int fmt_h, fmt;
+    uint8_t *h, *hs;
+    int64_t ld_h, ld_hs;
+    uint8_t *gq, *gs, *uq, *us;  // the checkpoint, or all null
+    int64_t ld_q, ld_s;
+};
+cudaError_t launch_swiglu_fwd(const SwigluFwdArgs &a, cudaStream_t stream);
+
+struct SwigluCkpt {
+    const uint8_t *gq, *gs, *uq, *us;
+    int64_t rows, cols, ld_q, ld_s;
+    int fmt;
+};
+cudaError_t launch_swiglu_bwd(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, uint16_t *dg,
+                              uint16_t *du, int64_t ld_d, cudaStream_t stream);
+
+struct SwigluGrads {
+    uint8_t *q[2], *s[2];        // dgate, dup: 1x128 along the rows
+    uint8_t *qt[3], *st[3];      // dgate, dup, h: 1x128 along the tokens, transposed
+    int64_t ld_q, ld_s, ld_qt, ld_st;
+    int fmt, fmt_t, fmt_h;
+};
+cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c,
+                                const SwigluGrads &g, cudaStream_t stream);
+
+}  // namespace fp8hg

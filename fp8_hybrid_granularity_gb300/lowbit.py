@@ -1,0 +1,368 @@
+"""4-bit microscaled tensors and SwiGLU with 8-bit activation checkpoints.
+
+Python binding of ``include/fp8hg_lowbit.h`` (the same ``libfp8hg.so``); the
+package exports every name here.  As in the rest of the package, arguments are
+checked and marshalled and the CUDA kernels do all of the computation.
+
+  fp4_tensor_scale(x)                               -> float32 tensor of one element (FP4_NV)
+  fp4_quant(x, kind, tensor_scale, transpose=False) -> Fp4Tensor
+  fp4_quant_dual(x, kind, tensor_scale)             -> Fp4Tensor, Fp4Tensor^T (one read)
+  fp4_dequant(q, out_dtype=bf16)                    -> values
+  fp4_gemm_scaled(a, b, out=None, out_dtype=bf16, accumulate=False)
+  fp4_linear(x, w, tensor_scale)                    quantize x and multiply, one call
+  fp8_swiglu_ckpt(gate, up, checkpoint=True)        -> QTensor, SwigluCkpt
+  fp8_swiglu_ckpt_bwd(dh, ckpt)                     -> [rows, 2 cols] BF16, dgate next to dup
+  fp8_swiglu_ckpt_bwd_q(dh, ckpt)                   -> the same as FP8 operands in both
+                                                       directions, and h transposed
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import (E4M3, E5M2, GRAN_1x128, OUT_BF16, OUT_FP32, GemmOpts, QTensor, _check, _round4,
+               _stream)
+from . import lib as _lib
+
+FP4_MX, FP4_NV = 0, 1
+FP4_BLOCK = {FP4_MX: 32, FP4_NV: 16}
+
+
+class _Fp4Operand(ctypes.Structure):
+    """fp4hg_operand of the C header."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("tensor_scale", ctypes.c_void_p), ("rows", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("kind", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _Ckpt(ctypes.Structure):
+    """fp8hg_swiglu_ckpt of the C header."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("gate_q", "gate_s", "up_q", "up_s")] +
+                [(n, ctypes.c_int64) for n in ("rows", "cols", "ld_q", "ld_s")] +
+                [("fmt", ctypes.c_int32), ("reserved", ctypes.c_int32)])
+
+
+class _Grads(ctypes.Structure):
+    """fp8hg_swiglu_grads of the C header."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in
+                 ("dgate_q", "dup_q", "dgate_s", "dup_s", "dgate_qt", "dup_qt", "dgate_st",
+                  "dup_st", "h_qt", "h_st")] +
+                [(n, ctypes.c_int64) for n in ("ld_q", "ld_s", "ld_qt", "ld_st")] +
+                [(n, ctypes.c_int32) for n in ("fmt", "fmt_t", "fmt_h", "reserved")])
+
+
+_bound = None
+
+
+def _fns():
+    """The library with the argument types of this module's functions set."""
+    global _bound
+    if _bound is None:
+        f = _lib()
+        P, I64, I, Z = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+        f.fp4_scale_bytes.argtypes = [I64, I64, I]
+        f.fp4_scale_bytes.restype = Z
+        f.fp4_tensor_scale_workspace.argtypes = []
+        f.fp4_tensor_scale_workspace.restype = Z
+        f.fp4_tensor_scale.argtypes = [P, I64, I64, I64, P, P, Z, P]
+        f.fp4_quant.argtypes = [P, I64, I64, I64, I, P, P, I64, P, P, I64, P, P]
+        f.fp4_dequant.argtypes = [P, P, I64, I, P]
+        f.fp4_gemm_scaled.argtypes = [P, P, P, I64, I, I, P, P]
+        f.fp4_linear_workspace.argtypes = [I64, I64, I]
+        f.fp4_linear_workspace.restype = Z
+        f.fp4_linear.argtypes = [P, I64, I64, P, P, P, I64, I, P, Z, P, P]
+        f.fp8_swiglu_ckpt.argtypes = [P, P, I64, I64, I64, I, P, I64, P, I64, I, P, P, P, P, I64,
+                                      I64, P]
+        f.fp8_swiglu_ckpt_bwd.argtypes = [P, I64, P, P, P, I64, P]
+        f.fp8_swiglu_ckpt_bwd_q.argtypes = [P, I64, P, P, P]
+        _bound = f
+    return _bound
+
+
+def _check_matrix(x, what="x"):
+    if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 2 or (x.stride(1) != 1 and
+                                                                      x.shape[1] > 1):
+        raise ValueError(f"{what} must be a 2-D CUDA bfloat16 tensor with unit column stride")
+
+
+def _ld(x) -> int:
+    """Row stride; a tensor of one row or none may carry any."""
+    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+
+
+def _ts(t):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_cuda or t.numel() != 1:
+        raise ValueError("tensor_scale must be a CUDA float32 tensor of one element")
+    return t.data_ptr()
+
+
+def _out_kind(out) -> int:
+    if out.dtype == torch.bfloat16:
+        return OUT_BF16
+    if out.dtype == torch.float32:
+        return OUT_FP32
+    raise ValueError("out must be bfloat16 or float32")
+
+
+def _check_out(out, rows, cols):
+    if tuple(out.shape) != (rows, cols) or not out.is_cuda or (out.stride(1) != 1 and cols > 1):
+        raise ValueError(f"out must be a CUDA tensor [{rows}, {cols}] with unit column stride")
+
+
+def _opts(wait_limit_ns, inject_fault):
+    if not wait_limit_ns and not inject_fault:
+        return None
+    return ctypes.byref(GemmOpts(wait_limit_ns, inject_fault, 0))
+
+
+@dataclass
+class Fp4Tensor:
+    """A 4-bit tensor [rows, k]: packed codes [rows, ld >= ceil(k/2)] (ld a
+    multiple of 16), scale bytes in tiles (one flat tensor, see the C header),
+    and for FP4_NV the tensor's scale (None: 1)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    rows: int
+    k: int
+    kind: int
+    tensor_scale: Optional[torch.Tensor] = None
+
+    def operand(self) -> _Fp4Operand:
+        c = self.codes
+        return _Fp4Operand(c.data_ptr(), self.scale.data_ptr(), _ts(self.tensor_scale), self.rows,
+                           self.k, c.stride(0) if self.rows > 1 else max(c.stride(0), c.shape[1]),
+                           self.kind, 0)
+
+    def scales(self) -> torch.Tensor:
+        """The scale bytes as [rows, ceil(k / block)] (a copy)."""
+        n = -(-self.k // FP4_BLOCK[self.kind])
+        r = -(-self.rows // 128)
+        t = self.scale.view(r, -1, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(r * 128, -1)
+        return t[:self.rows, :n].contiguous()
+
+
+def alloc_fp4(rows: int, k: int, kind: int, tensor_scale=None, device="cuda") -> Fp4Tensor:
+    """Output buffers for fp4_quant (codes' rows padded to 16 bytes)."""
+    codes = torch.empty((rows, (k + 31) // 32 * 16), dtype=torch.uint8, device=device)
+    per = 512 * (4 if kind == FP4_NV else 2)
+    scale = torch.empty((rows + 127) // 128 * ((k + 255) // 256) * per, dtype=torch.uint8,
+                        device=device)
+    return Fp4Tensor(codes, scale, rows, k, kind, tensor_scale)
+
+
+def fp4_tensor_scale(x, out=None, stream=None):
+    """The FP4_NV scale of a tensor: the smallest power of two t with
+    amax <= 6 * 448 * t (1 for a tensor of zeros), on the device."""
+    _check_matrix(x)
+    f = _fns()
+    out = out if out is not None else torch.empty(1, dtype=torch.float32, device=x.device)
+    n = f.fp4_tensor_scale_workspace()
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _check(f.fp4_tensor_scale(x.data_ptr(), x.shape[0], x.shape[1], _ld(x), _ts(out), ws.data_ptr(),
+                              n, _stream(stream)), "fp4_tensor_scale")
+    return out
+
+
+def _quant(x, kind, tensor_scale, rows_out, cols_out, stream, what):
+    q, t = rows_out, cols_out
+    rc = _fns().fp4_quant(x.data_ptr(), x.shape[0], x.shape[1], _ld(x), kind, _ts(tensor_scale),
+                          q.codes.data_ptr() if q else None, q.operand().ld if q else 0,
+                          q.scale.data_ptr() if q else None,
+                          t.codes.data_ptr() if t else None, t.operand().ld if t else 0,
+                          t.scale.data_ptr() if t else None, _stream(stream))
+    _check(rc, what)
+
+
+def _check_fp4(q, rows, k, kind):
+    if (q.rows, q.k, q.kind) != (rows, k, kind):
+        raise ValueError(f"out must be a 4-bit tensor [{rows}, {k}] of kind {kind}")
+
+
+def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
+              out: Optional[Fp4Tensor] = None, stream=None) -> Fp4Tensor:
+    """BF16 [rows, cols] to 4 bits along the rows, or (transpose=True) along the
+    columns, written as [cols, rows]."""
+    _check_matrix(x)
+    rows, cols = (x.shape[1], x.shape[0]) if transpose else x.shape
+    if out is None:
+        out = alloc_fp4(rows, cols, kind, tensor_scale, x.device)
+    _check_fp4(out, rows, cols, kind)
+    out.tensor_scale = tensor_scale
+    _quant(x, kind, tensor_scale, None if transpose else out, out if transpose else None, stream,
+           "fp4_quant")
+    return out
+
+
+def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Tensor] = None,
+                   out_t: Optional[Fp4Tensor] = None, stream=None):
+    """fp4_quant along the rows and along the columns from one read of x."""
+    _check_matrix(x)
+    rows, cols = x.shape
+    out = out if out is not None else alloc_fp4(rows, cols, kind, tensor_scale, x.device)
+    out_t = out_t if out_t is not None else alloc_fp4(cols, rows, kind, tensor_scale, x.device)
+    _check_fp4(out, rows, cols, kind)
+    _check_fp4(out_t, cols, rows, kind)
+    out.tensor_scale = out_t.tensor_scale = tensor_scale
+    _quant(x, kind, tensor_scale, out, out_t, stream, "fp4_quant_dual")
+    return out, out_t
+
+
+def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None, stream=None):
+    """The values of a 4-bit tensor, [rows, k], BF16 or FP32."""
+    if out is None:
+        out = torch.empty((q.rows, q.k), dtype=out_dtype or torch.bfloat16, device=q.codes.device)
+    _check_out(out, q.rows, q.k)
+    op = q.operand()
+    _check(_fns().fp4_dequant(ctypes.byref(op), out.data_ptr(), _ld(out), _out_kind(out),
+                              _stream(stream)), "fp4_dequant")
+    return out
+
+
+def fp4_gemm_scaled(a: Fp4Tensor, b: Fp4Tensor, out=None, out_dtype=None, accumulate: bool = False,
+                    wait_limit_ns: int = 0, inject_fault: int = 0, stream=None):
+    """C = A B^T (or C += A B^T) on two 4-bit tensors of the same kind."""
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((a.rows, b.rows), dtype=out_dtype or torch.bfloat16,
+                          device=a.codes.device)
+    _check_out(out, a.rows, b.rows)
+    oa, ob = a.operand(), b.operand()
+    _check(_fns().fp4_gemm_scaled(ctypes.byref(oa), ctypes.byref(ob), out.data_ptr(), _ld(out),
+                                  _out_kind(out), 1 if accumulate else 0,
+                                  _opts(wait_limit_ns, inject_fault), _stream(stream)),
+           "fp4_gemm_scaled")
+    return out
+
+
+def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, workspace=None,
+               stream=None):
+    """y = x w^T: x [rows, k] BF16 is quantized like w and multiplied, in one
+    call.  workspace: optional uint8 tensor of fp4_linear_workspace(...)
+    bytes (allocated per call if None)."""
+    _check_matrix(x)
+    if x.shape[1] != w.k:
+        raise ValueError(f"x has {x.shape[1]} columns, w {w.k}")
+    rows = x.shape[0]
+    if out is None:
+        out = torch.empty((rows, w.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
+    _check_out(out, rows, w.rows)
+    f = _fns()
+    if workspace is None:
+        workspace = torch.empty(f.fp4_linear_workspace(rows, w.k, w.kind), dtype=torch.uint8,
+                                device=x.device)
+    ow = w.operand()
+    _check(f.fp4_linear(x.data_ptr(), rows, _ld(x), _ts(tensor_scale), ctypes.byref(ow),
+                        out.data_ptr(), _ld(out), _out_kind(out), workspace.data_ptr(),
+                        workspace.numel(), None, _stream(stream)), "fp4_linear")
+    return out
+
+
+def fp4_linear_workspace(rows: int, k: int, kind: int) -> int:
+    """Bytes of workspace that fp4_linear needs."""
+    return int(_fns().fp4_linear_workspace(rows, k, kind))
+
+
+# ------------------------------------------------- SwiGLU, 8-bit checkpoints
+@dataclass
+class SwigluCkpt:
+    """gate and up [rows, cols] as FP8 with one UE8M0 scale per 128 columns."""
+    gate: QTensor
+    up: QTensor
+
+
+def _groups(rows, cols, fmt, device, lead=1):
+    """[rows, lead * cols] codes and their 1x128 scales (rows padded to 16 bytes)."""
+    cols *= lead
+    q = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)
+    g = (cols + 127) // 128
+    s = torch.empty((rows, _round4(g)), dtype=torch.uint8, device=device)
+    return QTensor(q[:, :cols], s, fmt, GRAN_1x128, g)
+
+
+def _ld_codes(q) -> int:
+    """Row stride of codes that are padded to 16 bytes (any, for one row)."""
+    return q.stride(0) if q.shape[0] > 1 else max(q.stride(0), (q.shape[1] + 15) // 16 * 16)
+
+
+def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bool = True,
+                    stream=None):
+    """h = silu(gate) * up, quantized per 1x128 group (the down projection's A
+    operand), and gate and up quantized the same way for the backward pass.
+    gate and up may be the two halves of one tensor.  checkpoint=False
+    (inference) writes h alone and returns (h, None)."""
+    _check_matrix(gate, "gate")
+    _check_matrix(up, "up")
+    if gate.shape != up.shape or _ld(gate) != _ld(up):
+        raise ValueError("gate and up must have the same shape and row stride")
+    rows, cols = gate.shape
+    h = _groups(rows, cols, fmt_h, gate.device)
+    g = u = None
+    ptr = [None] * 4
+    ld_q = ld_s = 0
+    if checkpoint:
+        g, u = (_groups(rows, cols, fmt, gate.device) for _ in range(2))
+        ptr = [g.codes.data_ptr(), g.scale.data_ptr(), u.codes.data_ptr(), u.scale.data_ptr()]
+        ld_q, ld_s = _ld_codes(g.codes), g.scale.stride(0)
+    _check(_fns().fp8_swiglu_ckpt(gate.data_ptr(), up.data_ptr(), rows, cols, _ld(gate), fmt_h,
+                                  h.codes.data_ptr(), _ld_codes(h.codes), h.scale.data_ptr(),
+                                  h.scale.stride(0), fmt, *ptr, ld_q, ld_s, _stream(stream)),
+           "fp8_swiglu_ckpt")
+    return h, SwigluCkpt(g, u) if checkpoint else None
+
+
+def _ckpt(c: SwigluCkpt, dh) -> _Ckpt:
+    g, u = c.gate, c.up
+    _check_matrix(dh, "dh")
+    if g.gran != GRAN_1x128 or u.gran != GRAN_1x128 or g.fmt != u.fmt:
+        raise ValueError("a checkpoint has 1x128 scales and one format")
+    if g.codes.shape != dh.shape or u.codes.shape != dh.shape:
+        raise ValueError("dh and the checkpoint must have the same shape")
+    if (_ld_codes(g.codes) != _ld_codes(u.codes) or
+            (g.codes.shape[0] > 1 and g.scale.stride(0) != u.scale.stride(0))):
+        raise ValueError("gate's and up's codes and scales must have the same strides")
+    rows, cols = dh.shape
+    return _Ckpt(g.codes.data_ptr(), g.scale.data_ptr(), u.codes.data_ptr(), u.scale.data_ptr(),
+                 rows, cols, _ld_codes(g.codes), g.scale.stride(0), g.fmt, 0)
+
+
+def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None, stream=None):
+    """Gradients of gate and up from dh [rows, cols] and the checkpoint, BF16:
+    one [rows, 2 cols] tensor, dgate in the first half, dup in the second."""
+    c = _ckpt(ckpt, dh)
+    rows, cols = dh.shape
+    if out is None:
+        out = torch.empty((rows, 2 * cols), dtype=torch.bfloat16, device=dh.device)
+    _check_out(out, rows, 2 * cols)
+    _check_matrix(out, "out")
+    _check(_fns().fp8_swiglu_ckpt_bwd(dh.data_ptr(), _ld(dh), ctypes.byref(c), out.data_ptr(),
+                                      out.data_ptr() + 2 * cols, _ld(out), _stream(stream)),
+           "fp8_swiglu_ckpt_bwd")
+    return out
+
+
+def fp8_swiglu_ckpt_bwd_q(dh, ckpt: SwigluCkpt, fmt: int = E5M2, fmt_t: int = E5M2,
+                          fmt_h: int = E4M3, stream=None):
+    """The gradients as FP8 operands: ([rows, 2 cols] per 1x128 group, dgate next
+    to dup; the same transposed, [2 cols, rows], per 128 tokens; h rebuilt from
+    the checkpoint and transposed, [cols, rows], per 128 tokens).  rows and cols
+    must be multiples of 128."""
+    c = _ckpt(ckpt, dh)
+    rows, cols = dh.shape
+    dev = dh.device
+    d = _groups(rows, cols, fmt, dev, lead=2)
+    t = _groups(2 * cols, rows, fmt_t, dev)
+    h = _groups(cols, rows, fmt_h, dev)
+    dq, ds, tq, tl = d.codes.data_ptr(), d.scale.data_ptr(), t.codes.data_ptr(), t.scale.data_ptr()
+    ld_qt, ld_st = t.codes.stride(0), t.scale.stride(0)
+    g = _Grads(dq, dq + cols, ds, ds + cols // 128, tq, tq + cols * ld_qt, tl, tl + cols * ld_st,
+               h.codes.data_ptr(), h.scale.data_ptr(), d.codes.stride(0), d.scale.stride(0), ld_qt,
+               ld_st, fmt, fmt_t, fmt_h, 0)
+    _check(_fns().fp8_swiglu_ckpt_bwd_q(dh.data_ptr(), _ld(dh), ctypes.byref(c), ctypes.byref(g),
+                                        _stream(stream)), "fp8_swiglu_ckpt_bwd_q")
+    return d, t, h
