@@ -360,3 +360,17 @@ def test_python_refusals(cuda_lib):
         fp8hg.fp4_gemm_scaled(w, stored(8, 64, NV, 1)[0])
     with pytest.raises(fp8hg.Fp8hgError):
         fp8hg.fp4_quant(x.bfloat16(), MX, torch.ones(1, device="cuda"))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n,k", [(4, 2000, 4096), (100, 400, 2048), (3000, 3000, 1024)])
+def test_product_timeout(cuda_lib, m, n, k, kind):
+    """A withheld copy and a short limit: the call returns, the status reads
+    TIMEOUT once, and the next call is right."""
+    a, va = stored(m, k, kind, 61)
+    b, vb = stored(n, k, kind, 62)
+    fp8hg.fp4_gemm_scaled(a, b, wait_limit_ns=20_000_000, inject_fault=1)
+    assert fp8hg.fp8hg_get_device_error() == 6
+    assert fp8hg.fp8hg_get_device_error() == 0
+    check_product(fp8hg.fp4_gemm_scaled(a, b), *product(va, vb), k)
+    assert fp8hg.fp8hg_get_device_error() == 0
