@@ -16,31 +16,11 @@
 
 #include "fp4_math.cuh"
 #include "lowbit.h"
+#include "ragged.cuh"
 
 namespace fp8hg {
 
 namespace {
-
-// Sixteen BF16 values from column c0 of a row as eight words, zeros past the
-// last column.
-template <bool VEC>
-__device__ __forceinline__ void load16(const uint16_t *row, int64_t c0, int64_t cols,
-                                       uint32_t (&w)[8]) {
-    if (VEC && c0 + 16 <= cols) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(row + c0);
-        const uint4 a = __ldg(p), b = __ldg(p + 1);
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t c = c0 + 2 * i;
-            const uint32_t lo = c < cols ? __ldg(row + c) : 0u;
-            const uint32_t hi = c + 1 < cols ? __ldg(row + c + 1) : 0u;
-            w[i] = lo | (hi << 16);
-        }
-    }
-}
 
 __device__ __forceinline__ uint32_t abs_max16(const uint32_t (&w)[8]) {
     uint32_t m = 0;
@@ -73,7 +53,7 @@ __device__ __forceinline__ uint32_t gather_scales(uint32_t byte, int lane) {
 // Block: `segs` segments of 16 elements (a multiple of 16) by some rows, a
 // thread each; the segments cover k padded to 256, so that the padding's
 // scale bytes are written too.
-template <bool NV, bool VEC>
+template <bool NV, bool WIDE>
 __global__ void __launch_bounds__(256)
     k_fp4_rows(const uint16_t *__restrict__ x, int64_t rows, int64_t cols, int64_t ld_x,
                const float *__restrict__ ts, uint8_t *__restrict__ q, int64_t ld_q,
@@ -90,7 +70,7 @@ __global__ void __launch_bounds__(256)
         const int64_t r = r0 + tid / segs;
         const bool in = tid / segs < rpb && r < rows && seg < total_segs;
         uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (in && c0 < cols) load16<VEC>(x + r * ld_x, c0, cols, w);
+        if (in && c0 < cols) ragged::load16<WIDE>(x + r * ld_x + c0, cols - c0, w);
         uint32_t m = abs_max16(w);
         if (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         const Fp4Scale<NV> sc(m, t);
@@ -115,7 +95,7 @@ __global__ void __launch_bounds__(256)
 // memory as well.
 constexpr int kTile = 128;
 
-template <bool NV, bool VEC, bool ROWS>
+template <bool NV, bool WIDE, bool ROWS>
 __global__ void __launch_bounds__(256)
     k_fp4_tile(const uint16_t *__restrict__ x, int64_t rows, int64_t cols, int64_t ld_x,
                const float *__restrict__ ts, uint8_t *__restrict__ q, int64_t ld_q,
@@ -139,7 +119,7 @@ __global__ void __launch_bounds__(256)
             const int64_t r = r0 + (tid >> 3) + i * 32;
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[i][j] = 0;
-            if (r < rows && c0 < cols) load16<VEC>(x + r * ld_x, c0, cols, w[i]);
+            if (r < rows && c0 < cols) ragged::load16<WIDE>(x + r * ld_x + c0, cols - c0, w[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -244,7 +224,7 @@ __global__ void __launch_bounds__(256)
 constexpr int kAmaxBlocks = 608;
 
 // Largest finite |x| pattern per CTA.
-template <bool VEC>
+template <bool WIDE>
 __global__ void __launch_bounds__(512)
     k_fp4_amax(const uint16_t *__restrict__ x, int64_t rows, int64_t segs, int64_t cols,
                int64_t ld_x, uint32_t *__restrict__ part) {
@@ -257,7 +237,7 @@ __global__ void __launch_bounds__(512)
     const int64_t dr = step / segs, dc = step % segs;
     for (; i < n; i += step) {
         uint32_t w[8];
-        load16<VEC>(x + r * ld_x, c * 16, cols, w);
+        ragged::load16<WIDE>(x + r * ld_x + c * 16, cols - c * 16, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t a = w[j] & 0x7FFF7FFFu;
@@ -292,28 +272,27 @@ __global__ void __launch_bounds__(32)
 }
 
 // ------------------------------------------------------------------- values
-template <bool NV, bool FP32>
+template <bool NV, bool FP32, bool WIDE>
 __global__ void __launch_bounds__(256)
     k_fp4_dequant(const uint8_t *__restrict__ q, const uint8_t *__restrict__ s,
                   const float *__restrict__ ts, int64_t rows, int64_t k, int64_t ld, int64_t tiles,
-                  void *__restrict__ out, int64_t ld_out, bool vec, int64_t segs) {
+                  void *__restrict__ out, int64_t ld_out, int segs) {
     const float t = NV && ts ? __ldg(ts) : 1.0f;
+    const int g = blockIdx.y * blockDim.x + threadIdx.x;
+    const int64_t c0 = static_cast<int64_t>(g) * 16, left = k - c0;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        for (int64_t g = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; g < segs;
-             g += static_cast<int64_t>(gridDim.y) * blockDim.x) {
-            const int64_t c0 = g * 16;
-            const int64_t left = k - c0;
+        float v[16];
+        if (g < segs) {
             uint32_t w[2] = {0, 0};
             const uint8_t *src = q + r * ld + c0 / 2;
             if (left >= 16) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
-                w[0] = v.x, w[1] = v.y;
+                const uint2 p = __ldg(reinterpret_cast<const uint2 *>(src));
+                w[0] = p.x, w[1] = p.y;
             } else {
                 for (int i = 0; i < (left + 1) / 2; ++i)
                     w[i >> 2] |= static_cast<uint32_t>(__ldg(src + i)) << (8 * (i & 3));
             }
             const float sc = fp4_scale_value<NV>(__ldg(s + fp4_scale_offset(r, NV ? g : g >> 1, tiles)));
-            float v[16];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float u[8];
@@ -324,38 +303,27 @@ __global__ void __launch_bounds__(256)
                     if (NV) v[8 * h + i] *= t;
                 }
             }
-            if constexpr (FP32) {
-                float *d = static_cast<float *>(out) + r * ld_out + c0;
-                if (vec && left >= 16) {
+        }
+        if constexpr (FP32) {
+            if (g >= segs) continue;
+            float *d = static_cast<float *>(out) + r * ld_out + c0;
+            if (WIDE && left >= 16) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        reinterpret_cast<float4 *>(d)[i] =
-                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < left) d[i] = v[i];
-                }
+                for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<float4 *>(d)[i] =
+                        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             } else {
-                uint16_t *d = static_cast<uint16_t *>(out) + r * ld_out + c0;
-                uint32_t p[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = ptx::cvt_bf16x2(v[2 * i], v[2 * i + 1]);
-                if (vec && left >= 16) {
-                    reinterpret_cast<uint4 *>(d)[0] = make_uint4(p[0], p[1], p[2], p[3]);
-                    reinterpret_cast<uint4 *>(d)[1] = make_uint4(p[4], p[5], p[6], p[7]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < left) d[i] = static_cast<uint16_t>(p[i >> 1] >> (16 * (i & 1)));
-                }
+                for (int i = 0; i < 16; ++i)
+                    if (i < left) d[i] = v[i];
             }
+        } else {
+            uint32_t p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = g < segs ? ptx::cvt_bf16x2(v[2 * i], v[2 * i + 1]) : 0u;
+            ragged::store16<WIDE>(static_cast<uint16_t *>(out) + r * ld_out + c0, left, p);
         }
     }
-}
-
-bool vec_ok(const void *p, int64_t ld) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
 }
 
 template <bool NV>
@@ -369,7 +337,7 @@ cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(rblocks < 0x7FFFFFFF ? rblocks : 0x7FFFFFFF),
                     static_cast<unsigned>((total + segs - 1) / segs));
     const int64_t tiles = fp4_scale_tiles(a.cols, a.kind);
-    if (vec_ok(a.x, a.ld_x))
+    if (ragged::wide(a.x, a.ld_x))
         k_fp4_rows<NV, true><<<grid, threads, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
                                                            a.ld_q, a.s, tiles, segs,
                                                            static_cast<int>(total));
@@ -380,18 +348,18 @@ cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-template <bool NV, bool VEC>
+template <bool NV, bool WIDE>
 cudaError_t quant_tile(const Fp4QuantArgs &a, cudaStream_t stream) {
     // tiles cover both directions' padding to 256
     const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256 * 2),
                     static_cast<unsigned>((a.rows + 255) / 256 * 2));
     const int64_t tiles = fp4_scale_tiles(a.cols, a.kind), tiles_t = fp4_scale_tiles(a.rows, a.kind);
     if (a.q)
-        k_fp4_tile<NV, VEC, true><<<grid, 256, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
+        k_fp4_tile<NV, WIDE, true><<<grid, 256, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
                                                             a.ld_q, a.s, tiles, a.qt, a.ld_qt, a.st,
                                                             tiles_t);
     else
-        k_fp4_tile<NV, VEC, false><<<grid, 256, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts,
+        k_fp4_tile<NV, WIDE, false><<<grid, 256, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts,
                                                              a.q, a.ld_q, a.s, tiles, a.qt, a.ld_qt,
                                                              a.st, tiles_t);
     return cudaGetLastError();
@@ -409,7 +377,7 @@ cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t col
     uint32_t *part = static_cast<uint32_t *>(ws);
     if (n > 0) {
         const unsigned g = static_cast<unsigned>(blocks);
-        if (vec_ok(x, ld_x)) k_fp4_amax<true><<<g, 512, 0, stream>>>(x, rows, segs, cols, ld_x, part);
+        if (ragged::wide(x, ld_x)) k_fp4_amax<true><<<g, 512, 0, stream>>>(x, rows, segs, cols, ld_x, part);
         else k_fp4_amax<false><<<g, 512, 0, stream>>>(x, rows, segs, cols, ld_x, part);
     }
     k_fp4_tensor_scale<<<1, 32, 0, stream>>>(part, static_cast<int>(blocks), scale);
@@ -419,7 +387,7 @@ cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t col
 cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, cudaStream_t stream) {
     const bool nv = a.kind == FP4_NV;
     if (!a.qt) return nv ? quant_rows<true>(a, stream) : quant_rows<false>(a, stream);
-    if (vec_ok(a.x, a.ld_x))
+    if (ragged::wide(a.x, a.ld_x))
         return nv ? quant_tile<true, true>(a, stream) : quant_tile<false, true>(a, stream);
     return nv ? quant_tile<true, false>(a, stream) : quant_tile<false, false>(a, stream);
 }
@@ -428,17 +396,21 @@ cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, int64_t ld_out, i
                                cudaStream_t stream) {
     const int64_t segs = (a.k + 15) / 16, tiles = fp4_scale_tiles(a.k, a.kind);
     const int threads = segs < 256 ? static_cast<int>((segs + 31) / 32 * 32) : 256;
-    const int64_t cb = (segs + threads - 1) / threads;
-    const dim3 grid(static_cast<unsigned>(a.rows < 0x7FFFFFFF ? a.rows : 0x7FFFFFFF),
-                    static_cast<unsigned>(cb < 65535 ? cb : 65535));
-    const bool vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ld_out % (fp32 ? 4 : 8) == 0;
+    const dim3 grid(static_cast<unsigned>(a.rows), static_cast<unsigned>((segs + threads - 1) / threads));
     auto go = [&](auto kern) {
-        kern<<<grid, threads, 0, stream>>>(a.codes, a.scale, a.ts, a.rows, a.k, a.ld, tiles, out,
-                                           ld_out, vec, segs);
+        kern<<<grid, threads, 0, stream>>>(a.codes, a.scale, a.ts, a.rows, a.k, a.ld, tiles, out, ld_out,
+                                           static_cast<int>(segs));
         return cudaGetLastError();
     };
-    if (a.kind == FP4_NV) return fp32 ? go(k_fp4_dequant<true, true>) : go(k_fp4_dequant<true, false>);
-    return fp32 ? go(k_fp4_dequant<false, true>) : go(k_fp4_dequant<false, false>);
+    const bool nv = a.kind == FP4_NV;
+    if (fp32) {
+        if (reinterpret_cast<uintptr_t>(out) % 16 == 0 && ld_out % 4 == 0)
+            return nv ? go(k_fp4_dequant<true, true, true>) : go(k_fp4_dequant<false, true, true>);
+        return nv ? go(k_fp4_dequant<true, true, false>) : go(k_fp4_dequant<false, true, false>);
+    }
+    if (ragged::wide(out, ld_out))
+        return nv ? go(k_fp4_dequant<true, false, true>) : go(k_fp4_dequant<false, false, true>);
+    return nv ? go(k_fp4_dequant<true, false, false>) : go(k_fp4_dequant<false, false, false>);
 }
 
 }  // namespace fp8hg

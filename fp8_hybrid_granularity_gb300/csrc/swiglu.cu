@@ -18,26 +18,11 @@
 
 #include "lowbit.h"
 #include "quant_math.cuh"
+#include "ragged.cuh"
 
 namespace fp8hg {
 
 namespace {
-
-template <bool VEC>
-__device__ __forceinline__ void load_bf16x16(const uint16_t *p, int64_t left, uint32_t (&w)[8]) {
-    if (VEC && left >= 16) {
-        const uint4 a = ptx::ld_stream_v4(p), b = ptx::ld_stream_v4(p + 8);
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t lo = 2 * i < left ? __ldg(p + 2 * i) : 0u;
-            const uint32_t hi = 2 * i + 1 < left ? __ldg(p + 2 * i + 1) : 0u;
-            w[i] = lo | (hi << 16);
-        }
-    }
-}
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -131,7 +116,7 @@ __device__ __forceinline__ void cast_bf16x16(const uint32_t (&w)[8], const Group
 }
 
 // ------------------------------------------------------------------- forward
-template <int FH, int FC, bool CKPT, bool VEC>
+template <int FH, int FC, bool CKPT, bool WIDE>
 __global__ void __launch_bounds__(256)
     k_swiglu_fwd(const SwigluFwdArgs a, int segs, int total_segs) {
     const int tid = threadIdx.x;
@@ -144,8 +129,8 @@ __global__ void __launch_bounds__(256)
         const bool in = tid / segs < rpb && r < a.rows && seg < total_segs;
         uint32_t g[8] = {0, 0, 0, 0, 0, 0, 0, 0}, u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (in && left > 0) {
-            load_bf16x16<VEC>(a.gate + r * a.ld_in + c0, left, g);
-            load_bf16x16<VEC>(a.up + r * a.ld_in + c0, left, u);
+            ragged::load16<WIDE>(a.gate + r * a.ld_in + c0, left, g);
+            ragged::load16<WIDE>(a.up + r * a.ld_in + c0, left, u);
         }
         float h[16];
         uint32_t mh = 0;
@@ -199,21 +184,23 @@ __device__ __forceinline__ void swiglu_grads(float g, float u, float dh, float &
     h = gs * u;
 }
 
-template <int FC, bool VEC>
+template <int FC, bool WIDE>
 __global__ void __launch_bounds__(256)
     k_swiglu_bwd(const uint16_t *__restrict__ dh, int64_t ld_dh, const SwigluCkpt c,
-                 uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int64_t ld_d, int64_t segs) {
+                 uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int64_t ld_d, int segs) {
+    // a warp takes 32 neighbouring segments of one row, whole warps past the
+    // row's end included: the stores exchange values between lanes
+    const int seg = (blockIdx.y * blockDim.x + threadIdx.x);
+    const int64_t c0 = static_cast<int64_t>(seg) * 16, left = c.cols - c0;
     for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
-        for (int64_t seg = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; seg < segs;
-             seg += static_cast<int64_t>(gridDim.y) * blockDim.x) {
-            const int64_t c0 = seg * 16, left = c.cols - c0;
+        uint32_t og[8] = {0, 0, 0, 0, 0, 0, 0, 0}, ou[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (seg < segs) {
             uint32_t w[8], gc[4], uc[4];
-            load_bf16x16<VEC>(dh + r * ld_dh + c0, left, w);
+            ragged::load16<WIDE>(dh + r * ld_dh + c0, left, w);
             load_bytes16(c.gq + r * c.ld_q + c0, left, gc);
             load_bytes16(c.uq + r * c.ld_q + c0, left, uc);
             const float sg = scale_pow2(__ldg(c.gs + r * c.ld_s + (seg >> 3)));
             const float su = scale_pow2(__ldg(c.us + r * c.ld_s + (seg >> 3)));
-            uint32_t og[8], ou[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float g[4], u[4], a[4], b[4], h;
@@ -228,110 +215,152 @@ __global__ void __launch_bounds__(256)
                 ou[2 * i] = ptx::cvt_bf16x2(b[0], b[1]);
                 ou[2 * i + 1] = ptx::cvt_bf16x2(b[2], b[3]);
             }
-            uint16_t *pg = dg + r * ld_d + c0, *pu = du + r * ld_d + c0;
-            if (VEC && left >= 16) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    reinterpret_cast<uint4 *>(pg)[i] =
-                        make_uint4(og[4 * i], og[4 * i + 1], og[4 * i + 2], og[4 * i + 3]);
-                    reinterpret_cast<uint4 *>(pu)[i] =
-                        make_uint4(ou[4 * i], ou[4 * i + 1], ou[4 * i + 2], ou[4 * i + 3]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < left) {
-                        pg[i] = static_cast<uint16_t>(og[i >> 1] >> (16 * (i & 1)));
-                        pu[i] = static_cast<uint16_t>(ou[i >> 1] >> (16 * (i & 1)));
-                    }
-            }
         }
+        ragged::store16<WIDE>(dg + r * ld_d + c0, left, og);
+        ragged::store16<WIDE>(du + r * ld_d + c0, left, ou);
     }
 }
 
 // ------------------------------------------------------------- backward, FP8
-// A CTA takes a tile of 128 tokens x 128 columns, one group in each direction
-// per row and column, and computes dg, du and h one after the other into
-// shared memory.
-constexpr int kT = 128, kPitch = 129;
+// Persistent, one CTA of 512 threads per SM, a tile of 128 tokens x 128
+// columns at a time: one group in each direction per row and column.
+//   rows     a thread takes 16 columns of two rows (eight lanes a row),
+//            computes dg, du and h, quantizes dg and du along the row at once
+//            and leaves all three in shared memory in FP32 (they have to be
+//            rounded once, from FP32, in each direction);
+//   columns  a thread takes 32 tokens of one column of each of the three
+//            (four lanes a column: 128 bytes of codes, a whole line).
+// The next tile's inputs are loaded into registers before the column pass, so
+// the loads run under it.
+//
+// Shared memory: value (r, c) at r * 128 + (r / 32) * 8 words plus c with its
+// 16-byte piece index i replaced by i ^ ((i / 8) & 3): the eight lanes of a row
+// write pieces in eight different bank groups, and the 8 columns x 4 row
+// quarters that a warp reads at a time fall into 32 banks.
+constexpr int kT = 128, Q_THREADS = 512;
+constexpr int kPlane = kT * kT + 3 * 8;          // words of one of the three
+constexpr int kQSmem = 3 * kPlane * 4;
 
 template <int F>
-__device__ __forceinline__ void emit_group16(const float (&v)[16], uint32_t m, uint8_t *q,
-                                             uint8_t *s, bool first) {
-    const GroupF32<F> gs(m);
-    uint32_t c[4];
+__device__ __forceinline__ void emit_codes(const float *v, int n4, const GroupF32<F> &gs, uint32_t *c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = gs.cast4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    *reinterpret_cast<uint4 *>(q) = make_uint4(c[0], c[1], c[2], c[3]);
-    if (first) *s = static_cast<uint8_t>(gs.byte);
-}
-__device__ __forceinline__ void emit_group16(int fmt, const float (&v)[16], uint32_t m, uint8_t *q,
-                                             uint8_t *s, bool first) {
-    if (fmt == FMT_E4M3) emit_group16<FMT_E4M3>(v, m, q, s, first);
-    else emit_group16<FMT_E5M2>(v, m, q, s, first);
+    for (int i = 0; i < n4; ++i) c[i] = gs.cast4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
-template <int FC>
-__global__ void __launch_bounds__(256)
-    k_swiglu_bwd_q(const uint16_t *__restrict__ dh, int64_t ld_dh, const SwigluCkpt c,
-                   const SwigluGrads o) {
-    extern __shared__ float tile[];
-    const int tid = threadIdx.x, seg = tid & 7;
-    const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kT, r0 = static_cast<int64_t>(blockIdx.y) * kT;
-    for (int which = 0; which < 3; ++which) {
-        const int fmt_t = which == 2 ? o.fmt_h : o.fmt_t;
-        for (int rr = tid >> 3; rr < kT; rr += 32) {
-            const int64_t r = r0 + rr, col = k0 + seg * 16;
-            uint32_t w[8], gc[4], uc[4];
-            load_bf16x16<true>(dh + r * ld_dh + col, 16, w);
-            load_bytes16(c.gq + r * c.ld_q + col, 16, gc);
-            load_bytes16(c.uq + r * c.ld_q + col, 16, uc);
-            const float sg = scale_pow2(__ldg(c.gs + r * c.ld_s + blockIdx.x));
-            const float su = scale_pow2(__ldg(c.us + r * c.ld_s + blockIdx.x));
-            float v[16];
-            uint32_t m = 0;
+// A thread's inputs of a tile: two rows (0 .. 3 + 64 apart) of 16 columns.
+struct TileIn {
+    uint32_t dh[2][8], g[2][4], u[2][4];
+    uint32_t sg[2], su[2];
+};
+
+template <bool WIDE>
+__device__ __forceinline__ void load_tile(TileIn &t, const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c,
+                                          int64_t r0, int64_t kb, int rr, int seg) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float g[4], u[4];
-                fp8x4_values<FC>(gc[i], g);
-                fp8x4_values<FC>(uc[i], u);
-                const float d[4] = {bf_lo(w[2 * i]), bf_hi(w[2 * i]), bf_lo(w[2 * i + 1]),
-                                    bf_hi(w[2 * i + 1])};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float a, b, h;
-                    swiglu_grads(g[j] * sg, u[j] * su, d[j], a, b, h);
-                    const float x = which == 0 ? a : which == 1 ? b : h;
-                    v[4 * i + j] = x;
-                    tile[rr * kPitch + seg * 16 + 4 * i + j] = x;
-                    m = max(m, abs_bits(x));
-                }
-            }
-            if (which < 2) {
-                m = group_max(m);
-                emit_group16(o.fmt, v, m, o.q[which] + r * o.ld_q + col,
-                             o.s[which] + r * o.ld_s + blockIdx.x, seg == 0);
-            }
+    for (int i = 0; i < 2; ++i) {
+        const int64_t r = r0 + rr + 64 * i, col = kb * kT + seg * 16;
+        if (WIDE) {
+            ragged::load16<true>(dh + r * ld_dh + col, 16, t.dh[i]);
+        } else {
+            const uint4 *p = reinterpret_cast<const uint4 *>(dh + r * ld_dh + col);
+            const uint4 a = __ldg(p), b = __ldg(p + 1);
+            t.dh[i][0] = a.x, t.dh[i][1] = a.y, t.dh[i][2] = a.z, t.dh[i][3] = a.w;
+            t.dh[i][4] = b.x, t.dh[i][5] = b.y, t.dh[i][6] = b.z, t.dh[i][7] = b.w;
         }
-        __syncthreads();
-        for (int cc = tid >> 3; cc < kT; cc += 32) {
-            float v[16];
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                v[i] = tile[(seg * 16 + i) * kPitch + cc];
-                m = max(m, abs_bits(v[i]));
-            }
-            m = group_max(m);
-            emit_group16(fmt_t, v, m, o.qt[which] + (k0 + cc) * o.ld_qt + r0 + seg * 16,
-                         o.st[which] + (k0 + cc) * o.ld_st + blockIdx.y, seg == 0);
-        }
-        __syncthreads();
+        load_bytes16(c.gq + r * c.ld_q + col, 16, t.g[i]);
+        load_bytes16(c.uq + r * c.ld_q + col, 16, t.u[i]);
+        t.sg[i] = __ldg(c.gs + r * c.ld_s + kb);
+        t.su[i] = __ldg(c.us + r * c.ld_s + kb);
     }
 }
 
-bool vec16(const void *p, int64_t ld) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
+template <int FC, int FR, int FT, int FH, bool WIDE>
+__global__ void __launch_bounds__(Q_THREADS, 1)
+    k_swiglu_bwd_q(const uint16_t *__restrict__ dh, int64_t ld_dh, const SwigluCkpt c, const SwigluGrads o,
+                   int kbs, int tiles) {
+    extern __shared__ __align__(16) float plane[];
+    const int tid = threadIdx.x, seg = tid & 7, rr = tid >> 3;
+    TileIn in;
+    int tile = blockIdx.x;
+    if (tile < tiles) load_tile<WIDE>(in, dh, ld_dh, c, static_cast<int64_t>(tile / kbs) * kT, tile % kbs, rr, seg);
+    for (; tile < tiles; tile += gridDim.x) {
+        const int64_t kb = tile % kbs, rb = tile / kbs, r0 = rb * kT;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = rr + 64 * i;
+            const float sg = scale_pow2(in.sg[i]), su = scale_pow2(in.su[i]);
+            float a[16], b[16];
+            uint32_t ma = 0, mb = 0;
+            float *dst = plane + row * kT + (row >> 5) * 8;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float g[4], u[4], h[4];
+                fp8x4_values<FC>(in.g[i][k], g);
+                fp8x4_values<FC>(in.u[i][k], u);
+                const float d[4] = {bf_lo(in.dh[i][2 * k]), bf_hi(in.dh[i][2 * k]), bf_lo(in.dh[i][2 * k + 1]),
+                                    bf_hi(in.dh[i][2 * k + 1])};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    swiglu_grads(g[j] * sg, u[j] * su, d[j], a[4 * k + j], b[4 * k + j], h[j]);
+                    ma = max(ma, abs_bits(a[4 * k + j]));
+                    mb = max(mb, abs_bits(b[4 * k + j]));
+                }
+                const int piece = (4 * seg + k) ^ ((seg >> 1) & 3);
+                *reinterpret_cast<float4 *>(dst + piece * 4) =
+                    make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
+                *reinterpret_cast<float4 *>(dst + kPlane + piece * 4) =
+                    make_float4(b[4 * k], b[4 * k + 1], b[4 * k + 2], b[4 * k + 3]);
+                *reinterpret_cast<float4 *>(dst + 2 * kPlane + piece * 4) = make_float4(h[0], h[1], h[2], h[3]);
+            }
+            const GroupF32<FR> ga(group_max(ma)), gb(group_max(mb));
+            const int64_t r = r0 + row, at = r * o.ld_q + kb * kT + seg * 16;
+            uint32_t q[4];
+            emit_codes<FR>(a, 4, ga, q);
+            *reinterpret_cast<uint4 *>(o.q[0] + at) = make_uint4(q[0], q[1], q[2], q[3]);
+            emit_codes<FR>(b, 4, gb, q);
+            *reinterpret_cast<uint4 *>(o.q[1] + at) = make_uint4(q[0], q[1], q[2], q[3]);
+            if (seg == 0) {
+                o.s[0][r * o.ld_s + kb] = static_cast<uint8_t>(ga.byte);
+                o.s[1][r * o.ld_s + kb] = static_cast<uint8_t>(gb.byte);
+            }
+        }
+        __syncthreads();
+        const int next = tile + gridDim.x;
+        if (next < tiles)
+            load_tile<WIDE>(in, dh, ld_dh, c, static_cast<int64_t>(next / kbs) * kT, next % kbs, rr, seg);
+        // column cc, tokens 32 quarter .. + 31
+        const int quarter = tid & 3, cc = tid >> 2;
+        const int word = (((cc >> 2) ^ ((cc >> 5) & 3)) << 2) + (cc & 3);
+        const float *src = plane + quarter * (32 * kT + 8) + word;
+#pragma unroll
+        for (int w = 0; w < 3; ++w) {
+            float v[32];
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                v[i] = src[w * kPlane + i * kT];
+                m = max(m, abs_bits(v[i]));
+            }
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            uint32_t q[8], byte;
+            if (w < 2) {
+                const GroupF32<FT> gs(m);
+                emit_codes<FT>(v, 8, gs, q);
+                byte = gs.byte;
+            } else {
+                const GroupF32<FH> gs(m);
+                emit_codes<FH>(v, 8, gs, q);
+                byte = gs.byte;
+            }
+            const int64_t col = kb * kT + cc;
+            uint4 *d = reinterpret_cast<uint4 *>(o.qt[w] + col * o.ld_qt + r0 + quarter * 32);
+            d[0] = make_uint4(q[0], q[1], q[2], q[3]);
+            d[1] = make_uint4(q[4], q[5], q[6], q[7]);
+            if (quarter == 0) o.st[w][col * o.ld_st + rb] = static_cast<uint8_t>(byte);
+        }
+        __syncthreads();
+    }
 }
 
 template <int FH, int FC, bool CKPT>
@@ -344,7 +373,7 @@ cudaError_t fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
     const int64_t rb = (a.rows + rpb - 1) / rpb;
     const dim3 grid(static_cast<unsigned>(rb < 0x7FFFFFFF ? rb : 0x7FFFFFFF),
                     static_cast<unsigned>((total + segs - 1) / segs));
-    if (vec16(a.gate, a.ld_in) && vec16(a.up, a.ld_in))
+    if (ragged::wide(a.gate, a.ld_in) && ragged::wide(a.up, a.ld_in))
         k_swiglu_fwd<FH, FC, CKPT, true><<<grid, threads, 0, stream>>>(a, segs, static_cast<int>(total));
     else
         k_swiglu_fwd<FH, FC, CKPT, false><<<grid, threads, 0, stream>>>(a, segs, static_cast<int>(total));
@@ -367,30 +396,59 @@ cudaError_t launch_swiglu_bwd(const uint16_t *dh, int64_t ld_dh, const SwigluCkp
                               uint16_t *du, int64_t ld_d, cudaStream_t stream) {
     const int64_t segs = (c.cols + 15) / 16;
     const int threads = segs < 256 ? static_cast<int>((segs + 31) / 32 * 32) : 256;
-    const int64_t cb = (segs + threads - 1) / threads;
-    const dim3 grid(static_cast<unsigned>(c.rows < 0x7FFFFFFF ? c.rows : 0x7FFFFFFF),
-                    static_cast<unsigned>(cb < 65535 ? cb : 65535));
-    const bool vec = vec16(dh, ld_dh) && vec16(dg, ld_d) && vec16(du, ld_d);
+    const dim3 grid(static_cast<unsigned>(c.rows), static_cast<unsigned>((segs + threads - 1) / threads));
+    const bool wide = ragged::wide(dh, ld_dh) && ragged::wide(dg, ld_d) && ragged::wide(du, ld_d);
     auto go = [&](auto kern) {
-        kern<<<grid, threads, 0, stream>>>(dh, ld_dh, c, dg, du, ld_d, segs);
+        kern<<<grid, threads, 0, stream>>>(dh, ld_dh, c, dg, du, ld_d, static_cast<int>(segs));
         return cudaGetLastError();
     };
-    if (c.fmt == FMT_E4M3) return vec ? go(k_swiglu_bwd<FMT_E4M3, true>) : go(k_swiglu_bwd<FMT_E4M3, false>);
-    return vec ? go(k_swiglu_bwd<FMT_E5M2, true>) : go(k_swiglu_bwd<FMT_E5M2, false>);
+    if (c.fmt == FMT_E4M3) return wide ? go(k_swiglu_bwd<FMT_E4M3, true>) : go(k_swiglu_bwd<FMT_E4M3, false>);
+    return wide ? go(k_swiglu_bwd<FMT_E5M2, true>) : go(k_swiglu_bwd<FMT_E5M2, false>);
 }
 
-cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c,
-                                const SwigluGrads &g, cudaStream_t stream) {
-    constexpr int smem = kT * kPitch * 4;
-    const dim3 grid(static_cast<unsigned>(c.cols / kT), static_cast<unsigned>(c.rows / kT));
+namespace {
+
+template <int FC, int FR, int FT, int FH>
+cudaError_t bwd_q(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
+                  cudaStream_t stream) {
+    const int64_t kbs = c.cols / kT, tiles = kbs * (c.rows / kT);
+    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (sms < 1) sms = 1;
+    const unsigned grid = static_cast<unsigned>(tiles < sms ? tiles : sms);
     auto go = [&](auto kern) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmem);
         if (e != cudaSuccess) return e;
-        kern<<<grid, 256, smem, stream>>>(dh, ld_dh, c, g);
+        kern<<<grid, Q_THREADS, kQSmem, stream>>>(dh, ld_dh, c, g, static_cast<int>(kbs), static_cast<int>(tiles));
         return cudaGetLastError();
     };
-    return c.fmt == FMT_E4M3 ? go(k_swiglu_bwd_q<FMT_E4M3>) : go(k_swiglu_bwd_q<FMT_E5M2>);
+    return ragged::wide(dh, ld_dh) ? go(k_swiglu_bwd_q<FC, FR, FT, FH, true>)
+                                   : go(k_swiglu_bwd_q<FC, FR, FT, FH, false>);
+}
+template <int FC, int FR, int FT>
+cudaError_t bwd_q_h(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
+                    cudaStream_t stream) {
+    return g.fmt_h == FMT_E4M3 ? bwd_q<FC, FR, FT, FMT_E4M3>(dh, ld_dh, c, g, stream)
+                               : bwd_q<FC, FR, FT, FMT_E5M2>(dh, ld_dh, c, g, stream);
+}
+template <int FC, int FR>
+cudaError_t bwd_q_t(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
+                    cudaStream_t stream) {
+    return g.fmt_t == FMT_E4M3 ? bwd_q_h<FC, FR, FMT_E4M3>(dh, ld_dh, c, g, stream)
+                               : bwd_q_h<FC, FR, FMT_E5M2>(dh, ld_dh, c, g, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
+                                cudaStream_t stream) {
+    if (c.fmt == FMT_E4M3)
+        return g.fmt == FMT_E4M3 ? bwd_q_t<FMT_E4M3, FMT_E4M3>(dh, ld_dh, c, g, stream)
+                                 : bwd_q_t<FMT_E4M3, FMT_E5M2>(dh, ld_dh, c, g, stream);
+    return g.fmt == FMT_E4M3 ? bwd_q_t<FMT_E5M2, FMT_E4M3>(dh, ld_dh, c, g, stream)
+                             : bwd_q_t<FMT_E5M2, FMT_E5M2>(dh, ld_dh, c, g, stream);
 }
 
 }  // namespace fp8hg

@@ -23,7 +23,7 @@ from typing import Optional
 
 import torch
 
-from . import (E4M3, E5M2, GRAN_1x128, OUT_BF16, OUT_FP32, GemmOpts, QTensor, _check, _round4,
+from . import (E4M3, E5M2, GRAN_1x128, OUT_BF16, OUT_FP32, Fp8hgError, GemmOpts, QTensor, _round4,
                _stream)
 from . import lib as _lib
 
@@ -55,6 +55,18 @@ class _Grads(ctypes.Structure):
 
 
 _bound = None
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(stream, x):
+    """The stream to launch on: x's device's current one if none is given (the
+    plain lookup: a call takes about as long as ten microseconds' work)."""
+    return _raw_stream(x.get_device()) if stream is None else _stream(stream)
+
+
+def _check(rc: int, what: str):
+    if rc != 0:
+        raise Fp8hgError(what, rc)
 
 
 def _fns():
@@ -132,11 +144,14 @@ class Fp4Tensor:
     kind: int
     tensor_scale: Optional[torch.Tensor] = None
 
-    def operand(self) -> _Fp4Operand:
+    def ld(self) -> int:
+        """Row stride of the codes, in bytes (a single row may carry any)."""
         c = self.codes
-        return _Fp4Operand(c.data_ptr(), self.scale.data_ptr(), _ts(self.tensor_scale), self.rows,
-                           self.k, c.stride(0) if self.rows > 1 else max(c.stride(0), c.shape[1]),
-                           self.kind, 0)
+        return c.stride(0) if self.rows > 1 else max(c.stride(0), c.shape[1])
+
+    def operand(self) -> _Fp4Operand:
+        return _Fp4Operand(self.codes.data_ptr(), self.scale.data_ptr(), _ts(self.tensor_scale),
+                           self.rows, self.k, self.ld(), self.kind, 0)
 
     def scales(self) -> torch.Tensor:
         """The scale bytes as [rows, ceil(k / block)] (a copy)."""
@@ -164,18 +179,19 @@ def fp4_tensor_scale(x, out=None, stream=None):
     n = f.fp4_tensor_scale_workspace()
     ws = torch.empty(n, dtype=torch.uint8, device=x.device)
     _check(f.fp4_tensor_scale(x.data_ptr(), x.shape[0], x.shape[1], _ld(x), _ts(out), ws.data_ptr(),
-                              n, _stream(stream)), "fp4_tensor_scale")
+                              n, _on(stream, x)), "fp4_tensor_scale")
     return out
 
 
+_NONE = (None, 0, None)
+
+
 def _quant(x, kind, tensor_scale, rows_out, cols_out, stream, what):
-    q, t = rows_out, cols_out
-    rc = _fns().fp4_quant(x.data_ptr(), x.shape[0], x.shape[1], _ld(x), kind, _ts(tensor_scale),
-                          q.codes.data_ptr() if q else None, q.operand().ld if q else 0,
-                          q.scale.data_ptr() if q else None,
-                          t.codes.data_ptr() if t else None, t.operand().ld if t else 0,
-                          t.scale.data_ptr() if t else None, _stream(stream))
-    _check(rc, what)
+    q = (rows_out.codes.data_ptr(), rows_out.ld(), rows_out.scale.data_ptr()) if rows_out else _NONE
+    t = (cols_out.codes.data_ptr(), cols_out.ld(), cols_out.scale.data_ptr()) if cols_out else _NONE
+    rows, cols = x.shape
+    _check(_fns().fp4_quant(x.data_ptr(), rows, cols, _ld(x), kind, _ts(tensor_scale), *q, *t,
+                            _on(stream, x)), what)
 
 
 def _check_fp4(q, rows, k, kind):
@@ -219,7 +235,7 @@ def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None, stream=None):
     _check_out(out, q.rows, q.k)
     op = q.operand()
     _check(_fns().fp4_dequant(ctypes.byref(op), out.data_ptr(), _ld(out), _out_kind(out),
-                              _stream(stream)), "fp4_dequant")
+                              _on(stream, out)), "fp4_dequant")
     return out
 
 
@@ -235,7 +251,7 @@ def fp4_gemm_scaled(a: Fp4Tensor, b: Fp4Tensor, out=None, out_dtype=None, accumu
     oa, ob = a.operand(), b.operand()
     _check(_fns().fp4_gemm_scaled(ctypes.byref(oa), ctypes.byref(ob), out.data_ptr(), _ld(out),
                                   _out_kind(out), 1 if accumulate else 0,
-                                  _opts(wait_limit_ns, inject_fault), _stream(stream)),
+                                  _opts(wait_limit_ns, inject_fault), _on(stream, out)),
            "fp4_gemm_scaled")
     return out
 
@@ -259,7 +275,7 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
     ow = w.operand()
     _check(f.fp4_linear(x.data_ptr(), rows, _ld(x), _ts(tensor_scale), ctypes.byref(ow),
                         out.data_ptr(), _ld(out), _out_kind(out), workspace.data_ptr(),
-                        workspace.numel(), None, _stream(stream)), "fp4_linear")
+                        workspace.numel(), None, _on(stream, x)), "fp4_linear")
     return out
 
 
@@ -276,13 +292,16 @@ class SwigluCkpt:
     up: QTensor
 
 
-def _groups(rows, cols, fmt, device, lead=1):
-    """[rows, lead * cols] codes and their 1x128 scales (rows padded to 16 bytes)."""
-    cols *= lead
-    q = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)
+def _groups(rows, cols, fmt, device):
+    """[rows, cols] codes (rows padded to 16 bytes) and their 1x128 scales."""
     g = (cols + 127) // 128
-    s = torch.empty((rows, _round4(g)), dtype=torch.uint8, device=device)
-    return QTensor(q[:, :cols], s, fmt, GRAN_1x128, g)
+    if cols % 16:
+        q = torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.uint8,
+                                device=device)
+    else:
+        q = torch.empty((rows, cols), dtype=torch.uint8, device=device)
+    return QTensor(q, torch.empty((rows, _round4(g)), dtype=torch.uint8, device=device), fmt,
+                   GRAN_1x128, g)
 
 
 def _ld_codes(q) -> int:
@@ -311,7 +330,7 @@ def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bo
         ld_q, ld_s = _ld_codes(g.codes), g.scale.stride(0)
     _check(_fns().fp8_swiglu_ckpt(gate.data_ptr(), up.data_ptr(), rows, cols, _ld(gate), fmt_h,
                                   h.codes.data_ptr(), _ld_codes(h.codes), h.scale.data_ptr(),
-                                  h.scale.stride(0), fmt, *ptr, ld_q, ld_s, _stream(stream)),
+                                  h.scale.stride(0), fmt, *ptr, ld_q, ld_s, _on(stream, gate)),
            "fp8_swiglu_ckpt")
     return h, SwigluCkpt(g, u) if checkpoint else None
 
@@ -341,7 +360,7 @@ def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None, stream=None):
     _check_out(out, rows, 2 * cols)
     _check_matrix(out, "out")
     _check(_fns().fp8_swiglu_ckpt_bwd(dh.data_ptr(), _ld(dh), ctypes.byref(c), out.data_ptr(),
-                                      out.data_ptr() + 2 * cols, _ld(out), _stream(stream)),
+                                      out.data_ptr() + 2 * cols, _ld(out), _on(stream, dh)),
            "fp8_swiglu_ckpt_bwd")
     return out
 
@@ -355,7 +374,7 @@ def fp8_swiglu_ckpt_bwd_q(dh, ckpt: SwigluCkpt, fmt: int = E5M2, fmt_t: int = E5
     c = _ckpt(ckpt, dh)
     rows, cols = dh.shape
     dev = dh.device
-    d = _groups(rows, cols, fmt, dev, lead=2)
+    d = _groups(rows, 2 * cols, fmt, dev)
     t = _groups(2 * cols, rows, fmt_t, dev)
     h = _groups(cols, rows, fmt_h, dev)
     dq, ds, tq, tl = d.codes.data_ptr(), d.scale.data_ptr(), t.codes.data_ptr(), t.scale.data_ptr()
@@ -364,5 +383,5 @@ def fp8_swiglu_ckpt_bwd_q(dh, ckpt: SwigluCkpt, fmt: int = E5M2, fmt_t: int = E5
                h.codes.data_ptr(), h.scale.data_ptr(), d.codes.stride(0), d.scale.stride(0), ld_qt,
                ld_st, fmt, fmt_t, fmt_h, 0)
     _check(_fns().fp8_swiglu_ckpt_bwd_q(dh.data_ptr(), _ld(dh), ctypes.byref(c), ctypes.byref(g),
-                                        _stream(stream)), "fp8_swiglu_ckpt_bwd_q")
+                                        _on(stream, dh)), "fp8_swiglu_ckpt_bwd_q")
     return d, t, h
