@@ -21,8 +21,7 @@
 // tensor with zeros, the scale padding along K holds zeros, and rows past the
 // last only reach outputs that are not stored.
 //
-//  k_fp4_wide   tiles of 256 x 192 (two accumulators that share each B tile),
-//               persistent, one CTA per SM.
+//  k_fp4_pair   tiles of 256 x 384 per pair of CTAs, persistent.
 //  k_fp4_few    few rows on one side: tiles of 128 x 16 .. 128, K split over
 //               the CTAs of a cluster.
 //
@@ -32,6 +31,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -39,6 +39,7 @@
 #include "fp4_math.cuh"
 #include "gemm_common.cuh"
 #include "lowbit.h"
+#include "ragged.cuh"
 
 namespace fp8hg {
 
@@ -75,58 +76,67 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
     return d;
 }
 
-// Shared and tensor memory of a kernel with MH accumulators of 128 rows by BN
-// columns, S operand stages and SLOTS scale slots in tensor memory (each freed
-// by the stage that used it, so SLOTS <= S).
-template <bool NV, int MH, int BN, int S, int SLOTS>
-struct Layout {
-    static constexpr int NG = NV ? 4 : 2;               // scale tiles per stage and 128 rows
-    static constexpr uint32_t SF = NG * 512;            // their bytes
-    static constexpr int NB = BN > 128 ? 2 : 1;         // 128-row scale tiles of B
-    static constexpr uint32_t A = MH * 128 * kStageBytes, B = BN * kStageBytes;
-    static constexpr uint32_t STAGE = A + B;
-    static constexpr uint32_t OFF_SF = S * STAGE;
-    static constexpr uint32_t SF_STAGE = (MH + NB) * SF;
-    static constexpr uint32_t OFF_BAR = OFF_SF + S * SF_STAGE;
-    // barriers: full[S], empty[S], scales[SLOTS], tfull, tempty, drain, drain2
-    static constexpr uint32_t BAR_EMPTY = 8 * S, BAR_SF = 16 * S, BAR_TFULL = 16 * S + 8 * SLOTS;
-    static constexpr uint32_t OFF_MISC = OFF_BAR + 256;
-    static_assert(BAR_TFULL + 32 <= 256, "barriers");
-    static_assert(OFF_MISC + 1040 <= 232448, "shared memory");
-    static constexpr uint32_t COL_SF = MH * BN;         // first scale column
-    static constexpr uint32_t COLS = (MH * 4 + NB * 4) * NG;
-    static_assert(SLOTS <= S, "a slot is freed by its stage's barrier");
-    static_assert(COL_SF + SLOTS * COLS <= 512, "tensor memory");
+// ---------------------------------------------------------------- pair tiles
+// Tiles of 256 x 192 NH of a pair of CTAs (a cluster of two), tcgen05.mma with
+// cta_group::2: per 64 elements of K one M = 256, N = 192 MMA for each of the
+// NH column parts.  Each CTA holds its 128 rows of A and, of each column part,
+// 96 rows of B; its tensor memory takes its 128 rows of the accumulators.
+//
+// NH = 2, the large products: a stage (256 elements of K) is 40 KB of operands
+// per CTA for 768 cycles of MMAs.  What a 4-bit product runs short of is
+// operand bytes: it takes as many per cycle as an FP8 one and reads a stage in
+// half the time, and an SM gets about 60 bytes a cycle from L2 here.  Single-CTA
+// tiles of 256 x 192 (two accumulators of 128 rows) need 56 KB for the same 768
+// cycles.  At 16384 x 3584 x 18944: 380 us with those tiles (MX; NV 447), 345
+// (369) with these.
+// NH = 1, where NH = 2 leaves pairs without a tile.
+//
+// Warps of each CTA: 0 TMA producer, 4-11 epilogue (a 32-row quarter of one
+// column part each); of the even CTA also 1 MMA issuer and 2, 3, 12, 13 scale
+// copiers, for both CTAs; of the odd CTA 1 forwarder.  Tensor memory: the
+// accumulators, then the scale slots: per 128 (NV: 64) elements of K four
+// columns for every 128 rows, B's first.
+constexpr int PM = 256, PH = 192, P_THREADS = 512;
+constexpr uint32_t EPI_BYTES = 4096;           // staging per epilogue warp
+template <bool NV, int NH_>
+struct PairLayout {
+    static constexpr int NH = NH_, PN = PH * NH;
+    static constexpr int NG = NV ? 4 : 2;      // scale tiles per stage and 128 rows
+    static constexpr int NB = NH == 2 ? 3 : 2; // 128-row scale tiles that a tile's columns touch
+    static constexpr int S = NH == 2 ? 4 : 6;
+    static constexpr int SLOTS = NH == 2 && NV ? 2 : NH == 2 ? 4 : S;
+    // stages at a tile's ends whose column parts go one after the other
+    static constexpr int SKEW = NH == 2 && NV ? 2 : 1;
+    static constexpr uint32_t SF = NG * 512;
+    static constexpr uint32_t A = 128 * kStageBytes, BH = PH / 2 * kStageBytes;
+    static constexpr uint32_t STAGE = A + NH * BH, SF_STAGE = (1 + NB) * SF;   // A's rows, then B's
+    static constexpr uint32_t OFF_SF = S * STAGE, OFF_BAR = OFF_SF + S * SF_STAGE;
+    // barriers: full (even CTA: both CTAs' bytes), empty (each CTA), scales
+    // (even CTA), tfull[2] and tempty[2] (each CTA), odd[2] (even CTA: the odd
+    // one's tempty), drain[5]
+    static constexpr uint32_t EMPTY = 8 * S, SCALES = 16 * S, TFULL = SCALES + 8 * SLOTS;
+    static constexpr uint32_t TEMPTY = TFULL + 16, ODD = TEMPTY + 16, DRAIN = ODD + 16;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + 256, OFF_EPI = OFF_MISC + 16;
+    static constexpr uint32_t SMEM = OFF_EPI + 4 * NH * EPI_BYTES + 1024;
+    static constexpr uint32_t GC = 4 * (1 + NB), COLS = GC * NG;   // columns of a scale group, of a slot
+    static_assert(DRAIN + 40 <= 256 && SMEM <= 232448 && PN + SLOTS * COLS <= 512, "");
+    // a slot is freed by its stage's barrier; the skewed stages are all in slots
+    static_assert(SLOTS <= S && SKEW <= SLOTS, "");
+    static_assert(A % 1024 == 0 && BH % 1024 == 0, "the swizzle repeats every 1 KB");
 };
 
-// The four (or fewer) MMAs per accumulator of one stage.
-template <bool NV, int MH, int BN, class L>
-__device__ __forceinline__ void issue_stage(uint32_t tmem, uint32_t slot_col, uint32_t b_shift,
-                                            uint32_t s_a, uint32_t s_b, uint32_t idesc, bool first) {
-    const uint64_t bd = desc_sw128(s_b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int g = NV ? j : j >> 1;
-        const uint32_t id = idesc | (NV ? 0u : ((j & 1) * 2u << 29) | ((j & 1) * 2u << 4));
-        const uint32_t sfb = slot_col + g * (L::NB * 4) + b_shift;
-#pragma unroll
-        for (int h = 0; h < MH; ++h) {
-            const uint64_t ad = desc_sw128(s_a + h * 128 * kStageBytes);
-            const uint32_t sfa = slot_col + L::NG * L::NB * 4 + (h * L::NG + g) * 4;
-            const uint32_t acc = first && j == 0 ? 0u : 1u;
-            if constexpr (NV) ptx::tc_mma_nvf4(tmem + h * BN, ad + 2 * j, bd + 2 * j, id, sfa, sfb, acc);
-            else ptx::tc_mma_mxf4(tmem + h * BN, ad + 2 * j, bd + 2 * j, id, sfa, sfb, acc);
-        }
-    }
+// One MMA: K step j of a stage, column part h, whose scale columns begin
+// `shift` columns into the slot's groups.  COLL: 1 leaves A in the collector
+// for the next MMA, 2 takes it from there.
+template <bool NV, class L, int COLL>
+__device__ __forceinline__ void mma_pair(uint32_t tmem, uint32_t slot_col, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                         int h, uint32_t shift, int j, uint32_t acc) {
+    const int g = NV ? j : j >> 1;
+    const uint32_t id = idesc | (NV ? 0u : ((j & 1) * 2u << 29) | ((j & 1) * 2u << 4));
+    const uint32_t sfb = slot_col + g * L::GC + h * (PH / 32) + shift, sfa = slot_col + g * L::GC + 4 * L::NB;
+    if constexpr (NV) ptx::tc_mma_nvf4_pair<COLL>(tmem + h * PH, ad + 2 * j, bd + 2 * j, id, sfa, sfb, acc);
+    else ptx::tc_mma_mxf4_pair<COLL>(tmem + h * PH, ad + 2 * j, bd + 2 * j, id, sfa, sfb, acc);
 }
-
-// ---------------------------------------------------------------- wide tiles
-constexpr int WM = 256, WN = 192, W_THREADS = 384;
-constexpr uint32_t EPI_BYTES = 4096;           // staging per epilogue warp
-template <bool NV>
-using WideLayout = Layout<NV, 2, WN, 3, NV ? 2 : 3>;
-template <bool NV>
-constexpr uint32_t wide_smem = WideLayout<NV>::OFF_MISC + 16 + 8 * EPI_BYTES + 1024;
 
 // 32 rows x 128 bytes through a warp's staging area, lane l holding row l's
 // 128 bytes (16-byte pieces XOR-swizzled by row).
@@ -205,186 +215,108 @@ __device__ __forceinline__ void write_f32(const uint8_t *stage, int lane, const 
     }
 }
 
-template <bool NV>
-__global__ void __launch_bounds__(W_THREADS, 1)
-    k_fp4_wide(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+// A wait on a barrier of this CTA whose arrivals may come from the other one.
+__device__ bool wait_pair(uint32_t bar, uint32_t parity, uint64_t limit, volatile uint32_t *abort_flag,
+                          unsigned int *err, uint32_t who) {
+    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t n = 1;; ++n) {
+        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+        if ((n & 15u) == 0) {
+            if (*abort_flag) return false;
+            if (ptx::globaltimer() - t0 > limit) {
+                *abort_flag = 1u;
+                atomicOr(err, 1u);
+                atomicCAS(err + 1, 0u, who);
+                return false;
+            }
+        }
+    }
+}
+
+template <bool NV, int NH>
+__global__ void __launch_bounds__(P_THREADS, 1)
+    k_fp4_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+               const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
                const Params p, const uint32_t idesc) {
-    using L = WideLayout<NV>;
-    constexpr int S = 3, SLOTS = NV ? 2 : 3;
+    using L = PairLayout<NV, NH>;
+    constexpr int S = L::S, SLOTS = L::SLOTS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
     const uint32_t bar = base + L::OFF_BAR;
-    const uint32_t tfull = bar + L::BAR_TFULL, tempty = tfull + 8, drain = tfull + 16, drain2 = tfull + 24;
+    const uint32_t empty = bar + L::EMPTY, scales = bar + L::SCALES, tfull = bar + L::TFULL,
+                   tempty = bar + L::TEMPTY, odd = bar + L::ODD, drain = bar + L::DRAIN;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + L::OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + L::OFF_MISC + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
     const uint64_t limit = p.wait_limit_ns, drain_limit = 2000000ull;
+    // the even CTA's barriers, as seen from either CTA
+    const uint32_t full_l = ptx::map_shared_rank(bar, 0), odd_l = ptx::map_shared_rank(odd, 0);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(bar + 8 * s, 1);                  // bytes landed
-            ptx::mbar_init(bar + L::BAR_EMPTY + 8 * s, 1);   // the stage's MMAs are done
+            ptx::mbar_init(bar + 8 * s, 1);
+            ptx::mbar_init(empty + 8 * s, 1);
         }
-        for (int i = 0; i < SLOTS; ++i) ptx::mbar_init(bar + L::BAR_SF + 8 * i, 1);
-        ptx::mbar_init(tfull, 1);
-        ptx::mbar_init(tempty, 256);
-        ptx::mbar_init(drain, 1);
-        ptx::mbar_init(drain2, 1);
+        for (int i = 0; i < SLOTS; ++i) ptx::mbar_init(scales + 8 * i, 1 + L::NB);   // the copiers
+        for (int h = 0; h < 2; ++h) {
+            ptx::mbar_init(tfull + 8 * h, 1);
+            ptx::mbar_init(tempty + 8 * h, 4);   // the half's four epilogue warps
+            ptx::mbar_init(odd + 8 * h, 1);
+        }
+        for (int i = 0; i < 5; ++i) ptx::mbar_init(drain + 8 * i, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tmap_a);
         ptx::prefetch_tmap(&tmap_b);
+        ptx::prefetch_tmap(&tmap_sa);
+        ptx::prefetch_tmap(&tmap_sb);
     }
     if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
-        ptx::tmem_relinquish();
+        ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
+        ptx::tmem_relinquish_pair();
     }
     ptx::tc_fence_before();
-    __syncthreads();
+    ptx::cluster_sync();   // both CTAs' barriers and tensor memory exist
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0) {
-        // ---------------------------------------------------------- producer
-        uint32_t it = 0;
-        bool ok = true;
-        const int rta = (p.M + 127) / 128, rtb = (p.N + 127) / 128;   // row tiles of scales
-        for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
-            int mb, nb;
-            tile_coords(tile, p.num_mb, p.num_nb, mb, nb);
-            const int ra = mb * 2, rb = nb * WN / 128;
-            const int na = min(2, rta - ra), nbt = min(2, rtb - rb);
-            const uint32_t bytes = L::STAGE + (na + nbt) * L::SF;
-            const uint8_t *ga = p.sa + static_cast<int64_t>(ra) * p.scale_tiles * 512;
-            const uint8_t *gb = p.sb + static_cast<int64_t>(rb) * p.scale_tiles * 512;
-            for (int kb = 0; kb < p.nk; ++kb) {
-                const uint32_t s = it % S, ph = (it / S) & 1u;
-                ok = wait_phase(bar + L::BAR_EMPTY + 8 * s, ph ^ 1u, limit, abort_flag, p.err, WHO_PRODUCER);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                // inject = 1 (a test of the timeout path): the first CTA
-                // never issues its first stage
-                if (lane == 0 && !(p.inject == 1 && blockIdx.x == 0 && it == 0)) {
-                    const uint32_t full = bar + 8 * s, sa = base + s * L::STAGE;
-                    const uint32_t sf = base + L::OFF_SF + s * L::SF_STAGE;
-                    ptx::mbar_arrive_expect_tx(full, bytes);
-                    ptx::tma_load_2d(sa, &tmap_a, full, kb * kStageBytes, mb * WM);
-                    ptx::tma_load_2d(sa + L::A, &tmap_b, full, kb * kStageBytes, nb * WN);
-                    const int64_t at = static_cast<int64_t>(kb) * L::SF, rt = p.scale_tiles * 512;
-                    for (int i = 0; i < na; ++i) ptx::bulk_load(sf + i * L::SF, ga + at + i * rt, L::SF, full);
-                    for (int i = 0; i < nbt; ++i)
-                        ptx::bulk_load(sf + (2 + i) * L::SF, gb + at + i * rt, L::SF, full);
-                }
-                __syncwarp();
-                ++it;
-            }
-        }
-        // the copies in flight land before the CTA ends
-        const uint32_t nd = it < S ? it : S;
-        for (uint32_t i = it - nd; i < it; ++i)
-            wait_phase(bar + 8 * (i % S), (i / S) & 1u, drain_limit, abort_flag, p.err, WHO_PRODUCER, false);
-    } else if (warp == 1) {
-        // -------------------------------------------------------- MMA issuer
-        uint32_t it = 0, tcount = 0;
-        bool ok = true;
-        for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
-            int mb, nb;
-            tile_coords(tile, p.num_mb, p.num_nb, mb, nb);
-            const uint32_t b_shift = (nb * WN % 128) / 32;
-            ok = wait_phase(tempty, (tcount & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            for (int kb = 0; kb < p.nk; ++kb) {
-                const uint32_t s = it % S, slot = it % SLOTS;
-                ok = wait_phase(bar + 8 * s, (it / S) & 1u, limit, abort_flag, p.err, WHO_MMA) &&
-                     wait_phase(bar + L::BAR_SF + 8 * slot, (it / SLOTS) & 1u, limit, abort_flag, p.err, WHO_MMA);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t sa = base + s * L::STAGE;
-                    issue_stage<NV, 2, WN, L>(tmem, tmem + L::COL_SF + slot * L::COLS, b_shift, sa, sa + L::A,
-                                              idesc, kb == 0);
-                    ptx::tc_commit(bar + L::BAR_EMPTY + 8 * s);
-                }
-                __syncwarp();
-                ++it;
-            }
-            if (!ok) break;
-            if (lane == 0) ptx::tc_commit(tfull);
-            __syncwarp();
-            ++tcount;
-        }
-        if (lane == 0) ptx::tc_commit(drain);
-        __syncwarp();
-        wait_phase(drain, 0u, drain_limit, abort_flag, p.err, WHO_MMA, false);
-    } else if (warp == 2) {
-        // ------------------------------------------- scales to tensor memory
-        uint32_t it = 0;
-        bool ok = true;
-        for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
-            for (int kb = 0; kb < p.nk; ++kb) {
-                const uint32_t s = it % S, slot = it % SLOTS;
-                ok = wait_phase(bar + 8 * s, (it / S) & 1u, limit, abort_flag, p.err, WHO_SCALES);
-                if (ok && it >= SLOTS) {
-                    // the slot is free when the MMAs of stage it - SLOTS are done
-                    const uint32_t u = it - SLOTS;
-                    ok = wait_phase(bar + L::BAR_EMPTY + 8 * (u % S), (u / S) & 1u, limit, abort_flag, p.err,
-                                    WHO_SCALES);
-                }
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t sf = base + L::OFF_SF + s * L::SF_STAGE;
-                    const uint32_t col = tmem + L::COL_SF + slot * L::COLS;
-#pragma unroll
-                    for (int g = 0; g < L::NG; ++g) {
-                        for (int i = 0; i < 2; ++i)
-                            ptx::tc_cp_32x128b_warpx4(col + g * 8 + i * 4,
-                                                      desc_scales(sf + (2 + i) * L::SF + g * 512));
-                        for (int h = 0; h < 2; ++h)
-                            ptx::tc_cp_32x128b_warpx4(col + L::NG * 8 + (h * L::NG + g) * 4,
-                                                      desc_scales(sf + h * L::SF + g * 512));
-                    }
-                    ptx::tc_commit(bar + L::BAR_SF + 8 * slot);
-                }
-                __syncwarp();
-                ++it;
-            }
-        }
-        if (lane == 0) ptx::tc_commit(drain2);
-        __syncwarp();
-        wait_phase(drain2, 0u, drain_limit, abort_flag, p.err, WHO_SCALES, false);
-    } else if (warp >= 4) {
+    // 512 threads are launched with 128 registers; the epilogue's two
+    // warpgroups take over what the others leave (2 * 128 * (168 + 80) <= 65536)
+    if (warp >= 4 && warp < 12) {
         // ---------------------------------------------------------- epilogue
+        ptx::setmaxnreg_inc<168>();
         const int q = warp & 3, half = (warp - 4) >> 2;
-        uint8_t *stage = gbase + L::OFF_MISC + 16 + (warp - 4) * EPI_BYTES;
+        uint8_t *stage = gbase + L::OFF_EPI + (warp - 4) * EPI_BYTES;
         const float alpha = (p.ta ? __ldg(p.ta) : 1.0f) * (p.tb ? __ldg(p.tb) : 1.0f);
         const bool vec = (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % (p.out_fp32 ? 4 : 8) == 0;
         uint32_t tcount = 0;
-        for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++tcount) {
+        for (int tile = half < NH ? pair : p.num_tiles; tile < p.num_tiles; tile += npairs, ++tcount) {
             int mb, nb;
             tile_coords(tile, p.num_mb, p.num_nb, mb, nb);
-            bool ok = wait_phase(tfull, tcount & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
+            bool ok = wait_phase(tfull + 8 * half, tcount & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
-            const int64_t row0 = static_cast<int64_t>(mb) * WM + half * 128 + q * 32;
-            const int64_t col0 = static_cast<int64_t>(nb) * WN;
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * WN;
+            const int64_t row0 = static_cast<int64_t>(mb) * PM + rank * 128 + q * 32;
+            const int64_t col0 = static_cast<int64_t>(nb) * L::PN + half * PH;
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * PH;
+            auto release = [&] {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(tempty + 8 * half);
+            };
             if (p.out_fp32 || p.accumulate) {
 #pragma unroll 1
-                for (int chunk = 0; chunk < WN / 32; ++chunk) {
+                for (int chunk = 0; chunk < PH / 32; ++chunk) {
                     uint32_t r[32];
                     ptx::tmem_ld_32x32b_x32(taddr + chunk * 32, r);
                     ptx::tmem_wait_ld();
-                    if (chunk == WN / 32 - 1) {
-                        ptx::tc_fence_before();
-                        ptx::mbar_arrive(tempty);
-                    }
+                    if (chunk == PH / 32 - 1) release();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
                     stage_row(stage, lane, r);
@@ -394,69 +326,286 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 }
                 continue;
             }
-            uint32_t packed[WN / 2];
+            uint32_t packed[PH / 2];
 #pragma unroll
-            for (int chunk = 0; chunk < WN / 32; ++chunk) {
-                uint32_t r[32];
-                ptx::tmem_ld_32x32b_x32(taddr + chunk * 32, r);
+            for (int chunk = 0; chunk < PH / 64; ++chunk) {
+                uint32_t r[64];
+                ptx::tmem_ld_32x32b_x64(taddr + chunk * 64, r);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    packed[chunk * 16 + e] = ptx::cvt_bf16x2(__uint_as_float(r[2 * e]) * alpha,
-                                                             __uint_as_float(r[2 * e + 1]) * alpha);
+                for (int e = 0; e < 32; ++e) {
+                    ptx::mul_f32x2(r[2 * e], r[2 * e + 1], alpha);
+                    packed[chunk * 32 + e] = ptx::cvt_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                }
             }
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(tempty);
+            release();
 #pragma unroll
-            for (int piece = 0; piece < WN / 64; ++piece) {
+            for (int piece = 0; piece < PH / 64; ++piece) {
                 stage_row(stage, lane, packed + piece * 32);
                 __syncwarp();
                 write_bf16(stage, lane, p, row0, col0 + piece * 64, vec);
                 __syncwarp();
             }
         }
+    } else {
+    ptx::setmaxnreg_dec<80>();
+    if (warp == 0) {
+        // ---------------------------------------------------------- producer
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < p.num_tiles && ok; tile += npairs) {
+                int mb, nb;
+                tile_coords(tile, p.num_mb, p.num_nb, mb, nb);
+                const int arow = mb * PM + static_cast<int>(rank) * 128;
+                const int brow = nb * L::PN + static_cast<int>(rank) * (PH / 2);
+                const int sarow = mb * 2 + static_cast<int>(rank), sbrow = nb * L::PN / 128;
+                for (int kb = 0; kb < p.nk; ++kb) {
+                    const uint32_t s = it % S, full = full_l + 8 * s;
+                    ok = wait_phase(empty + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag, p.err, WHO_PRODUCER);
+                    if (!ok) break;
+                    // inject = 1 (a test of the timeout path): the first
+                    // CTA never issues its first stage
+                    if (!(p.inject == 1 && blockIdx.x == 0 && it == 0)) {
+                        const uint32_t st = base + s * L::STAGE, sf = base + L::OFF_SF + s * L::SF_STAGE;
+                        if (leader) ptx::mbar_arrive_expect_tx(bar + 8 * s, 2 * (L::STAGE + L::SF_STAGE));
+                        ptx::tma_load_2d_pair(st, &tmap_a, full, kb * kStageBytes, arow);
+                        ptx::tma_load_2d_pair(st + L::A, &tmap_b, full, kb * kStageBytes, brow);
+                        if (NH == 2)
+                            ptx::tma_load_2d_pair(st + L::A + L::BH, &tmap_b, full, kb * kStageBytes, brow + PH);
+                        ptx::tma_load_3d_pair(sf, &tmap_sa, full, 0, kb * L::NG, sarow);
+                        ptx::tma_load_3d_pair(sf + L::SF, &tmap_sb, full, 0, kb * L::NG, sbrow);
+                    }
+                    ++it;
+                }
+            }
+            // the even CTA waits until both CTAs' last copies have landed; the
+            // cluster barrier below keeps the odd CTA resident until then
+            if (leader) {
+                const uint32_t nd = it < S ? it : S;
+                for (uint32_t i = it - nd; i < it; ++i)
+                    wait_phase(bar + 8 * (i % S), (i / S) & 1u, drain_limit, abort_flag, p.err, WHO_PRODUCER, false);
+            }
+            // A CTA that stopped early cannot tell which of its last copies
+            // have been counted: it gives them the drain bound to land.
+            if (!ok || *abort_flag) {
+                const uint64_t t0 = ptx::globaltimer();
+                while (ptx::globaltimer() - t0 < drain_limit) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1 && leader) {
+        // -------------------------------------------------------- MMA issuer
+        // The two column halves alternate, except in a tile's first and last
+        // SKEW stages, where one half's MMAs of those stages go before the
+        // other's: so the first accumulator is drained under the second one's
+        // last MMAs, and the second under the first one's first MMAs of the
+        // next tile.
+        if (lane == 0) {
+            uint32_t it = 0, tcount = 0;
+            bool ok = true;
+            uint32_t shift = 0;
+            // part h of the stage that comes `i` after stage `it`
+            auto issue = [&](uint32_t i, int h, bool zero) {
+                const uint32_t s = (it + i) % S;
+                const uint32_t st = base + s * L::STAGE, col = tmem + L::PN + (it + i) % SLOTS * L::COLS;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma_pair<NV, L, 0>(tmem, col, desc_sw128(st), desc_sw128(st + L::A + h * L::BH), idesc, h, shift, j,
+                                       zero && j == 0 ? 0u : 1u);
+                if (h == NH - 1) ptx::tc_commit_pair(empty + 8 * s, 0x3);
+            };
+            // the copiers have waited for the stage's bytes before they arrive
+            auto ready = [&](uint32_t i) {
+                return wait_phase(scales + 8 * ((it + i) % SLOTS), ((it + i) / SLOTS) & 1u, limit, abort_flag, p.err,
+                                  WHO_MMA);
+            };
+            for (int tile = pair; tile < p.num_tiles && ok; tile += npairs, ++tcount) {
+                int mb, nb;
+                tile_coords(tile, p.num_mb, p.num_nb, mb, nb);
+                shift = nb * L::PN % 128 / 32;
+                const int head = min(L::SKEW, p.nk), tail = min(L::SKEW, p.nk - head);
+                for (int h = 0; h < NH && ok; ++h) {
+                    ok = wait_phase(tempty + 8 * h, (tcount & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA) &&
+                         wait_pair(odd + 8 * h, (tcount & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA);
+                    for (int i = 0; i < head && ok; ++i) {
+                        ok = h != 0 || ready(i);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        issue(i, h, i == 0);
+                    }
+                    if (ok && tail == 0) ptx::tc_commit_pair(tfull + 8 * h, 0x3);
+                }
+                if (!ok) break;
+                it += head;
+                for (int kb = head; kb < p.nk - tail; ++kb, ++it) {
+                    ok = ready(0);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t s = it % S;
+                    const uint32_t st = base + s * L::STAGE, col = tmem + L::PN + it % SLOTS * L::COLS;
+                    const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + L::A);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        mma_pair<NV, L, NH == 2 ? 1 : 0>(tmem, col, ad, bd, idesc, 0, shift, j, 1u);
+                        if (NH == 2) mma_pair<NV, L, 2>(tmem, col, ad, bd + (L::BH >> 4), idesc, 1, shift, j, 1u);
+                    }
+                    ptx::tc_commit_pair(empty + 8 * s, 0x3);
+                }
+                for (int h = 0; h < NH && tail != 0 && ok; ++h) {
+                    for (int i = 0; i < tail && ok; ++i) {
+                        ok = h != 0 || ready(i);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        issue(i, h, false);
+                    }
+                    if (ok) ptx::tc_commit_pair(tfull + 8 * h, 0x3);
+                }
+                it += tail;
+            }
+            ptx::tc_commit_pair(drain, 0x1);
+            wait_phase(drain, 0u, drain_limit, abort_flag, p.err, WHO_MMA, false);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ forwarder (odd CTA)
+        // Tells the even CTA that this one's accumulators are drained.  An
+        // arrival in the other CTA is a release at cluster scope and waits
+        // for its thread's own stores: from an epilogue warp, with the last
+        // tile's stores in flight, that took 1300 cycles.
+        if (lane == 0) {
+            uint32_t tcount = 0;
+            bool ok = true;
+            for (int tile = pair; tile < p.num_tiles && ok; tile += npairs, ++tcount) {
+                for (int h = 0; h < NH && ok; ++h) {
+                    ok = wait_phase(tempty + 8 * h, tcount & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
+                    if (ok) ptx::mbar_arrive_cluster(odd_l + 8 * h);
+                }
+            }
+        }
+        __syncwarp();
+    } else if ((warp == 2 || warp == 3 || (warp >= 12 && warp < 11 + L::NB)) && leader) {
+        // ------------------------------------------- scales to tensor memory
+        // One of the 128-row tiles each (0: A's rows, then B's), into the slot
+        // that the MMAs of stage it - SLOTS freed.  A copy costs its
+        // thread about 80 cycles, so two copiers could not keep up with NV's
+        // 16 copies per stage.
+        if (lane == 0) {
+            const int row = warp < 4 ? warp - 2 : warp - 10;
+            const uint32_t dst = tmem + L::PN + (row == 0 ? 4 * L::NB : (row - 1) * 4);
+            const uint64_t src = desc_scales(base + L::OFF_SF + row * L::SF);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < p.num_tiles && ok; tile += npairs) {
+                for (int kb = 0; kb < p.nk; ++kb, ++it) {
+                    const uint32_t s = it % S, slot = it % SLOTS, u = it - SLOTS;
+                    ok = wait_pair(bar + 8 * s, (it / S) & 1u, limit, abort_flag, p.err, WHO_SCALES) &&
+                         (it < SLOTS || wait_phase(empty + 8 * (u % S), (u / S) & 1u, limit, abort_flag, p.err,
+                                                   WHO_SCALES));
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint64_t sd = src + s * (L::SF_STAGE >> 4);
+                    const uint32_t d = dst + slot * L::COLS;
+#pragma unroll
+                    for (int g = 0; g < L::NG; ++g) ptx::tc_cp_32x128b_warpx4_pair(d + g * L::GC, sd + g * 32);
+                    ptx::tc_commit_pair(scales + 8 * slot, 0x1);
+                }
+            }
+            ptx::tc_commit_pair(drain + 8 * (row + 1), 0x1);
+            wait_phase(drain + 8 * (row + 1), 0u, drain_limit, abort_flag, p.err, WHO_SCALES, false);
+        }
+        __syncwarp();
+    }
     }
 
-    __syncthreads();
+    // neither CTA leaves (or frees its tensor memory) while the other may still
+    // read its shared memory, signal its barriers or write its tensor memory
+    __syncwarp();
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc_pair(tmem, 512);
     }
 }
 
 // ------------------------------------------------------------------ few rows
 // P (128 rows per CTA, the MMA's M side) times Q (BN rows): with few tokens P
 // is the weights and Q the tokens, so that a token costs no row of a 128-row
-// tile.  The CTAs of a cluster take consecutive parts of K; each leaves its
-// FP32 partial tile in its own shared memory, and after a cluster barrier
-// adds up a slice of the columns from all of them, in the order of the parts
-// (the same bits every time), and stores it.
+// tile.  The CTAs of a cluster take consecutive parts of K; each sends the
+// FP32 partial sums of its tile to the CTAs that own them (a slice of P's rows
+// each), which add them up in the order of the parts (the same bits every
+// time) and store them.
+//
+// QUANT: Q comes in BF16 and the epilogue's warps, idle until the last MMA,
+// quantize it into the operand stages themselves, each CTA all of its part of
+// K: no quantization pass before the product, no codes in memory.
+//
+// What bounds a call of one token is latency: 38 MB of weights take 5.7 us,
+// and 18944 rows of 3584 take 8.4 us with the codes given.  So the first
+// stages' copies are issued before anything else is set up.
 constexpr int F_THREADS = 256;
-template <int BN>
-constexpr int few_stages = BN <= 32 ? 8 : BN == 64 ? 6 : 5;
 template <bool NV, int BN>
-using FewLayout = Layout<NV, 1, BN, few_stages<BN>, 4>;
-template <bool NV, int BN>
-constexpr uint32_t few_smem = FewLayout<NV, BN>::OFF_MISC + 16 + 1024;
+struct FewLayout {
+    static constexpr int S = BN <= 32 ? 8 : BN == 64 ? 6 : 4, SLOTS = 4, NG = NV ? 4 : 2;
+    static constexpr uint32_t SF = NG * 512, A = 128 * kStageBytes, B = BN * kStageBytes;
+    static constexpr uint32_t STAGE = A + B, OFF_SF = S * STAGE, SF_STAGE = 2 * SF;
+    static constexpr uint32_t OFF_SUM = OFF_SF + S * SF_STAGE;          // partial sums, 128 BN floats
+    // barriers: full[S], empty[S], scales[SLOTS], tfull, drain[2]
+    static constexpr uint32_t OFF_BAR = OFF_SUM + BN * 512, EMPTY = 8 * S, SCALES = 16 * S;
+    static constexpr uint32_t TFULL = SCALES + 8 * SLOTS, DRAIN = TFULL + 8;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + 256, SMEM = OFF_MISC + 16 + 1024;
+    static constexpr uint32_t COL_SF = BN, COLS = 8 * NG;
+    static constexpr uint32_t TCOLS = COL_SF + SLOTS * COLS <= 128 ? 128 : 256;
+    // each slot is freed by its stage's barrier
+    static_assert(SLOTS <= S && DRAIN + 16 <= 256 && SMEM <= 232448 && COL_SF + SLOTS * COLS <= TCOLS, "");
+};
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
+// Q in BF16, for QUANT.
+struct QInput {
+    const uint16_t *x;
+    int64_t ld, k;
+};
+
+// The four MMAs of one stage (128 rows of A by BN of B).
+template <bool NV, int BN, class L>
+__device__ __forceinline__ void issue_stage(uint32_t tmem, uint32_t slot_col, uint32_t b_shift, uint32_t s_a,
+                                            uint32_t s_b, uint32_t idesc, bool first) {
+    const uint64_t ad = desc_sw128(s_a), bd = desc_sw128(s_b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int g = NV ? j : j >> 1;
+        const uint32_t id = idesc | (NV ? 0u : ((j & 1) * 2u << 29) | ((j & 1) * 2u << 4));
+        const uint32_t sfb = slot_col + g * 4 + b_shift, sfa = slot_col + (L::NG + g) * 4;
+        const uint32_t acc = first && j == 0 ? 0u : 1u;
+        if constexpr (NV) ptx::tc_mma_nvf4(tmem, ad + 2 * j, bd + 2 * j, id, sfa, sfb, acc);
+        else ptx::tc_mma_mxf4(tmem, ad + 2 * j, bd + 2 * j, id, sfa, sfb, acc);
+    }
 }
 
-template <bool NV, int BN>
+__device__ __forceinline__ void store_out(const Params &p, int64_t at, float v) {
+    if (p.out_fp32) {
+        float *d = static_cast<float *>(p.c) + at;
+        *d = p.accumulate ? *d + v : v;
+    } else {
+        uint16_t *d = static_cast<uint16_t *>(p.c) + at;
+        if (p.accumulate) v += __uint_as_float(static_cast<uint32_t>(*d) << 16);
+        *d = static_cast<uint16_t>(ptx::cvt_bf16x2(v, 0.0f));
+    }
+}
+
+template <bool NV, int BN, bool QUANT>
 __global__ void __launch_bounds__(F_THREADS, 1)
     k_fp4_few(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-              const Params p, const uint32_t idesc) {
+              const Params p, const QInput qi, const uint32_t idesc) {
     using L = FewLayout<NV, BN>;
-    constexpr int S = few_stages<BN>, SLOTS = 4;
-    constexpr uint32_t TCOLS = L::COL_SF + SLOTS * L::COLS <= 128 ? 128 : 256;
+    constexpr int S = L::S, SLOTS = L::SLOTS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
     const uint32_t bar = base + L::OFF_BAR;
-    const uint32_t tfull = bar + L::BAR_TFULL, drain = tfull + 16, drain2 = tfull + 24;
+    const uint32_t tfull = bar + L::TFULL, drain = bar + L::DRAIN;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + L::OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + L::OFF_MISC + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -466,52 +615,66 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     const int kb0 = static_cast<int>(static_cast<int64_t>(part) * p.nk / splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * p.nk / splits);
     const int n = kb1 - kb0;                         // at least 1: splits <= nk
+    const int64_t row0 = static_cast<int64_t>(mb) * 128, col0 = static_cast<int64_t>(nb) * BN;
+    const int cols = static_cast<int>(min(static_cast<int64_t>(BN), p.N - col0));
+    const int rl = 7 - (31 - __clz(splits));               // this CTA's share of the sums: 2^rl rows
+    const int lr = cols <= 1 ? 0 : 32 - __clz(cols - 1);   // QUANT: 2^lr >= cols
+
+    const uint8_t *ga = p.sa + static_cast<int64_t>(mb) * p.scale_tiles * 512;
+    const uint8_t *gb = QUANT ? nullptr : p.sb + static_cast<int64_t>(nb) * BN / 128 * p.scale_tiles * 512;
+    auto load_stage = [&](int it) {
+        // inject = 1 (a test of the timeout path): the first CTA never issues
+        // its first stage
+        if (p.inject == 1 && blockIdx.x == 0 && it == 0) return;
+        const int s = it % S, kb = kb0 + it;
+        const uint32_t full = bar + 8 * s, sa = base + s * L::STAGE, sf = base + L::OFF_SF + s * L::SF_STAGE;
+        const int64_t at = static_cast<int64_t>(kb) * L::SF;
+        ptx::mbar_arrive_expect_tx(full, QUANT ? L::A + L::SF : L::STAGE + 2 * L::SF);
+        ptx::tma_load_2d(sa, &tmap_a, full, kb * kStageBytes, mb * 128);
+        ptx::bulk_load(sf, ga + at, L::SF, full);
+        if (!QUANT) {
+            ptx::tma_load_2d(sa + L::A, &tmap_b, full, kb * kStageBytes, nb * BN);
+            ptx::bulk_load(sf + L::SF, gb + at, L::SF, full);
+        }
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(bar + 8 * s, 1);
-            ptx::mbar_init(bar + L::BAR_EMPTY + 8 * s, 1);
+            ptx::mbar_init(bar + 8 * s, QUANT ? 1 + min(128, 16 << lr) : 1);   // the copies, the quantizing threads
+            ptx::mbar_init(bar + L::EMPTY + 8 * s, 1);
         }
-        for (int i = 0; i < SLOTS; ++i) ptx::mbar_init(bar + L::BAR_SF + 8 * i, 1);
+        for (int i = 0; i < SLOTS; ++i) ptx::mbar_init(bar + L::SCALES + 8 * i, 1);
         ptx::mbar_init(tfull, 1);
         ptx::mbar_init(drain, 1);
-        ptx::mbar_init(drain2, 1);
+        ptx::mbar_init(drain + 8, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
+        for (int it = 0; it < 2 && it < n; ++it) load_stage(it);
     }
     if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TCOLS);
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::TCOLS);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    // the others may write this CTA's shared memory once all have come here
+    if (splits > 1) ptx::cluster_arrive();
     const uint32_t tmem = *tmem_slot;
-    bool done = true;                                // this thread saw the accumulator complete
 
     if (warp == 0) {
-        const uint8_t *ga = p.sa + static_cast<int64_t>(mb) * p.scale_tiles * 512;
-        const uint8_t *gb = p.sb + static_cast<int64_t>(nb) * BN / 128 * p.scale_tiles * 512;
-        int it = 0;
+        int it = n < 2 ? n : 2;
         for (; it < n; ++it) {
             const int s = it % S;
-            bool ok = wait_phase(bar + L::BAR_EMPTY + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag, p.err,
-                                 WHO_PRODUCER);
+            bool ok = it < S || wait_phase(bar + L::EMPTY + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag, p.err, WHO_PRODUCER);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            if (lane == 0 && !(p.inject == 1 && blockIdx.x == 0 && it == 0)) {
-                const uint32_t full = bar + 8 * s, sa = base + s * L::STAGE;
-                const uint32_t sf = base + L::OFF_SF + s * L::SF_STAGE;
-                const int kb = kb0 + it;
-                const int64_t at = static_cast<int64_t>(kb) * L::SF;
-                ptx::mbar_arrive_expect_tx(full, L::STAGE + 2 * L::SF);
-                ptx::tma_load_2d(sa, &tmap_a, full, kb * kStageBytes, mb * 128);
-                ptx::tma_load_2d(sa + L::A, &tmap_b, full, kb * kStageBytes, nb * BN);
-                ptx::bulk_load(sf, ga + at, L::SF, full);
-                ptx::bulk_load(sf + L::SF, gb + at, L::SF, full);
-            }
+            if (lane == 0) load_stage(it);
             __syncwarp();
         }
+        // the copies in flight land before the CTA ends.  With QUANT a stage's
+        // phase also waits for the quantizing threads: where they have given
+        // up, the bound passes instead, in which the copies (microseconds) land.
         for (int i = it > S ? it - S : 0; i < it; ++i)
             wait_phase(bar + 8 * (i % S), (i / S) & 1u, drain_limit, abort_flag, p.err, WHO_PRODUCER, false);
     } else if (warp == 1) {
@@ -520,15 +683,14 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         for (int it = 0; it < n && ok; ++it) {
             const int s = it % S, slot = it % SLOTS;
             ok = wait_phase(bar + 8 * s, (it / S) & 1u, limit, abort_flag, p.err, WHO_MMA) &&
-                 wait_phase(bar + L::BAR_SF + 8 * slot, (it / SLOTS) & 1u, limit, abort_flag, p.err, WHO_MMA);
+                 wait_phase(bar + L::SCALES + 8 * slot, (it / SLOTS) & 1u, limit, abort_flag, p.err, WHO_MMA);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
             if (lane == 0) {
                 const uint32_t sa = base + s * L::STAGE;
-                issue_stage<NV, 1, BN, L>(tmem, tmem + L::COL_SF + slot * L::COLS, b_shift, sa, sa + L::A, idesc,
-                                          it == 0);
-                ptx::tc_commit(bar + L::BAR_EMPTY + 8 * s);
+                issue_stage<NV, BN, L>(tmem, tmem + L::COL_SF + slot * L::COLS, b_shift, sa, sa + L::A, idesc, it == 0);
+                ptx::tc_commit(bar + L::EMPTY + 8 * s);
             }
             __syncwarp();
         }
@@ -545,8 +707,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             ok = wait_phase(bar + 8 * s, (it / S) & 1u, limit, abort_flag, p.err, WHO_SCALES);
             if (ok && it >= SLOTS) {
                 const int u = it - SLOTS;
-                ok = wait_phase(bar + L::BAR_EMPTY + 8 * (u % S), (u / S) & 1u, limit, abort_flag, p.err,
-                                WHO_SCALES);
+                ok = wait_phase(bar + L::EMPTY + 8 * (u % S), (u / S) & 1u, limit, abort_flag, p.err, WHO_SCALES);
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
@@ -557,73 +718,134 @@ __global__ void __launch_bounds__(F_THREADS, 1)
 #pragma unroll
                 for (int g = 0; g < L::NG; ++g) {
                     ptx::tc_cp_32x128b_warpx4(col + g * 4, desc_scales(sf + L::SF + g * 512));
-                    ptx::tc_cp_32x128b_warpx4(col + L::NG * 4 + g * 4, desc_scales(sf + g * 512));
+                    ptx::tc_cp_32x128b_warpx4(col + (L::NG + g) * 4, desc_scales(sf + g * 512));
                 }
-                ptx::tc_commit(bar + L::BAR_SF + 8 * slot);
+                ptx::tc_commit(bar + L::SCALES + 8 * slot);
             }
             __syncwarp();
         }
-        if (lane == 0) ptx::tc_commit(drain2);
+        if (lane == 0) ptx::tc_commit(drain + 8);
         __syncwarp();
-        wait_phase(drain2, 0u, drain_limit, abort_flag, p.err, WHO_SCALES, false);
+        wait_phase(drain + 8, 0u, drain_limit, abort_flag, p.err, WHO_SCALES, false);
     } else if (warp >= 4) {
-        // the partial tile, column by column of 128 rows, over the operand
-        // stages (every copy and MMA is done once tfull completes)
-        done = wait_phase(tfull, 0u, limit, abort_flag, p.err, WHO_EPILOGUE);
-        done = __all_sync(0xFFFFFFFFu, done);
-        if (done) {
-            ptx::tc_fence_after();
-            float *part_tile = reinterpret_cast<float *>(gbase);
-            const int q = warp & 3;
-#pragma unroll 1
-            for (int c = 0; c < BN; c += 16) {
-                uint32_t r[16];
-                ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, r);
-                ptx::tmem_wait_ld();
+        bool ok = true;
+        if constexpr (QUANT) {
+            // The segments of 16 elements of a stage, 2^lr rows by 16 of them,
+            // go round the 128 threads, stage after stage; a thread has the
+            // loads of eight in flight (one token: all of its K in one go).
+            // Rows past the last are not written: they only reach outputs
+            // that are not stored.
+            const int tid = threadIdx.x - 128;
+            const float t = NV && p.tb ? __ldg(p.tb) : 1.0f;
+            for (int it0 = 0; it0 < n && ok; it0 += 64 >> lr) {
+                uint32_t w[8][8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) part_tile[(c + i) * 129 + q * 32 + lane] = __uint_as_float(r[i]);
+                for (int a = 0; a < 8; ++a) {
+                    const int idx = a * 128 + tid, row = (idx >> 4) & ((1 << lr) - 1), it = it0 + (idx >> (4 + lr));
+                    const int64_t c0 = static_cast<int64_t>(kb0 + it) * 256 + (idx & 15) * 16;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[a][e] = 0u;
+                    if (it < n && row < cols && c0 < qi.k)
+                        ragged::load16<false>(qi.x + (col0 + row) * qi.ld + c0, qi.k - c0, w[a]);
+                }
+#pragma unroll
+                for (int a = 0; a < 8; ++a) {
+                    const int idx = a * 128 + tid, row = (idx >> 4) & ((1 << lr) - 1), seg = idx & 15;
+                    const int it = it0 + (idx >> (4 + lr)), s = it % S;
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m = __vmaxu2(m, w[a][e] & 0x7FFF7FFFu);
+                    m = max(m & 0xFFFFu, m >> 16);
+                    if (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                    ok = ok && (it >= n || wait_phase(bar + L::EMPTY + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag,
+                                                      p.err, WHO_EPILOGUE));
+                    if (it < n && ok) {
+                        if (row < cols) {
+                            uint8_t *sq = gbase + s * L::STAGE + L::A;
+                            uint8_t *sf = gbase + L::OFF_SF + s * L::SF_STAGE + L::SF;
+                            const Fp4Scale<NV> sc(m, t);
+                            // the 128-byte swizzle of the operand tile
+                            *reinterpret_cast<uint2 *>(sq + row * 128 + (((seg >> 1) ^ (row & 7)) << 4) +
+                                                       (seg & 1) * 8) = make_uint2(sc.cast8(w[a]), sc.cast8(w[a] + 4));
+                            const int j = NV ? seg : seg >> 1;
+                            if (NV || (seg & 1) == 0)
+                                sf[(j >> 2) * 512 + row * 16 + (j & 3)] = static_cast<uint8_t>(sc.byte);
+                        }
+                        // once per stage: with more than eight rows after the
+                        // thread's last segment of it
+                        if (lr <= 3 || ((a + 1) & ((1 << (lr - 3)) - 1)) == 0) {
+                            ptx::fence_proxy_async_smem();
+                            ptx::mbar_arrive(bar + 8 * s);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        ok = ok && wait_phase(tfull, 0u, limit, abort_flag, p.err, WHO_EPILOGUE);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (splits > 1) ptx::cluster_wait();
+        if (ok) {
+            // row r's sums go to CTA r / (128 / splits): [part][column][its rows]
+            ptx::tc_fence_after();
+            const int q = warp & 3, r = q * 32 + lane;
+            const uint32_t off = base + L::OFF_SUM + (((part * BN) << rl) + (r & ((1 << rl) - 1))) * 4;
+            const uint32_t dst = splits > 1 ? ptx::map_shared_rank(off, r >> rl) : off, step = 4u << rl;
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 16) {
+                uint32_t v[16];
+                ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+                ptx::tmem_wait_ld();
+                const uint32_t d = dst + c * step;
+                if (splits > 1) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < cols) ptx::st_cluster_u32(d + i * step, v[i]);
+                } else {
+                    // columns past the last have room
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) ptx::st_shared_u32(d + i * step, v[i]);
+                }
             }
             ptx::tc_fence_before();
         }
     }
 
-    __syncthreads();
-    if (splits > 1) ptx::cluster_sync();
+    __syncwarp();
+    if (splits > 1) {
+        if (warp < 4) ptx::cluster_wait();
+        ptx::cluster_sync();
+    } else {
+        __syncthreads();
+    }
     if (!*abort_flag) {
         const float alpha = (p.ta ? __ldg(p.ta) : 1.0f) * (p.tb ? __ldg(p.tb) : 1.0f);
-        const int c0 = part * BN / splits, c1 = (part + 1) * BN / splits;
-        const int64_t row0 = static_cast<int64_t>(mb) * 128, col0 = static_cast<int64_t>(nb) * BN;
-        // consecutive threads along the output's contiguous direction
-        const bool along_p = p.sm == 1;
-        const int nc = c1 - c0;
-        for (int i = threadIdx.x; i < nc * 128; i += F_THREADS) {
-            const int r = along_p ? i & 127 : i / nc, c = along_p ? c0 + (i >> 7) : c0 + i % nc;
-            if (row0 + r >= p.M || col0 + c >= p.N) continue;
-            float v = 0.0f;
-            const uint32_t off = (c * 129 + r) * 4;
-            if (splits == 1) {
-                v = *reinterpret_cast<const float *>(gbase + off);
-            } else {
-                for (int k = 0; k < splits; ++k) v += ld_cluster_f32(ptx::map_shared_rank(base + off, k));
-            }
-            v *= alpha;
-            const int64_t at = (row0 + r) * p.sm + (col0 + c) * p.sn;
-            if (p.out_fp32) {
-                float *d = static_cast<float *>(p.c) + at;
-                *d = p.accumulate ? *d + v : v;
-            } else {
-                uint16_t *d = static_cast<uint16_t *>(p.c) + at;
-                if (p.accumulate) v += __uint_as_float(static_cast<uint32_t>(*d) << 16);
-                *d = static_cast<uint16_t>(ptx::cvt_bf16x2(v, 0.0f));
+        // this CTA's rows, one to a thread group's lane; columns go round the
+        // groups
+        const float *sum = reinterpret_cast<const float *>(gbase + L::OFF_SUM);
+        const int r = threadIdx.x & ((1 << rl) - 1);
+        const int64_t row = row0 + (part << rl) + r;
+        if (row < p.M) {
+            const int dc = F_THREADS >> rl;
+            for (int c = threadIdx.x >> rl; c < cols; c += 8 * dc) {
+                // eight columns' sums before their stores: a store through a
+                // generic pointer keeps later shared-memory reads behind it
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+                for (int k = 0; k < splits; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i * dc < cols) v[i] += sum[((k * BN + c + i * dc) << rl) + r];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i * dc < cols) store_out(p, row * p.sm + (col0 + c + i * dc) * p.sn, v[i] * alpha);
             }
         }
     }
-    // no CTA leaves while another still reads its shared memory
-    __syncwarp();
-    if (splits > 1) ptx::cluster_sync();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, TCOLS);
+        ptx::tmem_dealloc(tmem, L::TCOLS);
     }
 }
 
@@ -640,6 +862,21 @@ bool make_tmap(CUtensorMap *m, const Fp4Operand &o, uint32_t box_rows) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The scale tiles of an operand, [row tiles, tiles along K, 128 words], and a
+// copy of `rows` row tiles by one stage.
+bool make_scale_tmap(CUtensorMap *m, const Fp4Operand &o, int rows) {
+    TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    std::memset(m, 0, sizeof(*m));
+    const int64_t tiles = fp4_scale_tiles(o.k, o.kind);
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(tiles), static_cast<cuuint64_t>(fp4_row_tiles(o.rows))};
+    const cuuint64_t strides[2] = {512, static_cast<cuuint64_t>(tiles) * 512};
+    const cuuint32_t box[3] = {128, o.kind == FP4_NV ? 4u : 2u, static_cast<cuuint32_t>(rows)}, estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(o.scale), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 std::mutex g_mu;
 int g_sms[64] = {0};
 
@@ -649,37 +886,136 @@ cudaError_t allow_smem(K kern, uint32_t bytes) {
 }
 template <bool NV>
 cudaError_t set_attributes() {
-    cudaError_t e = allow_smem(k_fp4_wide<NV>, wide_smem<NV>);
-    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 16>, few_smem<NV, 16>);
-    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 32>, few_smem<NV, 32>);
-    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 64>, few_smem<NV, 64>);
-    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 128>, few_smem<NV, 128>);
+    cudaError_t e = allow_smem(k_fp4_pair<NV, 2>, PairLayout<NV, 2>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_pair<NV, 1>, PairLayout<NV, 1>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 16, false>, FewLayout<NV, 16>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 16, true>, FewLayout<NV, 16>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 32, true>, FewLayout<NV, 32>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 32, false>, FewLayout<NV, 32>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 64, false>, FewLayout<NV, 64>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 128, false>, FewLayout<NV, 128>::SMEM);
     return e;
 }
 
 // Instruction descriptor of the 4-bit kinds: E2M1 (1) for A and B in bits 7-9
 // and 10-12, N >> 3 in bits 17-22, the scale type in bit 23 (0: E4M3, 1:
 // UE8M0), M >> 4 in bits 24-28; scale-factor ids are added per MMA.
-uint32_t instruction(bool nv, int n) {
+uint32_t instruction(bool nv, int m, int n) {
     return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((nv ? 0u : 1u) << 23) |
-           (static_cast<uint32_t>(128 >> 4) << 24);
+           (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-template <bool NV, int BN>
-cudaError_t launch_few(const CUtensorMap &ta, const CUtensorMap &tb, const Params &p, cudaStream_t stream) {
+template <class K, class... Args>
+int launch_cluster(K kern, int64_t ctas, int cluster, int threads, uint32_t smem, cudaStream_t stream,
+                   const Args &...args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.num_tiles * p.splits));
-    cfg.blockDim = dim3(F_THREADS);
-    cfg.dynamicSmemBytes = few_smem<NV, BN>;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_fp4_few<NV, BN>, ta, tb, p, instruction(NV, BN));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e == cudaSuccess ? 0 : 2 + static_cast<int>(e);
+}
+
+// P and Q: the operands on the MMA's M and N side; swapped: P is B.
+void set_operands(Params &p, const Fp4GemmArgs &g, bool swapped, int tm, int tn) {
+    const Fp4Operand &P = swapped ? g.b : g.a, &Q = swapped ? g.a : g.b;
+    p.M = static_cast<int>(P.rows);
+    p.N = static_cast<int>(Q.rows);
+    p.num_mb = (p.M + tm - 1) / tm;
+    p.num_nb = (p.N + tn - 1) / tn;
+    p.sa = P.scale;
+    p.sb = Q.scale;
+    p.ta = P.ts;
+    p.tb = Q.ts;
+    p.sm = swapped ? 1 : g.ldc;
+    p.sn = swapped ? g.ldc : 1;
+}
+
+template <bool NV, int NH>
+int launch_pair(const Fp4GemmArgs &g, Params &p, int sms, cudaStream_t stream) {
+    using L = PairLayout<NV, NH>;
+    set_operands(p, g, false, PM, L::PN);
+    const int64_t tiles = static_cast<int64_t>(p.num_mb) * p.num_nb;
+    if (tiles > 0x7FFFFFFF) return 2 + static_cast<int>(cudaErrorInvalidValue);
+    p.num_tiles = static_cast<int>(tiles);
+    CUtensorMap ta, tb, tsa, tsb;
+    if (!make_tmap(&ta, g.a, 128) || !make_tmap(&tb, g.b, PH / 2) || !make_scale_tmap(&tsa, g.a, 1) ||
+        !make_scale_tmap(&tsb, g.b, L::NB))
+        return 1;
+    return launch_cluster(k_fp4_pair<NV, NH>, 2 * std::min<int64_t>(tiles, sms / 2), 2, P_THREADS, L::SMEM, stream, ta,
+                          tb, tsa, tsb, p, instruction(NV, PM, PH));
+}
+
+template <bool NV, int BN, bool QUANT>
+int launch_few(const Fp4GemmArgs &g, Params &p, bool swapped, int splits, cudaStream_t stream) {
+    set_operands(p, g, swapped, 128, BN);
+    const int64_t tiles = static_cast<int64_t>(p.num_mb) * p.num_nb;
+    if (tiles > 0x7FFFFFFF / 8) return 2 + static_cast<int>(cudaErrorInvalidValue);
+    p.num_tiles = static_cast<int>(tiles);
+    p.splits = splits;
+    CUtensorMap ta, tb;
+    if (!make_tmap(&ta, swapped ? g.b : g.a, 128)) return 1;
+    if (QUANT) tb = ta;   // not used
+    else if (!make_tmap(&tb, swapped ? g.a : g.b, BN)) return 1;
+    const QInput qi{g.x, g.ld_x, g.a.k};
+    return launch_cluster(k_fp4_few<NV, BN, QUANT>, tiles * splits, splits, F_THREADS, FewLayout<NV, BN>::SMEM, stream,
+                          ta, tb, p, qi, instruction(NV, 128, BN));
+}
+
+// Which kernel, from its time as measured on a GB300 (microseconds; MX, NV is
+// alike, 5 to 15 % slower throughout): a fixed part, then for every round of
+// tiles over the machine a part per stage of K and one per tile.
+//   pairs        4.5 + rounds (0.49 nk + 1.8) with 384 columns, (0.31 nk + 1.5) with 192
+//   few rows     3.8 + rounds (c nk / splits + e), (c, e) by the tile's columns: 0.29, 0.4 for 16
+//                ... 0.48, 2 for 128
+// So 8192 x 18944 x 3584 takes 191 us with 384 columns and 248 with 192; 1000 x
+// 3584 x 18944 44 and 31; 200 x 1536 x 8960 17 with pairs and 10 with four K
+// parts of few-row tiles; 128 x 18944 x 3584 15 and 17.
+struct Plan {
+    int nh, bn, splits;     // nh > 0: pair tiles of 192 nh columns; else bn and K parts
+    double us;
+};
+
+double rounds(int64_t tiles, int64_t slots) { return static_cast<double>((tiles + slots - 1) / slots); }
+
+Plan choose_few(int64_t rows, int64_t other, int nk, int sms) {
+    const int widths[4] = {16, 32, 64, 128};
+    const double stage[4] = {0.29, 0.31, 0.38, 0.48}, tile[4] = {0.4, 0.7, 1.6, 2.0};
+    Plan best{0, 16, 1, 1e300};
+    // the narrowest that holds all rows; of 64 and 128, with several tiles, the
+    // faster one (a tile of 16 or 32 columns cannot begin inside a scale tile)
+    for (int i = 0; i < 4; ++i) {
+        if (widths[i] < rows && i < 2) continue;
+        const int64_t tiles = (other + 127) / 128 * ((rows + widths[i] - 1) / widths[i]);
+        for (int s = 1; s <= 8 && s <= nk; s *= 2) {
+            // clusters of eight leave SMs of each GPC over
+            const double us = 3.8 + rounds(tiles * s, s == 8 && sms >= 10 ? sms * 4 / 5 : sms) *
+                                        (stage[i] * ((nk + s - 1) / s) + tile[i]);
+            if (us < best.us) best = {0, widths[i], s, us};
+        }
+        if (widths[i] >= rows) break;
+    }
+    return best;
+}
+
+Plan choose(int64_t m, int64_t n, int nk, int sms) {
+    Plan best = choose_few(std::min(m, n), std::max(m, n), nk, sms);
+    if (std::min(m, n) > 32 && sms >= 2) {
+        const int64_t mb = (m + PM - 1) / PM;
+        const double two = 4.5 + rounds(mb * ((n + 383) / 384), sms / 2) * (0.49 * nk + 1.8);
+        const double one = 4.5 + rounds(mb * ((n + 191) / 192), sms / 2) * (0.31 * nk + 1.5);
+        if (two < best.us) best = {2, 0, 1, two};
+        if (one < best.us) best = {1, 0, 1, one};
+    }
+    return best;
 }
 
 template <bool NV>
@@ -693,58 +1029,26 @@ int launch(const Fp4GemmArgs &g, int sms, cudaStream_t stream) {
     p.inject = g.inject_fault;
     p.wait_limit_ns = g.wait_limit_ns;
     p.err = g.err;
-    p.splits = 1;
-    CUtensorMap ta, tb;
-    const int64_t wide_tiles = ((g.a.rows + WM - 1) / WM) * ((g.b.rows + WN - 1) / WN);
-    if (g.a.rows > 128 && g.b.rows > 128 && 2 * wide_tiles > sms) {
-        p.M = static_cast<int>(g.a.rows);
-        p.N = static_cast<int>(g.b.rows);
-        p.num_mb = (p.M + WM - 1) / WM;
-        p.num_nb = (p.N + WN - 1) / WN;
-        if (wide_tiles > 0x7FFFFFFF) return 2 + static_cast<int>(cudaErrorInvalidValue);
-        p.num_tiles = static_cast<int>(wide_tiles);
-        p.sa = g.a.scale;
-        p.sb = g.b.scale;
-        p.ta = g.a.ts;
-        p.tb = g.b.ts;
-        p.sm = g.ldc;
-        p.sn = 1;
-        if (!make_tmap(&ta, g.a, WM) || !make_tmap(&tb, g.b, WN)) return 1;
-        const int grid = p.num_tiles < sms ? p.num_tiles : sms;
-        k_fp4_wide<NV><<<grid, W_THREADS, wide_smem<NV>, stream>>>(ta, tb, p, instruction(NV, WN));
-        const cudaError_t e = cudaGetLastError();
-        return e == cudaSuccess ? 0 : 2 + static_cast<int>(e);
+    if (g.x) {
+        const Plan plan = choose_few(g.a.rows, g.b.rows, p.nk, sms);
+        return plan.bn == 16 ? launch_few<NV, 16, true>(g, p, true, plan.splits, stream)
+                             : launch_few<NV, 32, true>(g, p, true, plan.splits, stream);
     }
-    // few rows on one side (or few tiles): that side is Q
-    const bool swap = g.a.rows <= g.b.rows;
-    const Fp4Operand &P = swap ? g.b : g.a, &Q = swap ? g.a : g.b;
-    p.M = static_cast<int>(P.rows);
-    p.N = static_cast<int>(Q.rows);
-    p.sa = P.scale;
-    p.sb = Q.scale;
-    p.ta = P.ts;
-    p.tb = Q.ts;
-    p.sm = swap ? 1 : g.ldc;
-    p.sn = swap ? g.ldc : 1;
-    const int bn = p.N <= 16 ? 16 : p.N <= 32 ? 32 : p.N <= 64 ? 64 : 128;
-    p.num_mb = (p.M + 127) / 128;
-    p.num_nb = (p.N + bn - 1) / bn;
-    const int64_t tiles = static_cast<int64_t>(p.num_mb) * p.num_nb;
-    if (tiles > 0x7FFFFFFF / 8) return 2 + static_cast<int>(cudaErrorInvalidValue);
-    p.num_tiles = static_cast<int>(tiles);
-    while (p.splits < 8 && p.splits * 2 <= p.nk && tiles * p.splits * 2 <= sms) p.splits *= 2;
-    if (!make_tmap(&ta, P, 128) || !make_tmap(&tb, Q, static_cast<uint32_t>(bn))) return 1;
-    cudaError_t e;
-    switch (bn) {
-    case 16: e = launch_few<NV, 16>(ta, tb, p, stream); break;
-    case 32: e = launch_few<NV, 32>(ta, tb, p, stream); break;
-    case 64: e = launch_few<NV, 64>(ta, tb, p, stream); break;
-    default: e = launch_few<NV, 128>(ta, tb, p, stream); break;
+    const bool swapped = g.a.rows <= g.b.rows;
+    const Plan plan = choose(g.a.rows, g.b.rows, p.nk, sms);
+    if (plan.nh == 2) return launch_pair<NV, 2>(g, p, sms, stream);
+    if (plan.nh == 1) return launch_pair<NV, 1>(g, p, sms, stream);
+    switch (plan.bn) {
+    case 16: return launch_few<NV, 16, false>(g, p, swapped, plan.splits, stream);
+    case 32: return launch_few<NV, 32, false>(g, p, swapped, plan.splits, stream);
+    case 64: return launch_few<NV, 64, false>(g, p, swapped, plan.splits, stream);
+    default: return launch_few<NV, 128, false>(g, p, swapped, plan.splits, stream);
     }
-    return e == cudaSuccess ? 0 : 2 + static_cast<int>(e);
 }
 
 }  // namespace
+
+bool fp4_linear_quantizes(int64_t rows) { return rows <= 32; }
 
 int launch_fp4_gemm(const Fp4GemmArgs &g, cudaStream_t stream) {
     int dev = 0;

@@ -48,6 +48,8 @@ cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, int64_t ld_out, i
 
 struct Fp4GemmArgs {
     Fp4Operand a, b;
+    const uint16_t *x = nullptr;   // A in BF16 instead, quantized on the way (then a: rows, k, kind, ts)
+    int64_t ld_x = 0;
     void *c;
     int64_t ldc;
     int out_fp32, accumulate;
@@ -55,6 +57,8 @@ struct Fp4GemmArgs {
     int inject_fault;
     unsigned int *err;
 };
+// Whether launch_fp4_gemm takes so many rows of A in BF16.
+bool fp4_linear_quantizes(int64_t rows);
 // 0 on success, 1 if a tensor map could not be encoded, cudaError_t + 2 on a
 // launch failure.
 int launch_fp4_gemm(const Fp4GemmArgs &g, cudaStream_t stream);

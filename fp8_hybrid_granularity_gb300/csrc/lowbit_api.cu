@@ -178,7 +178,7 @@ int fp4_gemm_scaled(const fp4hg_operand *a, const fp4hg_operand *b, void *c, int
 }
 
 size_t fp4_linear_workspace(int64_t rows, int64_t k, int kind) {
-    if (rows <= 0 || k <= 0 || !valid_kind(kind)) return 0;
+    if (rows <= 0 || k <= 0 || !valid_kind(kind) || fp8hg::fp4_linear_quantizes(rows)) return 0;
     return static_cast<size_t>(rows * codes_ld(k)) + fp4_scale_bytes(rows, k, kind);
 }
 
@@ -198,21 +198,29 @@ int fp4_linear(const uint16_t *x, int64_t rows, int64_t ld_x, const float *tenso
     if (rows == 0 || w->rows == 0) return FP8HG_OK;
     st = check_output(y, ld_y, w->rows, out);
     if (st != FP8HG_OK) return st;
-    if (!workspace || workspace_bytes < fp4_linear_workspace(rows, w->k, w->kind))
-        return FP8HG_ERR_INVALID_ARG;
-    if (!aligned(workspace, 16)) return FP8HG_ERR_ALIGNMENT;
-    const int64_t ld = codes_ld(w->k);
-    uint8_t *codes = static_cast<uint8_t *>(workspace), *scale = codes + rows * ld;
-    const cudaError_t e = fp8hg::launch_fp4_quant(
-        {x, rows, w->k, ld_x, w->kind, tensor_scale, codes, ld, scale, nullptr, 0, nullptr},
-        static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return FP8HG_ERR_CUDA;
     fp8hg::Fp4GemmArgs g{};
-    g.a = {codes, scale, tensor_scale, rows, w->k, ld, w->kind};
+    g.a = {nullptr, nullptr, tensor_scale, rows, w->k, 0, w->kind};
     g.b = operand(w);
     g.c = y;
     g.ldc = ld_y;
     g.out_fp32 = out == FP8HG_OUT_FP32;
+    if (fp8hg::fp4_linear_quantizes(rows)) {
+        g.x = x;
+        g.ld_x = ld_x;
+        return run_gemm(g, opts, stream);
+    }
+    if (!workspace || workspace_bytes < fp4_linear_workspace(rows, w->k, w->kind))
+        return FP8HG_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return FP8HG_ERR_ALIGNMENT;
+    uint8_t *codes = static_cast<uint8_t *>(workspace);
+    g.a.codes = codes;
+    g.a.ld = codes_ld(w->k);
+    uint8_t *scale = codes + rows * g.a.ld;
+    g.a.scale = scale;
+    const cudaError_t e = fp8hg::launch_fp4_quant(
+        {x, rows, w->k, ld_x, w->kind, tensor_scale, codes, g.a.ld, scale, nullptr, 0, nullptr},
+        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return FP8HG_ERR_CUDA;
     return run_gemm(g, opts, stream);
 }
 

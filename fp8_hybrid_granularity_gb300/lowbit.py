@@ -257,10 +257,10 @@ def fp4_gemm_scaled(a: Fp4Tensor, b: Fp4Tensor, out=None, out_dtype=None, accumu
 
 
 def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, workspace=None,
-               stream=None):
+               wait_limit_ns: int = 0, inject_fault: int = 0, stream=None):
     """y = x w^T: x [rows, k] BF16 is quantized like w and multiplied, in one
     call.  workspace: optional uint8 tensor of fp4_linear_workspace(...)
-    bytes (allocated per call if None)."""
+    bytes (allocated per call if None; up to 32 rows none is needed)."""
     _check_matrix(x)
     if x.shape[1] != w.k:
         raise ValueError(f"x has {x.shape[1]} columns, w {w.k}")
@@ -269,13 +269,14 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
         out = torch.empty((rows, w.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
     _check_out(out, rows, w.rows)
     f = _fns()
-    if workspace is None:
-        workspace = torch.empty(f.fp4_linear_workspace(rows, w.k, w.kind), dtype=torch.uint8,
-                                device=x.device)
+    n = f.fp4_linear_workspace(rows, w.k, w.kind)
+    if n and workspace is None:
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     ow = w.operand()
     _check(f.fp4_linear(x.data_ptr(), rows, _ld(x), _ts(tensor_scale), ctypes.byref(ow),
-                        out.data_ptr(), _ld(out), _out_kind(out), workspace.data_ptr(),
-                        workspace.numel(), None, _on(stream, x)), "fp4_linear")
+                        out.data_ptr(), _ld(out), _out_kind(out),
+                        workspace.data_ptr() if n else None, workspace.numel() if n else 0,
+                        _opts(wait_limit_ns, inject_fault), _on(stream, x)), "fp4_linear")
     return out
 
 

@@ -123,17 +123,18 @@ int fp4_gemm_scaled(const fp4hg_operand *a, const fp4hg_operand *b, void *c, int
                     int accumulate, const fp8hg_gemm_opts *opts, void *stream);
 
 /*
- * fp4_linear — y = x w^T with x quantized on the way: the same result as
- * fp4_quant of x followed by fp4_gemm_scaled, in one call.
+ * fp4_linear — y = x w^T with x quantized on the way: the result of fp4_quant
+ * of x followed by fp4_gemm_scaled, in one call.  Up to 32 rows (decoding) x
+ * is quantized inside the product.
  *
  *   x, ld_x        [rows, w->k] BF16, as fp4_quant
  *   tensor_scale   x's, as fp4_quant
  *   w              the weights, [n, k]
  *   y              [rows, n], row stride ld_y elements
  *   workspace      fp4_linear_workspace(rows, w->k, w->kind) bytes of device
- *                  memory, 16-byte aligned, owned by the caller; need not be
- *                  cleared.  Calls that may overlap on the GPU need separate
- *                  ones.
+ *                  memory (none up to 32 rows), 16-byte aligned, owned by the
+ *                  caller; need not be cleared.  Calls that may overlap on the
+ *                  GPU need separate ones.
  */
 size_t fp4_linear_workspace(int64_t rows, int64_t k, int kind);
 int fp4_linear(const uint16_t *x, int64_t rows, int64_t ld_x, const float *tensor_scale,

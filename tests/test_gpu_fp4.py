@@ -264,8 +264,9 @@ def test_product_ignores_what_lies_past_the_operands(cuda_lib):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("m,n,k", [(1, 1000, 3584), (7, 520, 1003), (16, 256, 512), (31, 640, 800),
-                                   (150, 300, 999), (600, 700, 1024)])
+@pytest.mark.parametrize("m,n,k", [(1, 1000, 3584), (1, 5, 18944), (2, 300, 250), (3, 9, 8960), (5, 4000, 300),
+                                   (7, 520, 1003), (9, 77, 2000), (16, 256, 512), (17, 40, 5000), (31, 640, 800),
+                                   (32, 3, 640), (33, 640, 800), (150, 300, 999), (600, 700, 1024)])
 def test_linear_is_quantize_then_multiply(cuda_lib, m, n, k, kind):
     bits = data(m, k, 41)
     if m > 2:
@@ -374,3 +375,16 @@ def test_product_timeout(cuda_lib, m, n, k, kind):
     assert fp8hg.fp8hg_get_device_error() == 0
     check_product(fp8hg.fp4_gemm_scaled(a, b), *product(va, vb), k)
     assert fp8hg.fp8hg_get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m", [1, 6, 20])
+def test_linear_timeout(cuda_lib, m, kind):
+    """The product that quantizes its rows itself, with a withheld copy."""
+    x = gpu(data(m, 4096, 63))
+    w, vw = stored(600, 4096, kind, 64)
+    want = fp8hg.fp4_linear(x, w)
+    fp8hg.fp4_linear(x, w, wait_limit_ns=20_000_000, inject_fault=1)
+    assert fp8hg.fp8hg_get_device_error() == 6
+    assert fp8hg.fp8hg_get_device_error() == 0
+    assert torch.equal(fp8hg.fp4_linear(x, w), want)

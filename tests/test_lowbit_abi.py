@@ -65,7 +65,7 @@ def test_scale_bytes(lib):
     assert lib.fp4_scale_bytes(1, 1, MX) == 1024 and lib.fp4_scale_bytes(1, 1, NV) == 2048
     assert lib.fp4_scale_bytes(129, 257, MX) == 4096 and lib.fp4_scale_bytes(128, 256, NV) == 2048
     assert lib.fp4_scale_bytes(0, 5, MX) == 0 and lib.fp4_scale_bytes(5, 5, 2) == 0
-    assert lib.fp4_linear_workspace(3, 100, MX) == 3 * 64 + 1024
+    assert lib.fp4_linear_workspace(33, 100, MX) == 33 * 64 + 1024 and lib.fp4_linear_workspace(32, 100, MX) == 0
     q = lambda rows, k, kind: fp8hg.alloc_fp4(rows, k, kind, device="cpu")
     for a in ((1, 1, MX), (129, 257, MX), (300, 3584, NV), (128, 256, NV)):
         assert q(*a).scale.numel() == lib.fp4_scale_bytes(*a)
@@ -130,9 +130,9 @@ def test_gemm_refusals(lib):
 
 
 def test_linear_refusals(lib):
-    need = lib.fp4_linear_workspace(4, 64, MX)
+    need = lib.fp4_linear_workspace(40, 64, MX)
 
-    def call(x=FAKE, rows=4, ld=64, t=None, w=None, y=FAKE, ldy=8, out=0, ws=FAKE, wb=need):
+    def call(x=FAKE, rows=40, ld=64, t=None, w=None, y=FAKE, ldy=8, out=0, ws=FAKE, wb=need):
         w = w or op()
         return lib.fp4_linear(x, rows, ld, t, ctypes.byref(w), y, ldy, out, ws, wb, None, None)
     assert call(x=None) == INVALID and call(ld=63) == INVALID and call(t=FAKE) == INVALID
