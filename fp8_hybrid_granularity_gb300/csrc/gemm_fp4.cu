@@ -542,9 +542,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 // quantize it into the operand stages themselves, each CTA all of its part of
 // K: no quantization pass before the product, no codes in memory.
 //
-// What bounds a call of one token is latency: 38 MB of weights take 5.7 us,
-// and 18944 rows of 3584 take 8.4 us with the codes given.  So the first
-// stages' copies are issued before anything else is set up.
+// What bounds a call of one token is latency: the 36 MB (MX) of 18944 x 3584
+// weights take 5.4 us from memory, the call 9.8 us with x quantized on the way.
+// So the first stages' copies are issued before the other warps have started.
 constexpr int F_THREADS = 256;
 template <bool NV, int BN>
 struct FewLayout {
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     const int64_t row0 = static_cast<int64_t>(mb) * 128, col0 = static_cast<int64_t>(nb) * BN;
     const int cols = static_cast<int>(min(static_cast<int64_t>(BN), p.N - col0));
     const int rl = 7 - (31 - __clz(splits));               // this CTA's share of the sums: 2^rl rows
-    const int lr = cols <= 1 ? 0 : 32 - __clz(cols - 1);   // QUANT: 2^lr >= cols
+    const int lr = cols <= 1 ? 0 : 32 - __clz(cols - 1);   // QUANT (at most eight rows): 2^lr >= cols
 
     const uint8_t *ga = p.sa + static_cast<int64_t>(mb) * p.scale_tiles * 512;
     const uint8_t *gb = QUANT ? nullptr : p.sb + static_cast<int64_t>(nb) * BN / 128 * p.scale_tiles * 512;
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(bar + 8 * s, QUANT ? 1 + min(128, 16 << lr) : 1);   // the copies, the quantizing threads
+            ptx::mbar_init(bar + 8 * s, QUANT ? 1 + (16 << lr) : 1);   // the copies, the quantizing threads
             ptx::mbar_init(bar + L::EMPTY + 8 * s, 1);
         }
         for (int i = 0; i < SLOTS; ++i) ptx::mbar_init(bar + L::SCALES + 8 * i, 1);
@@ -731,55 +731,59 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         bool ok = true;
         if constexpr (QUANT) {
             // The segments of 16 elements of a stage, 2^lr rows by 16 of them,
-            // go round the 128 threads, stage after stage; a thread has the
-            // loads of eight in flight (one token: all of its K in one go).
-            // Rows past the last are not written: they only reach outputs
-            // that are not stored.
+            // go round the 128 threads, stage after stage (one token: eight
+            // stages at a time), the next one's load in flight.  Rows past
+            // the last are not written: they only reach outputs that are not
+            // stored.  The loop is not unrolled: a decoding step runs it once
+            // or twice, and the instruction fetch of an unrolled one took
+            // longer than what it saved.
             const int tid = threadIdx.x - 128;
             const float t = NV && p.tb ? __ldg(p.tb) : 1.0f;
-            for (int it0 = 0; it0 < n && ok; it0 += 64 >> lr) {
-                uint32_t w[8][8];
+            const bool wide = (reinterpret_cast<uintptr_t>(qi.x) & 31) == 0 && (qi.ld & 15) == 0;
+            auto load = [&](int idx, uint32_t (&w)[8]) {
+                const int row = (idx >> 4) & ((1 << lr) - 1), it = idx >> (4 + lr);
+                const int64_t c0 = static_cast<int64_t>(kb0 + it) * 256 + (idx & 15) * 16;
 #pragma unroll
-                for (int a = 0; a < 8; ++a) {
-                    const int idx = a * 128 + tid, row = (idx >> 4) & ((1 << lr) - 1), it = it0 + (idx >> (4 + lr));
-                    const int64_t c0 = static_cast<int64_t>(kb0 + it) * 256 + (idx & 15) * 16;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[a][e] = 0u;
-                    if (it < n && row < cols && c0 < qi.k)
-                        ragged::load16<false>(qi.x + (col0 + row) * qi.ld + c0, qi.k - c0, w[a]);
+                for (int e = 0; e < 8; ++e) w[e] = 0u;
+                if (it < n && row < cols && c0 < qi.k) {
+                    const uint16_t *src = qi.x + (col0 + row) * qi.ld + c0;
+                    if (wide && c0 + 16 <= qi.k) ragged::load16<true>(src, 16, w);
+                    else ragged::load16<false>(src, qi.k - c0, w);
                 }
+            };
+            const int items = (n * (16 << lr) + 127) / 128;
+            uint32_t w[8], next[8];
+            load(tid, w);
+#pragma unroll 1
+            for (int a = 0; a < items; ++a) {
+                const int idx = a * 128 + tid, row = (idx >> 4) & ((1 << lr) - 1), seg = idx & 15;
+                const int it = idx >> (4 + lr), s = it % S;
+                load(idx + 128, next);
+                uint32_t m = 0;
 #pragma unroll
-                for (int a = 0; a < 8; ++a) {
-                    const int idx = a * 128 + tid, row = (idx >> 4) & ((1 << lr) - 1), seg = idx & 15;
-                    const int it = it0 + (idx >> (4 + lr)), s = it % S;
-                    uint32_t m = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) m = __vmaxu2(m, w[a][e] & 0x7FFF7FFFu);
-                    m = max(m & 0xFFFFu, m >> 16);
-                    if (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                    ok = ok && (it >= n || wait_phase(bar + L::EMPTY + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag,
-                                                      p.err, WHO_EPILOGUE));
-                    if (it < n && ok) {
-                        if (row < cols) {
-                            uint8_t *sq = gbase + s * L::STAGE + L::A;
-                            uint8_t *sf = gbase + L::OFF_SF + s * L::SF_STAGE + L::SF;
-                            const Fp4Scale<NV> sc(m, t);
-                            // the 128-byte swizzle of the operand tile
-                            *reinterpret_cast<uint2 *>(sq + row * 128 + (((seg >> 1) ^ (row & 7)) << 4) +
-                                                       (seg & 1) * 8) = make_uint2(sc.cast8(w[a]), sc.cast8(w[a] + 4));
-                            const int j = NV ? seg : seg >> 1;
-                            if (NV || (seg & 1) == 0)
-                                sf[(j >> 2) * 512 + row * 16 + (j & 3)] = static_cast<uint8_t>(sc.byte);
-                        }
-                        // once per stage: with more than eight rows after the
-                        // thread's last segment of it
-                        if (lr <= 3 || ((a + 1) & ((1 << (lr - 3)) - 1)) == 0) {
-                            ptx::fence_proxy_async_smem();
-                            ptx::mbar_arrive(bar + 8 * s);
-                        }
+                for (int e = 0; e < 8; ++e) m = __vmaxu2(m, w[e] & 0x7FFF7FFFu);
+                m = max(m & 0xFFFFu, m >> 16);
+                if (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                ok = ok && (it >= n || wait_phase(bar + L::EMPTY + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag,
+                                                  p.err, WHO_EPILOGUE));
+                if (it < n && ok) {
+                    if (row < cols) {
+                        uint8_t *sq = gbase + s * L::STAGE + L::A;
+                        uint8_t *sf = gbase + L::OFF_SF + s * L::SF_STAGE + L::SF;
+                        const Fp4Scale<NV> sc(m, t);
+                        // the 128-byte swizzle of the operand tile
+                        *reinterpret_cast<uint2 *>(sq + row * 128 + (((seg >> 1) ^ (row & 7)) << 4) + (seg & 1) * 8) =
+                            make_uint2(sc.cast8(w), sc.cast8(w + 4));
+                        const int j = NV ? seg : seg >> 1;
+                        if (NV || (seg & 1) == 0)
+                            sf[(j >> 2) * 512 + row * 16 + (j & 3)] = static_cast<uint8_t>(sc.byte);
                     }
-                    __syncwarp();
+                    ptx::fence_proxy_async_smem();
+                    ptx::mbar_arrive(bar + 8 * s);
                 }
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = next[e];
             }
         }
         ok = ok && wait_phase(tfull, 0u, limit, abort_flag, p.err, WHO_EPILOGUE);
@@ -890,7 +894,6 @@ cudaError_t set_attributes() {
     if (e == cudaSuccess) e = allow_smem(k_fp4_pair<NV, 1>, PairLayout<NV, 1>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 16, false>, FewLayout<NV, 16>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 16, true>, FewLayout<NV, 16>::SMEM);
-    if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 32, true>, FewLayout<NV, 32>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 32, false>, FewLayout<NV, 32>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 64, false>, FewLayout<NV, 64>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 128, false>, FewLayout<NV, 128>::SMEM);
@@ -1031,8 +1034,7 @@ int launch(const Fp4GemmArgs &g, int sms, cudaStream_t stream) {
     p.err = g.err;
     if (g.x) {
         const Plan plan = choose_few(g.a.rows, g.b.rows, p.nk, sms);
-        return plan.bn == 16 ? launch_few<NV, 16, true>(g, p, true, plan.splits, stream)
-                             : launch_few<NV, 32, true>(g, p, true, plan.splits, stream);
+        return launch_few<NV, 16, true>(g, p, true, plan.splits, stream);
     }
     const bool swapped = g.a.rows <= g.b.rows;
     const Plan plan = choose(g.a.rows, g.b.rows, p.nk, sms);
@@ -1048,7 +1050,10 @@ int launch(const Fp4GemmArgs &g, int sms, cudaStream_t stream) {
 
 }  // namespace
 
-bool fp4_linear_quantizes(int64_t rows) { return rows <= 32; }
+// Quantizing inside the product, every CTA for itself, against a quantization
+// pass before it (18944 x 3584, NV, microseconds): 11.6 and 13.9 for one row,
+// 12.9 and 14.2 for four, 15.3 and 13.9 for eight.
+bool fp4_linear_quantizes(int64_t rows) { return rows <= 4; }
 
 int launch_fp4_gemm(const Fp4GemmArgs &g, cudaStream_t stream) {
     int dev = 0;

@@ -260,7 +260,7 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
                wait_limit_ns: int = 0, inject_fault: int = 0, stream=None):
     """y = x w^T: x [rows, k] BF16 is quantized like w and multiplied, in one
     call.  workspace: optional uint8 tensor of fp4_linear_workspace(...)
-    bytes (allocated per call if None; up to 32 rows none is needed)."""
+    bytes (allocated per call if None; up to 4 rows none is needed)."""
     _check_matrix(x)
     if x.shape[1] != w.k:
         raise ValueError(f"x has {x.shape[1]} columns, w {w.k}")

@@ -93,6 +93,8 @@ int fp4_quant(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x, int k
  * A 4-bit tensor of `rows` rows of `k` elements: codes 16-byte aligned, row
  * stride ld bytes (a multiple of 16, at least ceil(k / 2)); scale 16-byte
  * aligned, fp4_scale_bytes(rows, k, kind) bytes; tensor_scale as fp4_quant.
+ * As fp4_quant leaves them: the unused half of a row's last byte (k odd) is 0,
+ * and no scale byte of the padding along k is a NaN.
  */
 typedef struct {
     const uint8_t *codes;
@@ -124,7 +126,7 @@ int fp4_gemm_scaled(const fp4hg_operand *a, const fp4hg_operand *b, void *c, int
 
 /*
  * fp4_linear — y = x w^T with x quantized on the way: the result of fp4_quant
- * of x followed by fp4_gemm_scaled, in one call.  Up to 32 rows (decoding) x
+ * of x followed by fp4_gemm_scaled, in one call.  Up to 4 rows (decoding) x
  * is quantized inside the product.
  *
  *   x, ld_x        [rows, w->k] BF16, as fp4_quant
@@ -132,7 +134,7 @@ int fp4_gemm_scaled(const fp4hg_operand *a, const fp4hg_operand *b, void *c, int
  *   w              the weights, [n, k]
  *   y              [rows, n], row stride ld_y elements
  *   workspace      fp4_linear_workspace(rows, w->k, w->kind) bytes of device
- *                  memory (none up to 32 rows), 16-byte aligned, owned by the
+ *                  memory (none up to 4 rows), 16-byte aligned, owned by the
  *                  caller; need not be cleared.  Calls that may overlap on the
  *                  GPU need separate ones.
  */
