@@ -1,18 +1,19 @@
 // Block scales and casts of the 4-bit formats (E2M1 values).
 //
 // As in quant_math.cuh the amax of a block is an integer maximum over BF16
-// patterns.  MX scales are read off its exponent field.  NV scales take two
-// correctly rounded divisions and one E4M3 cast per block; an element's
-// quotient x / d, d = s * t, is x * (1/d) followed by one residual step
-// (q + (x - q d) (1/d), two fused multiply-adds), which leaves the error of
-// the quotient below one FP32 rounding: with t a power of two d has four
-// significant bits and x eight, so x / d either equals a midpoint of two E2M1
-// values or is farther from it than that error, and the cast is the nearest
-// value of the exact quotient.  (A plain multiply by 1/d breaks such ties at
-// random.)
+// patterns.  MX scales are read off its exponent field.  An NV scale is
+// E4M3((amax / 6) / t), an element's quotient x / d with d = s * t.  All of
+// these quotients are a product with an (approximate) reciprocal and one
+// residual step, q + (x - q d) (1/d), two fused multiply-adds, which leaves the
+// error of the quotient below one FP32 rounding.  With t a power of two d has
+// four significant bits and x eight, so x / d either equals a midpoint of two
+// E2M1 values or is farther from it than that error, and the cast is the
+// nearest value of the exact quotient; the same holds for amax / 6 and E4M3.
+// (A plain multiply by 1/d breaks such ties at random.)
 #pragma once
 #include <cstdint>
 
+#include "pair_math.cuh"
 #include "quant_math.cuh"
 
 namespace fp8hg {
@@ -59,25 +60,36 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t byte) {
     }
 }
 
+// x / d from r = 1 / d (to a few units in the last place), see above.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+}
+
 template <bool NV>
 struct Fp4Scale {
     uint32_t byte;
     float mul;       // MX: 2^-e; NV: 1 / d
     float d;         // NV: s * t
     bool nan, sat;   // a non-finite block; NV: the E4M3 scale saturated
-    __device__ __forceinline__ Fp4Scale(uint32_t amax_bits, float t) {
+    // NV: t the tensor's scale, rt = 1 / t (MX: not used)
+    __device__ __forceinline__ Fp4Scale(uint32_t amax_bits, float t, float rt) {
         nan = amax_bits >= 0x7F80u;
         sat = false;
         d = 0.0f;
         mul = 0.0f;
         if constexpr (NV) {
-            const float q = __fdiv_rn(__fdiv_rn(__uint_as_float(amax_bits << 16), 6.0f), t);
-            byte = nan ? 0x7Fu : ptx::cvt_e4m3x2(q, 0.0f) & 0xFFu;
-            if (!nan && byte != 0u) {
-                d = __fmul_rn(fp4_scale_value<true>(byte), t);
-                mul = __frcp_rn(d);
-                sat = q > 448.0f;
-            }
+            // amax / 6 / t beyond 2^96 is taken as that: it saturates, and the
+            // residual stays finite
+            const float sixth = quotient(__uint_as_float(amax_bits << 16), 6.0f, 1.0f / 6.0f);
+            const float q = fminf(__fmul_rn(sixth, rt), 0x1p96f);
+            const float s = __fmaf_rn(__fmaf_rn(-q, t, sixth), rt, q);
+            sat = s > 448.0f;
+            byte = nan ? 0x7Fu : ptx::cvt_e4m3x2(s, 0.0f) & 0xFFu;
+            d = __fmul_rn(fp4_scale_value<true>(byte), t);
+            const bool none = nan || byte == 0u;
+            d = none ? 0.0f : d;
+            mul = none ? 0.0f : rcp_fast(d);
         } else {
             const int ef = static_cast<int>(amax_bits >> 7);
             const int e = ef == 0 ? -127 : clamp_exp(ef - 129);
@@ -88,31 +100,36 @@ struct Fp4Scale {
     // Eight BF16 values (four words) -> eight codes.  Non-finite block: 0.
     __device__ __forceinline__ uint32_t cast8(const uint32_t *w) const {
         float v[8];
+        const F2 m2 = f2(mul), nd2 = f2(-d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-        if constexpr (NV) {
-            if (sat) {   // keeps the quotient finite; all such values saturate
-                const float m = 8.0f * d;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -m), m);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            F2 x = f2_bf16(w[i]);
+            if constexpr (NV) {
+                if (sat) {   // keeps the quotient finite; all such values saturate
+                    const float m = 8.0f * d;
+                    x = f2(fminf(fmaxf(x.lo(), -m), m), fminf(fmaxf(x.hi(), -m), m));
+                }
+                const F2 q = mul2(x, m2);
+                const F2 r = fma2(fma2(q, nd2, x), m2, q);
                 // the sign is x's own: the residual of -0 is +0
-                const float q = __fmul_rn(v[i], mul);
-                v[i] = copysignf(__fmaf_rn(__fmaf_rn(-q, d, v[i]), mul, q), v[i]);
+                v[2 * i] = copysignf(r.lo(), x.lo());
+                v[2 * i + 1] = copysignf(r.hi(), x.hi());
+            } else {
+                x = mul2(x, m2);
+                v[2 * i] = x.lo();
+                v[2 * i + 1] = x.hi();
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], mul);
         }
         const uint32_t c = cvt_e2m1x8(v);
         return nan ? 0u : c;
     }
 };
+
+// The tensor scale's reciprocal as Fp4Scale takes it.
+template <bool NV>
+__device__ __forceinline__ float fp4_reciprocal(float t) {
+    return NV ? __frcp_rn(t) : 0.0f;
+}
 
 // Byte offset of (row, block j) in a scale array with `tiles` tiles along k.
 __device__ __forceinline__ int64_t fp4_scale_offset(int64_t row, int64_t j, int64_t tiles) {

@@ -12,6 +12,7 @@
 //  k_fp4_dequant values from codes and scales.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "fp4_math.cuh"
@@ -61,19 +62,29 @@ __global__ void __launch_bounds__(256)
     const int tid = threadIdx.x, lane = tid & 31;
     const int seg = blockIdx.y * segs + tid % segs;
     const int rpb = blockDim.x / segs;
-    const float t = NV && ts ? __ldg(ts) : 1.0f;
+    const float t = NV && ts ? __ldg(ts) : 1.0f, rt = fp4_reciprocal<NV>(t);
     const int64_t c0 = static_cast<int64_t>(seg) * 16;
     constexpr int LPB = NV ? 1 : 2;
-    // every lane of the warp stays in the loop for the shuffles
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < rows;
-         r0 += static_cast<int64_t>(gridDim.x) * rpb) {
+    // The next row's load is in flight while a row is cast: a CTA per row
+    // spent most of its time waiting for its one load (8192 x 3584, NV: 23.6 us).
+    // Every lane of the warp stays in the loop for the shuffles.
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rpb;
+    const bool mine = tid / segs < rpb && seg < total_segs;
+    uint32_t next[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    auto load = [&](int64_t r) {
+        if (mine && r < rows && c0 < cols) ragged::load16<WIDE>(x + r * ld_x + c0, cols - c0, next);
+    };
+    load(static_cast<int64_t>(blockIdx.x) * rpb + tid / segs);
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < rows; r0 += step) {
         const int64_t r = r0 + tid / segs;
-        const bool in = tid / segs < rpb && r < rows && seg < total_segs;
-        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (in && c0 < cols) ragged::load16<WIDE>(x + r * ld_x + c0, cols - c0, w);
+        const bool in = mine && r < rows;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = next[i];
+        load(r + step);
         uint32_t m = abs_max16(w);
         if (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        const Fp4Scale<NV> sc(m, t);
+        const Fp4Scale<NV> sc(m, t, rt);
         const uint32_t word = gather_scales<LPB>(sc.byte, lane);
         if (!in) continue;
         if (c0 < cols) {
@@ -109,7 +120,7 @@ __global__ void __launch_bounds__(256)
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile;
     const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const float t = NV && ts ? __ldg(ts) : 1.0f;
+    const float t = NV && ts ? __ldg(ts) : 1.0f, rt = fp4_reciprocal<NV>(t);
     {
         const int seg = tid & 7;
         const int64_t c0 = k0 + seg * 16;
@@ -133,7 +144,7 @@ __global__ void __launch_bounds__(256)
             if constexpr (ROWS) {
                 uint32_t m = abs_max16(w[i]);
                 if (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                const Fp4Scale<NV> sc(m, t);
+                const Fp4Scale<NV> sc(m, t, rt);
                 const uint32_t word = gather_scales<LPB>(sc.byte, lane);
                 if (lane % (4 * LPB) == 0)
                     *reinterpret_cast<uint32_t *>(scales[0] + (seg / (4 * LPB)) * 512 +
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(256)
             const int col = 2 * p + h;
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-                const Fp4Scale<NV> sc(h ? m[part] >> 16 : m[part] & 0xFFFFu, t);
+                const Fp4Scale<NV> sc(h ? m[part] >> 16 : m[part] & 0xFFFFu, t, rt);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t w[4];
@@ -326,6 +337,21 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+constexpr int kRowThreadsPerSm = 1536;   // 40 registers a thread
+
+int sms() {
+    static int n[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    if (!n[dev]) {
+        int v = 0;
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+        n[dev] = v > 0 ? v : 1;
+    }
+    return n[dev];
+}
+
 template <bool NV>
 cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
     const int64_t total = (a.cols + 255) / 256 * 16;      // segments, k padded to 256
@@ -333,9 +359,10 @@ cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
     const int segs = static_cast<int>((total / 16 + chunks - 1) / chunks * 16);
     const int rpb = 256 / segs;
     const int threads = (segs * rpb + 31) / 32 * 32;
-    const int64_t rblocks = (a.rows + rpb - 1) / rpb;
-    const dim3 grid(static_cast<unsigned>(rblocks < 0x7FFFFFFF ? rblocks : 0x7FFFFFFF),
-                    static_cast<unsigned>((total + segs - 1) / segs));
+    const int64_t rblocks = (a.rows + rpb - 1) / rpb, cblocks = (total + segs - 1) / segs;
+    // as many CTAs as fit at once
+    const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kRowThreadsPerSm / threads) / cblocks);
+    const dim3 grid(static_cast<unsigned>(std::min(rblocks, resident)), static_cast<unsigned>(cblocks));
     const int64_t tiles = fp4_scale_tiles(a.cols, a.kind);
     if (ragged::wide(a.x, a.ld_x))
         k_fp4_rows<NV, true><<<grid, threads, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,

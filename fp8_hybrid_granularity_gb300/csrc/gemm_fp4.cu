@@ -334,8 +334,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 ptx::tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    ptx::mul_f32x2(r[2 * e], r[2 * e + 1], alpha);
-                    packed[chunk * 32 + e] = ptx::cvt_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                    const F2 v = mul2(f2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f2(alpha));
+                    packed[chunk * 32 + e] = ptx::cvt_bf16x2(v.lo(), v.hi());
                 }
             }
             release();
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             // or twice, and the instruction fetch of an unrolled one took
             // longer than what it saved.
             const int tid = threadIdx.x - 128;
-            const float t = NV && p.tb ? __ldg(p.tb) : 1.0f;
+            const float t = NV && p.tb ? __ldg(p.tb) : 1.0f, rt = fp4_reciprocal<NV>(t);
             const bool wide = (reinterpret_cast<uintptr_t>(qi.x) & 31) == 0 && (qi.ld & 15) == 0;
             auto load = [&](int idx, uint32_t (&w)[8]) {
                 const int row = (idx >> 4) & ((1 << lr) - 1), it = idx >> (4 + lr);
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                     if (row < cols) {
                         uint8_t *sq = gbase + s * L::STAGE + L::A;
                         uint8_t *sf = gbase + L::OFF_SF + s * L::SF_STAGE + L::SF;
-                        const Fp4Scale<NV> sc(m, t);
+                        const Fp4Scale<NV> sc(m, t, rt);
                         // the 128-byte swizzle of the operand tile
                         *reinterpret_cast<uint2 *>(sq + row * 128 + (((seg >> 1) ^ (row & 7)) << 4) + (seg & 1) * 8) =
                             make_uint2(sc.cast8(w), sc.cast8(w + 4));

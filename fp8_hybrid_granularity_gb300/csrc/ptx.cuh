@@ -214,13 +214,6 @@ __device__ __forceinline__ void tmem_ld_32x32b_x64(uint32_t taddr, uint32_t (&r)
         : "r"(taddr)
         : "memory");
 }
-// Two products in one instruction.
-__device__ __forceinline__ void mul_f32x2(uint32_t &a, uint32_t &b, float m) {
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
-        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+r"(a), "+r"(b)
-        : "f"(m));
-}
 __device__ __forceinline__ void tmem_wait_ld() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }

@@ -14,9 +14,11 @@
 // A thread takes 16 neighbouring elements, eight threads a group of 128.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "lowbit.h"
+#include "pair_math.cuh"
 #include "quant_math.cuh"
 #include "ragged.cuh"
 
@@ -24,10 +26,12 @@ namespace fp8hg {
 
 namespace {
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + 2^(-g log2 e)) of two values.
+__device__ __forceinline__ F2 sigmoid2(F2 g) {
+    const F2 x = mul2(g, f2(-1.44269504f));
+    const F2 y = add2(f2(ex2_fast(x.lo()), ex2_fast(x.hi())), f2(1.0f));
+    return f2(rcp_fast(y.lo()), rcp_fast(y.hi()));
+}
 
 // Sixteen code bytes (aligned) to p, the first `left` of them.
 __device__ __forceinline__ void store_bytes16(uint8_t *p, const uint32_t (&c)[4], int64_t left) {
@@ -52,17 +56,12 @@ __device__ __forceinline__ void load_bytes16(const uint8_t *p, int64_t left, uin
     }
 }
 
-// Four FP8 codes -> floats.
+// Two FP8 codes -> their values times m.
 template <int FMT>
-__device__ __forceinline__ void fp8x4_values(uint32_t c, float (&v)[4]) {
-    const uint16_t lo = static_cast<uint16_t>(c), hi = static_cast<uint16_t>(c >> 16);
-    if constexpr (FMT == FMT_E4M3) {
-        ptx::f16x2_to_f32(ptx::cvt_f16x2_e4m3x2(lo), v[0], v[1]);
-        ptx::f16x2_to_f32(ptx::cvt_f16x2_e4m3x2(hi), v[2], v[3]);
-    } else {
-        ptx::f16x2_to_f32(ptx::cvt_f16x2_e5m2x2(lo), v[0], v[1]);
-        ptx::f16x2_to_f32(ptx::cvt_f16x2_e5m2x2(hi), v[2], v[3]);
-    }
+__device__ __forceinline__ F2 fp8x2_values(uint16_t c, F2 m) {
+    float lo, hi;
+    ptx::f16x2_to_f32(FMT == FMT_E4M3 ? ptx::cvt_f16x2_e4m3x2(c) : ptx::cvt_f16x2_e5m2x2(c), lo, hi);
+    return mul2(f2(lo, hi), m);
 }
 
 // A scale byte's power of two; NaN for the byte of a non-finite group.
@@ -82,13 +81,20 @@ struct GroupF32 {
         byte = nan ? 0xFFu : static_cast<uint32_t>(e + 127);
         mul = pow2f(-e);
     }
-    __device__ __forceinline__ uint32_t cast4(float a, float b, float c, float d) const {
-        const uint32_t v = cvt2<FMT>(a * mul, b * mul) | (cvt2<FMT>(c * mul, d * mul) << 16);
+    __device__ __forceinline__ uint32_t cast4(F2 a, F2 b) const {
+        const F2 m = f2(mul);
+        a = mul2(a, m);
+        b = mul2(b, m);
+        const uint32_t v = __byte_perm(cvt2<FMT>(a.lo(), a.hi()), cvt2<FMT>(b.lo(), b.hi()), 0x5410);
         return nan ? kNanCodes : v;
     }
 };
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// The larger of m and both magnitudes, as bit patterns (a NaN's is above all).
+__device__ __forceinline__ uint32_t max_abs(uint32_t m, F2 v) {
+    return max(m, max(abs_bits(v.lo()), abs_bits(v.hi())));
+}
 
 // Maximum over the eight lanes of a group (each half of a packed pair).
 __device__ __forceinline__ uint32_t group_max_u2(uint32_t m) {
@@ -102,17 +108,18 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m) {
     return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
 }
 
+// Sixteen BF16 values of a group with this amax -> codes; the scale byte.
 template <int FMT>
-__device__ __forceinline__ void cast_bf16x16(const uint32_t (&w)[8], const GroupScale<FMT, SCALE_UE8M0> &gs,
-                                             uint32_t (&c)[4]) {
-    uint32_t unused = 0;
+__device__ __forceinline__ uint32_t cast_bf16x16(const uint32_t (&w)[8], uint32_t amax_bits, uint32_t (&c)[4]) {
+    const GroupScale<FMT, SCALE_UE8M0> gs(amax_bits);
+    const F2 m = f2(gs.mul);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint2 v = quant8<FMT, false>(make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]),
-                                           gs.mul, unused);
-        c[2 * h] = gs.nan ? kNanCodes : v.x;
-        c[2 * h + 1] = gs.nan ? kNanCodes : v.y;
+    for (int i = 0; i < 4; ++i) {
+        const F2 a = mul2(f2_bf16(w[2 * i]), m), b = mul2(f2_bf16(w[2 * i + 1]), m);
+        const uint32_t v = __byte_perm(cvt2<FMT>(a.lo(), a.hi()), cvt2<FMT>(b.lo(), b.hi()), 0x5410);
+        c[i] = gs.nan ? kNanCodes : v;
     }
+    return gs.byte;
 }
 
 // ------------------------------------------------------------------- forward
@@ -123,22 +130,31 @@ __global__ void __launch_bounds__(256)
     const int seg = blockIdx.y * segs + tid % segs;
     const int rpb = blockDim.x / segs;
     const int64_t c0 = static_cast<int64_t>(seg) * 16, left = a.cols - c0;
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows;
-         r0 += static_cast<int64_t>(gridDim.x) * rpb) {
-        const int64_t r = r0 + tid / segs;
-        const bool in = tid / segs < rpb && r < a.rows && seg < total_segs;
-        uint32_t g[8] = {0, 0, 0, 0, 0, 0, 0, 0}, u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (in && left > 0) {
-            ragged::load16<WIDE>(a.gate + r * a.ld_in + c0, left, g);
-            ragged::load16<WIDE>(a.up + r * a.ld_in + c0, left, u);
+    // the next row's loads are in flight while a row is computed
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rpb;
+    const bool mine = tid / segs < rpb && seg < total_segs;
+    uint32_t ng[8] = {0, 0, 0, 0, 0, 0, 0, 0}, nu[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    auto load = [&](int64_t r) {
+        if (mine && r < a.rows && left > 0) {
+            ragged::load16<WIDE>(a.gate + r * a.ld_in + c0, left, ng);
+            ragged::load16<WIDE>(a.up + r * a.ld_in + c0, left, nu);
         }
-        float h[16];
+    };
+    load(static_cast<int64_t>(blockIdx.x) * rpb + tid / segs);
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows; r0 += step) {
+        const int64_t r = r0 + tid / segs;
+        const bool in = mine && r < a.rows;
+        uint32_t g[8], u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = ng[i], u[i] = nu[i];
+        load(r + step);
+        F2 h[8];
         uint32_t mh = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            h[2 * i] = bf_lo(g[i]) * sigmoid(bf_lo(g[i])) * bf_lo(u[i]);
-            h[2 * i + 1] = bf_hi(g[i]) * sigmoid(bf_hi(g[i])) * bf_hi(u[i]);
-            mh = max(mh, max(abs_bits(h[2 * i]), abs_bits(h[2 * i + 1])));
+            const F2 x = f2_bf16(g[i]);
+            h[i] = mul2(mul2(x, sigmoid2(x)), f2_bf16(u[i]));
+            mh = max_abs(mh, h[i]);
         }
         mh = group_max(mh);
         uint32_t mgu = 0;
@@ -156,32 +172,30 @@ __global__ void __launch_bounds__(256)
         const GroupF32<FH> sh(mh);
         uint32_t c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = sh.cast4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) c[i] = sh.cast4(h[2 * i], h[2 * i + 1]);
         store_bytes16(a.h + r * a.ld_h + c0, c, left);
         const int64_t grp = seg >> 3;
         if ((seg & 7) == 0) a.hs[r * a.ld_hs + grp] = static_cast<uint8_t>(sh.byte);
         if constexpr (CKPT) {
-            const GroupScale<FC, SCALE_UE8M0> sg(mgu & 0xFFFFu), su(mgu >> 16);
-            cast_bf16x16<FC>(g, sg, c);
+            const uint32_t bg = cast_bf16x16<FC>(g, mgu & 0xFFFFu, c);
             store_bytes16(a.gq + r * a.ld_q + c0, c, left);
-            cast_bf16x16<FC>(u, su, c);
+            const uint32_t bu = cast_bf16x16<FC>(u, mgu >> 16, c);
             store_bytes16(a.uq + r * a.ld_q + c0, c, left);
             if ((seg & 7) == 0) {
-                a.gs[r * a.ld_s + grp] = static_cast<uint8_t>(sg.byte);
-                a.us[r * a.ld_s + grp] = static_cast<uint8_t>(su.byte);
+                a.gs[r * a.ld_s + grp] = static_cast<uint8_t>(bg);
+                a.us[r * a.ld_s + grp] = static_cast<uint8_t>(bu);
             }
         }
     }
 }
 
 // ------------------------------------------------------------ backward, BF16
-// One element's gradients from the checkpoint's values.
-__device__ __forceinline__ void swiglu_grads(float g, float u, float dh, float &dg, float &du,
-                                             float &h) {
-    const float s = sigmoid(g), gs = g * s;
-    dg = dh * u * (s + gs * (1.0f - s));
-    du = dh * gs;
-    h = gs * u;
+// Two elements' gradients from the checkpoint's values.
+__device__ __forceinline__ void swiglu_grads(F2 g, F2 u, F2 dh, F2 &dg, F2 &du, F2 &h) {
+    const F2 s = sigmoid2(g), gs = mul2(g, s);
+    dg = mul2(mul2(dh, u), fma2(gs, fma2(s, f2(-1.0f), f2(1.0f)), s));
+    du = mul2(dh, gs);
+    h = mul2(gs, u);
 }
 
 template <int FC, bool WIDE>
@@ -199,21 +213,17 @@ __global__ void __launch_bounds__(256)
             ragged::load16<WIDE>(dh + r * ld_dh + c0, left, w);
             load_bytes16(c.gq + r * c.ld_q + c0, left, gc);
             load_bytes16(c.uq + r * c.ld_q + c0, left, uc);
-            const float sg = scale_pow2(__ldg(c.gs + r * c.ld_s + (seg >> 3)));
-            const float su = scale_pow2(__ldg(c.us + r * c.ld_s + (seg >> 3)));
+            const F2 sg = f2(scale_pow2(__ldg(c.gs + r * c.ld_s + (seg >> 3))));
+            const F2 su = f2(scale_pow2(__ldg(c.us + r * c.ld_s + (seg >> 3))));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float g[4], u[4], a[4], b[4], h;
-                fp8x4_values<FC>(gc[i], g);
-                fp8x4_values<FC>(uc[i], u);
-                const float d[4] = {bf_lo(w[2 * i]), bf_hi(w[2 * i]), bf_lo(w[2 * i + 1]),
-                                    bf_hi(w[2 * i + 1])};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) swiglu_grads(g[j] * sg, u[j] * su, d[j], a[j], b[j], h);
-                og[2 * i] = ptx::cvt_bf16x2(a[0], a[1]);
-                og[2 * i + 1] = ptx::cvt_bf16x2(a[2], a[3]);
-                ou[2 * i] = ptx::cvt_bf16x2(b[0], b[1]);
-                ou[2 * i + 1] = ptx::cvt_bf16x2(b[2], b[3]);
+            for (int i = 0; i < 8; ++i) {
+                const int sh = 16 * (i & 1);
+                const F2 g = fp8x2_values<FC>(static_cast<uint16_t>(gc[i >> 1] >> sh), sg);
+                const F2 u = fp8x2_values<FC>(static_cast<uint16_t>(uc[i >> 1] >> sh), su);
+                F2 a, b, h;
+                swiglu_grads(g, u, f2_bf16(w[i]), a, b, h);
+                og[i] = ptx::cvt_bf16x2(a.lo(), a.hi());
+                ou[i] = ptx::cvt_bf16x2(b.lo(), b.hi());
             }
         }
         ragged::store16<WIDE>(dg + r * ld_d + c0, left, og);
@@ -242,9 +252,9 @@ constexpr int kPlane = kT * kT + 3 * 8;          // words of one of the three
 constexpr int kQSmem = 3 * kPlane * 4;
 
 template <int F>
-__device__ __forceinline__ void emit_codes(const float *v, int n4, const GroupF32<F> &gs, uint32_t *c) {
+__device__ __forceinline__ void emit_codes(const F2 *v, int n4, const GroupF32<F> &gs, uint32_t *c) {
 #pragma unroll
-    for (int i = 0; i < n4; ++i) c[i] = gs.cast4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int i = 0; i < n4; ++i) c[i] = gs.cast4(v[2 * i], v[2 * i + 1]);
 }
 
 // A thread's inputs of a tile: two rows (0 .. 3 + 64 apart) of 16 columns.
@@ -288,29 +298,25 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int row = rr + 64 * i;
-            const float sg = scale_pow2(in.sg[i]), su = scale_pow2(in.su[i]);
-            float a[16], b[16];
+            const F2 sg = f2(scale_pow2(in.sg[i])), su = f2(scale_pow2(in.su[i]));
+            F2 a[8], b[8];
             uint32_t ma = 0, mb = 0;
             float *dst = plane + row * kT + (row >> 5) * 8;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float g[4], u[4], h[4];
-                fp8x4_values<FC>(in.g[i][k], g);
-                fp8x4_values<FC>(in.u[i][k], u);
-                const float d[4] = {bf_lo(in.dh[i][2 * k]), bf_hi(in.dh[i][2 * k]), bf_lo(in.dh[i][2 * k + 1]),
-                                    bf_hi(in.dh[i][2 * k + 1])};
+                F2 h[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    swiglu_grads(g[j] * sg, u[j] * su, d[j], a[4 * k + j], b[4 * k + j], h[j]);
-                    ma = max(ma, abs_bits(a[4 * k + j]));
-                    mb = max(mb, abs_bits(b[4 * k + j]));
+                for (int j = 0; j < 2; ++j) {
+                    const F2 g = fp8x2_values<FC>(static_cast<uint16_t>(in.g[i][k] >> (16 * j)), sg);
+                    const F2 u = fp8x2_values<FC>(static_cast<uint16_t>(in.u[i][k] >> (16 * j)), su);
+                    swiglu_grads(g, u, f2_bf16(in.dh[i][2 * k + j]), a[2 * k + j], b[2 * k + j], h[j]);
+                    ma = max_abs(ma, a[2 * k + j]);
+                    mb = max_abs(mb, b[2 * k + j]);
                 }
-                const int piece = (4 * seg + k) ^ ((seg >> 1) & 3);
-                *reinterpret_cast<float4 *>(dst + piece * 4) =
-                    make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
-                *reinterpret_cast<float4 *>(dst + kPlane + piece * 4) =
-                    make_float4(b[4 * k], b[4 * k + 1], b[4 * k + 2], b[4 * k + 3]);
-                *reinterpret_cast<float4 *>(dst + 2 * kPlane + piece * 4) = make_float4(h[0], h[1], h[2], h[3]);
+                const int piece = ((4 * seg + k) ^ ((seg >> 1) & 3)) * 4;
+                *reinterpret_cast<ulonglong2 *>(dst + piece) = make_ulonglong2(a[2 * k].v, a[2 * k + 1].v);
+                *reinterpret_cast<ulonglong2 *>(dst + kPlane + piece) = make_ulonglong2(b[2 * k].v, b[2 * k + 1].v);
+                *reinterpret_cast<ulonglong2 *>(dst + 2 * kPlane + piece) = make_ulonglong2(h[0].v, h[1].v);
             }
             const GroupF32<FR> ga(group_max(ma)), gb(group_max(mb));
             const int64_t r = r0 + row, at = r * o.ld_q + kb * kT + seg * 16;
@@ -334,12 +340,12 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
         const float *src = plane + quarter * (32 * kT + 8) + word;
 #pragma unroll
         for (int w = 0; w < 3; ++w) {
-            float v[32];
+            F2 v[16];
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                v[i] = src[w * kPlane + i * kT];
-                m = max(m, abs_bits(v[i]));
+            for (int i = 0; i < 16; ++i) {
+                v[i] = f2(src[w * kPlane + 2 * i * kT], src[w * kPlane + (2 * i + 1) * kT]);
+                m = max_abs(m, v[i]);
             }
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
@@ -363,6 +369,21 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
     }
 }
 
+constexpr int kFwdThreadsPerSm = 768;   // 80 registers a thread
+
+int sms() {
+    static int n[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    if (!n[dev]) {
+        int v = 0;
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+        n[dev] = v > 0 ? v : 1;
+    }
+    return n[dev];
+}
+
 template <int FH, int FC, bool CKPT>
 cudaError_t fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
     // segments of 16 columns, whole groups of eight; a chunk of at most 256
@@ -370,9 +391,10 @@ cudaError_t fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
     const int64_t total = (a.cols + 127) / 128 * 8, chunks = (total + 255) / 256;
     const int segs = static_cast<int>((total / 8 + chunks - 1) / chunks * 8);
     const int rpb = 256 / segs, threads = (segs * rpb + 31) / 32 * 32;
-    const int64_t rb = (a.rows + rpb - 1) / rpb;
-    const dim3 grid(static_cast<unsigned>(rb < 0x7FFFFFFF ? rb : 0x7FFFFFFF),
-                    static_cast<unsigned>((total + segs - 1) / segs));
+    const int64_t rb = (a.rows + rpb - 1) / rpb, cb = (total + segs - 1) / segs;
+    // as many CTAs as fit at once
+    const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kFwdThreadsPerSm / threads) / cb);
+    const dim3 grid(static_cast<unsigned>(std::min(rb, resident)), static_cast<unsigned>(cb));
     if (ragged::wide(a.gate, a.ld_in) && ragged::wide(a.up, a.ld_in))
         k_swiglu_fwd<FH, FC, CKPT, true><<<grid, threads, 0, stream>>>(a, segs, static_cast<int>(total));
     else
