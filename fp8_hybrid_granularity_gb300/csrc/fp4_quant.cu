@@ -26,7 +26,7 @@ namespace {
 __device__ __forceinline__ uint32_t abs_max16(const uint32_t (&w)[8]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    for (int i = 0; i < 8; ++i) m = max_abs_bf16x2(m, w[i]);
     return max(m & 0xFFFFu, m >> 16);
 }
 
@@ -54,8 +54,10 @@ __device__ __forceinline__ uint32_t gather_scales(uint32_t byte, int lane) {
 // Block: `segs` segments of 16 elements (a multiple of 16) by some rows, a
 // thread each; the segments cover k padded to 256, so that the padding's
 // scale bytes are written too.
+constexpr int kRowThreadsPerSm = 1280;   // 48 registers a thread
+
 template <bool NV, bool WIDE>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kRowThreadsPerSm / 256)
     k_fp4_rows(const uint16_t *__restrict__ x, int64_t rows, int64_t cols, int64_t ld_x,
                const float *__restrict__ ts, uint8_t *__restrict__ q, int64_t ld_q,
                uint8_t *__restrict__ s, int64_t tiles, int segs, int total_segs) {
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(256)
         for (int i = 0; i < 32; ++i) v[i] = *reinterpret_cast<const uint32_t *>(src + i * 256);
         uint32_t m[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m[i >> 4] = __vmaxu2(m[i >> 4], v[i] & 0x7FFF7FFFu);
+        for (int i = 0; i < 32; ++i) m[i >> 4] = max_abs_bf16x2(m[i >> 4], v[i]);
         if (!NV) m[0] = m[1] = __vmaxu2(m[0], m[1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -336,8 +338,6 @@ __global__ void __launch_bounds__(256)
         }
     }
 }
-
-constexpr int kRowThreadsPerSm = 1536;   // 40 registers a thread
 
 int sms() {
     static int n[64] = {0};

@@ -21,6 +21,20 @@ __device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
 __device__ __forceinline__ F2 f2_bf16(uint32_t w) {
     return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
+// The largest of three magnitudes, a NaN if one is (one instruction, where
+// maxima of bit patterns take one for each sign bit and one for each maximum).
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max_abs(float m, F2 v) { return max3_abs(m, v.lo(), v.hi()); }
+// Magnitudes of two BF16 pairs, the larger in each half (a NaN if one is).
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.NaN.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+    return r;
+}
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     F2 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));

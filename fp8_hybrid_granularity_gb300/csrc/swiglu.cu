@@ -73,28 +73,21 @@ __device__ __forceinline__ float scale_pow2(uint32_t byte) {
 template <int FMT>
 struct GroupF32 {
     uint32_t byte;
-    float mul;
-    bool nan;
-    __device__ __forceinline__ explicit GroupF32(uint32_t amax_bits) {
-        nan = amax_bits >= 0x7F800000u;
-        const int e = ue8m0_exponent_f32<FMT>(amax_bits);
+    float mul;       // 2^-e; a NaN for a non-finite group, which casts to 0x7F
+    __device__ __forceinline__ explicit GroupF32(float amax) {
+        const uint32_t bits = __float_as_uint(amax) & 0x7FFFFFFFu;
+        const bool nan = bits >= 0x7F800000u;
+        const int e = ue8m0_exponent_f32<FMT>(bits);
         byte = nan ? 0xFFu : static_cast<uint32_t>(e + 127);
-        mul = pow2f(-e);
+        mul = nan ? __uint_as_float(0x7FC00000u) : pow2f(-e);
     }
     __device__ __forceinline__ uint32_t cast4(F2 a, F2 b) const {
         const F2 m = f2(mul);
         a = mul2(a, m);
         b = mul2(b, m);
-        const uint32_t v = __byte_perm(cvt2<FMT>(a.lo(), a.hi()), cvt2<FMT>(b.lo(), b.hi()), 0x5410);
-        return nan ? kNanCodes : v;
+        return __byte_perm(cvt2<FMT>(a.lo(), a.hi()), cvt2<FMT>(b.lo(), b.hi()), 0x5410);
     }
 };
-
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-// The larger of m and both magnitudes, as bit patterns (a NaN's is above all).
-__device__ __forceinline__ uint32_t max_abs(uint32_t m, F2 v) {
-    return max(m, max(abs_bits(v.lo()), abs_bits(v.hi())));
-}
 
 // Maximum over the eight lanes of a group (each half of a packed pair).
 __device__ __forceinline__ uint32_t group_max_u2(uint32_t m) {
@@ -102,29 +95,30 @@ __device__ __forceinline__ uint32_t group_max_u2(uint32_t m) {
     m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     return __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
 }
-__device__ __forceinline__ uint32_t group_max(uint32_t m) {
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+__device__ __forceinline__ float group_max(float m) {
+    m = max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    return max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
 }
 
 // Sixteen BF16 values of a group with this amax -> codes; the scale byte.
 template <int FMT>
 __device__ __forceinline__ uint32_t cast_bf16x16(const uint32_t (&w)[8], uint32_t amax_bits, uint32_t (&c)[4]) {
     const GroupScale<FMT, SCALE_UE8M0> gs(amax_bits);
-    const F2 m = f2(gs.mul);
+    const F2 m = f2(gs.nan ? __uint_as_float(0x7FC00000u) : gs.mul);   // a NaN casts to 0x7F
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const F2 a = mul2(f2_bf16(w[2 * i]), m), b = mul2(f2_bf16(w[2 * i + 1]), m);
-        const uint32_t v = __byte_perm(cvt2<FMT>(a.lo(), a.hi()), cvt2<FMT>(b.lo(), b.hi()), 0x5410);
-        c[i] = gs.nan ? kNanCodes : v;
+        c[i] = __byte_perm(cvt2<FMT>(a.lo(), a.hi()), cvt2<FMT>(b.lo(), b.hi()), 0x5410);
     }
     return gs.byte;
 }
 
 // ------------------------------------------------------------------- forward
+constexpr int kFwdThreadsPerSm = 768;   // 80 registers a thread
+
 template <int FH, int FC, bool CKPT, bool WIDE>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kFwdThreadsPerSm / 256)
     k_swiglu_fwd(const SwigluFwdArgs a, int segs, int total_segs) {
     const int tid = threadIdx.x;
     const int seg = blockIdx.y * segs + tid % segs;
@@ -149,7 +143,7 @@ __global__ void __launch_bounds__(256)
         for (int i = 0; i < 8; ++i) g[i] = ng[i], u[i] = nu[i];
         load(r + step);
         F2 h[8];
-        uint32_t mh = 0;
+        float mh = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const F2 x = f2_bf16(g[i]);
@@ -163,8 +157,8 @@ __global__ void __launch_bounds__(256)
             uint32_t mg = 0, mu = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                mg = __vmaxu2(mg, g[i] & 0x7FFF7FFFu);
-                mu = __vmaxu2(mu, u[i] & 0x7FFF7FFFu);
+                mg = max_abs_bf16x2(mg, g[i]);
+                mu = max_abs_bf16x2(mu, u[i]);
             }
             mgu = group_max_u2(max(mg & 0xFFFFu, mg >> 16) | (max(mu & 0xFFFFu, mu >> 16) << 16));
         }
@@ -300,7 +294,7 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
             const int row = rr + 64 * i;
             const F2 sg = f2(scale_pow2(in.sg[i])), su = f2(scale_pow2(in.su[i]));
             F2 a[8], b[8];
-            uint32_t ma = 0, mb = 0;
+            float ma = 0.0f, mb = 0.0f;
             float *dst = plane + row * kT + (row >> 5) * 8;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -341,14 +335,14 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
 #pragma unroll
         for (int w = 0; w < 3; ++w) {
             F2 v[16];
-            uint32_t m = 0;
+            float m = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 v[i] = f2(src[w * kPlane + 2 * i * kT], src[w * kPlane + (2 * i + 1) * kT]);
                 m = max_abs(m, v[i]);
             }
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            m = max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
             uint32_t q[8], byte;
             if (w < 2) {
                 const GroupF32<FT> gs(m);
@@ -368,8 +362,6 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
         __syncthreads();
     }
 }
-
-constexpr int kFwdThreadsPerSm = 768;   // 80 registers a thread
 
 int sms() {
     static int n[64] = {0};
