@@ -97,31 +97,47 @@ struct Fp4Scale {
             if (!nan) mul = pow2f(-e);
         }
     }
-    // Eight BF16 values (four words) -> eight codes.  Non-finite block: 0.
-    __device__ __forceinline__ uint32_t cast8(const uint32_t *w) const {
+    // Eight values -> eight codes.  Non-finite block: 0.  NV: the residual step
+    // turns -0 into 0.
+    __device__ __forceinline__ uint32_t cast8(F2 (&x)[4]) const {
         float v[8];
         const F2 m2 = f2(mul), nd2 = f2(-d);
+        if (NV && sat) {   // keeps the quotients finite; all such values saturate
+            const float m = 8.0f * d;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = f2(fminf(fmaxf(x[i].lo(), -m), m), fminf(fmaxf(x[i].hi(), -m), m));
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            F2 x = f2_bf16(w[i]);
             if constexpr (NV) {
-                if (sat) {   // keeps the quotient finite; all such values saturate
-                    const float m = 8.0f * d;
-                    x = f2(fminf(fmaxf(x.lo(), -m), m), fminf(fmaxf(x.hi(), -m), m));
-                }
-                const F2 q = mul2(x, m2);
-                const F2 r = fma2(fma2(q, nd2, x), m2, q);
-                // the sign is x's own: the residual of -0 is +0
-                v[2 * i] = copysignf(r.lo(), x.lo());
-                v[2 * i + 1] = copysignf(r.hi(), x.hi());
+                const F2 q = mul2(x[i], m2);
+                x[i] = fma2(fma2(q, nd2, x[i]), m2, q);
             } else {
-                x = mul2(x, m2);
-                v[2 * i] = x.lo();
-                v[2 * i + 1] = x.hi();
+                x[i] = mul2(x[i], m2);
             }
+            v[2 * i] = x[i].lo();
+            v[2 * i + 1] = x[i].hi();
         }
         const uint32_t c = cvt_e2m1x8(v);
         return nan ? 0u : c;
+    }
+    // Eight BF16 values in four words.
+    __device__ __forceinline__ uint32_t cast8(const uint32_t *w) const {
+        F2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = f2_bf16(w[i]);
+        return cast8(x);
+    }
+    // The low (H = 0) or high halves of eight words.
+    template <int H>
+    __device__ __forceinline__ uint32_t cast8_half(const uint32_t *w) const {
+        F2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = H ? f2(__uint_as_float(w[2 * i] & 0xFFFF0000u), __uint_as_float(w[2 * i + 1] & 0xFFFF0000u))
+                     : f2(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i + 1] << 16));
+        return cast8(x);
     }
 };
 

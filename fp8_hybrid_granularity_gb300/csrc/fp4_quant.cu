@@ -180,14 +180,8 @@ __global__ void __launch_bounds__(256)
                 const Fp4Scale<NV> sc(h ? m[part] >> 16 : m[part] & 0xFFFFu, t, rt);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int at = part * 16 + half * 8 + 2 * i;
-                        w[i] = h ? __byte_perm(v[at], v[at + 1], 0x7632)
-                                 : __byte_perm(v[at], v[at + 1], 0x5410);
-                    }
-                    c[part * 2 + half] = sc.cast8(w);
+                    const uint32_t *w = v + part * 16 + half * 8;
+                    c[part * 2 + half] = h ? sc.template cast8_half<1>(w) : sc.template cast8_half<0>(w);
                 }
                 // block index along the rows within the tile
                 if (NV || part == 0) {
@@ -243,22 +237,32 @@ __global__ void __launch_bounds__(512)
                int64_t ld_x, uint32_t *__restrict__ part) {
     __shared__ uint32_t red[16];
     uint32_t m = 0;
-    // segments of 16 elements, rows and segments walked together
+    // segments of 16 elements, rows and segments walked together, the loads of
+    // four in flight
+    constexpr int U = WIDE ? 4 : 2;
     const int64_t n = rows * segs, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     int64_t r = i / segs, c = i % segs;
     const int64_t dr = step / segs, dc = step % segs;
-    for (; i < n; i += step) {
-        uint32_t w[8];
-        ragged::load16<WIDE>(x + r * ld_x + c * 16, cols - c * 16, w);
+    while (i < n) {
+        uint32_t w[U][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t a = w[j] & 0x7FFF7FFFu;
-            m = __vmaxu2(m, a & ~__vcmpgeu2(a, 0x7F807F80u));
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[u][j] = 0u;
+            if (i < n) ragged::load16<WIDE>(x + r * ld_x + c * 16, cols - c * 16, w[u]);
+            i += step;
+            r += dr;
+            c += dc;
+            if (c >= segs) c -= segs, ++r;
         }
-        r += dr;
-        c += dc;
-        if (c >= segs) c -= segs, ++r;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t a = w[u][j] & 0x7FFF7FFFu;
+                m = __vmaxu2(m, a & ~__vcmpgeu2(a, 0x7F807F80u));
+            }
     }
     m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
@@ -422,7 +426,9 @@ cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, cudaStream_t stream) {
 cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, int64_t ld_out, int fp32,
                                cudaStream_t stream) {
     const int64_t segs = (a.k + 15) / 16, tiles = fp4_scale_tiles(a.k, a.kind);
-    const int threads = segs < 256 ? static_cast<int>((segs + 31) / 32 * 32) : 256;
+    // a row's segments in equal blocks of whole warps
+    const int64_t chunks = (segs + 255) / 256;
+    const int threads = static_cast<int>(((segs + chunks - 1) / chunks + 31) / 32 * 32);
     const dim3 grid(static_cast<unsigned>(a.rows), static_cast<unsigned>((segs + threads - 1) / threads));
     auto go = [&](auto kern) {
         kern<<<grid, threads, 0, stream>>>(a.codes, a.scale, a.ts, a.rows, a.k, a.ld, tiles, out, ld_out,

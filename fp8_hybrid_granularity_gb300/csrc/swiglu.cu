@@ -408,8 +408,9 @@ cudaError_t launch_swiglu_fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_swiglu_bwd(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, uint16_t *dg,
                               uint16_t *du, int64_t ld_d, cudaStream_t stream) {
-    const int64_t segs = (c.cols + 15) / 16;
-    const int threads = segs < 256 ? static_cast<int>((segs + 31) / 32 * 32) : 256;
+    // a row's segments in equal blocks of whole warps
+    const int64_t segs = (c.cols + 15) / 16, chunks = (segs + 255) / 256;
+    const int threads = static_cast<int>(((segs + chunks - 1) / chunks + 31) / 32 * 32);
     const dim3 grid(static_cast<unsigned>(c.rows), static_cast<unsigned>((segs + threads - 1) / threads));
     const bool wide = ragged::wide(dh, ld_dh) && ragged::wide(dg, ld_d) && ragged::wide(du, ld_d);
     auto go = [&](auto kern) {

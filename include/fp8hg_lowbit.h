@@ -17,8 +17,8 @@
  *             (amax = 0: b = 0) — the rule of fp8_quant_mx32
  *   FP4HG_NV  16 elements share an E4M3 scale s, and the whole tensor one
  *             FP32 scale t: s = E4M3((amax / 6) / t), nearest even, at most
- *             448; the element's code is E2M1(x / (s t)), a zero of x's sign
- *             where s = 0
+ *             448; the element's code is E2M1(x / (s t)), 0 where x = -0, a
+ *             zero of x's sign where s = 0
  *
  * An element stands for code * 2^(b - 127), or code * s * t.  A block that
  * holds a NaN or an infinity gets the scale byte 0xFF (MX) or 0x7F (NV), a

@@ -86,7 +86,8 @@ def fp4_quant(x, kind, t=1.0):
             d = FP8[E4M3][s] * t
             v = np.where(d[:, None] > 0, b / np.where(d > 0, d, 1.0)[:, None], 0.0)
             s = np.where(bad, 0x7F, s)
-        c = nearest(E2M1, np.abs(v)) | (np.signbit(b) * 8)
+        # the sign of zero: MX keeps it, NV codes -0 as 0
+        c = nearest(E2M1, np.abs(v)) | ((np.signbit(b) if kind == MX else b < 0) * 8)
         codes[:, j * n:(j + 1) * n] = np.where(bad[:, None], 0, c)
         scales[:, j] = s
     return codes, scales
