@@ -226,23 +226,23 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------- backward, FP8
-// Persistent, one CTA of 512 threads per SM, a tile of 128 tokens x 128
+// Persistent, one CTA of 1024 threads per SM, a tile of 128 tokens x 128
 // columns at a time: one group in each direction per row and column.
-//   rows     a thread takes 16 columns of two rows (eight lanes a row),
-//            computes dg, du and h, quantizes dg and du along the row at once
-//            and leaves all three in shared memory in FP32 (they have to be
-//            rounded once, from FP32, in each direction);
-//   columns  a thread takes 32 tokens of one column of each of the three
-//            (four lanes a column: 128 bytes of codes, a whole line).
+//   rows     a thread takes 16 columns of a row (eight lanes a row), computes
+//            dg, du and h, quantizes dg and du along the row at once and leaves
+//            all three in shared memory in FP32 (they have to be rounded once,
+//            from FP32, in each direction);
+//   columns  a thread takes 16 tokens of one column of each of the three
+//            (eight lanes a column: 128 bytes of codes, a whole line).
 // The next tile's inputs are loaded into registers before the column pass, so
 // the loads run under it.
 //
-// Shared memory: value (r, c) at r * 128 + (r / 32) * 8 words plus c with its
+// Shared memory: value (r, c) at r * 128 + (r / 16) * 4 words plus c with its
 // 16-byte piece index i replaced by i ^ ((i / 8) & 3): the eight lanes of a row
-// write pieces in eight different bank groups, and the 8 columns x 4 row
-// quarters that a warp reads at a time fall into 32 banks.
-constexpr int kT = 128, Q_THREADS = 512;
-constexpr int kPlane = kT * kT + 3 * 8;          // words of one of the three
+// write pieces in eight different bank groups, and the 4 columns x 8 row
+// sixteenths that a warp reads at a time fall into 32 banks.
+constexpr int kT = 128, Q_THREADS = 1024;
+constexpr int kPlane = kT * kT + 8 * 4;          // words of one of the three
 constexpr int kQSmem = 3 * kPlane * 4;
 
 template <int F>
@@ -251,31 +251,28 @@ __device__ __forceinline__ void emit_codes(const F2 *v, int n4, const GroupF32<F
     for (int i = 0; i < n4; ++i) c[i] = gs.cast4(v[2 * i], v[2 * i + 1]);
 }
 
-// A thread's inputs of a tile: two rows (0 .. 3 + 64 apart) of 16 columns.
+// A thread's inputs of a tile: 16 columns of a row.
 struct TileIn {
-    uint32_t dh[2][8], g[2][4], u[2][4];
-    uint32_t sg[2], su[2];
+    uint32_t dh[8], g[4], u[4];
+    uint32_t sg, su;
 };
 
 template <bool WIDE>
 __device__ __forceinline__ void load_tile(TileIn &t, const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c,
-                                          int64_t r0, int64_t kb, int rr, int seg) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t r = r0 + rr + 64 * i, col = kb * kT + seg * 16;
-        if (WIDE) {
-            ragged::load16<true>(dh + r * ld_dh + col, 16, t.dh[i]);
-        } else {
-            const uint4 *p = reinterpret_cast<const uint4 *>(dh + r * ld_dh + col);
-            const uint4 a = __ldg(p), b = __ldg(p + 1);
-            t.dh[i][0] = a.x, t.dh[i][1] = a.y, t.dh[i][2] = a.z, t.dh[i][3] = a.w;
-            t.dh[i][4] = b.x, t.dh[i][5] = b.y, t.dh[i][6] = b.z, t.dh[i][7] = b.w;
-        }
-        load_bytes16(c.gq + r * c.ld_q + col, 16, t.g[i]);
-        load_bytes16(c.uq + r * c.ld_q + col, 16, t.u[i]);
-        t.sg[i] = __ldg(c.gs + r * c.ld_s + kb);
-        t.su[i] = __ldg(c.us + r * c.ld_s + kb);
+                                          int64_t r, int64_t kb, int seg) {
+    const int64_t col = kb * kT + seg * 16;
+    if (WIDE) {
+        ragged::load16<true>(dh + r * ld_dh + col, 16, t.dh);
+    } else {
+        const uint4 *p = reinterpret_cast<const uint4 *>(dh + r * ld_dh + col);
+        const uint4 a = __ldg(p), b = __ldg(p + 1);
+        t.dh[0] = a.x, t.dh[1] = a.y, t.dh[2] = a.z, t.dh[3] = a.w;
+        t.dh[4] = b.x, t.dh[5] = b.y, t.dh[6] = b.z, t.dh[7] = b.w;
     }
+    load_bytes16(c.gq + r * c.ld_q + col, 16, t.g);
+    load_bytes16(c.uq + r * c.ld_q + col, 16, t.u);
+    t.sg = __ldg(c.gs + r * c.ld_s + kb);
+    t.su = __ldg(c.us + r * c.ld_s + kb);
 }
 
 template <int FC, int FR, int FT, int FH, bool WIDE>
@@ -283,27 +280,25 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
     k_swiglu_bwd_q(const uint16_t *__restrict__ dh, int64_t ld_dh, const SwigluCkpt c, const SwigluGrads o,
                    int kbs, int tiles) {
     extern __shared__ __align__(16) float plane[];
-    const int tid = threadIdx.x, seg = tid & 7, rr = tid >> 3;
+    const int tid = threadIdx.x, seg = tid & 7, row = tid >> 3;
     TileIn in;
     int tile = blockIdx.x;
-    if (tile < tiles) load_tile<WIDE>(in, dh, ld_dh, c, static_cast<int64_t>(tile / kbs) * kT, tile % kbs, rr, seg);
+    if (tile < tiles) load_tile<WIDE>(in, dh, ld_dh, c, static_cast<int64_t>(tile / kbs) * kT + row, tile % kbs, seg);
     for (; tile < tiles; tile += gridDim.x) {
         const int64_t kb = tile % kbs, rb = tile / kbs, r0 = rb * kT;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = rr + 64 * i;
-            const F2 sg = f2(scale_pow2(in.sg[i])), su = f2(scale_pow2(in.su[i]));
+        {
+            const F2 sg = f2(scale_pow2(in.sg)), su = f2(scale_pow2(in.su));
             F2 a[8], b[8];
             float ma = 0.0f, mb = 0.0f;
-            float *dst = plane + row * kT + (row >> 5) * 8;
+            float *dst = plane + row * kT + (row >> 4) * 4;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 F2 h[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const F2 g = fp8x2_values<FC>(static_cast<uint16_t>(in.g[i][k] >> (16 * j)), sg);
-                    const F2 u = fp8x2_values<FC>(static_cast<uint16_t>(in.u[i][k] >> (16 * j)), su);
-                    swiglu_grads(g, u, f2_bf16(in.dh[i][2 * k + j]), a[2 * k + j], b[2 * k + j], h[j]);
+                    const F2 g = fp8x2_values<FC>(static_cast<uint16_t>(in.g[k] >> (16 * j)), sg);
+                    const F2 u = fp8x2_values<FC>(static_cast<uint16_t>(in.u[k] >> (16 * j)), su);
+                    swiglu_grads(g, u, f2_bf16(in.dh[2 * k + j]), a[2 * k + j], b[2 * k + j], h[j]);
                     ma = max_abs(ma, a[2 * k + j]);
                     mb = max_abs(mb, b[2 * k + j]);
                 }
@@ -327,37 +322,34 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
         __syncthreads();
         const int next = tile + gridDim.x;
         if (next < tiles)
-            load_tile<WIDE>(in, dh, ld_dh, c, static_cast<int64_t>(next / kbs) * kT, next % kbs, rr, seg);
-        // column cc, tokens 32 quarter .. + 31
-        const int quarter = tid & 3, cc = tid >> 2;
+            load_tile<WIDE>(in, dh, ld_dh, c, static_cast<int64_t>(next / kbs) * kT + row, next % kbs, seg);
+        // column cc, tokens 16 part .. + 15
+        const int part = tid & 7, cc = tid >> 3;
         const int word = (((cc >> 2) ^ ((cc >> 5) & 3)) << 2) + (cc & 3);
-        const float *src = plane + quarter * (32 * kT + 8) + word;
+        const float *src = plane + part * (16 * kT + 4) + word;
 #pragma unroll
         for (int w = 0; w < 3; ++w) {
-            F2 v[16];
+            F2 v[8];
             float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 v[i] = f2(src[w * kPlane + 2 * i * kT], src[w * kPlane + (2 * i + 1) * kT]);
                 m = max_abs(m, v[i]);
             }
-            m = max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            uint32_t q[8], byte;
+            m = group_max(m);
+            uint32_t q[4], byte;
             if (w < 2) {
                 const GroupF32<FT> gs(m);
-                emit_codes<FT>(v, 8, gs, q);
+                emit_codes<FT>(v, 4, gs, q);
                 byte = gs.byte;
             } else {
                 const GroupF32<FH> gs(m);
-                emit_codes<FH>(v, 8, gs, q);
+                emit_codes<FH>(v, 4, gs, q);
                 byte = gs.byte;
             }
             const int64_t col = kb * kT + cc;
-            uint4 *d = reinterpret_cast<uint4 *>(o.qt[w] + col * o.ld_qt + r0 + quarter * 32);
-            d[0] = make_uint4(q[0], q[1], q[2], q[3]);
-            d[1] = make_uint4(q[4], q[5], q[6], q[7]);
-            if (quarter == 0) o.st[w][col * o.ld_st + rb] = static_cast<uint8_t>(byte);
+            *reinterpret_cast<uint4 *>(o.qt[w] + col * o.ld_qt + r0 + part * 16) = make_uint4(q[0], q[1], q[2], q[3]);
+            if (part == 0) o.st[w][col * o.ld_st + rb] = static_cast<uint8_t>(byte);
         }
         __syncthreads();
     }
