@@ -289,27 +289,38 @@ __global__ void __launch_bounds__(32)
 }
 
 // ------------------------------------------------------------------- values
+constexpr int kDequantThreadsPerSm = 1536;   // 40 registers a thread
+
 template <bool NV, bool FP32, bool WIDE>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
     k_fp4_dequant(const uint8_t *__restrict__ q, const uint8_t *__restrict__ s,
                   const float *__restrict__ ts, int64_t rows, int64_t k, int64_t ld, int64_t tiles,
                   void *__restrict__ out, int64_t ld_out, int segs) {
     const float t = NV && ts ? __ldg(ts) : 1.0f;
     const int g = blockIdx.y * blockDim.x + threadIdx.x;
     const int64_t c0 = static_cast<int64_t>(g) * 16, left = k - c0;
+    // the next row's codes and scale are in flight while a row is written
+    uint2 next = make_uint2(0u, 0u);
+    uint32_t next_scale = 0;
+    auto load = [&](int64_t r) {
+        if (r >= rows || g >= segs) return;
+        const uint8_t *src = q + r * ld + c0 / 2;
+        if (left >= 16) {
+            next = __ldg(reinterpret_cast<const uint2 *>(src));
+        } else {
+            uint64_t v = 0;
+            for (int i = 0; i < (left + 1) / 2; ++i) v |= static_cast<uint64_t>(__ldg(src + i)) << (8 * i);
+            next = make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+        }
+        next_scale = __ldg(s + fp4_scale_offset(r, NV ? g : g >> 1, tiles));
+    };
+    load(blockIdx.x);
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const uint32_t w[2] = {next.x, next.y}, byte = next_scale;
+        load(r + gridDim.x);
         float v[16];
         if (g < segs) {
-            uint32_t w[2] = {0, 0};
-            const uint8_t *src = q + r * ld + c0 / 2;
-            if (left >= 16) {
-                const uint2 p = __ldg(reinterpret_cast<const uint2 *>(src));
-                w[0] = p.x, w[1] = p.y;
-            } else {
-                for (int i = 0; i < (left + 1) / 2; ++i)
-                    w[i >> 2] |= static_cast<uint32_t>(__ldg(src + i)) << (8 * (i & 3));
-            }
-            const float sc = fp4_scale_value<NV>(__ldg(s + fp4_scale_offset(r, NV ? g : g >> 1, tiles)));
+            const float sc = fp4_scale_value<NV>(byte);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float u[8];
@@ -429,7 +440,10 @@ cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, int64_t ld_out, i
     // a row's segments in equal blocks of whole warps
     const int64_t chunks = (segs + 255) / 256;
     const int threads = static_cast<int>(((segs + chunks - 1) / chunks + 31) / 32 * 32);
-    const dim3 grid(static_cast<unsigned>(a.rows), static_cast<unsigned>((segs + threads - 1) / threads));
+    const int64_t cb = (segs + threads - 1) / threads;
+    // as many CTAs as fit at once
+    const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kDequantThreadsPerSm / threads) / cb);
+    const dim3 grid(static_cast<unsigned>(std::min(a.rows, resident)), static_cast<unsigned>(cb));
     auto go = [&](auto kern) {
         kern<<<grid, threads, 0, stream>>>(a.codes, a.scale, a.ts, a.rows, a.k, a.ld, tiles, out, ld_out,
                                            static_cast<int>(segs));

@@ -3,6 +3,7 @@
 // the launches.  Nothing here allocates device memory or synchronizes.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -53,8 +54,18 @@ int check_opts(const fp8hg_gemm_opts *opts) {
     return opts->tile == 0 ? FP8HG_OK : FP8HG_ERR_UNSUPPORTED;
 }
 
+// The current device's error word; its address is looked up once per device.
+unsigned int *error_word() {
+    static std::atomic<unsigned int *> words[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fp8hg::device_error_word();
+    unsigned int *w = words[dev].load(std::memory_order_relaxed);
+    if (!w) words[dev].store(w = fp8hg::device_error_word(), std::memory_order_relaxed);
+    return w;
+}
+
 int run_gemm(fp8hg::Fp4GemmArgs &g, const fp8hg_gemm_opts *opts, void *stream) {
-    unsigned int *err = fp8hg::device_error_word();
+    unsigned int *err = error_word();
     if (!err) return FP8HG_ERR_CUDA;
     g.wait_limit_ns = opts && opts->wait_limit_ns ? opts->wait_limit_ns : kDefaultWaitNs;
     g.inject_fault = opts ? opts->inject_fault : 0;

@@ -18,6 +18,7 @@ checked and marshalled and the CUDA kernels do all of the computation.
 from __future__ import annotations
 
 import ctypes
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -232,7 +233,8 @@ def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None, stream=None):
     """The values of a 4-bit tensor, [rows, k], BF16 or FP32."""
     if out is None:
         out = torch.empty((q.rows, q.k), dtype=out_dtype or torch.bfloat16, device=q.codes.device)
-    _check_out(out, q.rows, q.k)
+    else:
+        _check_out(out, q.rows, q.k)
     op = q.operand()
     _check(_fns().fp4_dequant(ctypes.byref(op), out.data_ptr(), _ld(out), _out_kind(out),
                               _on(stream, out)), "fp4_dequant")
@@ -247,7 +249,8 @@ def fp4_gemm_scaled(a: Fp4Tensor, b: Fp4Tensor, out=None, out_dtype=None, accumu
             raise ValueError("accumulate needs out")
         out = torch.empty((a.rows, b.rows), dtype=out_dtype or torch.bfloat16,
                           device=a.codes.device)
-    _check_out(out, a.rows, b.rows)
+    else:
+        _check_out(out, a.rows, b.rows)
     oa, ob = a.operand(), b.operand()
     _check(_fns().fp4_gemm_scaled(ctypes.byref(oa), ctypes.byref(ob), out.data_ptr(), _ld(out),
                                   _out_kind(out), 1 if accumulate else 0,
@@ -267,17 +270,43 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
     rows = x.shape[0]
     if out is None:
         out = torch.empty((rows, w.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
-    _check_out(out, rows, w.rows)
-    f = _fns()
-    n = f.fp4_linear_workspace(rows, w.k, w.kind)
+    else:
+        _check_out(out, rows, w.rows)
+    stream = _on(stream, x)
+    n = 0 if rows <= 4 else _linear_bytes(rows, w.k, w.kind)
     if n and workspace is None:
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(n, x, stream)
     ow = w.operand()
-    _check(f.fp4_linear(x.data_ptr(), rows, _ld(x), _ts(tensor_scale), ctypes.byref(ow),
-                        out.data_ptr(), _ld(out), _out_kind(out),
-                        workspace.data_ptr() if n else None, workspace.numel() if n else 0,
-                        _opts(wait_limit_ns, inject_fault), _on(stream, x)), "fp4_linear")
+    _check(_fns().fp4_linear(x.data_ptr(), rows, _ld(x), _ts(tensor_scale), ctypes.byref(ow),
+                             out.data_ptr(), _ld(out), _out_kind(out),
+                             workspace.data_ptr() if n else None, workspace.numel() if n else 0,
+                             _opts(wait_limit_ns, inject_fault), stream), "fp4_linear")
     return out
+
+
+def _linear_bytes(rows, k, kind) -> int:
+    """fp4_linear_workspace of the library for more than four rows."""
+    return (rows * ((k + 31) // 32 * 16) +
+            (rows + 127) // 128 * ((k + 255) // 256) * (2048 if kind == FP4_NV else 1024))
+
+
+_scratch_of = threading.local()
+_SCRATCH = 1 << 20
+
+
+def _scratch(n, x, stream):
+    """n bytes on x's device for one call on `stream`.  Up to 1 MB they are kept
+    for the next call of this thread on the stream (an allocation takes a
+    third of such a call's time on the host); under stream capture, where the
+    graph may outlive them, and above that they are allocated."""
+    if n > _SCRATCH or torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(n, dtype=torch.uint8, device=x.device)
+    kept = _scratch_of.__dict__
+    key = (x.get_device(), stream)
+    t = kept.get(key)
+    if t is None:
+        t = kept[key] = torch.empty(_SCRATCH, dtype=torch.uint8, device=x.device)
+    return t
 
 
 def fp4_linear_workspace(rows: int, k: int, kind: int) -> int:
@@ -293,15 +322,19 @@ class SwigluCkpt:
     up: QTensor
 
 
+def _codes(rows, cols, device):
+    """[rows, cols] bytes, rows padded to 16."""
+    if cols % 16:
+        return torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.uint8,
+                                   device=device)
+    return torch.empty((rows, cols), dtype=torch.uint8, device=device)
+
+
 def _groups(rows, cols, fmt, device):
     """[rows, cols] codes (rows padded to 16 bytes) and their 1x128 scales."""
     g = (cols + 127) // 128
-    if cols % 16:
-        q = torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.uint8,
-                                device=device)
-    else:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=device)
-    return QTensor(q, torch.empty((rows, _round4(g)), dtype=torch.uint8, device=device), fmt,
+    return QTensor(_codes(rows, cols, device),
+                   torch.empty((rows, _round4(g)), dtype=torch.uint8, device=device), fmt,
                    GRAN_1x128, g)
 
 
@@ -321,19 +354,21 @@ def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bo
     if gate.shape != up.shape or _ld(gate) != _ld(up):
         raise ValueError("gate and up must have the same shape and row stride")
     rows, cols = gate.shape
-    h = _groups(rows, cols, fmt_h, gate.device)
-    g = u = None
-    ptr = [None] * 4
-    ld_q = ld_s = 0
+    dev, n, ld = gate.device, (cols + 127) // 128, (cols + 15) // 16 * 16
+    ls = _round4(n)
+    h, sh = _codes(rows, cols, dev), torch.empty((rows, ls), dtype=torch.uint8, device=dev)
+    ptr = (None, None, None, None)
     if checkpoint:
-        g, u = (_groups(rows, cols, fmt, gate.device) for _ in range(2))
-        ptr = [g.codes.data_ptr(), g.scale.data_ptr(), u.codes.data_ptr(), u.scale.data_ptr()]
-        ld_q, ld_s = _ld_codes(g.codes), g.scale.stride(0)
+        g, sg = _codes(rows, cols, dev), torch.empty((rows, ls), dtype=torch.uint8, device=dev)
+        u, su = _codes(rows, cols, dev), torch.empty((rows, ls), dtype=torch.uint8, device=dev)
+        ptr = (g.data_ptr(), sg.data_ptr(), u.data_ptr(), su.data_ptr())
     _check(_fns().fp8_swiglu_ckpt(gate.data_ptr(), up.data_ptr(), rows, cols, _ld(gate), fmt_h,
-                                  h.codes.data_ptr(), _ld_codes(h.codes), h.scale.data_ptr(),
-                                  h.scale.stride(0), fmt, *ptr, ld_q, ld_s, _on(stream, gate)),
-           "fp8_swiglu_ckpt")
-    return h, SwigluCkpt(g, u) if checkpoint else None
+                                  h.data_ptr(), ld, sh.data_ptr(), ls, fmt, *ptr, ld, ls,
+                                  _on(stream, gate)), "fp8_swiglu_ckpt")
+    h = QTensor(h, sh, fmt_h, GRAN_1x128, n)
+    if not checkpoint:
+        return h, None
+    return h, SwigluCkpt(QTensor(g, sg, fmt, GRAN_1x128, n), QTensor(u, su, fmt, GRAN_1x128, n))
 
 
 def _ckpt(c: SwigluCkpt, dh) -> _Ckpt:
@@ -358,8 +393,9 @@ def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None, stream=None):
     rows, cols = dh.shape
     if out is None:
         out = torch.empty((rows, 2 * cols), dtype=torch.bfloat16, device=dh.device)
-    _check_out(out, rows, 2 * cols)
-    _check_matrix(out, "out")
+    else:
+        _check_out(out, rows, 2 * cols)
+        _check_matrix(out, "out")
     _check(_fns().fp8_swiglu_ckpt_bwd(dh.data_ptr(), _ld(dh), ctypes.byref(c), out.data_ptr(),
                                       out.data_ptr() + 2 * cols, _ld(out), _on(stream, dh)),
            "fp8_swiglu_ckpt_bwd")

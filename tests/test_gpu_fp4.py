@@ -336,6 +336,34 @@ def test_captured_into_a_graph(cuda_lib):
     assert torch.equal(y, want)
 
 
+def test_linear_from_several_threads_and_streams(cuda_lib):
+    """Calls whose scratch is kept between them: streams of their own, one
+    stream shared by two threads, another size each time."""
+    import threading
+    ws = [stored(300 + 100 * i, 1024, MX, 80 + i)[0] for i in range(3)]
+    xs = [gpu(data(8 + 50 * i, 1024, 90 + i)) for i in range(3)]
+    want = [[fp8hg.fp4_linear(x, w) for w in ws] for x in xs]
+    torch.cuda.synchronize()
+    shared, bad = torch.cuda.Stream(), []
+
+    def work(stream):
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = [[fp8hg.fp4_linear(x, w) for w in ws] for x in xs]
+        stream.synchronize()
+        for i in range(3):
+            for j in range(3):
+                if not torch.equal(got[i][j], want[i][j]):
+                    bad.append((i, j))
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in (shared, shared, torch.cuda.Stream())]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_empty(cuda_lib):
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
     q = fp8hg.fp4_quant(x, MX)
@@ -343,6 +371,13 @@ def test_empty(cuda_lib):
     assert fp8hg.fp4_gemm_scaled(q, w).shape == (0, 8)
     assert fp8hg.fp4_linear(x, w).shape == (0, 8)
     assert fp8hg.fp4_tensor_scale(x).item() == 1.0
+
+
+def test_linear_scratch_size(cuda_lib):
+    from fp8_hybrid_granularity_gb300 import lowbit
+    for kind in (MX, NV):
+        for rows, k in ((5, 1), (127, 3584), (129, 257), (1000, 8960)):
+            assert lowbit._linear_bytes(rows, k, kind) == fp8hg.fp4_linear_workspace(rows, k, kind)
 
 
 def test_python_refusals(cuda_lib):
