@@ -148,9 +148,10 @@ __device__ __forceinline__ float fp4_reciprocal(float t) {
 }
 
 // Byte offset of (row, block j) in a scale array with `tiles` tiles along k.
-__device__ __forceinline__ int64_t fp4_scale_offset(int64_t row, int64_t j, int64_t tiles) {
-    const int r = static_cast<int>(row & 127);
-    return ((row >> 7) * tiles + (j >> 2)) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (j & 3);
+__device__ __forceinline__ int64_t fp4_scale_offset(uint32_t row, uint32_t j, uint32_t tiles) {
+    const uint32_t r = row & 127;
+    const uint64_t tile = static_cast<uint64_t>(row >> 7) * tiles + (j >> 2);
+    return static_cast<int64_t>(tile * 512 + (r & 31) * 16 + (r >> 5) * 4 + (j & 3));
 }
 
 }  // namespace fp8hg

@@ -31,7 +31,7 @@ __device__ __forceinline__ uint32_t abs_max16(const uint32_t (&w)[8]) {
 }
 
 // The low `n` bytes of eight code bytes to p (8-byte aligned).
-__device__ __forceinline__ void store_codes(uint8_t *p, uint32_t lo, uint32_t hi, int64_t n) {
+__device__ __forceinline__ void store_codes(uint8_t *p, uint32_t lo, uint32_t hi, int n) {
     if (n >= 8) {
         *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
     } else {
@@ -58,27 +58,27 @@ constexpr int kRowThreadsPerSm = 1280;   // 48 registers a thread
 
 template <bool NV, bool WIDE>
 __global__ void __launch_bounds__(256, kRowThreadsPerSm / 256)
-    k_fp4_rows(const uint16_t *__restrict__ x, int64_t rows, int64_t cols, int64_t ld_x,
-               const float *__restrict__ ts, uint8_t *__restrict__ q, int64_t ld_q,
-               uint8_t *__restrict__ s, int64_t tiles, int segs, int total_segs) {
+    k_fp4_rows(const uint16_t *__restrict__ x, uint32_t rows, int cols, uint32_t ld_x,
+               const float *__restrict__ ts, uint8_t *__restrict__ q, uint32_t ld_q,
+               uint8_t *__restrict__ s, uint32_t tiles, int segs, int total_segs) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int seg = blockIdx.y * segs + tid % segs;
     const int rpb = blockDim.x / segs;
     const float t = NV && ts ? __ldg(ts) : 1.0f, rt = fp4_reciprocal<NV>(t);
-    const int64_t c0 = static_cast<int64_t>(seg) * 16;
+    const int c0 = seg * 16;
     constexpr int LPB = NV ? 1 : 2;
     // The next row's load is in flight while a row is cast: a CTA per row
     // spent most of its time waiting for its one load (8192 x 3584, NV: 23.6 us).
     // Every lane of the warp stays in the loop for the shuffles.
-    const int64_t step = static_cast<int64_t>(gridDim.x) * rpb;
+    const uint32_t step = gridDim.x * rpb;
     const bool mine = tid / segs < rpb && seg < total_segs;
     uint32_t next[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    auto load = [&](int64_t r) {
-        if (mine && r < rows && c0 < cols) ragged::load16<WIDE>(x + r * ld_x + c0, cols - c0, next);
+    auto load = [&](uint32_t r) {
+        if (mine && r < rows && c0 < cols) ragged::load16<WIDE>(x + row_at(r, ld_x) + c0, cols - c0, next);
     };
-    load(static_cast<int64_t>(blockIdx.x) * rpb + tid / segs);
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < rows; r0 += step) {
-        const int64_t r = r0 + tid / segs;
+    load(blockIdx.x * rpb + tid / segs);
+    for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step) {
+        const uint32_t r = r0 + tid / segs;
         const bool in = mine && r < rows;
         uint32_t w[8];
 #pragma unroll
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(256, kRowThreadsPerSm / 256)
         if (!in) continue;
         if (c0 < cols) {
             const uint32_t lo = sc.cast8(w), hi = sc.cast8(w + 4);
-            store_codes(q + r * ld_q + c0 / 2, lo, hi, (cols - c0 + 1) / 2);
+            store_codes(q + row_at(r, ld_q) + c0 / 2, lo, hi, (cols - c0 + 1) / 2);
         }
         if (lane % (4 * LPB) == 0)
             *reinterpret_cast<uint32_t *>(s + fp4_scale_offset(r, seg / LPB, tiles)) = word;
@@ -110,34 +110,33 @@ constexpr int kTile = 128;
 
 template <bool NV, bool WIDE, bool ROWS>
 __global__ void __launch_bounds__(256)
-    k_fp4_tile(const uint16_t *__restrict__ x, int64_t rows, int64_t cols, int64_t ld_x,
-               const float *__restrict__ ts, uint8_t *__restrict__ q, int64_t ld_q,
-               uint8_t *__restrict__ s, int64_t tiles, uint8_t *__restrict__ qt, int64_t ld_qt,
-               uint8_t *__restrict__ st, int64_t tiles_t) {
+    k_fp4_tile(const uint16_t *__restrict__ x, int rows, int cols, uint32_t ld_x,
+               const float *__restrict__ ts, uint8_t *__restrict__ q, uint32_t ld_q,
+               uint8_t *__restrict__ s, uint32_t tiles, uint8_t *__restrict__ qt, uint32_t ld_qt,
+               uint8_t *__restrict__ st, uint32_t tiles_t) {
     constexpr int NT = NV ? 2 : 1;          // scale tiles of 4 blocks per 128 elements
     constexpr int LPB = NV ? 1 : 2;
     __shared__ __align__(16) uint8_t tile[kTile * 256];
     __shared__ __align__(16) uint8_t codes[kTile * 64];
     __shared__ __align__(16) uint8_t scales[2][NT * 512];
     const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile;
-    const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTile;
+    const int r0 = blockIdx.y * kTile, k0 = blockIdx.x * kTile;
     const float t = NV && ts ? __ldg(ts) : 1.0f, rt = fp4_reciprocal<NV>(t);
     {
         const int seg = tid & 7;
-        const int64_t c0 = k0 + seg * 16;
+        const int c0 = k0 + seg * 16;
         uint32_t w[4][8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + (tid >> 3) + i * 32;
+            const int r = r0 + (tid >> 3) + i * 32;
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[i][j] = 0;
-            if (r < rows && c0 < cols) ragged::load16<WIDE>(x + r * ld_x + c0, cols - c0, w[i]);
+            if (r < rows && c0 < cols) ragged::load16<WIDE>(x + row_at(r, ld_x) + c0, cols - c0, w[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int rr = (tid >> 3) + i * 32;
-            const int64_t r = r0 + rr;
+            const int r = r0 + rr;
             // 16-byte pieces 2 seg and 2 seg + 1, swapped in the row's upper
             // half so that eight lanes' writes fall into different banks
             uint4 *row = reinterpret_cast<uint4 *>(tile + rr * 256);
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(256)
                                                   (rr & 31) * 16 + (rr >> 5) * 4) = word;
                 if (r < rows && c0 < cols) {
                     const uint32_t lo = sc.cast8(w[i]), hi = sc.cast8(w[i] + 4);
-                    store_codes(q + r * ld_q + c0 / 2, lo, hi, (cols - c0 + 1) / 2);
+                    store_codes(q + row_at(r, ld_q) + c0 / 2, lo, hi, (cols - c0 + 1) / 2);
                 }
             }
         }
@@ -197,15 +196,15 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     // columns' codes: four lanes write one column's 64 bytes
     {
-        const int64_t bytes = (rows + 1) / 2;   // of a whole column
+        const int bytes = (rows + 1) / 2;   // of a whole column
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int idx = i * 256 + tid, col = idx >> 2, b = idx & 3;
-            const int64_t at = r0 / 2 + b * 16;
+            const int at = r0 / 2 + b * 16;
             if (k0 + col >= cols || at >= bytes) continue;
             const uint4 v = *reinterpret_cast<const uint4 *>(codes + col * 64 +
                                                              ((b ^ ((col >> 1) & 3)) << 4));
-            uint8_t *d = qt + (k0 + col) * ld_qt + at;
+            uint8_t *d = qt + row_at(k0 + col, ld_qt) + at;
             if (at + 16 <= bytes) {
                 *reinterpret_cast<uint4 *>(d) = v;
             } else {
@@ -218,52 +217,52 @@ __global__ void __launch_bounds__(256)
     // (this kernel's tile then lies past the tensor) and is written too
     if (tid < 32 * NT) {
         if (ROWS && r0 < rows)
-            reinterpret_cast<uint4 *>(s + ((r0 >> 7) * tiles + (k0 >> 7) * NT) * 512)[tid] =
+            reinterpret_cast<uint4 *>(s + (row_at(r0 >> 7, tiles) + (k0 >> 7) * NT) * 512)[tid] =
                 reinterpret_cast<const uint4 *>(scales[0])[tid];
     } else if (tid >= 64 && tid < 64 + 32 * NT) {
         if (k0 < cols)
-            reinterpret_cast<uint4 *>(st + ((k0 >> 7) * tiles_t + (r0 >> 7) * NT) * 512)[tid - 64] =
+            reinterpret_cast<uint4 *>(st + (row_at(k0 >> 7, tiles_t) + (r0 >> 7) * NT) * 512)[tid - 64] =
                 reinterpret_cast<const uint4 *>(scales[1])[tid - 64];
     }
 }
 
 // ------------------------------------------------------------- tensor scale
-constexpr int kAmaxBlocks = 608;
+constexpr int kAmaxBlocks = 512;     // partial maxima at most
+constexpr int kAmaxCtasPerSm = 2;    // as many as fit (54 registers a thread)
 
 // Largest finite |x| pattern per CTA.
 template <bool WIDE>
 __global__ void __launch_bounds__(512)
-    k_fp4_amax(const uint16_t *__restrict__ x, int64_t rows, int64_t segs, int64_t cols,
-               int64_t ld_x, uint32_t *__restrict__ part) {
+    k_fp4_amax(const uint16_t *__restrict__ x, int rows, int segs, int cols, uint32_t ld_x,
+               uint32_t *__restrict__ part) {
     __shared__ uint32_t red[16];
     uint32_t m = 0;
     // segments of 16 elements, rows and segments walked together, the loads of
     // four in flight
     constexpr int U = WIDE ? 4 : 2;
-    const int64_t n = rows * segs, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    int64_t r = i / segs, c = i % segs;
-    const int64_t dr = step / segs, dc = step % segs;
-    while (i < n) {
+    // a pattern plus 0x80 is negative as a signed half exactly if it is not finite
+    const uint32_t step = gridDim.x * blockDim.x;
+    uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;
+    uint32_t r = i / segs, c = i % segs;
+    const uint32_t dr = step / segs, dc = step % segs;
+    while (r < static_cast<uint32_t>(rows)) {
         uint32_t w[U][8];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[u][j] = 0u;
-            if (i < n) ragged::load16<WIDE>(x + r * ld_x + c * 16, cols - c * 16, w[u]);
-            i += step;
+            if (r < static_cast<uint32_t>(rows))
+                ragged::load16<WIDE>(x + row_at(r, ld_x) + c * 16, cols - static_cast<int>(c) * 16, w[u]);
             r += dr;
             c += dc;
-            if (c >= segs) c -= segs, ++r;
+            if (c >= static_cast<uint32_t>(segs)) c -= segs, ++r;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t a = w[u][j] & 0x7FFF7FFFu;
-                m = __vmaxu2(m, a & ~__vcmpgeu2(a, 0x7F807F80u));
-            }
+            for (int j = 0; j < 8; ++j) m = __vmaxs2(m, (w[u][j] & 0x7FFF7FFFu) + 0x00800080u);
     }
+    m = __vmaxs2(m, 0x00800080u) - 0x00800080u;
     m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -294,17 +293,17 @@ constexpr int kDequantThreadsPerSm = 1536;   // 40 registers a thread
 template <bool NV, bool FP32, bool WIDE>
 __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
     k_fp4_dequant(const uint8_t *__restrict__ q, const uint8_t *__restrict__ s,
-                  const float *__restrict__ ts, int64_t rows, int64_t k, int64_t ld, int64_t tiles,
-                  void *__restrict__ out, int64_t ld_out, int segs) {
+                  const float *__restrict__ ts, uint32_t rows, int k, uint32_t ld, uint32_t tiles,
+                  void *__restrict__ out, uint32_t ld_out, int segs) {
     const float t = NV && ts ? __ldg(ts) : 1.0f;
     const int g = blockIdx.y * blockDim.x + threadIdx.x;
-    const int64_t c0 = static_cast<int64_t>(g) * 16, left = k - c0;
+    const int c0 = g * 16, left = k - c0;
     // the next row's codes and scale are in flight while a row is written
     uint2 next = make_uint2(0u, 0u);
     uint32_t next_scale = 0;
-    auto load = [&](int64_t r) {
+    auto load = [&](uint32_t r) {
         if (r >= rows || g >= segs) return;
-        const uint8_t *src = q + r * ld + c0 / 2;
+        const uint8_t *src = q + row_at(r, ld) + c0 / 2;
         if (left >= 16) {
             next = __ldg(reinterpret_cast<const uint2 *>(src));
         } else {
@@ -315,7 +314,7 @@ __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
         next_scale = __ldg(s + fp4_scale_offset(r, NV ? g : g >> 1, tiles));
     };
     load(blockIdx.x);
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const uint32_t w[2] = {next.x, next.y}, byte = next_scale;
         load(r + gridDim.x);
         float v[16];
@@ -334,7 +333,7 @@ __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
         }
         if constexpr (FP32) {
             if (g >= segs) continue;
-            float *d = static_cast<float *>(out) + r * ld_out + c0;
+            float *d = static_cast<float *>(out) + row_at(r, ld_out) + c0;
             if (WIDE && left >= 16) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -349,7 +348,7 @@ __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
             uint32_t p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[i] = g < segs ? ptx::cvt_bf16x2(v[2 * i], v[2 * i + 1]) : 0u;
-            ragged::store16<WIDE>(static_cast<uint16_t *>(out) + r * ld_out + c0, left, p);
+            ragged::store16<WIDE>(static_cast<uint16_t *>(out) + row_at(r, ld_out) + c0, left, p);
         }
     }
 }
@@ -369,12 +368,12 @@ int sms() {
 
 template <bool NV>
 cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
-    const int64_t total = (a.cols + 255) / 256 * 16;      // segments, k padded to 256
+    const int64_t total = (a.cols + 255LL) / 256 * 16;      // segments, k padded to 256
     const int64_t chunks = (total + 255) / 256;
     const int segs = static_cast<int>((total / 16 + chunks - 1) / chunks * 16);
     const int rpb = 256 / segs;
     const int threads = (segs * rpb + 31) / 32 * 32;
-    const int64_t rblocks = (a.rows + rpb - 1) / rpb, cblocks = (total + segs - 1) / segs;
+    const int64_t rblocks = (static_cast<int64_t>(a.rows) + rpb - 1) / rpb, cblocks = (total + segs - 1) / segs;
     // as many CTAs as fit at once
     const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kRowThreadsPerSm / threads) / cblocks);
     const dim3 grid(static_cast<unsigned>(std::min(rblocks, resident)), static_cast<unsigned>(cblocks));
@@ -393,8 +392,8 @@ cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
 template <bool NV, bool WIDE>
 cudaError_t quant_tile(const Fp4QuantArgs &a, cudaStream_t stream) {
     // tiles cover both directions' padding to 256
-    const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256 * 2),
-                    static_cast<unsigned>((a.rows + 255) / 256 * 2));
+    const dim3 grid(static_cast<unsigned>((a.cols + 255LL) / 256 * 2),
+                    static_cast<unsigned>((a.rows + 255LL) / 256 * 2));
     const int64_t tiles = fp4_scale_tiles(a.cols, a.kind), tiles_t = fp4_scale_tiles(a.rows, a.kind);
     if (a.q)
         k_fp4_tile<NV, WIDE, true><<<grid, 256, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
@@ -411,11 +410,12 @@ cudaError_t quant_tile(const Fp4QuantArgs &a, cudaStream_t stream) {
 
 size_t fp4_tensor_scale_ws_bytes() { return kAmaxBlocks * sizeof(uint32_t); }
 
-cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x,
+cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int rows, int cols, uint32_t ld_x,
                                     float *scale, void *ws, cudaStream_t stream) {
-    const int64_t segs = (cols + 15) / 16, n = rows * segs;
-    int64_t blocks = (n + 511) / 512;
-    if (blocks > kAmaxBlocks) blocks = kAmaxBlocks;
+    const int segs = static_cast<int>((cols + 15LL) / 16);
+    const int64_t n = static_cast<int64_t>(rows) * segs;
+    const int64_t blocks = std::min({(n + 511) / 512, static_cast<int64_t>(kAmaxCtasPerSm) * sms(),
+                                     static_cast<int64_t>(kAmaxBlocks)});
     uint32_t *part = static_cast<uint32_t *>(ws);
     if (n > 0) {
         const unsigned g = static_cast<unsigned>(blocks);
@@ -434,7 +434,7 @@ cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, cudaStream_t stream) {
     return nv ? quant_tile<true, false>(a, stream) : quant_tile<false, false>(a, stream);
 }
 
-cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, int64_t ld_out, int fp32,
+cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, uint32_t ld_out, int fp32,
                                cudaStream_t stream) {
     const int64_t segs = (a.k + 15) / 16, tiles = fp4_scale_tiles(a.k, a.kind);
     // a row's segments in equal blocks of whole warps
@@ -445,8 +445,9 @@ cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, int64_t ld_out, i
     const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kDequantThreadsPerSm / threads) / cb);
     const dim3 grid(static_cast<unsigned>(std::min(a.rows, resident)), static_cast<unsigned>(cb));
     auto go = [&](auto kern) {
-        kern<<<grid, threads, 0, stream>>>(a.codes, a.scale, a.ts, a.rows, a.k, a.ld, tiles, out, ld_out,
-                                           static_cast<int>(segs));
+        kern<<<grid, threads, 0, stream>>>(a.codes, a.scale, a.ts, static_cast<uint32_t>(a.rows),
+                                           static_cast<int>(a.k), static_cast<uint32_t>(a.ld),
+                                           static_cast<uint32_t>(tiles), out, ld_out, static_cast<int>(segs));
         return cudaGetLastError();
     };
     const bool nv = a.kind == FP4_NV;

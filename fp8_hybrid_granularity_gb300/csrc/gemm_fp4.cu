@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                 if (it < n && row < cols && c0 < qi.k) {
                     const uint16_t *src = qi.x + (col0 + row) * qi.ld + c0;
                     if (wide && c0 + 16 <= qi.k) ragged::load16<true>(src, 16, w);
-                    else ragged::load16<false>(src, qi.k - c0, w);
+                    else ragged::load16<false>(src, static_cast<int>(qi.k - c0), w);
                 }
             };
             const int items = (n * (16 << lr) + 127) / 128;

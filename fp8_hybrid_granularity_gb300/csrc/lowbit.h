@@ -20,19 +20,22 @@ inline int64_t fp4_scale_tiles(int64_t k, int kind) {
 inline int64_t fp4_row_tiles(int64_t rows) { return (rows + 127) / 128; }
 
 size_t fp4_tensor_scale_ws_bytes();
-cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x,
+// Rows and columns of a tensor are below 2^31, its row strides too (elements or
+// bytes): a row's offset is then one widening multiplication.
+cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int rows, int cols, uint32_t ld_x,
                                     float *scale, void *ws, cudaStream_t stream);
 
 struct Fp4QuantArgs {
     const uint16_t *x;
-    int64_t rows, cols, ld_x;
+    int rows, cols;
+    uint32_t ld_x;
     int kind;
     const float *ts;
     uint8_t *q;              // along the rows, or null
-    int64_t ld_q;
+    uint32_t ld_q;
     uint8_t *s;
     uint8_t *qt;             // along the columns, or null
-    int64_t ld_qt;
+    uint32_t ld_qt;
     uint8_t *st;
 };
 cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, cudaStream_t stream);
@@ -43,7 +46,7 @@ struct Fp4Operand {
     int64_t rows, k, ld;
     int kind;
 };
-cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, int64_t ld_out, int fp32,
+cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, uint32_t ld_out, int fp32,
                                cudaStream_t stream);
 
 struct Fp4GemmArgs {
@@ -65,30 +68,38 @@ int launch_fp4_gemm(const Fp4GemmArgs &g, cudaStream_t stream);
 
 struct SwigluFwdArgs {
     const uint16_t *gate, *up;
-    int64_t rows, cols, ld_in;
+    int rows, cols;
+    uint32_t ld_in;
     int fmt_h, fmt;
     uint8_t *h, *hs;
-    int64_t ld_h, ld_hs;
+    uint32_t ld_h, ld_hs;
     uint8_t *gq, *gs, *uq, *us;  // the checkpoint, or all null
-    int64_t ld_q, ld_s;
+    uint32_t ld_q, ld_s;
 };
 cudaError_t launch_swiglu_fwd(const SwigluFwdArgs &a, cudaStream_t stream);
 
 struct SwigluCkpt {
     const uint8_t *gq, *gs, *uq, *us;
-    int64_t rows, cols, ld_q, ld_s;
+    int rows, cols;
+    uint32_t ld_q, ld_s;
     int fmt;
 };
-cudaError_t launch_swiglu_bwd(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, uint16_t *dg,
-                              uint16_t *du, int64_t ld_d, cudaStream_t stream);
+cudaError_t launch_swiglu_bwd(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c, uint16_t *dg,
+                              uint16_t *du, uint32_t ld_d, cudaStream_t stream);
 
 struct SwigluGrads {
     uint8_t *q[2], *s[2];        // dgate, dup: 1x128 along the rows
     uint8_t *qt[3], *st[3];      // dgate, dup, h: 1x128 along the tokens, transposed
-    int64_t ld_q, ld_s, ld_qt, ld_st;
+    uint32_t ld_q, ld_s, ld_qt, ld_st;
     int fmt, fmt_t, fmt_h;
+    unsigned int *err;
 };
-cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c,
+cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c,
                                 const SwigluGrads &g, cudaStream_t stream);
+
+// Offset of a row.
+__host__ __device__ inline int64_t row_at(uint32_t row, uint32_t ld) {
+    return static_cast<int64_t>(static_cast<uint64_t>(row) * ld);
+}
 
 }  // namespace fp8hg

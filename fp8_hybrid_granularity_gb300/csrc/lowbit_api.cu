@@ -23,6 +23,8 @@ constexpr uint64_t kDefaultWaitNs = 2000000000ull;   // 2 s
 // Sizes a grid or a tensor map can still hold: 2^30 along a contraction or a
 // row, 65535 tiles of 128 in a grid's second dimension.
 constexpr int64_t kMaxDim = int64_t(1) << 30;
+// Row strides (elements or bytes) of what the element-wise kernels touch.
+constexpr int64_t kMaxLd = 0x7FFFFFFF;
 constexpr int64_t kMaxTiled = int64_t(65535) * 128;
 
 // A 4-bit operand of a call that reads it.
@@ -81,6 +83,7 @@ int check_input(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x) {
     if (rows > kMaxDim || cols > kMaxDim) return FP8HG_ERR_SHAPE;
     if (rows == 0 || cols == 0) return FP8HG_OK;
     if (!x || ld_x < cols) return FP8HG_ERR_INVALID_ARG;
+    if (ld_x > kMaxLd) return FP8HG_ERR_SHAPE;
     return aligned(x, 2) ? FP8HG_OK : FP8HG_ERR_ALIGNMENT;
 }
 
@@ -89,10 +92,12 @@ int check_codes(const uint8_t *q, int64_t ld, int64_t bytes, const uint8_t *s) {
     if (!q && !s) return FP8HG_OK;
     if (!q || !s) return FP8HG_ERR_INVALID_ARG;
     if (!aligned(q, 16) || ld % 16 || !aligned(s, 16)) return FP8HG_ERR_ALIGNMENT;
+    if (ld > kMaxLd) return FP8HG_ERR_SHAPE;
     return ld >= bytes ? FP8HG_OK : FP8HG_ERR_INVALID_ARG;
 }
 
 int64_t codes_ld(int64_t k) { return (k + 31) / 32 * 16; }
+uint32_t u32(int64_t v) { return static_cast<uint32_t>(v); }   // a checked stride
 
 int check_ckpt(const fp8hg_swiglu_ckpt *c) {
     if (!c || !valid_fmt(c->fmt) || c->reserved != 0) return FP8HG_ERR_INVALID_ARG;
@@ -102,11 +107,13 @@ int check_ckpt(const fp8hg_swiglu_ckpt *c) {
     if (!c->gate_q || !c->gate_s || !c->up_q || !c->up_s) return FP8HG_ERR_INVALID_ARG;
     if (!aligned(c->gate_q, 16) || !aligned(c->up_q, 16) || c->ld_q % 16) return FP8HG_ERR_ALIGNMENT;
     if (c->ld_q < c->cols || c->ld_s < (c->cols + 127) / 128) return FP8HG_ERR_INVALID_ARG;
+    if (c->ld_q > kMaxLd || c->ld_s > kMaxLd) return FP8HG_ERR_SHAPE;
     return FP8HG_OK;
 }
 
 fp8hg::SwigluCkpt ckpt(const fp8hg_swiglu_ckpt *c) {
-    return {c->gate_q, c->gate_s, c->up_q, c->up_s, c->rows, c->cols, c->ld_q, c->ld_s, c->fmt};
+    return {c->gate_q, c->gate_s, c->up_q, c->up_s, static_cast<int>(c->rows), static_cast<int>(c->cols),
+            u32(c->ld_q), u32(c->ld_s), c->fmt};
 }
 
 }  // namespace
@@ -127,7 +134,8 @@ int fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x
     if (!scale || !workspace) return FP8HG_ERR_INVALID_ARG;
     if (!aligned(scale, 4) || !aligned(workspace, 16)) return FP8HG_ERR_ALIGNMENT;
     if (workspace_bytes < fp8hg::fp4_tensor_scale_ws_bytes()) return FP8HG_ERR_INVALID_ARG;
-    return status_from_cuda(fp8hg::launch_fp4_tensor_scale(x, rows, cols, ld_x, scale, workspace,
+    return status_from_cuda(fp8hg::launch_fp4_tensor_scale(x, static_cast<int>(rows), static_cast<int>(cols),
+                                                           u32(ld_x), scale, workspace,
                                                            static_cast<cudaStream_t>(stream)));
 }
 
@@ -146,8 +154,9 @@ int fp4_quant(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x, int k
     st = check_codes(q_t, ld_qt, (rows + 1) / 2, scale_t);
     if (st != FP8HG_OK) return st;
     if (q_t && rows > kMaxTiled) return FP8HG_ERR_SHAPE;
-    return status_from_cuda(fp8hg::launch_fp4_quant({x, rows, cols, ld_x, kind, tensor_scale, q,
-                                                     ld_q, scale, q_t, ld_qt, scale_t},
+    return status_from_cuda(fp8hg::launch_fp4_quant({x, static_cast<int>(rows), static_cast<int>(cols), u32(ld_x),
+                                                     kind, tensor_scale, q, u32(ld_q), scale, q_t, u32(ld_qt),
+                                                     scale_t},
                                                     static_cast<cudaStream_t>(stream)));
 }
 
@@ -158,7 +167,8 @@ int fp4_dequant(const fp4hg_operand *a, void *out, int64_t ld_out, int out_kind,
     if (a->rows == 0 || a->k == 0) return FP8HG_OK;
     st = check_output(out, ld_out, a->k, out_kind);
     if (st != FP8HG_OK) return st;
-    return status_from_cuda(fp8hg::launch_fp4_dequant(operand(a), out, ld_out,
+    if (ld_out > kMaxLd || a->ld > kMaxLd) return FP8HG_ERR_SHAPE;
+    return status_from_cuda(fp8hg::launch_fp4_dequant(operand(a), out, u32(ld_out),
                                                       out_kind == FP8HG_OUT_FP32,
                                                       static_cast<cudaStream_t>(stream)));
 }
@@ -229,7 +239,8 @@ int fp4_linear(const uint16_t *x, int64_t rows, int64_t ld_x, const float *tenso
     uint8_t *scale = codes + rows * g.a.ld;
     g.a.scale = scale;
     const cudaError_t e = fp8hg::launch_fp4_quant(
-        {x, rows, w->k, ld_x, w->kind, tensor_scale, codes, g.a.ld, scale, nullptr, 0, nullptr},
+        {x, static_cast<int>(rows), static_cast<int>(w->k), u32(ld_x), w->kind, tensor_scale, codes, u32(g.a.ld),
+         scale, nullptr, 0, nullptr},
         static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return FP8HG_ERR_CUDA;
     return run_gemm(g, opts, stream);
@@ -250,14 +261,16 @@ int fp8_swiglu_ckpt(const uint16_t *gate, const uint16_t *up, int64_t rows, int6
     if (!aligned(h, 16) || ld_h % 16) return FP8HG_ERR_ALIGNMENT;
     const int64_t groups = (cols + 127) / 128;
     if (ld_h < cols || ld_hs < groups) return FP8HG_ERR_INVALID_ARG;
+    if (ld_h > kMaxLd || ld_hs > kMaxLd) return FP8HG_ERR_SHAPE;
     if (keep) {
         if (!gate_q || !gate_s || !up_q || !up_s) return FP8HG_ERR_INVALID_ARG;
         if (!aligned(gate_q, 16) || !aligned(up_q, 16) || ld_q % 16) return FP8HG_ERR_ALIGNMENT;
         if (ld_q < cols || ld_s < groups) return FP8HG_ERR_INVALID_ARG;
+        if (ld_q > kMaxLd || ld_s > kMaxLd) return FP8HG_ERR_SHAPE;
     }
-    return status_from_cuda(fp8hg::launch_swiglu_fwd({gate, up, rows, cols, ld_in, fmt_h, fmt, h,
-                                                      h_scale, ld_h, ld_hs, gate_q, gate_s, up_q,
-                                                      up_s, ld_q, ld_s},
+    return status_from_cuda(fp8hg::launch_swiglu_fwd({gate, up, static_cast<int>(rows), static_cast<int>(cols),
+                                                      u32(ld_in), fmt_h, fmt, h, h_scale, u32(ld_h), u32(ld_hs),
+                                                      gate_q, gate_s, up_q, up_s, u32(ld_q), u32(ld_s)},
                                                      static_cast<cudaStream_t>(stream)));
 }
 
@@ -272,7 +285,8 @@ int fp8_swiglu_ckpt_bwd(const uint16_t *dh, int64_t ld_dh, const fp8hg_swiglu_ck
     if (st != FP8HG_OK) return st;
     st = check_output(dup, ld_d, c->cols, FP8HG_OUT_BF16);
     if (st != FP8HG_OK) return st;
-    return status_from_cuda(fp8hg::launch_swiglu_bwd(dh, ld_dh, ckpt(c), dgate, dup, ld_d,
+    if (ld_d > kMaxLd) return FP8HG_ERR_SHAPE;
+    return status_from_cuda(fp8hg::launch_swiglu_bwd(dh, u32(ld_dh), ckpt(c), dgate, dup, u32(ld_d),
                                                      static_cast<cudaStream_t>(stream)));
 }
 
@@ -289,7 +303,8 @@ int fp8_swiglu_ckpt_bwd_q(const uint16_t *dh, int64_t ld_dh, const fp8hg_swiglu_
     if (!aligned(dh, 16) || ld_dh % 8) return FP8HG_ERR_ALIGNMENT;
     fp8hg::SwigluGrads o{{g->dgate_q, g->dup_q}, {g->dgate_s, g->dup_s},
                          {g->dgate_qt, g->dup_qt, g->h_qt}, {g->dgate_st, g->dup_st, g->h_st},
-                         g->ld_q, g->ld_s, g->ld_qt, g->ld_st, g->fmt, g->fmt_t, g->fmt_h};
+                         u32(g->ld_q), u32(g->ld_s), u32(g->ld_qt), u32(g->ld_st), g->fmt, g->fmt_t, g->fmt_h,
+                         nullptr};
     for (int i = 0; i < 3; ++i) {
         if ((i < 2 && (!o.q[i] || !o.s[i])) || !o.qt[i] || !o.st[i]) return FP8HG_ERR_INVALID_ARG;
         if ((i < 2 && !aligned(o.q[i], 16)) || !aligned(o.qt[i], 16)) return FP8HG_ERR_ALIGNMENT;
@@ -297,7 +312,10 @@ int fp8_swiglu_ckpt_bwd_q(const uint16_t *dh, int64_t ld_dh, const fp8hg_swiglu_
     if (g->ld_q % 16 || g->ld_qt % 16) return FP8HG_ERR_ALIGNMENT;
     if (g->ld_q < c->cols || g->ld_s < c->cols / 128 || g->ld_qt < c->rows || g->ld_st < c->rows / 128)
         return FP8HG_ERR_INVALID_ARG;
-    return status_from_cuda(fp8hg::launch_swiglu_bwd_q(dh, ld_dh, ckpt(c), o,
+    if (g->ld_q > kMaxLd || g->ld_s > kMaxLd || g->ld_qt > kMaxLd || g->ld_st > kMaxLd) return FP8HG_ERR_SHAPE;
+    o.err = error_word();
+    if (!o.err) return FP8HG_ERR_CUDA;
+    return status_from_cuda(fp8hg::launch_swiglu_bwd_q(dh, u32(ld_dh), ckpt(c), o,
                                                        static_cast<cudaStream_t>(stream)));
 }
 

@@ -29,6 +29,12 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     return r;
 }
 __device__ __forceinline__ float max_abs(float m, F2 v) { return max3_abs(m, v.lo(), v.hi()); }
+// The largest magnitude of a warp, a NaN if one is.
+__device__ __forceinline__ float warp_max_abs(float m) {
+    float r;
+    asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+    return r;
+}
 // Magnitudes of two BF16 pairs, the larger in each half (a NaN if one is).
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) {
     uint32_t r;

@@ -40,7 +40,7 @@ __device__ __forceinline__ void shift_down(uint32_t (&w)[12], uint32_t b) {
 
 // Values p[0 .. 15], zeros from index `left` on (left > 0).
 template <bool WIDE>
-__device__ __forceinline__ void load16(const uint16_t *p, int64_t left, uint32_t (&v)[8]) {
+__device__ __forceinline__ void load16(const uint16_t *p, int left, uint32_t (&v)[8]) {
     if (WIDE && left >= 16) {
         asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
@@ -70,7 +70,7 @@ __device__ __forceinline__ void load16(const uint16_t *p, int64_t left, uint32_t
 // Values to p[0 .. 15], the first `left` of them (none if left <= 0).  Every
 // lane of the warp calls it; lanes without a row pass left = 0.
 template <bool WIDE>
-__device__ __forceinline__ void store16(uint16_t *p, int64_t left, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void store16(uint16_t *p, int left, const uint32_t (&v)[8]) {
     if (WIDE) {
         if (left >= 16) {
             asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),

@@ -34,7 +34,7 @@ __device__ __forceinline__ F2 sigmoid2(F2 g) {
 }
 
 // Sixteen code bytes (aligned) to p, the first `left` of them.
-__device__ __forceinline__ void store_bytes16(uint8_t *p, const uint32_t (&c)[4], int64_t left) {
+__device__ __forceinline__ void store_bytes16(uint8_t *p, const uint32_t (&c)[4], int left) {
     if (left >= 16) {
         *reinterpret_cast<uint4 *>(p) = make_uint4(c[0], c[1], c[2], c[3]);
     } else {
@@ -44,7 +44,7 @@ __device__ __forceinline__ void store_bytes16(uint8_t *p, const uint32_t (&c)[4]
     }
 }
 
-__device__ __forceinline__ void load_bytes16(const uint8_t *p, int64_t left, uint32_t (&c)[4]) {
+__device__ __forceinline__ void load_bytes16(const uint8_t *p, int left, uint32_t (&c)[4]) {
     if (left >= 16) {
         const uint4 v = ptx::ld_stream_v4(p);
         c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
@@ -56,38 +56,60 @@ __device__ __forceinline__ void load_bytes16(const uint8_t *p, int64_t left, uin
     }
 }
 
-// Two FP8 codes -> their values times m.
+// Four values -> four FP8 codes.
 template <int FMT>
-__device__ __forceinline__ F2 fp8x2_values(uint16_t c, F2 m) {
-    float lo, hi;
-    ptx::f16x2_to_f32(FMT == FMT_E4M3 ? ptx::cvt_f16x2_e4m3x2(c) : ptx::cvt_f16x2_e5m2x2(c), lo, hi);
-    return mul2(f2(lo, hi), m);
+__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
+    return FMT == FMT_E4M3 ? ptx::cvt_e4m3x4(a, b, c, d) : ptx::cvt_e5m2x4(a, b, c, d);
 }
 
-// A scale byte's power of two; NaN for the byte of a non-finite group.
+// Four FP8 codes -> their values times m.
+template <int FMT>
+__device__ __forceinline__ void fp8x4_values(uint32_t c, F2 m, F2 (&v)[2]) {
+    uint32_t h[2];
+    if constexpr (FMT == FMT_E4M3) ptx::cvt_f16x4_e4m3x4(c, h[0], h[1]);
+    else ptx::cvt_f16x4_e5m2x4(c, h[0], h[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float lo, hi;
+        ptx::f16x2_to_f32(h[i], lo, hi);
+        v[i] = mul2(f2(lo, hi), m);
+    }
+}
+
+// A scale byte's power of two (2^-127, a subnormal, for 0); NaN for the byte of
+// a non-finite group.
 __device__ __forceinline__ float scale_pow2(uint32_t byte) {
-    return byte == 0xFFu ? __uint_as_float(0x7FC00000u) : pow2f(static_cast<int>(byte) - 127);
+    return __uint_as_float((byte << 23) | (byte == 0u || byte == 0xFFu ? 0x400000u : 0u));
 }
 
-// FP32 group scale (round-up rule); non-finite: byte 0xFF.
-template <int FMT>
-struct GroupF32 {
+// A group's scale, the power of two at or above amax / FMAX (FMAX = 1.75 2^emax),
+// without a branch.  amax is the magnitude's bit pattern with MANT mantissa
+// bits below the exponent, from max3_abs or max_abs_bf16x2: adding just under a
+// quarter of the exponent's unit carries exactly if the mantissa is past 1.75.
+// Zero and values below the range: byte 0.  Non-finite: 0xFF and a NaN
+// multiplier, which casts to 0x7F.
+template <int FMT, int MANT>
+struct Group {
     uint32_t byte;
-    float mul;       // 2^-e; a NaN for a non-finite group, which casts to 0x7F
-    __device__ __forceinline__ explicit GroupF32(float amax) {
-        const uint32_t bits = __float_as_uint(amax) & 0x7FFFFFFFu;
-        const bool nan = bits >= 0x7F800000u;
-        const int e = ue8m0_exponent_f32<FMT>(bits);
-        byte = nan ? 0xFFu : static_cast<uint32_t>(e + 127);
-        mul = nan ? __uint_as_float(0x7FC00000u) : pow2f(-e);
+    float mul;       // 2^(127 - byte)
+    __device__ __forceinline__ explicit Group(float amax) { init(__float_as_uint(amax)); }
+    __device__ __forceinline__ explicit Group(uint32_t amax) { init(amax); }
+    __device__ __forceinline__ void init(uint32_t amax) {
+        constexpr int emax = (FMT == FMT_E4M3) ? 8 : 15;
+        const int e = max(static_cast<int>((amax + (1u << (MANT - 2)) - 1u) >> MANT) - emax, 0);
+        const bool nan = amax >= 0xFFu << MANT;
+        byte = nan ? 0xFFu : static_cast<uint32_t>(e);
+        mul = __uint_as_float(nan ? 0x7FC00000u : 0x7F000000u - (static_cast<uint32_t>(e) << 23));
     }
     __device__ __forceinline__ uint32_t cast4(F2 a, F2 b) const {
         const F2 m = f2(mul);
         a = mul2(a, m);
         b = mul2(b, m);
-        return __byte_perm(cvt2<FMT>(a.lo(), a.hi()), cvt2<FMT>(b.lo(), b.hi()), 0x5410);
+        return cvt4<FMT>(a.lo(), a.hi(), b.lo(), b.hi());
     }
 };
+template <int FMT>
+using GroupF32 = Group<FMT, 23>;
 
 // Maximum over the eight lanes of a group (each half of a packed pair).
 __device__ __forceinline__ uint32_t group_max_u2(uint32_t m) {
@@ -104,13 +126,9 @@ __device__ __forceinline__ float group_max(float m) {
 // Sixteen BF16 values of a group with this amax -> codes; the scale byte.
 template <int FMT>
 __device__ __forceinline__ uint32_t cast_bf16x16(const uint32_t (&w)[8], uint32_t amax_bits, uint32_t (&c)[4]) {
-    const GroupScale<FMT, SCALE_UE8M0> gs(amax_bits);
-    const F2 m = f2(gs.nan ? __uint_as_float(0x7FC00000u) : gs.mul);   // a NaN casts to 0x7F
+    const Group<FMT, 7> gs(amax_bits);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const F2 a = mul2(f2_bf16(w[2 * i]), m), b = mul2(f2_bf16(w[2 * i + 1]), m);
-        c[i] = __byte_perm(cvt2<FMT>(a.lo(), a.hi()), cvt2<FMT>(b.lo(), b.hi()), 0x5410);
-    }
+    for (int i = 0; i < 4; ++i) c[i] = gs.cast4(f2_bf16(w[2 * i]), f2_bf16(w[2 * i + 1]));
     return gs.byte;
 }
 
@@ -123,21 +141,23 @@ __global__ void __launch_bounds__(256, kFwdThreadsPerSm / 256)
     const int tid = threadIdx.x;
     const int seg = blockIdx.y * segs + tid % segs;
     const int rpb = blockDim.x / segs;
-    const int64_t c0 = static_cast<int64_t>(seg) * 16, left = a.cols - c0;
+    const int c0 = seg * 16, left = a.cols - c0;
     // the next row's loads are in flight while a row is computed
-    const int64_t step = static_cast<int64_t>(gridDim.x) * rpb;
+    const uint32_t step = gridDim.x * rpb;
     const bool mine = tid / segs < rpb && seg < total_segs;
     uint32_t ng[8] = {0, 0, 0, 0, 0, 0, 0, 0}, nu[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    auto load = [&](int64_t r) {
-        if (mine && r < a.rows && left > 0) {
-            ragged::load16<WIDE>(a.gate + r * a.ld_in + c0, left, ng);
-            ragged::load16<WIDE>(a.up + r * a.ld_in + c0, left, nu);
+    const uint32_t rows = a.rows;
+    auto load = [&](uint32_t r) {
+        if (mine && r < rows && left > 0) {
+            const int64_t at = row_at(r, a.ld_in) + c0;
+            ragged::load16<WIDE>(a.gate + at, left, ng);
+            ragged::load16<WIDE>(a.up + at, left, nu);
         }
     };
-    load(static_cast<int64_t>(blockIdx.x) * rpb + tid / segs);
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows; r0 += step) {
-        const int64_t r = r0 + tid / segs;
-        const bool in = mine && r < a.rows;
+    load(blockIdx.x * rpb + tid / segs);
+    for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step) {
+        const uint32_t r = r0 + tid / segs;
+        const bool in = mine && r < rows;
         uint32_t g[8], u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = ng[i], u[i] = nu[i];
@@ -167,17 +187,19 @@ __global__ void __launch_bounds__(256, kFwdThreadsPerSm / 256)
         uint32_t c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = sh.cast4(h[2 * i], h[2 * i + 1]);
-        store_bytes16(a.h + r * a.ld_h + c0, c, left);
-        const int64_t grp = seg >> 3;
-        if ((seg & 7) == 0) a.hs[r * a.ld_hs + grp] = static_cast<uint8_t>(sh.byte);
+        store_bytes16(a.h + row_at(r, a.ld_h) + c0, c, left);
+        const int grp = seg >> 3;
+        if ((seg & 7) == 0) a.hs[row_at(r, a.ld_hs) + grp] = static_cast<uint8_t>(sh.byte);
         if constexpr (CKPT) {
+            const int64_t at = row_at(r, a.ld_q) + c0;
             const uint32_t bg = cast_bf16x16<FC>(g, mgu & 0xFFFFu, c);
-            store_bytes16(a.gq + r * a.ld_q + c0, c, left);
+            store_bytes16(a.gq + at, c, left);
             const uint32_t bu = cast_bf16x16<FC>(u, mgu >> 16, c);
-            store_bytes16(a.uq + r * a.ld_q + c0, c, left);
+            store_bytes16(a.uq + at, c, left);
             if ((seg & 7) == 0) {
-                a.gs[r * a.ld_s + grp] = static_cast<uint8_t>(bg);
-                a.us[r * a.ld_s + grp] = static_cast<uint8_t>(bu);
+                const int64_t to = row_at(r, a.ld_s) + grp;
+                a.gs[to] = static_cast<uint8_t>(bg);
+                a.us[to] = static_cast<uint8_t>(bu);
             }
         }
     }
@@ -194,34 +216,38 @@ __device__ __forceinline__ void swiglu_grads(F2 g, F2 u, F2 dh, F2 &dg, F2 &du, 
 
 template <int FC, bool WIDE>
 __global__ void __launch_bounds__(256)
-    k_swiglu_bwd(const uint16_t *__restrict__ dh, int64_t ld_dh, const SwigluCkpt c,
-                 uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int64_t ld_d, int segs) {
+    k_swiglu_bwd(const uint16_t *__restrict__ dh, uint32_t ld_dh, const SwigluCkpt c,
+                 uint16_t *__restrict__ dg, uint16_t *__restrict__ du, uint32_t ld_d, int segs) {
     // a warp takes 32 neighbouring segments of one row, whole warps past the
     // row's end included: the stores exchange values between lanes
     const int seg = (blockIdx.y * blockDim.x + threadIdx.x);
-    const int64_t c0 = static_cast<int64_t>(seg) * 16, left = c.cols - c0;
-    for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
+    const int c0 = seg * 16, left = c.cols - c0;
+    for (uint32_t r = blockIdx.x; r < static_cast<uint32_t>(c.rows); r += gridDim.x) {
         uint32_t og[8] = {0, 0, 0, 0, 0, 0, 0, 0}, ou[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (seg < segs) {
             uint32_t w[8], gc[4], uc[4];
-            ragged::load16<WIDE>(dh + r * ld_dh + c0, left, w);
-            load_bytes16(c.gq + r * c.ld_q + c0, left, gc);
-            load_bytes16(c.uq + r * c.ld_q + c0, left, uc);
-            const F2 sg = f2(scale_pow2(__ldg(c.gs + r * c.ld_s + (seg >> 3))));
-            const F2 su = f2(scale_pow2(__ldg(c.us + r * c.ld_s + (seg >> 3))));
+            const int64_t at = row_at(r, c.ld_q) + c0, sat = row_at(r, c.ld_s) + (seg >> 3);
+            ragged::load16<WIDE>(dh + row_at(r, ld_dh) + c0, left, w);
+            load_bytes16(c.gq + at, left, gc);
+            load_bytes16(c.uq + at, left, uc);
+            const F2 sg = f2(scale_pow2(__ldg(c.gs + sat)));
+            const F2 su = f2(scale_pow2(__ldg(c.us + sat)));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int sh = 16 * (i & 1);
-                const F2 g = fp8x2_values<FC>(static_cast<uint16_t>(gc[i >> 1] >> sh), sg);
-                const F2 u = fp8x2_values<FC>(static_cast<uint16_t>(uc[i >> 1] >> sh), su);
-                F2 a, b, h;
-                swiglu_grads(g, u, f2_bf16(w[i]), a, b, h);
-                og[i] = ptx::cvt_bf16x2(a.lo(), a.hi());
-                ou[i] = ptx::cvt_bf16x2(b.lo(), b.hi());
+            for (int k = 0; k < 4; ++k) {
+                F2 g[2], u[2];
+                fp8x4_values<FC>(gc[k], sg, g);
+                fp8x4_values<FC>(uc[k], su, u);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    F2 a, b, h;
+                    swiglu_grads(g[j], u[j], f2_bf16(w[2 * k + j]), a, b, h);
+                    og[2 * k + j] = ptx::cvt_bf16x2(a.lo(), a.hi());
+                    ou[2 * k + j] = ptx::cvt_bf16x2(b.lo(), b.hi());
+                }
             }
         }
-        ragged::store16<WIDE>(dg + r * ld_d + c0, left, og);
-        ragged::store16<WIDE>(du + r * ld_d + c0, left, ou);
+        ragged::store16<WIDE>(dg + row_at(r, ld_d) + c0, left, og);
+        ragged::store16<WIDE>(du + row_at(r, ld_d) + c0, left, ou);
     }
 }
 
@@ -230,25 +256,56 @@ __global__ void __launch_bounds__(256)
 // columns at a time: one group in each direction per row and column.
 //   rows     a thread takes 16 columns of a row (eight lanes a row), computes
 //            dg, du and h, quantizes dg and du along the row at once and leaves
-//            all three in shared memory in FP32 (they have to be rounded once,
-//            from FP32, in each direction);
-//   columns  a thread takes 16 tokens of one column of each of the three
-//            (eight lanes a column: 128 bytes of codes, a whole line).
-// The next tile's inputs are loaded into registers before the column pass, so
-// the loads run under it.
-//
-// Shared memory: value (r, c) at r * 128 + (r / 16) * 4 words plus c with its
-// 16-byte piece index i replaced by i ^ ((i / 8) & 3): the eight lanes of a row
-// write pieces in eight different bank groups, and the 4 columns x 8 row
-// sixteenths that a warp reads at a time fall into 32 banks.
+//            all three in shared memory, a plane each, in FP32 (they are
+//            rounded once, from FP32, in each direction);
+//   columns  a warp takes four columns of each plane, a lane four tokens: one
+//            128-bit load per token, a column's maximum in one warp reduction,
+//            its 128 code bytes in one store.
+// Planes are handed over one by one: a warp waits only for the plane that it is
+// about to write or read (six mbarriers, every warp arrives once a tile), h
+// first, which the row part has ready before the row maxima of dg and du.  So
+// warps drift apart by most of a part and the arithmetic of one overlaps the
+// shared-memory work of the other; with a barrier of the CTA between the parts
+// 8192 x 8960 takes 162 us instead of 139.  The next tile is prefetched to L2
+// while this one's rows are computed and loaded to registers under the columns
+// (without the prefetch 150 us; HBM alone would take 98).
 constexpr int kT = 128, Q_THREADS = 1024;
-constexpr int kPlane = kT * kT + 8 * 4;          // words of one of the three
+constexpr int kPlane = kT * kT;                  // words of one of the three
 constexpr int kQSmem = 3 * kPlane * 4;
 
 template <int F>
 __device__ __forceinline__ void emit_codes(const F2 *v, int n4, const GroupF32<F> &gs, uint32_t *c) {
 #pragma unroll
     for (int i = 0; i < n4; ++i) c[i] = gs.cast4(v[2 * i], v[2 * i + 1]);
+}
+
+// Where a row's piece p (columns 4 p .. + 3) stands in shared memory.  Both
+// the writing lanes (pieces 4 seg + k of a row) and the reading ones (piece p
+// of every fourth row) fall on eight different 16-byte banks.
+__device__ __forceinline__ int plane_piece(int p, int row) { return p ^ ((p >> 3) & 3) ^ ((row >> 2) & 7); }
+
+// Four columns' groups of 128 tokens, four tokens per lane: scales (the column
+// lane & 3 in each lane), codes and the first four lanes' scale bytes.
+template <int FMT>
+__device__ __forceinline__ void emit_columns(const F2 (&v)[4][2], int lane, uint8_t *q, uint32_t ld, uint8_t *s) {
+    float m[4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        m[2 * c] = warp_max_abs(max3_abs(max3_abs(v[0][c].lo(), v[1][c].lo(), v[2][c].lo()), v[3][c].lo(), 0.0f));
+        m[2 * c + 1] = warp_max_abs(max3_abs(max3_abs(v[0][c].hi(), v[1][c].hi(), v[2][c].hi()), v[3][c].hi(), 0.0f));
+    }
+    const GroupF32<FMT> gs(lane & 2 ? (lane & 1 ? m[3] : m[2]) : (lane & 1 ? m[1] : m[0]));
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const F2 mul = f2(__shfl_sync(0xFFFFFFFFu, gs.mul, 2 * c), __shfl_sync(0xFFFFFFFFu, gs.mul, 2 * c + 1));
+        F2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = mul2(v[i][c], mul);
+        *reinterpret_cast<uint32_t *>(q) = cvt4<FMT>(x[0].lo(), x[1].lo(), x[2].lo(), x[3].lo());
+        *reinterpret_cast<uint32_t *>(q + ld) = cvt4<FMT>(x[0].hi(), x[1].hi(), x[2].hi(), x[3].hi());
+        q += 2 * static_cast<int64_t>(ld);
+    }
+    if (lane < 4) *s = static_cast<uint8_t>(gs.byte);
 }
 
 // A thread's inputs of a tile: 16 columns of a row.
@@ -258,100 +315,140 @@ struct TileIn {
 };
 
 template <bool WIDE>
-__device__ __forceinline__ void load_tile(TileIn &t, const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c,
-                                          int64_t r, int64_t kb, int seg) {
-    const int64_t col = kb * kT + seg * 16;
+__device__ __forceinline__ void load_tile(TileIn &t, const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c,
+                                          uint32_t r, uint32_t kb, int seg) {
+    const uint32_t col = kb * kT + seg * 16;
+    const uint16_t *src = dh + row_at(r, ld_dh) + col;
     if (WIDE) {
-        ragged::load16<true>(dh + r * ld_dh + col, 16, t.dh);
+        ragged::load16<true>(src, 16, t.dh);
     } else {
-        const uint4 *p = reinterpret_cast<const uint4 *>(dh + r * ld_dh + col);
+        const uint4 *p = reinterpret_cast<const uint4 *>(src);
         const uint4 a = __ldg(p), b = __ldg(p + 1);
         t.dh[0] = a.x, t.dh[1] = a.y, t.dh[2] = a.z, t.dh[3] = a.w;
         t.dh[4] = b.x, t.dh[5] = b.y, t.dh[6] = b.z, t.dh[7] = b.w;
     }
-    load_bytes16(c.gq + r * c.ld_q + col, 16, t.g);
-    load_bytes16(c.uq + r * c.ld_q + col, 16, t.u);
-    t.sg = __ldg(c.gs + r * c.ld_s + kb);
-    t.su = __ldg(c.us + r * c.ld_s + kb);
+    const int64_t at = row_at(r, c.ld_q) + col, sat = row_at(r, c.ld_s) + kb;
+    load_bytes16(c.gq + at, 16, t.g);
+    load_bytes16(c.uq + at, 16, t.u);
+    t.sg = __ldg(c.gs + sat);
+    t.su = __ldg(c.us + sat);
 }
+
+// Attempts of one wait (each suspends the warp for a while): seconds.
+constexpr uint32_t kTries = 1u << 22;
 
 template <int FC, int FR, int FT, int FH, bool WIDE>
 __global__ void __launch_bounds__(Q_THREADS, 1)
-    k_swiglu_bwd_q(const uint16_t *__restrict__ dh, int64_t ld_dh, const SwigluCkpt c, const SwigluGrads o,
-                   int kbs, int tiles) {
+    k_swiglu_bwd_q(const uint16_t *__restrict__ dh, uint32_t ld_dh, const SwigluCkpt c, const SwigluGrads o,
+                   uint32_t kbs, uint32_t rbs, uint32_t step_k, uint32_t step_r, unsigned int *err) {
     extern __shared__ __align__(16) float plane[];
-    const int tid = threadIdx.x, seg = tid & 7, row = tid >> 3;
+    __shared__ __align__(8) uint64_t bars[6];
+    const uint32_t bar = ptx::smem_u32(bars);
+    uint32_t phase = 0;
+    auto full = [&](int p) { return bar + 8 * p; };
+    auto empty = [&](int p) { return bar + 24 + 8 * p; };
+    const int tid = threadIdx.x, seg = tid & 7, row = tid >> 3, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) ptx::mbar_init(bar + 8 * i, Q_THREADS / 32);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    // every warp waits for and arrives at every barrier, once a tile
+    auto wait = [&](uint32_t which, uint32_t parity) {
+        if (ptx::mbar_try_wait(which, parity)) return true;
+#pragma unroll 1
+        for (uint32_t i = 0; i < kTries; ++i)
+            if (ptx::mbar_try_wait(which, parity)) return true;
+        atomicOr(err, 1u);
+        return false;
+    };
+    auto arrive = [&](uint32_t which) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(which);
+    };
     TileIn in;
-    int tile = blockIdx.x;
-    if (tile < tiles) load_tile<WIDE>(in, dh, ld_dh, c, static_cast<int64_t>(tile / kbs) * kT + row, tile % kbs, seg);
-    for (; tile < tiles; tile += gridDim.x) {
-        const int64_t kb = tile % kbs, rb = tile / kbs, r0 = rb * kT;
+    // tiles blockIdx.x, + gridDim.x (step_r rows of kbs and step_k), ...
+    uint32_t rb = blockIdx.x / kbs, kb = blockIdx.x % kbs;
+    if (rb < rbs) load_tile<WIDE>(in, dh, ld_dh, c, rb * kT + row, kb, seg);
+    while (rb < rbs) {
+        const uint32_t r0 = rb * kT;
+        uint32_t next_r = rb + step_r, next_k = kb + step_k;
+        if (next_k >= kbs) next_k -= kbs, ++next_r;
+        if (warp < 24 && next_r < rbs) {
+            // the next tile to L2, a line of 128 bytes per thread
+            const uint32_t r = next_r * kT + (tid & 127), k0 = next_k * kT;
+            const void *p = warp < 8    ? static_cast<const void *>(dh + row_at(r, ld_dh) + k0 + (tid >> 7) * 64)
+                            : warp < 16 ? static_cast<const void *>((warp < 12 ? c.gq : c.uq) + row_at(r, c.ld_q) + k0)
+                                        : static_cast<const void *>((warp < 20 ? c.gs : c.us) + row_at(r, c.ld_s) + next_k);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+        }
         {
             const F2 sg = f2(scale_pow2(in.sg)), su = f2(scale_pow2(in.su));
             F2 a[8], b[8];
             float ma = 0.0f, mb = 0.0f;
-            float *dst = plane + row * kT + (row >> 4) * 4;
+            const uint32_t off = (row * kT + plane_piece(4 * seg, row) * 4) * 4;   // piece 4 seg + k: off ^ 16 k
+            auto put = [&](int p, int k, F2 x, F2 y) {
+                *reinterpret_cast<ulonglong2 *>(reinterpret_cast<char *>(plane) + (off ^ (k << 4)) + p * kPlane * 4) =
+                    make_ulonglong2(x.v, y.v);
+            };
+            if (!wait(empty(2), phase ^ 1u)) return;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                F2 h[2];
+                F2 g[2], u[2], h[2];
+                fp8x4_values<FC>(in.g[k], sg, g);
+                fp8x4_values<FC>(in.u[k], su, u);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const F2 g = fp8x2_values<FC>(static_cast<uint16_t>(in.g[k] >> (16 * j)), sg);
-                    const F2 u = fp8x2_values<FC>(static_cast<uint16_t>(in.u[k] >> (16 * j)), su);
-                    swiglu_grads(g, u, f2_bf16(in.dh[2 * k + j]), a[2 * k + j], b[2 * k + j], h[j]);
+                    swiglu_grads(g[j], u[j], f2_bf16(in.dh[2 * k + j]), a[2 * k + j], b[2 * k + j], h[j]);
                     ma = max_abs(ma, a[2 * k + j]);
                     mb = max_abs(mb, b[2 * k + j]);
                 }
-                const int piece = ((4 * seg + k) ^ ((seg >> 1) & 3)) * 4;
-                *reinterpret_cast<ulonglong2 *>(dst + piece) = make_ulonglong2(a[2 * k].v, a[2 * k + 1].v);
-                *reinterpret_cast<ulonglong2 *>(dst + kPlane + piece) = make_ulonglong2(b[2 * k].v, b[2 * k + 1].v);
-                *reinterpret_cast<ulonglong2 *>(dst + 2 * kPlane + piece) = make_ulonglong2(h[0].v, h[1].v);
+                put(2, k, h[0], h[1]);
             }
+            arrive(full(2));
             const GroupF32<FR> ga(group_max(ma)), gb(group_max(mb));
-            const int64_t r = r0 + row, at = r * o.ld_q + kb * kT + seg * 16;
+            const int64_t at = row_at(r0 + row, o.ld_q) + kb * kT + seg * 16;
             uint32_t q[4];
+            if (!wait(empty(0), phase ^ 1u)) return;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) put(0, k, a[2 * k], a[2 * k + 1]);
+            arrive(full(0));
             emit_codes<FR>(a, 4, ga, q);
             *reinterpret_cast<uint4 *>(o.q[0] + at) = make_uint4(q[0], q[1], q[2], q[3]);
+            if (!wait(empty(1), phase ^ 1u)) return;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) put(1, k, b[2 * k], b[2 * k + 1]);
+            arrive(full(1));
             emit_codes<FR>(b, 4, gb, q);
             *reinterpret_cast<uint4 *>(o.q[1] + at) = make_uint4(q[0], q[1], q[2], q[3]);
             if (seg == 0) {
-                o.s[0][r * o.ld_s + kb] = static_cast<uint8_t>(ga.byte);
-                o.s[1][r * o.ld_s + kb] = static_cast<uint8_t>(gb.byte);
+                const int64_t to = row_at(r0 + row, o.ld_s) + kb;
+                o.s[0][to] = static_cast<uint8_t>(ga.byte);
+                o.s[1][to] = static_cast<uint8_t>(gb.byte);
             }
         }
-        __syncthreads();
-        const int next = tile + gridDim.x;
-        if (next < tiles)
-            load_tile<WIDE>(in, dh, ld_dh, c, static_cast<int64_t>(next / kbs) * kT + row, next % kbs, seg);
-        // column cc, tokens 16 part .. + 15
-        const int part = tid & 7, cc = tid >> 3;
-        const int word = (((cc >> 2) ^ ((cc >> 5) & 3)) << 2) + (cc & 3);
-        const float *src = plane + part * (16 * kT + 4) + word;
+        if (next_r < rbs) load_tile<WIDE>(in, dh, ld_dh, c, next_r * kT + row, next_k, seg);
+        // columns 4 warp .. + 3, tokens 4 lane .. + 3
+        const float *src = plane + lane * 4 * kT + plane_piece(warp, lane * 4) * 4;
+        const uint32_t col = kb * kT + warp * 4;
+        const int64_t to = row_at(col, o.ld_qt) + r0 + lane * 4, sto = row_at(col + (lane & 3), o.ld_st) + rb;
 #pragma unroll
-        for (int w = 0; w < 3; ++w) {
-            F2 v[8];
-            float m = 0.0f;
+        for (int i3 = 0; i3 < 3; ++i3) {
+            const int w = (i3 + 2) % 3;   // h first
+            if (!wait(full(w), phase)) return;
+            F2 v[4][2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = f2(src[w * kPlane + 2 * i * kT], src[w * kPlane + (2 * i + 1) * kT]);
-                m = max_abs(m, v[i]);
+            for (int i = 0; i < 4; ++i) {
+                const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(src + w * kPlane + i * kT);
+                v[i][0].v = p.x, v[i][1].v = p.y;
             }
-            m = group_max(m);
-            uint32_t q[4], byte;
-            if (w < 2) {
-                const GroupF32<FT> gs(m);
-                emit_codes<FT>(v, 4, gs, q);
-                byte = gs.byte;
-            } else {
-                const GroupF32<FH> gs(m);
-                emit_codes<FH>(v, 4, gs, q);
-                byte = gs.byte;
-            }
-            const int64_t col = kb * kT + cc;
-            *reinterpret_cast<uint4 *>(o.qt[w] + col * o.ld_qt + r0 + part * 16) = make_uint4(q[0], q[1], q[2], q[3]);
-            if (part == 0) o.st[w][col * o.ld_st + rb] = static_cast<uint8_t>(byte);
+            arrive(empty(w));
+            if (w < 2) emit_columns<FT>(v, lane, o.qt[w] + to, o.ld_qt, o.st[w] + sto);
+            else emit_columns<FH>(v, lane, o.qt[w] + to, o.ld_qt, o.st[w] + sto);
         }
-        __syncthreads();
+        phase ^= 1u;
+        rb = next_r, kb = next_k;
     }
 }
 
@@ -372,10 +469,10 @@ template <int FH, int FC, bool CKPT>
 cudaError_t fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
     // segments of 16 columns, whole groups of eight; a chunk of at most 256
     // segments per block, spread evenly
-    const int64_t total = (a.cols + 127) / 128 * 8, chunks = (total + 255) / 256;
+    const int64_t total = (a.cols + 127LL) / 128 * 8, chunks = (total + 255) / 256;
     const int segs = static_cast<int>((total / 8 + chunks - 1) / chunks * 8);
     const int rpb = 256 / segs, threads = (segs * rpb + 31) / 32 * 32;
-    const int64_t rb = (a.rows + rpb - 1) / rpb, cb = (total + segs - 1) / segs;
+    const int64_t rb = (static_cast<int64_t>(a.rows) + rpb - 1) / rpb, cb = (total + segs - 1) / segs;
     // as many CTAs as fit at once
     const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kFwdThreadsPerSm / threads) / cb);
     const dim3 grid(static_cast<unsigned>(std::min(rb, resident)), static_cast<unsigned>(cb));
@@ -398,10 +495,10 @@ cudaError_t launch_swiglu_fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
     return a.fmt_h == FMT_E4M3 ? fwd_h<FMT_E4M3>(a, stream) : fwd_h<FMT_E5M2>(a, stream);
 }
 
-cudaError_t launch_swiglu_bwd(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, uint16_t *dg,
-                              uint16_t *du, int64_t ld_d, cudaStream_t stream) {
+cudaError_t launch_swiglu_bwd(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c, uint16_t *dg,
+                              uint16_t *du, uint32_t ld_d, cudaStream_t stream) {
     // a row's segments in equal blocks of whole warps
-    const int64_t segs = (c.cols + 15) / 16, chunks = (segs + 255) / 256;
+    const int64_t segs = (c.cols + 15LL) / 16, chunks = (segs + 255) / 256;
     const int threads = static_cast<int>(((segs + chunks - 1) / chunks + 31) / 32 * 32);
     const dim3 grid(static_cast<unsigned>(c.rows), static_cast<unsigned>((segs + threads - 1) / threads));
     const bool wide = ragged::wide(dh, ld_dh) && ragged::wide(dg, ld_d) && ragged::wide(du, ld_d);
@@ -416,10 +513,9 @@ cudaError_t launch_swiglu_bwd(const uint16_t *dh, int64_t ld_dh, const SwigluCkp
 namespace {
 
 template <int FC, int FR, int FT, int FH>
-cudaError_t bwd_q(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
+cudaError_t bwd_q(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
                   cudaStream_t stream) {
     const int64_t kbs = c.cols / kT, tiles = kbs * (c.rows / kT);
-    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -428,20 +524,23 @@ cudaError_t bwd_q(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, const 
     auto go = [&](auto kern) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmem);
         if (e != cudaSuccess) return e;
-        kern<<<grid, Q_THREADS, kQSmem, stream>>>(dh, ld_dh, c, g, static_cast<int>(kbs), static_cast<int>(tiles));
+        kern<<<grid, Q_THREADS, kQSmem, stream>>>(dh, ld_dh, c, g, static_cast<uint32_t>(kbs),
+                                                   static_cast<uint32_t>(c.rows / kT),
+                                                   grid % static_cast<uint32_t>(kbs),
+                                                   grid / static_cast<uint32_t>(kbs), g.err);
         return cudaGetLastError();
     };
     return ragged::wide(dh, ld_dh) ? go(k_swiglu_bwd_q<FC, FR, FT, FH, true>)
                                    : go(k_swiglu_bwd_q<FC, FR, FT, FH, false>);
 }
 template <int FC, int FR, int FT>
-cudaError_t bwd_q_h(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
+cudaError_t bwd_q_h(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
                     cudaStream_t stream) {
     return g.fmt_h == FMT_E4M3 ? bwd_q<FC, FR, FT, FMT_E4M3>(dh, ld_dh, c, g, stream)
                                : bwd_q<FC, FR, FT, FMT_E5M2>(dh, ld_dh, c, g, stream);
 }
 template <int FC, int FR>
-cudaError_t bwd_q_t(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
+cudaError_t bwd_q_t(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
                     cudaStream_t stream) {
     return g.fmt_t == FMT_E4M3 ? bwd_q_h<FC, FR, FMT_E4M3>(dh, ld_dh, c, g, stream)
                                : bwd_q_h<FC, FR, FMT_E5M2>(dh, ld_dh, c, g, stream);
@@ -449,7 +548,7 @@ cudaError_t bwd_q_t(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, cons
 
 }  // namespace
 
-cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, int64_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
+cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
                                 cudaStream_t stream) {
     if (c.fmt == FMT_E4M3)
         return g.fmt == FMT_E4M3 ? bwd_q_t<FMT_E4M3, FMT_E4M3>(dh, ld_dh, c, g, stream)

@@ -5,7 +5,8 @@
  * uint16_t bit patterns with row strides in elements, codes and scale bytes
  * with row strides in bytes, a caller-owned stream, no allocation and no
  * synchronization, fp8hg_status return values, argument errors before any
- * launch.
+ * launch.  Rows and columns are at most 2^30, row strides below 2^31
+ * (FP8HG_ERR_SHAPE beyond).
  *
  * 4-bit values are E2M1 (sign, two exponent bits, one mantissa bit):
  * 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives, rounded to nearest even and

@@ -190,3 +190,27 @@ def test_swiglu_bwd_q_refusals(lib):
     assert call(ld_q=136) == ALIGN and call(ld_qt=136) == ALIGN and call(ld_q=112) == INVALID
     assert call(ld_s=0) == INVALID and call(ld_st=0) == INVALID and call(fmt_h=2) == INVALID
     assert call(reserved=1) == INVALID and call(c=ck(rows=0)) == OK
+
+
+def test_strides_of_31_bits(lib):
+    """Row strides past 2^31 - 1 are refused, not cut."""
+    big = 2 ** 31          # a multiple of 16
+    n = lib.fp4_tensor_scale_workspace()
+    assert lib.fp4_tensor_scale(FAKE, 4, 4, big, FAKE, FAKE, n, None) == SHAPE
+    quant = lambda ld=64, ldq=32, ldqt=16: lib.fp4_quant(FAKE, 4, 64, ld, MX, None, FAKE, ldq, FAKE, FAKE, ldqt, FAKE, None)
+    assert quant(ld=big) == SHAPE and quant(ldq=big) == SHAPE and quant(ldqt=big) == SHAPE
+    dequant = lambda o, ld=64: lib.fp4_dequant(ctypes.byref(o), FAKE, ld, 0, None)
+    assert dequant(op(), big) == SHAPE and dequant(op(ld=big)) == SHAPE
+    fwd = lambda **k: lib.fp8_swiglu_ckpt(FAKE, FAKE, 4, 128, k.get("ld", 128), E4M3, FAKE, k.get("ldh", 128), FAKE,
+                                          k.get("lhs", 1), E4M3, FAKE, FAKE, FAKE, FAKE, k.get("ldq", 128),
+                                          k.get("lds", 1), None)
+    assert all(fwd(**{k: big}) == SHAPE for k in ("ld", "ldh", "lhs", "ldq", "lds"))
+    bwd = lambda ld=128, c=None, ldd=128: lib.fp8_swiglu_ckpt_bwd(FAKE, ld, ctypes.byref(c or ck()), FAKE, FAKE, ldd, None)
+    assert bwd(ld=big) == SHAPE and bwd(ldd=big) == SHAPE
+    assert bwd(c=ck(ldq=big)) == SHAPE and bwd(c=ck(lds=big)) == SHAPE
+    names = [n for n, _ in lowbit._Grads._fields_]
+    base = dict({n: FAKE for n in names[:10]}, ld_q=128, ld_s=1, ld_qt=128, ld_st=1, fmt=E5M2,
+                fmt_t=E5M2, fmt_h=E4M3, reserved=0)
+    for name in ("ld_q", "ld_s", "ld_qt", "ld_st"):
+        g = lowbit._Grads(**{**base, name: big})
+        assert lib.fp8_swiglu_ckpt_bwd_q(FAKE, 128, ctypes.byref(ck()), ctypes.byref(g), None) == SHAPE, name
