@@ -14,10 +14,13 @@ checked and marshalled and the CUDA kernels do all of the computation.
   fp8_swiglu_ckpt_bwd(dh, ckpt)                     -> [rows, 2 cols] BF16, dgate next to dup
   fp8_swiglu_ckpt_bwd_q(dh, ckpt)                   -> the same as FP8 operands in both
                                                        directions, and h transposed
+
+Every one takes stream=, a torch stream or a raw handle, as well.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 from dataclasses import dataclass
 from typing import Optional
@@ -59,10 +62,26 @@ _bound = None
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on(stream, x):
-    """The stream to launch on: x's device's current one if none is given (the
-    plain lookup: a call takes about as long as ten microseconds' work)."""
-    return _raw_stream(x.get_device()) if stream is None else _stream(stream)
+def _on(x):
+    """The stream to launch on, x's device's current one (the plain lookup: a
+    call takes about as long as ten microseconds' work)."""
+    return _raw_stream(x.get_device())
+
+
+def _streamed(fn):
+    """Adds the keyword `stream` (a torch stream or a raw handle; None: the
+    current one): the call runs with it as the current stream, so that what it
+    allocates belongs to that stream and no other stream's pending work on
+    reused memory can reach it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _check(rc: int, what: str):
@@ -171,7 +190,8 @@ def alloc_fp4(rows: int, k: int, kind: int, tensor_scale=None, device="cuda") ->
     return Fp4Tensor(codes, scale, rows, k, kind, tensor_scale)
 
 
-def fp4_tensor_scale(x, out=None, stream=None):
+@_streamed
+def fp4_tensor_scale(x, out=None):
     """The FP4_NV scale of a tensor: the smallest power of two t with
     amax <= 6 * 448 * t (1 for a tensor of zeros), on the device."""
     _check_matrix(x)
@@ -180,19 +200,19 @@ def fp4_tensor_scale(x, out=None, stream=None):
     n = f.fp4_tensor_scale_workspace()
     ws = torch.empty(n, dtype=torch.uint8, device=x.device)
     _check(f.fp4_tensor_scale(x.data_ptr(), x.shape[0], x.shape[1], _ld(x), _ts(out), ws.data_ptr(),
-                              n, _on(stream, x)), "fp4_tensor_scale")
+                              n, _on(x)), "fp4_tensor_scale")
     return out
 
 
 _NONE = (None, 0, None)
 
 
-def _quant(x, kind, tensor_scale, rows_out, cols_out, stream, what):
+def _quant(x, kind, tensor_scale, rows_out, cols_out, what):
     q = (rows_out.codes.data_ptr(), rows_out.ld(), rows_out.scale.data_ptr()) if rows_out else _NONE
     t = (cols_out.codes.data_ptr(), cols_out.ld(), cols_out.scale.data_ptr()) if cols_out else _NONE
     rows, cols = x.shape
     _check(_fns().fp4_quant(x.data_ptr(), rows, cols, _ld(x), kind, _ts(tensor_scale), *q, *t,
-                            _on(stream, x)), what)
+                            _on(x)), what)
 
 
 def _check_fp4(q, rows, k, kind):
@@ -200,8 +220,9 @@ def _check_fp4(q, rows, k, kind):
         raise ValueError(f"out must be a 4-bit tensor [{rows}, {k}] of kind {kind}")
 
 
+@_streamed
 def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
-              out: Optional[Fp4Tensor] = None, stream=None) -> Fp4Tensor:
+              out: Optional[Fp4Tensor] = None) -> Fp4Tensor:
     """BF16 [rows, cols] to 4 bits along the rows, or (transpose=True) along the
     columns, written as [cols, rows]."""
     _check_matrix(x)
@@ -210,13 +231,14 @@ def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
         out = alloc_fp4(rows, cols, kind, tensor_scale, x.device)
     _check_fp4(out, rows, cols, kind)
     out.tensor_scale = tensor_scale
-    _quant(x, kind, tensor_scale, None if transpose else out, out if transpose else None, stream,
+    _quant(x, kind, tensor_scale, None if transpose else out, out if transpose else None,
            "fp4_quant")
     return out
 
 
+@_streamed
 def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Tensor] = None,
-                   out_t: Optional[Fp4Tensor] = None, stream=None):
+                   out_t: Optional[Fp4Tensor] = None):
     """fp4_quant along the rows and along the columns from one read of x."""
     _check_matrix(x)
     rows, cols = x.shape
@@ -225,11 +247,12 @@ def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Te
     _check_fp4(out, rows, cols, kind)
     _check_fp4(out_t, cols, rows, kind)
     out.tensor_scale = out_t.tensor_scale = tensor_scale
-    _quant(x, kind, tensor_scale, out, out_t, stream, "fp4_quant_dual")
+    _quant(x, kind, tensor_scale, out, out_t, "fp4_quant_dual")
     return out, out_t
 
 
-def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None, stream=None):
+@_streamed
+def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None):
     """The values of a 4-bit tensor, [rows, k], BF16 or FP32."""
     if out is None:
         out = torch.empty((q.rows, q.k), dtype=out_dtype or torch.bfloat16, device=q.codes.device)
@@ -237,12 +260,13 @@ def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None, stream=None):
         _check_out(out, q.rows, q.k)
     op = q.operand()
     _check(_fns().fp4_dequant(ctypes.byref(op), out.data_ptr(), _ld(out), _out_kind(out),
-                              _on(stream, out)), "fp4_dequant")
+                              _on(out)), "fp4_dequant")
     return out
 
 
+@_streamed
 def fp4_gemm_scaled(a: Fp4Tensor, b: Fp4Tensor, out=None, out_dtype=None, accumulate: bool = False,
-                    wait_limit_ns: int = 0, inject_fault: int = 0, stream=None):
+                    wait_limit_ns: int = 0, inject_fault: int = 0):
     """C = A B^T (or C += A B^T) on two 4-bit tensors of the same kind."""
     if out is None:
         if accumulate:
@@ -254,13 +278,14 @@ def fp4_gemm_scaled(a: Fp4Tensor, b: Fp4Tensor, out=None, out_dtype=None, accumu
     oa, ob = a.operand(), b.operand()
     _check(_fns().fp4_gemm_scaled(ctypes.byref(oa), ctypes.byref(ob), out.data_ptr(), _ld(out),
                                   _out_kind(out), 1 if accumulate else 0,
-                                  _opts(wait_limit_ns, inject_fault), _on(stream, out)),
+                                  _opts(wait_limit_ns, inject_fault), _on(out)),
            "fp4_gemm_scaled")
     return out
 
 
+@_streamed
 def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, workspace=None,
-               wait_limit_ns: int = 0, inject_fault: int = 0, stream=None):
+               wait_limit_ns: int = 0, inject_fault: int = 0):
     """y = x w^T: x [rows, k] BF16 is quantized like w and multiplied, in one
     call.  workspace: optional uint8 tensor of fp4_linear_workspace(...)
     bytes (allocated per call if None; up to 4 rows none is needed)."""
@@ -272,7 +297,7 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
         out = torch.empty((rows, w.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
     else:
         _check_out(out, rows, w.rows)
-    stream = _on(stream, x)
+    stream = _on(x)
     n = 0 if rows <= 4 else _linear_bytes(rows, w.k, w.kind)
     if n and workspace is None:
         workspace = _scratch(n, x, stream)
@@ -343,8 +368,8 @@ def _ld_codes(q) -> int:
     return q.stride(0) if q.shape[0] > 1 else max(q.stride(0), (q.shape[1] + 15) // 16 * 16)
 
 
-def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bool = True,
-                    stream=None):
+@_streamed
+def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bool = True):
     """h = silu(gate) * up, quantized per 1x128 group (the down projection's A
     operand), and gate and up quantized the same way for the backward pass.
     gate and up may be the two halves of one tensor.  checkpoint=False
@@ -364,7 +389,7 @@ def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bo
         ptr = (g.data_ptr(), sg.data_ptr(), u.data_ptr(), su.data_ptr())
     _check(_fns().fp8_swiglu_ckpt(gate.data_ptr(), up.data_ptr(), rows, cols, _ld(gate), fmt_h,
                                   h.data_ptr(), ld, sh.data_ptr(), ls, fmt, *ptr, ld, ls,
-                                  _on(stream, gate)), "fp8_swiglu_ckpt")
+                                  _on(gate)), "fp8_swiglu_ckpt")
     h = QTensor(h, sh, fmt_h, GRAN_1x128, n)
     if not checkpoint:
         return h, None
@@ -386,7 +411,8 @@ def _ckpt(c: SwigluCkpt, dh) -> _Ckpt:
                  rows, cols, _ld_codes(g.codes), g.scale.stride(0), g.fmt, 0)
 
 
-def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None, stream=None):
+@_streamed
+def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None):
     """Gradients of gate and up from dh [rows, cols] and the checkpoint, BF16:
     one [rows, 2 cols] tensor, dgate in the first half, dup in the second."""
     c = _ckpt(ckpt, dh)
@@ -397,13 +423,14 @@ def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None, stream=None):
         _check_out(out, rows, 2 * cols)
         _check_matrix(out, "out")
     _check(_fns().fp8_swiglu_ckpt_bwd(dh.data_ptr(), _ld(dh), ctypes.byref(c), out.data_ptr(),
-                                      out.data_ptr() + 2 * cols, _ld(out), _on(stream, dh)),
+                                      out.data_ptr() + 2 * cols, _ld(out), _on(dh)),
            "fp8_swiglu_ckpt_bwd")
     return out
 
 
+@_streamed
 def fp8_swiglu_ckpt_bwd_q(dh, ckpt: SwigluCkpt, fmt: int = E5M2, fmt_t: int = E5M2,
-                          fmt_h: int = E4M3, stream=None):
+                          fmt_h: int = E4M3):
     """The gradients as FP8 operands: ([rows, 2 cols] per 1x128 group, dgate next
     to dup; the same transposed, [2 cols, rows], per 128 tokens; h rebuilt from
     the checkpoint and transposed, [cols, rows], per 128 tokens).  rows and cols
@@ -420,5 +447,5 @@ def fp8_swiglu_ckpt_bwd_q(dh, ckpt: SwigluCkpt, fmt: int = E5M2, fmt_t: int = E5
                h.codes.data_ptr(), h.scale.data_ptr(), d.codes.stride(0), d.scale.stride(0), ld_qt,
                ld_st, fmt, fmt_t, fmt_h, 0)
     _check(_fns().fp8_swiglu_ckpt_bwd_q(dh.data_ptr(), _ld(dh), ctypes.byref(c), ctypes.byref(g),
-                                        _on(stream, dh)), "fp8_swiglu_ckpt_bwd_q")
+                                        _on(dh)), "fp8_swiglu_ckpt_bwd_q")
     return d, t, h

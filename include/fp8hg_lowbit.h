@@ -198,7 +198,9 @@ int fp8_swiglu_ckpt_bwd(const uint16_t *dh, int64_t ld_dh, const fp8hg_swiglu_ck
  *                                         [cols, rows/128] (ld_st)
  *   fmt_h, h_qt, h_st                     the same layout and strides for h
  * Requirements: rows and cols multiples of 128, dh 16-byte aligned with ld_dh
- * % 8 == 0, codes 16-byte aligned with strides that are multiples of 16.
+ * % 8 == 0, codes 16-byte aligned with strides that are multiples of 16.  The
+ * kernel's warps hand data to one another over bounded waits; one that ran out
+ * would be FP8HG_ERR_TIMEOUT from fp8hg_get_device_error.
  */
 typedef struct {
     uint8_t *dgate_q, *dup_q, *dgate_s, *dup_s;

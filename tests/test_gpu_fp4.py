@@ -423,3 +423,20 @@ def test_linear_timeout(cuda_lib, m, kind):
     assert fp8hg.fp8hg_get_device_error() == 6
     assert fp8hg.fp8hg_get_device_error() == 0
     assert torch.equal(fp8hg.fp4_linear(x, w), want)
+
+
+def test_given_stream_owns_what_a_call_allocates(cuda_lib):
+    """stream=: results may not land in memory that the current stream still
+    has work pending on.  The current stream is held up, writes to a tensor and
+    gives its memory back; the call on the other stream then allocates as much."""
+    x = gpu(data(512, 2048, 71))
+    want = fp8hg.fp4_quant(x, MX)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(20_000_000)
+        pending = [torch.empty_like(want.codes).fill_(0xEE), torch.empty_like(want.scale).fill_(0xEE)]
+        del pending
+        got = fp8hg.fp4_quant(x, MX, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got.codes[:, :1024], want.codes[:, :1024]) and torch.equal(got.scale, want.scale)
