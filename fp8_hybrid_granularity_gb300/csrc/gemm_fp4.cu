@@ -54,7 +54,8 @@ constexpr int kStageBytes = 128;   // of one row: 256 elements
 
 struct Params {
     int M, N, nk;                  // P rows (MMA's M side), Q rows (N side), K stages
-    int num_mb, num_nb, num_tiles;
+    int num_mb, num_nb, num_tiles; // pair tiles: NH parts wide, num_nb columns of them
+    int half_tiles;                // and, past the last column, num_mb of one part or none
     const uint8_t *sa, *sb;
     int64_t scale_tiles;           // 512-byte tiles per 128 rows
     const float *ta, *tb;
@@ -234,6 +235,29 @@ __device__ bool wait_pair(uint32_t bar, uint32_t parity, uint64_t limit, volatil
     }
 }
 
+// The tiles of a pair, in order: the wide ones dealt round, then those of one
+// part, which first go to the pairs that the last deal left out, two each.
+struct PairTiles {
+    int pair, npairs, wide, rem;   // `wide` of them for this pair; left over from the even deals
+    __device__ __forceinline__ PairTiles(const Params &p, int pair_, int npairs_)
+        : pair(pair_), npairs(npairs_), wide((p.num_tiles - pair_ + npairs_ - 1) / npairs_),
+          rem(p.num_tiles % npairs_) {}
+    // The i-th tile's place and its column parts; 0 past the last.
+    template <int NH>
+    __device__ __forceinline__ int get(const Params &p, int i, int &mb, int &nb) const {
+        if (i < wide) {
+            tile_coords(pair + i * npairs, p.num_mb, p.num_nb, mb, nb);
+            return NH;
+        }
+        if (NH == 1) return 0;
+        const int j = i - wide, low = npairs - rem;
+        const int u = pair < rem ? 2 * low + pair + j * npairs
+                                 : j < 2 ? pair - rem + j * low : 2 * low + pair + (j - 2) * npairs;
+        mb = u, nb = p.num_nb;
+        return u < p.half_tiles ? 1 : 0;
+    }
+};
+
 template <bool NV, int NH>
 __global__ void __launch_bounds__(P_THREADS, 1)
     k_fp4_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -253,6 +277,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const uint32_t rank = ptx::cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
+    const PairTiles tiles(p, pair, npairs);
     const uint64_t limit = p.wait_limit_ns, drain_limit = 2000000ull;
     // the even CTA's barriers, as seen from either CTA
     const uint32_t full_l = ptx::map_shared_rank(bar, 0), odd_l = ptx::map_shared_rank(odd, 0);
@@ -294,11 +319,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         uint8_t *stage = gbase + L::OFF_EPI + (warp - 4) * EPI_BYTES;
         const float alpha = (p.ta ? __ldg(p.ta) : 1.0f) * (p.tb ? __ldg(p.tb) : 1.0f);
         const bool vec = (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % (p.out_fp32 ? 4 : 8) == 0;
-        uint32_t tcount = 0;
-        for (int tile = half < NH ? pair : p.num_tiles; tile < p.num_tiles; tile += npairs, ++tcount) {
-            int mb, nb;
-            tile_coords(tile, p.num_mb, p.num_nb, mb, nb);
-            bool ok = wait_phase(tfull + 8 * half, tcount & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
+        for (int i = 0, mb, nb; tiles.get<NH>(p, i, mb, nb) > half; ++i) {
+            bool ok = wait_phase(tfull + 8 * half, i & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -354,9 +376,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int tile = pair; tile < p.num_tiles && ok; tile += npairs) {
-                int mb, nb;
-                tile_coords(tile, p.num_mb, p.num_nb, mb, nb);
+            for (int i = 0, mb, nb, parts; ok && (parts = tiles.get<NH>(p, i, mb, nb)) != 0; ++i) {
                 const int arow = mb * PM + static_cast<int>(rank) * 128;
                 const int brow = nb * L::PN + static_cast<int>(rank) * (PH / 2);
                 const int sarow = mb * 2 + static_cast<int>(rank), sbrow = nb * L::PN / 128;
@@ -368,10 +388,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     // CTA never issues its first stage
                     if (!(p.inject == 1 && blockIdx.x == 0 && it == 0)) {
                         const uint32_t st = base + s * L::STAGE, sf = base + L::OFF_SF + s * L::SF_STAGE;
-                        if (leader) ptx::mbar_arrive_expect_tx(bar + 8 * s, 2 * (L::STAGE + L::SF_STAGE));
+                        if (leader)
+                            ptx::mbar_arrive_expect_tx(bar + 8 * s, 2 * (L::A + parts * L::BH + L::SF_STAGE));
                         ptx::tma_load_2d_pair(st, &tmap_a, full, kb * kStageBytes, arow);
                         ptx::tma_load_2d_pair(st + L::A, &tmap_b, full, kb * kStageBytes, brow);
-                        if (NH == 2)
+                        if (parts == 2)
                             ptx::tma_load_2d_pair(st + L::A + L::BH, &tmap_b, full, kb * kStageBytes, brow + PH);
                         ptx::tma_load_3d_pair(sf, &tmap_sa, full, 0, kb * L::NG, sarow);
                         ptx::tma_load_3d_pair(sf + L::SF, &tmap_sb, full, 0, kb * L::NG, sbrow);
@@ -403,9 +424,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         // last MMAs, and the second under the first one's first MMAs of the
         // next tile.
         if (lane == 0) {
-            uint32_t it = 0, tcount = 0;
+            uint32_t it = 0, shift = 0;
+            int parts = 0;
             bool ok = true;
-            uint32_t shift = 0;
             // part h of the stage that comes `i` after stage `it`
             auto issue = [&](uint32_t i, int h, bool zero) {
                 const uint32_t s = (it + i) % S;
@@ -414,21 +435,19 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 for (int j = 0; j < 4; ++j)
                     mma_pair<NV, L, 0>(tmem, col, desc_sw128(st), desc_sw128(st + L::A + h * L::BH), idesc, h, shift, j,
                                        zero && j == 0 ? 0u : 1u);
-                if (h == NH - 1) ptx::tc_commit_pair(empty + 8 * s, 0x3);
+                if (h == parts - 1) ptx::tc_commit_pair(empty + 8 * s, 0x3);
             };
             // the copiers have waited for the stage's bytes before they arrive
             auto ready = [&](uint32_t i) {
                 return wait_phase(scales + 8 * ((it + i) % SLOTS), ((it + i) / SLOTS) & 1u, limit, abort_flag, p.err,
                                   WHO_MMA);
             };
-            for (int tile = pair; tile < p.num_tiles && ok; tile += npairs, ++tcount) {
-                int mb, nb;
-                tile_coords(tile, p.num_mb, p.num_nb, mb, nb);
+            for (int t = 0, mb, nb; ok && (parts = tiles.get<NH>(p, t, mb, nb)) != 0; ++t) {
                 shift = nb * L::PN % 128 / 32;
                 const int head = min(L::SKEW, p.nk), tail = min(L::SKEW, p.nk - head);
-                for (int h = 0; h < NH && ok; ++h) {
-                    ok = wait_phase(tempty + 8 * h, (tcount & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA) &&
-                         wait_pair(odd + 8 * h, (tcount & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA);
+                for (int h = 0; h < parts && ok; ++h) {
+                    ok = wait_phase(tempty + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA) &&
+                         wait_pair(odd + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA);
                     for (int i = 0; i < head && ok; ++i) {
                         ok = h != 0 || ready(i);
                         if (!ok) break;
@@ -439,7 +458,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 }
                 if (!ok) break;
                 it += head;
-                for (int kb = head; kb < p.nk - tail; ++kb, ++it) {
+                for (int kb = head; parts == 1 && kb < p.nk - tail; ++kb, ++it) {
+                    ok = ready(0);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    issue(0, 0, false);
+                }
+                for (int kb = head; parts == 2 && kb < p.nk - tail; ++kb, ++it) {
                     ok = ready(0);
                     if (!ok) break;
                     ptx::tc_fence_after();
@@ -448,12 +473,12 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + L::A);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        mma_pair<NV, L, NH == 2 ? 1 : 0>(tmem, col, ad, bd, idesc, 0, shift, j, 1u);
-                        if (NH == 2) mma_pair<NV, L, 2>(tmem, col, ad, bd + (L::BH >> 4), idesc, 1, shift, j, 1u);
+                        mma_pair<NV, L, 1>(tmem, col, ad, bd, idesc, 0, shift, j, 1u);
+                        mma_pair<NV, L, 2>(tmem, col, ad, bd + (L::BH >> 4), idesc, 1, shift, j, 1u);
                     }
                     ptx::tc_commit_pair(empty + 8 * s, 0x3);
                 }
-                for (int h = 0; h < NH && tail != 0 && ok; ++h) {
+                for (int h = 0; h < parts && tail != 0 && ok; ++h) {
                     for (int i = 0; i < tail && ok; ++i) {
                         ok = h != 0 || ready(i);
                         if (!ok) break;
@@ -475,11 +500,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         // for its thread's own stores: from an epilogue warp, with the last
         // tile's stores in flight, that took 1300 cycles.
         if (lane == 0) {
-            uint32_t tcount = 0;
             bool ok = true;
-            for (int tile = pair; tile < p.num_tiles && ok; tile += npairs, ++tcount) {
-                for (int h = 0; h < NH && ok; ++h) {
-                    ok = wait_phase(tempty + 8 * h, tcount & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
+            for (int i = 0, mb, nb, parts; ok && (parts = tiles.get<NH>(p, i, mb, nb)) != 0; ++i) {
+                for (int h = 0; h < parts && ok; ++h) {
+                    ok = wait_phase(tempty + 8 * h, i & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
                     if (ok) ptx::mbar_arrive_cluster(odd_l + 8 * h);
                 }
             }
@@ -497,7 +521,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             const uint64_t src = desc_scales(base + L::OFF_SF + row * L::SF);
             uint32_t it = 0;
             bool ok = true;
-            for (int tile = pair; tile < p.num_tiles && ok; tile += npairs) {
+            for (int i = 0, mb, nb; ok && tiles.get<NH>(p, i, mb, nb) != 0; ++i) {
                 for (int kb = 0; kb < p.nk; ++kb, ++it) {
                     const uint32_t s = it % S, slot = it % SLOTS, u = it - SLOTS;
                     ok = wait_pair(bar + 8 * s, (it / S) & 1u, limit, abort_flag, p.err, WHO_SCALES) &&
@@ -942,13 +966,17 @@ void set_operands(Params &p, const Fp4GemmArgs &g, bool swapped, int tm, int tn)
     p.sn = swapped ? g.ldc : 1;
 }
 
+// Whether the last column of 384-column tiles has at most 192 of them.
+bool half_column(int64_t n) { return n % (2 * PH) != 0 && n % (2 * PH) <= PH; }
+
 template <bool NV, int NH>
 int launch_pair(const Fp4GemmArgs &g, Params &p, int sms, cudaStream_t stream) {
     using L = PairLayout<NV, NH>;
     set_operands(p, g, false, PM, L::PN);
-    const int64_t tiles = static_cast<int64_t>(p.num_mb) * p.num_nb;
+    if (NH == 2 && half_column(p.N)) p.half_tiles = p.num_mb, --p.num_nb;
+    const int64_t tiles = static_cast<int64_t>(p.num_mb) * p.num_nb + p.half_tiles;
     if (tiles > 0x7FFFFFFF) return 2 + static_cast<int>(cudaErrorInvalidValue);
-    p.num_tiles = static_cast<int>(tiles);
+    p.num_tiles = static_cast<int>(tiles) - p.half_tiles;
     CUtensorMap ta, tb, tsa, tsb;
     if (!make_tmap(&ta, g.a, 128) || !make_tmap(&tb, g.b, PH / 2) || !make_scale_tmap(&tsa, g.a, 1) ||
         !make_scale_tmap(&tsb, g.b, L::NB))
@@ -989,6 +1017,15 @@ struct Plan {
 
 double rounds(int64_t tiles, int64_t slots) { return static_cast<double>((tiles + slots - 1) / slots); }
 
+// The longest of the pairs' shares (see PairTiles) of wide and half tiles that
+// take `tw` and `th`.
+double wide_pairs(int64_t wide, int64_t half, int64_t pairs, double tw, double th) {
+    const int64_t rem = wide % pairs, low = pairs - rem;
+    const int64_t first = std::min<int64_t>(2, (half + low - 1) / low);
+    const double more = half > 2 * low ? rounds(half - 2 * low, pairs) * th : 0.0;
+    return static_cast<double>(wide / pairs) * tw + std::max(rem ? tw : 0.0, static_cast<double>(first) * th) + more;
+}
+
 Plan choose_few(int64_t rows, int64_t other, int nk, int sms) {
     const int widths[4] = {16, 32, 64, 128};
     const double stage[4] = {0.29, 0.31, 0.38, 0.48}, tile[4] = {0.4, 0.7, 1.6, 2.0};
@@ -1013,10 +1050,11 @@ Plan choose(int64_t m, int64_t n, int nk, int sms) {
     Plan best = choose_few(std::min(m, n), std::max(m, n), nk, sms);
     if (std::min(m, n) > 32 && sms >= 2) {
         const int64_t mb = (m + PM - 1) / PM;
-        const double two = 4.5 + rounds(mb * ((n + 383) / 384), sms / 2) * (0.49 * nk + 1.8);
-        const double one = 4.5 + rounds(mb * ((n + 191) / 192), sms / 2) * (0.31 * nk + 1.5);
-        if (two < best.us) best = {2, 0, 1, two};
+        const double two = 4.5 + wide_pairs(mb * ((n + PH - 1) / (2 * PH)), half_column(n) ? mb : 0, sms / 2,
+                                            0.49 * nk + 1.8, 0.31 * nk + 1.5);
+        const double one = 4.5 + rounds(mb * ((n + PH - 1) / PH), sms / 2) * (0.31 * nk + 1.5);
         if (one < best.us) best = {1, 0, 1, one};
+        if (two < best.us) best = {2, 0, 1, two};
     }
     return best;
 }
