@@ -62,6 +62,7 @@ struct Params {
     void *c;
     int64_t sm, sn;                // C's strides along P and Q, elements
     int out_fp32, accumulate, inject;
+    int c_tma;                     // C's rows are written by TMA
     int splits;
     uint64_t wait_limit_ns;
     unsigned int *err;
@@ -88,12 +89,23 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
 // operand bytes: it takes as many per cycle as an FP8 one and reads a stage in
 // half the time, and an SM gets about 60 bytes a cycle from L2 here.  Single-CTA
 // tiles of 256 x 192 (two accumulators of 128 rows) need 56 KB for the same 768
-// cycles.  At 16384 x 3584 x 18944: 380 us with those tiles (MX; NV 447), 345
-// (369) with these.
+// cycles.  At 16384 x 3584 x 18944: 380 us with those tiles (MX; NV 447), 303
+// (350) with these: 7.3 (6.4) PFLOP/s, for which the GPU draws its power limit
+// (a second of it runs at 1.7 GHz; with zeros as operands a call takes 12 %
+// less).
 // NH = 1, where NH = 2 leaves pairs without a tile.
+// A last column of at most 192 columns is computed as half tiles of an NH = 2
+// launch: 8192 x 3584 x 3584 in four rounds of tiles instead of five (NV: 48
+// us instead of 55).
 //
-// Warps of each CTA: 0 TMA producer, 4-11 epilogue (a 32-row quarter of one
-// column part each); of the even CTA also 1 MMA issuer and 2, 3, 12, 13 scale
+// The ring of operand stages is short (four stages, 2.4 us of MMAs at best), so
+// what counts is how soon a stage is used and free again.  Its scales have
+// barriers and a producer of their own and are in tensor memory when it lands:
+// MX 16384 x 3584 x 18944 takes 334 us where a stage's scales come with it and
+// are copied after it.
+//
+// Warps of each CTA: 0 operand producer, 14 scale producer, 4-11 epilogue (a
+// 32-row quarter of one column part each); of the even CTA also 1 MMA issuer and 2, 3, 12, 13 scale
 // copiers, for both CTAs; of the odd CTA 1 forwarder.  Tensor memory: the
 // accumulators, then the scale slots: per 128 (NV: 64) elements of K four
 // columns for every 128 rows, B's first.
@@ -106,23 +118,21 @@ struct PairLayout {
     static constexpr int NB = NH == 2 ? 3 : 2; // 128-row scale tiles that a tile's columns touch
     static constexpr int S = NH == 2 ? 4 : 6;
     static constexpr int SLOTS = NH == 2 && NV ? 2 : NH == 2 ? 4 : S;
-    // stages at a tile's ends whose column parts go one after the other
-    static constexpr int SKEW = NH == 2 && NV ? 2 : 1;
     static constexpr uint32_t SF = NG * 512;
     static constexpr uint32_t A = 128 * kStageBytes, BH = PH / 2 * kStageBytes;
     static constexpr uint32_t STAGE = A + NH * BH, SF_STAGE = (1 + NB) * SF;   // A's rows, then B's
-    static constexpr uint32_t OFF_SF = S * STAGE, OFF_BAR = OFF_SF + S * SF_STAGE;
-    // barriers: full (even CTA: both CTAs' bytes), empty (each CTA), scales
-    // (even CTA), tfull[2] and tempty[2] (each CTA), odd[2] (even CTA: the odd
-    // one's tempty), drain[5]
-    static constexpr uint32_t EMPTY = 8 * S, SCALES = 16 * S, TFULL = SCALES + 8 * SLOTS;
+    static constexpr uint32_t OFF_SF = S * STAGE, OFF_EPI = OFF_SF + S * SF_STAGE;
+    static constexpr uint32_t OFF_BAR = OFF_EPI + 4 * NH * EPI_BYTES;
+    // barriers: full (even CTA: both CTAs' operands), empty (each CTA), sfull
+    // (even CTA: both CTAs' scales), scales (each CTA: copied to tensor memory),
+    // tfull[2] and tempty[2] (each CTA), odd[2] (even CTA: the odd one's
+    // tempty), drain[5]
+    static constexpr uint32_t EMPTY = 8 * S, SFULL = 16 * S, SCALES = 24 * S, TFULL = 32 * S;
     static constexpr uint32_t TEMPTY = TFULL + 16, ODD = TEMPTY + 16, DRAIN = ODD + 16;
-    static constexpr uint32_t OFF_MISC = OFF_BAR + 256, OFF_EPI = OFF_MISC + 16;
-    static constexpr uint32_t SMEM = OFF_EPI + 4 * NH * EPI_BYTES + 1024;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + 288, SMEM = OFF_MISC + 16 + 1024;
     static constexpr uint32_t GC = 4 * (1 + NB), COLS = GC * NG;   // columns of a scale group, of a slot
-    static_assert(DRAIN + 40 <= 256 && SMEM <= 232448 && PN + SLOTS * COLS <= 512, "");
-    // a slot is freed by its stage's barrier; the skewed stages are all in slots
-    static_assert(SLOTS <= S && SKEW <= SLOTS, "");
+    static_assert(DRAIN + 40 <= 288 && OFF_EPI % 1024 == 0 && SMEM <= 232448 && PN + SLOTS * COLS <= 512, "");
+    static_assert(SLOTS <= S, "a slot is freed by its stage's barrier");
     static_assert(A % 1024 == 0 && BH % 1024 == 0, "the swizzle repeats every 1 KB");
 };
 
@@ -151,32 +161,23 @@ __device__ __forceinline__ uint4 staged(const uint8_t *stage, int r, int c) {
     return *reinterpret_cast<const uint4 *>(stage + r * 128 + ((c ^ (r & 7)) << 4));
 }
 
-// The staged piece as 64 BF16 columns of C from (row0, col0).
+// The staged piece as 64 BF16 columns of C from (row0, col0), for a C that TMA
+// cannot write: two neighbouring columns per lane, row by row.
 __device__ __forceinline__ void write_bf16(const uint8_t *stage, int lane, const Params &p,
-                                           int64_t row0, int64_t col0, bool vec) {
+                                           int64_t row0, int64_t col0) {
     uint16_t *c = static_cast<uint16_t *>(p.c);
-    if (vec && col0 + 64 <= p.N) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int idx = i * 32 + lane, r = idx >> 3, q = idx & 7;
-            if (row0 + r < p.M)
-                *reinterpret_cast<uint4 *>(c + (row0 + r) * p.sm + col0 + q * 8) = staged(stage, r, q);
-        }
-    } else {
-        // two neighbouring columns per lane, row by row
-        const int64_t col = col0 + 2 * lane;
-        for (int r = 0; r < 32 && row0 + r < p.M; ++r) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-            uint16_t *d = c + (row0 + r) * p.sm + col;
-            if (col < p.N) d[0] = static_cast<uint16_t>(w);
-            if (col + 1 < p.N) d[1] = static_cast<uint16_t>(w >> 16);
-        }
+    const int64_t col = col0 + 2 * lane;
+    for (int r = 0; r < 32 && row0 + r < p.M; ++r) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(
+            stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+        uint16_t *d = c + (row0 + r) * p.sm + col;
+        if (col < p.N) d[0] = static_cast<uint16_t>(w);
+        if (col + 1 < p.N) d[1] = static_cast<uint16_t>(w >> 16);
     }
 }
 
-// The staged piece as 32 FP32 values per row from (row0, col0): FP32 output,
-// or an output that is read and added to first (one rounding).
+// The staged piece as 32 FP32 values per row from (row0, col0), for an output
+// that is read and added to first (one rounding), or FP32 that TMA cannot write.
 __device__ __forceinline__ void write_f32(const uint8_t *stage, int lane, const Params &p,
                                           int64_t row0, int64_t col0, bool vec) {
     if (p.out_fp32 && vec && col0 + 32 <= p.N) {
@@ -187,13 +188,9 @@ __device__ __forceinline__ void write_f32(const uint8_t *stage, int lane, const 
             if (row0 + r >= p.M) continue;
             float4 *d = reinterpret_cast<float4 *>(c + (row0 + r) * p.sm + col0 + q * 4);
             const uint4 w = staged(stage, r, q);
-            float4 v = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
-                                   __uint_as_float(w.w));
-            if (p.accumulate) {
-                const float4 o = *d;
-                v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-            }
-            *d = v;
+            const float4 o = *d;
+            *d = make_float4(__uint_as_float(w.x) + o.x, __uint_as_float(w.y) + o.y, __uint_as_float(w.z) + o.z,
+                             __uint_as_float(w.w) + o.w);
         }
         return;
     }
@@ -262,15 +259,15 @@ template <bool NV, int NH>
 __global__ void __launch_bounds__(P_THREADS, 1)
     k_fp4_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
-               const Params p, const uint32_t idesc) {
+               const __grid_constant__ CUtensorMap tmap_c, const Params p, const uint32_t idesc) {
     using L = PairLayout<NV, NH>;
     constexpr int S = L::S, SLOTS = L::SLOTS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
     const uint32_t bar = base + L::OFF_BAR;
-    const uint32_t empty = bar + L::EMPTY, scales = bar + L::SCALES, tfull = bar + L::TFULL,
-                   tempty = bar + L::TEMPTY, odd = bar + L::ODD, drain = bar + L::DRAIN;
+    const uint32_t empty = bar + L::EMPTY, scales = bar + L::SCALES, sfull = bar + L::SFULL,
+                   tfull = bar + L::TFULL, tempty = bar + L::TEMPTY, odd = bar + L::ODD, drain = bar + L::DRAIN;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + L::OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + L::OFF_MISC + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -280,14 +277,15 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const PairTiles tiles(p, pair, npairs);
     const uint64_t limit = p.wait_limit_ns, drain_limit = 2000000ull;
     // the even CTA's barriers, as seen from either CTA
-    const uint32_t full_l = ptx::map_shared_rank(bar, 0), odd_l = ptx::map_shared_rank(odd, 0);
+    const uint32_t full_l = ptx::map_shared_rank(bar, 0), sfull_l = full_l + L::SFULL, odd_l = full_l + L::ODD;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             ptx::mbar_init(bar + 8 * s, 1);
             ptx::mbar_init(empty + 8 * s, 1);
+            ptx::mbar_init(sfull + 8 * s, 1);
+            ptx::mbar_init(scales + 8 * s, 1 + L::NB);   // the copiers
         }
-        for (int i = 0; i < SLOTS; ++i) ptx::mbar_init(scales + 8 * i, 1 + L::NB);   // the copiers
         for (int h = 0; h < 2; ++h) {
             ptx::mbar_init(tfull + 8 * h, 1);
             ptx::mbar_init(tempty + 8 * h, 4);   // the half's four epilogue warps
@@ -314,11 +312,17 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     // warpgroups take over what the others leave (2 * 128 * (168 + 80) <= 65536)
     if (warp >= 4 && warp < 12) {
         // ---------------------------------------------------------- epilogue
+        // An accumulator goes to registers, C from there in pieces of 32 rows x
+        // 128 bytes through the warp's staging area: by TMA, which cuts off
+        // what lies past C's edges, or (an odd C, or one that is added to) by
+        // the lanes.  TMA instead of 16-byte stores of the lanes: BF16 2 to 4 %
+        // of the whole product, FP32 5 to 7 %.
         ptx::setmaxnreg_inc<168>();
         const int q = warp & 3, half = (warp - 4) >> 2;
         uint8_t *stage = gbase + L::OFF_EPI + (warp - 4) * EPI_BYTES;
         const float alpha = (p.ta ? __ldg(p.ta) : 1.0f) * (p.tb ? __ldg(p.tb) : 1.0f);
-        const bool vec = (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % (p.out_fp32 ? 4 : 8) == 0;
+        // a C that is added to, four values at a time (without `accumulate` such a C is TMA's)
+        const bool vec = p.accumulate && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % 4 == 0;
         for (int i = 0, mb, nb; tiles.get<NH>(p, i, mb, nb) > half; ++i) {
             bool ok = wait_phase(tfull + 8 * half, i & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -341,10 +345,18 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     if (chunk == PH / 32 - 1) release();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+                    if (p.c_tma && lane == 0) ptx::bulk_wait_read();
+                    __syncwarp();
                     stage_row(stage, lane, r);
+                    if (p.c_tma) ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    write_f32(stage, lane, p, row0, col0 + chunk * 32, vec);
-                    __syncwarp();
+                    if (!p.c_tma) {
+                        write_f32(stage, lane, p, row0, col0 + chunk * 32, vec);
+                    } else if (lane == 0 && row0 < p.M && col0 + chunk * 32 < p.N) {
+                        ptx::tma_store_2d(&tmap_c, ptx::smem_u32(stage), static_cast<int>(col0) + chunk * 32,
+                                          static_cast<int>(row0));
+                        ptx::bulk_commit();
+                    }
                 }
                 continue;
             }
@@ -363,184 +375,214 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             release();
 #pragma unroll
             for (int piece = 0; piece < PH / 64; ++piece) {
+                // (in this form it needs no more registers than there are)
+                if (p.c_tma) {
+                    if (lane == 0) ptx::bulk_wait_read();
+                    __syncwarp();
+                }
                 stage_row(stage, lane, packed + piece * 32);
-                __syncwarp();
-                write_bf16(stage, lane, p, row0, col0 + piece * 64, vec);
-                __syncwarp();
-            }
-        }
-    } else {
-    ptx::setmaxnreg_dec<80>();
-    if (warp == 0) {
-        // ---------------------------------------------------------- producer
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int i = 0, mb, nb, parts; ok && (parts = tiles.get<NH>(p, i, mb, nb)) != 0; ++i) {
-                const int arow = mb * PM + static_cast<int>(rank) * 128;
-                const int brow = nb * L::PN + static_cast<int>(rank) * (PH / 2);
-                const int sarow = mb * 2 + static_cast<int>(rank), sbrow = nb * L::PN / 128;
-                for (int kb = 0; kb < p.nk; ++kb) {
-                    const uint32_t s = it % S, full = full_l + 8 * s;
-                    ok = wait_phase(empty + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag, p.err, WHO_PRODUCER);
-                    if (!ok) break;
-                    // inject = 1 (a test of the timeout path): the first
-                    // CTA never issues its first stage
-                    if (!(p.inject == 1 && blockIdx.x == 0 && it == 0)) {
-                        const uint32_t st = base + s * L::STAGE, sf = base + L::OFF_SF + s * L::SF_STAGE;
-                        if (leader)
-                            ptx::mbar_arrive_expect_tx(bar + 8 * s, 2 * (L::A + parts * L::BH + L::SF_STAGE));
-                        ptx::tma_load_2d_pair(st, &tmap_a, full, kb * kStageBytes, arow);
-                        ptx::tma_load_2d_pair(st + L::A, &tmap_b, full, kb * kStageBytes, brow);
-                        if (parts == 2)
-                            ptx::tma_load_2d_pair(st + L::A + L::BH, &tmap_b, full, kb * kStageBytes, brow + PH);
-                        ptx::tma_load_3d_pair(sf, &tmap_sa, full, 0, kb * L::NG, sarow);
-                        ptx::tma_load_3d_pair(sf + L::SF, &tmap_sb, full, 0, kb * L::NG, sbrow);
+                if (p.c_tma) {
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && row0 < p.M && col0 + piece * 64 < p.N) {
+                        ptx::tma_store_2d(&tmap_c, ptx::smem_u32(stage), static_cast<int>(col0) + piece * 64,
+                                          static_cast<int>(row0));
+                        ptx::bulk_commit();
                     }
-                    ++it;
+                } else {
+                    __syncwarp();
+                    write_bf16(stage, lane, p, row0, col0 + piece * 64);
+                    __syncwarp();
                 }
             }
-            // the even CTA waits until both CTAs' last copies have landed; the
-            // cluster barrier below keeps the odd CTA resident until then
-            if (leader) {
-                const uint32_t nd = it < S ? it : S;
-                for (uint32_t i = it - nd; i < it; ++i)
-                    wait_phase(bar + 8 * (i % S), (i / S) & 1u, drain_limit, abort_flag, p.err, WHO_PRODUCER, false);
-            }
-            // A CTA that stopped early cannot tell which of its last copies
-            // have been counted: it gives them the drain bound to land.
+        }
+        if (p.c_tma && lane == 0) ptx::bulk_wait();
+    } else {
+        ptx::setmaxnreg_dec<80>();
+        // A producer's end, after `it` stages: the even CTA waits until both CTAs'
+        // last copies have landed, the odd one for the arrivals that free them (the
+        // cluster barrier below keeps each resident until the other is there).  A
+        // CTA that stopped early cannot tell which of its last copies have been
+        // counted: it gives them the drain bound to land.
+        auto landed = [&](uint32_t full, uint32_t freed, uint32_t it, bool ok) {
+            for (uint32_t i = it < S ? 0 : it - S; i < it; ++i)
+                wait_phase((leader ? full : freed) + 8 * (i % S), (i / S) & 1u, drain_limit, abort_flag, p.err,
+                           WHO_PRODUCER, false);
             if (!ok || *abort_flag) {
                 const uint64_t t0 = ptx::globaltimer();
                 while (ptx::globaltimer() - t0 < drain_limit) {
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp == 1 && leader) {
-        // -------------------------------------------------------- MMA issuer
-        // The two column halves alternate, except in a tile's first and last
-        // SKEW stages, where one half's MMAs of those stages go before the
-        // other's: so the first accumulator is drained under the second one's
-        // last MMAs, and the second under the first one's first MMAs of the
-        // next tile.
-        if (lane == 0) {
-            uint32_t it = 0, shift = 0;
-            int parts = 0;
-            bool ok = true;
-            // part h of the stage that comes `i` after stage `it`
-            auto issue = [&](uint32_t i, int h, bool zero) {
-                const uint32_t s = (it + i) % S;
-                const uint32_t st = base + s * L::STAGE, col = tmem + L::PN + (it + i) % SLOTS * L::COLS;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mma_pair<NV, L, 0>(tmem, col, desc_sw128(st), desc_sw128(st + L::A + h * L::BH), idesc, h, shift, j,
-                                       zero && j == 0 ? 0u : 1u);
-                if (h == parts - 1) ptx::tc_commit_pair(empty + 8 * s, 0x3);
-            };
-            // the copiers have waited for the stage's bytes before they arrive
-            auto ready = [&](uint32_t i) {
-                return wait_phase(scales + 8 * ((it + i) % SLOTS), ((it + i) / SLOTS) & 1u, limit, abort_flag, p.err,
-                                  WHO_MMA);
-            };
-            for (int t = 0, mb, nb; ok && (parts = tiles.get<NH>(p, t, mb, nb)) != 0; ++t) {
-                shift = nb * L::PN % 128 / 32;
-                const int head = min(L::SKEW, p.nk), tail = min(L::SKEW, p.nk - head);
-                for (int h = 0; h < parts && ok; ++h) {
-                    ok = wait_phase(tempty + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA) &&
-                         wait_pair(odd + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA);
-                    for (int i = 0; i < head && ok; ++i) {
-                        ok = h != 0 || ready(i);
+        };
+        if (warp == 0) {
+            // ---------------------------------------------------------- producer
+            if (lane == 0) {
+                uint32_t it = 0;
+                bool ok = true;
+                for (int i = 0, mb, nb, parts; ok && (parts = tiles.get<NH>(p, i, mb, nb)) != 0; ++i) {
+                    const int arow = mb * PM + static_cast<int>(rank) * 128;
+                    const int brow = nb * L::PN + static_cast<int>(rank) * (PH / 2);
+                    for (int kb = 0; kb < p.nk; ++kb) {
+                        const uint32_t s = it % S, full = full_l + 8 * s;
+                        ok = wait_phase(empty + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag, p.err, WHO_PRODUCER);
+                        if (!ok) break;
+                        // inject = 1 (a test of the timeout path): the first
+                        // CTA never issues its first stage
+                        if (!(p.inject == 1 && blockIdx.x == 0 && it == 0)) {
+                            const uint32_t st = base + s * L::STAGE;
+                            if (leader) ptx::mbar_arrive_expect_tx(bar + 8 * s, 2 * (L::A + parts * L::BH));
+                            ptx::tma_load_2d_pair(st, &tmap_a, full, kb * kStageBytes, arow);
+                            ptx::tma_load_2d_pair(st + L::A, &tmap_b, full, kb * kStageBytes, brow);
+                            if (parts == 2)
+                                ptx::tma_load_2d_pair(st + L::A + L::BH, &tmap_b, full, kb * kStageBytes, brow + PH);
+                        }
+                        ++it;
+                    }
+                }
+                landed(bar, empty, it, ok);
+            }
+            __syncwarp();
+        } else if (warp == 14) {
+            // ---------------------------------------------------- scale producer
+            // On its own, because a stage of scales is free again as soon as it is
+            // in tensor memory: the copies run ahead of the operands.
+            if (lane == 0) {
+                uint32_t it = 0;
+                bool ok = true;
+                for (int i = 0, mb, nb; ok && tiles.get<NH>(p, i, mb, nb) != 0; ++i) {
+                    const int sarow = mb * 2 + static_cast<int>(rank), sbrow = nb * L::PN / 128;
+                    for (int kb = 0; kb < p.nk; ++kb, ++it) {
+                        const uint32_t s = it % S, full = sfull_l + 8 * s, sf = base + L::OFF_SF + s * L::SF_STAGE;
+                        ok = wait_phase(scales + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag, p.err, WHO_PRODUCER);
+                        if (!ok) break;
+                        if (leader) ptx::mbar_arrive_expect_tx(sfull + 8 * s, 2 * L::SF_STAGE);
+                        ptx::tma_load_3d_pair(sf, &tmap_sa, full, 0, kb * L::NG, sarow);
+                        ptx::tma_load_3d_pair(sf + L::SF, &tmap_sb, full, 0, kb * L::NG, sbrow);
+                    }
+                }
+                landed(sfull, scales, it, ok);
+            }
+            __syncwarp();
+        } else if (warp == 1 && leader) {
+            // -------------------------------------------------------- MMA issuer
+            // The two column halves alternate, except in a tile's first and last
+            // stage, where one half's four MMAs go before the other's: so the first
+            // accumulator is drained under the second one's last MMAs, and the
+            // second under the first one's first MMAs of the next tile.  (This one
+            // thread's latency counts: with calls in its waits or another branch in
+            // the inner loop the product takes 2 to 5 % longer.)
+            if (lane == 0) {
+                uint32_t it = 0, shift = 0;
+                int parts = 0;
+                bool ok = true;
+                // part h of stage `it`
+                auto issue = [&](int h, bool zero) {
+                    const uint32_t s = it % S, st = base + s * L::STAGE, col = tmem + L::PN + it % SLOTS * L::COLS;
+    #pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_pair<NV, L, 0>(tmem, col, desc_sw128(st), desc_sw128(st + L::A + h * L::BH), idesc, h,
+                                           shift, j, zero && j == 0 ? 0u : 1u);
+                    if (h == parts - 1) ptx::tc_commit_pair(empty + 8 * s, 0x3);
+                };
+                auto ready = [&] {
+                    const uint32_t s = 8 * (it % S), parity = (it / S) & 1u;
+                    const bool r = wait_phase(scales + s, parity, limit, abort_flag, p.err, WHO_MMA) &&
+                                   wait_pair(bar + s, parity, limit, abort_flag, p.err, WHO_MMA);
+                    ptx::tc_fence_after();
+                    return r;
+                };
+                for (int t = 0, mb, nb; ok && (parts = tiles.get<NH>(p, t, mb, nb)) != 0; ++t) {
+                    shift = nb * L::PN % 128 / 32;
+                    for (int h = 0; h < parts && ok; ++h) {
+                        ok = wait_phase(tempty + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA) &&
+                             wait_pair(odd + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA) &&
+                             (h != 0 || ready());
                         if (!ok) break;
                         ptx::tc_fence_after();
-                        issue(i, h, i == 0);
+                        issue(h, true);
+                        if (p.nk == 1) ptx::tc_commit_pair(tfull + 8 * h, 0x3);
                     }
-                    if (ok && tail == 0) ptx::tc_commit_pair(tfull + 8 * h, 0x3);
-                }
-                if (!ok) break;
-                it += head;
-                for (int kb = head; parts == 1 && kb < p.nk - tail; ++kb, ++it) {
-                    ok = ready(0);
                     if (!ok) break;
-                    ptx::tc_fence_after();
-                    issue(0, 0, false);
-                }
-                for (int kb = head; parts == 2 && kb < p.nk - tail; ++kb, ++it) {
-                    ok = ready(0);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t s = it % S;
-                    const uint32_t st = base + s * L::STAGE, col = tmem + L::PN + it % SLOTS * L::COLS;
-                    const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + L::A);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        mma_pair<NV, L, 1>(tmem, col, ad, bd, idesc, 0, shift, j, 1u);
-                        mma_pair<NV, L, 2>(tmem, col, ad, bd + (L::BH >> 4), idesc, 1, shift, j, 1u);
+                    ++it;
+                    for (int kb = 1; parts == 1 && kb < p.nk - 1; ++kb, ++it) {
+                        ok = ready();
+                        if (!ok) break;
+                        issue(0, false);
                     }
-                    ptx::tc_commit_pair(empty + 8 * s, 0x3);
+                    for (int kb = 1; parts == 2 && kb < p.nk - 1; ++kb, ++it) {
+                        ok = ready();
+                        if (!ok) break;
+                        const uint32_t s = it % S;
+                        const uint32_t st = base + s * L::STAGE, col = tmem + L::PN + it % SLOTS * L::COLS;
+                        const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + L::A);
+    #pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            mma_pair<NV, L, 1>(tmem, col, ad, bd, idesc, 0, shift, j, 1u);
+                            mma_pair<NV, L, 2>(tmem, col, ad, bd + (L::BH >> 4), idesc, 1, shift, j, 1u);
+                        }
+                        ptx::tc_commit_pair(empty + 8 * s, 0x3);
+                    }
+                    if (p.nk == 1) continue;
+                    for (int h = 0; h < parts && ok; ++h) {
+                        ok = h != 0 || ready();
+                        if (!ok) break;
+                        issue(h, false);
+                        ptx::tc_commit_pair(tfull + 8 * h, 0x3);
+                    }
+                    ++it;
                 }
-                for (int h = 0; h < parts && tail != 0 && ok; ++h) {
-                    for (int i = 0; i < tail && ok; ++i) {
-                        ok = h != 0 || ready(i);
+                ptx::tc_commit_pair(drain, 0x1);
+                wait_phase(drain, 0u, drain_limit, abort_flag, p.err, WHO_MMA, false);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------ forwarder (odd CTA)
+            // Tells the even CTA that this one's accumulators are drained.  An
+            // arrival in the other CTA is a release at cluster scope and waits
+            // for its thread's own stores: from an epilogue warp, with the last
+            // tile's stores in flight, that took 1300 cycles.
+            if (lane == 0) {
+                bool ok = true;
+                for (int i = 0, mb, nb, parts; ok && (parts = tiles.get<NH>(p, i, mb, nb)) != 0; ++i) {
+                    for (int h = 0; h < parts && ok; ++h) {
+                        ok = wait_phase(tempty + 8 * h, i & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
+                        if (ok) ptx::mbar_arrive_cluster(odd_l + 8 * h);
+                    }
+                }
+            }
+            __syncwarp();
+        } else if ((warp == 2 || warp == 3 || (warp >= 12 && warp < 11 + L::NB)) && leader) {
+            // ------------------------------------------- scales to tensor memory
+            // One of the 128-row tiles each (0: A's rows, then B's), into the slot
+            // that the MMAs of stage it - SLOTS freed.  A copy costs its
+            // thread about 80 cycles, so two copiers could not keep up with NV's
+            // 16 copies per stage.
+            if (lane == 0) {
+                const int row = warp < 4 ? warp - 2 : warp - 10;
+                const uint32_t dst = tmem + L::PN + (row == 0 ? 4 * L::NB : (row - 1) * 4);
+                const uint64_t src = desc_scales(base + L::OFF_SF + row * L::SF);
+                uint32_t it = 0;
+                bool ok = true;
+                for (int i = 0, mb, nb; ok && tiles.get<NH>(p, i, mb, nb) != 0; ++i) {
+                    for (int kb = 0; kb < p.nk; ++kb, ++it) {
+                        const uint32_t s = it % S, slot = it % SLOTS, u = it - SLOTS;
+                        ok = wait_pair(sfull + 8 * s, (it / S) & 1u, limit, abort_flag, p.err, WHO_SCALES) &&
+                             (it < SLOTS || wait_phase(empty + 8 * (u % S), (u / S) & 1u, limit, abort_flag, p.err,
+                                                       WHO_SCALES));
                         if (!ok) break;
                         ptx::tc_fence_after();
-                        issue(i, h, false);
+                        const uint64_t sd = src + s * (L::SF_STAGE >> 4);
+                        const uint32_t d = dst + slot * L::COLS;
+    #pragma unroll
+                        for (int g = 0; g < L::NG; ++g) ptx::tc_cp_32x128b_warpx4_pair(d + g * L::GC, sd + g * 32);
+                        ptx::tc_commit_pair(scales + 8 * s, 0x3);
                     }
-                    if (ok) ptx::tc_commit_pair(tfull + 8 * h, 0x3);
                 }
-                it += tail;
+                ptx::tc_commit_pair(drain + 8 * (row + 1), 0x1);
+                wait_phase(drain + 8 * (row + 1), 0u, drain_limit, abort_flag, p.err, WHO_SCALES, false);
             }
-            ptx::tc_commit_pair(drain, 0x1);
-            wait_phase(drain, 0u, drain_limit, abort_flag, p.err, WHO_MMA, false);
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------ forwarder (odd CTA)
-        // Tells the even CTA that this one's accumulators are drained.  An
-        // arrival in the other CTA is a release at cluster scope and waits
-        // for its thread's own stores: from an epilogue warp, with the last
-        // tile's stores in flight, that took 1300 cycles.
-        if (lane == 0) {
-            bool ok = true;
-            for (int i = 0, mb, nb, parts; ok && (parts = tiles.get<NH>(p, i, mb, nb)) != 0; ++i) {
-                for (int h = 0; h < parts && ok; ++h) {
-                    ok = wait_phase(tempty + 8 * h, i & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
-                    if (ok) ptx::mbar_arrive_cluster(odd_l + 8 * h);
-                }
-            }
-        }
-        __syncwarp();
-    } else if ((warp == 2 || warp == 3 || (warp >= 12 && warp < 11 + L::NB)) && leader) {
-        // ------------------------------------------- scales to tensor memory
-        // One of the 128-row tiles each (0: A's rows, then B's), into the slot
-        // that the MMAs of stage it - SLOTS freed.  A copy costs its
-        // thread about 80 cycles, so two copiers could not keep up with NV's
-        // 16 copies per stage.
-        if (lane == 0) {
-            const int row = warp < 4 ? warp - 2 : warp - 10;
-            const uint32_t dst = tmem + L::PN + (row == 0 ? 4 * L::NB : (row - 1) * 4);
-            const uint64_t src = desc_scales(base + L::OFF_SF + row * L::SF);
-            uint32_t it = 0;
-            bool ok = true;
-            for (int i = 0, mb, nb; ok && tiles.get<NH>(p, i, mb, nb) != 0; ++i) {
-                for (int kb = 0; kb < p.nk; ++kb, ++it) {
-                    const uint32_t s = it % S, slot = it % SLOTS, u = it - SLOTS;
-                    ok = wait_pair(bar + 8 * s, (it / S) & 1u, limit, abort_flag, p.err, WHO_SCALES) &&
-                         (it < SLOTS || wait_phase(empty + 8 * (u % S), (u / S) & 1u, limit, abort_flag, p.err,
-                                                   WHO_SCALES));
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint64_t sd = src + s * (L::SF_STAGE >> 4);
-                    const uint32_t d = dst + slot * L::COLS;
-#pragma unroll
-                    for (int g = 0; g < L::NG; ++g) ptx::tc_cp_32x128b_warpx4_pair(d + g * L::GC, sd + g * 32);
-                    ptx::tc_commit_pair(scales + 8 * slot, 0x1);
-                }
-            }
-            ptx::tc_commit_pair(drain + 8 * (row + 1), 0x1);
-            wait_phase(drain + 8 * (row + 1), 0u, drain_limit, abort_flag, p.err, WHO_SCALES, false);
-        }
-        __syncwarp();
-    }
     }
 
     // neither CTA leaves (or frees its tensor memory) while the other may still
@@ -690,7 +732,8 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         int it = n < 2 ? n : 2;
         for (; it < n; ++it) {
             const int s = it % S;
-            bool ok = it < S || wait_phase(bar + L::EMPTY + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag, p.err, WHO_PRODUCER);
+            bool ok = it < S || wait_phase(bar + L::EMPTY + 8 * s, ((it / S) & 1u) ^ 1u, limit, abort_flag, p.err,
+                                           WHO_PRODUCER);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             if (lane == 0) load_stage(it);
@@ -905,6 +948,19 @@ bool make_scale_tmap(CUtensorMap *m, const Fp4Operand &o, int rows) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// BF16 C, written in pieces of 32 rows x 64 columns.
+bool make_out_tmap(CUtensorMap *m, const Params &p) {
+    TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    std::memset(m, 0, sizeof(*m));
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.sm) * (p.out_fp32 ? 4 : 2)};
+    const cuuint32_t box[2] = {p.out_fp32 ? 32u : 64u, 32}, estr[2] = {1, 1};
+    return enc(m, p.out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 std::mutex g_mu;
 int g_sms[64] = {0};
 
@@ -977,12 +1033,15 @@ int launch_pair(const Fp4GemmArgs &g, Params &p, int sms, cudaStream_t stream) {
     const int64_t tiles = static_cast<int64_t>(p.num_mb) * p.num_nb + p.half_tiles;
     if (tiles > 0x7FFFFFFF) return 2 + static_cast<int>(cudaErrorInvalidValue);
     p.num_tiles = static_cast<int>(tiles) - p.half_tiles;
-    CUtensorMap ta, tb, tsa, tsb;
+    CUtensorMap ta, tb, tsa, tsb, tc;
     if (!make_tmap(&ta, g.a, 128) || !make_tmap(&tb, g.b, PH / 2) || !make_scale_tmap(&tsa, g.a, 1) ||
         !make_scale_tmap(&tsb, g.b, L::NB))
         return 1;
+    tc = tsb;   // not used unless c_tma
+    p.c_tma = !p.accumulate && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % (p.out_fp32 ? 4 : 8) == 0 &&
+              make_out_tmap(&tc, p);
     return launch_cluster(k_fp4_pair<NV, NH>, 2 * std::min<int64_t>(tiles, sms / 2), 2, P_THREADS, L::SMEM, stream, ta,
-                          tb, tsa, tsb, p, instruction(NV, PM, PH));
+                          tb, tsa, tsb, tc, p, instruction(NV, PM, PH));
 }
 
 template <bool NV, int BN, bool QUANT>
@@ -1004,12 +1063,12 @@ int launch_few(const Fp4GemmArgs &g, Params &p, bool swapped, int splits, cudaSt
 // Which kernel, from its time as measured on a GB300 (microseconds; MX, NV is
 // alike, 5 to 15 % slower throughout): a fixed part, then for every round of
 // tiles over the machine a part per stage of K and one per tile.
-//   pairs        4.5 + rounds (0.49 nk + 1.8) with 384 columns, (0.31 nk + 1.5) with 192
+//   pairs        4.5 + rounds (0.46 nk + 2.4) with 384 columns, (0.30 nk + 1.6) with 192
 //   few rows     3.8 + rounds (c nk / splits + e), (c, e) by the tile's columns: 0.29, 0.4 for 16
 //                ... 0.48, 2 for 128
-// So 8192 x 18944 x 3584 takes 191 us with 384 columns and 248 with 192; 1000 x
-// 3584 x 18944 44 and 31; 200 x 1536 x 8960 17 with pairs and 10 with four K
-// parts of few-row tiles; 128 x 18944 x 3584 15 and 17.
+// So 8192 x 8960 x 1536 takes 57 us with 384 columns and 69 with 192; 1024 x
+// 3584 x 18944 38 and 29; 256 x 1536 x 8960 16 with pairs and 9.5 with four K
+// parts of few-row tiles; 256 x 18944 x 3584 15 and 26.
 struct Plan {
     int nh, bn, splits;     // nh > 0: pair tiles of 192 nh columns; else bn and K parts
     double us;
@@ -1051,8 +1110,8 @@ Plan choose(int64_t m, int64_t n, int nk, int sms) {
     if (std::min(m, n) > 32 && sms >= 2) {
         const int64_t mb = (m + PM - 1) / PM;
         const double two = 4.5 + wide_pairs(mb * ((n + PH - 1) / (2 * PH)), half_column(n) ? mb : 0, sms / 2,
-                                            0.49 * nk + 1.8, 0.31 * nk + 1.5);
-        const double one = 4.5 + rounds(mb * ((n + PH - 1) / PH), sms / 2) * (0.31 * nk + 1.5);
+                                            0.46 * nk + 2.4, 0.30 * nk + 1.6);
+        const double one = 4.5 + rounds(mb * ((n + PH - 1) / PH), sms / 2) * (0.30 * nk + 1.6);
         if (one < best.us) best = {1, 0, 1, one};
         if (two < best.us) best = {2, 0, 1, two};
     }

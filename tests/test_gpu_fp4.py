@@ -440,3 +440,26 @@ def test_given_stream_owns_what_a_call_allocates(cuda_lib):
         got = fp8hg.fp4_quant(x, MX, stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(got.codes[:, :1024], want.codes[:, :1024]) and torch.equal(got.scale, want.scale)
+
+
+# (m, n, k): wide tiles dealt over the machine and a last column of half tiles:
+# fewer, one and two rounds of half tiles; one stage of K; a column of exactly
+# half a tile; nothing but half tiles next to one wide column
+HALF_COLUMNS = [(9000, 2000, 2048), (17900, 480, 2000), (5000, 2112, 250), (20000, 576, 700), (30000, 400, 130)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n,k", HALF_COLUMNS)
+def test_product_with_a_half_column(cuda_lib, m, n, k, kind):
+    """Into views of wider tensors at offsets that TMA can and cannot write:
+    the values, and nothing outside."""
+    a, va = stored(m, k, kind, 81)
+    b, vb = stored(n, k, kind, 82)
+    c, s = product(va, vb)
+    for dt, off, extra in ((torch.bfloat16, 8, 24), (torch.bfloat16, 3, 9), (torch.float32, 4, 12)):
+        wide = torch.full((m + 2, n + extra), 7.0, dtype=dt, device="cuda")
+        view = wide[1:m + 1, off:off + n]
+        fp8hg.fp4_gemm_scaled(a, b, out=view)
+        check_product(view, c, s, k)
+        view.fill_(7.0)
+        assert bool((wide == 7.0).all())
