@@ -27,6 +27,7 @@ __device__ __forceinline__ uint32_t abs_max16(const uint32_t (&w)[8]) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max_abs_bf16x2(m, w[i]);
+    m = magnitudes(m);
     return max(m & 0xFFFFu, m >> 16);
 }
 
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(256)
         uint32_t m[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < 32; ++i) m[i >> 4] = max_abs_bf16x2(m[i >> 4], v[i]);
+        m[0] = magnitudes(m[0]), m[1] = magnitudes(m[1]);
         if (!NV) m[0] = m[1] = __vmaxu2(m[0], m[1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

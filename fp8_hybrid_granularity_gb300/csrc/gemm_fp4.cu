@@ -98,7 +98,7 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
 // launch: 8192 x 3584 x 3584 in four rounds of tiles instead of five (NV: 48
 // us instead of 55).
 //
-// The ring of operand stages is short (four stages, 2.4 us of MMAs at best), so
+// The ring of operand stages is short (four stages, 1.6 us of MMAs), so
 // what counts is how soon a stage is used and free again.  Its scales have
 // barriers and a producer of their own and are in tensor memory when it lands:
 // MX 16384 x 3584 x 18944 takes 334 us where a stage's scales come with it and

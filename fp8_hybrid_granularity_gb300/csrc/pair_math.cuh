@@ -35,12 +35,16 @@ __device__ __forceinline__ float warp_max_abs(float m) {
     asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
     return r;
 }
-// Magnitudes of two BF16 pairs, the larger in each half (a NaN if one is).
+// The larger magnitude in each half of two BF16 pairs (a NaN if one is); the
+// sign bits are left over from the operands' (one instruction, where clearing
+// them first takes two).
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) {
     uint32_t r;
-    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.NaN.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w));
     return r;
 }
+// Both halves' magnitudes.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t m) { return m & 0x7FFF7FFFu; }
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     F2 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));

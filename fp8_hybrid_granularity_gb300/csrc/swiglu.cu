@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(256, kFwdThreadsPerSm / 256)
                 mg = max_abs_bf16x2(mg, g[i]);
                 mu = max_abs_bf16x2(mu, u[i]);
             }
+            mg = magnitudes(mg), mu = magnitudes(mu);
             mgu = group_max_u2(max(mg & 0xFFFFu, mg >> 16) | (max(mu & 0xFFFFu, mu >> 16) << 16));
         }
         if (!in || left <= 0) continue;
