@@ -89,24 +89,31 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
 // operand bytes: it takes as many per cycle as an FP8 one and reads a stage in
 // half the time, and an SM gets about 60 bytes a cycle from L2 here.  Single-CTA
 // tiles of 256 x 192 (two accumulators of 128 rows) need 56 KB for the same 768
-// cycles.  At 16384 x 3584 x 18944: 380 us with those tiles (MX; NV 447), 303
-// (350) with these: 7.3 (6.4) PFLOP/s, for which the GPU draws its power limit
-// (a second of it runs at 1.7 GHz; with zeros as operands a call takes 12 %
-// less).
+// cycles.  At 16384 x 3584 x 18944: 380 us with those tiles (MX; NV 447), 297
+// (343) with these: 7.5 (6.5) PFLOP/s, for which the GPU draws its power limit
+// (a second of it runs at 1.7 (1.9) GHz; with zeros as operands a call takes 12
+// (7) % less).
 // NH = 1, where NH = 2 leaves pairs without a tile.
 // A last column of at most 192 columns is computed as half tiles of an NH = 2
-// launch: 8192 x 3584 x 3584 in four rounds of tiles instead of five (NV: 48
-// us instead of 55).
+// launch: 8192 x 3584 x 3584 in four rounds of tiles instead of five (NV, at
+// the time: 48 us instead of 55).
 //
 // The ring of operand stages is short (four stages, 1.6 us of MMAs), so
 // what counts is how soon a stage is used and free again.  Its scales have
 // barriers and a producer of their own and are in tensor memory when it lands:
-// MX 16384 x 3584 x 18944 takes 334 us where a stage's scales come with it and
-// are copied after it.
+// with a stage's scales coming with it and copied after it MX 16384 x 3584 x
+// 18944 took 10 % longer.
+//
+// At a tile's end the MMAs wait until an accumulator is in the epilogue's
+// registers.  The epilogue's warps of both CTAs say so themselves, by a relaxed
+// arrival: no memory is handed over, and a releasing one (cluster scope) first
+// waits for what its SM has under way, 1300 to 2400 cycles of each tile.  So
+// 16384 x 18944 x 3584 takes 357 us instead of 384 (NV), 8192 x 8960 x 1536 54
+// instead of 61.
 //
 // Warps of each CTA: 0 operand producer, 14 scale producer, 4-11 epilogue (a
-// 32-row quarter of one column part each); of the even CTA also 1 MMA issuer and 2, 3, 12, 13 scale
-// copiers, for both CTAs; of the odd CTA 1 forwarder.  Tensor memory: the
+// 32-row quarter of one column part each); of the even CTA also 1 MMA issuer
+// and 2, 3, 12, 13 scale copiers, for both CTAs.  Tensor memory: the
 // accumulators, then the scale slots: per 128 (NV: 64) elements of K four
 // columns for every 128 rows, B's first.
 constexpr int PM = 256, PH = 192, P_THREADS = 512;
@@ -125,10 +132,9 @@ struct PairLayout {
     static constexpr uint32_t OFF_BAR = OFF_EPI + 4 * NH * EPI_BYTES;
     // barriers: full (even CTA: both CTAs' operands), empty (each CTA), sfull
     // (even CTA: both CTAs' scales), scales (each CTA: copied to tensor memory),
-    // tfull[2] and tempty[2] (each CTA), odd[2] (even CTA: the odd one's
-    // tempty), drain[5]
+    // tfull[2] (each CTA), tempty[2] (even CTA: both CTAs' epilogues), drain[5]
     static constexpr uint32_t EMPTY = 8 * S, SFULL = 16 * S, SCALES = 24 * S, TFULL = 32 * S;
-    static constexpr uint32_t TEMPTY = TFULL + 16, ODD = TEMPTY + 16, DRAIN = ODD + 16;
+    static constexpr uint32_t TEMPTY = TFULL + 16, DRAIN = TEMPTY + 16;
     static constexpr uint32_t OFF_MISC = OFF_BAR + 288, SMEM = OFF_MISC + 16 + 1024;
     static constexpr uint32_t GC = 4 * (1 + NB), COLS = GC * NG;   // columns of a scale group, of a slot
     static_assert(DRAIN + 40 <= 288 && OFF_EPI % 1024 == 0 && SMEM <= 232448 && PN + SLOTS * COLS <= 512, "");
@@ -267,7 +273,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     uint8_t *gbase = smem_raw + (base - raw);
     const uint32_t bar = base + L::OFF_BAR;
     const uint32_t empty = bar + L::EMPTY, scales = bar + L::SCALES, sfull = bar + L::SFULL,
-                   tfull = bar + L::TFULL, tempty = bar + L::TEMPTY, odd = bar + L::ODD, drain = bar + L::DRAIN;
+                   tfull = bar + L::TFULL, tempty = bar + L::TEMPTY, drain = bar + L::DRAIN;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + L::OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + L::OFF_MISC + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const PairTiles tiles(p, pair, npairs);
     const uint64_t limit = p.wait_limit_ns, drain_limit = 2000000ull;
     // the even CTA's barriers, as seen from either CTA
-    const uint32_t full_l = ptx::map_shared_rank(bar, 0), sfull_l = full_l + L::SFULL, odd_l = full_l + L::ODD;
+    const uint32_t full_l = ptx::map_shared_rank(bar, 0), sfull_l = full_l + L::SFULL, tempty_l = full_l + L::TEMPTY;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -288,8 +294,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         }
         for (int h = 0; h < 2; ++h) {
             ptx::mbar_init(tfull + 8 * h, 1);
-            ptx::mbar_init(tempty + 8 * h, 4);   // the half's four epilogue warps
-            ptx::mbar_init(odd + 8 * h, 1);
+            ptx::mbar_init(tempty + 8 * h, 8);   // the half's four epilogue warps of each CTA
         }
         for (int i = 0; i < 5; ++i) ptx::mbar_init(drain + 8 * i, 1);
         *abort_flag = 0u;
@@ -334,28 +339,34 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             auto release = [&] {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(tempty + 8 * half);
+                if (lane == 0) ptx::mbar_arrive_relaxed(tempty_l + 8 * half);
             };
             if (p.out_fp32 || p.accumulate) {
 #pragma unroll 1
-                for (int chunk = 0; chunk < PH / 32; ++chunk) {
-                    uint32_t r[32];
-                    ptx::tmem_ld_32x32b_x32(taddr + chunk * 32, r);
-                    ptx::tmem_wait_ld();
-                    if (chunk == PH / 32 - 1) release();
+                for (int part = 0; part < 3; ++part) {
+                    uint32_t r[2][32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                    if (p.c_tma && lane == 0) ptx::bulk_wait_read();
-                    __syncwarp();
-                    stage_row(stage, lane, r);
-                    if (p.c_tma) ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (!p.c_tma) {
-                        write_f32(stage, lane, p, row0, col0 + chunk * 32, vec);
-                    } else if (lane == 0 && row0 < p.M && col0 + chunk * 32 < p.N) {
-                        ptx::tma_store_2d(&tmap_c, ptx::smem_u32(stage), static_cast<int>(col0) + chunk * 32,
-                                          static_cast<int>(row0));
-                        ptx::bulk_commit();
+                    for (int c = 0; c < 2; ++c)
+                        ptx::tmem_ld_32x32b_x32(taddr + (part * (2) + c) * 32, r[c]);
+                    ptx::tmem_wait_ld();
+                    if (part == 2) release();
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int at = (part * (2) + c) * 32;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[c][e] = __float_as_uint(__uint_as_float(r[c][e]) * alpha);
+                        if (p.c_tma && lane == 0) ptx::bulk_wait_read();
+                        __syncwarp();
+                        stage_row(stage, lane, r[c]);
+                        if (p.c_tma) ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (!p.c_tma) {
+                            write_f32(stage, lane, p, row0, col0 + at, vec);
+                        } else if (lane == 0 && row0 < p.M && col0 + at < p.N) {
+                            ptx::tma_store_2d(&tmap_c, ptx::smem_u32(stage), static_cast<int>(col0) + at,
+                                              static_cast<int>(row0));
+                            ptx::bulk_commit();
+                        }
                     }
                 }
                 continue;
@@ -478,7 +489,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 // part h of stage `it`
                 auto issue = [&](int h, bool zero) {
                     const uint32_t s = it % S, st = base + s * L::STAGE, col = tmem + L::PN + it % SLOTS * L::COLS;
-    #pragma unroll
+#pragma unroll
                     for (int j = 0; j < 4; ++j)
                         mma_pair<NV, L, 0>(tmem, col, desc_sw128(st), desc_sw128(st + L::A + h * L::BH), idesc, h,
                                            shift, j, zero && j == 0 ? 0u : 1u);
@@ -491,12 +502,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     ptx::tc_fence_after();
                     return r;
                 };
-                for (int t = 0, mb, nb; ok && (parts = tiles.get<NH>(p, t, mb, nb)) != 0; ++t) {
+                int mb, nb, next = tiles.get<NH>(p, 0, mb, nb);
+                for (int t = 0; ok && next != 0; ++t) {
+                    parts = next;
                     shift = nb * L::PN % 128 / 32;
+                    ok = ready();
                     for (int h = 0; h < parts && ok; ++h) {
-                        ok = wait_phase(tempty + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA) &&
-                             wait_pair(odd + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA) &&
-                             (h != 0 || ready());
+                        ok = wait_pair(tempty + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA);
                         if (!ok) break;
                         ptx::tc_fence_after();
                         issue(h, true);
@@ -504,6 +516,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     }
                     if (!ok) break;
                     ++it;
+                    next = tiles.get<NH>(p, t + 1, mb, nb);   // under the MMAs: its divisions take a while
                     for (int kb = 1; parts == 1 && kb < p.nk - 1; ++kb, ++it) {
                         ok = ready();
                         if (!ok) break;
@@ -515,7 +528,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                         const uint32_t s = it % S;
                         const uint32_t st = base + s * L::STAGE, col = tmem + L::PN + it % SLOTS * L::COLS;
                         const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + L::A);
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             mma_pair<NV, L, 1>(tmem, col, ad, bd, idesc, 0, shift, j, 1u);
                             mma_pair<NV, L, 2>(tmem, col, ad, bd + (L::BH >> 4), idesc, 1, shift, j, 1u);
@@ -533,22 +546,6 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 }
                 ptx::tc_commit_pair(drain, 0x1);
                 wait_phase(drain, 0u, drain_limit, abort_flag, p.err, WHO_MMA, false);
-            }
-            __syncwarp();
-        } else if (warp == 1) {
-            // ------------------------------------------------ forwarder (odd CTA)
-            // Tells the even CTA that this one's accumulators are drained.  An
-            // arrival in the other CTA is a release at cluster scope and waits
-            // for its thread's own stores: from an epilogue warp, with the last
-            // tile's stores in flight, that took 1300 cycles.
-            if (lane == 0) {
-                bool ok = true;
-                for (int i = 0, mb, nb, parts; ok && (parts = tiles.get<NH>(p, i, mb, nb)) != 0; ++i) {
-                    for (int h = 0; h < parts && ok; ++h) {
-                        ok = wait_phase(tempty + 8 * h, i & 1u, limit, abort_flag, p.err, WHO_EPILOGUE);
-                        if (ok) ptx::mbar_arrive_cluster(odd_l + 8 * h);
-                    }
-                }
             }
             __syncwarp();
         } else if ((warp == 2 || warp == 3 || (warp >= 12 && warp < 11 + L::NB)) && leader) {
@@ -573,7 +570,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                         ptx::tc_fence_after();
                         const uint64_t sd = src + s * (L::SF_STAGE >> 4);
                         const uint32_t d = dst + slot * L::COLS;
-    #pragma unroll
+#pragma unroll
                         for (int g = 0; g < L::NG; ++g) ptx::tc_cp_32x128b_warpx4_pair(d + g * L::GC, sd + g * 32);
                         ptx::tc_commit_pair(scales + 8 * s, 0x3);
                     }
