@@ -1063,7 +1063,7 @@ int launch_few(const Fp4GemmArgs &g, Params &p, bool swapped, int splits, cudaSt
 //   pairs        4.5 + rounds (0.46 nk + 2.4) with 384 columns, (0.30 nk + 1.6) with 192
 //   few rows     3.8 + rounds (c nk / splits + e), (c, e) by the tile's columns: 0.29, 0.4 for 16
 //                ... 0.48, 2 for 128
-// So 8192 x 8960 x 1536 takes 57 us with 384 columns and 69 with 192; 1024 x
+// So 8192 x 8960 x 1536 takes 52 us with 384 columns and 55 with 192; 1024 x
 // 3584 x 18944 38 and 29; 256 x 1536 x 8960 16 with pairs and 9.5 with four K
 // parts of few-row tiles; 256 x 18944 x 3584 15 and 26.
 struct Plan {
