@@ -1110,7 +1110,7 @@ Plan choose(int64_t m, int64_t n, int nk, int sms) {
                                             0.46 * nk + 2.4, 0.30 * nk + 1.6);
         const double one = 4.5 + rounds(mb * ((n + PH - 1) / PH), sms / 2) * (0.30 * nk + 1.6);
         if (one < best.us) best = {1, 0, 1, one};
-        if (two < best.us) best = {2, 0, 1, two};
+        if (n > PH && two < best.us) best = {2, 0, 1, two};
     }
     return best;
 }

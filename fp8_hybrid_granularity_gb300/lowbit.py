@@ -62,6 +62,20 @@ _bound = None
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+_cuda_device = torch._C._cuda_getDevice
+# the allocation behind torch.empty without its argument handling: in a row of
+# small calls an output costs the host 1.4 us instead of 4
+_empty_strided = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+_empty_strided = getattr(_empty_strided, "_empty_strided_cuda", None)
+
+
+def _allocator(x):
+    """A function of sizes, strides and type that allocates on x's device."""
+    if _empty_strided is not None and x.get_device() == _cuda_device():
+        return _empty_strided
+    return lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device=x.device)
+
+
 def _on(x):
     """The stream to launch on, x's device's current one (the plain lookup: a
     call takes about as long as ten microseconds' work)."""
@@ -184,10 +198,20 @@ class Fp4Tensor:
 def alloc_fp4(rows: int, k: int, kind: int, tensor_scale=None, device="cuda") -> Fp4Tensor:
     """Output buffers for fp4_quant (codes' rows padded to 16 bytes)."""
     codes = torch.empty((rows, (k + 31) // 32 * 16), dtype=torch.uint8, device=device)
-    per = 512 * (4 if kind == FP4_NV else 2)
-    scale = torch.empty((rows + 127) // 128 * ((k + 255) // 256) * per, dtype=torch.uint8,
-                        device=device)
+    scale = torch.empty(_scale_bytes(rows, k, kind), dtype=torch.uint8, device=device)
     return Fp4Tensor(codes, scale, rows, k, kind, tensor_scale)
+
+
+def _scale_bytes(rows, k, kind) -> int:
+    """fp4_scale_bytes of the library."""
+    return (rows + 127) // 128 * ((k + 255) // 256) * (2048 if kind == FP4_NV else 1024)
+
+
+def _alloc(rows, k, kind, tensor_scale, x) -> Fp4Tensor:
+    """alloc_fp4 on x's device."""
+    new, ld = _allocator(x), (k + 31) // 32 * 16
+    return Fp4Tensor(new((rows, ld), (ld, 1), torch.uint8),
+                     new((_scale_bytes(rows, k, kind),), (1,), torch.uint8), rows, k, kind, tensor_scale)
 
 
 @_streamed
@@ -196,11 +220,11 @@ def fp4_tensor_scale(x, out=None):
     amax <= 6 * 448 * t (1 for a tensor of zeros), on the device."""
     _check_matrix(x)
     f = _fns()
-    out = out if out is not None else torch.empty(1, dtype=torch.float32, device=x.device)
+    out = out if out is not None else _allocator(x)((1,), (1,), torch.float32)
     n = f.fp4_tensor_scale_workspace()
-    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _check(f.fp4_tensor_scale(x.data_ptr(), x.shape[0], x.shape[1], _ld(x), _ts(out), ws.data_ptr(),
-                              n, _on(x)), "fp4_tensor_scale")
+    stream = _on(x)
+    _check(f.fp4_tensor_scale(x.data_ptr(), x.shape[0], x.shape[1], _ld(x), _ts(out),
+                              _scratch(n, x, stream).data_ptr(), n, stream), "fp4_tensor_scale")
     return out
 
 
@@ -228,7 +252,7 @@ def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
     _check_matrix(x)
     rows, cols = (x.shape[1], x.shape[0]) if transpose else x.shape
     if out is None:
-        out = alloc_fp4(rows, cols, kind, tensor_scale, x.device)
+        out = _alloc(rows, cols, kind, tensor_scale, x)
     _check_fp4(out, rows, cols, kind)
     out.tensor_scale = tensor_scale
     _quant(x, kind, tensor_scale, None if transpose else out, out if transpose else None,
@@ -242,8 +266,8 @@ def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Te
     """fp4_quant along the rows and along the columns from one read of x."""
     _check_matrix(x)
     rows, cols = x.shape
-    out = out if out is not None else alloc_fp4(rows, cols, kind, tensor_scale, x.device)
-    out_t = out_t if out_t is not None else alloc_fp4(cols, rows, kind, tensor_scale, x.device)
+    out = out if out is not None else _alloc(rows, cols, kind, tensor_scale, x)
+    out_t = out_t if out_t is not None else _alloc(cols, rows, kind, tensor_scale, x)
     _check_fp4(out, rows, cols, kind)
     _check_fp4(out_t, cols, rows, kind)
     out.tensor_scale = out_t.tensor_scale = tensor_scale
@@ -255,7 +279,7 @@ def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Te
 def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None):
     """The values of a 4-bit tensor, [rows, k], BF16 or FP32."""
     if out is None:
-        out = torch.empty((q.rows, q.k), dtype=out_dtype or torch.bfloat16, device=q.codes.device)
+        out = _allocator(q.codes)((q.rows, q.k), (q.k, 1), out_dtype or torch.bfloat16)
     else:
         _check_out(out, q.rows, q.k)
     op = q.operand()
@@ -271,8 +295,7 @@ def fp4_gemm_scaled(a: Fp4Tensor, b: Fp4Tensor, out=None, out_dtype=None, accumu
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((a.rows, b.rows), dtype=out_dtype or torch.bfloat16,
-                          device=a.codes.device)
+        out = _allocator(a.codes)((a.rows, b.rows), (b.rows, 1), out_dtype or torch.bfloat16)
     else:
         _check_out(out, a.rows, b.rows)
     oa, ob = a.operand(), b.operand()
@@ -294,7 +317,7 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
         raise ValueError(f"x has {x.shape[1]} columns, w {w.k}")
     rows = x.shape[0]
     if out is None:
-        out = torch.empty((rows, w.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
+        out = _allocator(x)((rows, w.rows), (w.rows, 1), out_dtype or torch.bfloat16)
     else:
         _check_out(out, rows, w.rows)
     stream = _on(x)
@@ -311,8 +334,7 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
 
 def _linear_bytes(rows, k, kind) -> int:
     """fp4_linear_workspace of the library for more than four rows."""
-    return (rows * ((k + 31) // 32 * 16) +
-            (rows + 127) // 128 * ((k + 255) // 256) * (2048 if kind == FP4_NV else 1024))
+    return rows * ((k + 31) // 32 * 16) + _scale_bytes(rows, k, kind)
 
 
 _scratch_of = threading.local()
@@ -347,20 +369,13 @@ class SwigluCkpt:
     up: QTensor
 
 
-def _codes(rows, cols, device):
-    """[rows, cols] bytes, rows padded to 16."""
-    if cols % 16:
-        return torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.uint8,
-                                   device=device)
-    return torch.empty((rows, cols), dtype=torch.uint8, device=device)
-
-
-def _groups(rows, cols, fmt, device):
-    """[rows, cols] codes (rows padded to 16 bytes) and their 1x128 scales."""
+def _groups(rows, cols, fmt, new):
+    """[rows, cols] codes (rows padded to 16 bytes) and their 1x128 scales; new:
+    from _allocator."""
     g = (cols + 127) // 128
-    return QTensor(_codes(rows, cols, device),
-                   torch.empty((rows, _round4(g)), dtype=torch.uint8, device=device), fmt,
-                   GRAN_1x128, g)
+    ls = _round4(g)
+    return QTensor(new((rows, cols), ((cols + 15) // 16 * 16, 1), torch.uint8),
+                   new((rows, ls), (ls, 1), torch.uint8), fmt, GRAN_1x128, g)
 
 
 def _ld_codes(q) -> int:
@@ -376,24 +391,21 @@ def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bo
     (inference) writes h alone and returns (h, None)."""
     _check_matrix(gate, "gate")
     _check_matrix(up, "up")
-    if gate.shape != up.shape or _ld(gate) != _ld(up):
+    ld_in = _ld(gate)
+    if gate.shape != up.shape or ld_in != _ld(up):
         raise ValueError("gate and up must have the same shape and row stride")
     rows, cols = gate.shape
-    dev, n, ld = gate.device, (cols + 127) // 128, (cols + 15) // 16 * 16
-    ls = _round4(n)
-    h, sh = _codes(rows, cols, dev), torch.empty((rows, ls), dtype=torch.uint8, device=dev)
-    ptr = (None, None, None, None)
+    ld, new = (cols + 15) // 16 * 16, _allocator(gate)
+    h = _groups(rows, cols, fmt_h, new)
+    ckpt, ptr, ls = None, (None, None, None, None), h.scale.shape[1]
     if checkpoint:
-        g, sg = _codes(rows, cols, dev), torch.empty((rows, ls), dtype=torch.uint8, device=dev)
-        u, su = _codes(rows, cols, dev), torch.empty((rows, ls), dtype=torch.uint8, device=dev)
-        ptr = (g.data_ptr(), sg.data_ptr(), u.data_ptr(), su.data_ptr())
-    _check(_fns().fp8_swiglu_ckpt(gate.data_ptr(), up.data_ptr(), rows, cols, _ld(gate), fmt_h,
-                                  h.data_ptr(), ld, sh.data_ptr(), ls, fmt, *ptr, ld, ls,
+        g, u = _groups(rows, cols, fmt, new), _groups(rows, cols, fmt, new)
+        ptr = (g.codes.data_ptr(), g.scale.data_ptr(), u.codes.data_ptr(), u.scale.data_ptr())
+        ckpt = SwigluCkpt(g, u)
+    _check(_fns().fp8_swiglu_ckpt(gate.data_ptr(), up.data_ptr(), rows, cols, ld_in, fmt_h,
+                                  h.codes.data_ptr(), ld, h.scale.data_ptr(), ls, fmt, *ptr, ld, ls,
                                   _on(gate)), "fp8_swiglu_ckpt")
-    h = QTensor(h, sh, fmt_h, GRAN_1x128, n)
-    if not checkpoint:
-        return h, None
-    return h, SwigluCkpt(QTensor(g, sg, fmt, GRAN_1x128, n), QTensor(u, su, fmt, GRAN_1x128, n))
+    return h, ckpt
 
 
 def _ckpt(c: SwigluCkpt, dh) -> _Ckpt:
@@ -418,7 +430,7 @@ def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None):
     c = _ckpt(ckpt, dh)
     rows, cols = dh.shape
     if out is None:
-        out = torch.empty((rows, 2 * cols), dtype=torch.bfloat16, device=dh.device)
+        out = _allocator(dh)((rows, 2 * cols), (2 * cols, 1), torch.bfloat16)
     else:
         _check_out(out, rows, 2 * cols)
         _check_matrix(out, "out")
@@ -437,10 +449,10 @@ def fp8_swiglu_ckpt_bwd_q(dh, ckpt: SwigluCkpt, fmt: int = E5M2, fmt_t: int = E5
     must be multiples of 128."""
     c = _ckpt(ckpt, dh)
     rows, cols = dh.shape
-    dev = dh.device
-    d = _groups(rows, 2 * cols, fmt, dev)
-    t = _groups(2 * cols, rows, fmt_t, dev)
-    h = _groups(cols, rows, fmt_h, dev)
+    new = _allocator(dh)
+    d = _groups(rows, 2 * cols, fmt, new)
+    t = _groups(2 * cols, rows, fmt_t, new)
+    h = _groups(cols, rows, fmt_h, new)
     dq, ds, tq, tl = d.codes.data_ptr(), d.scale.data_ptr(), t.codes.data_ptr(), t.scale.data_ptr()
     ld_qt, ld_st = t.codes.stride(0), t.scale.stride(0)
     g = _Grads(dq, dq + cols, ds, ds + cols // 128, tq, tq + cols * ld_qt, tl, tl + cols * ld_st,
