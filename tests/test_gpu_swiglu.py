@@ -305,3 +305,32 @@ def test_on_another_stream_and_in_a_graph(cuda_lib):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("rows,cols", [(2048, 3840), (3968, 640), (128, 32768)])
+def test_backward_quantized_over_many_tiles(cuda_lib, rows, cols):
+    """More tiles than SMs, several per CTA: every stripe of 128 tokens comes out
+    as it does alone (where no CTA has more than one tile to hand on)."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    rand = lambda: (torch.randn((rows, cols), generator=g, device="cuda") *
+                    torch.exp(2 * torch.randn((rows, 1), generator=g, device="cuda"))).bfloat16()
+    dh = rand()
+    _, ck = fp8hg.fp8_swiglu_ckpt(rand(), rand())
+    d, t, h = fp8hg.fp8_swiglu_ckpt_bwd_q(dh, ck)
+    step = 128 if rows > 128 else 0
+    for r in range(0, rows, 128):
+        for c in range(0, cols, cols if step else 4096):
+            n = cols if step else 4096
+            part = fp8hg.SwigluCkpt(*(fp8hg.QTensor(q.codes[r:r + 128, c:c + n], q.scale[r:r + 128, c // 128:], q.fmt,
+                                                    q.gran, n // 128) for q in (ck.gate, ck.up)))
+            d1, t1, h1 = fp8hg.fp8_swiglu_ckpt_bwd_q(dh[r:r + 128, c:c + n], part)
+            for half in (0, 1):
+                at, to = half * cols + c, half * n
+                assert torch.equal(d.codes[r:r + 128, at:at + n], d1.codes[:, to:to + n])
+                assert torch.equal(d.scales()[r:r + 128, at // 128:(at + n) // 128],
+                                   d1.scales()[:, to // 128:(to + n) // 128])
+                assert torch.equal(t.codes[at:at + n, r:r + 128], t1.codes[to:to + n])
+                assert torch.equal(t.scales()[at:at + n, r // 128:r // 128 + 1], t1.scales()[to:to + n])
+            assert torch.equal(h.codes[c:c + n, r:r + 128], h1.codes)
+            assert torch.equal(h.scales()[c:c + n, r // 128:r // 128 + 1], h1.scales())
+    assert fp8hg.fp8hg_get_device_error() == 0
