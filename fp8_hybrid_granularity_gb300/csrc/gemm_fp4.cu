@@ -89,8 +89,8 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
 // operand bytes: it takes as many per cycle as an FP8 one and reads a stage in
 // half the time, and an SM gets about 60 bytes a cycle from L2 here.  Single-CTA
 // tiles of 256 x 192 (two accumulators of 128 rows) need 56 KB for the same 768
-// cycles.  At 16384 x 3584 x 18944: 380 us with those tiles (MX; NV 447), 297
-// (343) with these: 7.5 (6.5) PFLOP/s, for which the GPU draws its power limit
+// cycles.  At 16384 x 3584 x 18944: 380 us with those tiles (MX; NV 447), 296
+// (337) with these: 7.5 (6.6) PFLOP/s, for which the GPU draws its power limit
 // (a second of it runs at 1.7 (1.9) GHz; with zeros as operands a call takes 12
 // (7) % less).
 // NH = 1, where NH = 2 leaves pairs without a tile.
@@ -102,7 +102,11 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
 // what counts is how soon a stage is used and free again.  Its scales have
 // barriers and a producer of their own and are in tensor memory when it lands:
 // with a stage's scales coming with it and copied after it MX 16384 x 3584 x
-// 18944 took 10 % longer.
+// 18944 took 10 % longer.  NV has tensor memory for two stages of scales, so the
+// second next stage's are copied while the next one's MMAs run, which is just
+// too short (with two slots instead of four MX takes as long as NV).  Filling
+// half a slot at a time gains NV 4 % where K is long and loses 2 to 4 % where a
+// tile has less than ten stages: the MMA thread waits twice a stage.
 //
 // At a tile's end the MMAs wait until an accumulator is in the epilogue's
 // registers.  The epilogue's warps of both CTAs say so themselves, by a relaxed
@@ -130,8 +134,9 @@ struct PairLayout {
     static constexpr uint32_t STAGE = A + NH * BH, SF_STAGE = (1 + NB) * SF;   // A's rows, then B's
     static constexpr uint32_t OFF_SF = S * STAGE, OFF_EPI = OFF_SF + S * SF_STAGE;
     static constexpr uint32_t OFF_BAR = OFF_EPI + 4 * NH * EPI_BYTES;
-    // barriers: full (even CTA: both CTAs' operands), empty (each CTA), sfull
-    // (even CTA: both CTAs' scales), scales (each CTA: copied to tensor memory),
+    // barriers: full (even CTA: both CTAs' operands, and their scales in tensor
+    // memory), empty (each CTA), sfull (even CTA: both CTAs' scales), scales
+    // (each CTA: copied to tensor memory),
     // tfull[2] (each CTA), tempty[2] (even CTA: both CTAs' epilogues), drain[5]
     static constexpr uint32_t EMPTY = 8 * S, SFULL = 16 * S, SCALES = 24 * S, TFULL = 32 * S;
     static constexpr uint32_t TEMPTY = TFULL + 16, DRAIN = TEMPTY + 16;
@@ -287,10 +292,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(bar + 8 * s, 1);
+            ptx::mbar_init(bar + 8 * s, 2 + L::NB);      // the bytes and the scale copiers
             ptx::mbar_init(empty + 8 * s, 1);
             ptx::mbar_init(sfull + 8 * s, 1);
-            ptx::mbar_init(scales + 8 * s, 1 + L::NB);   // the copiers
+            ptx::mbar_init(scales + 8 * s, 1 + L::NB);
         }
         for (int h = 0; h < 2; ++h) {
             ptx::mbar_init(tfull + 8 * h, 1);
@@ -496,9 +501,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     if (h == parts - 1) ptx::tc_commit_pair(empty + 8 * s, 0x3);
                 };
                 auto ready = [&] {
-                    const uint32_t s = 8 * (it % S), parity = (it / S) & 1u;
-                    const bool r = wait_phase(scales + s, parity, limit, abort_flag, p.err, WHO_MMA) &&
-                                   wait_pair(bar + s, parity, limit, abort_flag, p.err, WHO_MMA);
+                    const bool r = wait_pair(bar + 8 * (it % S), (it / S) & 1u, limit, abort_flag, p.err, WHO_MMA);
                     ptx::tc_fence_after();
                     return r;
                 };
@@ -572,7 +575,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                         const uint32_t d = dst + slot * L::COLS;
 #pragma unroll
                         for (int g = 0; g < L::NG; ++g) ptx::tc_cp_32x128b_warpx4_pair(d + g * L::GC, sd + g * 32);
-                        ptx::tc_commit_pair(scales + 8 * s, 0x3);
+                        ptx::tc_commit_pair(bar + 8 * s, 0x1);      // for the MMAs
+                        ptx::tc_commit_pair(scales + 8 * s, 0x3);   // for the scale producers
                     }
                 }
                 ptx::tc_commit_pair(drain + 8 * (row + 1), 0x1);
