@@ -59,13 +59,14 @@ constexpr int kRowThreadsPerSm = 1280;   // 48 registers a thread
 
 template <bool NV, bool WIDE>
 __global__ void __launch_bounds__(256, kRowThreadsPerSm / 256)
-    k_fp4_rows(const uint16_t *__restrict__ x, uint32_t rows, int cols, uint32_t ld_x,
-               const float *__restrict__ ts, uint8_t *__restrict__ q, uint32_t ld_q,
-               uint8_t *__restrict__ s, uint32_t tiles, int segs, int total_segs) {
+    k_fp4_rows(const uint16_t *x, uint32_t rows, int cols, uint32_t ld_x,
+               const float *ts, uint8_t *q, uint32_t ld_q,
+               uint8_t *s, uint32_t tiles, int segs, int total_segs) {
+    ptx::grid_begin();
     const int tid = threadIdx.x, lane = tid & 31;
     const int seg = blockIdx.y * segs + tid % segs;
     const int rpb = blockDim.x / segs;
-    const float t = NV && ts ? __ldg(ts) : 1.0f, rt = fp4_reciprocal<NV>(t);
+    const float t = NV && ts ? ptx::ld_f32(ts) : 1.0f, rt = fp4_reciprocal<NV>(t);
     const int c0 = seg * 16;
     constexpr int LPB = NV ? 1 : 2;
     // The next row's load is in flight while a row is cast: a CTA per row
@@ -111,10 +112,11 @@ constexpr int kTile = 128;
 
 template <bool NV, bool WIDE, bool ROWS>
 __global__ void __launch_bounds__(256)
-    k_fp4_tile(const uint16_t *__restrict__ x, int rows, int cols, uint32_t ld_x,
-               const float *__restrict__ ts, uint8_t *__restrict__ q, uint32_t ld_q,
-               uint8_t *__restrict__ s, uint32_t tiles, uint8_t *__restrict__ qt, uint32_t ld_qt,
-               uint8_t *__restrict__ st, uint32_t tiles_t) {
+    k_fp4_tile(const uint16_t *x, int rows, int cols, uint32_t ld_x,
+               const float *ts, uint8_t *q, uint32_t ld_q,
+               uint8_t *s, uint32_t tiles, uint8_t *qt, uint32_t ld_qt,
+               uint8_t *st, uint32_t tiles_t) {
+    ptx::grid_begin();
     constexpr int NT = NV ? 2 : 1;          // scale tiles of 4 blocks per 128 elements
     constexpr int LPB = NV ? 1 : 2;
     __shared__ __align__(16) uint8_t tile[kTile * 256];
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(256)
     __shared__ __align__(16) uint8_t scales[2][NT * 512];
     const int tid = threadIdx.x, lane = tid & 31;
     const int r0 = blockIdx.y * kTile, k0 = blockIdx.x * kTile;
-    const float t = NV && ts ? __ldg(ts) : 1.0f, rt = fp4_reciprocal<NV>(t);
+    const float t = NV && ts ? ptx::ld_f32(ts) : 1.0f, rt = fp4_reciprocal<NV>(t);
     {
         const int seg = tid & 7;
         const int c0 = k0 + seg * 16;
@@ -237,8 +239,9 @@ constexpr int kAmaxCtasPerSm = 4;
 // Largest finite |x| pattern per CTA.
 template <bool WIDE>
 __global__ void __launch_bounds__(512, kAmaxCtasPerSm)
-    k_fp4_amax(const uint16_t *__restrict__ x, int rows, int segs, int cols, uint32_t ld_x,
-               uint32_t *__restrict__ part) {
+    k_fp4_amax(const uint16_t *x, int rows, int segs, int cols, uint32_t ld_x,
+               uint32_t *part) {
+    ptx::grid_begin();
     __shared__ uint32_t red[16];
     uint32_t m = 0;
     // segments of 16 elements, rows and segments walked together
@@ -277,10 +280,11 @@ __global__ void __launch_bounds__(512, kAmaxCtasPerSm)
 }
 
 __global__ void __launch_bounds__(32)
-    k_fp4_tensor_scale(const uint32_t *__restrict__ part, int n, float *__restrict__ scale) {
+    k_fp4_tensor_scale(const uint32_t *part, int n, float *scale) {
+    ptx::grid_begin();
     uint32_t m = 0;
 #pragma unroll 8
-    for (int i = threadIdx.x; i < n; i += 32) m = max(m, part[i]);
+    for (int i = threadIdx.x; i < n; i += 32) m = max(m, ptx::ld_u32(part + i));
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if (threadIdx.x == 0) {
         // 2688 = 1.3125 * 2^11, a mantissa field of 40: the power of two goes
@@ -296,10 +300,11 @@ constexpr int kDequantThreadsPerSm = 1536;   // 40 registers a thread
 
 template <bool NV, bool FP32, bool WIDE>
 __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
-    k_fp4_dequant(const uint8_t *__restrict__ q, const uint8_t *__restrict__ s,
-                  const float *__restrict__ ts, uint32_t rows, int k, uint32_t ld, uint32_t tiles,
-                  void *__restrict__ out, uint32_t ld_out, int segs) {
-    const float t = NV && ts ? __ldg(ts) : 1.0f;
+    k_fp4_dequant(const uint8_t *q, const uint8_t *s,
+                  const float *ts, uint32_t rows, int k, uint32_t ld, uint32_t tiles,
+                  void *out, uint32_t ld_out, int segs) {
+    ptx::grid_begin();
+    const float t = NV && ts ? ptx::ld_f32(ts) : 1.0f;
     const int g = blockIdx.y * blockDim.x + threadIdx.x;
     const int c0 = g * 16, left = k - c0;
     // the next row's codes and scale are in flight while a row is written
@@ -309,13 +314,13 @@ __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
         if (r >= rows || g >= segs) return;
         const uint8_t *src = q + row_at(r, ld) + c0 / 2;
         if (left >= 16) {
-            next = __ldg(reinterpret_cast<const uint2 *>(src));
+            next = ptx::ld_v2(src);
         } else {
             uint64_t v = 0;
-            for (int i = 0; i < (left + 1) / 2; ++i) v |= static_cast<uint64_t>(__ldg(src + i)) << (8 * i);
+            for (int i = 0; i < (left + 1) / 2; ++i) v |= static_cast<uint64_t>(ptx::ld_u8(src + i)) << (8 * i);
             next = make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
         }
-        next_scale = __ldg(s + fp4_scale_offset(r, NV ? g : g >> 1, tiles));
+        next_scale = ptx::ld_u8(s + fp4_scale_offset(r, NV ? g : g >> 1, tiles));
     };
     load(blockIdx.x);
     for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -382,15 +387,8 @@ cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
     const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kRowThreadsPerSm / threads) / cblocks);
     const dim3 grid(static_cast<unsigned>(std::min(rblocks, resident)), static_cast<unsigned>(cblocks));
     const int64_t tiles = fp4_scale_tiles(a.cols, a.kind);
-    if (ragged::wide(a.x, a.ld_x))
-        k_fp4_rows<NV, true><<<grid, threads, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
-                                                           a.ld_q, a.s, tiles, segs,
-                                                           static_cast<int>(total));
-    else
-        k_fp4_rows<NV, false><<<grid, threads, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
-                                                            a.ld_q, a.s, tiles, segs,
-                                                            static_cast<int>(total));
-    return cudaGetLastError();
+    return launch_after(ragged::wide(a.x, a.ld_x) ? k_fp4_rows<NV, true> : k_fp4_rows<NV, false>, grid, threads, 0,
+                        stream, 1, a.x, a.rows, a.cols, a.ld_x, a.ts, a.q, a.ld_q, a.s, tiles, segs, total);
 }
 
 template <bool NV, bool WIDE>
@@ -399,15 +397,8 @@ cudaError_t quant_tile(const Fp4QuantArgs &a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>((a.cols + 255LL) / 256 * 2),
                     static_cast<unsigned>((a.rows + 255LL) / 256 * 2));
     const int64_t tiles = fp4_scale_tiles(a.cols, a.kind), tiles_t = fp4_scale_tiles(a.rows, a.kind);
-    if (a.q)
-        k_fp4_tile<NV, WIDE, true><<<grid, 256, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts, a.q,
-                                                            a.ld_q, a.s, tiles, a.qt, a.ld_qt, a.st,
-                                                            tiles_t);
-    else
-        k_fp4_tile<NV, WIDE, false><<<grid, 256, 0, stream>>>(a.x, a.rows, a.cols, a.ld_x, a.ts,
-                                                             a.q, a.ld_q, a.s, tiles, a.qt, a.ld_qt,
-                                                             a.st, tiles_t);
-    return cudaGetLastError();
+    return launch_after(a.q ? k_fp4_tile<NV, WIDE, true> : k_fp4_tile<NV, WIDE, false>, grid, 256, 0, stream, 1, a.x,
+                        a.rows, a.cols, a.ld_x, a.ts, a.q, a.ld_q, a.s, tiles, a.qt, a.ld_qt, a.st, tiles_t);
 }
 
 }  // namespace
@@ -422,12 +413,12 @@ cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int rows, int cols, uint3
                                      static_cast<int64_t>(kAmaxBlocks)});
     uint32_t *part = static_cast<uint32_t *>(ws);
     if (n > 0) {
-        const unsigned g = static_cast<unsigned>(blocks);
-        if (ragged::wide(x, ld_x)) k_fp4_amax<true><<<g, 512, 0, stream>>>(x, rows, segs, cols, ld_x, part);
-        else k_fp4_amax<false><<<g, 512, 0, stream>>>(x, rows, segs, cols, ld_x, part);
+        const cudaError_t e = launch_after(ragged::wide(x, ld_x) ? k_fp4_amax<true> : k_fp4_amax<false>,
+                                           static_cast<unsigned>(blocks), 512, 0, stream, 1, x, rows, segs, cols, ld_x,
+                                           part);
+        if (e != cudaSuccess) return e;
     }
-    k_fp4_tensor_scale<<<1, 32, 0, stream>>>(part, static_cast<int>(blocks), scale);
-    return cudaGetLastError();
+    return launch_after(k_fp4_tensor_scale, 1, 32, 0, stream, 1, part, blocks, scale);
 }
 
 cudaError_t launch_fp4_quant(const Fp4QuantArgs &a, cudaStream_t stream) {
@@ -449,10 +440,8 @@ cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, uint32_t ld_out, 
     const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kDequantThreadsPerSm / threads) / cb);
     const dim3 grid(static_cast<unsigned>(std::min(a.rows, resident)), static_cast<unsigned>(cb));
     auto go = [&](auto kern) {
-        kern<<<grid, threads, 0, stream>>>(a.codes, a.scale, a.ts, static_cast<uint32_t>(a.rows),
-                                           static_cast<int>(a.k), static_cast<uint32_t>(a.ld),
-                                           static_cast<uint32_t>(tiles), out, ld_out, static_cast<int>(segs));
-        return cudaGetLastError();
+        return launch_after(kern, grid, threads, 0, stream, 1, a.codes, a.scale, a.ts, a.rows, a.k, a.ld, tiles, out,
+                            ld_out, segs);
     };
     const bool nv = a.kind == FP4_NV;
     if (fp32) {

@@ -313,6 +313,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
         ptx::tmem_relinquish_pair();
     }
+    // The kernel after this one is not launched early: its CTAs, though they only
+    // wait, slow this one down (8192 x 8960 x 1536 backward, a quantizer and two
+    // products: 126 us against 116).
+    ptx::grid_wait();
     ptx::tc_fence_before();
     ptx::cluster_sync();   // both CTAs' barriers and tensor memory exist
     ptx::tc_fence_after();
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         ptx::setmaxnreg_inc<168>();
         const int q = warp & 3, half = (warp - 4) >> 2;
         uint8_t *stage = gbase + L::OFF_EPI + (warp - 4) * EPI_BYTES;
-        const float alpha = (p.ta ? __ldg(p.ta) : 1.0f) * (p.tb ? __ldg(p.tb) : 1.0f);
+        const float alpha = (p.ta ? ptx::ld_f32(p.ta) : 1.0f) * (p.tb ? ptx::ld_f32(p.tb) : 1.0f);
         // a C that is added to, four values at a time (without `accumulate` such a C is TMA's)
         const bool vec = p.accumulate && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % 4 == 0;
         for (int i = 0, mb, nb; tiles.get<NH>(p, i, mb, nb) > half; ++i) {
@@ -716,8 +720,10 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         ptx::mbar_init(drain + 8, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
-        for (int it = 0; it < 2 && it < n; ++it) load_stage(it);
     }
+    ptx::grid_begin();
+    if (threadIdx.x == 0)
+        for (int it = 0; it < 2 && it < n; ++it) load_stage(it);
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::TCOLS);
         ptx::tmem_relinquish();
@@ -806,7 +812,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             // or twice, and the instruction fetch of an unrolled one took
             // longer than what it saved.
             const int tid = threadIdx.x - 128;
-            const float t = NV && p.tb ? __ldg(p.tb) : 1.0f, rt = fp4_reciprocal<NV>(t);
+            const float t = NV && p.tb ? ptx::ld_f32(p.tb) : 1.0f, rt = fp4_reciprocal<NV>(t);
             const bool wide = (reinterpret_cast<uintptr_t>(qi.x) & 31) == 0 && (qi.ld & 15) == 0;
             auto load = [&](int idx, uint32_t (&w)[8]) {
                 const int row = (idx >> 4) & ((1 << lr) - 1), it = idx >> (4 + lr);
@@ -891,7 +897,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         __syncthreads();
     }
     if (!*abort_flag) {
-        const float alpha = (p.ta ? __ldg(p.ta) : 1.0f) * (p.tb ? __ldg(p.tb) : 1.0f);
+        const float alpha = (p.ta ? ptx::ld_f32(p.ta) : 1.0f) * (p.tb ? ptx::ld_f32(p.tb) : 1.0f);
         // this CTA's rows, one to a thread group's lane; columns go round the
         // groups
         const float *sum = reinterpret_cast<const float *>(gbase + L::OFF_SUM);
@@ -992,19 +998,7 @@ uint32_t instruction(bool nv, int m, int n) {
 template <class K, class... Args>
 int launch_cluster(K kern, int64_t ctas, int cluster, int threads, uint32_t smem, cudaStream_t stream,
                    const Args &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    const cudaError_t e = launch_after(kern, static_cast<unsigned>(ctas), threads, smem, stream, cluster, args...);
     return e == cudaSuccess ? 0 : 2 + static_cast<int>(e);
 }
 

@@ -97,6 +97,29 @@ struct SwigluGrads {
 cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c,
                                 const SwigluGrads &g, cudaStream_t stream);
 
+// Launches a kernel that begins with ptx::grid_begin() or grid_wait(), under the
+// end of the stream's last kernel where that allows it: 1 to 2 us less from one
+// kernel to the next.  cluster > 1: that many CTAs in a cluster.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                         const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Offset of a row.
 __host__ __device__ inline int64_t row_at(uint32_t row, uint32_t ld) {
     return static_cast<int64_t>(static_cast<uint64_t>(row) * ld);

@@ -464,6 +464,50 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
     return r;
 }
 
+// A kernel that is launched under the end of the one before it in its stream
+// (programmatic serialization) begins with grid_wait: from there on all of that
+// kernel's work is done and visible.  grid_begin also allows the next kernel to
+// be launched under this one.  What such a kernel reads can change while it is
+// already resident: it is read with ordinary loads, not as constant for the
+// kernel's life (ld.global.nc).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_begin() {
+    grid_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ uint4 ld_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+// Past L1: read once.
+__device__ __forceinline__ uint4 ld_once_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_v2(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_u32(const void *p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_f32(const float *p) { return __uint_as_float(ld_u32(p)); }
+__device__ __forceinline__ uint32_t ld_u8(const uint8_t *p) {
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 // Streaming 16-byte global load that does not allocate in L1.
 __device__ __forceinline__ uint4 ld_stream_v4(const void *p) {
     uint4 v;

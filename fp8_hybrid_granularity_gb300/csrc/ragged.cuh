@@ -42,10 +42,11 @@ __device__ __forceinline__ void shift_down(uint32_t (&w)[12], uint32_t b) {
 template <bool WIDE>
 __device__ __forceinline__ void load16(const uint16_t *p, int left, uint32_t (&v)[8]) {
     if (WIDE && left >= 16) {
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
                        "=r"(v[6]), "=r"(v[7])
-                     : "l"(p));
+                     : "l"(p)
+                     : "memory");
         return;
     }
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
@@ -56,7 +57,7 @@ __device__ __forceinline__ void load16(const uint16_t *p, int left, uint32_t (&v
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (s + bytes > 16u * i) q = __ldg(g + i);
+        if (s + bytes > 16u * i) q = ptx::ld_v4(g + i);
         w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
     shift_down(w, s);

@@ -46,13 +46,13 @@ __device__ __forceinline__ void store_bytes16(uint8_t *p, const uint32_t (&c)[4]
 
 __device__ __forceinline__ void load_bytes16(const uint8_t *p, int left, uint32_t (&c)[4]) {
     if (left >= 16) {
-        const uint4 v = ptx::ld_stream_v4(p);
+        const uint4 v = ptx::ld_once_v4(p);
         c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
     } else {
         c[0] = c[1] = c[2] = c[3] = 0u;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (i < left) c[i >> 2] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i & 3));
+            if (i < left) c[i >> 2] |= ptx::ld_u8(p + i) << (8 * (i & 3));
     }
 }
 
@@ -138,6 +138,7 @@ constexpr int kFwdThreadsPerSm = 768;   // 80 registers a thread
 template <int FH, int FC, bool CKPT, bool WIDE>
 __global__ void __launch_bounds__(256, kFwdThreadsPerSm / 256)
     k_swiglu_fwd(const SwigluFwdArgs a, int segs, int total_segs) {
+    ptx::grid_begin();
     const int tid = threadIdx.x;
     const int seg = blockIdx.y * segs + tid % segs;
     const int rpb = blockDim.x / segs;
@@ -217,8 +218,9 @@ __device__ __forceinline__ void swiglu_grads(F2 g, F2 u, F2 dh, F2 &dg, F2 &du, 
 
 template <int FC, bool WIDE>
 __global__ void __launch_bounds__(256)
-    k_swiglu_bwd(const uint16_t *__restrict__ dh, uint32_t ld_dh, const SwigluCkpt c,
-                 uint16_t *__restrict__ dg, uint16_t *__restrict__ du, uint32_t ld_d, int segs) {
+    k_swiglu_bwd(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt c,
+                 uint16_t *dg, uint16_t *du, uint32_t ld_d, int segs) {
+    ptx::grid_begin();
     // a warp takes 32 neighbouring segments of one row, whole warps past the
     // row's end included: the stores exchange values between lanes
     const int seg = (blockIdx.y * blockDim.x + threadIdx.x);
@@ -231,8 +233,8 @@ __global__ void __launch_bounds__(256)
             ragged::load16<WIDE>(dh + row_at(r, ld_dh) + c0, left, w);
             load_bytes16(c.gq + at, left, gc);
             load_bytes16(c.uq + at, left, uc);
-            const F2 sg = f2(scale_pow2(__ldg(c.gs + sat)));
-            const F2 su = f2(scale_pow2(__ldg(c.us + sat)));
+            const F2 sg = f2(scale_pow2(ptx::ld_u8(c.gs + sat)));
+            const F2 su = f2(scale_pow2(ptx::ld_u8(c.us + sat)));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 F2 g[2], u[2];
@@ -324,15 +326,15 @@ __device__ __forceinline__ void load_tile(TileIn &t, const uint16_t *dh, uint32_
         ragged::load16<true>(src, 16, t.dh);
     } else {
         const uint4 *p = reinterpret_cast<const uint4 *>(src);
-        const uint4 a = __ldg(p), b = __ldg(p + 1);
+        const uint4 a = ptx::ld_v4(p), b = ptx::ld_v4(p + 1);
         t.dh[0] = a.x, t.dh[1] = a.y, t.dh[2] = a.z, t.dh[3] = a.w;
         t.dh[4] = b.x, t.dh[5] = b.y, t.dh[6] = b.z, t.dh[7] = b.w;
     }
     const int64_t at = row_at(r, c.ld_q) + col, sat = row_at(r, c.ld_s) + kb;
     load_bytes16(c.gq + at, 16, t.g);
     load_bytes16(c.uq + at, 16, t.u);
-    t.sg = __ldg(c.gs + sat);
-    t.su = __ldg(c.us + sat);
+    t.sg = ptx::ld_u8(c.gs + sat);
+    t.su = ptx::ld_u8(c.us + sat);
 }
 
 // Attempts of one wait (each suspends the warp for a while): seconds.
@@ -340,7 +342,7 @@ constexpr uint32_t kTries = 1u << 22;
 
 template <int FC, int FR, int FT, int FH, bool WIDE>
 __global__ void __launch_bounds__(Q_THREADS, 1)
-    k_swiglu_bwd_q(const uint16_t *__restrict__ dh, uint32_t ld_dh, const SwigluCkpt c, const SwigluGrads o,
+    k_swiglu_bwd_q(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt c, const SwigluGrads o,
                    uint32_t kbs, uint32_t rbs, uint32_t step_k, uint32_t step_r, unsigned int *err) {
     extern __shared__ __align__(16) float plane[];
     __shared__ __align__(8) uint64_t bars[6];
@@ -355,6 +357,7 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
         ptx::fence_mbar_init();
     }
     __syncthreads();
+    ptx::grid_begin();
     // every warp waits for and arrives at every barrier, once a tile
     auto wait = [&](uint32_t which, uint32_t parity) {
         if (ptx::mbar_try_wait(which, parity)) return true;
@@ -381,7 +384,8 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
             const uint32_t r = next_r * kT + (tid & 127), k0 = next_k * kT;
             const void *p = warp < 8    ? static_cast<const void *>(dh + row_at(r, ld_dh) + k0 + (tid >> 7) * 64)
                             : warp < 16 ? static_cast<const void *>((warp < 12 ? c.gq : c.uq) + row_at(r, c.ld_q) + k0)
-                                        : static_cast<const void *>((warp < 20 ? c.gs : c.us) + row_at(r, c.ld_s) + next_k);
+                                        : static_cast<const void *>((warp < 20 ? c.gs : c.us) + row_at(r, c.ld_s) +
+                                                                    next_k);
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
         }
         {
@@ -477,11 +481,9 @@ cudaError_t fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
     // as many CTAs as fit at once
     const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kFwdThreadsPerSm / threads) / cb);
     const dim3 grid(static_cast<unsigned>(std::min(rb, resident)), static_cast<unsigned>(cb));
-    if (ragged::wide(a.gate, a.ld_in) && ragged::wide(a.up, a.ld_in))
-        k_swiglu_fwd<FH, FC, CKPT, true><<<grid, threads, 0, stream>>>(a, segs, static_cast<int>(total));
-    else
-        k_swiglu_fwd<FH, FC, CKPT, false><<<grid, threads, 0, stream>>>(a, segs, static_cast<int>(total));
-    return cudaGetLastError();
+    const bool wide = ragged::wide(a.gate, a.ld_in) && ragged::wide(a.up, a.ld_in);
+    return launch_after(wide ? k_swiglu_fwd<FH, FC, CKPT, true> : k_swiglu_fwd<FH, FC, CKPT, false>, grid, threads, 0,
+                        stream, 1, a, segs, total);
 }
 
 template <int FH>
@@ -504,8 +506,7 @@ cudaError_t launch_swiglu_bwd(const uint16_t *dh, uint32_t ld_dh, const SwigluCk
     const dim3 grid(static_cast<unsigned>(c.rows), static_cast<unsigned>((segs + threads - 1) / threads));
     const bool wide = ragged::wide(dh, ld_dh) && ragged::wide(dg, ld_d) && ragged::wide(du, ld_d);
     auto go = [&](auto kern) {
-        kern<<<grid, threads, 0, stream>>>(dh, ld_dh, c, dg, du, ld_d, static_cast<int>(segs));
-        return cudaGetLastError();
+        return launch_after(kern, grid, threads, 0, stream, 1, dh, ld_dh, c, dg, du, ld_d, segs);
     };
     if (c.fmt == FMT_E4M3) return wide ? go(k_swiglu_bwd<FMT_E4M3, true>) : go(k_swiglu_bwd<FMT_E4M3, false>);
     return wide ? go(k_swiglu_bwd<FMT_E5M2, true>) : go(k_swiglu_bwd<FMT_E5M2, false>);
@@ -525,11 +526,8 @@ cudaError_t bwd_q(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c, const
     auto go = [&](auto kern) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmem);
         if (e != cudaSuccess) return e;
-        kern<<<grid, Q_THREADS, kQSmem, stream>>>(dh, ld_dh, c, g, static_cast<uint32_t>(kbs),
-                                                   static_cast<uint32_t>(c.rows / kT),
-                                                   grid % static_cast<uint32_t>(kbs),
-                                                   grid / static_cast<uint32_t>(kbs), g.err);
-        return cudaGetLastError();
+        return launch_after(kern, grid, Q_THREADS, kQSmem, stream, 1, dh, ld_dh, c, g, kbs, c.rows / kT, grid % kbs,
+                            grid / kbs, g.err);
     };
     return ragged::wide(dh, ld_dh) ? go(k_swiglu_bwd_q<FC, FR, FT, FH, true>)
                                    : go(k_swiglu_bwd_q<FC, FR, FT, FH, false>);

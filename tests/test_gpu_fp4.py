@@ -463,3 +463,46 @@ def test_product_with_a_half_column(cuda_lib, m, n, k, kind):
         check_product(view, c, s, k)
         view.fill_(7.0)
         assert bool((wide == 7.0).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(3, 520), (64, 1024), (700, 1536)])
+def test_calls_in_a_row_see_each_others_results(cuda_lib, rows, cols, kind):
+    """Kernels are launched under the end of the one before: every call of a
+    chain without a pause, over the same few buffers, gives what it gives alone."""
+    n = 24
+    xs = [gpu(data(rows, cols, 900 + i)) for i in range(n)]
+    w, _ = stored(256, cols, kind, 91)
+    x = torch.empty_like(xs[0])
+    ts = torch.ones(1, device="cuda") if kind == NV else None
+    q, qt = fp8hg.alloc_fp4(rows, cols, kind), fp8hg.alloc_fp4(cols, rows, kind)
+
+    def chain(src, out):
+        x.copy_(src)                       # a kernel that is not the library's
+        if kind == NV:
+            fp8hg.fp4_tensor_scale(x, out=ts)
+        fp8hg.fp4_quant_dual(x, kind, ts, out=q, out_t=qt)
+        fp8hg.fp4_dequant(q, out=x)        # in place of its own source
+        fp8hg.fp4_dequant(qt, out=out[0])
+        fp8hg.fp4_linear(x, w, ts, out=out[1])
+        fp8hg.fp4_quant(x, kind, ts, out=q)
+        fp8hg.fp4_gemm_scaled(q, w, out=out[2])
+        h, _ = fp8hg.fp8_swiglu_ckpt(out[1][:, :128], out[1][:, 128:])
+        out[3].copy_(h.codes)
+
+    def outputs():
+        e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")
+        return [e(cols, rows), e(rows, 256), e(rows, 256), torch.empty((rows, 128), dtype=torch.uint8, device="cuda")]
+    want = []
+    for src in xs:
+        want.append(outputs())
+        torch.cuda.synchronize()
+        chain(src, want[-1])
+        torch.cuda.synchronize()
+    got = [outputs() for _ in xs]
+    torch.cuda.synchronize()
+    for src, out in zip(xs, got):
+        chain(src, out)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(a, b))
