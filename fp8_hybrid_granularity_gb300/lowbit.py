@@ -128,10 +128,15 @@ def _fns():
     return _bound
 
 
-def _check_matrix(x, what="x"):
-    if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 2 or (x.stride(1) != 1 and
-                                                                      x.shape[1] > 1):
-        raise ValueError(f"{what} must be a 2-D CUDA bfloat16 tensor with unit column stride")
+def _matrix(x, what="x"):
+    """Rows, columns and row stride of a BF16 input."""
+    if x.dtype == torch.bfloat16 and x.is_cuda and x.dim() == 2:
+        rows, cols = x.shape
+        ld, unit = x.stride()
+        if unit == 1 or cols <= 1:
+            # a tensor of one row or none may carry any row stride
+            return rows, cols, ld if rows > 1 else max(ld, cols)
+    raise ValueError(f"{what} must be a 2-D CUDA bfloat16 tensor with unit column stride")
 
 
 def _ld(x) -> int:
@@ -218,12 +223,12 @@ def _alloc(rows, k, kind, tensor_scale, x) -> Fp4Tensor:
 def fp4_tensor_scale(x, out=None):
     """The FP4_NV scale of a tensor: the smallest power of two t with
     amax <= 6 * 448 * t (1 for a tensor of zeros), on the device."""
-    _check_matrix(x)
+    rows, cols, ld = _matrix(x)
     f = _fns()
     out = out if out is not None else _allocator(x)((1,), (1,), torch.float32)
     n = f.fp4_tensor_scale_workspace()
     stream = _on(x)
-    _check(f.fp4_tensor_scale(x.data_ptr(), x.shape[0], x.shape[1], _ld(x), _ts(out),
+    _check(f.fp4_tensor_scale(x.data_ptr(), rows, cols, ld, _ts(out),
                               _scratch(n, x, stream).data_ptr(), n, stream), "fp4_tensor_scale")
     return out
 
@@ -231,11 +236,10 @@ def fp4_tensor_scale(x, out=None):
 _NONE = (None, 0, None)
 
 
-def _quant(x, kind, tensor_scale, rows_out, cols_out, what):
+def _quant(x, shape, kind, tensor_scale, rows_out, cols_out, what):
     q = (rows_out.codes.data_ptr(), rows_out.ld(), rows_out.scale.data_ptr()) if rows_out else _NONE
     t = (cols_out.codes.data_ptr(), cols_out.ld(), cols_out.scale.data_ptr()) if cols_out else _NONE
-    rows, cols = x.shape
-    _check(_fns().fp4_quant(x.data_ptr(), rows, cols, _ld(x), kind, _ts(tensor_scale), *q, *t,
+    _check(_fns().fp4_quant(x.data_ptr(), *shape, kind, _ts(tensor_scale), *q, *t,
                             _on(x)), what)
 
 
@@ -249,13 +253,13 @@ def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
               out: Optional[Fp4Tensor] = None) -> Fp4Tensor:
     """BF16 [rows, cols] to 4 bits along the rows, or (transpose=True) along the
     columns, written as [cols, rows]."""
-    _check_matrix(x)
-    rows, cols = (x.shape[1], x.shape[0]) if transpose else x.shape
+    shape = _matrix(x)
+    rows, cols = (shape[1], shape[0]) if transpose else shape[:2]
     if out is None:
         out = _alloc(rows, cols, kind, tensor_scale, x)
     _check_fp4(out, rows, cols, kind)
     out.tensor_scale = tensor_scale
-    _quant(x, kind, tensor_scale, None if transpose else out, out if transpose else None,
+    _quant(x, shape, kind, tensor_scale, None if transpose else out, out if transpose else None,
            "fp4_quant")
     return out
 
@@ -264,14 +268,14 @@ def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
 def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Tensor] = None,
                    out_t: Optional[Fp4Tensor] = None):
     """fp4_quant along the rows and along the columns from one read of x."""
-    _check_matrix(x)
-    rows, cols = x.shape
+    shape = _matrix(x)
+    rows, cols = shape[:2]
     out = out if out is not None else _alloc(rows, cols, kind, tensor_scale, x)
     out_t = out_t if out_t is not None else _alloc(cols, rows, kind, tensor_scale, x)
     _check_fp4(out, rows, cols, kind)
     _check_fp4(out_t, cols, rows, kind)
     out.tensor_scale = out_t.tensor_scale = tensor_scale
-    _quant(x, kind, tensor_scale, out, out_t, "fp4_quant_dual")
+    _quant(x, shape, kind, tensor_scale, out, out_t, "fp4_quant_dual")
     return out, out_t
 
 
@@ -312,21 +316,21 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
     """y = x w^T: x [rows, k] BF16 is quantized like w and multiplied, in one
     call.  workspace: optional uint8 tensor of fp4_linear_workspace(...)
     bytes (allocated per call if None; up to 4 rows none is needed)."""
-    _check_matrix(x)
-    if x.shape[1] != w.k:
-        raise ValueError(f"x has {x.shape[1]} columns, w {w.k}")
-    rows = x.shape[0]
+    rows, k, ld = _matrix(x)
+    if k != w.k:
+        raise ValueError(f"x has {k} columns, w {w.k}")
     if out is None:
-        out = _allocator(x)((rows, w.rows), (w.rows, 1), out_dtype or torch.bfloat16)
+        out, ld_out = _allocator(x)((rows, w.rows), (w.rows, 1), out_dtype or torch.bfloat16), w.rows
     else:
         _check_out(out, rows, w.rows)
+        ld_out = _ld(out)
     stream = _on(x)
-    n = 0 if rows <= 4 else _linear_bytes(rows, w.k, w.kind)
+    n = 0 if rows <= 4 else _linear_bytes(rows, k, w.kind)
     if n and workspace is None:
         workspace = _scratch(n, x, stream)
     ow = w.operand()
-    _check(_fns().fp4_linear(x.data_ptr(), rows, _ld(x), _ts(tensor_scale), ctypes.byref(ow),
-                             out.data_ptr(), _ld(out), _out_kind(out),
+    _check(_fns().fp4_linear(x.data_ptr(), rows, ld, _ts(tensor_scale), ctypes.byref(ow),
+                             out.data_ptr(), ld_out, _out_kind(out),
                              workspace.data_ptr() if n else None, workspace.numel() if n else 0,
                              _opts(wait_limit_ns, inject_fault), stream), "fp4_linear")
     return out
@@ -389,12 +393,9 @@ def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bo
     operand), and gate and up quantized the same way for the backward pass.
     gate and up may be the two halves of one tensor.  checkpoint=False
     (inference) writes h alone and returns (h, None)."""
-    _check_matrix(gate, "gate")
-    _check_matrix(up, "up")
-    ld_in = _ld(gate)
-    if gate.shape != up.shape or ld_in != _ld(up):
+    shape = rows, cols, ld_in = _matrix(gate, "gate")
+    if _matrix(up, "up") != shape:
         raise ValueError("gate and up must have the same shape and row stride")
-    rows, cols = gate.shape
     ld, new = (cols + 15) // 16 * 16, _allocator(gate)
     h = _groups(rows, cols, fmt_h, new)
     ckpt, ptr, ls = None, (None, None, None, None), h.scale.shape[1]
@@ -408,34 +409,33 @@ def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bo
     return h, ckpt
 
 
-def _ckpt(c: SwigluCkpt, dh) -> _Ckpt:
+def _ckpt(c: SwigluCkpt, dh):
+    """The checkpoint for the library; dh's rows, columns and row stride."""
     g, u = c.gate, c.up
-    _check_matrix(dh, "dh")
+    shape = rows, cols, _ = _matrix(dh, "dh")
     if g.gran != GRAN_1x128 or u.gran != GRAN_1x128 or g.fmt != u.fmt:
         raise ValueError("a checkpoint has 1x128 scales and one format")
-    if g.codes.shape != dh.shape or u.codes.shape != dh.shape:
+    if g.codes.shape != (rows, cols) or u.codes.shape != (rows, cols):
         raise ValueError("dh and the checkpoint must have the same shape")
-    if (_ld_codes(g.codes) != _ld_codes(u.codes) or
-            (g.codes.shape[0] > 1 and g.scale.stride(0) != u.scale.stride(0))):
+    ld, ls = _ld_codes(g.codes), g.scale.stride(0)
+    if ld != _ld_codes(u.codes) or (rows > 1 and ls != u.scale.stride(0)):
         raise ValueError("gate's and up's codes and scales must have the same strides")
-    rows, cols = dh.shape
     return _Ckpt(g.codes.data_ptr(), g.scale.data_ptr(), u.codes.data_ptr(), u.scale.data_ptr(),
-                 rows, cols, _ld_codes(g.codes), g.scale.stride(0), g.fmt, 0)
+                 rows, cols, ld, ls, g.fmt, 0), shape
 
 
 @_streamed
 def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None):
     """Gradients of gate and up from dh [rows, cols] and the checkpoint, BF16:
     one [rows, 2 cols] tensor, dgate in the first half, dup in the second."""
-    c = _ckpt(ckpt, dh)
-    rows, cols = dh.shape
+    c, (rows, cols, ld) = _ckpt(ckpt, dh)
     if out is None:
-        out = _allocator(dh)((rows, 2 * cols), (2 * cols, 1), torch.bfloat16)
+        out, ld_out = _allocator(dh)((rows, 2 * cols), (2 * cols, 1), torch.bfloat16), 2 * cols
     else:
         _check_out(out, rows, 2 * cols)
-        _check_matrix(out, "out")
-    _check(_fns().fp8_swiglu_ckpt_bwd(dh.data_ptr(), _ld(dh), ctypes.byref(c), out.data_ptr(),
-                                      out.data_ptr() + 2 * cols, _ld(out), _on(dh)),
+        ld_out = _matrix(out, "out")[2]
+    to = out.data_ptr()
+    _check(_fns().fp8_swiglu_ckpt_bwd(dh.data_ptr(), ld, ctypes.byref(c), to, to + 2 * cols, ld_out, _on(dh)),
            "fp8_swiglu_ckpt_bwd")
     return out
 
@@ -447,8 +447,7 @@ def fp8_swiglu_ckpt_bwd_q(dh, ckpt: SwigluCkpt, fmt: int = E5M2, fmt_t: int = E5
     to dup; the same transposed, [2 cols, rows], per 128 tokens; h rebuilt from
     the checkpoint and transposed, [cols, rows], per 128 tokens).  rows and cols
     must be multiples of 128."""
-    c = _ckpt(ckpt, dh)
-    rows, cols = dh.shape
+    c, (rows, cols, ld) = _ckpt(ckpt, dh)
     new = _allocator(dh)
     d = _groups(rows, 2 * cols, fmt, new)
     t = _groups(2 * cols, rows, fmt_t, new)
@@ -458,6 +457,6 @@ def fp8_swiglu_ckpt_bwd_q(dh, ckpt: SwigluCkpt, fmt: int = E5M2, fmt_t: int = E5
     g = _Grads(dq, dq + cols, ds, ds + cols // 128, tq, tq + cols * ld_qt, tl, tl + cols * ld_st,
                h.codes.data_ptr(), h.scale.data_ptr(), d.codes.stride(0), d.scale.stride(0), ld_qt,
                ld_st, fmt, fmt_t, fmt_h, 0)
-    _check(_fns().fp8_swiglu_ckpt_bwd_q(dh.data_ptr(), _ld(dh), ctypes.byref(c), ctypes.byref(g),
-                                        _on(dh)), "fp8_swiglu_ckpt_bwd_q")
+    _check(_fns().fp8_swiglu_ckpt_bwd_q(dh.data_ptr(), ld, ctypes.byref(c), ctypes.byref(g), _on(dh)),
+           "fp8_swiglu_ckpt_bwd_q")
     return d, t, h
