@@ -1,6 +1,12 @@
 // 4-bit quantizer kernels: BF16 -> E2M1 codes and block scales, the tensor
-// scale, and back to values.  All are bound by HBM: 2 bytes read and about
-// 0.53 (MX) or 0.56 (NV) written per element and direction.
+// scale, and back to values.  Their floor is HBM: 2 bytes read and about 0.53
+// (MX) or 0.56 (NV) written per element and direction; beside it stand issue
+// slots, 11 (NV along the rows) and 17 (NV both ways) instructions per element.
+// At 8192 x 8960, in us and of the measured copy rate:
+//   rows        MX 32 (86 %)   NV 33 (85 %)
+//   both ways   MX 41 (82 %)   NV 48 (71 %)
+//   values      MX 33 (83 %)   NV 31 (90 %)
+//   tensor scale               24 (90 %), its second launch included
 //
 //  k_fp4_rows    along the rows: a thread takes 16 elements (an NV block, or
 //                half an MX block, whose other half is in the next lane), so
@@ -107,7 +113,8 @@ __global__ void __launch_bounds__(256, kRowThreadsPerSm / 256)
 // neighbouring columns over 32 rows (conflict-free 4-byte reads).  Codes of
 // the columns go through shared memory so that a column's 64 bytes leave as
 // whole sectors.  Scale tiles (128 rows x 4 blocks) are assembled in shared
-// memory as well.
+// memory as well.  With 512 threads a tile, half as much for each, it takes 54 us
+// instead of 48 (NV, 8192 x 8960).
 constexpr int kTile = 128;
 
 template <bool NV, bool WIDE, bool ROWS>

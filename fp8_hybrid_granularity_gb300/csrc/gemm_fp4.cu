@@ -614,7 +614,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 // K: no quantization pass before the product, no codes in memory.
 //
 // What bounds a call of one token is latency: the 36 MB (MX) of 18944 x 3584
-// weights take 5.4 us from memory, the call 9.8 us with x quantized on the way.
+// weights take 5.4 us from memory, the call 8.8 us with x quantized on the way
+// (NV 5.7 and 10.5).
 // So the first stages' copies are issued before the other warps have started.
 constexpr int F_THREADS = 256;
 template <bool NV, int BN>
@@ -1143,8 +1144,10 @@ int launch(const Fp4GemmArgs &g, int sms, cudaStream_t stream) {
 }  // namespace
 
 // Quantizing inside the product, every CTA for itself, against a quantization
-// pass before it (18944 x 3584, NV, microseconds): 11.6 and 13.9 for one row,
-// 12.9 and 14.2 for four, 15.3 and 13.9 for eight.
+// pass before it (microseconds): 18944 x 3584 NV 10.5 and 12.1 for one row, 11.6
+// and 12.3 for four (MX 8.8 and 9.6, 11.5 and 10.3); 1536 x 8960 NV 6.7 and 7.3
+// for four.  At eight rows it takes longer (by 10 %).  The host launches once
+// instead of twice.
 bool fp4_linear_quantizes(int64_t rows) { return rows <= 4; }
 
 int launch_fp4_gemm(const Fp4GemmArgs &g, cudaStream_t stream) {
