@@ -90,7 +90,7 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
 // half the time, and an SM gets about 60 bytes a cycle from L2 here.  Single-CTA
 // tiles of 256 x 192 (two accumulators of 128 rows) need 56 KB for the same 768
 // cycles.  At 16384 x 3584 x 18944: 380 us with those tiles (MX; NV 447), 296
-// (337) with these: 7.5 (6.6) PFLOP/s, for which the GPU draws its power limit
+// (327) with these: 7.5 (6.8) PFLOP/s, for which the GPU draws its power limit
 // (a second of it runs at 1.7 (1.9) GHz; with zeros as operands a call takes 12
 // (7) % less).
 // NH = 1, where NH = 2 leaves pairs without a tile.
@@ -104,9 +104,7 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
 // with a stage's scales coming with it and copied after it MX 16384 x 3584 x
 // 18944 took 10 % longer.  NV has tensor memory for two stages of scales, so the
 // second next stage's are copied while the next one's MMAs run, which is just
-// too short (with two slots instead of four MX takes as long as NV).  Filling
-// half a slot at a time gains NV 4 % where K is long and loses 2 to 4 % where a
-// tile has less than ten stages: the MMA thread waits twice a stage.
+// too short (with two slots instead of four MX takes as long as NV); SUB below.
 //
 // At a tile's end the MMAs wait until an accumulator is in the epilogue's
 // registers.  The epilogue's warps of both CTAs say so themselves, by a relaxed
@@ -136,13 +134,14 @@ struct PairLayout {
     static constexpr uint32_t OFF_BAR = OFF_EPI + 4 * NH * EPI_BYTES;
     // barriers: full (even CTA: both CTAs' operands, and their scales in tensor
     // memory), empty (each CTA), sfull (even CTA: both CTAs' scales), scales
-    // (each CTA: copied to tensor memory),
+    // (each CTA: copied to tensor memory), rest (even CTA: the second half of a
+    // stage's scales copied),
     // tfull[2] (each CTA), tempty[2] (even CTA: both CTAs' epilogues), drain[5]
-    static constexpr uint32_t EMPTY = 8 * S, SFULL = 16 * S, SCALES = 24 * S, TFULL = 32 * S;
+    static constexpr uint32_t EMPTY = 8 * S, SFULL = 16 * S, SCALES = 24 * S, REST = 32 * S, TFULL = 40 * S;
     static constexpr uint32_t TEMPTY = TFULL + 16, DRAIN = TEMPTY + 16;
-    static constexpr uint32_t OFF_MISC = OFF_BAR + 288, SMEM = OFF_MISC + 16 + 1024;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + 320, SMEM = OFF_MISC + 16 + 1024;
     static constexpr uint32_t GC = 4 * (1 + NB), COLS = GC * NG;   // columns of a scale group, of a slot
-    static_assert(DRAIN + 40 <= 288 && OFF_EPI % 1024 == 0 && SMEM <= 232448 && PN + SLOTS * COLS <= 512, "");
+    static_assert(DRAIN + 40 <= 320 && OFF_EPI % 1024 == 0 && SMEM <= 232448 && PN + SLOTS * COLS <= 512, "");
     static_assert(SLOTS <= S, "a slot is freed by its stage's barrier");
     static_assert(A % 1024 == 0 && BH % 1024 == 0, "the swizzle repeats every 1 KB");
 };
@@ -266,7 +265,11 @@ struct PairTiles {
     }
 };
 
-template <bool NV, int NH>
+// SUB = 2 (NV): the MMAs of a stage's first half wait only for that half's
+// scales.  With two slots (see above) the copies into a slot begin when the stage
+// before last is done and are on the way of the next MMAs; the second wait costs
+// the MMA thread some 75 cycles a stage.
+template <bool NV, int NH, int SUB>
 __global__ void __launch_bounds__(P_THREADS, 1)
     k_fp4_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
     const uint32_t bar = base + L::OFF_BAR;
-    const uint32_t empty = bar + L::EMPTY, scales = bar + L::SCALES, sfull = bar + L::SFULL,
+    const uint32_t empty = bar + L::EMPTY, scales = bar + L::SCALES, sfull = bar + L::SFULL, rest = bar + L::REST,
                    tfull = bar + L::TFULL, tempty = bar + L::TEMPTY, drain = bar + L::DRAIN;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + L::OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + L::OFF_MISC + 4);
@@ -296,6 +299,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             ptx::mbar_init(empty + 8 * s, 1);
             ptx::mbar_init(sfull + 8 * s, 1);
             ptx::mbar_init(scales + 8 * s, 1 + L::NB);
+            ptx::mbar_init(rest + 8 * s, 1 + L::NB);
         }
         for (int h = 0; h < 2; ++h) {
             ptx::mbar_init(tfull + 8 * h, 1);
@@ -509,11 +513,17 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     ptx::tc_fence_after();
                     return r;
                 };
+                auto ready_rest = [&] {
+                    if (SUB == 1) return true;
+                    const bool r = wait_phase(rest + 8 * (it % S), (it / S) & 1u, limit, abort_flag, p.err, WHO_MMA);
+                    ptx::tc_fence_after();
+                    return r;
+                };
                 int mb, nb, next = tiles.get<NH>(p, 0, mb, nb);
                 for (int t = 0; ok && next != 0; ++t) {
                     parts = next;
                     shift = nb * L::PN % 128 / 32;
-                    ok = ready();
+                    ok = ready() && ready_rest();
                     for (int h = 0; h < parts && ok; ++h) {
                         ok = wait_pair(tempty + 8 * h, (t & 1u) ^ 1u, limit, abort_flag, p.err, WHO_MMA);
                         if (!ok) break;
@@ -525,7 +535,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     ++it;
                     next = tiles.get<NH>(p, t + 1, mb, nb);   // under the MMAs: its divisions take a while
                     for (int kb = 1; parts == 1 && kb < p.nk - 1; ++kb, ++it) {
-                        ok = ready();
+                        ok = ready() && ready_rest();
                         if (!ok) break;
                         issue(0, false);
                     }
@@ -537,6 +547,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                         const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + L::A);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
+                            if (SUB == 2 && j == 2) {
+                                ok = ready_rest();
+                                if (!ok) break;
+                            }
                             mma_pair<NV, L, 1>(tmem, col, ad, bd, idesc, 0, shift, j, 1u);
                             mma_pair<NV, L, 2>(tmem, col, ad, bd + (L::BH >> 4), idesc, 1, shift, j, 1u);
                         }
@@ -544,7 +558,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     }
                     if (p.nk == 1) continue;
                     for (int h = 0; h < parts && ok; ++h) {
-                        ok = h != 0 || ready();
+                        ok = h != 0 || (ready() && ready_rest());
                         if (!ok) break;
                         issue(h, false);
                         ptx::tc_commit_pair(tfull + 8 * h, 0x3);
@@ -578,8 +592,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                         const uint64_t sd = src + s * (L::SF_STAGE >> 4);
                         const uint32_t d = dst + slot * L::COLS;
 #pragma unroll
-                        for (int g = 0; g < L::NG; ++g) ptx::tc_cp_32x128b_warpx4_pair(d + g * L::GC, sd + g * 32);
-                        ptx::tc_commit_pair(bar + 8 * s, 0x1);      // for the MMAs
+                        for (int g = 0; g < L::NG; ++g) {
+                            ptx::tc_cp_32x128b_warpx4_pair(d + g * L::GC, sd + g * 32);
+                            if (g == L::NG / SUB - 1) ptx::tc_commit_pair(bar + 8 * s, 0x1);   // for the MMAs
+                        }
+                        if (SUB == 2) ptx::tc_commit_pair(rest + 8 * s, 0x1);
                         ptx::tc_commit_pair(scales + 8 * s, 0x3);   // for the scale producers
                     }
                 }
@@ -978,8 +995,9 @@ cudaError_t allow_smem(K kern, uint32_t bytes) {
 }
 template <bool NV>
 cudaError_t set_attributes() {
-    cudaError_t e = allow_smem(k_fp4_pair<NV, 2>, PairLayout<NV, 2>::SMEM);
-    if (e == cudaSuccess) e = allow_smem(k_fp4_pair<NV, 1>, PairLayout<NV, 1>::SMEM);
+    cudaError_t e = allow_smem(k_fp4_pair<NV, 2, 1>, PairLayout<NV, 2>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_pair<NV, 2, NV ? 2 : 1>, PairLayout<NV, 2>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_pair<NV, 1, 1>, PairLayout<NV, 1>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 16, false>, FewLayout<NV, 16>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 16, true>, FewLayout<NV, 16>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 32, false>, FewLayout<NV, 32>::SMEM);
@@ -1021,7 +1039,7 @@ void set_operands(Params &p, const Fp4GemmArgs &g, bool swapped, int tm, int tn)
 // Whether the last column of 384-column tiles has at most 192 of them.
 bool half_column(int64_t n) { return n % (2 * PH) != 0 && n % (2 * PH) <= PH; }
 
-template <bool NV, int NH>
+template <bool NV, int NH, int SUB>
 int launch_pair(const Fp4GemmArgs &g, Params &p, int sms, cudaStream_t stream) {
     using L = PairLayout<NV, NH>;
     set_operands(p, g, false, PM, L::PN);
@@ -1036,8 +1054,8 @@ int launch_pair(const Fp4GemmArgs &g, Params &p, int sms, cudaStream_t stream) {
     tc = tsb;   // not used unless c_tma
     p.c_tma = !p.accumulate && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % (p.out_fp32 ? 4 : 8) == 0 &&
               make_out_tmap(&tc, p);
-    return launch_cluster(k_fp4_pair<NV, NH>, 2 * std::min<int64_t>(tiles, sms / 2), 2, P_THREADS, L::SMEM, stream, ta,
-                          tb, tsa, tsb, tc, p, instruction(NV, PM, PH));
+    return launch_cluster(k_fp4_pair<NV, NH, SUB>, 2 * std::min<int64_t>(tiles, sms / 2), 2, P_THREADS, L::SMEM, stream,
+                          ta, tb, tsa, tsb, tc, p, instruction(NV, PM, PH));
 }
 
 template <bool NV, int BN, bool QUANT>
@@ -1131,8 +1149,12 @@ int launch(const Fp4GemmArgs &g, int sms, cudaStream_t stream) {
     }
     const bool swapped = g.a.rows <= g.b.rows;
     const Plan plan = choose(g.a.rows, g.b.rows, p.nk, sms);
-    if (plan.nh == 2) return launch_pair<NV, 2>(g, p, sms, stream);
-    if (plan.nh == 1) return launch_pair<NV, 1>(g, p, sms, stream);
+    // NV, a stage's scales in two halves: 16384 x 3584 x 18944 327 us against 338,
+    // 8192 x 18944 x 3584 (14 stages) 178 against 181, but 8192 x 8960 x 1536 (6)
+    // 54 against 53 and 3584 x 18944 x 1000 (4) 37 against 36
+    if (plan.nh == 2 && NV && p.nk >= 12) return launch_pair<NV, 2, NV ? 2 : 1>(g, p, sms, stream);
+    if (plan.nh == 2) return launch_pair<NV, 2, 1>(g, p, sms, stream);
+    if (plan.nh == 1) return launch_pair<NV, 1, 1>(g, p, sms, stream);
     switch (plan.bn) {
     case 16: return launch_few<NV, 16, false>(g, p, swapped, plan.splits, stream);
     case 32: return launch_few<NV, 32, false>(g, p, swapped, plan.splits, stream);

@@ -399,7 +399,7 @@ def test_python_refusals(cuda_lib):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("m,n,k", [(4, 2000, 4096), (100, 400, 2048), (3000, 3000, 1024)])
+@pytest.mark.parametrize("m,n,k", [(4, 2000, 4096), (100, 400, 2048), (3000, 3000, 1024), (5000, 2304, 4000)])
 def test_product_timeout(cuda_lib, m, n, k, kind):
     """A withheld copy and a short limit: the call returns, the status reads
     TIMEOUT once, and the next call is right."""
@@ -445,7 +445,8 @@ def test_given_stream_owns_what_a_call_allocates(cuda_lib):
 # (m, n, k): wide tiles dealt over the machine and a last column of half tiles:
 # fewer, one and two rounds of half tiles; one stage of K; a column of exactly
 # half a tile; nothing but half tiles next to one wide column
-HALF_COLUMNS = [(9000, 2000, 2048), (17900, 480, 2000), (5000, 2112, 250), (20000, 576, 700), (30000, 400, 130)]
+HALF_COLUMNS = [(9000, 2000, 2048), (17900, 480, 2000), (5000, 2112, 250), (20000, 576, 700), (30000, 400, 130),
+                (5000, 2400, 4000)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
