@@ -104,7 +104,7 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
 // with a stage's scales coming with it and copied after it MX 16384 x 3584 x
 // 18944 took 10 % longer.  NV has tensor memory for two stages of scales, so the
 // second next stage's are copied while the next one's MMAs run, which is just
-// too short (with two slots instead of four MX takes as long as NV); SUB below.
+// too short (with two slots instead of four MX takes as long as NV); see SUB.
 //
 // At a tile's end the MMAs wait until an accumulator is in the epilogue's
 // registers.  The epilogue's warps of both CTAs say so themselves, by a relaxed
@@ -127,6 +127,12 @@ struct PairLayout {
     static constexpr int NB = NH == 2 ? 3 : 2; // 128-row scale tiles that a tile's columns touch
     static constexpr int S = NH == 2 ? 4 : 6;
     static constexpr int SLOTS = NH == 2 && NV ? 2 : NH == 2 ? 4 : S;
+    // Parts of a stage's scales that the MMAs wait for separately.  With two slots
+    // the copies into one begin when the stage before last is done and are in the
+    // way of the next MMAs: in halves 16384 x 3584 x 18944 takes 327 us instead of
+    // 338, 8192 x 18944 x 3584 178 instead of 181; the second wait costs the MMA
+    // thread some 75 cycles a stage, 3584 x 18944 x 1000 37 us instead of 36.
+    static constexpr int SUB = SLOTS == 2 ? 2 : 1;
     static constexpr uint32_t SF = NG * 512;
     static constexpr uint32_t A = 128 * kStageBytes, BH = PH / 2 * kStageBytes;
     static constexpr uint32_t STAGE = A + NH * BH, SF_STAGE = (1 + NB) * SF;   // A's rows, then B's
@@ -265,17 +271,13 @@ struct PairTiles {
     }
 };
 
-// SUB = 2 (NV): the MMAs of a stage's first half wait only for that half's
-// scales.  With two slots (see above) the copies into a slot begin when the stage
-// before last is done and are on the way of the next MMAs; the second wait costs
-// the MMA thread some 75 cycles a stage.
-template <bool NV, int NH, int SUB>
+template <bool NV, int NH>
 __global__ void __launch_bounds__(P_THREADS, 1)
     k_fp4_pair(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
                const __grid_constant__ CUtensorMap tmap_c, const Params p, const uint32_t idesc) {
     using L = PairLayout<NV, NH>;
-    constexpr int S = L::S, SLOTS = L::SLOTS;
+    constexpr int S = L::S, SLOTS = L::SLOTS, SUB = L::SUB;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
@@ -995,9 +997,8 @@ cudaError_t allow_smem(K kern, uint32_t bytes) {
 }
 template <bool NV>
 cudaError_t set_attributes() {
-    cudaError_t e = allow_smem(k_fp4_pair<NV, 2, 1>, PairLayout<NV, 2>::SMEM);
-    if (e == cudaSuccess) e = allow_smem(k_fp4_pair<NV, 2, NV ? 2 : 1>, PairLayout<NV, 2>::SMEM);
-    if (e == cudaSuccess) e = allow_smem(k_fp4_pair<NV, 1, 1>, PairLayout<NV, 1>::SMEM);
+    cudaError_t e = allow_smem(k_fp4_pair<NV, 2>, PairLayout<NV, 2>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_fp4_pair<NV, 1>, PairLayout<NV, 1>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 16, false>, FewLayout<NV, 16>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 16, true>, FewLayout<NV, 16>::SMEM);
     if (e == cudaSuccess) e = allow_smem(k_fp4_few<NV, 32, false>, FewLayout<NV, 32>::SMEM);
@@ -1039,7 +1040,7 @@ void set_operands(Params &p, const Fp4GemmArgs &g, bool swapped, int tm, int tn)
 // Whether the last column of 384-column tiles has at most 192 of them.
 bool half_column(int64_t n) { return n % (2 * PH) != 0 && n % (2 * PH) <= PH; }
 
-template <bool NV, int NH, int SUB>
+template <bool NV, int NH>
 int launch_pair(const Fp4GemmArgs &g, Params &p, int sms, cudaStream_t stream) {
     using L = PairLayout<NV, NH>;
     set_operands(p, g, false, PM, L::PN);
@@ -1054,7 +1055,7 @@ int launch_pair(const Fp4GemmArgs &g, Params &p, int sms, cudaStream_t stream) {
     tc = tsb;   // not used unless c_tma
     p.c_tma = !p.accumulate && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % (p.out_fp32 ? 4 : 8) == 0 &&
               make_out_tmap(&tc, p);
-    return launch_cluster(k_fp4_pair<NV, NH, SUB>, 2 * std::min<int64_t>(tiles, sms / 2), 2, P_THREADS, L::SMEM, stream,
+    return launch_cluster(k_fp4_pair<NV, NH>, 2 * std::min<int64_t>(tiles, sms / 2), 2, P_THREADS, L::SMEM, stream,
                           ta, tb, tsa, tsb, tc, p, instruction(NV, PM, PH));
 }
 
@@ -1149,12 +1150,8 @@ int launch(const Fp4GemmArgs &g, int sms, cudaStream_t stream) {
     }
     const bool swapped = g.a.rows <= g.b.rows;
     const Plan plan = choose(g.a.rows, g.b.rows, p.nk, sms);
-    // NV, a stage's scales in two halves: 16384 x 3584 x 18944 327 us against 338,
-    // 8192 x 18944 x 3584 (14 stages) 178 against 181, but 8192 x 8960 x 1536 (6)
-    // 54 against 53 and 3584 x 18944 x 1000 (4) 37 against 36
-    if (plan.nh == 2 && NV && p.nk >= 12) return launch_pair<NV, 2, NV ? 2 : 1>(g, p, sms, stream);
-    if (plan.nh == 2) return launch_pair<NV, 2, 1>(g, p, sms, stream);
-    if (plan.nh == 1) return launch_pair<NV, 1, 1>(g, p, sms, stream);
+    if (plan.nh == 2) return launch_pair<NV, 2>(g, p, sms, stream);
+    if (plan.nh == 1) return launch_pair<NV, 1>(g, p, sms, stream);
     switch (plan.bn) {
     case 16: return launch_few<NV, 16, false>(g, p, swapped, plan.splits, stream);
     case 32: return launch_few<NV, 32, false>(g, p, swapped, plan.splits, stream);
