@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256, kRowThreadsPerSm / 256)
     k_fp4_rows(const uint16_t *x, uint32_t rows, int cols, uint32_t ld_x,
                const float *ts, uint8_t *q, uint32_t ld_q,
                uint8_t *s, uint32_t tiles, int segs, int total_segs) {
-    ptx::grid_begin();
+    ptx::grid_begin(static_cast<int64_t>(rows) * cols);
     const int tid = threadIdx.x, lane = tid & 31;
     const int seg = blockIdx.y * segs + tid % segs;
     const int rpb = blockDim.x / segs;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256)
                const float *ts, uint8_t *q, uint32_t ld_q,
                uint8_t *s, uint32_t tiles, uint8_t *qt, uint32_t ld_qt,
                uint8_t *st, uint32_t tiles_t) {
-    ptx::grid_begin();
+    ptx::grid_begin(static_cast<int64_t>(rows) * cols);
     constexpr int NT = NV ? 2 : 1;          // scale tiles of 4 blocks per 128 elements
     constexpr int LPB = NV ? 1 : 2;
     __shared__ __align__(16) uint8_t tile[kTile * 256];
@@ -248,7 +248,7 @@ template <bool WIDE>
 __global__ void __launch_bounds__(512, kAmaxCtasPerSm)
     k_fp4_amax(const uint16_t *x, int rows, int segs, int cols, uint32_t ld_x,
                uint32_t *part) {
-    ptx::grid_begin();
+    ptx::grid_begin(static_cast<int64_t>(rows) * cols);
     __shared__ uint32_t red[16];
     uint32_t m = 0;
     // segments of 16 elements, rows and segments walked together
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(512, kAmaxCtasPerSm)
 
 __global__ void __launch_bounds__(32)
     k_fp4_tensor_scale(const uint32_t *part, int n, float *scale) {
-    ptx::grid_begin();
+    ptx::grid_begin(n);
     uint32_t m = 0;
 #pragma unroll 8
     for (int i = threadIdx.x; i < n; i += 32) m = max(m, ptx::ld_u32(part + i));
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
     k_fp4_dequant(const uint8_t *q, const uint8_t *s,
                   const float *ts, uint32_t rows, int k, uint32_t ld, uint32_t tiles,
                   void *out, uint32_t ld_out, int segs) {
-    ptx::grid_begin();
+    ptx::grid_begin(static_cast<int64_t>(rows) * k);
     const float t = NV && ts ? ptx::ld_f32(ts) : 1.0f;
     const int g = blockIdx.y * blockDim.x + threadIdx.x;
     const int c0 = g * 16, left = k - c0;

@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         *abort_flag = 0u;
         ptx::fence_mbar_init();
     }
-    ptx::grid_begin();
+    ptx::grid_begin(1);   // a short one
     if (threadIdx.x == 0)
         for (int it = 0; it < 2 && it < n; ++it) load_stage(it);
     if (warp == 1) {

@@ -146,7 +146,7 @@ constexpr int kFwdThreadsPerSm = 768;   // 80 registers a thread
 template <int FH, int FC, bool CKPT, bool WIDE>
 __global__ void __launch_bounds__(256, kFwdThreadsPerSm / 256)
     k_swiglu_fwd(const SwigluFwdArgs a, int segs, int total_segs) {
-    ptx::grid_begin();
+    ptx::grid_begin(static_cast<int64_t>(a.rows) * a.cols);
     const int tid = threadIdx.x;
     const int seg = blockIdx.y * segs + tid % segs;
     const int rpb = blockDim.x / segs;
@@ -228,7 +228,7 @@ template <int FC, bool WIDE>
 __global__ void __launch_bounds__(256)
     k_swiglu_bwd(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt c,
                  uint16_t *dg, uint16_t *du, uint32_t ld_d, int segs) {
-    ptx::grid_begin();
+    ptx::grid_begin(static_cast<int64_t>(c.rows) * c.cols);
     // a warp takes 32 neighbouring segments of one row, whole warps past the
     // row's end included: the stores exchange values between lanes
     const int seg = (blockIdx.y * blockDim.x + threadIdx.x);
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
         ptx::fence_mbar_init();
     }
     __syncthreads();
-    ptx::grid_begin();
+    ptx::grid_begin(static_cast<int64_t>(c.rows) * c.cols);
     // every warp waits for and arrives at every barrier, once a tile
     auto wait = [&](uint32_t which, uint32_t parity) {
         if (ptx::mbar_try_wait(which, parity)) return true;
