@@ -92,7 +92,9 @@ def _streamed(fn):
         if stream is None:
             return fn(*args, **kw)
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream))
+            # 0 is the default stream; ExternalStream(0) would be a new one
+            handle = _stream(stream)
+            stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
     return call
