@@ -63,17 +63,22 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 _cuda_device = torch._C._cuda_getDevice
-# the allocation behind torch.empty without its argument handling: in a row of
-# small calls an output costs the host 1.4 us instead of 4
-_empty_strided = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
-_empty_strided = getattr(_empty_strided, "_empty_strided_cuda", None)
 
 
-def _allocator(x):
-    """A function of sizes, strides and type that allocates on x's device."""
-    if _empty_strided is not None and x.get_device() == _cuda_device():
-        return _empty_strided
-    return lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device=x.device)
+def _here(t) -> bool:
+    """Whether t is on the current device: the one that a call launches on, and
+    whose memory it may touch."""
+    device = t.get_device()
+    return device >= 0 and device == _cuda_device()
+
+
+# the allocation (sizes, strides, type) on the current device; torch.empty without
+# its argument handling: in a row of small calls an output costs the host 1.4 us
+# instead of 4
+_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+if _new is None:
+    def _new(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
 
 
 def _on(x):
@@ -132,13 +137,13 @@ def _fns():
 
 def _matrix(x, what="x"):
     """Rows, columns and row stride of a BF16 input."""
-    if x.dtype == torch.bfloat16 and x.is_cuda and x.dim() == 2:
+    if x.dtype == torch.bfloat16 and x.dim() == 2 and _here(x):
         rows, cols = x.shape
         ld, unit = x.stride()
         if unit == 1 or cols <= 1:
             # a tensor of one row or none may carry any row stride
             return rows, cols, ld if rows > 1 else max(ld, cols)
-    raise ValueError(f"{what} must be a 2-D CUDA bfloat16 tensor with unit column stride")
+    raise ValueError(f"{what} must be a 2-D bfloat16 tensor on the current CUDA device with unit column stride")
 
 
 def _ld(x) -> int:
@@ -149,8 +154,8 @@ def _ld(x) -> int:
 def _ts(t):
     if t is None:
         return None
-    if t.dtype != torch.float32 or not t.is_cuda or t.numel() != 1:
-        raise ValueError("tensor_scale must be a CUDA float32 tensor of one element")
+    if t.dtype != torch.float32 or t.numel() != 1 or not _here(t):
+        raise ValueError("tensor_scale must be a float32 tensor of one element on the current CUDA device")
     return t.data_ptr()
 
 
@@ -163,8 +168,8 @@ def _out_kind(out) -> int:
 
 
 def _check_out(out, rows, cols):
-    if tuple(out.shape) != (rows, cols) or not out.is_cuda or (out.stride(1) != 1 and cols > 1):
-        raise ValueError(f"out must be a CUDA tensor [{rows}, {cols}] with unit column stride")
+    if tuple(out.shape) != (rows, cols) or not _here(out) or (out.stride(1) != 1 and cols > 1):
+        raise ValueError(f"out must be a tensor [{rows}, {cols}] on the current CUDA device with unit column stride")
 
 
 def _opts(wait_limit_ns, inject_fault):
@@ -190,9 +195,16 @@ class Fp4Tensor:
         c = self.codes
         return c.stride(0) if self.rows > 1 else max(c.stride(0), c.shape[1])
 
+    def buffers(self):
+        """Address and row stride of the codes, address of the scale bytes."""
+        c, s = self.codes, self.scale
+        if not (_here(c) and _here(s)):
+            raise ValueError("a 4-bit tensor's codes and scale must be on the current CUDA device")
+        return c.data_ptr(), self.ld(), s.data_ptr()
+
     def operand(self) -> _Fp4Operand:
-        return _Fp4Operand(self.codes.data_ptr(), self.scale.data_ptr(), _ts(self.tensor_scale),
-                           self.rows, self.k, self.ld(), self.kind, 0)
+        codes, ld, scale = self.buffers()
+        return _Fp4Operand(codes, scale, _ts(self.tensor_scale), self.rows, self.k, ld, self.kind, 0)
 
     def scales(self) -> torch.Tensor:
         """The scale bytes as [rows, ceil(k / block)] (a copy)."""
@@ -214,11 +226,11 @@ def _scale_bytes(rows, k, kind) -> int:
     return (rows + 127) // 128 * ((k + 255) // 256) * (2048 if kind == FP4_NV else 1024)
 
 
-def _alloc(rows, k, kind, tensor_scale, x) -> Fp4Tensor:
-    """alloc_fp4 on x's device."""
-    new, ld = _allocator(x), (k + 31) // 32 * 16
-    return Fp4Tensor(new((rows, ld), (ld, 1), torch.uint8),
-                     new((_scale_bytes(rows, k, kind),), (1,), torch.uint8), rows, k, kind, tensor_scale)
+def _alloc(rows, k, kind, tensor_scale) -> Fp4Tensor:
+    """alloc_fp4 on the current device."""
+    ld = (k + 31) // 32 * 16
+    return Fp4Tensor(_new((rows, ld), (ld, 1), torch.uint8),
+                     _new((_scale_bytes(rows, k, kind),), (1,), torch.uint8), rows, k, kind, tensor_scale)
 
 
 @_streamed
@@ -227,7 +239,7 @@ def fp4_tensor_scale(x, out=None):
     amax <= 6 * 448 * t (1 for a tensor of zeros), on the device."""
     rows, cols, ld = _matrix(x)
     f = _fns()
-    out = out if out is not None else _allocator(x)((1,), (1,), torch.float32)
+    out = out if out is not None else _new((1,), (1,), torch.float32)
     n = f.fp4_tensor_scale_workspace()
     stream = _on(x)
     _check(f.fp4_tensor_scale(x.data_ptr(), rows, cols, ld, _ts(out),
@@ -239,8 +251,8 @@ _NONE = (None, 0, None)
 
 
 def _quant(x, shape, kind, tensor_scale, rows_out, cols_out, what):
-    q = (rows_out.codes.data_ptr(), rows_out.ld(), rows_out.scale.data_ptr()) if rows_out else _NONE
-    t = (cols_out.codes.data_ptr(), cols_out.ld(), cols_out.scale.data_ptr()) if cols_out else _NONE
+    q = rows_out.buffers() if rows_out else _NONE
+    t = cols_out.buffers() if cols_out else _NONE
     _check(_fns().fp4_quant(x.data_ptr(), *shape, kind, _ts(tensor_scale), *q, *t,
                             _on(x)), what)
 
@@ -258,7 +270,7 @@ def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
     shape = _matrix(x)
     rows, cols = (shape[1], shape[0]) if transpose else shape[:2]
     if out is None:
-        out = _alloc(rows, cols, kind, tensor_scale, x)
+        out = _alloc(rows, cols, kind, tensor_scale)
     _check_fp4(out, rows, cols, kind)
     out.tensor_scale = tensor_scale
     _quant(x, shape, kind, tensor_scale, None if transpose else out, out if transpose else None,
@@ -272,8 +284,8 @@ def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Te
     """fp4_quant along the rows and along the columns from one read of x."""
     shape = _matrix(x)
     rows, cols = shape[:2]
-    out = out if out is not None else _alloc(rows, cols, kind, tensor_scale, x)
-    out_t = out_t if out_t is not None else _alloc(cols, rows, kind, tensor_scale, x)
+    out = out if out is not None else _alloc(rows, cols, kind, tensor_scale)
+    out_t = out_t if out_t is not None else _alloc(cols, rows, kind, tensor_scale)
     _check_fp4(out, rows, cols, kind)
     _check_fp4(out_t, cols, rows, kind)
     out.tensor_scale = out_t.tensor_scale = tensor_scale
@@ -285,7 +297,7 @@ def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Te
 def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None):
     """The values of a 4-bit tensor, [rows, k], BF16 or FP32."""
     if out is None:
-        out = _allocator(q.codes)((q.rows, q.k), (q.k, 1), out_dtype or torch.bfloat16)
+        out = _new((q.rows, q.k), (q.k, 1), out_dtype or torch.bfloat16)
     else:
         _check_out(out, q.rows, q.k)
     op = q.operand()
@@ -301,7 +313,7 @@ def fp4_gemm_scaled(a: Fp4Tensor, b: Fp4Tensor, out=None, out_dtype=None, accumu
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = _allocator(a.codes)((a.rows, b.rows), (b.rows, 1), out_dtype or torch.bfloat16)
+        out = _new((a.rows, b.rows), (b.rows, 1), out_dtype or torch.bfloat16)
     else:
         _check_out(out, a.rows, b.rows)
     oa, ob = a.operand(), b.operand()
@@ -322,7 +334,7 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
     if k != w.k:
         raise ValueError(f"x has {k} columns, w {w.k}")
     if out is None:
-        out, ld_out = _allocator(x)((rows, w.rows), (w.rows, 1), out_dtype or torch.bfloat16), w.rows
+        out, ld_out = _new((rows, w.rows), (w.rows, 1), out_dtype or torch.bfloat16), w.rows
     else:
         _check_out(out, rows, w.rows)
         ld_out = _ld(out)
@@ -330,6 +342,8 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
     n = 0 if rows <= 4 else _linear_bytes(rows, k, w.kind)
     if n and workspace is None:
         workspace = _scratch(n, x, stream)
+    elif n and not _here(workspace):
+        raise ValueError("workspace must be on the current CUDA device")
     ow = w.operand()
     _check(_fns().fp4_linear(x.data_ptr(), rows, ld, _ts(tensor_scale), ctypes.byref(ow),
                              out.data_ptr(), ld_out, _out_kind(out),
@@ -375,13 +389,12 @@ class SwigluCkpt:
     up: QTensor
 
 
-def _groups(rows, cols, fmt, new):
-    """[rows, cols] codes (rows padded to 16 bytes) and their 1x128 scales; new:
-    from _allocator."""
+def _groups(rows, cols, fmt):
+    """[rows, cols] codes (rows padded to 16 bytes) and their 1x128 scales."""
     g = (cols + 127) // 128
     ls = _round4(g)
-    return QTensor(new((rows, cols), ((cols + 15) // 16 * 16, 1), torch.uint8),
-                   new((rows, ls), (ls, 1), torch.uint8), fmt, GRAN_1x128, g)
+    return QTensor(_new((rows, cols), ((cols + 15) // 16 * 16, 1), torch.uint8),
+                   _new((rows, ls), (ls, 1), torch.uint8), fmt, GRAN_1x128, g)
 
 
 def _ld_codes(q) -> int:
@@ -398,11 +411,11 @@ def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bo
     shape = rows, cols, ld_in = _matrix(gate, "gate")
     if _matrix(up, "up") != shape:
         raise ValueError("gate and up must have the same shape and row stride")
-    ld, new = (cols + 15) // 16 * 16, _allocator(gate)
-    h = _groups(rows, cols, fmt_h, new)
+    ld = (cols + 15) // 16 * 16
+    h = _groups(rows, cols, fmt_h)
     ckpt, ptr, ls = None, (None, None, None, None), h.scale.shape[1]
     if checkpoint:
-        g, u = _groups(rows, cols, fmt, new), _groups(rows, cols, fmt, new)
+        g, u = _groups(rows, cols, fmt), _groups(rows, cols, fmt)
         ptr = (g.codes.data_ptr(), g.scale.data_ptr(), u.codes.data_ptr(), u.scale.data_ptr())
         ckpt = SwigluCkpt(g, u)
     _check(_fns().fp8_swiglu_ckpt(gate.data_ptr(), up.data_ptr(), rows, cols, ld_in, fmt_h,
@@ -415,6 +428,8 @@ def _ckpt(c: SwigluCkpt, dh):
     """The checkpoint for the library; dh's rows, columns and row stride."""
     g, u = c.gate, c.up
     shape = rows, cols, _ = _matrix(dh, "dh")
+    if not (_here(g.codes) and _here(g.scale) and _here(u.codes) and _here(u.scale)):
+        raise ValueError("a checkpoint's codes and scales must be on the current CUDA device")
     if g.gran != GRAN_1x128 or u.gran != GRAN_1x128 or g.fmt != u.fmt:
         raise ValueError("a checkpoint has 1x128 scales and one format")
     if g.codes.shape != (rows, cols) or u.codes.shape != (rows, cols):
@@ -432,7 +447,7 @@ def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None):
     one [rows, 2 cols] tensor, dgate in the first half, dup in the second."""
     c, (rows, cols, ld) = _ckpt(ckpt, dh)
     if out is None:
-        out, ld_out = _allocator(dh)((rows, 2 * cols), (2 * cols, 1), torch.bfloat16), 2 * cols
+        out, ld_out = _new((rows, 2 * cols), (2 * cols, 1), torch.bfloat16), 2 * cols
     else:
         _check_out(out, rows, 2 * cols)
         ld_out = _matrix(out, "out")[2]
@@ -450,10 +465,9 @@ def fp8_swiglu_ckpt_bwd_q(dh, ckpt: SwigluCkpt, fmt: int = E5M2, fmt_t: int = E5
     the checkpoint and transposed, [cols, rows], per 128 tokens).  rows and cols
     must be multiples of 128."""
     c, (rows, cols, ld) = _ckpt(ckpt, dh)
-    new = _allocator(dh)
-    d = _groups(rows, 2 * cols, fmt, new)
-    t = _groups(2 * cols, rows, fmt_t, new)
-    h = _groups(cols, rows, fmt_h, new)
+    d = _groups(rows, 2 * cols, fmt)
+    t = _groups(2 * cols, rows, fmt_t)
+    h = _groups(cols, rows, fmt_h)
     dq, ds, tq, tl = d.codes.data_ptr(), d.scale.data_ptr(), t.codes.data_ptr(), t.scale.data_ptr()
     ld_qt, ld_st = t.codes.stride(0), t.scale.stride(0)
     g = _Grads(dq, dq + cols, ds, ds + cols // 128, tq, tq + cols * ld_qt, tl, tl + cols * ld_st,

@@ -32,3 +32,108 @@ def test_stream_handles(monkeypatch):
     assert call(1, w=2) == 3 and entered == []
     assert call(1, w=2, stream=own) == 3 and call(2, stream=0x5000) == 2 and call(3, stream=0) == 3
     assert entered == [own, ("external", 0x5000), "default"]
+
+
+class StandIn:
+    """A tensor that says it is on GPU `device`; its memory, never used, is the
+    CPU's."""
+
+    def __init__(self, t, device=0):
+        self._t, self._device = t, device
+        self.dtype, self.shape = t.dtype, t.shape
+        self.is_cuda, self.device = True, torch.device("cuda", device)
+
+    def get_device(self):
+        return self._device
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+class Reached(Exception):
+    """The library was called."""
+
+
+@pytest.fixture
+def gpu0(monkeypatch):
+    """GPU 0 is current; the library only says that it was reached."""
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                if name.endswith("_workspace"):
+                    return 4096
+                raise Reached(name)
+            return call
+
+    monkeypatch.setattr(lowbit, "_cuda_device", lambda: 0)
+    monkeypatch.setattr(lowbit, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(lowbit, "_fns", Library)
+    # what the calls allocate is on GPU 0 too
+    monkeypatch.setattr(lowbit, "_new", lambda *a: StandIn(torch.empty_strided(*a[:2], dtype=a[2])), raising=False)
+    monkeypatch.setattr(lowbit, "_scratch", lambda n, x, stream: StandIn(torch.empty(n, dtype=torch.uint8)))
+    return lambda t: StandIn(t)
+
+
+def bf16(rows, cols):
+    return torch.zeros(rows, cols, dtype=torch.bfloat16)
+
+
+def fp4(on, rows=40, k=64, kind=fp8hg.FP4_MX, ts=None):
+    q = fp8hg.alloc_fp4(rows, k, kind, ts, device="cpu")
+    q.codes, q.scale = on(q.codes), on(q.scale)
+    return q
+
+
+def ckpt(on, rows=4, cols=128):
+    half = lambda: fp8hg.QTensor(on(torch.zeros(rows, cols, dtype=torch.uint8)),
+                                 on(torch.zeros(rows, (cols + 511) // 512 * 4, dtype=torch.uint8)), fp8hg.E4M3,
+                                 fp8hg.GRAN_1x128, (cols + 127) // 128)
+    return fp8hg.SwigluCkpt(half(), half())
+
+
+def f32(*shape):
+    return torch.zeros(shape)
+
+
+# every tensor argument of every call: name -> the call with one argument from `one`, the others from `on`
+CALLS = {
+    "tensor_scale x": lambda on, one: fp8hg.fp4_tensor_scale(one(bf16(4, 64))),
+    "tensor_scale out": lambda on, one: fp8hg.fp4_tensor_scale(on(bf16(4, 64)), out=one(f32(1))),
+    "quant x": lambda on, one: fp8hg.fp4_quant(one(bf16(4, 64))),
+    "quant scale": lambda on, one: fp8hg.fp4_quant(on(bf16(4, 64)), fp8hg.FP4_NV, one(f32(1))),
+    "quant out": lambda on, one: fp8hg.fp4_quant(on(bf16(40, 64)), out=fp4(one)),
+    "quant transposed out": lambda on, one: fp8hg.fp4_quant(on(bf16(64, 40)), transpose=True, out=fp4(one)),
+    "dual x": lambda on, one: fp8hg.fp4_quant_dual(one(bf16(40, 64))),
+    "dual out": lambda on, one: fp8hg.fp4_quant_dual(on(bf16(40, 64)), out=fp4(one)),
+    "dual out_t": lambda on, one: fp8hg.fp4_quant_dual(on(bf16(40, 64)), out_t=fp4(one, 64, 40)),
+    "dequant q": lambda on, one: fp8hg.fp4_dequant(fp4(one)),
+    "dequant out": lambda on, one: fp8hg.fp4_dequant(fp4(on), out=one(bf16(40, 64))),
+    "gemm a": lambda on, one: fp8hg.fp4_gemm_scaled(fp4(one), fp4(on)),
+    "gemm b": lambda on, one: fp8hg.fp4_gemm_scaled(fp4(on), fp4(one)),
+    "gemm scale": lambda on, one: fp8hg.fp4_gemm_scaled(fp4(on, kind=fp8hg.FP4_NV, ts=one(f32(1))),
+                                                        fp4(on, kind=fp8hg.FP4_NV)),
+    "gemm out": lambda on, one: fp8hg.fp4_gemm_scaled(fp4(on), fp4(on), out=one(bf16(40, 40))),
+    "linear x": lambda on, one: fp8hg.fp4_linear(one(bf16(8, 64)), fp4(on)),
+    "linear w": lambda on, one: fp8hg.fp4_linear(on(bf16(8, 64)), fp4(one)),
+    "linear out": lambda on, one: fp8hg.fp4_linear(on(bf16(8, 64)), fp4(on), out=one(bf16(8, 40))),
+    "linear workspace": lambda on, one: fp8hg.fp4_linear(on(bf16(8, 64)), fp4(on),
+                                                         workspace=one(torch.zeros(2048, dtype=torch.uint8))),
+    "swiglu gate": lambda on, one: fp8hg.fp8_swiglu_ckpt(one(bf16(4, 128)), on(bf16(4, 128))),
+    "swiglu up": lambda on, one: fp8hg.fp8_swiglu_ckpt(on(bf16(4, 128)), one(bf16(4, 128))),
+    "bwd dh": lambda on, one: fp8hg.fp8_swiglu_ckpt_bwd(one(bf16(4, 128)), ckpt(on)),
+    "bwd checkpoint": lambda on, one: fp8hg.fp8_swiglu_ckpt_bwd(on(bf16(4, 128)), ckpt(one)),
+    "bwd out": lambda on, one: fp8hg.fp8_swiglu_ckpt_bwd(on(bf16(4, 128)), ckpt(on), out=one(bf16(4, 256))),
+    "bwd_q dh": lambda on, one: fp8hg.fp8_swiglu_ckpt_bwd_q(one(bf16(128, 128)), ckpt(on, 128)),
+    "bwd_q checkpoint": lambda on, one: fp8hg.fp8_swiglu_ckpt_bwd_q(on(bf16(128, 128)), ckpt(one, 128)),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_tensors_elsewhere_are_refused(gpu0, name):
+    """A call launches on the current device: tensors of another GPU, or of
+    the CPU, never reach it."""
+    with pytest.raises(Reached):
+        CALLS[name](gpu0, gpu0)
+    for elsewhere in (lambda t: StandIn(t, 1), lambda t: t):
+        with pytest.raises(ValueError):
+            CALLS[name](gpu0, elsewhere)
