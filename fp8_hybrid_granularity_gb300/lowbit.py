@@ -196,10 +196,18 @@ class Fp4Tensor:
         return c.stride(0) if self.rows > 1 else max(c.stride(0), c.shape[1])
 
     def buffers(self):
-        """Address and row stride of the codes, address of the scale bytes."""
+        """Address and row stride of the codes, address of the scale bytes, which
+        have to hold what rows and k say."""
         c, s = self.codes, self.scale
         if not (_here(c) and _here(s)):
             raise ValueError("a 4-bit tensor's codes and scale must be on the current CUDA device")
+        rows, n = self.rows, (self.k + 1) // 2
+        if (c.dim() != 2 or c.element_size() != 1 or c.shape[0] < rows or c.shape[1] < n or
+                (c.stride(1) != 1 and n > 1)):
+            raise ValueError(f"codes must be a byte tensor of [{rows}, at least {n}] with unit column stride")
+        n = _scale_bytes(rows, self.k, self.kind)
+        if s.element_size() != 1 or s.numel() < n or not s.is_contiguous():
+            raise ValueError(f"scale must be a contiguous byte tensor of at least {n} elements")
         return c.data_ptr(), self.ld(), s.data_ptr()
 
     def operand(self) -> _Fp4Operand:
@@ -342,8 +350,8 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
     n = 0 if rows <= 4 else _linear_bytes(rows, k, w.kind)
     if n and workspace is None:
         workspace = _scratch(n, x, stream)
-    elif n and not _here(workspace):
-        raise ValueError("workspace must be on the current CUDA device")
+    elif n and not (_here(workspace) and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
     ow = w.operand()
     _check(_fns().fp4_linear(x.data_ptr(), rows, ld, _ts(tensor_scale), ctypes.byref(ow),
                              out.data_ptr(), ld_out, _out_kind(out),

@@ -137,3 +137,64 @@ def test_tensors_elsewhere_are_refused(gpu0, name):
     for elsewhere in (lambda t: StandIn(t, 1), lambda t: t):
         with pytest.raises(ValueError):
             CALLS[name](gpu0, elsewhere)
+
+
+# a 4-bit tensor of 130 rows of 300, and ways in which its buffers hold less than that
+FP4_CALLS = {
+    "quant out": lambda q: fp8hg.fp4_quant(StandIn(bf16(130, 300)), q.kind, out=q),
+    "quant transposed out": lambda q: fp8hg.fp4_quant(StandIn(bf16(300, 130)), q.kind, transpose=True, out=q),
+    "dual out": lambda q: fp8hg.fp4_quant_dual(StandIn(bf16(130, 300)), q.kind, out=q),
+    "dual out_t": lambda q: fp8hg.fp4_quant_dual(StandIn(bf16(300, 130)), q.kind, out_t=q),
+    "dequant": lambda q: fp8hg.fp4_dequant(q),
+    "gemm a": lambda q: fp8hg.fp4_gemm_scaled(q, fp4(StandIn, 8, 300, q.kind)),
+    "gemm b": lambda q: fp8hg.fp4_gemm_scaled(fp4(StandIn, 8, 300, q.kind), q),
+    "linear w": lambda q: fp8hg.fp4_linear(StandIn(bf16(2, 300)), q),
+}
+
+
+def broken(field, value):
+    def change(q):
+        setattr(q, field, StandIn(value))
+    return change
+
+
+def buffers_that_do_not_hold(kind):
+    n = fp8hg.alloc_fp4(130, 300, kind, device="cpu").scale.numel()
+    u8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8)
+    return {
+        "codes with a row too few": broken("codes", u8(129, 160)),
+        "codes with a byte too few a row": broken("codes", u8(130, 160)[:, :149]),
+        "codes of another type": broken("codes", torch.zeros(130, 160, dtype=torch.int16)),
+        "codes of every second byte": broken("codes", u8(130, 320)[:, ::2]),
+        "flat codes": broken("codes", u8(130 * 160)),
+        "scale with a byte too few": broken("scale", u8(n - 1)),
+        "scale of 128 rows": broken("scale", u8(n // 2)),
+        "scale of every second byte": broken("scale", u8(2 * n)[::2]),
+        "scale of another type": broken("scale", torch.zeros(n)),
+    }
+
+
+@pytest.mark.parametrize("kind", [fp8hg.FP4_MX, fp8hg.FP4_NV])
+@pytest.mark.parametrize("name", FP4_CALLS)
+def test_buffers_that_do_not_hold_the_tensor(gpu0, name, kind):
+    """A 4-bit tensor whose codes or scale bytes hold less than rows and k say
+    is refused: a kernel would read or write past them."""
+    with pytest.raises(Reached):
+        FP4_CALLS[name](fp4(gpu0, 130, 300, kind))
+    # more than the tensor needs, and one-byte types other than uint8, are as good
+    q = fp4(gpu0, 130, 300, kind)
+    broken("codes", torch.zeros(200, 176, dtype=torch.int8))(q)
+    broken("scale", torch.zeros(8, 2048, dtype=torch.uint8))(q)
+    with pytest.raises(Reached):
+        FP4_CALLS[name](q)
+    for what, change in buffers_that_do_not_hold(kind).items():
+        q = fp4(gpu0, 130, 300, kind)
+        change(q)
+        with pytest.raises(ValueError):
+            FP4_CALLS[name](q)
+            pytest.fail(what)
+
+
+def test_workspace_with_gaps(gpu0):
+    with pytest.raises(ValueError):
+        fp8hg.fp4_linear(gpu0(bf16(8, 64)), fp4(gpu0), workspace=gpu0(torch.zeros(8192, dtype=torch.uint8)[::2]))
