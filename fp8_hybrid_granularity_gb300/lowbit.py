@@ -442,6 +442,15 @@ def _ckpt(c: SwigluCkpt, dh):
         raise ValueError("a checkpoint has 1x128 scales and one format")
     if g.codes.shape != (rows, cols) or u.codes.shape != (rows, cols):
         raise ValueError("dh and the checkpoint must have the same shape")
+    groups = (cols + 127) // 128
+    for q in (g, u):
+        c, s = q.codes, q.scale
+        if c.element_size() != 1 or (c.stride(1) != 1 and cols > 1):
+            raise ValueError("a checkpoint's codes must be bytes with unit column stride")
+        if (s.dim() != 2 or s.element_size() != 1 or s.shape[0] < rows or s.shape[1] < groups or
+                (s.stride(1) != 1 and groups > 1)):
+            raise ValueError(f"a checkpoint's scales must be a byte tensor of [{rows}, at least {groups}] "
+                             "with unit column stride")
     ld, ls = _ld_codes(g.codes), g.scale.stride(0)
     if ld != _ld_codes(u.codes) or (rows > 1 and ls != u.scale.stride(0)):
         raise ValueError("gate's and up's codes and scales must have the same strides")

@@ -198,3 +198,26 @@ def test_buffers_that_do_not_hold_the_tensor(gpu0, name, kind):
 def test_workspace_with_gaps(gpu0):
     with pytest.raises(ValueError):
         fp8hg.fp4_linear(gpu0(bf16(8, 64)), fp4(gpu0), workspace=gpu0(torch.zeros(8192, dtype=torch.uint8)[::2]))
+
+
+CKPT_CALLS = {
+    "bwd": lambda c: fp8hg.fp8_swiglu_ckpt_bwd(StandIn(bf16(128, 640)), c),
+    "bwd_q": lambda c: fp8hg.fp8_swiglu_ckpt_bwd_q(StandIn(bf16(128, 640)), c),
+}
+
+
+@pytest.mark.parametrize("name", CKPT_CALLS)
+@pytest.mark.parametrize("half", ["gate", "up"])
+def test_checkpoint_buffers_that_do_not_hold_it(gpu0, name, half):
+    """[128, 640] codes and [128, 5 of 8] scale bytes, and ways to hold less."""
+    u8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8)
+    with pytest.raises(Reached):
+        CKPT_CALLS[name](ckpt(gpu0, 128, 640))
+    for field, value in (("codes", u8(128, 1280)[:, ::2]), ("codes", torch.zeros(128, 640, dtype=torch.int16)),
+                         ("scale", u8(127, 8)), ("scale", u8(128, 8)[:, :4]), ("scale", u8(128, 16)[:, ::2]),
+                         ("scale", u8(128 * 8)), ("scale", torch.zeros(128, 8))):
+        c = ckpt(gpu0, 128, 640)
+        setattr(getattr(c, half), field, gpu0(value))
+        with pytest.raises(ValueError):
+            CKPT_CALLS[name](c)
+            pytest.fail(f"{field} {tuple(value.shape)} {value.dtype}")
