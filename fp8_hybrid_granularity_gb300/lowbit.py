@@ -135,20 +135,25 @@ def _fns():
     return _bound
 
 
+def _round16(n: int) -> int:
+    """The row stride that a tensor of one row is given: its own says nothing,
+    and may be too small, misaligned or unlike another operand's."""
+    return (n + 15) // 16 * 16
+
+
 def _matrix(x, what="x"):
     """Rows, columns and row stride of a BF16 input."""
     if x.dtype == torch.bfloat16 and x.dim() == 2 and _here(x):
         rows, cols = x.shape
         ld, unit = x.stride()
         if unit == 1 or cols <= 1:
-            # a tensor of one row or none may carry any row stride
-            return rows, cols, ld if rows > 1 else max(ld, cols)
+            return rows, cols, ld if rows > 1 else _round16(cols)
     raise ValueError(f"{what} must be a 2-D bfloat16 tensor on the current CUDA device with unit column stride")
 
 
 def _ld(x) -> int:
-    """Row stride; a tensor of one row or none may carry any."""
-    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+    """Row stride of an output or of FP8 codes."""
+    return x.stride(0) if x.shape[0] > 1 else _round16(x.shape[1])
 
 
 def _ts(t):
@@ -191,9 +196,8 @@ class Fp4Tensor:
     tensor_scale: Optional[torch.Tensor] = None
 
     def ld(self) -> int:
-        """Row stride of the codes, in bytes (a single row may carry any)."""
-        c = self.codes
-        return c.stride(0) if self.rows > 1 else max(c.stride(0), c.shape[1])
+        """Row stride of the codes, in bytes."""
+        return self.codes.stride(0) if self.rows > 1 else _round16((self.k + 1) // 2)
 
     def buffers(self):
         """Address and row stride of the codes, address of the scale bytes, which
@@ -401,13 +405,8 @@ def _groups(rows, cols, fmt):
     """[rows, cols] codes (rows padded to 16 bytes) and their 1x128 scales."""
     g = (cols + 127) // 128
     ls = _round4(g)
-    return QTensor(_new((rows, cols), ((cols + 15) // 16 * 16, 1), torch.uint8),
+    return QTensor(_new((rows, cols), (_round16(cols), 1), torch.uint8),
                    _new((rows, ls), (ls, 1), torch.uint8), fmt, GRAN_1x128, g)
-
-
-def _ld_codes(q) -> int:
-    """Row stride of codes that are padded to 16 bytes (any, for one row)."""
-    return q.stride(0) if q.shape[0] > 1 else max(q.stride(0), (q.shape[1] + 15) // 16 * 16)
 
 
 @_streamed
@@ -419,7 +418,7 @@ def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bo
     shape = rows, cols, ld_in = _matrix(gate, "gate")
     if _matrix(up, "up") != shape:
         raise ValueError("gate and up must have the same shape and row stride")
-    ld = (cols + 15) // 16 * 16
+    ld = _round16(cols)
     h = _groups(rows, cols, fmt_h)
     ckpt, ptr, ls = None, (None, None, None, None), h.scale.shape[1]
     if checkpoint:
@@ -451,8 +450,8 @@ def _ckpt(c: SwigluCkpt, dh):
                 (s.stride(1) != 1 and groups > 1)):
             raise ValueError(f"a checkpoint's scales must be a byte tensor of [{rows}, at least {groups}] "
                              "with unit column stride")
-    ld, ls = _ld_codes(g.codes), g.scale.stride(0)
-    if ld != _ld_codes(u.codes) or (rows > 1 and ls != u.scale.stride(0)):
+    ld, ls = _ld(g.codes), g.scale.stride(0) if rows > 1 else groups
+    if ld != _ld(u.codes) or (rows > 1 and ls != u.scale.stride(0)):
         raise ValueError("gate's and up's codes and scales must have the same strides")
     return _Ckpt(g.codes.data_ptr(), g.scale.data_ptr(), u.codes.data_ptr(), u.scale.data_ptr(),
                  rows, cols, ld, ls, g.fmt, 0), shape

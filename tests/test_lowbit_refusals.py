@@ -221,3 +221,28 @@ def test_checkpoint_buffers_that_do_not_hold_it(gpu0, name, half):
         with pytest.raises(ValueError):
             CKPT_CALLS[name](c)
             pytest.fail(f"{field} {tuple(value.shape)} {value.dtype}")
+
+
+def row(n, stride, dtype=torch.bfloat16):
+    """One row of n elements with a row stride that says nothing."""
+    return torch.zeros(2 * (n + stride), dtype=dtype).as_strided((1, n), (stride, 1))
+
+
+@pytest.mark.parametrize("stride", [0, 1, 99, 129, 4096])
+def test_strides_of_one_row_say_nothing(gpu0, stride):
+    """Operands of one row are taken with any row stride, also unlike each other's."""
+    for call in (lambda: fp8hg.fp8_swiglu_ckpt(gpu0(row(128, stride)), gpu0(bf16(1, 128))),
+                 lambda: fp8hg.fp8_swiglu_ckpt(gpu0(bf16(1, 128)), gpu0(row(128, stride))),
+                 lambda: fp8hg.fp4_linear(gpu0(row(64, stride)), fp4(gpu0))):
+        with pytest.raises(Reached):
+            call()
+    assert lowbit._matrix(gpu0(row(100, stride))) == (1, 100, 112) and lowbit._ld(gpu0(row(100, stride))) == 112
+    q = fp4(gpu0, 1, 100)
+    broken("codes", row(64, stride, torch.uint8))(q)
+    assert q.ld() == 64 and q.buffers()[1] == 64
+    c = ckpt(gpu0, 1, 128)
+    c.gate.codes, c.up.scale = gpu0(row(128, stride, torch.uint8)), gpu0(row(4, stride, torch.uint8))
+    with pytest.raises(Reached):
+        fp8hg.fp8_swiglu_ckpt_bwd(gpu0(row(128, stride)), c)
+    native = lowbit._ckpt(c, gpu0(row(128, stride)))[0]
+    assert (native.ld_q, native.ld_s) == (128, 1)
