@@ -68,8 +68,7 @@ _cuda_device = torch._C._cuda_getDevice
 def _here(t) -> bool:
     """Whether t is on the current device: the one that a call launches on, and
     whose memory it may touch."""
-    device = t.get_device()
-    return device >= 0 and device == _cuda_device()
+    return t.get_device() == _cuda_device()   # -1 on the CPU
 
 
 # the allocation (sizes, strides, type) on the current device; torch.empty without
@@ -164,17 +163,22 @@ def _ts(t):
     return t.data_ptr()
 
 
-def _out_kind(out) -> int:
-    if out.dtype == torch.bfloat16:
+def _out_kind(dtype) -> int:
+    if dtype == torch.bfloat16:
         return OUT_BF16
-    if out.dtype == torch.float32:
+    if dtype == torch.float32:
         return OUT_FP32
     raise ValueError("out must be bfloat16 or float32")
 
 
-def _check_out(out, rows, cols):
+def _result(out, rows, cols, dtype):
+    """The caller's output, checked, or a new one of a type; its row stride and kind."""
+    if out is None:
+        dtype = dtype or torch.bfloat16
+        return _new((rows, cols), (cols, 1), dtype), cols, _out_kind(dtype)
     if tuple(out.shape) != (rows, cols) or not _here(out) or (out.stride(1) != 1 and cols > 1):
         raise ValueError(f"out must be a tensor [{rows}, {cols}] on the current CUDA device with unit column stride")
+    return out, _ld(out), _out_kind(out.dtype)
 
 
 def _opts(wait_limit_ns, inject_fault):
@@ -202,17 +206,18 @@ class Fp4Tensor:
     def buffers(self):
         """Address and row stride of the codes, address of the scale bytes, which
         have to hold what rows and k say."""
-        c, s = self.codes, self.scale
-        if not (_here(c) and _here(s)):
+        c, s, rows, n = self.codes, self.scale, self.rows, (self.k + 1) // 2
+        device = _cuda_device()
+        if c.get_device() != device or s.get_device() != device:
             raise ValueError("a 4-bit tensor's codes and scale must be on the current CUDA device")
-        rows, n = self.rows, (self.k + 1) // 2
-        if (c.dim() != 2 or c.element_size() != 1 or c.shape[0] < rows or c.shape[1] < n or
-                (c.stride(1) != 1 and n > 1)):
+        shape, stride = c.shape, c.stride()
+        if (len(shape) != 2 or shape[0] < rows or shape[1] < n or (stride[1] != 1 and n > 1) or
+                c.itemsize != 1):
             raise ValueError(f"codes must be a byte tensor of [{rows}, at least {n}] with unit column stride")
-        n = _scale_bytes(rows, self.k, self.kind)
-        if s.element_size() != 1 or s.numel() < n or not s.is_contiguous():
-            raise ValueError(f"scale must be a contiguous byte tensor of at least {n} elements")
-        return c.data_ptr(), self.ld(), s.data_ptr()
+        size = _scale_bytes(rows, self.k, self.kind)
+        if s.numel() < size or s.itemsize != 1 or not s.is_contiguous():
+            raise ValueError(f"scale must be a contiguous byte tensor of at least {size} elements")
+        return c.data_ptr(), stride[0] if rows > 1 else _round16(n), s.data_ptr()
 
     def operand(self) -> _Fp4Operand:
         codes, ld, scale = self.buffers()
@@ -238,11 +243,17 @@ def _scale_bytes(rows, k, kind) -> int:
     return (rows + 127) // 128 * ((k + 255) // 256) * (2048 if kind == FP4_NV else 1024)
 
 
-def _alloc(rows, k, kind, tensor_scale) -> Fp4Tensor:
-    """alloc_fp4 on the current device."""
+def _output(out, rows, k, kind, tensor_scale):
+    """The caller's 4-bit output, checked, or a new one (alloc_fp4 on the current
+    device), and what its buffers() returns."""
+    if out is not None:
+        if (out.rows, out.k, out.kind) != (rows, k, kind):
+            raise ValueError(f"out must be a 4-bit tensor [{rows}, {k}] of kind {kind}")
+        return out, out.buffers()
     ld = (k + 31) // 32 * 16
-    return Fp4Tensor(_new((rows, ld), (ld, 1), torch.uint8),
-                     _new((_scale_bytes(rows, k, kind),), (1,), torch.uint8), rows, k, kind, tensor_scale)
+    codes = _new((rows, ld), (ld, 1), torch.uint8)
+    scale = _new((_scale_bytes(rows, k, kind),), (1,), torch.uint8)
+    return Fp4Tensor(codes, scale, rows, k, kind, tensor_scale), (codes.data_ptr(), ld, scale.data_ptr())
 
 
 @_streamed
@@ -262,18 +273,6 @@ def fp4_tensor_scale(x, out=None):
 _NONE = (None, 0, None)
 
 
-def _quant(x, shape, kind, tensor_scale, rows_out, cols_out, what):
-    q = rows_out.buffers() if rows_out else _NONE
-    t = cols_out.buffers() if cols_out else _NONE
-    _check(_fns().fp4_quant(x.data_ptr(), *shape, kind, _ts(tensor_scale), *q, *t,
-                            _on(x)), what)
-
-
-def _check_fp4(q, rows, k, kind):
-    if (q.rows, q.k, q.kind) != (rows, k, kind):
-        raise ValueError(f"out must be a 4-bit tensor [{rows}, {k}] of kind {kind}")
-
-
 @_streamed
 def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
               out: Optional[Fp4Tensor] = None) -> Fp4Tensor:
@@ -281,12 +280,10 @@ def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
     columns, written as [cols, rows]."""
     shape = _matrix(x)
     rows, cols = (shape[1], shape[0]) if transpose else shape[:2]
-    if out is None:
-        out = _alloc(rows, cols, kind, tensor_scale)
-    _check_fp4(out, rows, cols, kind)
+    out, to = _output(out, rows, cols, kind, tensor_scale)
     out.tensor_scale = tensor_scale
-    _quant(x, shape, kind, tensor_scale, None if transpose else out, out if transpose else None,
-           "fp4_quant")
+    both = _NONE + to if transpose else to + _NONE
+    _check(_fns().fp4_quant(x.data_ptr(), *shape, kind, _ts(tensor_scale), *both, _on(x)), "fp4_quant")
     return out
 
 
@@ -296,25 +293,19 @@ def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Te
     """fp4_quant along the rows and along the columns from one read of x."""
     shape = _matrix(x)
     rows, cols = shape[:2]
-    out = out if out is not None else _alloc(rows, cols, kind, tensor_scale)
-    out_t = out_t if out_t is not None else _alloc(cols, rows, kind, tensor_scale)
-    _check_fp4(out, rows, cols, kind)
-    _check_fp4(out_t, cols, rows, kind)
+    out, to = _output(out, rows, cols, kind, tensor_scale)
+    out_t, to_t = _output(out_t, cols, rows, kind, tensor_scale)
     out.tensor_scale = out_t.tensor_scale = tensor_scale
-    _quant(x, shape, kind, tensor_scale, out, out_t, "fp4_quant_dual")
+    _check(_fns().fp4_quant(x.data_ptr(), *shape, kind, _ts(tensor_scale), *to, *to_t, _on(x)), "fp4_quant_dual")
     return out, out_t
 
 
 @_streamed
 def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None):
     """The values of a 4-bit tensor, [rows, k], BF16 or FP32."""
-    if out is None:
-        out = _new((q.rows, q.k), (q.k, 1), out_dtype or torch.bfloat16)
-    else:
-        _check_out(out, q.rows, q.k)
     op = q.operand()
-    _check(_fns().fp4_dequant(ctypes.byref(op), out.data_ptr(), _ld(out), _out_kind(out),
-                              _on(out)), "fp4_dequant")
+    out, ld_out, kind = _result(out, q.rows, q.k, out_dtype)
+    _check(_fns().fp4_dequant(ctypes.byref(op), out.data_ptr(), ld_out, kind, _on(out)), "fp4_dequant")
     return out
 
 
@@ -322,16 +313,12 @@ def fp4_dequant(q: Fp4Tensor, out=None, out_dtype=None):
 def fp4_gemm_scaled(a: Fp4Tensor, b: Fp4Tensor, out=None, out_dtype=None, accumulate: bool = False,
                     wait_limit_ns: int = 0, inject_fault: int = 0):
     """C = A B^T (or C += A B^T) on two 4-bit tensors of the same kind."""
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs out")
-        out = _new((a.rows, b.rows), (b.rows, 1), out_dtype or torch.bfloat16)
-    else:
-        _check_out(out, a.rows, b.rows)
+    if out is None and accumulate:
+        raise ValueError("accumulate needs out")
     oa, ob = a.operand(), b.operand()
-    _check(_fns().fp4_gemm_scaled(ctypes.byref(oa), ctypes.byref(ob), out.data_ptr(), _ld(out),
-                                  _out_kind(out), 1 if accumulate else 0,
-                                  _opts(wait_limit_ns, inject_fault), _on(out)),
+    out, ld_out, kind = _result(out, a.rows, b.rows, out_dtype)
+    _check(_fns().fp4_gemm_scaled(ctypes.byref(oa), ctypes.byref(ob), out.data_ptr(), ld_out, kind,
+                                  1 if accumulate else 0, _opts(wait_limit_ns, inject_fault), _on(out)),
            "fp4_gemm_scaled")
     return out
 
@@ -345,20 +332,16 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
     rows, k, ld = _matrix(x)
     if k != w.k:
         raise ValueError(f"x has {k} columns, w {w.k}")
-    if out is None:
-        out, ld_out = _new((rows, w.rows), (w.rows, 1), out_dtype or torch.bfloat16), w.rows
-    else:
-        _check_out(out, rows, w.rows)
-        ld_out = _ld(out)
+    ow = w.operand()
+    out, ld_out, kind = _result(out, rows, w.rows, out_dtype)
     stream = _on(x)
     n = 0 if rows <= 4 else _linear_bytes(rows, k, w.kind)
     if n and workspace is None:
         workspace = _scratch(n, x, stream)
     elif n and not (_here(workspace) and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
-    ow = w.operand()
     _check(_fns().fp4_linear(x.data_ptr(), rows, ld, _ts(tensor_scale), ctypes.byref(ow),
-                             out.data_ptr(), ld_out, _out_kind(out),
+                             out.data_ptr(), ld_out, kind,
                              workspace.data_ptr() if n else None, workspace.numel() if n else 0,
                              _opts(wait_limit_ns, inject_fault), stream), "fp4_linear")
     return out
@@ -431,30 +414,37 @@ def fp8_swiglu_ckpt(gate, up, fmt: int = E4M3, fmt_h: int = E4M3, checkpoint: bo
     return h, ckpt
 
 
+def _half(q, rows, cols, device):
+    """Addresses and row strides of a checkpoint half's codes and scales, which
+    have to hold [rows, cols] and a byte per 128 columns."""
+    c, s, groups = q.codes, q.scale, (cols + 127) // 128
+    if c.get_device() != device or s.get_device() != device:
+        raise ValueError("a checkpoint's codes and scales must be on the current CUDA device")
+    if c.shape != (rows, cols):
+        raise ValueError("dh and the checkpoint must have the same shape")
+    ld, unit = c.stride()
+    if c.itemsize != 1 or (unit != 1 and cols > 1):
+        raise ValueError("a checkpoint's codes must be bytes with unit column stride")
+    shape, stride = s.shape, s.stride()
+    if (len(shape) != 2 or shape[0] < rows or shape[1] < groups or (stride[1] != 1 and groups > 1) or
+            s.itemsize != 1):
+        raise ValueError(f"a checkpoint's scales must be bytes [{rows}, at least {groups}] with unit column stride")
+    return (c.data_ptr(), s.data_ptr(), ld, stride[0]) if rows > 1 else (c.data_ptr(), s.data_ptr(), _round16(cols),
+                                                                         groups)
+
+
 def _ckpt(c: SwigluCkpt, dh):
     """The checkpoint for the library; dh's rows, columns and row stride."""
     g, u = c.gate, c.up
     shape = rows, cols, _ = _matrix(dh, "dh")
-    if not (_here(g.codes) and _here(g.scale) and _here(u.codes) and _here(u.scale)):
-        raise ValueError("a checkpoint's codes and scales must be on the current CUDA device")
     if g.gran != GRAN_1x128 or u.gran != GRAN_1x128 or g.fmt != u.fmt:
         raise ValueError("a checkpoint has 1x128 scales and one format")
-    if g.codes.shape != (rows, cols) or u.codes.shape != (rows, cols):
-        raise ValueError("dh and the checkpoint must have the same shape")
-    groups = (cols + 127) // 128
-    for q in (g, u):
-        c, s = q.codes, q.scale
-        if c.element_size() != 1 or (c.stride(1) != 1 and cols > 1):
-            raise ValueError("a checkpoint's codes must be bytes with unit column stride")
-        if (s.dim() != 2 or s.element_size() != 1 or s.shape[0] < rows or s.shape[1] < groups or
-                (s.stride(1) != 1 and groups > 1)):
-            raise ValueError(f"a checkpoint's scales must be a byte tensor of [{rows}, at least {groups}] "
-                             "with unit column stride")
-    ld, ls = _ld(g.codes), g.scale.stride(0) if rows > 1 else groups
-    if ld != _ld(u.codes) or (rows > 1 and ls != u.scale.stride(0)):
+    device = dh.get_device()
+    gq, gs, ld, ls = _half(g, rows, cols, device)
+    uq, us, ld_u, ls_u = _half(u, rows, cols, device)
+    if ld != ld_u or ls != ls_u:
         raise ValueError("gate's and up's codes and scales must have the same strides")
-    return _Ckpt(g.codes.data_ptr(), g.scale.data_ptr(), u.codes.data_ptr(), u.scale.data_ptr(),
-                 rows, cols, ld, ls, g.fmt, 0), shape
+    return _Ckpt(gq, gs, uq, us, rows, cols, ld, ls, g.fmt, 0), shape
 
 
 @_streamed
@@ -462,11 +452,9 @@ def fp8_swiglu_ckpt_bwd(dh, ckpt: SwigluCkpt, out=None):
     """Gradients of gate and up from dh [rows, cols] and the checkpoint, BF16:
     one [rows, 2 cols] tensor, dgate in the first half, dup in the second."""
     c, (rows, cols, ld) = _ckpt(ckpt, dh)
-    if out is None:
-        out, ld_out = _new((rows, 2 * cols), (2 * cols, 1), torch.bfloat16), 2 * cols
-    else:
-        _check_out(out, rows, 2 * cols)
-        ld_out = _matrix(out, "out")[2]
+    out, ld_out, kind = _result(out, rows, 2 * cols, torch.bfloat16)
+    if kind != OUT_BF16:
+        raise ValueError("out must be bfloat16")
     to = out.data_ptr()
     _check(_fns().fp8_swiglu_ckpt_bwd(dh.data_ptr(), ld, ctypes.byref(c), to, to + 2 * cols, ld_out, _on(dh)),
            "fp8_swiglu_ckpt_bwd")
