@@ -248,6 +248,25 @@ __device__ bool wait_pair(uint32_t bar, uint32_t parity, uint64_t limit, volatil
     }
 }
 
+// The tensors' scales (NV) as two factors of a sum: 1 and their product, or, where
+// that leaves FP32's normal range (each may be 2^-100 .. 2^117), the smaller and the
+// larger.  A sum of products of codes and E4M3 scales is 0 or between 2^-20 and
+// 2^53 in magnitude, so its product with the smaller one leaves the range only if
+// the result does.
+template <bool NV>
+struct TensorScales {
+    float first = 1.0f, second = 1.0f;
+    bool split = false;
+    __device__ __forceinline__ explicit TensorScales(const Params &p) {
+        if constexpr (NV) {
+            const float a = p.ta ? ptx::ld_f32(p.ta) : 1.0f, b = p.tb ? ptx::ld_f32(p.tb) : 1.0f;
+            second = a * b;
+            split = !(second >= 0x1p-126f && second < 0x1p128f);
+            if (split) first = a < b ? a : b, second = a < b ? b : a;
+        }
+    }
+};
+
 // The tiles of a pair, in order: the wide ones dealt round, then those of one
 // part, which first go to the pairs that the last deal left out, two each.
 struct PairTiles {
@@ -340,7 +359,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         ptx::setmaxnreg_inc<168>();
         const int q = warp & 3, half = (warp - 4) >> 2;
         uint8_t *stage = gbase + L::OFF_EPI + (warp - 4) * EPI_BYTES;
-        const float alpha = (p.ta ? ptx::ld_f32(p.ta) : 1.0f) * (p.tb ? ptx::ld_f32(p.tb) : 1.0f);
+        const TensorScales<NV> ts(p);
+        const float alpha = ts.second;
         // a C that is added to, four values at a time (without `accumulate` such a C is TMA's)
         const bool vec = p.accumulate && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % 4 == 0;
         for (int i = 0, mb, nb; tiles.get<NH>(p, i, mb, nb) > half; ++i) {
@@ -356,26 +376,29 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_relaxed(tempty_l + 8 * half);
             };
-            if (p.out_fp32 || p.accumulate) {
+            // (scales in two steps are rare: they take this path too, and cost the other nothing)
+            if (p.out_fp32 || p.accumulate || ts.split) {
+                const bool tma = p.c_tma && p.out_fp32;
 #pragma unroll 1
                 for (int part = 0; part < 3; ++part) {
                     uint32_t r[2][32];
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        ptx::tmem_ld_32x32b_x32(taddr + (part * (2) + c) * 32, r[c]);
+                        ptx::tmem_ld_32x32b_x32(taddr + (part * 2 + c) * 32, r[c]);
                     ptx::tmem_wait_ld();
                     if (part == 2) release();
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int at = (part * (2) + c) * 32;
+                        const int at = (part * 2 + c) * 32;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) r[c][e] = __float_as_uint(__uint_as_float(r[c][e]) * alpha);
-                        if (p.c_tma && lane == 0) ptx::bulk_wait_read();
+                        for (int e = 0; e < 32; ++e)
+                            r[c][e] = __float_as_uint(__uint_as_float(r[c][e]) * ts.first * alpha);
+                        if (tma && lane == 0) ptx::bulk_wait_read();
                         __syncwarp();
                         stage_row(stage, lane, r[c]);
-                        if (p.c_tma) ptx::fence_proxy_async_smem();
+                        if (tma) ptx::fence_proxy_async_smem();
                         __syncwarp();
-                        if (!p.c_tma) {
+                        if (!tma) {
                             write_f32(stage, lane, p, row0, col0 + at, vec);
                         } else if (lane == 0 && row0 < p.M && col0 + at < p.N) {
                             ptx::tma_store_2d(&tmap_c, ptx::smem_u32(stage), static_cast<int>(col0) + at,
@@ -917,7 +940,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         __syncthreads();
     }
     if (!*abort_flag) {
-        const float alpha = (p.ta ? ptx::ld_f32(p.ta) : 1.0f) * (p.tb ? ptx::ld_f32(p.tb) : 1.0f);
+        const TensorScales<NV> ts(p);
         // this CTA's rows, one to a thread group's lane; columns go round the
         // groups
         const float *sum = reinterpret_cast<const float *>(gbase + L::OFF_SUM);
@@ -937,7 +960,8 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                         if (c + i * dc < cols) v[i] += sum[((k * BN + c + i * dc) << rl) + r];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (c + i * dc < cols) store_out(p, row * p.sm + (col0 + c + i * dc) * p.sn, v[i] * alpha);
+                    if (c + i * dc < cols)
+                        store_out(p, row * p.sm + (col0 + c + i * dc) * p.sn, v[i] * ts.first * ts.second);
             }
         }
     }

@@ -57,7 +57,8 @@ size_t fp4_scale_bytes(int64_t rows, int64_t k, int kind);
  * fp4_tensor_scale — the FP32 scale of a tensor for FP4HG_NV: the smallest
  * power of two t with amax <= 6 * 448 * t, so that no block's scale saturates;
  * 1 for a tensor of zeros.  NaNs and infinities are left out of amax (their
- * blocks are marked by the quantizer); t is at least 2^-100.
+ * blocks are marked by the quantizer); t is at least 2^-100 and, as amax is
+ * below 2^128, at most 2^117.
  *
  *   x          [rows, cols] BF16, row stride ld_x elements, 2-byte aligned
  *   scale      device pointer, one float
@@ -77,7 +78,8 @@ int fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x
  *                 cols, 2-byte aligned (16-byte loads where x is 16-byte
  *                 aligned and ld_x a multiple of 8)
  *   tensor_scale  FP4HG_NV: device pointer to t, or NULL for 1; a positive
- *                 normal number between 2^-100 and 2^100.  FP4HG_MX: NULL
+ *                 number between 2^-100 and 2^117 (what fp4_tensor_scale
+ *                 gives).  FP4HG_MX: NULL
  *   q, scale      codes [rows, ceil(cols / 2)] (ld_q bytes, a multiple of 16,
  *                 16-byte aligned) and scale bytes of the [rows, cols] tensor,
  *                 or both NULL
@@ -121,6 +123,8 @@ int fp4_dequant(const fp4hg_operand *a, void *out, int64_t ld_out, int out_kind,
  *               element size
  *   opts        NULL or fp8hg_gemm_opts (tile must be 0): bounded waits as in
  *               fp8_gemm_scaled_ex
+ * The tensors' scales meet the FP32 sums one after the other where their product
+ * is no normal FP32 number: C overflows or vanishes only where its value does.
  */
 int fp4_gemm_scaled(const fp4hg_operand *a, const fp4hg_operand *b, void *c, int64_t ldc, int out,
                     int accumulate, const fp8hg_gemm_opts *opts, void *stream);

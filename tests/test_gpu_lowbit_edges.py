@@ -70,3 +70,82 @@ def test_strides_of_one_row(cuda_lib, n, stride):
             to = one_row(y.to(out), stride)
             fp8hg.fp4_gemm_scaled(q, w, out=to)
             assert torch.equal(to, fp8hg.fp4_gemm_scaled(q, w, out_dtype=out))
+
+
+# ----------------------------------------------------------- scales far apart
+def extreme(rows, k, bytes_, seed, t):
+    """An NV tensor of positive values with scale bytes in a range, the first row
+    zeros, and its values without t."""
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(1, 8, (rows, k)).astype(np.uint8)
+    codes[0] = 0
+    scales = rng.integers(*bytes_, (rows, -(-k // 16))).astype(np.uint8)
+    q = fp8hg.Fp4Tensor(torch.from_numpy(ref.pack(codes)).cuda(),
+                        torch.from_numpy(ref.tile_scales(scales, k, NV)).cuda(), rows, k, NV,
+                        torch.tensor([t], dtype=torch.float32, device="cuda"))
+    return q, ref.fp4_values(codes, scales, NV)
+
+
+HIGH, LOW = (0x70, 0x7F), (0x01, 0x04)     # E4M3 scales of 128 .. 448, of 2^-9 .. 3 2^-9
+# tensor scales whose product is 0, subnormal (not a power of two: bits lost), infinite, or in range
+PAIRS = [(2.0 ** -75, 2.0 ** -76, HIGH), (1.37 * 2.0 ** -100, 1.21 * 2.0 ** -40, HIGH),
+         (2.0 ** 65, 2.0 ** 65, LOW), (2.0 ** 117, 2.0 ** 15, LOW), (2.0 ** 117, 2.0 ** -100, HIGH),
+         (1.5 * 2.0 ** -100, 2.0 ** 100, LOW)]
+
+
+@pytest.mark.parametrize("m,n", [(3, 140), (40, 200), (150, 300), (700, 900), (3000, 2300)])
+@pytest.mark.parametrize("ta,tb,bytes_", PAIRS)
+def test_tensor_scales_whose_product_leaves_fp32(cuda_lib, m, n, ta, tb, bytes_):
+    """Results in FP32's normal range are right wherever the product of the two
+    scales lies, and zero rows are zeros.  The sums are within 2^-21 a step of 64
+    products (as everywhere in these tests; all products are positive); each scale
+    factor and the output round once more."""
+    k = 1024 if bytes_ == HIGH else 64
+    a, va = extreme(m, k, bytes_, m + n, ta)
+    b, vb = extreme(n, k, bytes_, m + n + 1, tb)
+    ta, tb = float(np.float32(ta)), float(np.float32(tb))
+    c = va @ vb.T
+    assert 2.0 ** -125 < c[1:, 1:].min() * ta * tb and c.max() * ta * tb < 2.0 ** 127
+    tol = ((k // 64 + 4) * 2.0 ** -21 + 2 * 2.0 ** -24) * c
+    for out, ulp in ((torch.float32, 2.0 ** -23), (torch.bfloat16, 2.0 ** -8)):
+        got = fp8hg.fp4_gemm_scaled(a, b, out_dtype=out)
+        v = got.double().cpu().numpy() / ta / tb
+        assert (np.abs(v - c) <= tol + ulp * c).all(), float(np.nanmax(np.abs(v - c) / np.maximum(c, 1e-30)))
+        assert not v[0].any() and not v[:, 0].any()
+        added = torch.zeros_like(got)
+        fp8hg.fp4_gemm_scaled(a, b, out=added, accumulate=True)
+        assert torch.equal(added, got)
+
+
+@pytest.mark.parametrize("value", [2.0 ** 55, 2.0 ** 58])
+def test_decoding_with_scales_whose_product_leaves_fp32(cuda_lib, value):
+    """x quantized inside the product and before it, tensor scales of 2^65 each:
+    rows of zeros give zeros (at 2^55 all are, x's block scales round to 0)."""
+    k, t = 512, 2.0 ** 65
+    w, vw = extreme(300, k, LOW, 1, t)
+    for m in (1, 4, 9):
+        x = np.zeros((m, k))
+        x[1:] = value
+        codes, scales = ref.fp4_quant(x, NV, t)
+        c = ref.fp4_values(codes, scales, NV) @ vw.T
+        assert c.max() * t * t < 2.0 ** 127 and (m == 1 or c.any() == (value > 2.0 ** 56))
+        y = fp8hg.fp4_linear(torch.from_numpy(x).cuda().bfloat16(), w, torch.tensor([t], device="cuda"))
+        v = y.double().cpu().numpy() / t / t
+        assert (np.abs(v - c) <= ((k // 64 + 4) * 2.0 ** -21 + 2.0 ** -8) * c).all()
+
+
+def test_largest_tensor_scale(cuda_lib):
+    """The scale of a tensor that holds BF16's largest value is 2^117, and the
+    quantizer takes it."""
+    x = rand(5, 512, 7).float() * 2.0 ** 120
+    x[2, 3] = torch.finfo(torch.bfloat16).max
+    x = x.bfloat16()
+    ts = fp8hg.fp4_tensor_scale(x)
+    assert ts.item() == 2.0 ** 117
+    codes, scales = ref.fp4_quant(x.double().cpu().numpy(), NV, 2.0 ** 117)
+    q, qt = fp8hg.fp4_quant_dual(x, NV, ts)
+    assert np.array_equal(q.scales().cpu().numpy(), scales)
+    assert np.array_equal(ref.unpack(q.codes.cpu().numpy(), 512), codes)
+    codes, scales = ref.fp4_quant(x.t().double().cpu().numpy(), NV, 2.0 ** 117)
+    assert np.array_equal(qt.scales().cpu().numpy(), scales)
+    assert np.array_equal(ref.unpack(qt.codes.cpu().numpy(), 5), codes)
