@@ -579,6 +579,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                             mma_pair<NV, L, 1>(tmem, col, ad, bd, idesc, 0, shift, j, 1u);
                             mma_pair<NV, L, 2>(tmem, col, ad, bd + (L::BH >> 4), idesc, 1, shift, j, 1u);
                         }
+                        if (!ok) break;
                         ptx::tc_commit_pair(empty + 8 * s, 0x3);
                     }
                     if (p.nk == 1) continue;
@@ -621,7 +622,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                             ptx::tc_cp_32x128b_warpx4_pair(d + g * L::GC, sd + g * 32);
                             if (g == L::NG / SUB - 1) ptx::tc_commit_pair(bar + 8 * s, 0x1);   // for the MMAs
                         }
-                        if (SUB == 2) ptx::tc_commit_pair(rest + 8 * s, 0x1);
+                        // inject = 2 (a test of the timeout path): the second half
+                        // of the first pair's second tile's second stage never comes
+                        if (SUB == 2 && !(p.inject == 2 && pair == 0 && it == static_cast<uint32_t>(p.nk) + 1))
+                            ptx::tc_commit_pair(rest + 8 * s, 0x1);
                         ptx::tc_commit_pair(scales + 8 * s, 0x3);   // for the scale producers
                     }
                 }
@@ -1174,6 +1178,7 @@ int launch(const Fp4GemmArgs &g, int sms, cudaStream_t stream) {
     }
     const bool swapped = g.a.rows <= g.b.rows;
     const Plan plan = choose(g.a.rows, g.b.rows, p.nk, sms);
+    if (p.inject == 2 && plan.nh != 2) return 1;   // no stage's scales come in halves
     if (plan.nh == 2) return launch_pair<NV, 2>(g, p, sms, stream);
     if (plan.nh == 1) return launch_pair<NV, 1>(g, p, sms, stream);
     switch (plan.bn) {

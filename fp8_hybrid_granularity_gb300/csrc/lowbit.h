@@ -62,8 +62,8 @@ struct Fp4GemmArgs {
 };
 // Whether launch_fp4_gemm takes so many rows of A in BF16.
 bool fp4_linear_quantizes(int64_t rows);
-// 0 on success, 1 if a tensor map could not be encoded, cudaError_t + 2 on a
-// launch failure.
+// 0 on success, 1 if a tensor map could not be encoded or a fault cannot be
+// injected in the kernel that the shape takes, cudaError_t + 2 on a launch failure.
 int launch_fp4_gemm(const Fp4GemmArgs &g, cudaStream_t stream);
 
 struct SwigluFwdArgs {

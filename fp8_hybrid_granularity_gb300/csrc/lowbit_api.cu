@@ -50,9 +50,9 @@ int check_output(const void *c, int64_t ldc, int64_t cols, int out) {
     return aligned(c, out == FP8HG_OUT_BF16 ? 2 : 4) ? FP8HG_OK : FP8HG_ERR_ALIGNMENT;
 }
 
-int check_opts(const fp8hg_gemm_opts *opts) {
+int check_opts(const fp8hg_gemm_opts *opts, int max_inject) {
     if (!opts) return FP8HG_OK;
-    if (opts->inject_fault < 0 || opts->inject_fault > 1) return FP8HG_ERR_INVALID_ARG;
+    if (opts->inject_fault < 0 || opts->inject_fault > max_inject) return FP8HG_ERR_INVALID_ARG;
     return opts->tile == 0 ? FP8HG_OK : FP8HG_ERR_UNSUPPORTED;
 }
 
@@ -73,7 +73,7 @@ int run_gemm(fp8hg::Fp4GemmArgs &g, const fp8hg_gemm_opts *opts, void *stream) {
     g.inject_fault = opts ? opts->inject_fault : 0;
     g.err = err;
     const int rc = fp8hg::launch_fp4_gemm(g, static_cast<cudaStream_t>(stream));
-    if (rc == 1) return FP8HG_ERR_UNSUPPORTED;   // a tensor map could not be encoded
+    if (rc == 1) return FP8HG_ERR_UNSUPPORTED;
     return rc == 0 ? FP8HG_OK : FP8HG_ERR_CUDA;
 }
 
@@ -183,7 +183,7 @@ int fp4_gemm_scaled(const fp4hg_operand *a, const fp4hg_operand *b, void *c, int
     if (st != FP8HG_OK) return st;
     if (a->kind != b->kind) return FP8HG_ERR_UNSUPPORTED;
     if (a->k != b->k || a->k == 0) return FP8HG_ERR_SHAPE;
-    st = check_opts(opts);
+    st = check_opts(opts, a->kind == FP4HG_NV ? 2 : 1);
     if (st != FP8HG_OK) return st;
     if (a->rows == 0 || b->rows == 0) return FP8HG_OK;
     st = check_output(c, ldc, b->rows, out);
@@ -214,7 +214,7 @@ int fp4_linear(const uint16_t *x, int64_t rows, int64_t ld_x, const float *tenso
     if (st != FP8HG_OK) return st;
     if (tensor_scale && w->kind == FP4HG_MX) return FP8HG_ERR_INVALID_ARG;
     if (tensor_scale && !aligned(tensor_scale, 4)) return FP8HG_ERR_ALIGNMENT;
-    st = check_opts(opts);
+    st = check_opts(opts, 1);
     if (st != FP8HG_OK) return st;
     if (rows == 0 || w->rows == 0) return FP8HG_OK;
     st = check_output(y, ld_y, w->rows, out);

@@ -122,7 +122,11 @@ int fp4_dequant(const fp4hg_operand *a, void *out, int64_t ld_out, int out_kind,
  *   c           [a->rows, b->rows], row stride ldc elements, aligned to its
  *               element size
  *   opts        NULL or fp8hg_gemm_opts (tile must be 0): bounded waits as in
- *               fp8_gemm_scaled_ex
+ *               fp8_gemm_scaled_ex; tiles of C that a wait has run out for are
+ *               not written.  inject_fault = 1: the first CTA never issues its
+ *               first copy; 2 (FP4HG_NV): half of the scales of one stage of K
+ *               never come, late in the first CTAs' work (FP8HG_ERR_UNSUPPORTED
+ *               for shapes whose kernel has no such halves)
  * The tensors' scales meet the FP32 sums one after the other where their product
  * is no normal FP32 number: C overflows or vanishes only where its value does.
  */

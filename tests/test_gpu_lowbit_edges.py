@@ -149,3 +149,46 @@ def test_largest_tensor_scale(cuda_lib):
     codes, scales = ref.fp4_quant(x.t().double().cpu().numpy(), NV, 2.0 ** 117)
     assert np.array_equal(qt.scales().cpu().numpy(), scales)
     assert np.array_equal(ref.unpack(qt.codes.cpu().numpy(), 5), codes)
+
+
+# ------------------------------------------------- a wait that runs out late
+@pytest.mark.parametrize("out,added", [(torch.bfloat16, False), (torch.float32, False), (torch.float32, True),
+                                       (torch.bfloat16, True)], ids=["bf16", "f32", "f32-added", "bf16-added"])
+def test_wait_that_runs_out_within_a_stage(cuda_lib, out, added):
+    """Half of a stage's scales withheld in a pair's second tile, the stages after
+    it on their way: the status reads TIMEOUT once, what is stored is right, the tile is
+    not stored, and the next call is right.  Added to a C of odd rows the first
+    tile is stored long after that wait has begun: the second one's accumulator is
+    waited for last."""
+    from test_gpu_fp4 import bound, check_product, product, stored
+    m, n, k = 9000, 3840, 1024                 # wide tiles, four stages each, five a pair
+    a, va = stored(m, k, NV, 101)
+    b, vb = stored(n, k, NV, 102)
+    c, s = product(va, vb)
+    mark = 0.0 if added else float(torch.tensor(1e9).to(out))
+    assert np.abs(c).max() < 1e8
+    got = torch.empty((m, n + 1), dtype=out, device="cuda")[:, 1:] if added else torch.empty((m, n), dtype=out,
+                                                                                            device="cuda")
+    tol = bound(s, k, c, out)
+    for _ in range(6):
+        got.fill_(mark)
+        fp8hg.fp4_gemm_scaled(a, b, out=got, accumulate=added, wait_limit_ns=20_000_000, inject_fault=2)
+        assert fp8hg.fp8hg_get_device_error() == 6 and fp8hg.fp8hg_get_device_error() == 0
+        v = got.double().cpu().numpy()
+        wrong = (np.abs(v - c) > tol) & (v != mark)
+        assert not wrong.any(), np.argwhere(wrong)[:4]
+        assert (v == mark).any()
+    got.fill_(0)
+    check_product(fp8hg.fp4_gemm_scaled(a, b, out=got, accumulate=added), c, s, k)
+    assert fp8hg.fp8hg_get_device_error() == 0
+
+
+def test_fault_that_a_shape_cannot_have(cuda_lib):
+    from test_gpu_fp4 import stored
+    for kind, status in ((MX, 1), (NV, 4)):
+        a, b = stored(3, 64, kind, 1)[0], stored(40, 64, kind, 2)[0]
+        with pytest.raises(fp8hg.Fp8hgError) as e:
+            fp8hg.fp4_gemm_scaled(a, b, inject_fault=2)
+        assert e.value.status == status
+    with pytest.raises(fp8hg.Fp8hgError):
+        fp8hg.fp4_linear(rand(9, 64, 1), b, inject_fault=2)
