@@ -192,3 +192,14 @@ def test_fault_that_a_shape_cannot_have(cuda_lib):
         assert e.value.status == status
     with pytest.raises(fp8hg.Fp8hgError):
         fp8hg.fp4_linear(rand(9, 64, 1), b, inject_fault=2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n", [(1000, 3584), (2048, 2300)])
+def test_product_of_a_long_k(cuda_lib, m, n, kind):
+    """74 stages of K in the kernels of larger products."""
+    from test_gpu_fp4 import check_product, product, stored
+    k = 18944
+    a, va = stored(m, k, kind, 111)
+    b, vb = stored(n, k, kind, 112)
+    check_product(fp8hg.fp4_gemm_scaled(a, b, out_dtype=torch.float32), *product(va, vb), k)
