@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256, kRowThreadsPerSm / 256)
                uint8_t *s, uint32_t tiles, int segs, int total_segs) {
     ptx::grid_begin(static_cast<int64_t>(rows) * cols);
     const int tid = threadIdx.x, lane = tid & 31;
-    const int seg = blockIdx.y * segs + tid % segs;
+    const int seg = blockIdx.x * segs + tid % segs;
     const int rpb = blockDim.x / segs;
     const float t = NV && ts ? ptx::ld_f32(ts) : 1.0f, rt = fp4_reciprocal<NV>(t);
     const int c0 = seg * 16;
@@ -78,14 +78,14 @@ __global__ void __launch_bounds__(256, kRowThreadsPerSm / 256)
     // The next row's load is in flight while a row is cast: a CTA per row
     // spent most of its time waiting for its one load (8192 x 3584, NV: 23.6 us).
     // Every lane of the warp stays in the loop for the shuffles.
-    const uint32_t step = gridDim.x * rpb;
+    const uint32_t step = gridDim.y * rpb;
     const bool mine = tid / segs < rpb && seg < total_segs;
     uint32_t next[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     auto load = [&](uint32_t r) {
         if (mine && r < rows && c0 < cols) ragged::load16<WIDE>(x + row_at(r, ld_x) + c0, cols - c0, next);
     };
-    load(blockIdx.x * rpb + tid / segs);
-    for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step) {
+    load(blockIdx.y * rpb + tid / segs);
+    for (uint32_t r0 = blockIdx.y * rpb; r0 < rows; r0 += step) {
         const uint32_t r = r0 + tid / segs;
         const bool in = mine && r < rows;
         uint32_t w[8];
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
                   void *out, uint32_t ld_out, int segs) {
     ptx::grid_begin(static_cast<int64_t>(rows) * k);
     const float t = NV && ts ? ptx::ld_f32(ts) : 1.0f;
-    const int g = blockIdx.y * blockDim.x + threadIdx.x;
+    const int g = blockIdx.x * blockDim.x + threadIdx.x;
     const int c0 = g * 16, left = k - c0;
     // the next row's codes and scale are in flight while a row is written
     uint2 next = make_uint2(0u, 0u);
@@ -329,10 +329,10 @@ __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
         }
         next_scale = ptx::ld_u8(s + fp4_scale_offset(r, NV ? g : g >> 1, tiles));
     };
-    load(blockIdx.x);
-    for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    load(blockIdx.y);
+    for (uint32_t r = blockIdx.y; r < rows; r += gridDim.y) {
         const uint32_t w[2] = {next.x, next.y}, byte = next_scale;
-        load(r + gridDim.x);
+        load(r + gridDim.y);
         float v[16];
         if (g < segs) {
             const float sc = fp4_scale_value<NV>(byte);
@@ -392,7 +392,7 @@ cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
     const int64_t rblocks = (static_cast<int64_t>(a.rows) + rpb - 1) / rpb, cblocks = (total + segs - 1) / segs;
     // as many CTAs as fit at once
     const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kRowThreadsPerSm / threads) / cblocks);
-    const dim3 grid(static_cast<unsigned>(std::min(rblocks, resident)), static_cast<unsigned>(cblocks));
+    const dim3 grid = chunks_first(std::min(rblocks, resident), cblocks);
     const int64_t tiles = fp4_scale_tiles(a.cols, a.kind);
     return launch_after(ragged::wide(a.x, a.ld_x) ? k_fp4_rows<NV, true> : k_fp4_rows<NV, false>, grid, threads, 0,
                         stream, 1, a.x, a.rows, a.cols, a.ld_x, a.ts, a.q, a.ld_q, a.s, tiles, segs, total);
@@ -445,7 +445,7 @@ cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, uint32_t ld_out, 
     const int64_t cb = (segs + threads - 1) / threads;
     // as many CTAs as fit at once
     const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kDequantThreadsPerSm / threads) / cb);
-    const dim3 grid(static_cast<unsigned>(std::min(a.rows, resident)), static_cast<unsigned>(cb));
+    const dim3 grid = chunks_first(std::min(a.rows, resident), cb);
     auto go = [&](auto kern) {
         return launch_after(kern, grid, threads, 0, stream, 1, a.codes, a.scale, a.ts, a.rows, a.k, a.ld, tiles, out,
                             ld_out, segs);

@@ -20,12 +20,13 @@ inline bool valid_fmt(int f) { return f == FP8HG_E4M3 || f == FP8HG_E5M2; }
 inline bool valid_kind(int k) { return k == FP4HG_MX || k == FP4HG_NV; }
 
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;   // 2 s
-// Sizes a grid or a tensor map can still hold: 2^30 along a contraction or a
-// row, 65535 tiles of 128 in a grid's second dimension.
+// What 32-bit indices of rows, columns and tiles hold with room to spare.
 constexpr int64_t kMaxDim = int64_t(1) << 30;
 // Row strides (elements or bytes) of what the element-wise kernels touch.
 constexpr int64_t kMaxLd = 0x7FFFFFFF;
-constexpr int64_t kMaxTiled = int64_t(65535) * 128;
+// Rows of the quantizer along the columns: its tiles of 128, in pairs (the scales'
+// padding to 256), are a grid's second dimension.
+constexpr int64_t kMaxTileRows = fp8hg::kGridY / 2 * int64_t(256);
 
 // A 4-bit operand of a call that reads it.
 int check_operand(const fp4hg_operand *o) {
@@ -153,7 +154,7 @@ int fp4_quant(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x, int k
     if (st != FP8HG_OK) return st;
     st = check_codes(q_t, ld_qt, (rows + 1) / 2, scale_t);
     if (st != FP8HG_OK) return st;
-    if (q_t && rows > kMaxTiled) return FP8HG_ERR_SHAPE;
+    if (q_t && rows > kMaxTileRows) return FP8HG_ERR_SHAPE;
     return status_from_cuda(fp8hg::launch_fp4_quant({x, static_cast<int>(rows), static_cast<int>(cols), u32(ld_x),
                                                      kind, tensor_scale, q, u32(ld_q), scale, q_t, u32(ld_qt),
                                                      scale_t},
@@ -299,7 +300,7 @@ int fp8_swiglu_ckpt_bwd_q(const uint16_t *dh, int64_t ld_dh, const fp8hg_swiglu_
     st = check_input(dh, c->rows, c->cols, ld_dh);
     if (st != FP8HG_OK) return st;
     if (c->rows == 0 || c->cols == 0) return FP8HG_OK;
-    if (c->rows % 128 || c->cols % 128 || c->rows > kMaxTiled) return FP8HG_ERR_SHAPE;
+    if (c->rows % 128 || c->cols % 128) return FP8HG_ERR_SHAPE;
     if (!aligned(dh, 16) || ld_dh % 8) return FP8HG_ERR_ALIGNMENT;
     fp8hg::SwigluGrads o{{g->dgate_q, g->dup_q}, {g->dgate_s, g->dup_s},
                          {g->dgate_qt, g->dup_qt, g->h_qt}, {g->dgate_st, g->dup_st, g->h_st},

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(256, kFwdThreadsPerSm / 256)
     k_swiglu_fwd(const SwigluFwdArgs a, int segs, int total_segs) {
     ptx::grid_begin(static_cast<int64_t>(a.rows) * a.cols);
     const int tid = threadIdx.x;
-    const int seg = blockIdx.y * segs + tid % segs;
+    const int seg = column_chunk() * segs + tid % segs;
     const int rpb = blockDim.x / segs;
     const int c0 = seg * 16, left = a.cols - c0;
     // the next row's loads are in flight while a row is computed
@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(256)
     ptx::grid_begin(static_cast<int64_t>(c.rows) * c.cols);
     // a warp takes 32 neighbouring segments of one row, whole warps past the
     // row's end included: the stores exchange values between lanes
-    const int seg = (blockIdx.y * blockDim.x + threadIdx.x);
+    const int seg = (blockIdx.x * blockDim.x + threadIdx.x);
     const int c0 = seg * 16, left = c.cols - c0;
-    for (uint32_t r = blockIdx.x; r < static_cast<uint32_t>(c.rows); r += gridDim.x) {
+    for (uint32_t r = blockIdx.y; r < static_cast<uint32_t>(c.rows); r += gridDim.y) {
         uint32_t og[8] = {0, 0, 0, 0, 0, 0, 0, 0}, ou[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (seg < segs) {
             uint32_t w[8], gc[4], uc[4];
@@ -488,7 +488,7 @@ cudaError_t fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
     const int64_t rb = (static_cast<int64_t>(a.rows) + rpb - 1) / rpb, cb = (total + segs - 1) / segs;
     // as many CTAs as fit at once
     const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kFwdThreadsPerSm / threads) / cb);
-    const dim3 grid(static_cast<unsigned>(std::min(rb, resident)), static_cast<unsigned>(cb));
+    const dim3 grid = rows_first(std::min(rb, resident), cb);
     const bool wide = ragged::wide(a.gate, a.ld_in) && ragged::wide(a.up, a.ld_in);
     return launch_after(wide ? k_swiglu_fwd<FH, FC, CKPT, true> : k_swiglu_fwd<FH, FC, CKPT, false>, grid, threads, 0,
                         stream, 1, a, segs, total);
@@ -511,7 +511,7 @@ cudaError_t launch_swiglu_bwd(const uint16_t *dh, uint32_t ld_dh, const SwigluCk
     // a row's segments in equal blocks of whole warps
     const int64_t segs = (c.cols + 15LL) / 16, chunks = (segs + 255) / 256;
     const int threads = static_cast<int>(((segs + chunks - 1) / chunks + 31) / 32 * 32);
-    const dim3 grid(static_cast<unsigned>(c.rows), static_cast<unsigned>((segs + threads - 1) / threads));
+    const dim3 grid = chunks_first(c.rows, (segs + threads - 1) / threads);
     const bool wide = ragged::wide(dh, ld_dh) && ragged::wide(dg, ld_d) && ragged::wide(du, ld_d);
     auto go = [&](auto kern) {
         return launch_after(kern, grid, threads, 0, stream, 1, dh, ld_dh, c, dg, du, ld_d, segs);

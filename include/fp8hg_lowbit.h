@@ -84,7 +84,7 @@ int fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x
  *                 16-byte aligned) and scale bytes of the [rows, cols] tensor,
  *                 or both NULL
  *   q_t, scale_t  codes [cols, ceil(rows / 2)] (ld_qt) and scale bytes of the
- *                 [cols, rows] tensor, or both NULL
+ *                 [cols, rows] tensor, or both NULL; rows at most 32767 * 256
  * Blocks run from the first column (row); the last one may be shorter.  The
  * unused half of a last byte is 0.  Scale arrays are 16-byte aligned.
  */

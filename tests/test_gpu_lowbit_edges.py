@@ -203,3 +203,88 @@ def test_product_of_a_long_k(cuda_lib, m, n, kind):
     a, va = stored(m, k, kind, 111)
     b, vb = stored(n, k, kind, 112)
     check_product(fp8hg.fp4_gemm_scaled(a, b, out_dtype=torch.float32), *product(va, vb), k)
+
+
+# ------------------------------------------------------------------ long axes
+LONG = 65536 * 4096 + 3 * 4096 + 304      # columns: more chunks of 4096 than a grid has in its second dimension
+
+
+def folded(x):
+    """The whole chunks of 4096 columns of a few long rows, as rows of 4096."""
+    return x[:, :LONG // 4096 * 4096].reshape(-1, 4096)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_quantizer_of_very_long_rows(cuda_lib, kind):
+    """Two rows of 2^28 columns and more, against the same data in short rows."""
+    x = rand(2, LONG, 121)
+    q, short = fp8hg.fp4_quant(x, kind), fp8hg.fp4_quant(folded(x).contiguous(), kind)
+    assert torch.equal(folded(q.codes.repeat_interleave(2, 1)[:, :LONG])[:, ::2], short.codes)
+    n = 4096 // ref.BLOCK[kind]
+    whole = LONG // 4096 * n
+    assert torch.equal(q.scales()[:, :whole].reshape(-1, n), short.scales())
+    tail = fp8hg.fp4_quant(x[:, whole * ref.BLOCK[kind]:], kind)
+    assert torch.equal(q.scales()[:, whole:], tail.scales())
+    v = fp8hg.fp4_dequant(q)
+    assert torch.equal(folded(v), fp8hg.fp4_dequant(short))
+    assert torch.equal(v[:, whole * ref.BLOCK[kind]:], fp8hg.fp4_dequant(tail))
+    del v
+    assert torch.equal(folded(fp8hg.fp4_dequant(q, out_dtype=torch.float32)),
+                       fp8hg.fp4_dequant(short, out_dtype=torch.float32))
+
+
+def test_swiglu_of_very_long_rows(cuda_lib):
+    g, u, dh = (rand(2, LONG, 131 + i) for i in range(3))
+    cut = LONG // 4096 * 4096
+    h, ck = fp8hg.fp8_swiglu_ckpt(g, u)
+    parts = [[folded(t).contiguous() for t in (g, u, dh)], [t[:, cut:] for t in (g, u, dh)]]
+    d = fp8hg.fp8_swiglu_ckpt_bwd(dh, ck)
+    halves = [d[:, :LONG], d[:, LONG:]]
+    for i, (pg, pu, pdh) in enumerate(parts):
+        at = (lambda t: t[:, cut:]) if i else folded
+        ats = (lambda s: s[:, cut // 128:]) if i else lambda s: s[:, :cut // 128].reshape(-1, 32)
+        ph, pck = fp8hg.fp8_swiglu_ckpt(pg, pu)
+        for a, b in ((h, ph), (ck.gate, pck.gate), (ck.up, pck.up)):
+            assert torch.equal(at(a.codes), b.codes) and torch.equal(ats(a.scales()), b.scales())
+        pd = fp8hg.fp8_swiglu_ckpt_bwd(pdh, pck)
+        n = pdh.shape[1]
+        assert torch.equal(at(halves[0]), pd[:, :n]) and torch.equal(at(halves[1]), pd[:, n:])
+
+
+def test_most_rows_of_the_quantizer_along_the_columns(cuda_lib):
+    """As many rows as are taken; one more is refused, and the refusal leaves nothing behind."""
+    rows = 32767 * 256
+    x = rand(rows + 1, 32, 141)
+    with pytest.raises(fp8hg.Fp8hgError) as e:
+        fp8hg.fp4_quant(x, MX, transpose=True)
+    assert e.value.status == 3
+    fp8hg.fp8_quant_token(rand(128, 128, 142))
+    for kind in (MX, NV):
+        q, qt = fp8hg.fp4_quant_dual(x[:rows], kind)
+        assert torch.equal(q.codes, fp8hg.fp4_quant(x[:rows], kind).codes)
+        s = qt.scales()
+        for at in (0, 12345 * 256, rows - 256):
+            part = fp8hg.fp4_quant(x[at:at + 256], kind, transpose=True)
+            assert torch.equal(qt.codes[:, at // 2:at // 2 + 128], part.codes)
+            n = ref.BLOCK[kind]
+            assert torch.equal(s[:, at // n:at // n + 256 // n], part.scales())
+
+
+def test_many_rows_of_the_swiglu_backward(cuda_lib):
+    """More rows than a grid's second dimension would hold in tiles, and rows that
+    the CTAs of a column step through."""
+    rows = 65536 * 128 + 128
+    g, u, dh = (rand(rows, 128, 151 + i) for i in range(3))
+    h, ck = fp8hg.fp8_swiglu_ckpt(g, u)
+    d = fp8hg.fp8_swiglu_ckpt_bwd(dh, ck)
+    dq, dt, ht = fp8hg.fp8_swiglu_ckpt_bwd_q(dh, ck)
+    for at in (0, 70000 * 64, rows - 128):
+        r = slice(at, at + 128)
+        ph, pck = fp8hg.fp8_swiglu_ckpt(g[r], u[r])
+        assert torch.equal(h.codes[r], ph.codes) and torch.equal(ck.gate.codes[r], pck.gate.codes)
+        assert torch.equal(d[r], fp8hg.fp8_swiglu_ckpt_bwd(dh[r], pck))
+        a, b, c = fp8hg.fp8_swiglu_ckpt_bwd_q(dh[r], pck)
+        assert torch.equal(dq.codes[r], a.codes) and torch.equal(dq.scales()[r], a.scales())
+        assert torch.equal(dt.codes[:, r], b.codes) and torch.equal(ht.codes[:, r], c.codes)
+        assert torch.equal(ht.scales()[:, at // 128:at // 128 + 1], c.scales())
+    assert fp8hg.fp8hg_get_device_error() == 0

@@ -246,3 +246,11 @@ def test_strides_of_one_row_say_nothing(gpu0, stride):
         fp8hg.fp8_swiglu_ckpt_bwd(gpu0(row(128, stride)), c)
     native = lowbit._ckpt(c, gpu0(row(128, stride)))[0]
     assert (native.ld_q, native.ld_s) == (128, 1)
+
+
+def test_rows_of_the_quantizer_along_the_columns():
+    """One row more than its grid holds is refused before the launch."""
+    fake, rows = 0x10000, 32767 * 256 + 1
+    call = lowbit._fns().fp4_quant
+    assert call(fake, rows, 32, 32, fp8hg.FP4_MX, None, None, 0, None, fake, 2 ** 22, fake, None) == 3
+    assert call(fake, rows, 32, 32, fp8hg.FP4_MX, None, fake, 16, fake, fake, 2 ** 22, fake, None) == 3
