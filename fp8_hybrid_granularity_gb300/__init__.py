@@ -183,7 +183,7 @@ class QTensor:
     ncols_scale: int
 
     def scales(self):
-        return self.scale.narrow(1, 0, self.ncols_scale)
+        return self.scale[:, :self.ncols_scale]
 
     def operand(self) -> Operand:
         c, s = self.codes, self.scale

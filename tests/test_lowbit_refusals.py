@@ -254,3 +254,15 @@ def test_rows_of_the_quantizer_along_the_columns():
     call = lowbit._fns().fp4_quant
     assert call(fake, rows, 32, 32, fp8hg.FP4_MX, None, None, 0, None, fake, 2 ** 22, fake, None) == 3
     assert call(fake, rows, 32, 32, fp8hg.FP4_MX, None, fake, 16, fake, fake, 2 ** 22, fake, None) == 3
+
+
+def test_scale_views():
+    """QTensor.scales() is the unpadded slice: of whatever holds the scales, and
+    of no more columns than there are."""
+    import numpy as np
+    for s in (torch.arange(32, dtype=torch.uint8).reshape(4, 8), np.arange(32, dtype=np.uint8).reshape(4, 8)):
+        for n in (0, 5, 8, 9):
+            got = fp8hg.QTensor(None, s, fp8hg.E4M3, fp8hg.GRAN_1x128, n).scales()
+            assert tuple(got.shape) == (4, min(n, 8)) and (got == s[:, :n]).all()
+            got[...] = 7                    # a view
+            assert (s[:, :n] == 7).all()
