@@ -226,8 +226,8 @@ class Fp4Tensor:
     def scales(self) -> torch.Tensor:
         """The scale bytes as [rows, ceil(k / block)] (a copy)."""
         n = -(-self.k // FP4_BLOCK[self.kind])
-        r = -(-self.rows // 128)
-        t = self.scale.view(r, -1, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(r * 128, -1)
+        r, tiles = -(-self.rows // 128), -(-self.k // 256) * (4 if self.kind == FP4_NV else 2)
+        t = self.scale.view(-1)[:r * tiles * 512].view(r, tiles, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(r * 128, tiles * 4)
         return t[:self.rows, :n].contiguous()
 
 

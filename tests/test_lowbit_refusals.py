@@ -266,3 +266,20 @@ def test_scale_views():
             assert tuple(got.shape) == (4, min(n, 8)) and (got == s[:, :n]).all()
             got[...] = 7                    # a view
             assert (s[:, :n] == 7).all()
+
+
+@pytest.mark.parametrize("kind,block", [(fp8hg.FP4_MX, 32), (fp8hg.FP4_NV, 16)])
+@pytest.mark.parametrize("rows,k", [(0, 64), (5, 0), (0, 0), (5, 70), (129, 257)])
+def test_fp4_scales_of_any_size(kind, block, rows, k):
+    """Fp4Tensor.scales() of empty tensors, and from scale arrays larger than the tensor needs."""
+    q = fp8hg.alloc_fp4(rows, k, kind, device="cpu")
+    q.scale.copy_(torch.arange(q.scale.numel()) % 251)
+    want = q.scales()
+    assert want.shape == (rows, -(-k // block)) and want.dtype == torch.uint8
+    tiles = -(-k // 256) * 256 // block // 4
+    for r, j in ((0, 0), (rows - 1, want.shape[1] - 1)):
+        if want.numel():
+            at = ((r // 128) * tiles + j // 4) * 512 + r % 32 * 16 + r % 128 // 32 * 4 + j % 4
+            assert want[r, j] == q.scale[at]
+    q.scale = torch.cat((q.scale, torch.zeros(777, dtype=torch.uint8)))
+    assert torch.equal(q.scales(), want)
