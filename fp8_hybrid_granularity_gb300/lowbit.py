@@ -281,9 +281,9 @@ def fp4_quant(x, kind: int = FP4_MX, tensor_scale=None, transpose: bool = False,
     shape = _matrix(x)
     rows, cols = (shape[1], shape[0]) if transpose else shape[:2]
     out, to = _output(out, rows, cols, kind, tensor_scale)
-    out.tensor_scale = tensor_scale
     both = _NONE + to if transpose else to + _NONE
     _check(_fns().fp4_quant(x.data_ptr(), *shape, kind, _ts(tensor_scale), *both, _on(x)), "fp4_quant")
+    out.tensor_scale = tensor_scale
     return out
 
 
@@ -295,8 +295,8 @@ def fp4_quant_dual(x, kind: int = FP4_MX, tensor_scale=None, out: Optional[Fp4Te
     rows, cols = shape[:2]
     out, to = _output(out, rows, cols, kind, tensor_scale)
     out_t, to_t = _output(out_t, cols, rows, kind, tensor_scale)
-    out.tensor_scale = out_t.tensor_scale = tensor_scale
     _check(_fns().fp4_quant(x.data_ptr(), *shape, kind, _ts(tensor_scale), *to, *to_t, _on(x)), "fp4_quant_dual")
+    out.tensor_scale = out_t.tensor_scale = tensor_scale
     return out, out_t
 
 

@@ -283,3 +283,20 @@ def test_fp4_scales_of_any_size(kind, block, rows, k):
             assert want[r, j] == q.scale[at]
     q.scale = torch.cat((q.scale, torch.zeros(777, dtype=torch.uint8)))
     assert torch.equal(q.scales(), want)
+
+
+def test_refused_calls_change_nothing(monkeypatch, gpu0):
+    """The outputs given to a call that the library refuses keep their tensor scale."""
+    class Library:
+        def fp4_quant(self, *args):
+            return 1
+
+    monkeypatch.setattr(lowbit, "_fns", Library)
+    old, new = gpu0(f32(1)), gpu0(f32(1))
+    q, qt = (fp4(gpu0, *shape, fp8hg.FP4_NV, old) for shape in ((40, 64), (64, 40)))
+    for call in (lambda: fp8hg.fp4_quant(gpu0(bf16(40, 64)), fp8hg.FP4_NV, new, out=q),
+                 lambda: fp8hg.fp4_quant(gpu0(bf16(64, 40)), fp8hg.FP4_NV, new, transpose=True, out=q),
+                 lambda: fp8hg.fp4_quant_dual(gpu0(bf16(40, 64)), fp8hg.FP4_NV, new, out=q, out_t=qt)):
+        with pytest.raises(fp8hg.Fp8hgError):
+            call()
+        assert q.tensor_scale is old and qt.tensor_scale is old
