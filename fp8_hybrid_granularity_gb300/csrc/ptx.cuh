@@ -18,6 +18,12 @@ __device__ __forceinline__ uint64_t globaltimer() {
     return t;
 }
 
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -42,6 +48,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+// A wait of at most limit_ns (below 2^31: the timer's low word goes round in 4.3 s)
+// in a kernel that has two registers to spare for it; false if it ran out.
+__device__ __forceinline__ bool mbar_wait_ns(uint32_t bar, uint32_t parity, uint32_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t t0 = globaltimer_lo();
+#pragma unroll 1
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+    } while (globaltimer_lo() - t0 < limit_ns);
+    return false;
 }
 
 // Registers per thread of the calling warpgroup (every warp of it calls).  An

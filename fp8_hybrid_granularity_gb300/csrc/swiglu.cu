@@ -345,8 +345,8 @@ __device__ __forceinline__ void load_tile(TileIn &t, const uint16_t *dh, uint32_
     t.su = ptx::ld_u8(c.us + sat);
 }
 
-// Attempts of one wait (each suspends the warp for a while): seconds.
-constexpr uint32_t kTries = 1u << 22;
+// The limit of one wait: 2 s.
+constexpr uint32_t kWaitNs = 2000000000u;
 
 template <int FC, int FR, int FT, int FH, bool WIDE>
 __global__ void __launch_bounds__(Q_THREADS, 1)
@@ -368,10 +368,7 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
     ptx::grid_begin(static_cast<int64_t>(c.rows) * c.cols);
     // every warp waits for and arrives at every barrier, once a tile
     auto wait = [&](uint32_t which, uint32_t parity) {
-        if (ptx::mbar_try_wait(which, parity)) return true;
-#pragma unroll 1
-        for (uint32_t i = 0; i < kTries; ++i)
-            if (ptx::mbar_try_wait(which, parity)) return true;
+        if (ptx::mbar_wait_ns(which, parity, kWaitNs)) return true;
         atomicOr(err, 1u);
         return false;
     };
