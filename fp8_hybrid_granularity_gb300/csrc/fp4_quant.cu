@@ -369,19 +369,6 @@ __global__ void __launch_bounds__(256, kDequantThreadsPerSm / 256)
     }
 }
 
-int sms() {
-    static int n[64] = {0};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) dev = 0;
-    if (!n[dev]) {
-        int v = 0;
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-        n[dev] = v > 0 ? v : 1;
-    }
-    return n[dev];
-}
-
 template <bool NV>
 cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
     const int64_t total = (a.cols + 255LL) / 256 * 16;      // segments, k padded to 256
@@ -391,7 +378,7 @@ cudaError_t quant_rows(const Fp4QuantArgs &a, cudaStream_t stream) {
     const int threads = (segs * rpb + 31) / 32 * 32;
     const int64_t rblocks = (static_cast<int64_t>(a.rows) + rpb - 1) / rpb, cblocks = (total + segs - 1) / segs;
     // as many CTAs as fit at once
-    const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kRowThreadsPerSm / threads) / cblocks);
+    const int64_t per_sm = kRowThreadsPerSm / threads, resident = std::max<int64_t>(1, sm_count() * per_sm / cblocks);
     const dim3 grid = chunks_first(std::min(rblocks, resident), cblocks);
     const int64_t tiles = fp4_scale_tiles(a.cols, a.kind);
     return launch_after(ragged::wide(a.x, a.ld_x) ? k_fp4_rows<NV, true> : k_fp4_rows<NV, false>, grid, threads, 0,
@@ -416,7 +403,7 @@ cudaError_t launch_fp4_tensor_scale(const uint16_t *x, int rows, int cols, uint3
                                     float *scale, void *ws, cudaStream_t stream) {
     const int segs = static_cast<int>((cols + 15LL) / 16);
     const int64_t n = static_cast<int64_t>(rows) * segs;
-    const int64_t blocks = std::min({(n + 1023) / 1024, static_cast<int64_t>(kAmaxCtasPerSm) * sms(),
+    const int64_t blocks = std::min({(n + 1023) / 1024, static_cast<int64_t>(kAmaxCtasPerSm) * sm_count(),
                                      static_cast<int64_t>(kAmaxBlocks)});
     uint32_t *part = static_cast<uint32_t *>(ws);
     if (n > 0) {
@@ -444,7 +431,7 @@ cudaError_t launch_fp4_dequant(const Fp4Operand &a, void *out, uint32_t ld_out, 
     const int threads = static_cast<int>(((segs + chunks - 1) / chunks + 31) / 32 * 32);
     const int64_t cb = (segs + threads - 1) / threads;
     // as many CTAs as fit at once
-    const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kDequantThreadsPerSm / threads) / cb);
+    const int64_t per_sm = kDequantThreadsPerSm / threads, resident = std::max<int64_t>(1, sm_count() * per_sm / cb);
     const dim3 grid = chunks_first(std::min(a.rows, resident), cb);
     auto go = [&](auto kern) {
         return launch_after(kern, grid, threads, 0, stream, 1, a.codes, a.scale, a.ts, a.rows, a.k, a.ld, tiles, out,

@@ -1017,7 +1017,7 @@ bool make_out_tmap(CUtensorMap *m, const Params &p) {
 }
 
 std::mutex g_mu;
-int g_sms[64] = {0};
+bool g_ready[64] = {false};   // the kernels' attributes are set on a device
 
 template <class K>
 cudaError_t allow_smem(K kern, uint32_t bytes) {
@@ -1204,16 +1204,14 @@ int launch_fp4_gemm(const Fp4GemmArgs &g, cudaStream_t stream) {
     if (dev < 0 || dev >= 64) dev = 0;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        if (!g_sms[dev]) {
+        if (!g_ready[dev]) {
             cudaError_t e = set_attributes<true>();
             if (e == cudaSuccess) e = set_attributes<false>();
             if (e != cudaSuccess) return 2 + static_cast<int>(e);
-            int n = 0;
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-            g_sms[dev] = n > 0 ? n : 1;
+            g_ready[dev] = true;
         }
     }
-    return g.a.kind == FP4_NV ? launch<true>(g, g_sms[dev], stream) : launch<false>(g, g_sms[dev], stream);
+    return g.a.kind == FP4_NV ? launch<true>(g, sm_count(), stream) : launch<false>(g, sm_count(), stream);
 }
 
 }  // namespace fp8hg

@@ -97,6 +97,9 @@ struct SwigluGrads {
 cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c,
                                 const SwigluGrads &g, cudaStream_t stream);
 
+// SMs of the current device (looked up once per device; any thread).
+int sm_count();
+
 // Launches a kernel that begins with ptx::grid_begin() or grid_wait(), under the
 // end of the stream's last kernel where that allows it: 1 to 2 us less from one
 // kernel to the next.  cluster > 1: that many CTAs in a cluster.

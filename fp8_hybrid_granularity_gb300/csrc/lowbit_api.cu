@@ -119,6 +119,18 @@ fp8hg::SwigluCkpt ckpt(const fp8hg_swiglu_ckpt *c) {
 
 }  // namespace
 
+int fp8hg::sm_count() {
+    static std::atomic<int> counts[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    n = counts[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+        counts[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 extern "C" {
 
 size_t fp4_scale_bytes(int64_t rows, int64_t k, int kind) {

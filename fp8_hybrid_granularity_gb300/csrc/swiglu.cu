@@ -462,19 +462,6 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
     }
 }
 
-int sms() {
-    static int n[64] = {0};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) dev = 0;
-    if (!n[dev]) {
-        int v = 0;
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-        n[dev] = v > 0 ? v : 1;
-    }
-    return n[dev];
-}
-
 template <int FH, int FC, bool CKPT>
 cudaError_t fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
     // segments of 16 columns, whole groups of eight; a chunk of at most 256
@@ -484,7 +471,7 @@ cudaError_t fwd(const SwigluFwdArgs &a, cudaStream_t stream) {
     const int rpb = 256 / segs, threads = (segs * rpb + 31) / 32 * 32;
     const int64_t rb = (static_cast<int64_t>(a.rows) + rpb - 1) / rpb, cb = (total + segs - 1) / segs;
     // as many CTAs as fit at once
-    const int64_t resident = std::max<int64_t>(1, sms() * static_cast<int64_t>(kFwdThreadsPerSm / threads) / cb);
+    const int64_t per_sm = kFwdThreadsPerSm / threads, resident = std::max<int64_t>(1, sm_count() * per_sm / cb);
     const dim3 grid = rows_first(std::min(rb, resident), cb);
     const bool wide = ragged::wide(a.gate, a.ld_in) && ragged::wide(a.up, a.ld_in);
     return launch_after(wide ? k_swiglu_fwd<FH, FC, CKPT, true> : k_swiglu_fwd<FH, FC, CKPT, false>, grid, threads, 0,
@@ -523,11 +510,7 @@ template <int FC, int FR, int FT, int FH>
 cudaError_t bwd_q(const uint16_t *dh, uint32_t ld_dh, const SwigluCkpt &c, const SwigluGrads &g,
                   cudaStream_t stream) {
     const int64_t kbs = c.cols / kT, tiles = kbs * (c.rows / kT);
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (sms < 1) sms = 1;
-    const unsigned grid = static_cast<unsigned>(tiles < sms ? tiles : sms);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, sm_count()));
     auto go = [&](auto kern) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmem);
         if (e != cudaSuccess) return e;
