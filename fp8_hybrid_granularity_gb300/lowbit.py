@@ -335,7 +335,7 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
     ow = w.operand()
     out, ld_out, kind = _result(out, rows, w.rows, out_dtype)
     stream = _on(x)
-    n = 0 if rows <= 4 else _linear_bytes(rows, k, w.kind)
+    n = _linear_bytes(rows, k, w.kind)
     if n and workspace is None:
         workspace = _scratch(n, x, stream)
     elif n and not (_here(workspace) and workspace.is_contiguous()):
@@ -348,8 +348,9 @@ def fp4_linear(x, w: Fp4Tensor, tensor_scale=None, out=None, out_dtype=None, wor
 
 
 def _linear_bytes(rows, k, kind) -> int:
-    """fp4_linear_workspace of the library for more than four rows."""
-    return rows * ((k + 31) // 32 * 16) + _scale_bytes(rows, k, kind)
+    """fp4_linear_workspace of the library, which quantizes up to four rows in the
+    product."""
+    return 0 if rows <= 4 else rows * ((k + 31) // 32 * 16) + _scale_bytes(rows, k, kind)
 
 
 _scratch_of = threading.local()

@@ -300,3 +300,11 @@ def test_refused_calls_change_nothing(monkeypatch, gpu0):
         with pytest.raises(fp8hg.Fp8hgError):
             call()
         assert q.tensor_scale is old and qt.tensor_scale is old
+
+
+@pytest.mark.parametrize("kind", [fp8hg.FP4_MX, fp8hg.FP4_NV])
+def test_linear_scratch_is_what_the_library_needs(kind):
+    """Rows that the product quantizes itself need none: one rule for both sides."""
+    for rows in list(range(12)) + [127, 128, 129, 1000]:
+        for k in (1, 64, 257, 3584):
+            assert lowbit._linear_bytes(rows, k, kind) == lowbit._fns().fp4_linear_workspace(rows, k, kind)
