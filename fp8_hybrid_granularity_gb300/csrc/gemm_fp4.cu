@@ -933,6 +933,10 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                 }
             }
             ptx::tc_fence_before();
+        } else if (splits > 1 && lane == 0) {
+            // the other CTAs' sums lack this part: none of the cluster stores
+            const uint32_t flag = base + L::OFF_MISC + 4;
+            for (int i = 0; i < splits; ++i) ptx::st_cluster_u32(ptx::map_shared_rank(flag, i), 1u);
         }
     }
 

@@ -183,6 +183,26 @@ def test_wait_that_runs_out_within_a_stage(cuda_lib, out, added):
     assert fp8hg.fp8hg_get_device_error() == 0
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(3, 2000, 4096), (20, 2000, 4096), (50, 700, 8192), (100, 400, 8192), (2500, 2400, 1024)])
+def test_nothing_incomplete_is_stored(cuda_lib, m, n, k, out, kind):
+    """The first copy withheld: what is stored is right, also by the CTAs that
+    share a tile's K with the one that waited in vain."""
+    from test_gpu_fp4 import bound, product, stored
+    a, va = stored(m, k, kind, 161)
+    b, vb = stored(n, k, kind, 162)
+    c, s = product(va, vb)
+    mark = float(torch.tensor(1e9).to(out))
+    got = torch.full((m, n), mark, dtype=out, device="cuda")
+    fp8hg.fp4_gemm_scaled(a, b, out=got, wait_limit_ns=20_000_000, inject_fault=1)
+    assert fp8hg.fp8hg_get_device_error() == 6
+    v = got.double().cpu().numpy()
+    wrong = (np.abs(v - c) > bound(s, k, c, out)) & (v != mark)
+    assert not wrong.any(), np.argwhere(wrong)[:4]
+    assert (v == mark).any()
+
+
 def test_fault_that_a_shape_cannot_have(cuda_lib):
     from test_gpu_fp4 import stored
     for kind, status in ((MX, 1), (NV, 4)):
