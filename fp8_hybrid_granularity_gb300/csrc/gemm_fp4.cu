@@ -361,6 +361,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         uint8_t *stage = gbase + L::OFF_EPI + (warp - 4) * EPI_BYTES;
         const TensorScales<NV> ts(p);
         const float alpha = ts.second;
+        // scales in two steps are rare: BF16 outputs then go the way of those that are
+        // added to, so that the common path has nothing to ask
+        const bool tma = p.c_tma && (p.out_fp32 || !ts.split);
         // a C that is added to, four values at a time (without `accumulate` such a C is TMA's)
         const bool vec = p.accumulate && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0 && p.sm % 4 == 0;
         for (int i = 0, mb, nb; tiles.get<NH>(p, i, mb, nb) > half; ++i) {
@@ -376,9 +379,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_relaxed(tempty_l + 8 * half);
             };
-            // (scales in two steps are rare: they take this path too, and cost the other nothing)
             if (p.out_fp32 || p.accumulate || ts.split) {
-                const bool tma = p.c_tma && p.out_fp32;
 #pragma unroll 1
                 for (int part = 0; part < 3; ++part) {
                     uint32_t r[2][32];
@@ -425,12 +426,12 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 #pragma unroll
             for (int piece = 0; piece < PH / 64; ++piece) {
                 // (in this form it needs no more registers than there are)
-                if (p.c_tma) {
+                if (tma) {
                     if (lane == 0) ptx::bulk_wait_read();
                     __syncwarp();
                 }
                 stage_row(stage, lane, packed + piece * 32);
-                if (p.c_tma) {
+                if (tma) {
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && row0 < p.M && col0 + piece * 64 < p.N) {
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 }
             }
         }
-        if (p.c_tma && lane == 0) ptx::bulk_wait();
+        if (tma && lane == 0) ptx::bulk_wait();
     } else {
         ptx::setmaxnreg_dec<80>();
         // A producer's end, after `it` stages: the even CTA waits until both CTAs'
