@@ -3,10 +3,11 @@
 // (MX) or 0.56 (NV) written per element and direction; beside it stand issue
 // slots, 11 (NV along the rows) and 17 (NV both ways) instructions per element.
 // At 8192 x 8960, in us and of the measured copy rate:
-//   rows        MX 32 (86 %)   NV 33 (85 %)
+//   rows        MX 31 (88 %)   NV 32 (86 %)
 //   both ways   MX 41 (82 %)   NV 48 (71 %)
-//   values      MX 33 (83 %)   NV 31 (90 %)
-//   tensor scale               24 (90 %), its second launch included
+//   columns     MX 31 (88 %)   NV 34 (81 %)
+//   values      MX 31 (90 %)   NV 31 (91 %);   in FP32 92 (54 %)
+//   tensor scale               24 to 25 (87 to 91 %), its second launch included
 //
 //  k_fp4_rows    along the rows: a thread takes 16 elements (an NV block, or
 //                half an MX block, whose other half is in the next lane), so
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------- tensor scale
 // Four CTAs an SM with two loads of 32 bytes in flight per thread: 8192 x 8960
-// takes 25 us (87 % of the copy rate), with two CTAs and four loads 28.
+// takes 24 to 25 us, with two CTAs and four loads 28.
 constexpr int kAmaxBlocks = 1024;    // partial maxima at most
 constexpr int kAmaxCtasPerSm = 4;
 

@@ -661,8 +661,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 // K: no quantization pass before the product, no codes in memory.
 //
 // What bounds a call of one token is latency: the 36 MB (MX) of 18944 x 3584
-// weights take 5.4 us from memory, the call 8.8 us with x quantized on the way
-// (NV 5.7 and 10.5).
+// weights take 5.4 us from memory, the call 9.1 us with x quantized on the way
+// (NV 5.7 and 10.6), and 7.7 (9.4) where the call before left them in L2.
 // So the first stages' copies are issued before the other warps have started.
 constexpr int F_THREADS = 256;
 template <bool NV, int BN>
@@ -1203,10 +1203,12 @@ int launch(const Fp4GemmArgs &g, int sms, cudaStream_t stream) {
 }  // namespace
 
 // Quantizing inside the product, every CTA for itself, against a quantization
-// pass before it (microseconds): 18944 x 3584 NV 10.5 and 12.1 for one row, 11.6
-// and 12.3 for four (MX 8.8 and 9.6, 11.5 and 10.3); 1536 x 8960 NV 6.7 and 7.3
-// for four.  At eight rows it takes longer (by 10 %).  The host launches once
-// instead of twice.
+// pass before it (microseconds, weights from memory; MX / NV):
+//   18944 x 3584   1 row 9.1 and 10.4 / 10.6 and 11.9   4 rows 9.6 and 10.4 / 11.3 and 12.0
+//   1536 x 8960    1 row 5.8 and 6.9 / 6.8 and 7.6      4 rows 6.2 and 7.1 / 6.9 and 7.7
+//   3584 x 18944   1 row 10.7 and 11.8 / 12.9 and 13.9  4 rows 11.4 and 12.0 / 13.2 and 13.9
+// With the weights in L2 the gain is 0.3 to 0.5.  At eight rows the product's own
+// quantization took 10 % longer.  The host launches once instead of twice.
 bool fp4_linear_quantizes(int64_t rows) { return rows <= 4; }
 
 int launch_fp4_gemm(const Fp4GemmArgs &g, cudaStream_t stream) {

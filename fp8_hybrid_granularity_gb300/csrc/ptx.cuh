@@ -488,7 +488,8 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
 // be launched while this one still runs, not only at its end, if this one is
 // short: for a tensor of 1000 x 3584 that saves 1 us a kernel, but the next
 // one's waiting CTAs slow a long one down (8192 x 8960 by 0.5 to 1 us of 30 to 50,
-// 16384 x 18944 by 5 of 343).  What such a kernel reads can change while it is
+// 16384 x 18944 by 5 of 343).  The limit, 2^24 elements whatever their size, lies
+// between these points; sizes in between were not measured.  What such a kernel reads can change while it is
 // already resident: it is read with ordinary loads, not as constant for the
 // kernel's life (ld.global.nc).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

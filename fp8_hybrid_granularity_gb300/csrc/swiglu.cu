@@ -9,17 +9,19 @@
 //
 // exp and the quotient are the fast forms: their relative error (about 1e-6)
 // is far below the 2^-4 and 2^-9 of the casts that follow, and s stays within
-// [0, 1] (exp overflowing to infinity gives 0).
+// [0, 1].  Below FP32's normal range, 2^-126 (g < -87.3), s is taken as 0.
 //
 // A thread takes 16 neighbouring elements, eight threads a group of 128.
 // In us and of the measured copy rate:
 //                          8192 x 8960    16384 x 18944
-//   forward                 84 (91 %)       341 (95 %)
-//   without checkpoints     57 (96 %)       234 (98 %)
-//   backward, BF16          88 (99 %)       363 (101 %)
-//   backward, FP8          138 (71 %)       580 (71 %)
-// Rows that begin at odd addresses (8192 x 5003) reach 71 %: their 16-byte pieces
-// are shifted and exchanged between lanes.
+//   forward                 82 (93 %)       341 (95 %)
+//   without checkpoints     56 (98 %)       234 (98 %)
+//   backward, BF16          84 (104 %)      349 (106 %)
+//   backward, FP8          137 (72 %)       572 (72 %)
+// At 8192 x 5003, where rows begin at odd addresses, the forward reaches 73 %: a lane
+// loads up to three 16-byte pieces each of gate and up for its 32 bytes and shifts
+// them into place.  The BF16 backward reaches 77 %: its stores also exchange pieces
+// between lanes.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -279,7 +281,8 @@ __global__ void __launch_bounds__(256)
 // shared-memory work of the other; with a barrier of the CTA between the parts
 // 8192 x 8960 takes 162 us instead of 139.  The next tile is prefetched to L2
 // while this one's rows are computed and loaded to registers under the columns
-// (without the prefetch 150 us; HBM alone would take 98).
+// (without the prefetch 150 us; HBM alone would take 98).  At the 64 registers that
+// 1024 threads leave, 28 bytes a thread are spilled.
 constexpr int kT = 128, Q_THREADS = 1024;
 constexpr int kPlane = kT * kT;                  // words of one of the three
 constexpr int kQSmem = 3 * kPlane * 4;

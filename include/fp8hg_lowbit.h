@@ -75,8 +75,9 @@ int fp4_tensor_scale(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x
  * or both from one read.
  *
  *   x             [rows, cols] BF16, row stride ld_x elements; any rows and
- *                 cols, 2-byte aligned (16-byte loads where x is 16-byte
- *                 aligned and ld_x a multiple of 8)
+ *                 cols, 2-byte aligned (32-byte loads where x is 32-byte
+ *                 aligned and ld_x a multiple of 16, shifted 16-byte pieces
+ *                 elsewhere)
  *   tensor_scale  FP4HG_NV: device pointer to t, or NULL for 1; a positive
  *                 number between 2^-100 and 2^117 (what fp4_tensor_scale
  *                 gives).  FP4HG_MX: NULL
@@ -166,8 +167,9 @@ int fp4_linear(const uint16_t *x, int64_t rows, int64_t ld_x, const float *tenso
  *                 the checkpoint: codes [rows, cols] (ld_q bytes) and scales
  *                 [rows, G] (ld_s), or all four NULL (inference)
  * Any rows and cols; h, gate_q and up_q 16-byte aligned with strides that are
- * multiples of 16; gate and up 2-byte aligned (16-byte loads where they are
- * 16-byte aligned and ld_in a multiple of 8).
+ * multiples of 16; gate and up 2-byte aligned (32-byte loads where they are
+ * 32-byte aligned and ld_in a multiple of 16, shifted 16-byte pieces elsewhere).
+ * 1 / (1 + exp(-g)) below 2^-126 counts as 0, here and in the backward calls.
  */
 int fp8_swiglu_ckpt(const uint16_t *gate, const uint16_t *up, int64_t rows, int64_t cols,
                     int64_t ld_in, int fmt_h, uint8_t *h, int64_t ld_h, uint8_t *h_scale,
@@ -207,8 +209,8 @@ int fp8_swiglu_ckpt_bwd(const uint16_t *dh, int64_t ld_dh, const fp8hg_swiglu_ck
  *   fmt_h, h_qt, h_st                     the same layout and strides for h
  * Requirements: rows and cols multiples of 128, dh 16-byte aligned with ld_dh
  * % 8 == 0, codes 16-byte aligned with strides that are multiples of 16.  The
- * kernel's warps hand data to one another over bounded waits; one that ran out
- * would be FP8HG_ERR_TIMEOUT from fp8hg_get_device_error.
+ * kernel's warps hand data to one another over waits of at most 2 s; one that ran
+ * out would be FP8HG_ERR_TIMEOUT from fp8hg_get_device_error.
  */
 typedef struct {
     uint8_t *dgate_q, *dup_q, *dgate_s, *dup_s;
