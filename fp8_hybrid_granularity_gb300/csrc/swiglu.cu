@@ -143,7 +143,7 @@ __device__ __forceinline__ uint32_t cast_bf16x16(const uint32_t (&w)[8], uint32_
 }
 
 // ------------------------------------------------------------------- forward
-constexpr int kFwdThreadsPerSm = 768;   // 80 registers a thread
+constexpr int kFwdThreadsPerSm = 768;   // 76 registers a thread
 
 template <int FH, int FC, bool CKPT, bool WIDE>
 __global__ void __launch_bounds__(256, kFwdThreadsPerSm / 256)
