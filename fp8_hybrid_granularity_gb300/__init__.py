@@ -21,6 +21,8 @@ Tensor-level API (same names as the C entry points):
   fp8hg_get_device_error(stream=None)
   fp4_* and fp8_swiglu_ckpt*                            4-bit tensors and SwiGLU with 8-bit
                                                         checkpoints (see lowbit.py)
+  layernorm, fp8_layernorm, layernorm_bwd, lora_*       layer norm and low-rank adapters
+                                                        (see adapt.py)
 
 Scale arrays are allocated with their column count rounded up to a multiple
 of four (the GEMM reads scale bytes four at a time); ``QTensor.scales()``
@@ -589,12 +591,18 @@ _LOWBIT = ("FP4_MX", "FP4_NV", "Fp4Tensor", "SwigluCkpt", "alloc_fp4", "fp4_tens
            "fp8_swiglu_ckpt_bwd_q")
 
 
+_ADAPT = ("LoraAdapters", "LoraPlan", "layernorm", "fp8_layernorm", "layernorm_bwd", "lora_plan",
+          "lora_add", "lora_add_bwd")
+
+
 def __getattr__(name):
-    # lowbit.py's tensors need torch at import time, which this module does
-    # not; its names are loaded on first use
-    if name in _LOWBIT:
-        from . import lowbit
-        for n in _LOWBIT:
-            globals()[n] = getattr(lowbit, n)
-        return globals()[name]
+    # lowbit.py's and adapt.py's tensors need torch at import time, which this
+    # module does not; their names are loaded on first use
+    for names, module in ((_LOWBIT, "lowbit"), (_ADAPT, "adapt")):
+        if name in names:
+            import importlib
+            m = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(m, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,160 @@
+// What the layer norm's forward and backward kernels share: rows held in
+// registers, sixteen neighbouring columns a thread.
+#pragma once
+#include <cstdint>
+
+#include "adapt.h"
+#include "pair_math.cuh"
+#include "ragged.cuh"
+
+namespace fp8hg {
+namespace norm {
+
+// Sixteen values as loaded: BF16 pairs or FP32.
+template <bool F32>
+struct Raw {
+    uint32_t w[F32 ? 16 : 8];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 16 : 8); ++i) w[i] = 0u;
+    }
+    template <bool WIDE>
+    __device__ __forceinline__ void load(const void *base, int64_t at, int left) {
+        if constexpr (F32) ragged::load16<WIDE>(static_cast<const float *>(base) + at, left, w);
+        else ragged::load16<WIDE>(static_cast<const uint16_t *>(base) + at, left, w);
+    }
+    __device__ __forceinline__ F2 pair(int i) const {
+        if constexpr (F32) return f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return f2_bf16(w[i]);
+    }
+};
+
+// Sixteen values to base[at ...] in BF16 or FP32 (every lane of the warp calls it).
+template <bool WIDE>
+__device__ __forceinline__ void store_values(void *base, int f32, int64_t at, int left, const F2 (&v)[8]) {
+    if (f32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[2 * i] = __float_as_uint(v[i].lo()), w[2 * i + 1] = __float_as_uint(v[i].hi());
+        ragged::store16<WIDE>(static_cast<float *>(base) + at, left, w);
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = ptx::cvt_bf16x2(v[i].lo(), v[i].hi());
+        ragged::store16<WIDE>(static_cast<uint16_t *>(base) + at, left, w);
+    }
+}
+
+// Sixteen parameters from column c0 on; `none` without a tensor, 0 past the last.
+__device__ __forceinline__ void load_params(const void *p, int f32, float none, int c0, int left, F2 (&v)[8]) {
+    if (left <= 0 || p == nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f2(left > 0 ? none : 0.0f);
+    } else if (f32) {
+        Raw<true> r;
+        r.load<false>(p, c0, left);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r.pair(i);
+    } else {
+        Raw<false> r;
+        r.load<false>(p, c0, left);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r.pair(i);
+    }
+}
+
+// Zeros from element `left` on.
+__device__ __forceinline__ void cut(F2 (&v)[8], int left) {
+    if (left < 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f2(2 * i < left ? v[i].lo() : 0.0f, 2 * i + 1 < left ? v[i].hi() : 0.0f);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float total(const F2 (&v)[8]) {
+    const F2 a = add2(add2(v[0], v[1]), add2(v[2], v[3])), b = add2(add2(v[4], v[5]), add2(v[6], v[7]));
+    const F2 s = add2(a, b);
+    return s.lo() + s.hi();
+}
+
+// Sums (and maxima) over the threads of a row: `warps` whole warps.  Every
+// thread of the CTA calls them in step; two buffers in turn, so that one
+// barrier per sum is enough.
+struct RowReduce {
+    float2 *buf;     // [2][32]
+    int warps, first, turn;
+    __device__ __forceinline__ RowReduce(float2 *b, int tpr)
+        : buf(b), warps(tpr / 32), first(threadIdx.x / tpr * (tpr / 32)), turn(0) {}
+    __device__ __forceinline__ float2 sum(float a, float b) {
+        a = warp_sum(a);
+        b = warp_sum(b);
+        if (warps == 1) return make_float2(a, b);
+        float2 *t = buf + 32 * turn;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) t[threadIdx.x / 32] = make_float2(a, b);
+        __syncthreads();
+        float2 r = t[first];
+        for (int i = 1; i < warps; ++i) r.x += t[first + i].x, r.y += t[first + i].y;
+        return r;
+    }
+    __device__ __forceinline__ float sum(float a) {
+        a = warp_sum(a);
+        if (warps == 1) return a;
+        float2 *t = buf + 32 * turn;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) t[threadIdx.x / 32].x = a;
+        __syncthreads();
+        float r = t[first].x;
+        for (int i = 1; i < warps; ++i) r += t[first + i].x;
+        return r;
+    }
+    __device__ __forceinline__ float max(float m) {
+        m = warp_max_abs(m);
+        if (warps == 1) return m;
+        float2 *t = buf + 32 * turn;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) t[threadIdx.x / 32].x = m;
+        __syncthreads();
+        float r = t[first].x;
+        for (int i = 1; i < warps; ++i) r = max3_abs(r, r, t[first + i].x);
+        return r;
+    }
+};
+
+// A thread's sixteen parameters in shared memory: pieces of four, the threads'
+// pieces next to one another, so that neither access meets a bank twice.
+__device__ __forceinline__ void keep_params(float *at, int t, int tpr, const F2 (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        reinterpret_cast<float4 *>(at)[j * tpr + t] =
+            make_float4(v[2 * j].lo(), v[2 * j].hi(), v[2 * j + 1].lo(), v[2 * j + 1].hi());
+}
+__device__ __forceinline__ void kept_params(const float *at, int t, int tpr, int j, F2 &a, F2 &b) {
+    const float4 q = reinterpret_cast<const float4 *>(at)[j * tpr + t];
+    a = f2(q.x, q.y);
+    b = f2(q.z, q.w);
+}
+
+// How a row is dealt out where it fits the registers: threads a row (whole
+// warps), rows a CTA.
+constexpr int kRegCols = 8192;
+constexpr int kSms = 152;
+struct Shape {
+    int tpr, rpb;
+};
+inline Shape shape_of(int64_t cols) {
+    Shape s;
+    s.tpr = static_cast<int>(cols > kRegCols ? 512 : (cols + 511) / 512 * 32);
+    s.rpb = s.tpr >= 256 ? 1 : 256 / s.tpr;
+    return s;
+}
+inline bool wide_rows(const void *p, int f32, int64_t ld) { return f32 ? ragged::wide_f32(p, ld) : ragged::wide(p, ld); }
+
+}  // namespace norm
+}  // namespace fp8hg

@@ -1,0 +1,282 @@
+// Layer norm, backward.
+//
+//   xh = (x - mean) rstd,  g = dy w
+//   dx = rstd (g - sum(g) / n - xh sum(g xh) / n) [+ add]
+//   dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// in FP32 between the loads and the stores, from the statistics that the
+// forward pass kept.  Bound by HBM: x, dy (and add) are read once, dx written
+// once.  Laid out like the forward pass (a row in registers, 16 columns a thread);
+// the sums for dw and db stay in registers over all rows of a CTA and leave as
+// one row of partial sums per CTA, which a second kernel adds in a fixed order:
+// results do not depend on timing.  Rows of more than 8192 columns are read twice
+// for dx and once more, by columns, for dw and db.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "norm.cuh"
+
+namespace fp8hg {
+
+namespace {
+
+using namespace norm;
+
+// Sixteen columns' sums of dw and db of one row after the other into `sums`.
+__device__ __forceinline__ void gather(float *sums, int cols, int c0, bool first, const F2 (&dw)[8], const F2 (&db)[8]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int c = c0 + i;
+        if (c < cols) {
+            const float vw = i & 1 ? dw[i / 2].hi() : dw[i / 2].lo();
+            const float vb = i & 1 ? db[i / 2].hi() : db[i / 2].lo();
+            sums[c] = first ? vw : sums[c] + vw;
+            sums[cols + c] = first ? vb : sums[cols + c] + vb;
+        }
+    }
+}
+
+template <bool XF32, bool DF32, bool WIDE>
+__global__ void __launch_bounds__(512) k_norm_bwd(const NormBwdArgs a, int tpr) {
+    extern __shared__ float4 shared[];     // w; after the last row the sums, [2][cols], of several rows at a time
+    __shared__ float2 red[2 * 32];
+    ptx::grid_begin(static_cast<int64_t>(a.rows) * a.cols);
+    RowReduce row(red, tpr);
+    const int t = threadIdx.x % tpr, rpb = blockDim.x / tpr;
+    const int c0 = t * 16, cols_left = a.cols - c0;
+    const uint32_t rows = a.rows, step = gridDim.x * rpb;
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    Raw<XF32> nx, add;
+    Raw<DF32> nd;
+    nx.zero();
+    nd.zero();
+    add.zero();
+    float2 nst = make_float2(0.0f, 0.0f);
+    auto load = [&](uint32_t r) {
+        if (r < rows && cols_left > 0) {
+            nst = reinterpret_cast<const float2 *>(a.stats)[r];
+            nx.template load<WIDE>(a.x, row_at(r, a.ld_x) + c0, cols_left);
+            nd.template load<WIDE>(a.dy, row_at(r, a.ld_dy) + c0, cols_left);
+        }
+    };
+    uint32_t r = blockIdx.x * rpb + threadIdx.x / tpr;
+    load(r);
+    float *w = reinterpret_cast<float *>(shared);
+    if (threadIdx.x < tpr) {
+        F2 v[8];
+        load_params(a.weight, a.param_f32, 1.0f, c0, cols_left, v);
+        keep_params(w, t, tpr, v);
+    }
+    __syncthreads();
+    F2 dw[8], db[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[i] = db[i] = f2(0.0f);
+    for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
+        const bool in = r < rows;
+        if (a.add != nullptr && in && cols_left > 0) add.template load<WIDE>(a.add, row_at(r, a.ld_add) + c0, cols_left);
+        const float mean = nst.x, rstd = nst.y;
+        F2 xh[8], g[8], p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            xh[i] = mul2(add2(nx.pair(i), f2(-mean)), f2(rstd));
+            g[i] = nd.pair(i);
+        }
+        load(r + step);
+        if (in) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dw[i] = fma2(g[i], xh[i], dw[i]);
+                db[i] = add2(db[i], g[i]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            F2 w0, w1;
+            kept_params(w, t, tpr, j, w0, w1);
+            g[2 * j] = mul2(g[2 * j], w0);
+            g[2 * j + 1] = mul2(g[2 * j + 1], w1);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = mul2(g[i], xh[i]);
+        const float2 s = row.sum(total(g), total(p));
+        const F2 mg = f2(-s.x * inv_n), mgx = f2(-s.y * inv_n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = fma2(f2(rstd), fma2(xh[i], mgx, add2(g[i], mg)), add.pair(i));
+        store_values<WIDE>(a.dx, XF32, row_at(r, a.ld_dx) + c0, in ? cols_left : 0, g);
+    }
+    if (a.ws == nullptr) return;
+    float *part = a.ws + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    if (rpb == 1) {
+        store_values<false>(part, 1, c0, cols_left, dw);
+        store_values<false>(part, 1, a.cols + c0, cols_left, db);
+        return;
+    }
+    __syncthreads();
+    for (int q = 0; q < rpb; ++q) {
+        if (threadIdx.x / tpr == q) gather(w, a.cols, c0, q == 0, dw, db);
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) part[c] = w[c];
+}
+
+// dx of rows of any length, a CTA each.
+template <bool XF32, bool DF32>
+__global__ void __launch_bounds__(512) k_norm_bwd_long(const NormBwdArgs a) {
+    __shared__ float2 red[2 * 32];
+    ptx::grid_wait();
+    const int tpr = blockDim.x;
+    RowReduce row(red, tpr);
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    const uint32_t rows = a.rows;
+    for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const float2 st = reinterpret_cast<const float2 *>(a.stats)[r];
+        F2 xh[8], g[8];
+        auto piece = [&](int64_t c0) {
+            const int left = static_cast<int>(a.cols - c0);
+            Raw<XF32> x;
+            Raw<DF32> dy;
+            x.template load<false>(a.x, row_at(r, a.ld_x) + c0, left);
+            dy.template load<false>(a.dy, row_at(r, a.ld_dy) + c0, left);
+            F2 w[8];
+            load_params(a.weight, a.param_f32, 1.0f, static_cast<int>(c0), left, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                xh[i] = mul2(add2(x.pair(i), f2(-st.x)), f2(st.y));
+                g[i] = mul2(dy.pair(i), w[i]);
+            }
+        };
+        const int64_t first = threadIdx.x * 16, pass = tpr * 16;
+        float sg = 0.0f, sgx = 0.0f;
+        for (int64_t c0 = first; c0 < a.cols; c0 += pass) {
+            piece(c0);
+            F2 p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = mul2(g[i], xh[i]);
+            sg += total(g);
+            sgx += total(p);
+        }
+        const float2 s = row.sum(sg, sgx);
+        const F2 mg = f2(-s.x * inv_n), mgx = f2(-s.y * inv_n);
+        for (int64_t c0 = first; c0 - (threadIdx.x & 31) * 16 < a.cols; c0 += pass) {
+            const int left = static_cast<int>(a.cols - c0);
+            Raw<XF32> add;
+            add.zero();
+            if (left > 0) {
+                piece(c0);
+                if (a.add != nullptr) add.template load<false>(a.add, row_at(r, a.ld_add) + c0, left);
+            }
+            F2 dx[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dx[i] = fma2(f2(st.y), fma2(xh[i], mgx, add2(g[i], mg)), add.pair(i));
+            store_values<false>(a.dx, XF32, row_at(r, a.ld_dx) + c0, left, dx);
+        }
+        __syncthreads();   // a warp past its last piece is not a row ahead of the sums
+    }
+}
+
+// Partial sums for dw and db of such rows: a warp takes 512 columns of every
+// eighth row of the CTA's part.
+constexpr int kColRows = 256;
+template <bool XF32, bool DF32>
+__global__ void __launch_bounds__(256) k_norm_columns(const NormBwdArgs a) {
+    __shared__ float sums[2 * 512];
+    ptx::grid_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * 512, c0 = base + lane * 16;
+    const int left = static_cast<int>(a.cols - c0);
+    const uint32_t per = (static_cast<uint32_t>(a.rows) + gridDim.y - 1) / gridDim.y, from = blockIdx.y * per;
+    const uint32_t to = min(static_cast<uint32_t>(a.rows), from + per);
+    F2 dw[8], db[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[i] = db[i] = f2(0.0f);
+    if (left > 0) {
+        for (uint32_t r = from + warp; r < to; r += 8) {
+            Raw<XF32> x;
+            Raw<DF32> dy;
+            x.template load<false>(a.x, row_at(r, a.ld_x) + c0, left);
+            dy.template load<false>(a.dy, row_at(r, a.ld_dy) + c0, left);
+            const float2 st = reinterpret_cast<const float2 *>(a.stats)[r];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dw[i] = fma2(dy.pair(i), mul2(add2(x.pair(i), f2(-st.x)), f2(st.y)), dw[i]);
+                db[i] = add2(db[i], dy.pair(i));
+            }
+        }
+    }
+    for (int q = 0; q < 8; ++q) {
+        if (warp == q) gather(sums, 512, lane * 16, q == 0, dw, db);
+        __syncthreads();
+    }
+    float *part = a.ws + static_cast<int64_t>(blockIdx.y) * 2 * a.cols;
+    for (int i = threadIdx.x; i < 512; i += 256) {
+        if (base + i < a.cols) {
+            part[base + i] = sums[i];
+            part[a.cols + base + i] = sums[512 + i];
+        }
+    }
+}
+
+// Partial sums [parts][2 cols] to dw and db: 32 columns a CTA, 16 warps that
+// take every 16th row each.
+__global__ void __launch_bounds__(512) k_norm_sums(const float *ws, int parts, int cols, float *dweight, float *dbias) {
+    __shared__ float sums[16][33];
+    ptx::grid_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane, n = 2 * static_cast<int64_t>(cols);
+    float s = 0.0f;
+    if (c < n) {
+#pragma unroll 4
+        for (int p = warp; p < parts; p += 16) s += ptx::ld_f32(ws + p * n + c);
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < n) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += sums[i][lane];
+        float *to = c < cols ? dweight : dbias;
+        if (to != nullptr) to[c < cols ? c : c - cols] = s;
+    }
+}
+
+// Rows of partial sums for dw and db: CTAs of the kernel that makes them.
+int norm_parts(int64_t rows, int64_t cols) {
+    if (cols > kRegCols) return static_cast<int>(std::min<int64_t>((rows + kColRows - 1) / kColRows, 32));
+    const Shape s = shape_of(cols);
+    return static_cast<int>(std::min<int64_t>((rows + s.rpb - 1) / s.rpb, kSms * std::max(1, 512 / (s.tpr * s.rpb))));
+}
+
+template <bool XF32, bool DF32>
+cudaError_t run(const NormBwdArgs &a, cudaStream_t stream) {
+    const int parts = norm_parts(a.rows, a.cols);
+    cudaError_t e;
+    if (a.cols > kRegCols) {
+        e = launch_after(&k_norm_bwd_long<XF32, DF32>, dim3(std::min(a.rows, 2 * kSms)), 512, 0, stream, 1, a);
+        if (e == cudaSuccess && a.ws != nullptr)
+            e = launch_after(&k_norm_columns<XF32, DF32>, dim3((a.cols + 511) / 512, parts), 256, 0, stream, 1, a);
+    } else {
+        const Shape s = shape_of(a.cols);
+        const bool wide = wide_rows(a.x, a.x_f32, a.ld_x) && wide_rows(a.dy, a.dy_f32, a.ld_dy) &&
+                          wide_rows(a.dx, a.x_f32, a.ld_dx) && (a.add == nullptr || wide_rows(a.add, a.x_f32, a.ld_add));
+        const size_t smem = (s.rpb > 1 ? 2 : 1) * 16 * sizeof(float) * s.tpr;   // at most 32 KB
+        e = wide ? launch_after(&k_norm_bwd<XF32, DF32, true>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr)
+                 : launch_after(&k_norm_bwd<XF32, DF32, false>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr);
+    }
+    if (e != cudaSuccess || a.ws == nullptr) return e;
+    return launch_after(&k_norm_sums, dim3(static_cast<unsigned>((2 * static_cast<int64_t>(a.cols) + 31) / 32)), 512, 0,
+                        stream, 1, static_cast<const float *>(a.ws), parts, a.cols, a.dweight, a.dbias);
+}
+
+}  // namespace
+
+size_t norm_bwd_ws_bytes(int64_t rows, int64_t cols) {
+    return static_cast<size_t>(norm_parts(rows, cols)) * 2 * static_cast<size_t>(cols) * sizeof(float);
+}
+
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t stream) {
+    if (a.x_f32) return a.dy_f32 ? run<true, true>(a, stream) : run<true, false>(a, stream);
+    return a.dy_f32 ? run<false, true>(a, stream) : run<false, false>(a, stream);
+}
+
+}  // namespace fp8hg

@@ -1,5 +1,5 @@
-// Sixteen neighbouring BF16 values per thread, loaded from and stored to rows
-// of any alignment.
+// Sixteen neighbouring BF16 (or FP32) values per thread, loaded from and stored
+// to rows of any alignment.
 //
 // WIDE: the address is a multiple of 32 bytes (the row stride too): one
 // 32-byte access, a whole sector per lane.  (Two 16-byte loads that bypass L1
@@ -122,9 +122,109 @@ __device__ __forceinline__ void store16(uint16_t *p, int left, const uint32_t (&
     }
 }
 
+// Sixteen neighbouring FP32 values per thread, by the same rules: WIDE rows in
+// 32-byte accesses, others (a multiple of 4 bytes) in aligned 16-byte granules.
+template <bool WIDE>
+__device__ __forceinline__ void load16(const float *p, int left, uint32_t (&v)[16]) {
+    if (WIDE && left >= 16) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(v[8 * i]), "=r"(v[8 * i + 1]), "=r"(v[8 * i + 2]), "=r"(v[8 * i + 3]),
+                           "=r"(v[8 * i + 4]), "=r"(v[8 * i + 5]), "=r"(v[8 * i + 6]), "=r"(v[8 * i + 7])
+                         : "l"(p + 8 * i)
+                         : "memory");
+        return;
+    }
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const uint32_t s = static_cast<uint32_t>(a >> 2) & 3u;
+    const uint4 *g = reinterpret_cast<const uint4 *>(a & ~static_cast<uintptr_t>(15));
+    const uint32_t words = left >= 16 ? 16u : static_cast<uint32_t>(left);
+    uint32_t w[20];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (s + words > 4u * i) q = ptx::ld_v4(g + i);
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+    }
+    if (s & 2) {
+#pragma unroll
+        for (int i = 0; i < 18; ++i) w[i] = w[i + 2];
+    }
+    if (s & 1) {
+#pragma unroll
+        for (int i = 0; i < 17; ++i) w[i] = w[i + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < words ? w[i] : 0u;
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void store16(float *p, int left, const uint32_t (&v)[16]) {
+    if (WIDE && left >= 16) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 8 * i), "r"(v[8 * i]),
+                         "r"(v[8 * i + 1]), "r"(v[8 * i + 2]), "r"(v[8 * i + 3]), "r"(v[8 * i + 4]),
+                         "r"(v[8 * i + 5]), "r"(v[8 * i + 6]), "r"(v[8 * i + 7])
+                         : "memory");
+        return;
+    }
+    if (WIDE) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < left) p[i] = __uint_as_float(v[i]);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const int words = left >= 16 ? 16 : left > 0 ? left : 0;
+    const int d = static_cast<int>(-static_cast<intptr_t>(a >> 2) & 3);   // to the next granule
+    uint32_t w[20];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = v[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[16 + i] = __shfl_down_sync(0xFFFFFFFFu, v[i], 1);
+    const uintptr_t na = __shfl_down_sync(0xFFFFFFFFu, static_cast<unsigned long long>(a), 1);
+    const int nwords = __shfl_down_sync(0xFFFFFFFFu, words, 1);
+    // the last granule is complete with the next lane's first d words
+    const bool joined = lane < 31 && words == 16 && na == a + 64 && nwords >= d && d != 0;
+    const bool head_done = __shfl_up_sync(0xFFFFFFFFu, joined ? 1 : 0, 1) && lane > 0;
+    const int from = head_done ? d : 0;            // first word this lane still has to write
+    if (words == 16) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i >= from && i < d) p[i] = __uint_as_float(w[i]);
+        if (!joined && d != 0) {
+#pragma unroll
+            for (int i = 13; i < 16; ++i)
+                if (i >= d + 12) p[i] = __uint_as_float(w[i]);
+        }
+        if (d & 2) {
+#pragma unroll
+            for (int i = 0; i < 18; ++i) w[i] = w[i + 2];
+        }
+        if (d & 1) {
+#pragma unroll
+            for (int i = 0; i < 17; ++i) w[i] = w[i + 1];
+        }
+        uint4 *g = reinterpret_cast<uint4 *>(a + 4 * d);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) g[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        if (joined || d == 0) g[3] = make_uint4(w[12], w[13], w[14], w[15]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i >= from && i < words) p[i] = __uint_as_float(w[i]);
+    }
+}
+
 // Whether rows from p with stride ld (elements) take the WIDE forms.
 inline bool wide(const void *p, int64_t ld) {
     return reinterpret_cast<uintptr_t>(p) % 32 == 0 && ld % 16 == 0;
+}
+inline bool wide_f32(const void *p, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % 32 == 0 && ld % 8 == 0;
 }
 
 }  // namespace ragged

@@ -27,9 +27,8 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "fp8_group.cuh"
 #include "lowbit.h"
-#include "pair_math.cuh"
-#include "quant_math.cuh"
 #include "ragged.cuh"
 
 namespace fp8hg {
@@ -43,17 +42,6 @@ __device__ __forceinline__ F2 sigmoid2(F2 g) {
     return f2(rcp_fast(y.lo()), rcp_fast(y.hi()));
 }
 
-// Sixteen code bytes (aligned) to p, the first `left` of them.
-__device__ __forceinline__ void store_bytes16(uint8_t *p, const uint32_t (&c)[4], int left) {
-    if (left >= 16) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(c[0], c[1], c[2], c[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < left) p[i] = static_cast<uint8_t>(c[i >> 2] >> (8 * (i & 3)));
-    }
-}
-
 __device__ __forceinline__ void load_bytes16(const uint8_t *p, int left, uint32_t (&c)[4]) {
     if (left >= 16) {
         const uint4 v = ptx::ld_once_v4(p);
@@ -64,12 +52,6 @@ __device__ __forceinline__ void load_bytes16(const uint8_t *p, int left, uint32_
         for (int i = 0; i < 16; ++i)
             if (i < left) c[i >> 2] |= ptx::ld_u8(p + i) << (8 * (i & 3));
     }
-}
-
-// Four values -> four FP8 codes.
-template <int FMT>
-__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
-    return FMT == FMT_E4M3 ? ptx::cvt_e4m3x4(a, b, c, d) : ptx::cvt_e5m2x4(a, b, c, d);
 }
 
 // Four FP8 codes -> their values times m.
@@ -92,45 +74,11 @@ __device__ __forceinline__ float scale_pow2(uint32_t byte) {
     return __uint_as_float((byte << 23) | (byte == 0u || byte == 0xFFu ? 0x400000u : 0u));
 }
 
-// A group's scale, the power of two at or above amax / FMAX (FMAX = 1.75 2^emax),
-// without a branch.  amax is the magnitude's bit pattern with MANT mantissa
-// bits below the exponent, from max3_abs or max_abs_bf16x2: adding just under a
-// quarter of the exponent's unit carries exactly if the mantissa is past 1.75.
-// Zero and values below the range: byte 0.  Non-finite: 0xFF and a NaN
-// multiplier, which casts to 0x7F.
-template <int FMT, int MANT>
-struct Group {
-    uint32_t byte;
-    float mul;       // 2^(127 - byte)
-    __device__ __forceinline__ explicit Group(float amax) { init(__float_as_uint(amax)); }
-    __device__ __forceinline__ explicit Group(uint32_t amax) { init(amax); }
-    __device__ __forceinline__ void init(uint32_t amax) {
-        constexpr int emax = (FMT == FMT_E4M3) ? 8 : 15;
-        const int e = max(static_cast<int>((amax + (1u << (MANT - 2)) - 1u) >> MANT) - emax, 0);
-        const bool nan = amax >= 0xFFu << MANT;
-        byte = nan ? 0xFFu : static_cast<uint32_t>(e);
-        mul = __uint_as_float(nan ? 0x7FC00000u : 0x7F000000u - (static_cast<uint32_t>(e) << 23));
-    }
-    __device__ __forceinline__ uint32_t cast4(F2 a, F2 b) const {
-        const F2 m = f2(mul);
-        a = mul2(a, m);
-        b = mul2(b, m);
-        return cvt4<FMT>(a.lo(), a.hi(), b.lo(), b.hi());
-    }
-};
-template <int FMT>
-using GroupF32 = Group<FMT, 23>;
-
-// Maximum over the eight lanes of a group (each half of a packed pair).
+// Maximum over the eight lanes of a group, each half of a packed pair.
 __device__ __forceinline__ uint32_t group_max_u2(uint32_t m) {
     m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     return __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-}
-__device__ __forceinline__ float group_max(float m) {
-    m = max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    return max3_abs(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
 }
 
 // Sixteen BF16 values of a group with this amax -> codes; the scale byte.
