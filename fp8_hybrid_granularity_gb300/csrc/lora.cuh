@@ -1,17 +1,38 @@
-// What the adapters' kernels share: tiles of rows in shared memory, the tokens
-// of a tile, FP32 values as sums of BF16 ones.
+// What the adapters' kernels share.
+//
+//   v[t] = x[t] A_g^T,  y[t] = base[t] + s_g v[t] B_g^T     (g: the token's adapter)
+//   dv[t] = s_g dy[t] B_g,  dx[t] = base[t] + dv[t] A_g
+//   dA_g = sum over its tokens of dv[t]^T x[t],  dB_g = s_g sum of dy[t]^T v[t]
+//
+//   shrink   rows of r from rows of n or k        (lora_shrink.cu)
+//   expand   rows of n or k from rows of r        (lora_expand.cuh)
+//   outer    sums over the tokens                 (lora_outer.cu)
+//
+// Tokens come in tiles of up to 128 of one adapter, gathered through the plan's
+// order.  x, dy, A and B are BF16 and their products exact; sums are FP32.  The
+// tensor core cuts its sums off instead of rounding them, so sums that FP32
+// results are made of leave it after 64 products (for each part) and are added up
+// in registers.  v and dv, FP32 sums, enter the next product as two BF16 parts (16
+// bits of them, for results in BF16) or three (24 bits, for FP32).
+//
+// 2 r operations per value of x, dy or y and r small: HBM is the bound.  What
+// streams (x, dy, base) goes by asynchronous copies into shared memory, several
+// steps ahead, and from there to the one lane that needs it; four lanes share 64
+// columns of a row, 16 neighbouring ones each.  A product's sum does not mind the
+// order of its terms, nor a result that of its columns: the fragments take the
+// lane's 16 values as they lie, the other operand, shared by the CTA's warps, is
+// picked accordingly.  Rows at odd addresses go through registers.
 #pragma once
 #include <cstdint>
 
 #include "adapt.h"
+#include "norm.cuh"
 #include "ptx.cuh"
 
 namespace fp8hg {
 namespace lora {
 
-// Bytes of a row of `cols` 16-bit values in shared memory: 16 more than it
-// needs, so that eight rows' 16-byte pieces fall on different banks.
-__host__ __device__ constexpr int row_bytes(int cols) { return 2 * cols + 16; }
+constexpr int kSms = 152;
 
 // A tile of the plan.
 struct Tile {
@@ -45,14 +66,130 @@ __device__ __forceinline__ void copy8(uint32_t dst, const uint16_t *p, int left)
 
 // v as the sum of PARTS BF16 values: 16 bits of it with two, all 24 with three.
 template <int PARTS>
-__device__ __forceinline__ void split(float v, uint16_t (&h)[PARTS]) {
+__device__ __forceinline__ void split(float v, uint32_t (&h)[PARTS]) {
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-        h[i] = static_cast<uint16_t>(ptx::cvt_bf16x2(v, 0.0f) & 0xFFFFu);
+        h[i] = ptx::cvt_bf16x2(v, 0.0f) & 0xFFFFu;
         // an infinity or a NaN is in the first part alone
-        v = (h[i] & 0x7F80u) == 0x7F80u ? 0.0f : v - __uint_as_float(static_cast<uint32_t>(h[i]) << 16);
+        v = (h[i] & 0x7F80u) == 0x7F80u ? 0.0f : v - __uint_as_float(h[i] << 16);
     }
 }
+
+__host__ __device__ constexpr int padded(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+inline bool aligned_to(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+// Dynamic shared memory beyond 48 KB is asked for once per kernel and device.
+template <class K>
+cudaError_t with_smem(K kern, size_t bytes, unsigned long long &done) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (__atomic_load_n(&done, __ATOMIC_RELAXED) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e != cudaSuccess) {
+        cudaGetLastError();   // reported here, not by the next call that asks
+        return e;
+    }
+    __atomic_fetch_or(&done, bit, __ATOMIC_RELAXED);
+    return cudaSuccess;
+}
+
+// Sixteen rows of 64 columns, a warp's part of a step: 16-byte piece p of row r.
+// Copied a line (or two) of a row after the other, so that no sector is asked for
+// twice; read back by the four lanes of a row, two rows at a time.
+template <int PIECES>
+__device__ __forceinline__ uint32_t slot(uint32_t ring, int stage, int r, int p) {
+    return ring + ((stage * (kLoraTile / 16) + threadIdx.x / 32) * 16 + r) * (PIECES * 16) + (p ^ (r & 7)) * 16;
+}
+
+// The long side's splits of shrink: one round of CTAs over the plan's tiles, at
+// least 128 columns each.  On the device from the plan, on the host an upper bound.
+constexpr int kShrinkCols = 64;
+__host__ __device__ constexpr int shrink_slots(int rp) { return kSms * (rp <= 32 ? 3 : rp <= 64 ? 2 : 1); }
+__host__ __device__ inline int shrink_splits(int64_t tiles, int k, int rp) {
+    const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
+    int64_t n = shrink_slots(rp) / (tiles < 1 ? 1 : tiles);
+    n = n < (steps + 1) / 2 ? n : (steps + 1) / 2;
+    n = n < 1 ? 1 : n > 32 ? 32 : n;
+    const int64_t per = (steps + n - 1) / n;
+    return static_cast<int>((steps + per - 1) / per);
+}
+// More than any number of tiles with `tokens` tokens gives.
+inline int most_splits(const LoraPlan &p, int k, int rp) {
+    const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
+    const int64_t n = shrink_slots(rp) / ((p.tokens + kLoraTile - 1) / kLoraTile);
+    return static_cast<int>(n < 1 ? 1 : n > 32 ? (steps < 32 ? steps : 32) : n < steps ? n : steps);
+}
+__device__ __forceinline__ int adapter_tiles(const LoraPlan &p) { return p.words[p.tile_first() + p.adapters]; }
+
+struct ShrinkArgs {
+    LoraPlan plan;
+    const uint16_t *x;
+    uint32_t ld_x;
+    const uint16_t *w;               // [adapters][r][k], or trans: [adapters][k][r]
+    int64_t stride_w;
+    uint32_t ld_w;
+    LoraWeights lw;                  // ranks
+    int k;                           // the long side
+    float *out;                      // [splits][tokens in the plan's order][padded(r)]
+};
+cudaError_t launch_shrink(const ShrinkArgs &a, bool trans, cudaStream_t stream);
+
+struct ExpandArgs {
+    LoraPlan plan;
+    const float *rows;               // [splits][tokens in the plan's order][padded(r)]
+    int long_side;                   // that they were summed over, 0: one split
+    const uint16_t *w;               // [adapters][n][r], or trans: [adapters][r][n]
+    int64_t stride_w;
+    uint32_t ld_w;
+    LoraWeights lw;                  // ranks, scale
+    int n;                           // columns
+    const void *base;
+    void *y;
+    uint32_t ld_base, ld_y;
+    float *v_out;                    // the rows of r for the backward pass, or null
+    uint32_t ld_v;
+};
+cudaError_t launch_expand(const ExpandArgs &a, bool f32, cudaStream_t stream);
+cudaError_t launch_expand_t(const ExpandArgs &a, bool f32, cudaStream_t stream);     // trans
+
+// One of the two sums over the tokens.
+struct OuterSide {
+    const uint16_t *d;               // [tokens][n]
+    uint32_t ld;
+    int n, blocks;                   // columns, and blocks of them
+    const uint16_t *vt;              // [parts][padded(r)][tiles x 128 tokens]
+    void *out;                       // [adapters] of n x r: strides
+    int64_t stride_n, stride_r, stride_g;
+    float *ws;                       // [2 chunks][n][padded(r)]
+};
+struct OuterArgs {
+    LoraPlan plan;
+    LoraWeights lw;
+    OuterSide side[2];
+    int chunks;                      // of the tiles
+    int f32;
+    int64_t plane;                   // from one part of vt to the next
+    // tiles of a chunk
+    __device__ __forceinline__ int tiles(int all) const { return max(1, (all + chunks - 1) / chunks); }
+};
+size_t outer_vt_bytes(const LoraPlan &p, int r);
+int outer_chunks(const LoraPlan &p, int n, int k, int r);
+struct PrepArgs {
+    LoraPlan plan;
+    LoraWeights lw;
+    const float *v;                  // [tokens][ld_v], or null
+    uint32_t ld_v;
+    const float *dv;                 // [splits][tokens in the plan's order][padded(r)], or null
+    int long_side;                   // that they were summed over
+    float *sum;                      // dv's sum, or null
+    uint16_t *vt[2];                 // of v and of dv
+    int64_t plane;
+    int parts;
+};
+cudaError_t launch_prep(const PrepArgs &a, cudaStream_t stream);
+cudaError_t launch_outer(OuterArgs &a, cudaStream_t stream);
 
 }  // namespace lora
 }  // namespace fp8hg
