@@ -11,6 +11,25 @@
 
 namespace fp8hg {
 
+// Dynamic shared memory beyond 48 KB is asked for once per kernel and device, as
+// much as any of its launches takes.
+template <class K>
+cudaError_t with_smem(K kern, size_t bytes, size_t most, unsigned long long &done) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (__atomic_load_n(&done, __ATOMIC_RELAXED) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    if (e != cudaSuccess) {
+        cudaGetLastError();   // reported here, not by the next call that asks
+        return e;
+    }
+    __atomic_fetch_or(&done, bit, __ATOMIC_RELAXED);
+    return cudaSuccess;
+}
+
 // ---------------------------------------------------------------- layer norm
 
 struct NormArgs {

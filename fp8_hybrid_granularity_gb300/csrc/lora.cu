@@ -94,7 +94,7 @@ cudaError_t launch_lora_plan(const int *ids, const LoraPlan &p, int *words, cuda
     static unsigned long long done;
     const int buckets = p.adapters + 1;
     const int warps = std::max(1, std::min(32, kPlanSmem / (4 * buckets)));
-    const cudaError_t e = lora::with_smem(&k_lora_plan, kPlanSmem, done);
+    const cudaError_t e = with_smem(&k_lora_plan, kPlanSmem, kPlanSmem, done);
     if (e != cudaSuccess) return e;
     return launch_after(&k_lora_plan, dim3(1), warps * 32, static_cast<size_t>(warps) * buckets * 4, stream, 1, ids, p.tokens,
                         p.adapters, words);

@@ -77,24 +77,6 @@ __device__ __forceinline__ void split(float v, uint32_t (&h)[PARTS]) {
 
 __host__ __device__ constexpr int padded(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 inline bool aligned_to(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-// Dynamic shared memory beyond 48 KB is asked for once per kernel and device.
-template <class K>
-cudaError_t with_smem(K kern, size_t bytes, unsigned long long &done) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (__atomic_load_n(&done, __ATOMIC_RELAXED) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e != cudaSuccess) {
-        cudaGetLastError();   // reported here, not by the next call that asks
-        return e;
-    }
-    __atomic_fetch_or(&done, bit, __ATOMIC_RELAXED);
-    return cudaSuccess;
-}
-
 // Sixteen rows of 64 columns, a warp's part of a step: 16-byte piece p of row r.
 // Copied a line (or two) of a row after the other, so that no sector is asked for
 // twice; read back by the four lanes of a row, two rows at a time.

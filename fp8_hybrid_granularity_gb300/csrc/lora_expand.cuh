@@ -242,7 +242,7 @@ cudaError_t run(const ExpandArgs &a, cudaStream_t stream) {
     using S = Shape<RP, TRANS, F32>;
     static unsigned long long done;
     auto *kern = &k_lora_expand<RP, TRANS, F32, WIDE, WAL>;
-    const cudaError_t e = with_smem(kern, S::SMEM, done);
+    const cudaError_t e = with_smem(kern, S::SMEM, S::SMEM, done);
     if (e != cudaSuccess) return e;
     const int64_t most = static_cast<int64_t>(a.plan.max_tiles()) * ((static_cast<int64_t>(a.n) + kCols - 1) / kCols);
     return launch_after(kern, dim3(static_cast<unsigned>(std::min<int64_t>(most, S::CTAS * kSms))), kThreads, S::SMEM, stream, 1, a);

@@ -350,7 +350,7 @@ cudaError_t run(const OuterArgs &a, cudaStream_t stream) {
     static unsigned long long done;
     using S = Shape<RP, PARTS>;
     auto *kern = &k_lora_outer<RP, PARTS, WIDE>;
-    const cudaError_t e = with_smem(kern, S::SMEM, done);
+    const cudaError_t e = with_smem(kern, S::SMEM, S::SMEM, done);
     if (e != cudaSuccess) return e;
     return launch_after(kern, dim3(a.side[0].blocks + a.side[1].blocks, a.chunks), 256, S::SMEM, stream, 1, a);
 }

@@ -181,7 +181,7 @@ cudaError_t run(const ShrinkArgs &a, cudaStream_t stream) {
     using S = Shape<RP, TRANS>;
     static unsigned long long done;
     auto *kern = &k_lora_shrink<RP, TRANS, WIDE, WAL>;
-    const cudaError_t e = with_smem(kern, S::SMEM, done);
+    const cudaError_t e = with_smem(kern, S::SMEM, S::SMEM, done);
     if (e != cudaSuccess) return e;
     return launch_after(kern, dim3(a.plan.max_tiles(), most_splits(a.plan, a.k, RP)), kThreads, S::SMEM, stream, 1, a);
 }

@@ -64,22 +64,22 @@ __device__ __forceinline__ void emit(const NormArgs &a, int q_kind, uint32_t r, 
         a.s[row_at(r, a.ld_s) + (q_kind == Q_ROW ? 0 : c0 >> 7)] = static_cast<uint8_t>(byte);
 }
 
-template <bool XF32, bool WIDE, int Q>
-__global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr) {
+template <bool XF32, bool WIDE>
+__global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr, int q_kind) {
     extern __shared__ float4 params[];    // w, b
-    __shared__ float2 red[2 * 32];
+    __shared__ float red[2][32][4];
     ptx::grid_begin(static_cast<int64_t>(a.rows) * a.cols);
     RowReduce row(red, tpr);
-    const int t = threadIdx.x % tpr, rpb = blockDim.x / tpr;
+    const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, rpb = blockDim.x / tpr;
     const int c0 = t * 16, cols_left = a.cols - c0;
     const uint32_t rows = a.rows, step = gridDim.x * rpb;
     const float inv_n = 1.0f / static_cast<float>(a.cols);
-    uint32_t r = blockIdx.x * rpb + threadIdx.x / tpr;
+    uint32_t r = blockIdx.x * rpb + group;
     Raw<XF32> next;
     next.zero();
     if (r < rows && cols_left > 0) next.template load<WIDE>(a.x, row_at(r, a.ld_x) + c0, cols_left);
     float *w = reinterpret_cast<float *>(params), *b = w + 16 * tpr;
-    if (threadIdx.x < tpr) {
+    if (group == 0) {
         F2 v[8];
         load_params(a.weight, a.param_f32, 1.0f, c0, cols_left, v);
         keep_params(w, t, tpr, v);
@@ -88,29 +88,36 @@ __global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr) {
     }
     __syncthreads();
     for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
-        F2 d[8], p[8];
+        F2 d[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[i] = next.pair(i);
         if (r + step < rows && cols_left > 0) next.template load<WIDE>(a.x, row_at(r + step, a.ld_x) + c0, cols_left);
         const float mean = row.sum(total(d)) * inv_n;
+        const F2 m = f2(-mean);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = add2(d[i], f2(-mean));
+        for (int i = 0; i < 8; ++i) d[i] = add2(d[i], m);
         cut(d, cols_left);
+        F2 sq = mul2(d[0], d[0]), sp = mul2(d[1], d[1]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = mul2(d[i], d[i]);
-        const float rstd = 1.0f / sqrtf(row.sum(total(p)) * inv_n + a.eps);
+        for (int i = 2; i < 8; i += 2) {
+            sq = fma2(d[i], d[i], sq);
+            sp = fma2(d[i + 1], d[i + 1], sp);
+        }
+        sq = add2(sq, sp);
+        const float rstd = 1.0f / sqrtf(row.sum(sq.lo() + sq.hi()) * inv_n + a.eps);
         if (a.stats != nullptr && t == 0 && r < rows)
             reinterpret_cast<float2 *>(a.stats)[r] = make_float2(mean, rstd);
+        const F2 s = f2(rstd);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             F2 w0, w1, b0, b1;
             kept_params(w, t, tpr, j, w0, w1);
             kept_params(b, t, tpr, j, b0, b1);
-            d[2 * j] = fma2(mul2(d[2 * j], f2(rstd)), w0, b0);
-            d[2 * j + 1] = fma2(mul2(d[2 * j + 1], f2(rstd)), w1, b1);
+            d[2 * j] = fma2(mul2(d[2 * j], s), w0, b0);
+            d[2 * j + 1] = fma2(mul2(d[2 * j + 1], s), w1, b1);
         }
-        const float amax = Q == Q_ROW ? row.max(max_of(d)) : 0.0f;
-        emit<WIDE>(a, Q, r, c0, r < rows ? cols_left : 0, amax, d);
+        const float amax = q_kind == Q_ROW ? row.max(max_of(d)) : 0.0f;
+        emit<WIDE>(a, q_kind, r, c0, r < rows ? cols_left : 0, amax, d);
     }
 }
 
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr) {
 // pieces of 16 columns a thread.
 template <bool XF32>
 __global__ void __launch_bounds__(512) k_norm_long(const NormArgs a, int q_kind) {
-    __shared__ float2 red[2 * 32];
+    __shared__ float red[2][32][4];
     ptx::grid_wait();
     const int tpr = blockDim.x;
     RowReduce row(red, tpr);
@@ -190,12 +197,11 @@ cudaError_t run(const NormArgs &a, int q_kind, cudaStream_t stream) {
     const int threads = s.tpr * s.rpb;
     const int grid = std::min((a.rows + s.rpb - 1) / s.rpb, kSms * std::max(1, 1024 / threads));
     const size_t smem = 2 * 16 * sizeof(float) * s.tpr;
-    auto *kern = q_kind == Q_NONE ? &k_norm<XF32, WIDE, Q_NONE> : q_kind == Q_ROW ? &k_norm<XF32, WIDE, Q_ROW> : &k_norm<XF32, WIDE, Q_GROUP>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
-    return launch_after(kern, dim3(grid), threads, smem, stream, 1, a, s.tpr);
+    auto *kern = &k_norm<XF32, WIDE>;
+    static unsigned long long done;
+    const cudaError_t e = with_smem(kern, smem, 2 * 16 * sizeof(float) * 512, done);
+    if (e != cudaSuccess) return e;
+    return launch_after(kern, dim3(grid), threads, smem, stream, 1, a, s.tpr, q_kind);
 }
 
 }  // namespace

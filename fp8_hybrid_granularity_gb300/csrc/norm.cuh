@@ -83,47 +83,86 @@ __device__ __forceinline__ float total(const F2 (&v)[8]) {
     return s.lo() + s.hi();
 }
 
-// Sums (and maxima) over the threads of a row: `warps` whole warps.  Every
-// thread of the CTA calls them in step; two buffers in turn, so that one
-// barrier per sum is enough.
+// One, two or four sums (or a maximum) over the threads of a row: `warps` whole
+// warps, at most 16.  Every thread of the CTA calls them in step; two buffers in
+// turn, so that one barrier for each set is enough.
 struct RowReduce {
-    float2 *buf;     // [2][32]
+    float (*buf)[32][4];     // [2] of a warp's four values
     int warps, first, turn;
-    __device__ __forceinline__ RowReduce(float2 *b, int tpr)
+    __device__ __forceinline__ RowReduce(float (*b)[32][4], int tpr)
         : buf(b), warps(tpr / 32), first(threadIdx.x / tpr * (tpr / 32)), turn(0) {}
-    __device__ __forceinline__ float2 sum(float a, float b) {
-        a = warp_sum(a);
-        b = warp_sum(b);
-        if (warps == 1) return make_float2(a, b);
-        float2 *t = buf + 32 * turn;
-        turn ^= 1;
-        if ((threadIdx.x & 31) == 0) t[threadIdx.x / 32] = make_float2(a, b);
+
+    // The row's from the warps': lane l has value l / (32 / N) of warp l % (32 / N).
+    template <int N, bool MAX>
+    __device__ __forceinline__ void across(float (&v)[N]) {
+        constexpr int W = 32 / N < 16 ? 32 / N : 16;
+        const int lane = threadIdx.x & 31, at = lane % (32 / N);
         __syncthreads();
-        float2 r = t[first];
-        for (int i = 1; i < warps; ++i) r.x += t[first + i].x, r.y += t[first + i].y;
-        return r;
+        const float (*t)[4] = buf[turn] + first;
+        turn ^= 1;
+        float a = at < warps ? t[at][lane / (32 / N)] : 0.0f;
+        if (W < 16 && at + W < warps) {
+            const float u = t[at + W][lane / (32 / N)];
+            a = MAX ? max3_abs(a, a, u) : a + u;
+        }
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) {
+            const float u = __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            a = MAX ? max3_abs(a, a, u) : a + u;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, a, i * (32 / N));
     }
     __device__ __forceinline__ float sum(float a) {
-        a = warp_sum(a);
-        if (warps == 1) return a;
-        float2 *t = buf + 32 * turn;
-        turn ^= 1;
-        if ((threadIdx.x & 31) == 0) t[threadIdx.x / 32].x = a;
-        __syncthreads();
-        float r = t[first].x;
-        for (int i = 1; i < warps; ++i) r += t[first + i].x;
-        return r;
+        float v[1] = {warp_sum(a)};
+        if (warps > 1) {
+            if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x / 32][0] = v[0];
+            across<1, false>(v);
+        }
+        return v[0];
     }
-    __device__ __forceinline__ float max(float m) {
-        m = warp_max_abs(m);
-        if (warps == 1) return m;
-        float2 *t = buf + 32 * turn;
-        turn ^= 1;
-        if ((threadIdx.x & 31) == 0) t[threadIdx.x / 32].x = m;
-        __syncthreads();
-        float r = t[first].x;
-        for (int i = 1; i < warps; ++i) r = max3_abs(r, r, t[first + i].x);
-        return r;
+    __device__ __forceinline__ float max(float a) {
+        float v[1] = {warp_max_abs(a)};
+        if (warps > 1) {
+            if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x / 32][0] = v[0];
+            across<1, true>(v);
+        }
+        return v[0];
+    }
+    __device__ __forceinline__ void sum(float (&v)[2]) {
+        const bool up = threadIdx.x & 16;
+        float a = (up ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[1], 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        if (warps > 1) {
+            if ((threadIdx.x & 15) == 0) buf[turn][threadIdx.x / 32][(threadIdx.x >> 4) & 1] = a;
+            across<2, false>(v);
+        } else {
+            v[0] = __shfl_sync(0xFFFFFFFFu, a, 0);
+            v[1] = __shfl_sync(0xFFFFFFFFu, a, 16);
+        }
+    }
+    // four: halves, then quarters of the warp take over one value each
+    __device__ __forceinline__ void sum(float (&v)[4]) {
+        const int lane = threadIdx.x & 31;
+        const bool up = lane & 16, odd = lane & 8;
+        float a = (up ? v[2] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
+        float b = (up ? v[3] : v[1]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[1] : v[3], 16);
+        a = (odd ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        if (warps > 1) {
+            if ((lane & 7) == 0) buf[turn][threadIdx.x / 32][lane >> 3] = a;
+            across<4, false>(v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, a, 8 * i);
+        }
+    }
+    __device__ __forceinline__ float2 sum(float a, float b) {
+        float v[2] = {a, b};
+        sum(v);
+        return make_float2(v[0], v[1]);
     }
 };
 

@@ -41,7 +41,7 @@ __device__ __forceinline__ void gather(float *sums, int cols, int c0, bool first
 template <bool XF32, bool DF32, bool WIDE>
 __global__ void __launch_bounds__(512) k_norm_bwd(const NormBwdArgs a, int tpr) {
     extern __shared__ float4 shared[];     // w; after the last row the sums, [2][cols], of several rows at a time
-    __shared__ float2 red[2 * 32];
+    __shared__ float red[2][32][4];
     ptx::grid_begin(static_cast<int64_t>(a.rows) * a.cols);
     RowReduce row(red, tpr);
     const int t = threadIdx.x % tpr, rpb = blockDim.x / tpr;
@@ -121,10 +121,169 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormBwdArgs a, int tpr) 
     for (int c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) part[c] = w[c];
 }
 
+// The same for rows of up to 4096 columns that begin at multiples of 32 bytes: R
+// rows at a time (their sums share a barrier), which come through shared memory,
+// STAGES - 1 sets of rows ahead.  A warp copies its own 512 columns of a row, 16
+// bytes a lane next to one another, and reads them back, 16 columns a lane.
+constexpr int kRingCols = 4096;
+template <bool XF32, bool DF32>
+struct Ring {
+    static constexpr int R = XF32 || DF32 ? 1 : 2;
+    static constexpr int STAGES = R == 1 ? 3 : 2;
+    static constexpr int X = XF32 ? 2048 : 1024, D = DF32 ? 2048 : 1024;     // bytes of a warp's columns
+    static constexpr int bytes(int warps, bool add) { return STAGES * R * (X + D + (add ? X : 0)) * warps; }
+};
+
+template <bool F32>
+__device__ __forceinline__ void copy_columns(uint32_t to, const void *base, int64_t at, int left) {
+    constexpr int E = F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31, bytes = max(0, min(512, left)) * E;
+#pragma unroll
+    for (int h = 0; h < E; ++h) {
+        const int p = h * 32 + lane, n = max(0, min(16, bytes - 16 * p));
+        ptx::cp_async16(to + (p ^ ((p >> 3) & 3)) * 16,
+                        static_cast<const uint8_t *>(base) + (n > 0 ? at * E + 16 * p : 0), n);
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void read_columns(uint32_t from, Raw<F32> &v) {
+    constexpr int N = F32 ? 4 : 2;
+#pragma unroll
+    for (int h = 0; h < N; ++h) {
+        const int p = (threadIdx.x & 31) * N + h;
+        ptx::ld_shared_v4(from + (p ^ ((p >> 3) & 3)) * 16, v.w[4 * h], v.w[4 * h + 1], v.w[4 * h + 2], v.w[4 * h + 3]);
+    }
+}
+
+template <bool XF32, bool DF32>
+__global__ void __launch_bounds__(256, 2) k_norm_bwd_ring(const NormBwdArgs a, int tpr) {
+    using S = Ring<XF32, DF32>;
+    constexpr int R = S::R;
+    extern __shared__ float4 shared[];     // the rings, w; after the last row the sums, [2][cols], of several rows at a time
+    __shared__ float red[2][32][4];
+    ptx::grid_begin(static_cast<int64_t>(a.rows) * a.cols);
+    RowReduce row(red, tpr);
+    const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, warps = blockDim.x / 32, rpb = blockDim.x / tpr * R;
+    const int c0 = t * 16, cols_left = a.cols - c0, w0 = t / 32 * 512;
+    const uint32_t rows = a.rows, step = gridDim.x * rpb;
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    const bool with_add = a.add != nullptr;
+    const int set = S::X + S::D + (with_add ? S::X : 0);
+    const uint32_t ring = ptx::smem_u32(shared) + threadIdx.x / 32 * set;
+    auto slot = [&](int stage, int i) { return ring + (stage * R + i) * warps * set; };
+    float2 st[S::STAGES - 1][R];
+    uint32_t r = blockIdx.x * rpb + group * R;
+    auto copy = [&](uint32_t r, int stage) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int left = r + i < rows ? a.cols - w0 : 0;
+            copy_columns<XF32>(slot(stage, i), a.x, row_at(r + i, a.ld_x) + w0, left);
+            copy_columns<DF32>(slot(stage, i) + S::X, a.dy, row_at(r + i, a.ld_dy) + w0, left);
+            if (with_add) copy_columns<XF32>(slot(stage, i) + S::X + S::D, a.add, row_at(r + i, a.ld_add) + w0, left);
+        }
+        ptx::cp_async_commit();
+    };
+    auto stat = [&](uint32_t r) { return r < rows ? reinterpret_cast<const float2 *>(a.stats)[r] : make_float2(0.0f, 0.0f); };
+#pragma unroll
+    for (int k = 0; k < S::STAGES; ++k) copy(r + k * step, k);
+#pragma unroll
+    for (int k = 0; k < S::STAGES - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < R; ++i) st[k][i] = stat(r + k * step + i);
+    float *w = reinterpret_cast<float *>(shared) + S::STAGES * R * warps * set / 4;
+    if (group == 0) {
+        F2 v[8];
+        load_params(a.weight, a.param_f32, 1.0f, c0, cols_left, v);
+        keep_params(w, t, tpr, v);
+    }
+    __syncthreads();
+    F2 dw[8], db[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[i] = db[i] = f2(0.0f);
+    int stage = 0;
+    for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
+        ptx::cp_async_wait<S::STAGES - 1>();
+        __syncwarp();
+        Raw<XF32> x[R];
+        Raw<DF32> dy[R];
+        float sums[2 * R], mean[R], rstd[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            read_columns(slot(stage, i), x[i]);
+            read_columns(slot(stage, i) + S::X, dy[i]);
+            mean[i] = st[0][i].x, rstd[i] = st[0][i].y;
+        }
+#pragma unroll
+        for (int k = 0; k + 1 < S::STAGES - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < R; ++i) st[k][i] = st[k + 1][i];
+#pragma unroll
+        for (int i = 0; i < R; ++i) st[S::STAGES - 2][i] = stat(r + (S::STAGES - 1) * step + i);
+        // rows past the last are zeros, and so are their statistics
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            F2 sg = f2(0.0f), sgx = f2(0.0f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                F2 wj[2];
+                kept_params(w, t, tpr, j, wj[0], wj[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const F2 d = dy[i].pair(2 * j + e), xh = mul2(add2(x[i].pair(2 * j + e), f2(-mean[i])), f2(rstd[i]));
+                    dw[2 * j + e] = fma2(d, xh, dw[2 * j + e]);
+                    db[2 * j + e] = add2(db[2 * j + e], d);
+                    const F2 g = mul2(d, wj[e]);
+                    sg = add2(sg, g);
+                    sgx = fma2(g, xh, sgx);
+                }
+            }
+            sums[2 * i] = sg.lo() + sg.hi();
+            sums[2 * i + 1] = sgx.lo() + sgx.hi();
+        }
+        row.sum(sums);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const F2 mg = f2(-sums[2 * i] * inv_n), mgx = f2(-sums[2 * i + 1] * inv_n), rs = f2(rstd[i]);
+            Raw<XF32> add;
+            add.zero();
+            if (with_add) read_columns(slot(stage, i) + S::X + S::D, add);
+            F2 dx[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                F2 wj[2];
+                kept_params(w, t, tpr, j, wj[0], wj[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const F2 xh = mul2(add2(x[i].pair(2 * j + e), f2(-mean[i])), rs), g = mul2(dy[i].pair(2 * j + e), wj[e]);
+                    dx[2 * j + e] = fma2(rs, fma2(xh, mgx, add2(g, mg)), add.pair(2 * j + e));
+                }
+            }
+            store_values<true>(a.dx, XF32, row_at(r + i, a.ld_dx) + c0, r + i < rows ? cols_left : 0, dx);
+        }
+        __syncwarp();
+        copy(r + S::STAGES * step, stage);
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+    }
+    ptx::cp_async_wait<0>();
+    if (a.ws == nullptr) return;
+    float *part = a.ws + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    if (blockDim.x == tpr) {
+        store_values<false>(part, 1, c0, cols_left, dw);
+        store_values<false>(part, 1, a.cols + c0, cols_left, db);
+        return;
+    }
+    __syncthreads();
+    for (int q = 0; q < static_cast<int>(blockDim.x) / tpr; ++q) {
+        if (group == q) gather(w, a.cols, c0, q == 0, dw, db);
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) part[c] = w[c];
+}
+
 // dx of rows of any length, a CTA each.
 template <bool XF32, bool DF32>
 __global__ void __launch_bounds__(512) k_norm_bwd_long(const NormBwdArgs a) {
-    __shared__ float2 red[2 * 32];
+    __shared__ float red[2][32][4];
     ptx::grid_wait();
     const int tpr = blockDim.x;
     RowReduce row(red, tpr);
@@ -260,8 +419,17 @@ cudaError_t run(const NormBwdArgs &a, cudaStream_t stream) {
         const bool wide = wide_rows(a.x, a.x_f32, a.ld_x) && wide_rows(a.dy, a.dy_f32, a.ld_dy) &&
                           wide_rows(a.dx, a.x_f32, a.ld_dx) && (a.add == nullptr || wide_rows(a.add, a.x_f32, a.ld_add));
         const size_t smem = (s.rpb > 1 ? 2 : 1) * 16 * sizeof(float) * s.tpr;   // at most 32 KB
-        e = wide ? launch_after(&k_norm_bwd<XF32, DF32, true>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr)
-                 : launch_after(&k_norm_bwd<XF32, DF32, false>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr);
+        if (wide && a.cols <= kRingCols) {
+            using G = Ring<XF32, DF32>;
+            static unsigned long long done;
+            const size_t rings = G::bytes(s.tpr * s.rpb / 32, a.add != nullptr);
+            e = with_smem(&k_norm_bwd_ring<XF32, DF32>, smem + rings, G::bytes(8, true) + 16 * 1024, done);
+            if (e == cudaSuccess)
+                e = launch_after(&k_norm_bwd_ring<XF32, DF32>, dim3(parts), s.tpr * s.rpb, smem + rings, stream, 1, a, s.tpr);
+        } else {
+            e = wide ? launch_after(&k_norm_bwd<XF32, DF32, true>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr)
+                     : launch_after(&k_norm_bwd<XF32, DF32, false>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr);
+        }
     }
     if (e != cudaSuccess || a.ws == nullptr) return e;
     return launch_after(&k_norm_sums, dim3(static_cast<unsigned>((2 * static_cast<int64_t>(a.cols) + 31) / 32)), 512, 0,
