@@ -77,13 +77,43 @@ __device__ __forceinline__ void split(float v, uint32_t (&h)[PARTS]) {
 
 __host__ __device__ constexpr int padded(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 inline bool aligned_to(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-// Sixteen rows of 64 columns, a warp's part of a step: 16-byte piece p of row r.
-// Copied a line (or two) of a row after the other, so that no sector is asked for
-// twice; read back by the four lanes of a row, two rows at a time.
+// Sixteen rows of 64 columns, a warp's part of a step: offset of 16-byte piece p of
+// row r in a stage of the ring.  Copied a line (or two) of a row after the other, so
+// that no sector is asked for twice; read back by the four lanes of a row, two
+// rows at a time.
 template <int PIECES>
-__device__ __forceinline__ uint32_t slot(uint32_t ring, int stage, int r, int p) {
-    return ring + ((stage * (kLoraTile / 16) + threadIdx.x / 32) * 16 + r) * (PIECES * 16) + (p ^ (r & 7)) * 16;
+__device__ __forceinline__ uint32_t slot(int r, int p) {
+    return (threadIdx.x / 32 * 16 + r) * (PIECES * 16) + (p ^ (r & 7)) * 16;
 }
+
+// A thread's share of the copies of the other operand's tiles, ROWS x COLS values
+// in rows of ROW bytes (and 32 more after every 16 rows if PAD): the same pieces of
+// every tile, `step` elements on from one to the next.
+template <int ROWS, int COLS, int ROW, bool PAD, bool ALIGNED>
+struct TileCopy {
+    static constexpr int P = COLS / 8, N = (ROWS * P + 255) / 256;
+    const uint16_t *from[N];
+    int rows, cols;          // of a whole tile that are there
+
+    __device__ __forceinline__ TileCopy(const uint16_t *w, uint32_t ld, int rows_, int cols_) : rows(rows_), cols(cols_) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) from[i] = w + row_at(row(i), ld) + col();
+    }
+    static __device__ __forceinline__ int row(int i) { return (threadIdx.x + 256 * i) / P; }
+    static __device__ __forceinline__ int col() { return threadIdx.x % P * 8; }     // 256 is a multiple of P
+    static __device__ __forceinline__ uint32_t at(int i) { return row(i) * ROW + (PAD ? row(i) / 16 * 32 : 0) + 2 * col(); }
+    // rows_left, cols_left: of this tile
+    __device__ __forceinline__ void copy(uint32_t to, const uint16_t *any, int rows_left, int cols_left, int64_t step) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (ROWS * P < 256 && row(i) >= ROWS) break;
+            const bool in = row(i) < min(rows, rows_left);
+            const int left = in ? min(cols, cols_left) - col() : 0;
+            copy8<ALIGNED>(to + at(i), left > 0 ? from[i] : any, left);
+            from[i] += step;
+        }
+    }
+};
 
 // The long side's splits of shrink: one round of CTAs over the plan's tiles, at
 // least 128 columns each.  On the device from the plan, on the host an upper bound.

@@ -63,69 +63,63 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32>::CTAS) k_lora_
             token[i] = m < tile.count ? a.plan.words[a.plan.order() + tile.first + m] : -1;
         }
         // the rows that the lane copies
+        constexpr int E = F32 ? 4 : 8, ES = 16 / E;      // elements of a piece, their size
+        const int64_t n0 = static_cast<int64_t>(first) * kCols;
         const uint8_t *row[16 / S::ROWS];
+        bool have[16 / S::ROWS];
+        const bool with_base = active && a.base != nullptr;
         if constexpr (WIDE) {
 #pragma unroll
             for (int i = 0; i < 16 / S::ROWS; ++i) {
                 const int m = warp * 16 + i * S::ROWS + lane / S::PIECES;
-                row[i] = nullptr;
-                if (m < tile.count && a.base != nullptr)
-                    row[i] = static_cast<const uint8_t *>(a.base) + row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_base) * (F32 ? 4 : 2) +
-                             lane % S::PIECES * 16;
+                have[i] = m < tile.count && with_base;
+                row[i] = static_cast<const uint8_t *>(a.base);
+                if (have[i]) row[i] += (row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_base) + n0) * ES + lane % S::PIECES * 16;
             }
         }
+        TileCopy<TRANS ? RP : kCols, TRANS ? kCols : RP, S::ROW, !TRANS, WAL> wc(w + (TRANS ? n0 : n0 * a.ld_w), a.ld_w, TRANS ? rank : kCols,
+                                                                                 TRANS ? kCols : rank);
+        const int64_t wstep = TRANS ? kCols : static_cast<int64_t>(kCols) * a.ld_w;
+        int in_stage = 0, left = static_cast<int>(a.n - n0);      // of the next copies
         norm::Raw<F32> late[2];      // rows at odd addresses: from load to store
-        auto load = [&](int step) {
-            const int stage = step % S::STAGES, n = (first + step) * kCols, left = a.n - n;
-            const uint32_t to = wbase + stage * S::W;
-            if (rank > 0) {
-                if constexpr (TRANS) {
-                    for (int i = threadIdx.x; i < RP * (kCols / 8); i += kThreads) {
-                        const int r = i / (kCols / 8), c = i % (kCols / 8) * 8;
-                        const bool in = r < rank && c < left;
-                        copy8<WAL>(to + r * S::ROW + 2 * c, in ? w + row_at(r, a.ld_w) + n + c : a.w, in ? left - c : 0);
+        auto load = [&]() {
+            if (rank > 0) wc.copy(wbase + in_stage * S::W, a.w, TRANS ? RP : left, TRANS ? left : RP, wstep);
+            if (with_base) {
+                if constexpr (WIDE) {
+                    const int n = max(0, min(16, ES * (left - lane % S::PIECES * E)));
+#pragma unroll
+                    for (int i = 0; i < 16 / S::ROWS; ++i) {
+                        ptx::cp_async16(ring + in_stage * S::BASE + slot<S::PIECES>(i * S::ROWS + lane / S::PIECES, lane % S::PIECES),
+                                        have[i] && n > 0 ? row[i] : static_cast<const uint8_t *>(a.base), have[i] ? n : 0);
+                        row[i] += kCols * ES;
                     }
                 } else {
-                    for (int i = threadIdx.x; i < kCols * (RP / 8); i += kThreads) {
-                        const int r = i / (RP / 8), c = i % (RP / 8) * 8;
-                        const bool in = r < left && c < rank;
-                        copy8<WAL>(to + r * S::ROW + r / 16 * 32 + 2 * c, in ? w + row_at(n + r, a.ld_w) + c : a.w, in ? rank - c : 0);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int n = token[i] < 0 ? 0 : left - 16 * t;
+                        if (n > 0) late[i].template load<false>(a.base, row_at(token[i], a.ld_base) + a.n - left + 16 * t, n);
+                        else late[i].zero();
                     }
                 }
             }
-            if (!active || a.base == nullptr) return;
-            if constexpr (WIDE) {
-                constexpr int E = F32 ? 4 : 8;     // elements of a piece
-                const int c = max(0, min(E, left - lane % S::PIECES * E));
-#pragma unroll
-                for (int i = 0; i < 16 / S::ROWS; ++i) {
-                    const bool in = row[i] != nullptr && c > 0;
-                    ptx::cp_async16(slot<S::PIECES>(ring, stage, i * S::ROWS + lane / S::PIECES, lane % S::PIECES),
-                                    in ? row[i] + static_cast<int64_t>(n) * (16 / E) : static_cast<const uint8_t *>(a.base), in ? c * (16 / E) : 0);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int have = token[i] < 0 ? 0 : left - 16 * t;
-                    if (have > 0) late[i].template load<false>(a.base, row_at(token[i], a.ld_base) + n + 16 * t, have);
-                    else late[i].zero();
-                }
-            }
+            left -= kCols;
         };
-        auto store_late = [&](int step) {
-            if (WIDE || !active || a.base == nullptr) return;
+        auto store_late = [&]() {
+            if (!WIDE && with_base) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int p = 0; p < S::PIECES / 4; ++p) {
-                    const uint32_t *v = late[i].w + 4 * p;
-                    ptx::st_shared_v4(slot<S::PIECES>(ring, step % S::STAGES, i * 8 + g, t * (S::PIECES / 4) + p), v[0], v[1], v[2], v[3]);
-                }
+                    for (int p = 0; p < S::PIECES / 4; ++p) {
+                        const uint32_t *v = late[i].w + 4 * p;
+                        ptx::st_shared_v4(ring + in_stage * S::BASE + slot<S::PIECES>(i * 8 + g, t * (S::PIECES / 4) + p), v[0], v[1], v[2], v[3]);
+                    }
+            }
+            in_stage = in_stage + 1 == S::STAGES ? 0 : in_stage + 1;
         };
         for (int s = 0; s < S::STAGES - 1; ++s) {
             if (s < steps) {
-                load(s);
-                store_late(s);
+                load();
+                store_late();
             }
             ptx::cp_async_commit();
         }
@@ -157,80 +151,88 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32>::CTAS) k_lora_
                 for (int p = 0; p < S::PARTS; ++p) f[p][ks >> 1][i + 2 * (ks & 1)] = lo[p] | hi[p] << 16;
             }
 
+        // the lane's places of the weights: rows of two neighbouring terms, 16 columns each,
+        // or column i of fragment j, row 16 (i / 2) + 2 j + (i & 1)
+        const int wi = lane & 7;
+        const uint32_t wlane = wbase + (TRANS ? 2 * t * S::ROW + 32 * (g >> 1)
+                                              : (16 * (wi >> 1) + 2 * (lane >> 4) + (wi & 1)) * S::ROW + (wi >> 1) * 32 + ((lane >> 3) & 1) * 16);
+        int64_t yat[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) yat[i] = token[i] >= 0 ? row_at(token[i], a.ld_y) + n0 + 16 * t : 0;
+        int stage = 0, out_left = static_cast<int>(a.n - n0) - 16 * t;
         for (int s = 0; s < steps; ++s) {
             ptx::cp_async_wait<S::STAGES - 2>();
             __syncthreads();
             const bool more = s + S::STAGES - 1 < steps;
-            if (more) load(s + S::STAGES - 1);
+            if (more) load();
             ptx::cp_async_commit();
-            if (!active) continue;
-            const int stage = s % S::STAGES;
-            const uint32_t wat = wbase + stage * S::W;
-            norm::Raw<F32> in[2];
-            float acc[8][4];
+            if (active) {
+                const uint32_t wat = wlane + stage * S::W;
+                norm::Raw<F32> in[2];
+                float acc[8][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                in[i].zero();
-                if (a.base != nullptr) {
+                for (int i = 0; i < 2; ++i) {
+                    in[i].zero();
+                    if (with_base) {
 #pragma unroll
-                    for (int h = 0; h < S::PIECES / 4; ++h)
-                        ptx::ld_shared_v4(slot<S::PIECES>(ring, stage, i * 8 + g, t * (S::PIECES / 4) + h), in[i].w[4 * h], in[i].w[4 * h + 1],
-                                          in[i].w[4 * h + 2], in[i].w[4 * h + 3]);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const F2 p = in[i].pair(j);
-                    acc[j][2 * i] = F32 ? 0.0f : p.lo();
-                    acc[j][2 * i + 1] = F32 ? 0.0f : p.hi();
-                }
-            }
-            if (rank > 0) {
-#pragma unroll
-                for (int ks = 0; ks < S::KS; ++ks) {
-                    uint32_t b[8][2];
-                    if constexpr (TRANS) {
-                        // rows of two neighbouring terms, 16 columns each: the lane's column of a pair
-                        uint32_t u[4][8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t p = wat + (ks * 16 + 2 * t + (e & 1) + (e >> 1) * 8) * S::ROW + 32 * (g >> 1);
-                            ptx::ld_shared_v4(p, u[e][0], u[e][1], u[e][2], u[e][3]);
-                            ptx::ld_shared_v4(p + 16, u[e][4], u[e][5], u[e][6], u[e][7]);
-                        }
-                        const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            b[j][0] = __byte_perm(u[0][j], u[1][j], sel);
-                            b[j][1] = __byte_perm(u[2][j], u[3][j], sel);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            // column i of fragment j: row 16 (i / 2) + 2 j + (i & 1)
-                            const int i = lane & 7, r = 16 * (i >> 1) + 2 * (j + (lane >> 4)) + (i & 1);
-                            uint32_t m[4];
-                            ptx::ldmatrix_x4<false>(wat + r * S::ROW + r / 16 * 32 + (ks * 16 + ((lane >> 3) & 1) * 8) * 2, m);
-                            b[j][0] = m[0], b[j][1] = m[1], b[j + 1][0] = m[2], b[j + 1][1] = m[3];
-                        }
+                        for (int h = 0; h < S::PIECES / 4; ++h)
+                            ptx::ld_shared_v4(ring + stage * S::BASE + slot<S::PIECES>(i * 8 + g, t * (S::PIECES / 4) + h), in[i].w[4 * h],
+                                              in[i].w[4 * h + 1], in[i].w[4 * h + 2], in[i].w[4 * h + 3]);
                     }
 #pragma unroll
-                    for (int p = 0; p < S::PARTS; ++p)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) ptx::mma_bf16(acc[j], f[p][ks], b[j][0], b[j][1]);
+                    for (int j = 0; j < 8; ++j) {
+                        const F2 p = in[i].pair(j);
+                        acc[j][2 * i] = F32 ? 0.0f : p.lo();
+                        acc[j][2 * i + 1] = F32 ? 0.0f : p.hi();
+                    }
                 }
-            }
-            const int c = (first + s) * kCols + 16 * t;
+                if (rank > 0) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                F2 out[8];
+                    for (int ks = 0; ks < S::KS; ++ks) {
+                        uint32_t b[8][2];
+                        if constexpr (TRANS) {
+                            uint32_t u[4][8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    out[j] = f2(acc[j][2 * i], acc[j][2 * i + 1]);
-                    if constexpr (F32) out[j] = add2(in[i].pair(j), out[j]);
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t p = wat + (ks * 16 + (e & 1) + (e >> 1) * 8) * S::ROW;
+                                ptx::ld_shared_v4(p, u[e][0], u[e][1], u[e][2], u[e][3]);
+                                ptx::ld_shared_v4(p + 16, u[e][4], u[e][5], u[e][6], u[e][7]);
+                            }
+                            const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                b[j][0] = __byte_perm(u[0][j], u[1][j], sel);
+                                b[j][1] = __byte_perm(u[2][j], u[3][j], sel);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2) {
+                                uint32_t m[4];
+                                ptx::ldmatrix_x4<false>(wat + 2 * j * S::ROW + ks * 32, m);
+                                b[j][0] = m[0], b[j][1] = m[1], b[j + 1][0] = m[2], b[j + 1][1] = m[3];
+                            }
+                        }
+#pragma unroll
+                        for (int p = 0; p < S::PARTS; ++p)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) ptx::mma_bf16(acc[j], f[p][ks], b[j][0], b[j][1]);
+                    }
                 }
-                norm::store_values<WIDE>(a.y, F32, token[i] >= 0 ? row_at(token[i], a.ld_y) + c : 0, token[i] >= 0 ? a.n - c : 0, out);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    F2 out[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        out[j] = f2(acc[j][2 * i], acc[j][2 * i + 1]);
+                        if constexpr (F32) out[j] = add2(in[i].pair(j), out[j]);
+                    }
+                    norm::store_values<WIDE>(a.y, F32, yat[i], token[i] >= 0 ? out_left : 0, out);
+                    yat[i] += kCols;
+                }
+                out_left -= kCols;
             }
-            if (more) store_late(s + S::STAGES - 1);
+            if (more) store_late();
+            stage = stage + 1 == S::STAGES ? 0 : stage + 1;
         }
         ptx::cp_async_wait<0>();
         __syncthreads();      // before the next tile's copies

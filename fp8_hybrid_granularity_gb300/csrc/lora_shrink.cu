@@ -48,120 +48,126 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS>::CTAS) k_lora_shrin
 
     // the rows that the lane copies: every fourth of the warp's (those it reads, at odd addresses)
     const uint16_t *row[4];
+    bool have[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = warp * 16 + (WIDE ? i * 4 + lane / 8 : (i & 1) * 8 + g);
-        row[i] = m < tile.count ? a.x + row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_x) + (WIDE ? lane % 8 * 8 : 16 * t) : nullptr;
+    for (int i = 0; i < (WIDE ? 4 : 2); ++i) {
+        const int m = warp * 16 + (WIDE ? i * 4 + lane / 8 : i * 8 + g);
+        have[i] = m < tile.count;
+        row[i] = a.x;
+        if (have[i])
+            row[i] += row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_x) + (WIDE ? lane % 8 * 8 : 16 * t) + first * kCols;
     }
     const bool active = warp * 16 < tile.count;
+    const int64_t k0 = static_cast<int64_t>(first) * kCols;
+    TileCopy<TRANS ? kCols : RP, TRANS ? RP : kCols, S::ROW, TRANS, WAL> wc(w + (TRANS ? k0 * a.ld_w : k0), a.ld_w, TRANS ? kCols : rank,
+                                                                             TRANS ? rank : kCols);
+    const int64_t wstep = TRANS ? static_cast<int64_t>(kCols) * a.ld_w : kCols;
+    int in_stage = 0, left = a.k - first * kCols;      // of the next copies
     uint32_t late[2][8];     // rows at odd addresses: from load to store
-    auto load = [&](int step) {
-        const int stage = step % S::STAGES, k = (first + step) * kCols, left = a.k - k;
-        const uint32_t to = base + stage * S::W;
-        if constexpr (TRANS) {
-            for (int i = tid; i < kCols * (RP / 8); i += kThreads) {
-                const int r = i / (RP / 8), c = i % (RP / 8) * 8;
-                const bool in = r < left && c < rank;
-                copy8<WAL>(to + r * S::ROW + r / 16 * 32 + 2 * c, in ? w + row_at(k + r, a.ld_w) + c : a.w, in ? rank - c : 0);
-            }
-        } else {
-            for (int i = tid; i < RP * (kCols / 8); i += kThreads) {
-                const int r = i / (kCols / 8), c = i % (kCols / 8) * 8;
-                const bool in = r < rank && c < left;
-                copy8<WAL>(to + r * S::ROW + 2 * c, in ? w + row_at(r, a.ld_w) + k + c : a.w, in ? left - c : 0);
-            }
-        }
-        if (!active) return;
-        if constexpr (WIDE) {
+    auto load = [&]() {
+        wc.copy(base + in_stage * S::W, a.w, TRANS ? left : RP, TRANS ? RP : left, wstep);
+        if (active) {
+            if constexpr (WIDE) {
+                const int n = max(0, min(16, 2 * (left - lane % 8 * 8)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = row[i] == nullptr ? 0 : max(0, min(8, left - lane % 8 * 8));
-                ptx::cp_async16(slot<8>(ring, stage, i * 4 + lane / 8, lane % 8), n > 0 ? row[i] + k : a.x, 2 * n);
-            }
-        } else {
+                for (int i = 0; i < 4; ++i) {
+                    ptx::cp_async16(ring + in_stage * S::X + slot<8>(i * 4 + lane / 8, lane % 8), have[i] && n > 0 ? row[i] : a.x, have[i] ? n : 0);
+                    row[i] += kCols;
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int have = row[i] == nullptr ? 0 : left - 16 * t;
-                if (have > 0) {
-                    ragged::load16<false>(row[i] + k, have, late[i]);
-                } else {
+                for (int i = 0; i < 2; ++i) {
+                    const int n = have[i] ? left - 16 * t : 0;
+                    if (n > 0) {
+                        ragged::load16<false>(row[i], n, late[i]);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) late[i][j] = 0u;
+                        for (int j = 0; j < 8; ++j) late[i][j] = 0u;
+                    }
+                    row[i] += kCols;
                 }
             }
         }
+        left -= kCols;
     };
-    auto store_late = [&](int step) {
-        if (WIDE || !active) return;
+    auto store_late = [&]() {
+        if (!WIDE && active) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const uint32_t(&v)[8] = late[p / 2];
-            const int h = p % 2 * 4;
-            ptx::st_shared_v4(slot<8>(ring, step % S::STAGES, p / 2 * 8 + g, 2 * t + p % 2), v[h], v[h + 1], v[h + 2], v[h + 3]);
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t(&v)[8] = late[p / 2];
+                const int h = p % 2 * 4;
+                ptx::st_shared_v4(ring + in_stage * S::X + slot<8>(p / 2 * 8 + g, 2 * t + p % 2), v[h], v[h + 1], v[h + 2], v[h + 3]);
+            }
         }
+        in_stage = in_stage + 1 == S::STAGES ? 0 : in_stage + 1;
     };
     for (int s = 0; s < S::STAGES - 1; ++s) {
         if (s < steps) {
-            load(s);
-            store_late(s);
+            load();
+            store_late();
         }
         ptx::cp_async_commit();
     }
     float sum[RP / 8][4];
 #pragma unroll
     for (int j = 0; j < RP / 8; ++j) sum[j][0] = sum[j][1] = sum[j][2] = sum[j][3] = 0.0f;
+    // the lane's places: of x; of W rows j * 8 + g, or of row 16 (i / 2) + (i & 1), and
+    // 2 on: a lane's terms
+    const uint32_t xat = ring + slot<8>(g, 2 * t);
+    const int wi = lane & 7;
+    const uint32_t wat = base + (TRANS ? (16 * (wi >> 1) + (wi & 1) + 2 * ((lane >> 3) & 1)) * S::ROW + (wi >> 1) * 32 + (lane >> 4) * 16
+                                       : g * S::ROW + 32 * t);
+    int stage = 0;
     for (int s = 0; s < steps; ++s) {
         ptx::cp_async_wait<S::STAGES - 2>();
         __syncthreads();
         const bool more = s + S::STAGES - 1 < steps;
-        if (more) load(s + S::STAGES - 1);
+        if (more) load();
         ptx::cp_async_commit();
-        if (!active) continue;
-        const int stage = s % S::STAGES;
-        const uint32_t at = base + stage * S::W;
-        uint32_t f[2][8];
+        if (active) {
+            const uint32_t at = wat + stage * S::W, xp = xat + stage * S::X;
+            uint32_t f[2][8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            ptx::ld_shared_v4(slot<8>(ring, stage, i * 8 + g, 2 * t), f[i][0], f[i][1], f[i][2], f[i][3]);
-            ptx::ld_shared_v4(slot<8>(ring, stage, i * 8 + g, 2 * t + 1), f[i][4], f[i][5], f[i][6], f[i][7]);
-        }
-        // sums of 64 products, then to registers
-        auto products = [&](int j, const uint32_t (&b)[8]) {
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t fa[4] = {f[0][2 * q], f[1][2 * q], f[0][2 * q + 1], f[1][2 * q + 1]};
-                ptx::mma_bf16(acc, fa, b[2 * q], b[2 * q + 1]);
+            for (int i = 0; i < 2; ++i) {
+                ptx::ld_shared_v4(xp + i * 8 * 128, f[i][0], f[i][1], f[i][2], f[i][3]);
+                ptx::ld_shared_v4((xp ^ 16) + i * 8 * 128, f[i][4], f[i][5], f[i][6], f[i][7]);
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) sum[j][q] += acc[q];
-        };
-        if constexpr (TRANS) {
-#pragma unroll
-            for (int jj = 0; jj < RP / 16; ++jj) {
-                uint32_t b0[8], b1[8];
+            // sums of 64 products, then to registers
+            auto products = [&](int j, const uint32_t (&b)[8]) {
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    // rows 16 (i / 2) + 4 q + (i & 1), and 2 on: a lane's terms
-                    const int i = lane & 7, r = 16 * (i >> 1) + 4 * q + (i & 1) + ((lane >> 3) & 1) * 2;
-                    uint32_t m[4];
-                    ptx::ldmatrix_x4<true>(at + r * S::ROW + r / 16 * 32 + (jj * 16 + (lane >> 4) * 8) * 2, m);
-                    b0[2 * q] = m[0], b0[2 * q + 1] = m[1], b1[2 * q] = m[2], b1[2 * q + 1] = m[3];
+                    const uint32_t fa[4] = {f[0][2 * q], f[1][2 * q], f[0][2 * q + 1], f[1][2 * q + 1]};
+                    ptx::mma_bf16(acc, fa, b[2 * q], b[2 * q + 1]);
                 }
-                products(2 * jj, b0);
-                products(2 * jj + 1, b1);
-            }
-        } else {
 #pragma unroll
-            for (int j = 0; j < RP / 8; ++j) {
-                uint32_t b[8];
-                const uint32_t p = at + (j * 8 + g) * S::ROW + 32 * t;
-                ptx::ld_shared_v4(p, b[0], b[1], b[2], b[3]);
-                ptx::ld_shared_v4(p + 16, b[4], b[5], b[6], b[7]);
-                products(j, b);
+                for (int q = 0; q < 4; ++q) sum[j][q] += acc[q];
+            };
+            if constexpr (TRANS) {
+#pragma unroll
+                for (int jj = 0; jj < RP / 16; ++jj) {
+                    uint32_t b0[8], b1[8];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t m[4];
+                        ptx::ldmatrix_x4<true>(at + q * 4 * S::ROW + jj * 32, m);
+                        b0[2 * q] = m[0], b0[2 * q + 1] = m[1], b1[2 * q] = m[2], b1[2 * q + 1] = m[3];
+                    }
+                    products(2 * jj, b0);
+                    products(2 * jj + 1, b1);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < RP / 8; ++j) {
+                    uint32_t b[8];
+                    ptx::ld_shared_v4(at + j * 8 * S::ROW, b[0], b[1], b[2], b[3]);
+                    ptx::ld_shared_v4(at + j * 8 * S::ROW + 16, b[4], b[5], b[6], b[7]);
+                    products(j, b);
+                }
             }
         }
-        if (more) store_late(s + S::STAGES - 1);
+        if (more) store_late();
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
     }
     ptx::cp_async_wait<0>();
     float *out = a.out + (static_cast<int64_t>(blockIdx.y) * a.plan.tokens + tile.first) * RP;

@@ -64,6 +64,71 @@ __device__ __forceinline__ void emit(const NormArgs &a, int q_kind, uint32_t r, 
         a.s[row_at(r, a.ld_s) + (q_kind == Q_ROW ? 0 : c0 >> 7)] = static_cast<uint8_t>(byte);
 }
 
+// The parameters to shared memory, by the first group of threads.
+__device__ __forceinline__ void keep_both(const NormArgs &a, int group, int t, int tpr, float *w, float *b) {
+    if (group == 0) {
+        F2 v[8];
+        load_params(a.weight, a.param_f32, 1.0f, t * 16, a.cols - t * 16, v);
+        keep_params(w, t, tpr, v);
+        load_params(a.bias, a.param_f32, 0.0f, t * 16, a.cols - t * 16, v);
+        keep_params(b, t, tpr, v);
+    }
+    __syncthreads();
+}
+
+// R rows at a time from their values in registers: the mean, the differences, rstd,
+// y and where it goes.  The rows' sums share shuffles and a barrier, and their
+// parameters are read from shared memory once.
+template <bool WIDE, int R>
+__device__ __forceinline__ void finish(const NormArgs &a, int q_kind, uint32_t r, int t, int tpr, float inv_n, RowReduce &row, const float *w,
+                                       const float *b, F2 (&d)[R][8], float (&mean)[R], float (&rstd)[R]) {
+    const int c0 = t * 16, cols_left = a.cols - c0;
+    const uint32_t rows = a.rows;
+#pragma unroll
+    for (int i = 0; i < R; ++i) mean[i] = total(d[i]);
+    row.sum(mean);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        mean[i] *= inv_n;
+        const F2 m = f2(-mean[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[i][j] = add2(d[i][j], m);
+        cut(d[i], cols_left);
+        F2 sq = mul2(d[i][0], d[i][0]), sp = mul2(d[i][1], d[i][1]);
+#pragma unroll
+        for (int j = 2; j < 8; j += 2) {
+            sq = fma2(d[i][j], d[i][j], sq);
+            sp = fma2(d[i][j + 1], d[i][j + 1], sp);
+        }
+        sq = add2(sq, sp);
+        rstd[i] = sq.lo() + sq.hi();
+    }
+    row.sum(rstd);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        rstd[i] = rsqrtf(rstd[i] * inv_n + a.eps);
+        if (a.stats != nullptr && t == 0 && r + i < rows) reinterpret_cast<float2 *>(a.stats)[r + i] = make_float2(mean[i], rstd[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        F2 w0, w1, b0, b1;
+        kept_params(w, t, tpr, j, w0, w1);
+        kept_params(b, t, tpr, j, b0, b1);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const F2 s = f2(rstd[i]);
+            d[i][2 * j] = fma2(mul2(d[i][2 * j], s), w0, b0);
+            d[i][2 * j + 1] = fma2(mul2(d[i][2 * j + 1], s), w1, b1);
+        }
+    }
+    float amax[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) amax[i] = q_kind == Q_ROW ? max_of(d[i]) : 0.0f;
+    if (q_kind == Q_ROW) row.max(amax);
+#pragma unroll
+    for (int i = 0; i < R; ++i) emit<WIDE>(a, q_kind, r + i, c0, r + i < rows ? cols_left : 0, amax[i], d[i]);
+}
+
 template <bool XF32, bool WIDE>
 __global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr, int q_kind) {
     extern __shared__ float4 params[];    // w, b
@@ -79,46 +144,62 @@ __global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr, int q_k
     next.zero();
     if (r < rows && cols_left > 0) next.template load<WIDE>(a.x, row_at(r, a.ld_x) + c0, cols_left);
     float *w = reinterpret_cast<float *>(params), *b = w + 16 * tpr;
-    if (group == 0) {
-        F2 v[8];
-        load_params(a.weight, a.param_f32, 1.0f, c0, cols_left, v);
-        keep_params(w, t, tpr, v);
-        load_params(a.bias, a.param_f32, 0.0f, c0, cols_left, v);
-        keep_params(b, t, tpr, v);
-    }
-    __syncthreads();
+    keep_both(a, group, t, tpr, w, b);
     for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
-        F2 d[8];
+        F2 d[1][8];
+        float mean[1], rstd[1];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = next.pair(i);
+        for (int j = 0; j < 8; ++j) d[0][j] = next.pair(j);
         if (r + step < rows && cols_left > 0) next.template load<WIDE>(a.x, row_at(r + step, a.ld_x) + c0, cols_left);
-        const float mean = row.sum(total(d)) * inv_n;
-        const F2 m = f2(-mean);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = add2(d[i], m);
-        cut(d, cols_left);
-        F2 sq = mul2(d[0], d[0]), sp = mul2(d[1], d[1]);
-#pragma unroll
-        for (int i = 2; i < 8; i += 2) {
-            sq = fma2(d[i], d[i], sq);
-            sp = fma2(d[i + 1], d[i + 1], sp);
-        }
-        sq = add2(sq, sp);
-        const float rstd = 1.0f / sqrtf(row.sum(sq.lo() + sq.hi()) * inv_n + a.eps);
-        if (a.stats != nullptr && t == 0 && r < rows)
-            reinterpret_cast<float2 *>(a.stats)[r] = make_float2(mean, rstd);
-        const F2 s = f2(rstd);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            F2 w0, w1, b0, b1;
-            kept_params(w, t, tpr, j, w0, w1);
-            kept_params(b, t, tpr, j, b0, b1);
-            d[2 * j] = fma2(mul2(d[2 * j], s), w0, b0);
-            d[2 * j + 1] = fma2(mul2(d[2 * j + 1], s), w1, b1);
-        }
-        const float amax = q_kind == Q_ROW ? row.max(max_of(d)) : 0.0f;
-        emit<WIDE>(a, q_kind, r, c0, r < rows ? cols_left : 0, amax, d);
+        finish<WIDE>(a, q_kind, r, t, tpr, inv_n, row, w, b, d, mean, rstd);
     }
+}
+
+// Many rows of up to 4096 columns that begin at multiples of 32 bytes: R at a time,
+// through shared memory, the next ones' copies in flight.
+constexpr int kRingCols = 4096;
+template <bool XF32, int R>
+__global__ void __launch_bounds__(256, 2) k_norm_ring(const NormArgs a, int tpr, int q_kind) {
+    constexpr int X = XF32 ? 2048 : 1024, STAGES = 2;     // bytes of a warp's columns
+    extern __shared__ float4 params[];    // w, b, the rings
+    __shared__ float red[2][32][4];
+    ptx::grid_begin(static_cast<int64_t>(a.rows) * a.cols);
+    RowReduce row(red, tpr);
+    const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, rpb = blockDim.x / tpr * R, warps = blockDim.x / 32;
+    const int w0 = t / 32 * 512;
+    const uint32_t rows = a.rows, step = gridDim.x * rpb;
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    float *w = reinterpret_cast<float *>(params), *b = w + 16 * tpr;
+    const uint32_t ring = ptx::smem_u32(b + 16 * tpr) + threadIdx.x / 32 * X;
+    auto copy = [&](uint32_t r, int stage) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            copy_columns<XF32>(ring + (stage * R + i) * warps * X, a.x, row_at(r + i, a.ld_x) + w0, r + i < rows ? a.cols - w0 : 0);
+        ptx::cp_async_commit();
+    };
+    uint32_t r = blockIdx.x * rpb + group * R;
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k) copy(r + k * step, k);
+    keep_both(a, group, t, tpr, w, b);
+    int stage = 0;
+    for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
+        ptx::cp_async_wait<STAGES - 1>();
+        __syncwarp();
+        F2 d[R][8];
+        float mean[R], rstd[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            Raw<XF32> x;
+            read_columns(ring + (stage * R + i) * warps * X, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[i][j] = x.pair(j);
+        }
+        __syncwarp();
+        copy(r + STAGES * step, stage);
+        stage ^= 1;
+        finish<true>(a, q_kind, r, t, tpr, inv_n, row, w, b, d, mean, rstd);
+    }
+    ptx::cp_async_wait<0>();
 }
 
 // Rows of any length, a CTA each: the row is read for each of its sums, in
@@ -158,7 +239,7 @@ __global__ void __launch_bounds__(512) k_norm_long(const NormArgs a, int q_kind)
             for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], v[i]);
             s += total(v);
         }
-        const float rstd = 1.0f / sqrtf(row.sum(s) * inv_n + a.eps);
+        const float rstd = rsqrtf(row.sum(s) * inv_n + a.eps);
         if (a.stats != nullptr && threadIdx.x == 0) reinterpret_cast<float2 *>(a.stats)[r] = make_float2(mean, rstd);
         auto value = [&](int64_t c0, F2 (&v)[8]) {
             const int left = static_cast<int>(a.cols - c0);
@@ -191,17 +272,26 @@ __global__ void __launch_bounds__(512) k_norm_long(const NormArgs a, int q_kind)
     }
 }
 
+// Copies ahead pay off where a CTA has a few sets of rows.
 template <bool XF32, bool WIDE>
 cudaError_t run(const NormArgs &a, int q_kind, cudaStream_t stream) {
     const Shape s = shape_of(a.cols);
     const int threads = s.tpr * s.rpb;
-    const int grid = std::min((a.rows + s.rpb - 1) / s.rpb, kSms * std::max(1, 1024 / threads));
-    const size_t smem = 2 * 16 * sizeof(float) * s.tpr;
-    auto *kern = &k_norm<XF32, WIDE>;
+    const size_t params = 2 * 16 * sizeof(float) * s.tpr;
+    if (WIDE && a.cols <= kRingCols && a.rows >= 4 * s.rpb * kSms) {
+        constexpr int R = XF32 ? 1 : 4, kWarpBytes = 2 * R * (XF32 ? 2048 : 1024);
+        static unsigned long long done;
+        const size_t smem = params + kWarpBytes * (threads / 32);
+        const cudaError_t e = with_smem(&k_norm_ring<XF32, R>, smem, 32 * 1024 + kWarpBytes * 8, done);
+        if (e != cudaSuccess) return e;
+        const int sets = (a.rows + s.rpb * R - 1) / (s.rpb * R);
+        return launch_after(&k_norm_ring<XF32, R>, dim3(std::min(sets, 2 * kSms)), threads, smem, stream, 1, a, s.tpr, q_kind);
+    }
     static unsigned long long done;
-    const cudaError_t e = with_smem(kern, smem, 2 * 16 * sizeof(float) * 512, done);
+    const cudaError_t e = with_smem(&k_norm<XF32, WIDE>, params, 2 * 16 * sizeof(float) * 512, done);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, dim3(grid), threads, smem, stream, 1, a, s.tpr, q_kind);
+    const int grid = std::min((a.rows + s.rpb - 1) / s.rpb, kSms * std::max(1, 1024 / threads));
+    return launch_after(&k_norm<XF32, WIDE>, dim3(grid), threads, params, stream, 1, a, s.tpr, q_kind);
 }
 
 }  // namespace

@@ -159,6 +159,17 @@ struct RowReduce {
             for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, a, 8 * i);
         }
     }
+    __device__ __forceinline__ void sum(float (&v)[1]) { v[0] = sum(v[0]); }
+    __device__ __forceinline__ void max(float (&v)[1]) { v[0] = max(v[0]); }
+    template <int N>
+    __device__ __forceinline__ void max(float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = warp_max_abs(v[i]);
+            if (warps > 1 && (threadIdx.x & 31) == 0) buf[turn][threadIdx.x / 32][i] = v[i];
+        }
+        if (warps > 1) across<N, true>(v);
+    }
     __device__ __forceinline__ float2 sum(float a, float b) {
         float v[2] = {a, b};
         sum(v);
@@ -178,6 +189,29 @@ __device__ __forceinline__ void kept_params(const float *at, int t, int tpr, int
     const float4 q = reinterpret_cast<const float4 *>(at)[j * tpr + t];
     a = f2(q.x, q.y);
     b = f2(q.z, q.w);
+}
+
+// A warp's 512 columns of a row through shared memory: copied 16 bytes a lane next
+// to one another (no sector is asked for twice), read back 16 columns a lane.
+template <bool F32>
+__device__ __forceinline__ void copy_columns(uint32_t to, const void *base, int64_t at, int left) {
+    constexpr int E = F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31, bytes = max(0, min(512, left)) * E;
+#pragma unroll
+    for (int h = 0; h < E; ++h) {
+        const int p = h * 32 + lane, n = max(0, min(16, bytes - 16 * p));
+        ptx::cp_async16(to + (p ^ ((p >> 3) & 3)) * 16,
+                        static_cast<const uint8_t *>(base) + (n > 0 ? at * E + 16 * p : 0), n);
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void read_columns(uint32_t from, Raw<F32> &v) {
+    constexpr int N = F32 ? 4 : 2;
+#pragma unroll
+    for (int h = 0; h < N; ++h) {
+        const int p = (threadIdx.x & 31) * N + h;
+        ptx::ld_shared_v4(from + (p ^ ((p >> 3) & 3)) * 16, v.w[4 * h], v.w[4 * h + 1], v.w[4 * h + 2], v.w[4 * h + 3]);
+    }
 }
 
 // How a row is dealt out where it fits the registers: threads a row (whole

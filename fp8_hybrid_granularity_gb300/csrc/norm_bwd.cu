@@ -123,8 +123,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormBwdArgs a, int tpr) 
 
 // The same for rows of up to 4096 columns that begin at multiples of 32 bytes: R
 // rows at a time (their sums share a barrier), which come through shared memory,
-// STAGES - 1 sets of rows ahead.  A warp copies its own 512 columns of a row, 16
-// bytes a lane next to one another, and reads them back, 16 columns a lane.
+// STAGES - 1 sets of rows ahead.
 constexpr int kRingCols = 4096;
 template <bool XF32, bool DF32>
 struct Ring {
@@ -133,27 +132,6 @@ struct Ring {
     static constexpr int X = XF32 ? 2048 : 1024, D = DF32 ? 2048 : 1024;     // bytes of a warp's columns
     static constexpr int bytes(int warps, bool add) { return STAGES * R * (X + D + (add ? X : 0)) * warps; }
 };
-
-template <bool F32>
-__device__ __forceinline__ void copy_columns(uint32_t to, const void *base, int64_t at, int left) {
-    constexpr int E = F32 ? 4 : 2;
-    const int lane = threadIdx.x & 31, bytes = max(0, min(512, left)) * E;
-#pragma unroll
-    for (int h = 0; h < E; ++h) {
-        const int p = h * 32 + lane, n = max(0, min(16, bytes - 16 * p));
-        ptx::cp_async16(to + (p ^ ((p >> 3) & 3)) * 16,
-                        static_cast<const uint8_t *>(base) + (n > 0 ? at * E + 16 * p : 0), n);
-    }
-}
-template <bool F32>
-__device__ __forceinline__ void read_columns(uint32_t from, Raw<F32> &v) {
-    constexpr int N = F32 ? 4 : 2;
-#pragma unroll
-    for (int h = 0; h < N; ++h) {
-        const int p = (threadIdx.x & 31) * N + h;
-        ptx::ld_shared_v4(from + (p ^ ((p >> 3) & 3)) * 16, v.w[4 * h], v.w[4 * h + 1], v.w[4 * h + 2], v.w[4 * h + 3]);
-    }
-}
 
 template <bool XF32, bool DF32>
 __global__ void __launch_bounds__(256, 2) k_norm_bwd_ring(const NormBwdArgs a, int tpr) {
