@@ -70,7 +70,8 @@ cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t stream);
 // The tokens of a batch grouped by adapter, as int32 words in device memory:
 // [0] tiles, then first position and first tile of every adapter (one more than
 // adapters: the tokens without one), the tokens in that order, and the tiles
-// (adapter or -1, first position) of up to kLoraTile tokens of one adapter each.
+// (adapter or -1, first position, tokens, 0) of up to kLoraTile tokens of one
+// adapter each.
 constexpr int kLoraTile = 128;
 constexpr int kLoraMaxAdapters = 4096;
 constexpr int kLoraMaxRank = 128;
@@ -80,12 +81,12 @@ struct LoraPlan {
     __host__ __device__ int64_t starts() const { return 4; }
     __host__ __device__ int64_t tile_first() const { return starts() + adapters + 2; }
     __host__ __device__ int64_t order() const { return tile_first() + adapters + 2; }
-    __host__ __device__ int64_t tiles() const { return order() + tokens + ((order() + tokens) & 1); }
+    __host__ __device__ int64_t tiles() const { return (order() + tokens + 3) / 4 * 4; }
     // no more tiles than this
     __host__ __device__ int max_tiles() const {
         return tokens / kLoraTile + (adapters + 1 < tokens ? adapters + 1 : tokens);
     }
-    __host__ __device__ int64_t size() const { return tiles() + 2 * static_cast<int64_t>(max_tiles()); }
+    __host__ __device__ int64_t size() const { return tiles() + 4 * static_cast<int64_t>(max_tiles()); }
 };
 cudaError_t launch_lora_plan(const int *ids, const LoraPlan &p, int *words, cudaStream_t stream);
 

@@ -66,10 +66,8 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const int *ids, int tokens, 
             counts[w * buckets + b] = bn;
             bn += c;
         }
-        for (int f = first; f < bn; f += kLoraTile, ++bt) {
-            words[p.tiles() + 2 * static_cast<int64_t>(bt)] = b == adapters ? -1 : b;
-            words[p.tiles() + 2 * static_cast<int64_t>(bt) + 1] = f;
-        }
+        for (int f = first; f < bn; f += kLoraTile, ++bt)
+            reinterpret_cast<int4 *>(words + p.tiles())[bt] = make_int4(b == adapters ? -1 : b, f, min(kLoraTile, bn - f), 0);
     }
     if (b1 == buckets && b0 < b1) {
         words[p.starts() + buckets] = bn;

@@ -39,10 +39,8 @@ struct Tile {
     int adapter, first, count;
 };
 __device__ __forceinline__ Tile tile_at(const LoraPlan &p, int i) {
-    const int2 t = reinterpret_cast<const int2 *>(p.words + p.tiles())[i];
-    const int *starts = p.words + p.starts();
-    const int end = starts[(t.x < 0 ? p.adapters : t.x) + 1];
-    return {t.x, t.y, min(kLoraTile, end - t.y)};
+    const int4 t = reinterpret_cast<const int4 *>(p.words + p.tiles())[i];
+    return {t.x, t.y, t.z};
 }
 __device__ __forceinline__ int rank_of(const LoraWeights &w, int g) {
     return w.ranks == nullptr ? w.r : max(0, min(w.r, w.ranks[g]));
@@ -118,12 +116,13 @@ struct TileCopy {
 // The long side's splits of shrink: one round of CTAs over the plan's tiles, at
 // least 128 columns each.  On the device from the plan, on the host an upper bound.
 constexpr int kShrinkCols = 64;
+constexpr int kMaxSplits = 16;
 __host__ __device__ constexpr int shrink_slots(int rp) { return kSms * (rp <= 32 ? 3 : rp <= 64 ? 2 : 1); }
 __host__ __device__ inline int shrink_splits(int64_t tiles, int k, int rp) {
     const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
     int64_t n = shrink_slots(rp) / (tiles < 1 ? 1 : tiles);
     n = n < (steps + 1) / 2 ? n : (steps + 1) / 2;
-    n = n < 1 ? 1 : n > 32 ? 32 : n;
+    n = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
     const int64_t per = (steps + n - 1) / n;
     return static_cast<int>((steps + per - 1) / per);
 }
@@ -131,7 +130,8 @@ __host__ __device__ inline int shrink_splits(int64_t tiles, int k, int rp) {
 inline int most_splits(const LoraPlan &p, int k, int rp) {
     const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
     const int64_t n = shrink_slots(rp) / ((p.tokens + kLoraTile - 1) / kLoraTile);
-    return static_cast<int>(n < 1 ? 1 : n > 32 ? (steps < 32 ? steps : 32) : n < steps ? n : steps);
+    const int64_t most = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
+    return static_cast<int>(most < steps ? most : steps);
 }
 __device__ __forceinline__ int adapter_tiles(const LoraPlan &p) { return p.words[p.tile_first() + p.adapters]; }
 

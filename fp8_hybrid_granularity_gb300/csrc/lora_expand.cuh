@@ -125,28 +125,50 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32>::CTAS) k_lora_
         }
 
         uint32_t f[S::PARTS][S::KS][4];
+        // the rows of r: partial sums in their order, U splits' loads in flight
+        constexpr int U = S::KS <= 4 ? 8 / S::KS : 1;
+        float v[2][2 * S::KS][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int ks = 0; ks < 2 * S::KS; ++ks) v[i][ks][0] = v[i][ks][1] = 0.0f;
+        const float *vp = a.rows + (tile.first + warp * 16 + g) * static_cast<int64_t>(RP) + 2 * t;
+        const int64_t next = static_cast<int64_t>(a.plan.tokens) * RP;
+        for (int s0 = 0; s0 < splits && active && rank > 0; s0 += U) {
+            uint2 q[U][2][2 * S::KS];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int ks = 0; ks < 2 * S::KS; ++ks) {
+                        q[u][i][ks] = make_uint2(0u, 0u);
+                        if (s0 + u < splits && token[i] >= 0) q[u][i][ks] = ptx::ld_v2(vp + (s0 + u) * next + i * 8 * RP + ks * 8);
+                    }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int ks = 0; ks < 2 * S::KS; ++ks) {
+                        v[i][ks][0] += __uint_as_float(q[u][i][ks].x);
+                        v[i][ks][1] += __uint_as_float(q[u][i][ks].y);
+                    }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int ks = 0; ks < 2 * S::KS; ++ks) {
                 const int r = ks * 8 + 2 * t;
-                float v[2] = {0.0f, 0.0f};
-                if (token[i] >= 0 && r < rank) {
-                    const float *p = a.rows + (tile.first + warp * 16 + i * 8 + g) * static_cast<int64_t>(RP) + r;
-                    for (int s = 0; s < splits; ++s, p += static_cast<int64_t>(a.plan.tokens) * RP) {
-                        const uint2 q = ptx::ld_v2(p);
-                        v[0] += __uint_as_float(q.x), v[1] += __uint_as_float(q.y);
-                    }
-                    if (r + 1 >= rank) v[1] = 0.0f;
-                }
+                const float v0 = r < rank ? v[i][ks][0] : 0.0f, v1 = r + 1 < rank ? v[i][ks][1] : 0.0f;
                 if (a.v_out != nullptr && first == 0 && token[i] >= 0) {
                     float *to = a.v_out + row_at(token[i], a.ld_v) + r;
-                    if (r < a.lw.r) to[0] = v[0];
-                    if (r + 1 < a.lw.r) to[1] = v[1];
+                    if (r < a.lw.r) to[0] = v0;
+                    if (r + 1 < a.lw.r) to[1] = v1;
                 }
                 uint32_t lo[S::PARTS], hi[S::PARTS];
-                split<S::PARTS>(v[0] * scale, lo);
-                split<S::PARTS>(v[1] * scale, hi);
+                lora::split<S::PARTS>(v0 * scale, lo);
+                lora::split<S::PARTS>(v1 * scale, hi);
 #pragma unroll
                 for (int p = 0; p < S::PARTS; ++p) f[p][ks >> 1][i + 2 * (ks & 1)] = lo[p] | hi[p] << 16;
             }

@@ -83,15 +83,17 @@ __global__ void __launch_bounds__(256) k_lora_prep(const PrepArgs a) {
 }
 
 // -------------------------------------------------------------------- outer
+// Sixteen warps: eight times the columns, and the rows of r in two halves.
+constexpr int kThreads = 512;
 template <int RP, int PARTS>
 struct Shape {
     static constexpr int CT = RP <= 64 ? 4 : 2;          // fragments of 16 columns, a warp
     static constexpr int CL = 2 * CT;                    // neighbouring columns of a lane
     static constexpr int COLS = 8 * 16 * CT;             // of a CTA
+    static constexpr int J = RP / 16;                    // fragments of 8 rows of r, a warp
     static constexpr int V = PARTS * RP * kChunk * 2;    // of a step
     static constexpr int D = kChunk * COLS * 2;
-    static constexpr int CTAS = RP <= 16 ? 2 : 1;
-    static constexpr int STAGES = RP <= 16 ? 3 : 4;
+    static constexpr int STAGES = 4;
     static constexpr int SMEM = STAGES * (V + D);
 };
 
@@ -126,7 +128,7 @@ __device__ __forceinline__ void load_cols(const uint16_t *p, int left, uint32_t 
 }
 
 template <int RP, int PARTS, bool WIDE>
-__global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(const OuterArgs a) {
+__global__ void __launch_bounds__(kThreads) k_lora_outer(const OuterArgs a) {
     using S = Shape<RP, PARTS>;
     extern __shared__ __align__(128) uint8_t smem[];
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * (static_cast<int64_t>(a.side[0].n) + a.side[1].n));
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(co
     const OuterSide &o = a.side[second];
     const int n0 = (blockIdx.x - (second ? a.side[0].blocks : 0)) * S::COLS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
-    const int col = n0 + warp * 16 * S::CT + g * S::CL, left = o.n - col;
+    const int half = warp >> 3, wcol = warp & 7, col = n0 + wcol * 16 * S::CT + g * S::CL, left = o.n - col;
     const int *tile_first = a.plan.words + a.plan.tile_first(), *order = a.plan.words + a.plan.order();
     const int all = adapter_tiles(a.plan), per = a.tiles(all);
     const int t0 = blockIdx.y * per, t1 = min(all, t0 + per);
@@ -142,24 +144,34 @@ __global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(co
     const uint32_t vring = ptx::smem_u32(smem), ring = vring + S::STAGES * S::V;
     const int64_t ld_vt = static_cast<int64_t>(a.plan.max_tiles()) * kLoraTile;
 
-    // the copies' place, some steps ahead of the products': a tile, 32 tokens of it
+    // the copies' place, some steps ahead of the products': a tile, 32 tokens of it.
+    // The tile and the tokens of the next copies are asked for a step before them.
     int ahead = t0, ahead_c = 0, stage_in = 0;
-    Tile from = tile_at(a.plan, t0);
-    uint32_t late[8][S::CL / 2];     // rows at odd addresses: from load to store
+    Tile from = tile_at(a.plan, t0), then = tile_at(a.plan, min(t0 + 1, t1 - 1));
+    int token[4];
+    auto look_up = [&]() {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int m = ahead_c * kChunk + 8 * t + 4 * half + e;
+            token[e] = ahead < t1 && m < from.count && left > 0 ? order[from.first + m] : -1;
+        }
+    };
+    look_up();
+    // of a lane's eight rows the warp copies four, the warp of the other half the others
+    uint32_t late[4][S::CL / 2];     // rows at odd addresses: from load to store
     auto load = [&]() {
-        for (int q = tid; q < PARTS * RP * (kChunk / 8); q += 256) {
+        for (int q = tid; q < PARTS * RP * (kChunk / 8); q += kThreads) {
             const int r = q / (kChunk / 8), m = q % (kChunk / 8) * 8;     // r: part and row
             ptx::cp_async16(vring + stage_in * S::V + q * 16,
                             o.vt + (r / RP) * a.plane + (r % RP) * ld_vt + static_cast<int64_t>(ahead) * kLoraTile + ahead_c * kChunk + m, 16);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int m = ahead_c * kChunk + 8 * t + e;
-            const int have = m < from.count ? left : 0;
-            const uint16_t *p = have > 0 ? o.d + row_at(order[from.first + m], o.ld) + col : o.d;
+        for (int e = 0; e < 4; ++e) {
+            const int have = token[e] >= 0 ? left : 0;
+            const uint16_t *p = have > 0 ? o.d + row_at(token[e], o.ld) + col : o.d;
             if constexpr (WIDE) {
                 const int n = max(0, min(S::CL, have));
-                const uint32_t to = ring + (((stage_in * 8 + warp) * 8 + e) * 32 + lane) * (2 * S::CL);
+                const uint32_t to = ring + (((stage_in * 8 + wcol) * 8 + 4 * half + e) * 32 + lane) * (2 * S::CL);
                 if constexpr (S::CL == 8) ptx::cp_async16(to, p, 2 * n);
                 else ptx::cp_async8(to, p, 2 * n);
             } else if (have > 0) {
@@ -173,8 +185,8 @@ __global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(co
     auto store_late = [&](int stage) {
         if (WIDE) return;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t to = ring + (((stage * 8 + warp) * 8 + e) * 32 + lane) * (2 * S::CL);
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t to = ring + (((stage * 8 + wcol) * 8 + 4 * half + e) * 32 + lane) * (2 * S::CL);
             if constexpr (S::CL == 8) ptx::st_shared_v4(to, late[e][0], late[e][1], late[e][2], late[e][3]);
             else ptx::st_shared_v2(to, late[e][0], late[e][1]);
         }
@@ -183,8 +195,11 @@ __global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(co
         stage_in = stage_in + 1 == S::STAGES ? 0 : stage_in + 1;
         if (++ahead_c * kChunk >= from.count) {
             ahead_c = 0;
-            if (++ahead < t1) from = tile_at(a.plan, ahead);
+            ++ahead;
+            from = then;
+            then = tile_at(a.plan, min(ahead + 1, t1 - 1));
         }
+        look_up();
     };
     for (int s = 0; s < S::STAGES - 1; ++s) {
         if (ahead < t1) {
@@ -195,17 +210,18 @@ __global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(co
         ptx::cp_async_commit();
     }
 
-    float sum[S::CT][RP / 8][4];
+    float sum[S::CT][S::J][4];
     auto clear = [&]() {
 #pragma unroll
         for (int i = 0; i < S::CT; ++i)
 #pragma unroll
-            for (int j = 0; j < RP / 8; ++j) sum[i][j][0] = sum[i][j][1] = sum[i][j][2] = sum[i][j][3] = 0.0f;
+            for (int j = 0; j < S::J; ++j) sum[i][j][0] = sum[i][j][1] = sum[i][j][2] = sum[i][j][3] = 0.0f;
     };
     clear();
     int stage = 0;
     for (int i = t0; i < t1; ++i) {
         const Tile tile = tile_at(a.plan, i);
+        const int begin = tile_first[tile.adapter], end = tile_first[tile.adapter + 1];
         for (int c = 0; c * kChunk < tile.count; ++c) {
             ptx::cp_async_wait<S::STAGES - 2>();
             __syncthreads();
@@ -218,7 +234,7 @@ __global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(co
             uint32_t d[8][S::CL / 2];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t p = ring + (((stage * 8 + warp) * 8 + e) * 32 + lane) * (2 * S::CL);
+                const uint32_t p = ring + (((stage * 8 + wcol) * 8 + e) * 32 + lane) * (2 * S::CL);
                 if constexpr (S::CL == 8) ptx::ld_shared_v4(p, d[e][0], d[e][1], d[e][2], d[e][3]);
                 else ptx::ld_shared_v2(p, d[e][0], d[e][1]);
             }
@@ -235,11 +251,11 @@ __global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(co
                 }
             // sums of 32 tokens' products, then to registers
 #pragma unroll
-            for (int j = 0; j < RP / 8; ++j) {
+            for (int j = 0; j < S::J; ++j) {
                 uint32_t b[PARTS][4];
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
-                    ptx::ld_shared_v4(vring + stage * S::V + (p * RP + j * 8 + g) * (2 * kChunk) + 16 * t, b[p][0], b[p][1], b[p][2], b[p][3]);
+                    ptx::ld_shared_v4(vring + stage * S::V + (p * RP + (half * S::J + j) * 8 + g) * (2 * kChunk) + 16 * t, b[p][0], b[p][1], b[p][2], b[p][3]);
                 float acc[S::CT][4];
 #pragma unroll
                 for (int k = 0; k < S::CT; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
@@ -257,7 +273,6 @@ __global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(co
             if (filled >= 0) store_late(filled);
             stage = stage + 1 == S::STAGES ? 0 : stage + 1;
         }
-        const int begin = tile_first[tile.adapter], end = tile_first[tile.adapter + 1];
         if (i + 1 < t1 && i + 1 < end) continue;
         // the adapter's last tile, here or at all
         const bool whole = begin >= t0 && end <= t1;
@@ -265,8 +280,8 @@ __global__ void __launch_bounds__(256, (Shape<RP, PARTS>::CTAS)) k_lora_outer(co
 #pragma unroll
         for (int k = 0; k < S::CT; ++k)
 #pragma unroll
-            for (int j = 0; j < RP / 8; ++j) {
-                const int r = j * 8 + 2 * t;
+            for (int j = 0; j < S::J; ++j) {
+                const int r = (half * S::J + j) * 8 + 2 * t;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int c = col + 2 * k + e;
@@ -352,7 +367,7 @@ cudaError_t run(const OuterArgs &a, cudaStream_t stream) {
     auto *kern = &k_lora_outer<RP, PARTS, WIDE>;
     const cudaError_t e = with_smem(kern, S::SMEM, S::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, dim3(a.side[0].blocks + a.side[1].blocks, a.chunks), 256, S::SMEM, stream, 1, a);
+    return launch_after(kern, dim3(a.side[0].blocks + a.side[1].blocks, a.chunks), kThreads, S::SMEM, stream, 1, a);
 }
 template <int RP>
 cudaError_t pick(const OuterArgs &a, bool wide, cudaStream_t stream) {
@@ -372,7 +387,7 @@ size_t outer_vt_bytes(const LoraPlan &p, int r) {
 }
 // Chunks of the tiles: one round of CTAs.
 int outer_chunks(const LoraPlan &p, int n, int k, int r) {
-    const int rp = padded(r), slots = kSms * (rp <= 16 ? 2 : 1);
+    const int rp = padded(r), slots = kSms;
     return std::max(1, std::min(p.max_tiles(), slots / (blocks_of(n, rp) + blocks_of(k, rp))));
 }
 

@@ -35,10 +35,10 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS>::CTAS) k_lora_shrin
     using S = Shape<RP, TRANS>;
     extern __shared__ __align__(128) uint8_t smem[];
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * a.k);
+    const Tile tile = tile_at(a.plan, blockIdx.x);      // its place is there, if it is a tile or not
     const int tiles = adapter_tiles(a.plan);
     const int splits = shrink_splits(tiles, a.k, RP);
     if (static_cast<int>(blockIdx.x) >= tiles || static_cast<int>(blockIdx.y) >= splits) return;
-    const Tile tile = tile_at(a.plan, blockIdx.x);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
     const int rank = rank_of(a.lw, tile.adapter);
     const uint16_t *w = a.w + tile.adapter * a.stride_w;

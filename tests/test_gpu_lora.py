@@ -66,9 +66,9 @@ def test_plan(cuda_lib, t, g):
     assert torch.equal(w[6 + g:8 + 2 * g].long(), first) and int(w[0]) == int(first[-1])
     at = 8 + 2 * g
     assert torch.equal(w[at:at + t].long(), torch.sort(bucket, stable=True)[1])
-    at += t + ((at + t) & 1)
-    got = w[at:at + 2 * int(w[0])].view(-1, 2)
-    want = [(i if i < g else -1, int(starts[i]) + 128 * j) for i in range(g + 1) for j in range(int(tiles[i]))]
+    at += t + -(at + t) % 4
+    got = w[at:at + 4 * int(w[0])].view(-1, 4)
+    want = [(i if i < g else -1, int(starts[i]) + 128 * j, min(128, int(counts[i]) - 128 * j), 0) for i in range(g + 1) for j in range(int(tiles[i]))]
     assert got.tolist() == [list(e) for e in want]
 
 
