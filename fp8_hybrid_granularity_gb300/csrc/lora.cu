@@ -194,14 +194,14 @@ cudaError_t launch_lora_add_bwd(const LoraBwdArgs &a, cudaStream_t stream) {
         p.vt[0] = vt0;
         p.vt[1] = vt1;
         p.parts = a.dw_f32 ? 3 : 2;
-        p.plane = static_cast<int64_t>(ws.vt / sizeof(uint16_t) / 3);
         e = lora::launch_prep(p, stream);
         if (e != cudaSuccess) return e;
         lora::OuterArgs o{};
         o.plan = a.plan;
         o.lw = a.w;
         o.f32 = a.dw_f32;
-        o.plane = p.plane;
+        o.err = error_word();
+        if (o.err == nullptr) return cudaErrorUnknown;
         o.side[0] = {a.dy, a.ld_dy, a.w.n, 0, vt0, a.db, a.w.r, 1, static_cast<int64_t>(a.w.n) * a.w.r, parts};
         o.side[1] = {a.x, a.ld_x, a.w.k, 0, vt1, a.da, 1, a.w.k, static_cast<int64_t>(a.w.k) * a.w.r, nullptr};
         o.side[1].ws = parts + 2 * static_cast<size_t>(ws.chunks) * a.w.n * lora::padded(a.w.r);

@@ -171,7 +171,7 @@ struct OuterSide {
     const uint16_t *d;               // [tokens][n]
     uint32_t ld;
     int n, blocks;                   // columns, and blocks of them
-    const uint16_t *vt;              // [parts][padded(r)][tiles x 128 tokens]
+    const uint16_t *vt;              // by 64 tokens: [parts][padded(r)][64], swizzled
     void *out;                       // [adapters] of n x r: strides
     int64_t stride_n, stride_r, stride_g;
     float *ws;                       // [2 chunks][n][padded(r)]
@@ -182,7 +182,7 @@ struct OuterArgs {
     OuterSide side[2];
     int chunks;                      // of the tiles
     int f32;
-    int64_t plane;                   // from one part of vt to the next
+    unsigned int *err;               // the device's error word
     // tiles of a chunk
     __device__ __forceinline__ int tiles(int all) const { return max(1, (all + chunks - 1) / chunks); }
 };
@@ -197,7 +197,6 @@ struct PrepArgs {
     int long_side;                   // that they were summed over
     float *sum;                      // dv's sum, or null
     uint16_t *vt[2];                 // of v and of dv
-    int64_t plane;
     int parts;
 };
 cudaError_t launch_prep(const PrepArgs &a, cudaStream_t stream);

@@ -2,25 +2,25 @@
 // v[t][r], for dB (d = dy) and dA (d = x, v = dv) in one launch.
 //
 // The rows of r come first, in a kernel of their own: partial sums added, scaled,
-// taken apart into BF16 parts and transposed, so that a fragment's terms, the
-// tokens, are neighbours.  Of d's rows a lane takes 8 (or 4) neighbouring columns
-// of eight tokens, through its own slots, and puts the pairs of tokens together
-// itself.  A CTA takes 512 (or 256) columns and a chunk of the tiles; an
-// adapter whose tokens are in several chunks leaves partial sums there, which one
-// more kernel adds in a fixed order.
+// taken apart into BF16 parts and transposed, a step's tokens next to one another
+// as the tensor core takes them.  Then 128 columns of d are the rows of a
+// tcgen05.mma, the parts of the rows of r its columns, 64 tokens a step its K: d is
+// read once, in rows as they lie (its tile is an operand whose rows, not its K, are
+// contiguous), and every part has sums of its own.  A CTA takes 256 (or 128)
+// columns and a chunk of the tiles; an adapter whose tokens are in several chunks
+// leaves partial sums there, which one more kernel adds in a fixed order.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
 
+#include "gemm_common.cuh"
 #include "lora.cuh"
 
 namespace fp8hg {
 namespace lora {
 
 namespace {
-
-constexpr int kChunk = 32;           // tokens of a lane's eight rows
 
 // ------------------------------------------------------------ rows of r, prepared
 // A tile's 16 rows of r a CTA.
@@ -75,27 +75,45 @@ __global__ void __launch_bounds__(256) k_lora_prep(const PrepArgs a) {
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) w[p][e] = lo[p] | hi[p] << 16;
     }
-    const int64_t ld = static_cast<int64_t>(a.plan.max_tiles()) * kLoraTile;
+    // as it will stand in shared memory: 64 tokens, a row of 128 bytes for each part and
+    // row of r, its 16-byte pieces exchanged as the tensor core's swizzle has it
+    uint8_t *to = reinterpret_cast<uint8_t *>(a.vt[side]) + (2 * static_cast<int64_t>(blockIdx.x) + m / 64) * (PARTS * RP * 128) +
+                  (r0 + r) * 128 + ((m % 64 / 8) ^ (r & 7)) * 16;
 #pragma unroll
-    for (int p = 0; p < PARTS; ++p)
-        *reinterpret_cast<uint4 *>(a.vt[side] + p * a.plane + (r0 + r) * ld + static_cast<int64_t>(blockIdx.x) * kLoraTile + m) =
-            make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+    for (int p = 0; p < PARTS; ++p) *reinterpret_cast<uint4 *>(to + p * RP * 128) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
 // -------------------------------------------------------------------- outer
-// Sixteen warps: eight times the columns, and the rows of r in two halves.
-constexpr int kThreads = 512;
+constexpr int kStep = 64;            // tokens
+constexpr int kCopyWarps = 4, kSumWarps = 8;
+constexpr int kThreads = (kCopyWarps + kSumWarps + 1) * 32;
+constexpr uint64_t kWaitNs = 2000000000ull;
+// Steps whose products stay in tensor memory before they are added up in FP32: 32
+// sums of 16, each cut off, are off by some 4e-7 of the result.
+constexpr int kSteps = 8;
+
 template <int RP, int PARTS>
 struct Shape {
-    static constexpr int CT = RP <= 64 ? 4 : 2;          // fragments of 16 columns, a warp
-    static constexpr int CL = 2 * CT;                    // neighbouring columns of a lane
-    static constexpr int COLS = 8 * 16 * CT;             // of a CTA
-    static constexpr int J = RP / 16;                    // fragments of 8 rows of r, a warp
-    static constexpr int V = PARTS * RP * kChunk * 2;    // of a step
-    static constexpr int D = kChunk * COLS * 2;
-    static constexpr int STAGES = 4;
-    static constexpr int SMEM = STAGES * (V + D);
+    static constexpr int BLOCKS = RP <= 64 ? 2 : 1;      // of 128 columns
+    static constexpr int COLS = 128 * BLOCKS;            // of a CTA
+    static constexpr int N = PARTS * RP;                 // of a block in tensor memory
+    static constexpr int MMAS = N > 256 ? 2 : 1;
+    static constexpr int A = kStep * COLS * 2, B = N * 128;
+    static constexpr int STAGES = 224 * 1024 / (A + B) < 5 ? 224 * 1024 / (A + B) : 5;
+    static constexpr int BARS = 8 * (2 * STAGES + 3);
+    static constexpr int SMEM = 1024 + STAGES * (A + B) + BARS + 16;
+    static constexpr int TMEM = BLOCKS * N <= 64 ? 64 : BLOCKS * N <= 128 ? 128 : BLOCKS * N <= 256 ? 256 : 512;
+    static constexpr int SUMS = BLOCKS == 2 ? RP : RP / 2;   // rows of r of a thread
 };
+
+// Descriptor of an operand whose rows (here: columns of d) lie next to one another, in
+// blocks of 64 (128 bytes, swizzled) by kStep: a block's groups of eight tokens are
+// 1024 bytes apart, the blocks kStep * 128.
+__device__ __forceinline__ uint64_t desc_columns(uint32_t saddr) {
+    uint64_t d = gemm_common::desc_sw128(saddr);
+    d &= ~(static_cast<uint64_t>(0x3FFF) << 16);
+    return d | static_cast<uint64_t>(kStep * 128 / 16) << 16;
+}
 
 // CL columns from p on (`left` > 0 of them there), zeros behind: the aligned
 // 16-byte pieces that hold them, moved into place.
@@ -127,185 +145,239 @@ __device__ __forceinline__ void load_cols(const uint16_t *p, int left, uint32_t 
     for (int i = 0; i < CL / 2; ++i) w[i] = bytes >= 4u * i + 4u ? v[i] : bytes > 4u * i ? v[i] & 0xFFFFu : 0u;
 }
 
+// Warps: four copy (a token's columns at a time; the first one the rows of r as well),
+// eight add up, one issues the products.
 template <int RP, int PARTS, bool WIDE>
-__global__ void __launch_bounds__(kThreads) k_lora_outer(const OuterArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_lora_outer(const OuterArgs a) {
     using S = Shape<RP, PARTS>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * (static_cast<int64_t>(a.side[0].n) + a.side[1].n));
     const bool second = static_cast<int>(blockIdx.x) >= a.side[0].blocks;
     const OuterSide &o = a.side[second];
     const int n0 = (blockIdx.x - (second ? a.side[0].blocks : 0)) * S::COLS;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
-    const int half = warp >> 3, wcol = warp & 7, col = n0 + wcol * 16 * S::CT + g * S::CL, left = o.n - col;
     const int *tile_first = a.plan.words + a.plan.tile_first(), *order = a.plan.words + a.plan.order();
     const int all = adapter_tiles(a.plan), per = a.tiles(all);
     const int t0 = blockIdx.y * per, t1 = min(all, t0 + per);
     if (t0 >= t1) return;
-    const uint32_t vring = ptx::smem_u32(smem), ring = vring + S::STAGES * S::V;
-    const int64_t ld_vt = static_cast<int64_t>(a.plan.max_tiles()) * kLoraTile;
 
-    // the copies' place, some steps ahead of the products': a tile, 32 tokens of it.
-    // The tile and the tokens of the next copies are asked for a step before them.
-    int ahead = t0, ahead_c = 0, stage_in = 0;
-    Tile from = tile_at(a.plan, t0), then = tile_at(a.plan, min(t0 + 1, t1 - 1));
-    int token[4];
-    auto look_up = [&]() {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int m = ahead_c * kChunk + 8 * t + 4 * half + e;
-            token[e] = ahead < t1 && m < from.count && left > 0 ? order[from.first + m] : -1;
+    const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    const uint32_t sa = base, sb = base + S::STAGES * S::A, bars = sb + S::STAGES * S::B;
+    const uint32_t full = bars, empty = full + 8 * S::STAGES, sum_full = empty + 8 * S::STAGES, sum_empty = sum_full + 8, drain = sum_empty + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (bars + S::BARS - raw));
+    volatile uint32_t *abort_flag = tmem_slot + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            ptx::mbar_init(full + 8 * i, kCopyWarps + 1);
+            ptx::mbar_init(empty + 8 * i, 1);
         }
-    };
-    look_up();
-    // of a lane's eight rows the warp copies four, the warp of the other half the others
-    uint32_t late[4][S::CL / 2];     // rows at odd addresses: from load to store
-    auto load = [&]() {
-        for (int q = tid; q < PARTS * RP * (kChunk / 8); q += kThreads) {
-            const int r = q / (kChunk / 8), m = q % (kChunk / 8) * 8;     // r: part and row
-            ptx::cp_async16(vring + stage_in * S::V + q * 16,
-                            o.vt + (r / RP) * a.plane + (r % RP) * ld_vt + static_cast<int64_t>(ahead) * kLoraTile + ahead_c * kChunk + m, 16);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int have = token[e] >= 0 ? left : 0;
-            const uint16_t *p = have > 0 ? o.d + row_at(token[e], o.ld) + col : o.d;
-            if constexpr (WIDE) {
-                const int n = max(0, min(S::CL, have));
-                const uint32_t to = ring + (((stage_in * 8 + wcol) * 8 + 4 * half + e) * 32 + lane) * (2 * S::CL);
-                if constexpr (S::CL == 8) ptx::cp_async16(to, p, 2 * n);
-                else ptx::cp_async8(to, p, 2 * n);
-            } else if (have > 0) {
-                load_cols<S::CL>(p, have, late[e]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < S::CL / 2; ++i) late[e][i] = 0u;
-            }
-        }
-    };
-    auto store_late = [&](int stage) {
-        if (WIDE) return;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t to = ring + (((stage * 8 + wcol) * 8 + 4 * half + e) * 32 + lane) * (2 * S::CL);
-            if constexpr (S::CL == 8) ptx::st_shared_v4(to, late[e][0], late[e][1], late[e][2], late[e][3]);
-            else ptx::st_shared_v2(to, late[e][0], late[e][1]);
-        }
-    };
-    auto step_on = [&]() {
-        stage_in = stage_in + 1 == S::STAGES ? 0 : stage_in + 1;
-        if (++ahead_c * kChunk >= from.count) {
-            ahead_c = 0;
-            ++ahead;
-            from = then;
-            then = tile_at(a.plan, min(ahead + 1, t1 - 1));
-        }
-        look_up();
-    };
-    for (int s = 0; s < S::STAGES - 1; ++s) {
-        if (ahead < t1) {
-            load();
-            store_late(stage_in);
-            step_on();
-        }
-        ptx::cp_async_commit();
+        ptx::mbar_init(sum_full, 1);
+        ptx::mbar_init(sum_empty, kSumWarps);
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
     }
-
-    float sum[S::CT][S::J][4];
-    auto clear = [&]() {
-#pragma unroll
-        for (int i = 0; i < S::CT; ++i)
-#pragma unroll
-            for (int j = 0; j < S::J; ++j) sum[i][j][0] = sum[i][j][1] = sum[i][j][2] = sum[i][j][3] = 0.0f;
+    if (warp == kCopyWarps + kSumWarps) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), S::TMEM);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, gemm_common::wait_phase(bar, parity, kWaitNs, abort_flag, a.err, 0x40u + warp));
     };
-    clear();
-    int stage = 0;
-    for (int i = t0; i < t1; ++i) {
-        const Tile tile = tile_at(a.plan, i);
-        const int begin = tile_first[tile.adapter], end = tile_first[tile.adapter + 1];
-        for (int c = 0; c * kChunk < tile.count; ++c) {
-            ptx::cp_async_wait<S::STAGES - 2>();
-            __syncthreads();
-            const int filled = ahead < t1 ? stage_in : -1;
-            if (filled >= 0) {
-                load();
-                step_on();
+
+    if (warp < kCopyWarps) {
+        // a token's row: 16 bytes a lane, one row (two with one block) at a time
+        constexpr int ROWS = 2 / S::BLOCKS, EACH = kStep / kCopyWarps / ROWS;
+        const int piece = lane % (32 / ROWS), sub = lane / (32 / ROWS), left = o.n - n0 - piece * 8;
+        const int bytes = max(0, min(16, 2 * left));
+        const uint32_t to0 = sa + piece / 8 * (kStep * 128);
+        // this step's tokens, a lane each; the next step's are asked for meanwhile
+        auto look_up = [&](const Tile &tile, int h) {
+            const int m = h * kStep + warp * (kStep / kCopyWarps) + lane;
+            return lane < kStep / kCopyWarps && m < tile.count ? order[tile.first + m] : -1;
+        };
+        Tile tile = tile_at(a.plan, t0), next = tile_at(a.plan, min(t0 + 1, t1 - 1));
+        int token = look_up(tile, 0), stage = 0, lag_stage = 0, it = 0, h = 0;
+        uint32_t parity = 1;
+        bool ok = true;
+        constexpr int LAG = S::STAGES - 2;
+        for (int t = t0; t < t1 && ok; ++it) {
+            const int now = token, t_now = t, h_now = h;
+            h += 1;
+            if (h * kStep >= tile.count) {
+                h = 0;
+                ++t;
+                tile = next;
+                next = tile_at(a.plan, min(t + 1, t1 - 1));
+            }
+            token = look_up(tile, h);
+            ok = wait(empty + 8 * stage, parity);
+            if (!ok) break;
+            if (warp == 0 && lane == 0) {
+                ptx::mbar_arrive_expect_tx(full + 8 * stage, S::B);
+                ptx::bulk_load(sb + stage * S::B, reinterpret_cast<const uint8_t *>(o.vt) + (2 * static_cast<int64_t>(t_now) + h_now) * S::B, S::B,
+                               full + 8 * stage);
+            }
+            const uint32_t to = to0 + stage * S::A;
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) {
+                    const int i = e * ROWS + sub, m = warp * (kStep / kCopyWarps) + i, tok = __shfl_sync(0xFFFFFFFFu, now, i);
+                    const bool in = tok >= 0 && bytes > 0;
+                    ptx::cp_async16(to + m * 128 + ((piece ^ m) & 7) * 16, in ? o.d + row_at(tok, o.ld) + n0 + piece * 8 : o.d, in ? bytes : 0);
+                }
+            } else {
+                // eight rows' loads in flight
+#pragma unroll
+                for (int e0 = 0; e0 < EACH; e0 += 8) {
+                    uint32_t w[8][4];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int tok = __shfl_sync(0xFFFFFFFFu, now, (e0 + e) * ROWS + sub);
+                        w[e][0] = w[e][1] = w[e][2] = w[e][3] = 0u;
+                        if (tok >= 0 && left > 0) load_cols<8>(o.d + row_at(tok, o.ld) + n0 + piece * 8, left, w[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int m = warp * (kStep / kCopyWarps) + (e0 + e) * ROWS + sub;
+                        ptx::st_shared_v4(to + m * 128 + ((piece ^ m) & 7) * 16, w[e][0], w[e][1], w[e][2], w[e][3]);
+                    }
+                }
             }
             ptx::cp_async_commit();
-            uint32_t d[8][S::CL / 2];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t p = ring + (((stage * 8 + wcol) * 8 + e) * 32 + lane) * (2 * S::CL);
-                if constexpr (S::CL == 8) ptx::ld_shared_v4(p, d[e][0], d[e][1], d[e][2], d[e][3]);
-                else ptx::ld_shared_v2(p, d[e][0], d[e][1]);
+            if (it >= LAG) {
+                ptx::cp_async_wait<LAG>();
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(full + 8 * lag_stage);
+                lag_stage = lag_stage + 1 == S::STAGES ? 0 : lag_stage + 1;
             }
-            // pairs of tokens: [step of 16][fragment][its four words]
-            uint32_t f[2][S::CT][4];
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int k = 0; k < S::CT; ++k) {
-                    f[q][k][0] = __byte_perm(d[4 * q][k], d[4 * q + 1][k], 0x5410);
-                    f[q][k][1] = __byte_perm(d[4 * q][k], d[4 * q + 1][k], 0x7632);
-                    f[q][k][2] = __byte_perm(d[4 * q + 2][k], d[4 * q + 3][k], 0x5410);
-                    f[q][k][3] = __byte_perm(d[4 * q + 2][k], d[4 * q + 3][k], 0x7632);
-                }
-            // sums of 32 tokens' products, then to registers
-#pragma unroll
-            for (int j = 0; j < S::J; ++j) {
-                uint32_t b[PARTS][4];
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-                    ptx::ld_shared_v4(vring + stage * S::V + (p * RP + (half * S::J + j) * 8 + g) * (2 * kChunk) + 16 * t, b[p][0], b[p][1], b[p][2], b[p][3]);
-                float acc[S::CT][4];
-#pragma unroll
-                for (int k = 0; k < S::CT; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int k = 0; k < S::CT; ++k) ptx::mma_bf16(acc[k], f[q][k], b[p][2 * q], b[p][2 * q + 1]);
-#pragma unroll
-                for (int k = 0; k < S::CT; ++k)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) sum[k][j][q] += acc[k][q];
-            }
-            if (filled >= 0) store_late(filled);
-            stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+            if (++stage == S::STAGES) stage = 0, parity ^= 1;
         }
-        if (i + 1 < t1 && i + 1 < end) continue;
-        // the adapter's last tile, here or at all
-        const bool whole = begin >= t0 && end <= t1;
-        float *part = o.ws + (2 * static_cast<int64_t>(blockIdx.y) + (begin < t0 ? 0 : 1)) * o.n * RP;
+        ptx::cp_async_wait<0>();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        for (int i = 0; i < min(it, LAG) && ok; ++i) {
+            if (lane == 0) ptx::mbar_arrive(full + 8 * lag_stage);
+            lag_stage = lag_stage + 1 == S::STAGES ? 0 : lag_stage + 1;
+        }
+        // the last copies of the rows of r land before the CTA ends
+        if (warp == 0) {
+            for (int i = max(0, it - S::STAGES); i < it; ++i)
+                gemm_common::wait_phase(full + 8 * (i % S::STAGES), (i / S::STAGES) & 1, ok ? kWaitNs : 2000000ull, abort_flag, a.err, 0x40u, false);
+        }
+    } else if (warp < kCopyWarps + kSumWarps) {
+        const int q = warp & 3, half = (warp - kCopyWarps) >> 2;
+        const int c = n0 + (S::BLOCKS == 2 ? half * 128 : 0) + q * 32 + lane, r0 = S::BLOCKS == 2 ? 0 : half * S::SUMS;
+        const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16) + (S::BLOCKS == 2 ? half * S::N : r0);
+        float sum[S::SUMS];
 #pragma unroll
-        for (int k = 0; k < S::CT; ++k)
+        for (int i = 0; i < S::SUMS; ++i) sum[i] = 0.0f;
+        uint32_t parity = 0;
+        bool ok = true;
+        int steps = 0;
+        for (int t = t0; t < t1 && ok; ++t) {
+            const Tile tile = tile_at(a.plan, t);
+            const int begin = tile_first[tile.adapter], end = tile_first[tile.adapter + 1];
+            steps += (tile.count + kStep - 1) / kStep;
+            const bool last = t + 1 == t1 || t + 1 == end;
+            if (!last && steps + 2 <= kSteps) continue;
+            steps = 0;
+            ok = wait(sum_full, parity);
+            if (!ok) break;
+            parity ^= 1;
+            ptx::tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < S::J; ++j) {
-                const int r = (half * S::J + j) * 8 + 2 * t;
+            for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c = col + 2 * k + e;
-                    if (c >= o.n) continue;
-                    const float v0 = sum[k][j][2 * e], v1 = sum[k][j][2 * e + 1];
-                    if (!whole) {
-                        *reinterpret_cast<float2 *>(part + static_cast<int64_t>(c) * RP + r) = make_float2(v0, v1);
-                        continue;
-                    }
-                    const int64_t to = tile.adapter * o.stride_g + c * o.stride_n + r * o.stride_r;
+                for (int i = 0; i < S::SUMS; i += 16) {
+                    uint32_t v[16];
+                    ptx::tmem_ld_32x32b_x16(from + p * RP + i, v);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[i + e] += __uint_as_float(v[e]);
+                }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sum_empty);
+            if (!last) continue;
+            // the adapter's last tile, here or at all
+            if (c < o.n) {
+                if (begin >= t0 && end <= t1) {
+                    const int64_t to = tile.adapter * o.stride_g + c * o.stride_n + r0 * o.stride_r;
+                    const int have = a.lw.r - r0;
                     if (a.f32) {
                         float *p = static_cast<float *>(o.out) + to;
-                        if (r < a.lw.r) p[0] = v0;
-                        if (r + 1 < a.lw.r) p[o.stride_r] = v1;
+#pragma unroll
+                        for (int i = 0; i < S::SUMS; ++i, p += o.stride_r)
+                            if (i < have) *p = sum[i];
                     } else {
                         uint16_t *p = static_cast<uint16_t *>(o.out) + to;
-                        if (r < a.lw.r) p[0] = static_cast<uint16_t>(ptx::cvt_bf16x2(v0, 0.0f));
-                        if (r + 1 < a.lw.r) p[o.stride_r] = static_cast<uint16_t>(ptx::cvt_bf16x2(v1, 0.0f));
+#pragma unroll
+                        for (int i = 0; i < S::SUMS; ++i, p += o.stride_r)
+                            if (i < have) *p = static_cast<uint16_t>(ptx::cvt_bf16x2(sum[i], 0.0f));
                     }
+                } else {
+                    float *part = o.ws + ((2 * static_cast<int64_t>(blockIdx.y) + (begin < t0 ? 0 : 1)) * o.n + c) * RP + r0;
+#pragma unroll
+                    for (int i = 0; i < S::SUMS; i += 4)
+                        *reinterpret_cast<float4 *>(part + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
                 }
             }
-        clear();
+#pragma unroll
+            for (int i = 0; i < S::SUMS; ++i) sum[i] = 0.0f;
+        }
+    } else if (warp == kCopyWarps + kSumWarps) {
+        // sums FP32, operands BF16, d with its columns (not its tokens) next to one another
+        constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (static_cast<uint32_t>(S::N / S::MMAS / 8) << 17) | (8u << 24);
+        int stage = 0, steps = 0, sets = 0;
+        uint32_t parity = 0;
+        bool ok = true;
+        for (int t = t0; t < t1 && ok; ++t) {
+            const Tile tile = tile_at(a.plan, t);
+            const int end = tile_first[tile.adapter + 1], mine = (tile.count + kStep - 1) / kStep;
+            for (int h = 0; h < mine; ++h, ++steps) {
+                if (steps == 0) {
+                    ok = wait(sum_empty, (sets & 1) ^ 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                }
+                ok = wait(full + 8 * stage, parity);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t ad = desc_columns(sa + stage * S::A), bd = gemm_common::desc_sw128(sb + stage * S::B);
+#pragma unroll
+                    for (int k = 0; k < kStep / 16; ++k)
+#pragma unroll
+                        for (int b = 0; b < S::BLOCKS; ++b)
+#pragma unroll
+                            for (int i = 0; i < S::MMAS; ++i)
+                                ptx::tc_mma_bf16(tmem + b * S::N + i * (S::N / S::MMAS), ad + b * (2 * kStep * 128 / 16) + k * (16 * 128 / 16),
+                                                 bd + i * (S::N / S::MMAS * 128 / 16) + k * 2, idesc, steps > 0 || k > 0);
+                    ptx::tc_commit(empty + 8 * stage);
+                }
+                __syncwarp();
+                if (++stage == S::STAGES) stage = 0, parity ^= 1;
+            }
+            if (ok && (t + 1 == t1 || t + 1 == end || steps + 2 > kSteps)) {
+                if (lane == 0) ptx::tc_commit(sum_full);
+                __syncwarp();
+                steps = 0;
+                ++sets;
+            }
+        }
+        if (lane == 0) ptx::tc_commit(drain);
+        __syncwarp();
+        gemm_common::wait_phase(drain, 0, kWaitNs, abort_flag, a.err, 0x40u + warp, false);
     }
-    ptx::cp_async_wait<0>();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kCopyWarps + kSumWarps) ptx::tmem_dealloc(tmem, S::TMEM);
 }
 
 // The adapters of several chunks, and zeros for those without a token: 32 by 32

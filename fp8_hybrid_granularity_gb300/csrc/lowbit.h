@@ -99,6 +99,8 @@ cudaError_t launch_swiglu_bwd_q(const uint16_t *dh, uint32_t ld_dh, const Swiglu
 
 // SMs of the current device (looked up once per device; any thread).
 int sm_count();
+// The current device's error word, looked up once per device (null on failure).
+unsigned int *error_word();
 
 // Launches a kernel that begins with ptx::grid_begin() or grid_wait(), under the
 // end of the stream's last kernel where that allows it: 1 to 2 us less from one

@@ -57,18 +57,8 @@ int check_opts(const fp8hg_gemm_opts *opts, int max_inject) {
     return opts->tile == 0 ? FP8HG_OK : FP8HG_ERR_UNSUPPORTED;
 }
 
-// The current device's error word; its address is looked up once per device.
-unsigned int *error_word() {
-    static std::atomic<unsigned int *> words[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fp8hg::device_error_word();
-    unsigned int *w = words[dev].load(std::memory_order_relaxed);
-    if (!w) words[dev].store(w = fp8hg::device_error_word(), std::memory_order_relaxed);
-    return w;
-}
-
 int run_gemm(fp8hg::Fp4GemmArgs &g, const fp8hg_gemm_opts *opts, void *stream) {
-    unsigned int *err = error_word();
+    unsigned int *err = fp8hg::error_word();
     if (!err) return FP8HG_ERR_CUDA;
     g.wait_limit_ns = opts && opts->wait_limit_ns ? opts->wait_limit_ns : kDefaultWaitNs;
     g.inject_fault = opts ? opts->inject_fault : 0;
@@ -118,6 +108,15 @@ fp8hg::SwigluCkpt ckpt(const fp8hg_swiglu_ckpt *c) {
 }
 
 }  // namespace
+
+unsigned int *fp8hg::error_word() {
+    static std::atomic<unsigned int *> words[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fp8hg::device_error_word();
+    unsigned int *w = words[dev].load(std::memory_order_relaxed);
+    if (!w) words[dev].store(w = fp8hg::device_error_word(), std::memory_order_relaxed);
+    return w;
+}
 
 int fp8hg::sm_count() {
     static std::atomic<int> counts[64];
@@ -326,7 +325,7 @@ int fp8_swiglu_ckpt_bwd_q(const uint16_t *dh, int64_t ld_dh, const fp8hg_swiglu_
     if (g->ld_q < c->cols || g->ld_s < c->cols / 128 || g->ld_qt < c->rows || g->ld_st < c->rows / 128)
         return FP8HG_ERR_INVALID_ARG;
     if (g->ld_q > kMaxLd || g->ld_s > kMaxLd || g->ld_qt > kMaxLd || g->ld_st > kMaxLd) return FP8HG_ERR_SHAPE;
-    o.err = error_word();
+    o.err = fp8hg::error_word();
     if (!o.err) return FP8HG_ERR_CUDA;
     return status_from_cuda(fp8hg::launch_swiglu_bwd_q(dh, u32(ld_dh), ckpt(c), o,
                                                        static_cast<cudaStream_t>(stream)));
