@@ -100,7 +100,7 @@ cudaError_t launch_lora_plan(const int *ids, const LoraPlan &p, int *words, cuda
 
 size_t lora_ws_bytes(int64_t tokens, int adapters, int r, int64_t k) {
     const int rp = lora::padded(r);
-    return static_cast<size_t>(lora::most_splits({nullptr, static_cast<int>(tokens), adapters}, static_cast<int>(k), rp)) * tokens * rp *
+    return static_cast<size_t>(lora::most_splits({nullptr, static_cast<int>(tokens), adapters}, static_cast<int>(k))) * tokens * rp *
            sizeof(float);
 }
 
@@ -115,12 +115,21 @@ cudaError_t launch_lora_add(const LoraArgs &a, cudaStream_t stream) {
     s.lw = a.w;
     s.k = a.w.k;
     s.out = a.ws;
-    const cudaError_t e = lora::launch_shrink(s, false, stream);
+    s.err = error_word();
+    if (s.err == nullptr) return cudaErrorUnknown;
+    cudaError_t e = lora::launch_shrink(s, false, stream);
     if (e != cudaSuccess) return e;
+    // Each CTA of a tile would add up its partial sums: left to them where there are
+    // few tokens, one kernel more otherwise.
+    const bool apart = a.plan.tokens > kLoraTile && (a.v != nullptr || lora::most_splits(a.plan, a.w.k) > 1);
+    if (apart) {
+        e = lora::launch_sum({a.plan, a.w, a.ws, a.w.k, a.v, a.ld_v}, stream);
+        if (e != cudaSuccess) return e;
+    }
     lora::ExpandArgs x{};
     x.plan = a.plan;
     x.rows = a.ws;
-    x.long_side = a.w.k;
+    x.long_side = apart ? 0 : a.w.k;
     x.w = a.w.b;
     x.stride_w = a.w.stride_b;
     x.ld_w = a.w.ld_b;
@@ -130,7 +139,7 @@ cudaError_t launch_lora_add(const LoraArgs &a, cudaStream_t stream) {
     x.y = a.y;
     x.ld_base = a.ld_base;
     x.ld_y = a.ld_y;
-    x.v_out = a.v;
+    x.v_out = apart ? nullptr : a.v;
     x.ld_v = a.ld_v;
     return lora::launch_expand(x, a.y_f32, stream);
 }
@@ -179,6 +188,8 @@ cudaError_t launch_lora_add_bwd(const LoraBwdArgs &a, cudaStream_t stream) {
         s.lw = a.w;
         s.k = a.w.n;
         s.out = partial;
+        s.err = error_word();
+        if (s.err == nullptr) return cudaErrorUnknown;
         e = lora::launch_shrink(s, true, stream);
         if (e != cudaSuccess) return e;
     }

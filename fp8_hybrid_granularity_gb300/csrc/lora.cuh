@@ -26,6 +26,7 @@
 #include <cstdint>
 
 #include "adapt.h"
+#include "gemm_common.cuh"
 #include "norm.cuh"
 #include "ptx.cuh"
 
@@ -33,6 +34,7 @@ namespace fp8hg {
 namespace lora {
 
 constexpr int kSms = 152;
+constexpr uint64_t kWaitNs = 2000000000ull;      // of a warp for another one of its CTA
 
 // A tile of the plan.
 struct Tile {
@@ -44,6 +46,14 @@ __device__ __forceinline__ Tile tile_at(const LoraPlan &p, int i) {
 }
 __device__ __forceinline__ int rank_of(const LoraWeights &w, int g) {
     return w.ranks == nullptr ? w.r : max(0, min(w.r, w.ranks[g]));
+}
+
+// Descriptor of an operand whose rows, not its K, lie next to one another: blocks of
+// 64 rows (128 bytes, swizzled) by `ks` of K; a block's groups of eight K are 1024
+// bytes apart, the blocks ks * 128.
+__device__ __forceinline__ uint64_t desc_columns(uint32_t saddr, int ks) {
+    const uint64_t d = gemm_common::desc_sw128(saddr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
+    return d | static_cast<uint64_t>(ks * 128 / 16) << 16;
 }
 
 // Eight values from p on, the first `left` of them (zeros behind), to 16 bytes
@@ -60,6 +70,35 @@ __device__ __forceinline__ void copy8(uint32_t dst, const uint16_t *p, int left)
             if (i < n) w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
         ptx::st_shared_v4(dst, w[0], w[1], w[2], w[3]);
     }
+}
+
+// Eight values from p on, the first `left` > 0 of them (zeros behind): the aligned
+// 16-byte pieces that hold them, moved into place.
+__device__ __forceinline__ void load8(const uint16_t *p, int left, uint32_t (&w)[4]) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint32_t s = static_cast<uint32_t>(at & 15), bytes = 2u * static_cast<uint32_t>(min(8, left));
+    const uint4 *q = reinterpret_cast<const uint4 *>(at & ~static_cast<uintptr_t>(15));
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (s + bytes > 16u * i) u = ptx::ld_v4(q + i);
+        v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+    }
+    if (s & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) v[i] = v[i + 2];
+    }
+    if (s & 4) {
+#pragma unroll
+        for (int i = 0; i < 7; ++i) v[i] = v[i + 1];
+    }
+    if (s & 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bytes >= 4u * i + 4u ? v[i] : bytes > 4u * i ? v[i] & 0xFFFFu : 0u;
 }
 
 // v as the sum of PARTS BF16 values: 16 bits of it with two, all 24 with three.
@@ -117,19 +156,18 @@ struct TileCopy {
 // least 128 columns each.  On the device from the plan, on the host an upper bound.
 constexpr int kShrinkCols = 64;
 constexpr int kMaxSplits = 16;
-__host__ __device__ constexpr int shrink_slots(int rp) { return kSms * (rp <= 32 ? 3 : rp <= 64 ? 2 : 1); }
-__host__ __device__ inline int shrink_splits(int64_t tiles, int k, int rp) {
+__host__ __device__ inline int shrink_splits(int64_t tiles, int k) {
     const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
-    int64_t n = shrink_slots(rp) / (tiles < 1 ? 1 : tiles);
+    int64_t n = kSms / (tiles < 1 ? 1 : tiles);
     n = n < (steps + 1) / 2 ? n : (steps + 1) / 2;
     n = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
     const int64_t per = (steps + n - 1) / n;
     return static_cast<int>((steps + per - 1) / per);
 }
 // More than any number of tiles with `tokens` tokens gives.
-inline int most_splits(const LoraPlan &p, int k, int rp) {
+inline int most_splits(const LoraPlan &p, int k) {
     const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
-    const int64_t n = shrink_slots(rp) / ((p.tokens + kLoraTile - 1) / kLoraTile);
+    const int64_t n = kSms / ((p.tokens + kLoraTile - 1) / kLoraTile);
     const int64_t most = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
     return static_cast<int>(most < steps ? most : steps);
 }
@@ -145,8 +183,19 @@ struct ShrinkArgs {
     LoraWeights lw;                  // ranks
     int k;                           // the long side
     float *out;                      // [splits][tokens in the plan's order][padded(r)]
+    unsigned int *err;               // the device's error word
 };
 cudaError_t launch_shrink(const ShrinkArgs &a, bool trans, cudaStream_t stream);
+
+struct SumArgs {
+    LoraPlan plan;
+    LoraWeights lw;                  // ranks, r
+    float *rows;                     // [splits][tokens in the plan's order][padded(r)]
+    int long_side;
+    float *v_out;                    // the sums by token, for the backward pass, or null
+    uint32_t ld_v;
+};
+cudaError_t launch_sum(const SumArgs &a, cudaStream_t stream);
 
 struct ExpandArgs {
     LoraPlan plan;

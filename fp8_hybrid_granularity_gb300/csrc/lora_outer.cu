@@ -14,7 +14,6 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "gemm_common.cuh"
 #include "lora.cuh"
 
 namespace fp8hg {
@@ -33,7 +32,7 @@ __global__ void __launch_bounds__(256) k_lora_prep(const PrepArgs a) {
     const Tile tile = tile_at(a.plan, blockIdx.x);
     const int rank = rank_of(a.lw, tile.adapter), tid = threadIdx.x, r0 = blockIdx.z * 16;
     const float scale = a.lw.scale == nullptr ? 1.0f : a.lw.scale[tile.adapter];
-    const int splits = side == 0 ? 0 : shrink_splits(tiles, a.long_side, RP);
+    const int splits = side == 0 ? 0 : shrink_splits(tiles, a.long_side);
 #pragma unroll
     for (int h = 0; h < kLoraTile * 4 / 256; ++h) {
         const int m = (h * 256 + tid) / 4, c = tid % 4 * 4, r = r0 + c;
@@ -87,7 +86,6 @@ __global__ void __launch_bounds__(256) k_lora_prep(const PrepArgs a) {
 constexpr int kStep = 64;            // tokens
 constexpr int kCopyWarps = 4, kSumWarps = 8;
 constexpr int kThreads = (kCopyWarps + kSumWarps + 1) * 32;
-constexpr uint64_t kWaitNs = 2000000000ull;
 // Steps whose products stay in tensor memory before they are added up in FP32: 32
 // sums of 16, each cut off, are off by some 4e-7 of the result.
 constexpr int kSteps = 8;
@@ -105,45 +103,6 @@ struct Shape {
     static constexpr int TMEM = BLOCKS * N <= 64 ? 64 : BLOCKS * N <= 128 ? 128 : BLOCKS * N <= 256 ? 256 : 512;
     static constexpr int SUMS = BLOCKS == 2 ? RP : RP / 2;   // rows of r of a thread
 };
-
-// Descriptor of an operand whose rows (here: columns of d) lie next to one another, in
-// blocks of 64 (128 bytes, swizzled) by kStep: a block's groups of eight tokens are
-// 1024 bytes apart, the blocks kStep * 128.
-__device__ __forceinline__ uint64_t desc_columns(uint32_t saddr) {
-    uint64_t d = gemm_common::desc_sw128(saddr);
-    d &= ~(static_cast<uint64_t>(0x3FFF) << 16);
-    return d | static_cast<uint64_t>(kStep * 128 / 16) << 16;
-}
-
-// CL columns from p on (`left` > 0 of them there), zeros behind: the aligned
-// 16-byte pieces that hold them, moved into place.
-template <int CL>
-__device__ __forceinline__ void load_cols(const uint16_t *p, int left, uint32_t (&w)[CL / 2]) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const uint32_t s = static_cast<uint32_t>(at & 15), bytes = 2u * static_cast<uint32_t>(min(CL, left));
-    const uint4 *q = reinterpret_cast<const uint4 *>(at & ~static_cast<uintptr_t>(15));
-    uint32_t v[8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (s + bytes > 16u * i) u = ptx::ld_v4(q + i);
-        v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
-    }
-    if (s & 8) {
-#pragma unroll
-        for (int i = 0; i < 6; ++i) v[i] = v[i + 2];
-    }
-    if (s & 4) {
-#pragma unroll
-        for (int i = 0; i < 7; ++i) v[i] = v[i + 1];
-    }
-    if (s & 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 16);
-    }
-#pragma unroll
-    for (int i = 0; i < CL / 2; ++i) w[i] = bytes >= 4u * i + 4u ? v[i] : bytes > 4u * i ? v[i] & 0xFFFFu : 0u;
-}
 
 // Warps: four copy (a token's columns at a time; the first one the rows of r as well),
 // eight add up, one issues the products.
@@ -204,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(const OuterArgs a) {
         int token = look_up(tile, 0), stage = 0, lag_stage = 0, it = 0, h = 0;
         uint32_t parity = 1;
         bool ok = true;
-        constexpr int LAG = S::STAGES - 2;
+        constexpr int LAG = WIDE ? S::STAGES - 2 : 0;
         for (int t = t0; t < t1 && ok; ++it) {
             const int now = token, t_now = t, h_now = h;
             h += 1;
@@ -239,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(const OuterArgs a) {
                     for (int e = 0; e < 8; ++e) {
                         const int tok = __shfl_sync(0xFFFFFFFFu, now, (e0 + e) * ROWS + sub);
                         w[e][0] = w[e][1] = w[e][2] = w[e][3] = 0u;
-                        if (tok >= 0 && left > 0) load_cols<8>(o.d + row_at(tok, o.ld) + n0 + piece * 8, left, w[e]);
+                        if (tok >= 0 && left > 0) load8(o.d + row_at(tok, o.ld) + n0 + piece * 8, left, w[e]);
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -350,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(const OuterArgs a) {
                 if (!ok) break;
                 ptx::tc_fence_after();
                 if (lane == 0) {
-                    const uint64_t ad = desc_columns(sa + stage * S::A), bd = gemm_common::desc_sw128(sb + stage * S::B);
+                    const uint64_t ad = desc_columns(sa + stage * S::A, kStep), bd = gemm_common::desc_sw128(sb + stage * S::B);
 #pragma unroll
                     for (int k = 0; k < kStep / 16; ++k)
 #pragma unroll

@@ -1,8 +1,13 @@
 // Adapters: rows of r from rows of the long side k (or n), out[t] = x[t] W_g^T.
 //
-// A CTA takes a tile of up to 128 tokens, 16 a warp, and a part of the long side
-// (partial sums in FP32; the kernels behind add them in a fixed order), 64
-// columns a step.  W's tile of a step is shared by the warps.
+// A CTA takes a tile of up to 128 tokens, the rows of a tcgen05.mma, and a part of the
+// long side (partial sums in FP32; the kernels behind add them in a fixed order), 64
+// columns a step; the rows of r are its columns.  W's tile is an operand with its K
+// (A_g) or its rows (B_g, in the backward pass) next to one another.  Steps take
+// turns at the sums in tensor memory, 512 columns of it, so that a sum is cut off
+// only 4 times in as many steps as there are sums; they are added at the end.  Rows
+// past a tile's tokens, and past an adapter's rank, hold anything: they meet no
+// other row's sums, and nobody reads theirs.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -15,171 +20,195 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = kLoraTile / 16 * 32;
 constexpr int kCols = kShrinkCols;
+constexpr int kCopyWarps = 4;        // these read the sums at the end: a token a lane
+constexpr int kThreads = (kCopyWarps + 1) * 32;
 
 template <int RP, bool TRANS>
 struct Shape {
-    static constexpr int STAGES = RP <= 32 ? 3 : RP <= 64 ? 4 : 6;
-    static constexpr int CTAS = shrink_slots(RP) / kSms;
-    static constexpr int ROW = TRANS ? 2 * RP + 16 : 2 * kCols + 16;
-    // 32 bytes more after every 16 rows of the transposed form: its fragments
-    // take every sixteenth row
-    static constexpr int W = TRANS ? kCols * ROW + kCols / 16 * 32 : RP * ROW;
-    static constexpr int X = kLoraTile * kCols * 2;
-    static constexpr int SMEM = STAGES * (W + X);
+    // transposed: whole rows of 128 bytes, so 64 rows of r at least
+    static constexpr int N = TRANS && RP < 64 ? 64 : RP;
+    static constexpr int X = kLoraTile * 128, W = TRANS ? (N / 64) * kCols * 128 : N * 128;
+    static constexpr int STAGES = 216 * 1024 / (X + W) < 8 ? 216 * 1024 / (X + W) : 8;
+    static constexpr int SUMS = 512 / N < 8 ? 512 / N : 8;
+    static constexpr int TMEM = SUMS * N < 128 ? 128 : SUMS * N;
+    static constexpr int BARS = 8 * (2 * STAGES + 1);
+    static constexpr int SMEM = 1024 + STAGES * (X + W) + BARS + 16;
+    // pieces of 16 bytes of W's tile, a thread
+    static constexpr int P = TRANS ? RP / 8 : 8, ROWS = TRANS ? kCols : RP, PIECES = ROWS * P / (kCopyWarps * 32);
 };
 
 template <int RP, bool TRANS, bool WIDE, bool WAL>
-__global__ void __launch_bounds__(kThreads, Shape<RP, TRANS>::CTAS) k_lora_shrink(const ShrinkArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(const ShrinkArgs a) {
     using S = Shape<RP, TRANS>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * a.k);
     const Tile tile = tile_at(a.plan, blockIdx.x);      // its place is there, if it is a tile or not
-    const int tiles = adapter_tiles(a.plan);
-    const int splits = shrink_splits(tiles, a.k, RP);
+    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(tiles, a.k);
     if (static_cast<int>(blockIdx.x) >= tiles || static_cast<int>(blockIdx.y) >= splits) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
-    const int rank = rank_of(a.lw, tile.adapter);
-    const uint16_t *w = a.w + tile.adapter * a.stride_w;
-    const uint32_t ring = ptx::smem_u32(smem), base = ring + S::STAGES * S::X;
     const int all = (a.k + kCols - 1) / kCols, per = (all + splits - 1) / splits;
     const int first = blockIdx.y * per, steps = min(all - first, per);
 
-    // the rows that the lane copies: every fourth of the warp's (those it reads, at odd addresses)
-    const uint16_t *row[4];
-    bool have[4];
-#pragma unroll
-    for (int i = 0; i < (WIDE ? 4 : 2); ++i) {
-        const int m = warp * 16 + (WIDE ? i * 4 + lane / 8 : i * 8 + g);
-        have[i] = m < tile.count;
-        row[i] = a.x;
-        if (have[i])
-            row[i] += row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_x) + (WIDE ? lane % 8 * 8 : 16 * t) + first * kCols;
+    const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    const uint32_t sx = base, sw = base + S::STAGES * S::X, full = sw + S::STAGES * S::W;
+    const uint32_t empty = full + 8 * S::STAGES, done = empty + 8 * S::STAGES;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (full + S::BARS - raw));
+    volatile uint32_t *abort_flag = tmem_slot + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            ptx::mbar_init(full + 8 * i, kCopyWarps);
+            ptx::mbar_init(empty + 8 * i, 1);
+        }
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
     }
-    const bool active = warp * 16 < tile.count;
-    const int64_t k0 = static_cast<int64_t>(first) * kCols;
-    TileCopy<TRANS ? kCols : RP, TRANS ? RP : kCols, S::ROW, TRANS, WAL> wc(w + (TRANS ? k0 * a.ld_w : k0), a.ld_w, TRANS ? kCols : rank,
-                                                                             TRANS ? rank : kCols);
-    const int64_t wstep = TRANS ? static_cast<int64_t>(kCols) * a.ld_w : kCols;
-    int in_stage = 0, left = a.k - first * kCols;      // of the next copies
-    uint32_t late[2][8];     // rows at odd addresses: from load to store
-    auto load = [&]() {
-        wc.copy(base + in_stage * S::W, a.w, TRANS ? left : RP, TRANS ? RP : left, wstep);
-        if (active) {
+    if (warp == kCopyWarps) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), S::TMEM);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, gemm_common::wait_phase(bar, parity, kWaitNs, abort_flag, a.err, 0x20u + warp));
+    };
+
+    if (warp < kCopyWarps) {
+        // rows of x: eight lanes each, 32 of them a warp
+        const int piece = lane % 8, m0 = warp * 32 + lane / 8;
+        const int64_t k0 = static_cast<int64_t>(first) * kCols;
+        const uint16_t *row[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int m = m0 + 4 * e;
+            row[e] = m < tile.count ? a.x + row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_x) + k0 + piece * 8 : nullptr;
+        }
+        // pieces of W: rows of r, or of the long side
+        const int rank = rank_of(a.lw, tile.adapter), tid = threadIdx.x, wc = tid % S::P * 8;
+        const uint16_t *w = a.w + tile.adapter * a.stride_w + (TRANS ? k0 * a.ld_w : k0) + wc;
+        const uint16_t *wrow[S::PIECES];
+        uint32_t wto[S::PIECES];
+#pragma unroll
+        for (int i = 0; i < S::PIECES; ++i) {
+            const int r = tid / S::P + i * (kCopyWarps * 32 / S::P);
+            wrow[i] = w + row_at(r, a.ld_w);
+            wto[i] = sw + (TRANS ? wc / 64 * (kCols * 128) : 0) + r * 128 + ((wc / 8 % 8) ^ (r & 7)) * 16;
+        }
+        const int64_t wstep = TRANS ? static_cast<int64_t>(kCols) * a.ld_w : kCols;
+        int left = a.k - first * kCols, stage = 0, lag_stage = 0;
+        uint32_t parity = 1;
+        bool ok = true;
+        int it = 0;
+        constexpr int LAG = WIDE && WAL ? S::STAGES - 2 : 0;
+        for (; it < steps; ++it, left -= kCols) {
+            ok = wait(empty + 8 * stage, parity);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < S::PIECES; ++i) {
+                const int r = tid / S::P + i * (kCopyWarps * 32 / S::P);
+                // of a row past the end: zeros along the long side, nothing past the rank
+                const int have = TRANS ? (r < left ? rank - wc : 0) : left - wc;
+                if (TRANS ? wc < rank : r < rank) copy8<WAL>(wto[i] + stage * S::W, have > 0 ? wrow[i] : a.w, have);
+                wrow[i] += wstep;
+            }
+            const uint32_t to = sx + stage * S::X + m0 * 128;
+            const int n = left - piece * 8;
             if constexpr (WIDE) {
-                const int n = max(0, min(16, 2 * (left - lane % 8 * 8)));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ptx::cp_async16(ring + in_stage * S::X + slot<8>(i * 4 + lane / 8, lane % 8), have[i] && n > 0 ? row[i] : a.x, have[i] ? n : 0);
-                    row[i] += kCols;
+                for (int e = 0; e < 8; ++e) {
+                    if (row[e] != nullptr) {
+                        ptx::cp_async16(to + e * 512 + ((piece ^ (m0 + 4 * e)) & 7) * 16, n > 0 ? row[e] : a.x, max(0, min(16, 2 * n)));
+                        row[e] += kCols;
+                    }
                 }
             } else {
+                uint32_t v[8][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int n = have[i] ? left - 16 * t : 0;
-                    if (n > 0) {
-                        ragged::load16<false>(row[i], n, late[i]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) late[i][j] = 0u;
+                for (int e = 0; e < 8; ++e) {
+                    v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0u;
+                    if (row[e] != nullptr) {
+                        if (n > 0) load8(row[e], n, v[e]);
+                        row[e] += kCols;
                     }
-                    row[i] += kCols;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (row[e] != nullptr) ptx::st_shared_v4(to + e * 512 + ((piece ^ (m0 + 4 * e)) & 7) * 16, v[e][0], v[e][1], v[e][2], v[e][3]);
+            }
+            ptx::cp_async_commit();
+            if (it >= LAG) {
+                ptx::cp_async_wait<LAG>();
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(full + 8 * lag_stage);
+                lag_stage = lag_stage + 1 == S::STAGES ? 0 : lag_stage + 1;
+            }
+            if (++stage == S::STAGES) stage = 0, parity ^= 1;
+        }
+        ptx::cp_async_wait<0>();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        for (int i = 0; i < min(it, LAG) && ok; ++i) {
+            if (lane == 0) ptx::mbar_arrive(full + 8 * lag_stage);
+            lag_stage = lag_stage + 1 == S::STAGES ? 0 : lag_stage + 1;
+        }
+        ok = ok && wait(done, 0) && *abort_flag == 0u;
+        if (ok) {
+            ptx::tc_fence_after();
+            const int m = warp * 32 + lane;
+            float *out = a.out + (static_cast<int64_t>(blockIdx.y) * a.plan.tokens + tile.first + m) * RP;
+            const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+            const int sums = min(steps, S::SUMS);
+#pragma unroll
+            for (int c = 0; c < RP; c += 16) {
+                uint32_t v[16];
+                ptx::tmem_ld_32x32b_x16(from + c, v);
+                ptx::tmem_wait_ld();
+                float s[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(v[e]);
+                for (int i = 1; i < sums; ++i) {
+                    ptx::tmem_ld_32x32b_x16(from + i * S::N + c, v);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[e] += __uint_as_float(v[e]);
+                }
+                if (m < tile.count) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(out + c + e) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
                 }
             }
         }
-        left -= kCols;
-    };
-    auto store_late = [&]() {
-        if (!WIDE && active) {
+    } else {
+        // sums FP32, operands BF16
+        constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (TRANS ? 1u << 16 : 0u) | (static_cast<uint32_t>(S::N / 8) << 17) | (8u << 24);
+        int stage = 0, sum = 0;
+        uint32_t parity = 0;
+        for (int it = 0; it < steps; ++it) {
+            if (!wait(full + 8 * stage, parity)) break;
+            ptx::tc_fence_after();
+            if (lane == 0) {
+                const uint64_t xd = gemm_common::desc_sw128(sx + stage * S::X);
+                const uint64_t wd = TRANS ? desc_columns(sw + stage * S::W, kCols) : gemm_common::desc_sw128(sw + stage * S::W);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const uint32_t(&v)[8] = late[p / 2];
-                const int h = p % 2 * 4;
-                ptx::st_shared_v4(ring + in_stage * S::X + slot<8>(p / 2 * 8 + g, 2 * t + p % 2), v[h], v[h + 1], v[h + 2], v[h + 3]);
+                for (int k = 0; k < kCols / 16; ++k)
+                    ptx::tc_mma_bf16(tmem + sum * S::N, xd + 2 * k, wd + (TRANS ? k * (16 * 128 / 16) : 2 * k), idesc, it >= S::SUMS || k > 0);
+                ptx::tc_commit(empty + 8 * stage);
             }
+            __syncwarp();
+            if (++stage == S::STAGES) stage = 0, parity ^= 1;
+            if (++sum == S::SUMS) sum = 0;
         }
-        in_stage = in_stage + 1 == S::STAGES ? 0 : in_stage + 1;
-    };
-    for (int s = 0; s < S::STAGES - 1; ++s) {
-        if (s < steps) {
-            load();
-            store_late();
-        }
-        ptx::cp_async_commit();
+        if (lane == 0) ptx::tc_commit(done);
+        __syncwarp();
+        gemm_common::wait_phase(done, 0, kWaitNs, abort_flag, a.err, 0x20u + warp, false);
     }
-    float sum[RP / 8][4];
-#pragma unroll
-    for (int j = 0; j < RP / 8; ++j) sum[j][0] = sum[j][1] = sum[j][2] = sum[j][3] = 0.0f;
-    // the lane's places: of x; of W rows j * 8 + g, or of row 16 (i / 2) + (i & 1), and
-    // 2 on: a lane's terms
-    const uint32_t xat = ring + slot<8>(g, 2 * t);
-    const int wi = lane & 7;
-    const uint32_t wat = base + (TRANS ? (16 * (wi >> 1) + (wi & 1) + 2 * ((lane >> 3) & 1)) * S::ROW + (wi >> 1) * 32 + (lane >> 4) * 16
-                                       : g * S::ROW + 32 * t);
-    int stage = 0;
-    for (int s = 0; s < steps; ++s) {
-        ptx::cp_async_wait<S::STAGES - 2>();
-        __syncthreads();
-        const bool more = s + S::STAGES - 1 < steps;
-        if (more) load();
-        ptx::cp_async_commit();
-        if (active) {
-            const uint32_t at = wat + stage * S::W, xp = xat + stage * S::X;
-            uint32_t f[2][8];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                ptx::ld_shared_v4(xp + i * 8 * 128, f[i][0], f[i][1], f[i][2], f[i][3]);
-                ptx::ld_shared_v4((xp ^ 16) + i * 8 * 128, f[i][4], f[i][5], f[i][6], f[i][7]);
-            }
-            // sums of 64 products, then to registers
-            auto products = [&](int j, const uint32_t (&b)[8]) {
-                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t fa[4] = {f[0][2 * q], f[1][2 * q], f[0][2 * q + 1], f[1][2 * q + 1]};
-                    ptx::mma_bf16(acc, fa, b[2 * q], b[2 * q + 1]);
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) sum[j][q] += acc[q];
-            };
-            if constexpr (TRANS) {
-#pragma unroll
-                for (int jj = 0; jj < RP / 16; ++jj) {
-                    uint32_t b0[8], b1[8];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t m[4];
-                        ptx::ldmatrix_x4<true>(at + q * 4 * S::ROW + jj * 32, m);
-                        b0[2 * q] = m[0], b0[2 * q + 1] = m[1], b1[2 * q] = m[2], b1[2 * q + 1] = m[3];
-                    }
-                    products(2 * jj, b0);
-                    products(2 * jj + 1, b1);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < RP / 8; ++j) {
-                    uint32_t b[8];
-                    ptx::ld_shared_v4(at + j * 8 * S::ROW, b[0], b[1], b[2], b[3]);
-                    ptx::ld_shared_v4(at + j * 8 * S::ROW + 16, b[4], b[5], b[6], b[7]);
-                    products(j, b);
-                }
-            }
-        }
-        if (more) store_late();
-        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
-    }
-    ptx::cp_async_wait<0>();
-    float *out = a.out + (static_cast<int64_t>(blockIdx.y) * a.plan.tokens + tile.first) * RP;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int m = warp * 16 + h * 8 + g;
-        if (m < tile.count) {
-#pragma unroll
-            for (int j = 0; j < RP / 8; ++j)
-                *reinterpret_cast<float2 *>(out + m * RP + j * 8 + 2 * t) = make_float2(sum[j][2 * h], sum[j][2 * h + 1]);
-        }
-    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kCopyWarps) ptx::tmem_dealloc(tmem, S::TMEM);
 }
 
 template <int RP, bool TRANS, bool WIDE, bool WAL>
@@ -189,7 +218,7 @@ cudaError_t run(const ShrinkArgs &a, cudaStream_t stream) {
     auto *kern = &k_lora_shrink<RP, TRANS, WIDE, WAL>;
     const cudaError_t e = with_smem(kern, S::SMEM, S::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, dim3(a.plan.max_tiles(), most_splits(a.plan, a.k, RP)), kThreads, S::SMEM, stream, 1, a);
+    return launch_after(kern, dim3(a.plan.max_tiles(), most_splits(a.plan, a.k)), kThreads, S::SMEM, stream, 1, a);
 }
 template <int RP, bool TRANS>
 cudaError_t pick(const ShrinkArgs &a, cudaStream_t stream) {
@@ -212,6 +241,45 @@ cudaError_t by_rank(const ShrinkArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_shrink(const ShrinkArgs &a, bool trans, cudaStream_t stream) {
     return trans ? by_rank<true>(a, stream) : by_rank<false>(a, stream);
+}
+
+namespace {
+
+// A tile's partial sums added up in place (in the first ones), 32 rows a CTA.
+__global__ void __launch_bounds__(256) k_lora_sum(const SumArgs a, int rp) {
+    ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * rp);
+    const Tile tile = tile_at(a.plan, blockIdx.x);
+    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(tiles, a.long_side), quads = rp / 4;
+    if (static_cast<int>(blockIdx.x) >= a.plan.words[0]) return;
+    const int rank = tile.adapter < 0 ? 0 : rank_of(a.lw, tile.adapter);
+    const int64_t next = static_cast<int64_t>(a.plan.tokens) * rp;
+    for (int i = threadIdx.x; i < 32 * quads; i += 256) {
+        const int m = blockIdx.y * 32 + i / quads, r = i % quads * 4;
+        if (m >= tile.count) break;
+        float *p = a.rows + (tile.first + m) * static_cast<int64_t>(rp) + r;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (r < rank) {
+#pragma unroll 8
+            for (int s = 0; s < splits; ++s) {
+                const uint4 q = ptx::ld_v4(p + s * next);
+                v[0] += __uint_as_float(q.x), v[1] += __uint_as_float(q.y);
+                v[2] += __uint_as_float(q.z), v[3] += __uint_as_float(q.w);
+            }
+            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if (a.v_out != nullptr) {
+            float *to = a.v_out + row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_v) + r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (r + e < a.lw.r) to[e] = r + e < rank ? v[e] : 0.0f;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_sum(const SumArgs &a, cudaStream_t stream) {
+    return launch_after(&k_lora_sum, dim3(a.plan.max_tiles(), kLoraTile / 32), 256, 0, stream, 1, a, padded(a.lw.r));
 }
 
 }  // namespace lora
