@@ -70,8 +70,8 @@ cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t stream);
 // The tokens of a batch grouped by adapter, as int32 words in device memory:
 // [0] tiles, then first position and first tile of every adapter (one more than
 // adapters: the tokens without one), the tokens in that order, and the tiles
-// (adapter or -1, first position, tokens, 0) of up to kLoraTile tokens of one
-// adapter each.
+// (adapter or -1, first position, tokens, first token where they are neighbours or
+// -1) of up to kLoraTile tokens of one adapter each.
 constexpr int kLoraTile = 128;
 constexpr int kLoraMaxAdapters = 4096;
 constexpr int kLoraMaxRank = 128;

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const int *ids, int tokens, 
             bn += c;
         }
         for (int f = first; f < bn; f += kLoraTile, ++bt)
-            reinterpret_cast<int4 *>(words + p.tiles())[bt] = make_int4(b == adapters ? -1 : b, f, min(kLoraTile, bn - f), 0);
+            reinterpret_cast<int4 *>(words + p.tiles())[bt] = make_int4(b == adapters ? -1 : b, f, min(kLoraTile, bn - f), -1);
     }
     if (b1 == buckets && b0 < b1) {
         words[p.starts() + buckets] = bn;
@@ -83,6 +83,14 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const int *ids, int tokens, 
         __syncwarp();
         if (b >= 0 && lane == __ffs(same) - 1) mine[b] += __popc(same);
         __syncwarp();
+    }
+    // an adapter's tokens are in ascending order: neighbours, if the last one says so
+    __syncthreads();
+    const int tiles = words[0];
+    for (int b = tid; b < tiles; b += blockDim.x) {
+        int4 *tile = reinterpret_cast<int4 *>(words + p.tiles()) + b;
+        const int from_token = words[p.order() + tile->y];
+        if (words[p.order() + tile->y + tile->z - 1] - from_token == tile->z - 1) tile->w = from_token;
     }
 }
 

@@ -38,11 +38,11 @@ constexpr uint64_t kWaitNs = 2000000000ull;      // of a warp for another one of
 
 // A tile of the plan.
 struct Tile {
-    int adapter, first, count;
+    int adapter, first, count, row;      // row: the first token's, if they are neighbours, or -1
 };
 __device__ __forceinline__ Tile tile_at(const LoraPlan &p, int i) {
     const int4 t = reinterpret_cast<const int4 *>(p.words + p.tiles())[i];
-    return {t.x, t.y, t.z};
+    return {t.x, t.y, t.z, t.w};
 }
 __device__ __forceinline__ int rank_of(const LoraWeights &w, int g) {
     return w.ranks == nullptr ? w.r : max(0, min(w.r, w.ranks[g]));
@@ -172,6 +172,17 @@ inline int most_splits(const LoraPlan &p, int k) {
     return static_cast<int>(most < steps ? most : steps);
 }
 __device__ __forceinline__ int adapter_tiles(const LoraPlan &p) { return p.words[p.tile_first() + p.adapters]; }
+
+// A map of neighbouring rows, 64 BF16 values of each a piece, zeros past the last row
+// and column; false if the driver does not take it.
+inline bool rows_map(CUtensorMap *m, const uint16_t *p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    const TensorMapEncodeFn enc = tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)}, strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 struct ShrinkArgs {
     LoraPlan plan;

@@ -106,8 +106,10 @@ struct Shape {
 
 // Warps: four copy (a token's columns at a time; the first one the rows of r as well),
 // eight add up, one issues the products.
+// WIDE: rows that TMA takes (16-byte multiples); a step of 64 neighbours is copied by it.
 template <int RP, int PARTS, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1) k_lora_outer(const OuterArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    k_lora_outer(const OuterArgs a, const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1) {
     using S = Shape<RP, PARTS>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * (static_cast<int64_t>(a.side[0].n) + a.side[1].n));
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(const OuterArgs a) {
         constexpr int LAG = WIDE ? S::STAGES - 2 : 0;
         for (int t = t0; t < t1 && ok; ++it) {
             const int now = token, t_now = t, h_now = h;
+            const int together = WIDE && tile.row >= 0 && h * kStep + kStep <= tile.count ? tile.row + h * kStep : -1;
             h += 1;
             if (h * kStep >= tile.count) {
                 h = 0;
@@ -177,12 +180,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(const OuterArgs a) {
             ok = wait(empty + 8 * stage, parity);
             if (!ok) break;
             if (warp == 0 && lane == 0) {
-                ptx::mbar_arrive_expect_tx(full + 8 * stage, S::B);
+                ptx::mbar_arrive_expect_tx(full + 8 * stage, S::B + (together >= 0 ? S::A : 0));
+                for (int i = 0; i < S::COLS / 64 && together >= 0; ++i)
+                    ptx::tma_load_2d(sa + stage * S::A + i * (kStep * 128), second ? &map1 : &map0, full + 8 * stage, n0 + i * 64, together);
                 ptx::bulk_load(sb + stage * S::B, reinterpret_cast<const uint8_t *>(o.vt) + (2 * static_cast<int64_t>(t_now) + h_now) * S::B, S::B,
                                full + 8 * stage);
             }
             const uint32_t to = to0 + stage * S::A;
-            if constexpr (WIDE) {
+            __syncwarp();
+            if (together >= 0) {
+            } else if constexpr (WIDE) {
 #pragma unroll
                 for (int e = 0; e < EACH; ++e) {
                     const int i = e * ROWS + sub, m = warp * (kStep / kCopyWarps) + i, tok = __shfl_sync(0xFFFFFFFFu, now, i);
@@ -392,18 +399,18 @@ int cols(int rp) { return rp <= 64 ? Shape<64, 2>::COLS : Shape<128, 2>::COLS; }
 int blocks_of(int n, int rp) { return (n + cols(rp) - 1) / cols(rp); }
 
 template <int RP, int PARTS, bool WIDE>
-cudaError_t run(const OuterArgs &a, cudaStream_t stream) {
+cudaError_t run(const OuterArgs &a, const CUtensorMap (&map)[2], cudaStream_t stream) {
     static unsigned long long done;
     using S = Shape<RP, PARTS>;
     auto *kern = &k_lora_outer<RP, PARTS, WIDE>;
     const cudaError_t e = with_smem(kern, S::SMEM, S::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, dim3(a.side[0].blocks + a.side[1].blocks, a.chunks), kThreads, S::SMEM, stream, 1, a);
+    return launch_after(kern, dim3(a.side[0].blocks + a.side[1].blocks, a.chunks), kThreads, S::SMEM, stream, 1, a, map[0], map[1]);
 }
 template <int RP>
-cudaError_t pick(const OuterArgs &a, bool wide, cudaStream_t stream) {
-    if (a.f32) return wide ? run<RP, 3, true>(a, stream) : run<RP, 3, false>(a, stream);
-    return wide ? run<RP, 2, true>(a, stream) : run<RP, 2, false>(a, stream);
+cudaError_t pick(const OuterArgs &a, bool wide, const CUtensorMap (&map)[2], cudaStream_t stream) {
+    if (a.f32) return wide ? run<RP, 3, true>(a, map, stream) : run<RP, 3, false>(a, map, stream);
+    return wide ? run<RP, 2, true>(a, map, stream) : run<RP, 2, false>(a, map, stream);
 }
 template <int RP>
 cudaError_t prep(const PrepArgs &a, cudaStream_t stream) {
@@ -435,16 +442,18 @@ cudaError_t launch_outer(OuterArgs &a, cudaStream_t stream) {
     const int rp = padded(a.lw.r);
     bool wide = true;
     int64_t most = 0;
-    for (OuterSide &o : a.side) {
+    CUtensorMap map[2] = {};
+    for (int i = 0; i < 2; ++i) {
+        OuterSide &o = a.side[i];
         o.blocks = o.out != nullptr ? blocks_of(o.n, rp) : 0;
         if (o.out == nullptr) continue;
-        wide = wide && aligned_to(o.d, 16) && o.ld % 8 == 0;
+        wide = wide && aligned_to(o.d, 16) && o.ld % 8 == 0 && rows_map(&map[i], o.d, a.plan.tokens, o.n, o.ld, kStep);
         most = std::max<int64_t>(most, o.n);
     }
-    const cudaError_t e = rp == 16   ? pick<16>(a, wide, stream)
-                          : rp == 32 ? pick<32>(a, wide, stream)
-                          : rp == 64 ? pick<64>(a, wide, stream)
-                                     : pick<128>(a, wide, stream);
+    const cudaError_t e = rp == 16   ? pick<16>(a, wide, map, stream)
+                          : rp == 32 ? pick<32>(a, wide, map, stream)
+                          : rp == 64 ? pick<64>(a, wide, map, stream)
+                                     : pick<128>(a, wide, map, stream);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((most + 31) / 32, 1024)), std::min(a.plan.adapters, 64), 2);
     return launch_after(&k_lora_join, grid, 256, 0, stream, 1, a, rp);

@@ -38,8 +38,12 @@ struct Shape {
     static constexpr int P = TRANS ? RP / 8 : 8, ROWS = TRANS ? kCols : RP, PIECES = ROWS * P / (kCopyWarps * 32);
 };
 
+// WIDE, WAL: rows of x, and W, that TMA takes (16-byte multiples).  A tile whose tokens are
+// neighbours is copied by it; rows that are not, by the warps.  (TMA's own gather
+// takes 82 us where the warps take 36, at 8192 x 8960, r 64.)
 template <int RP, bool TRANS, bool WIDE, bool WAL>
-__global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(const ShrinkArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    k_lora_shrink(const ShrinkArgs a, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w) {
     using S = Shape<RP, TRANS>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * a.k);
@@ -57,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(const ShrinkArgs a)
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
-            ptx::mbar_init(full + 8 * i, kCopyWarps);
+            ptx::mbar_init(full + 8 * i, kCopyWarps + 1);
             ptx::mbar_init(empty + 8 * i, 1);
         }
         ptx::mbar_init(done, 1);
@@ -97,51 +101,70 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(const ShrinkArgs a)
             wrow[i] = w + row_at(r, a.ld_w);
             wto[i] = sw + (TRANS ? wc / 64 * (kCols * 128) : 0) + r * 128 + ((wc / 8 % 8) ^ (r & 7)) * 16;
         }
+        constexpr int LAG = S::STAGES - 2;
         const int64_t wstep = TRANS ? static_cast<int64_t>(kCols) * a.ld_w : kCols;
-        int left = a.k - first * kCols, stage = 0, lag_stage = 0;
+        int left = a.k - first * kCols, stage = 0, lag_stage = 0, it = 0;
         uint32_t parity = 1;
         bool ok = true;
-        int it = 0;
-        constexpr int LAG = WIDE && WAL ? S::STAGES - 2 : 0;
+        // by TMA: x, W; a step's arrivals lag behind its copies where the warps make some
+        const bool tma_x = WIDE && tile.row >= 0;
+        const int lag = tma_x && WAL ? 0 : WIDE ? LAG : 0, tx = (tma_x ? S::X : 0) + (WAL ? S::W : 0);
         for (; it < steps; ++it, left -= kCols) {
             ok = wait(empty + 8 * stage, parity);
             if (!ok) break;
+            if (threadIdx.x == 0) {
+                const uint32_t bar = full + 8 * stage;
+                const int k = (first + it) * kCols;
+                ptx::mbar_arrive_expect_tx(bar, tx);
+                if (tma_x) ptx::tma_load_2d(sx + stage * S::X, &map_x, bar, k, tile.row);
+                if constexpr (WAL && TRANS) {
 #pragma unroll
-            for (int i = 0; i < S::PIECES; ++i) {
-                const int r = tid / S::P + i * (kCopyWarps * 32 / S::P);
-                // of a row past the end: zeros along the long side, nothing past the rank
-                const int have = TRANS ? (r < left ? rank - wc : 0) : left - wc;
-                if (TRANS ? wc < rank : r < rank) copy8<WAL>(wto[i] + stage * S::W, have > 0 ? wrow[i] : a.w, have);
-                wrow[i] += wstep;
+                    for (int i = 0; i < S::N / 64; ++i) ptx::tma_load_3d(sw + stage * S::W + i * (kCols * 128), &map_w, bar, i * 64, k, tile.adapter);
+                } else if constexpr (WAL) {
+                    ptx::tma_load_3d(sw + stage * S::W, &map_w, bar, k, 0, tile.adapter);
+                }
             }
-            const uint32_t to = sx + stage * S::X + m0 * 128;
-            const int n = left - piece * 8;
-            if constexpr (WIDE) {
+            __syncwarp();
+            if constexpr (!WAL) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (row[e] != nullptr) {
-                        ptx::cp_async16(to + e * 512 + ((piece ^ (m0 + 4 * e)) & 7) * 16, n > 0 ? row[e] : a.x, max(0, min(16, 2 * n)));
-                        row[e] += kCols;
-                    }
+                for (int i = 0; i < S::PIECES; ++i) {
+                    const int r = tid / S::P + i * (kCopyWarps * 32 / S::P);
+                    // of a row past the end: zeros along the long side, nothing past the rank
+                    const int have = TRANS ? (r < left ? rank - wc : 0) : left - wc;
+                    if (TRANS ? wc < rank : r < rank) copy8<false>(wto[i] + stage * S::W, have > 0 ? wrow[i] : a.w, have);
+                    wrow[i] += wstep;
                 }
-            } else {
-                uint32_t v[8][4];
+            }
+            if (!tma_x) {
+                const uint32_t to = sx + stage * S::X + m0 * 128;
+                const int n = left - piece * 8;
+                if constexpr (WIDE) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0u;
-                    if (row[e] != nullptr) {
-                        if (n > 0) load8(row[e], n, v[e]);
-                        row[e] += kCols;
+                    for (int e = 0; e < 8; ++e) {
+                        if (row[e] != nullptr) {
+                            ptx::cp_async16(to + e * 512 + ((piece ^ (m0 + 4 * e)) & 7) * 16, n > 0 ? row[e] : a.x, max(0, min(16, 2 * n)));
+                            row[e] += kCols;
+                        }
                     }
-                }
+                } else {
+                    uint32_t v[8][4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (row[e] != nullptr) ptx::st_shared_v4(to + e * 512 + ((piece ^ (m0 + 4 * e)) & 7) * 16, v[e][0], v[e][1], v[e][2], v[e][3]);
+                    for (int e = 0; e < 8; ++e) {
+                        v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0u;
+                        if (row[e] != nullptr) {
+                            if (n > 0) load8(row[e], n, v[e]);
+                            row[e] += kCols;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (row[e] != nullptr) ptx::st_shared_v4(to + e * 512 + ((piece ^ (m0 + 4 * e)) & 7) * 16, v[e][0], v[e][1], v[e][2], v[e][3]);
+                }
             }
             ptx::cp_async_commit();
-            if (it >= LAG) {
-                ptx::cp_async_wait<LAG>();
-                ptx::fence_proxy_async_smem();
+            if (it >= lag) {
+                if (WIDE && !tma_x) ptx::cp_async_wait<LAG>();
+                if (!(tma_x && WAL)) ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(full + 8 * lag_stage);
                 lag_stage = lag_stage + 1 == S::STAGES ? 0 : lag_stage + 1;
@@ -151,10 +174,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(const ShrinkArgs a)
         ptx::cp_async_wait<0>();
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        for (int i = 0; i < min(it, LAG) && ok; ++i) {
+        for (int i = 0; i < min(it, lag) && ok; ++i) {
             if (lane == 0) ptx::mbar_arrive(full + 8 * lag_stage);
             lag_stage = lag_stage + 1 == S::STAGES ? 0 : lag_stage + 1;
         }
+        // after a wait that ran out, the copies under way land before the CTA ends
+        for (int i = max(0, it - S::STAGES); i < it && !ok && warp == 0; ++i)
+            gemm_common::wait_phase(full + 8 * (i % S::STAGES), (i / S::STAGES) & 1, 2000000ull, abort_flag, a.err, 0u, false);
         ok = ok && wait(done, 0) && *abort_flag == 0u;
         if (ok) {
             ptx::tc_fence_after();
@@ -212,20 +238,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(const ShrinkArgs a)
 }
 
 template <int RP, bool TRANS, bool WIDE, bool WAL>
-cudaError_t run(const ShrinkArgs &a, cudaStream_t stream) {
+cudaError_t run(const ShrinkArgs &a, const CUtensorMap &map_x, const CUtensorMap &map_w, cudaStream_t stream) {
     using S = Shape<RP, TRANS>;
     static unsigned long long done;
     auto *kern = &k_lora_shrink<RP, TRANS, WIDE, WAL>;
     const cudaError_t e = with_smem(kern, S::SMEM, S::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, dim3(a.plan.max_tiles(), most_splits(a.plan, a.k)), kThreads, S::SMEM, stream, 1, a);
+    return launch_after(kern, dim3(a.plan.max_tiles(), most_splits(a.plan, a.k)), kThreads, S::SMEM, stream, 1, a, map_x, map_w);
+}
+// W as [adapters][rows][long side], 64 values of the latter (or of a row of r) a piece.
+bool weights_map(CUtensorMap *m, const ShrinkArgs &a, int rows, int cols, int box_rows) {
+    const TensorMapEncodeFn enc = tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t ld = static_cast<cuuint64_t>(a.ld_w) * 2;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(a.plan.adapters)};
+    // one adapter: any stride
+    const cuuint64_t strides[2] = {ld, a.plan.adapters > 1 ? static_cast<cuuint64_t>(a.stride_w) * 2 : ld};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(a.w), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 template <int RP, bool TRANS>
 cudaError_t pick(const ShrinkArgs &a, cudaStream_t stream) {
-    const bool wide = aligned_to(a.x, 16) && a.ld_x % 8 == 0;
-    const bool wal = aligned_to(a.w, 16) && a.ld_w % 8 == 0 && a.stride_w % 8 == 0;
-    if (wide) return wal ? run<RP, TRANS, true, true>(a, stream) : run<RP, TRANS, true, false>(a, stream);
-    return wal ? run<RP, TRANS, false, true>(a, stream) : run<RP, TRANS, false, false>(a, stream);
+    CUtensorMap map_x = {}, map_w = {};
+    const bool wide = aligned_to(a.x, 16) && a.ld_x % 8 == 0 && rows_map(&map_x, a.x, a.plan.tokens, a.k, a.ld_x, kLoraTile);
+    // a map's strides are not zero (one adapter for all)
+    const bool wal = aligned_to(a.w, 16) && a.ld_w % 8 == 0 && a.stride_w % 8 == 0 && (a.plan.adapters == 1 || a.stride_w > 0) &&
+                     weights_map(&map_w, a, TRANS ? a.k : a.lw.r, TRANS ? a.lw.r : a.k, TRANS ? kCols : RP);
+    if (wide) return wal ? run<RP, TRANS, true, true>(a, map_x, map_w, stream) : run<RP, TRANS, true, false>(a, map_x, map_w, stream);
+    return wal ? run<RP, TRANS, false, true>(a, map_x, map_w, stream) : run<RP, TRANS, false, false>(a, map_x, map_w, stream);
 }
 template <bool TRANS>
 cudaError_t by_rank(const ShrinkArgs &a, cudaStream_t stream) {

@@ -68,8 +68,11 @@ def test_plan(cuda_lib, t, g):
     assert torch.equal(w[at:at + t].long(), torch.sort(bucket, stable=True)[1])
     at += t + -(at + t) % 4
     got = w[at:at + 4 * int(w[0])].view(-1, 4)
-    want = [(i if i < g else -1, int(starts[i]) + 128 * j, min(128, int(counts[i]) - 128 * j), 0) for i in range(g + 1) for j in range(int(tiles[i]))]
-    assert got.tolist() == [list(e) for e in want]
+    want = [(i if i < g else -1, int(starts[i]) + 128 * j, min(128, int(counts[i]) - 128 * j)) for i in range(g + 1) for j in range(int(tiles[i]))]
+    assert got[:, :3].tolist() == [list(e) for e in want]
+    for _, first, count, row in got.tolist():
+        tokens = w[8 + 2 * g + first:8 + 2 * g + first + count].tolist()
+        assert row == (tokens[0] if tokens == list(range(tokens[0], tokens[0] + count)) else -1)
 
 
 @pytest.mark.parametrize("size", SIZES)
