@@ -16,15 +16,16 @@ Every one takes stream=, a torch stream or a raw handle, as well.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
-from . import E4M3, GRAN_1x128, GRAN_ROW, OUT_BF16, OUT_FP32, QTensor
+from . import E4M3, GRAN_1x128, GRAN_ROW, OUT_BF16, OUT_FP32, QTensor, _round4
 from . import lib as _lib
 from . import lowbit
-from .lowbit import _check, _groups, _new, _round16, _streamed
+from .lowbit import _check, _new, _round16, _streamed
 
 MAX_RANK, MAX_ADAPTERS, MAX_TOKENS = 128, 4096, 1 << 24
 
@@ -66,14 +67,7 @@ def _fns():
 
 
 _KIND = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32}
-
-
-def _here(t) -> bool:
-    return lowbit._here(t)
-
-
-def _on(x):
-    return lowbit._on(x)
+_BF16, _F32, _EITHER = {torch.bfloat16: OUT_BF16}, {torch.float32: OUT_FP32}, _KIND
 
 
 def _kind(dtype, what) -> int:
@@ -83,55 +77,55 @@ def _kind(dtype, what) -> int:
     return kind
 
 
-def _matrix(x, what, dtypes, shape=None):
-    """Rows, columns and row stride of a matrix of one of the types (and of a shape)."""
-    if x.dtype in dtypes and x.dim() == 2 and _here(x):
-        rows, cols = x.shape
+def _matrix(x, what, kinds, device, shape=None):
+    """Shape, row stride and kind of a matrix of one of the types (and of a shape)."""
+    kind, size = kinds.get(x.dtype), x.shape
+    if kind is not None and len(size) == 2 and x.get_device() == device and (shape is None or size == shape):
         ld, unit = x.stride()
-        if (shape is None or (rows, cols) == shape) and (unit == 1 or cols <= 1):
-            return rows, cols, ld if rows > 1 else _round16(cols)
-    names = " or ".join(str(d).replace("torch.", "") for d in dtypes)
+        if unit == 1 or size[1] <= 1:
+            return size, ld if size[0] > 1 else _round16(size[1]), kind
+    names = " or ".join(str(d).replace("torch.", "") for d in kinds)
     size = "2-D" if shape is None else f"[{shape[0]}, {shape[1]}]"
     raise ValueError(f"{what} must be a {size} {names} tensor on the current CUDA device with unit column stride")
 
 
-_BF16, _F32, _EITHER = (torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32)
+def _param(p, what, cols, device):
+    """Address and kind of the norm's weight or bias."""
+    kind = _KIND.get(p.dtype)
+    if kind is None or p.shape != (cols,) or p.get_device() != device or not p.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous bfloat16 or float32 tensor [{cols}] on the current CUDA device")
+    return p.data_ptr(), kind
 
 
-def _params(weight, bias, cols):
+def _params(weight, bias, cols, device):
     """Addresses of weight and bias and their kind."""
-    kind = OUT_FP32
-    for what, p in (("weight", weight), ("bias", bias)):
-        if p is not None:
-            if p.dtype not in _KIND or tuple(p.shape) != (cols,) or not _here(p) or (cols > 1 and p.stride(0) != 1):
-                raise ValueError(f"{what} must be a contiguous bfloat16 or float32 tensor [{cols}] on the current CUDA device")
-            kind = _KIND[p.dtype]
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+    if weight is None:
+        return (None, None, OUT_FP32) if bias is None else (None, *_param(bias, "bias", cols, device))
+    w, kind = _param(weight, "weight", cols, device)
+    if bias is None:
+        return w, None, kind
+    b, kind_b = _param(bias, "bias", cols, device)
+    if kind_b != kind:
         raise ValueError("weight and bias must have the same type")
-    return _address(weight), _address(bias), kind
+    return w, b, kind
 
 
 def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _result(out, rows, cols, dtype, what="out"):
+def _result(out, shape, dtype, device):
     """The caller's output, checked, or a new one; its row stride and kind."""
     if out is None:
-        return _new((rows, cols), (cols, 1), dtype), cols, _kind(dtype, what)
-    _, _, ld = _matrix(out, what, _EITHER, (rows, cols))
-    return out, ld, _KIND[out.dtype]
+        return _new(tuple(shape), (shape[1], 1), dtype), shape[1], _kind(dtype, "out")
+    _, ld, kind = _matrix(out, "out", _EITHER, device, shape)
+    return out, ld, kind
 
 
-def _scratch(n, x, stream):
-    return lowbit._scratch(n, x, stream)
-
-
-def _norm(x, weight, bias, eps, y, ld_y, y_kind, codes, stats):
-    rows, cols, ld = _matrix(x, "x", _EITHER)
-    w, b, kind = _params(weight, bias, cols)
-    _check(_fns().fp8hg_layernorm(x.data_ptr(), _KIND[x.dtype], rows, cols, ld, w, b, kind, eps, _address(y), y_kind, ld_y,
-                                  codes, stats.data_ptr(), _on(x)), "layernorm")
+@functools.lru_cache(maxsize=4096)
+def _bytes(name, *sizes) -> int:
+    """A workspace size of the library, a function of sizes alone."""
+    return getattr(_fns(), name)(*sizes)
 
 
 @_streamed
@@ -139,10 +133,14 @@ def layernorm(x, weight=None, bias=None, eps: float = 1e-5, out=None, out_dtype=
     """y = (x - mean) rstd weight + bias of every row of x [rows, cols], BF16 or
     FP32, in out_dtype (x's), and stats [rows, 2], mean and rstd in FP32, for
     layernorm_bwd."""
-    rows, cols, _ = _matrix(x, "x", _EITHER)
-    y, ld, kind = _result(out, rows, cols, out_dtype or x.dtype)
+    device = lowbit._cuda_device()
+    shape, ld, kind = _matrix(x, "x", _EITHER, device)
+    rows, cols = shape
+    w, b, kind_p = _params(weight, bias, cols, device)
+    y, ld_y, kind_y = _result(out, shape, out_dtype or x.dtype, device)
     stats = _new((rows, 2), (2, 1), torch.float32)
-    _norm(x, weight, bias, eps, y, ld, kind, None, stats)
+    _check((_bound or _fns()).fp8hg_layernorm(x.data_ptr(), kind, rows, cols, ld, w, b, kind_p, eps, y.data_ptr(), kind_y, ld_y, None,
+                                              stats.data_ptr(), lowbit._raw_stream(device)), "layernorm")
     return y, stats
 
 
@@ -152,17 +150,25 @@ def fp8_layernorm(x, weight=None, bias=None, eps: float = 1e-5, group: int = 0, 
     like fp8_quant_token: one UE8M0 scale per token (group=0) or per 128 columns
     (128; any number of columns, the last group may be shorter).  with_y=True also
     gives y in BF16, from the same read: QTensor, y or None, stats."""
-    rows, cols, _ = _matrix(x, "x", _EITHER)
-    if group not in (0, 128):
-        raise ValueError("group must be 0 or 128")
-    if group:
-        q = _groups(rows, cols, fmt)
+    device = lowbit._cuda_device()
+    shape, ld, kind = _matrix(x, "x", _EITHER, device)
+    rows, cols = shape
+    w, b, kind_p = _params(weight, bias, cols, device)
+    ld_q = _round16(cols)
+    if group == 128:
+        groups = (cols + 127) // 128
+        ld_s = _round4(groups)
+        q = QTensor(_new((rows, cols), (ld_q, 1), torch.uint8), _new((rows, ld_s), (ld_s, 1), torch.uint8), fmt, GRAN_1x128, groups)
+    elif group == 0:
+        ld_s = 1
+        q = QTensor(_new((rows, cols), (ld_q, 1), torch.uint8), _new((rows, 1), (1, 1), torch.uint8), fmt, GRAN_ROW, 1)
     else:
-        q = QTensor(_new((rows, cols), (_round16(cols), 1), torch.uint8), _new((rows, 1), (1, 1), torch.uint8), fmt, GRAN_ROW, 1)
+        raise ValueError("group must be 0 or 128")
     y = _new((rows, cols), (cols, 1), torch.bfloat16) if with_y else None
     stats = _new((rows, 2), (2, 1), torch.float32)
-    codes = _Codes(q.codes.data_ptr(), q.scale.data_ptr(), _round16(cols), max(1, q.scale.stride(0)), group, fmt)
-    _norm(x, weight, bias, eps, y, cols, OUT_BF16, ctypes.byref(codes), stats)
+    codes = _Codes(q.codes.data_ptr(), q.scale.data_ptr(), ld_q, max(1, ld_s), group, fmt)
+    _check((_bound or _fns()).fp8hg_layernorm(x.data_ptr(), kind, rows, cols, ld, w, b, kind_p, eps, _address(y), OUT_BF16, cols,
+                                              ctypes.byref(codes), stats.data_ptr(), lowbit._raw_stream(device)), "fp8_layernorm")
     return q, y, stats
 
 
@@ -171,25 +177,28 @@ def layernorm_bwd(dy, x, weight, stats, add=None, out=None, params: bool = True)
     """dx (x's type), dweight and dbias (FP32) from dy, x and the forward pass's
     stats.  add: another branch's gradient of x, added to dx (may be out).
     params=False: dx alone, (dx, None, None)."""
-    rows, cols, ld_x = _matrix(x, "x", _EITHER)
-    _, _, ld_dy = _matrix(dy, "dy", _EITHER, (rows, cols))
-    w, _, kind = _params(weight, None, cols)
-    if stats.dtype != torch.float32 or tuple(stats.shape) != (rows, 2) or not stats.is_contiguous() or not _here(stats):
+    device = lowbit._cuda_device()
+    shape, ld_x, kind = _matrix(x, "x", _EITHER, device)
+    rows, cols = shape
+    _, ld_dy, kind_dy = _matrix(dy, "dy", _EITHER, device, shape)
+    w, _, kind_p = _params(weight, None, cols, device)
+    if stats.dtype != torch.float32 or stats.shape != (rows, 2) or stats.get_device() != device or not stats.is_contiguous():
         raise ValueError(f"stats must be a contiguous float32 tensor [{rows}, 2] on the current CUDA device")
-    ld_add = 0 if add is None else _matrix(add, "add", (x.dtype,), (rows, cols))[2]
+    same = _BF16 if kind == OUT_BF16 else _F32
+    ld_add = 0 if add is None else _matrix(add, "add", same, device, shape)[1]
     if out is None:
         out, ld_dx = _new((rows, cols), (cols, 1), x.dtype), cols
     else:
-        ld_dx = _matrix(out, "out", (x.dtype,), (rows, cols))[2]
-    dw = _new((cols,), (1,), torch.float32) if params else None
-    db = _new((cols,), (1,), torch.float32) if params else None
-    f = _fns()
-    stream = _on(x)
-    n = f.fp8hg_layernorm_bwd_workspace(rows, cols) if params else 0
-    ws = _scratch(n, x, stream).data_ptr() if n else None
-    _check(f.fp8hg_layernorm_bwd(dy.data_ptr(), _KIND[dy.dtype], ld_dy, x.data_ptr(), _KIND[x.dtype], ld_x, rows, cols, w, kind,
-                                 stats.data_ptr(), _address(add), ld_add, out.data_ptr(), ld_dx, _address(dw), _address(db), ws, n,
-                                 stream), "layernorm_bwd")
+        ld_dx = _matrix(out, "out", same, device, shape)[1]
+    stream, dw, db, ws, n = lowbit._raw_stream(device), None, None, None, 0
+    if params:
+        dw, db = _new((cols,), (1,), torch.float32), _new((cols,), (1,), torch.float32)
+        n = _bytes("fp8hg_layernorm_bwd_workspace", rows, cols)
+        if n:
+            ws = lowbit._scratch(n, x, stream).data_ptr()
+    _check((_bound or _fns()).fp8hg_layernorm_bwd(dy.data_ptr(), kind_dy, ld_dy, x.data_ptr(), kind, ld_x, rows, cols, w, kind_p,
+                                                  stats.data_ptr(), _address(add), ld_add, out.data_ptr(), ld_dx, _address(dw),
+                                                  _address(db), ws, n, stream), "layernorm_bwd")
     return out, dw, db
 
 
@@ -205,23 +214,26 @@ class LoraAdapters:
     scale: Optional[torch.Tensor] = None
     ranks: Optional[torch.Tensor] = None
 
-    def operand(self) -> _Lora:
-        a, b = self.a, self.b
-        if not (a.dtype == b.dtype == torch.bfloat16 and a.dim() == b.dim() == 3 and _here(a) and _here(b)):
+    def operand(self, device=None) -> _Lora:
+        a, b, scale, ranks = self.a, self.b, self.scale, self.ranks
+        device = lowbit._cuda_device() if device is None else device
+        if not (a.dtype == b.dtype == torch.bfloat16 and a.dim() == b.dim() == 3 and a.get_device() == device and b.get_device() == device):
             raise ValueError("A and B must be 3-D bfloat16 tensors on the current CUDA device")
         g, r, k = a.shape
-        n = b.shape[1]
-        if b.shape[0] != g or b.shape[2] != r:
+        g_b, n, r_b = b.shape
+        if g_b != g or r_b != r:
             raise ValueError("A [adapters, r, k] and B [adapters, n, r] must have the same adapters and rank")
-        if (k > 1 and a.stride(2) != 1) or (r > 1 and b.stride(2) != 1):
+        stride_a, ld_a, unit_a = a.stride()
+        stride_b, ld_b, unit_b = b.stride()
+        if (unit_a != 1 and k > 1) or (unit_b != 1 and r > 1):
             raise ValueError("A and B must have unit stride along k and r")
-        for what, t, dtype in (("scale", self.scale, torch.float32), ("ranks", self.ranks, torch.int32)):
-            if t is not None and (t.dtype != dtype or tuple(t.shape) != (g,) or not t.is_contiguous() or not _here(t)):
-                raise ValueError(f"{what} must be a contiguous {str(dtype)[6:]} tensor [{g}] on the current CUDA device")
+        if scale is not None and (scale.dtype != torch.float32 or scale.shape != (g,) or scale.get_device() != device or not scale.is_contiguous()):
+            raise ValueError(f"scale must be a contiguous float32 tensor [{g}] on the current CUDA device")
+        if ranks is not None and (ranks.dtype != torch.int32 or ranks.shape != (g,) or ranks.get_device() != device or not ranks.is_contiguous()):
+            raise ValueError(f"ranks must be a contiguous int32 tensor [{g}] on the current CUDA device")
         # strides of a dimension of one element say nothing
-        ld_a, ld_b = a.stride(1) if r > 1 else _round16(k), b.stride(1) if n > 1 else _round16(r)
-        return _Lora(a.data_ptr(), b.data_ptr(), _address(self.scale), _address(self.ranks), g, r, n, k,
-                     a.stride(0) if g > 1 else 0, ld_a, b.stride(0) if g > 1 else 0, ld_b)
+        return _Lora(a.data_ptr(), b.data_ptr(), _address(scale), _address(ranks), g, r, n, k, stride_a if g > 1 else 0,
+                     ld_a if r > 1 else _round16(k), stride_b if g > 1 else 0, ld_b if n > 1 else _round16(r))
 
 
 @dataclass
@@ -235,7 +247,7 @@ class LoraPlan:
     def address(self, tokens, adapters):
         if (self.tokens, self.adapters) != (tokens, adapters):
             raise ValueError(f"the plan is of {self.tokens} tokens and {self.adapters} adapters, the call of {tokens} and {adapters}")
-        if not _here(self.words):
+        if self.words.get_device() != lowbit._cuda_device():
             raise ValueError("the plan must be on the current CUDA device")
         return self.words.data_ptr()
 
@@ -245,7 +257,7 @@ def lora_plan(ids, adapters: int) -> LoraPlan:
     """Groups the tokens of a batch by their adapters, ids [tokens] in int32: one
     that is negative, or not below `adapters`, is a token without an adapter.  Made
     once per batch, for every projection of every layer, forward and backward."""
-    if ids.dtype != torch.int32 or ids.dim() != 1 or not ids.is_contiguous() or not _here(ids):
+    if ids.dtype != torch.int32 or ids.dim() != 1 or not ids.is_contiguous() or ids.get_device() != lowbit._cuda_device():
         raise ValueError("ids must be a contiguous int32 tensor [tokens] on the current CUDA device")
     tokens = ids.shape[0]
     if not 1 <= adapters <= MAX_ADAPTERS or tokens > MAX_TOKENS:
@@ -253,7 +265,7 @@ def lora_plan(ids, adapters: int) -> LoraPlan:
     f = _fns()
     n = f.fp8hg_lora_plan_bytes(tokens, adapters)
     words = _new((n // 4,), (1,), torch.int32)
-    _check(f.fp8hg_lora_plan(ids.data_ptr(), tokens, adapters, words.data_ptr(), n, _on(ids)), "lora_plan")
+    _check(f.fp8hg_lora_plan(ids.data_ptr(), tokens, adapters, words.data_ptr(), n, lowbit._raw_stream(ids.get_device())), "lora_plan")
     return LoraPlan(words, tokens, adapters)
 
 
@@ -264,25 +276,26 @@ def lora_add(base, x, adapters: LoraAdapters, plan: LoraPlan, out=None, keep: bo
     zeros, then out_dtype), x [tokens, k] its BF16 input.  out may be base.
     Returns y and, with keep=True, x A^T [tokens, r] in FP32 for lora_add_bwd
     (None otherwise)."""
-    w = adapters.operand()
-    tokens, _, ld_x = _matrix(x, "x", _BF16, (x.shape[0], w.k) if x.dim() == 2 else None)
-    ld_base, dtype = 0, out_dtype or torch.bfloat16
+    device = lowbit._cuda_device()
+    w = adapters.operand(device)
+    tokens = x.shape[0]
+    ld_x = _matrix(x, "x", _BF16, device, (tokens, w.k))[1]
+    shape, ld_base, dtype = (tokens, w.n), 0, out_dtype or torch.bfloat16
     if base is not None:
-        _, _, ld_base = _matrix(base, "base", _EITHER, (tokens, w.n))
+        ld_base = _matrix(base, "base", _EITHER, device, shape)[1]
         dtype = base.dtype
         if out_dtype not in (None, dtype):
             raise ValueError("out_dtype must be base's type")
-    out, ld, kind = _result(out, tokens, w.n, dtype)
+    out, ld, kind = _result(out, shape, dtype, device)
     if base is not None and out.dtype != dtype:
         raise ValueError("base and out must have the same type")
     p = plan.address(tokens, w.adapters)
     v = _new((tokens, w.r), (w.r, 1), torch.float32) if keep else None
-    f = _fns()
-    stream = _on(x)
-    n = f.fp8hg_lora_workspace(tokens, w.adapters, w.r, w.k)
-    ws = _scratch(n, x, stream).data_ptr() if n else None
-    _check(f.fp8hg_lora_add(ctypes.byref(w), p, tokens, x.data_ptr(), ld_x, _address(base), ld_base, out.data_ptr(), ld, kind,
-                            _address(v), w.r, ws, n, stream), "lora_add")
+    stream = lowbit._raw_stream(device)
+    n = _bytes("fp8hg_lora_workspace", tokens, w.adapters, w.r, w.k)
+    ws = lowbit._scratch(n, x, stream).data_ptr() if n else None
+    _check((_bound or _fns()).fp8hg_lora_add(ctypes.byref(w), p, tokens, x.data_ptr(), ld_x, _address(base), ld_base, out.data_ptr(), ld,
+                                             kind, _address(v), w.r, ws, n, stream), "lora_add")
     return out, v
 
 
@@ -295,19 +308,21 @@ def lora_add_bwd(dy, x, v, adapters: LoraAdapters, plan: LoraPlan, base=None, ou
     projection's own data gradient (None: zeros, then out_dtype); out may be base.
     The gradients of A and B have params_dtype; params=False: dx alone, and x and v
     may be None."""
-    w = adapters.operand()
-    tokens, _, ld_dy = _matrix(dy, "dy", _BF16, (dy.shape[0], w.n) if dy.dim() == 2 else None)
-    ld_x = ld_v = 0
+    device = lowbit._cuda_device()
+    w = adapters.operand(device)
+    tokens = dy.shape[0]
+    ld_dy = _matrix(dy, "dy", _BF16, device, (tokens, w.n))[1]
+    shape, ld_x, ld_v = (tokens, w.k), 0, 0
     if params:
-        ld_x = _matrix(x, "x", _BF16, (tokens, w.k))[2]
-        ld_v = _matrix(v, "v", _F32, (tokens, w.r))[2]
+        ld_x = _matrix(x, "x", _BF16, device, shape)[1]
+        ld_v = _matrix(v, "v", _F32, device, (tokens, w.r))[1]
     ld_base, dtype = 0, out_dtype or torch.bfloat16
     if base is not None:
-        _, _, ld_base = _matrix(base, "base", _EITHER, (tokens, w.k))
+        ld_base = _matrix(base, "base", _EITHER, device, shape)[1]
         dtype = base.dtype
         if out_dtype not in (None, dtype):
             raise ValueError("out_dtype must be base's type")
-    out, ld, kind = _result(out, tokens, w.k, dtype)
+    out, ld, kind = _result(out, shape, dtype, device)
     if base is not None and out.dtype != dtype:
         raise ValueError("base and out must have the same type")
     p = plan.address(tokens, w.adapters)
@@ -317,11 +332,10 @@ def lora_add_bwd(dy, x, v, adapters: LoraAdapters, plan: LoraPlan, base=None, ou
         dw_kind = _kind(params_dtype, "the gradients of A and B")
         da = _new((w.adapters, w.r, w.k), (w.r * w.k, w.k, 1), params_dtype)
         db = _new((w.adapters, w.n, w.r), (w.n * w.r, w.r, 1), params_dtype)
-    f = _fns()
-    stream = _on(dy)
-    n = f.fp8hg_lora_bwd_workspace(tokens, w.adapters, w.r, w.n, w.k)
-    ws = _scratch(n, dy, stream).data_ptr() if n else None
-    _check(f.fp8hg_lora_add_bwd(ctypes.byref(w), p, tokens, dy.data_ptr(), ld_dy, _address(x) if params else None, ld_x,
-                                _address(v) if params else None, ld_v, _address(base), ld_base, out.data_ptr(), ld, kind,
-                                _address(da), _address(db), dw_kind, ws, n, stream), "lora_add_bwd")
+    stream = lowbit._raw_stream(device)
+    n = _bytes("fp8hg_lora_bwd_workspace", tokens, w.adapters, w.r, w.n, w.k)
+    ws = lowbit._scratch(n, dy, stream).data_ptr() if n else None
+    _check((_bound or _fns()).fp8hg_lora_add_bwd(ctypes.byref(w), p, tokens, dy.data_ptr(), ld_dy, _address(x) if params else None, ld_x,
+                                                 _address(v) if params else None, ld_v, _address(base), ld_base, out.data_ptr(), ld, kind,
+                                                 _address(da), _address(db), dw_kind, ws, n, stream), "lora_add_bwd")
     return out, da, db
