@@ -106,10 +106,33 @@ cudaError_t launch_lora_plan(const int *ids, const LoraPlan &p, int *words, cuda
                         p.adapters, words);
 }
 
-size_t lora_ws_bytes(int64_t tokens, int adapters, int r, int64_t k) {
+namespace {
+
+size_t partial_bytes(int64_t tokens, int adapters, int r, int64_t k) {
     const int rp = lora::padded(r);
     return static_cast<size_t>(lora::most_splits({nullptr, static_cast<int>(tokens), adapters}, static_cast<int>(k))) * tokens * rp *
            sizeof(float);
+}
+
+bool rows_aligned(const uint16_t *p, uint32_t ld) { return lora::aligned_to(p, 16) && ld % 8 == 0; }
+
+// Rows for the kernels that TMA feeds: as they are, or copied to `to` where that is
+// foreseen (odd strides of rows with a multiple of 8 columns are left to the kernels'
+// own copies).
+cudaError_t rows_for(const LoraPlan &plan, const uint16_t *&p, uint32_t &ld, int cols, uint8_t *to, int &packed, cudaStream_t stream) {
+    packed = !rows_aligned(p, ld) && cols % 8 != 0;
+    if (!packed) return cudaSuccess;
+    uint16_t *rows = reinterpret_cast<uint16_t *>(to);
+    const cudaError_t e = lora::launch_pack(plan, p, ld, cols, rows, stream);
+    p = rows;
+    ld = static_cast<uint32_t>(lora::ld_packed(cols));
+    return e;
+}
+
+}  // namespace
+
+size_t lora_ws_bytes(int64_t tokens, int adapters, int r, int64_t k) {
+    return partial_bytes(tokens, adapters, r, k) + lora::packed_bytes(tokens, k);
 }
 
 cudaError_t launch_lora_add(const LoraArgs &a, cudaStream_t stream) {
@@ -125,7 +148,9 @@ cudaError_t launch_lora_add(const LoraArgs &a, cudaStream_t stream) {
     s.out = a.ws;
     s.err = error_word();
     if (s.err == nullptr) return cudaErrorUnknown;
-    cudaError_t e = lora::launch_shrink(s, false, stream);
+    cudaError_t e = rows_for(a.plan, s.x, s.ld_x, a.w.k, reinterpret_cast<uint8_t *>(a.ws) + partial_bytes(a.plan.tokens, a.plan.adapters, a.w.r, a.w.k),
+                             s.packed, stream);
+    if (e == cudaSuccess) e = lora::launch_shrink(s, false, stream);
     if (e != cudaSuccess) return e;
     // Each CTA of a tile would add up its partial sums: left to them where there are
     // few tokens, one kernel more otherwise.
@@ -155,19 +180,22 @@ cudaError_t launch_lora_add(const LoraArgs &a, cudaStream_t stream) {
 namespace {
 
 // The backward pass's workspace: dv's partial sums and its sum, v and dv in
-// parts, the partial sums over the tokens.
+// parts, the partial sums over the tokens, copies of dy and x.
 struct Workspace {
-    size_t partial, sum, vt, total;
+    size_t partial, sum, vt, outer, dy, x, total;
     int chunks;
 };
 Workspace workspace_of(const LoraPlan &p, int r, int n, int k) {
     Workspace w;
     const size_t rows = static_cast<size_t>(p.tokens) * lora::padded(r) * sizeof(float);
-    w.partial = lora_ws_bytes(p.tokens, p.adapters, r, n);
+    w.partial = partial_bytes(p.tokens, p.adapters, r, n);
     w.sum = rows;
     w.vt = lora::outer_vt_bytes(p, r);
     w.chunks = lora::outer_chunks(p, n, k, r);
-    w.total = w.partial + w.sum + 2 * w.vt + 2 * static_cast<size_t>(w.chunks) * (static_cast<size_t>(n) + k) * lora::padded(r) * sizeof(float);
+    w.outer = 2 * static_cast<size_t>(w.chunks) * (static_cast<size_t>(n) + k) * lora::padded(r) * sizeof(float);
+    w.dy = lora::packed_bytes(p.tokens, n);
+    w.x = lora::packed_bytes(p.tokens, k);
+    w.total = w.partial + w.sum + 2 * w.vt + w.outer + w.dy + w.x;
     return w;
 }
 
@@ -183,13 +211,21 @@ cudaError_t launch_lora_add_bwd(const LoraBwdArgs &a, cudaStream_t stream) {
     float *partial = reinterpret_cast<float *>(at), *sum = reinterpret_cast<float *>(at + ws.partial);
     uint16_t *vt0 = reinterpret_cast<uint16_t *>(at + ws.partial + ws.sum), *vt1 = vt0 + ws.vt / sizeof(uint16_t);
     float *parts = reinterpret_cast<float *>(vt1 + ws.vt / sizeof(uint16_t));
+    uint8_t *copies = reinterpret_cast<uint8_t *>(parts) + ws.outer;
     cudaError_t e;
+    const uint16_t *dy = a.dy, *xr = a.x;
+    uint32_t ld_dy = a.ld_dy, ld_x = a.ld_x;
+    int packed_dy = 0, packed_x = 0;
+    e = rows_for(a.plan, dy, ld_dy, a.w.n, copies, packed_dy, stream);
+    if (e == cudaSuccess && a.da != nullptr) e = rows_for(a.plan, xr, ld_x, a.w.k, copies + ws.dy, packed_x, stream);
+    if (e != cudaSuccess) return e;
     const bool rows = a.dx != nullptr || a.da != nullptr, outer = a.da != nullptr || a.db != nullptr;
     if (rows) {
         lora::ShrinkArgs s{};
         s.plan = a.plan;
-        s.x = a.dy;
-        s.ld_x = a.ld_dy;
+        s.x = dy;
+        s.ld_x = ld_dy;
+        s.packed = packed_dy;
         s.w = a.w.b;
         s.stride_w = a.w.stride_b;
         s.ld_w = a.w.ld_b;
@@ -221,8 +257,8 @@ cudaError_t launch_lora_add_bwd(const LoraBwdArgs &a, cudaStream_t stream) {
         o.f32 = a.dw_f32;
         o.err = error_word();
         if (o.err == nullptr) return cudaErrorUnknown;
-        o.side[0] = {a.dy, a.ld_dy, a.w.n, 0, vt0, a.db, a.w.r, 1, static_cast<int64_t>(a.w.n) * a.w.r, parts};
-        o.side[1] = {a.x, a.ld_x, a.w.k, 0, vt1, a.da, 1, a.w.k, static_cast<int64_t>(a.w.k) * a.w.r, nullptr};
+        o.side[0] = {dy, ld_dy, a.w.n, 0, packed_dy, vt0, a.db, a.w.r, 1, static_cast<int64_t>(a.w.n) * a.w.r, parts};
+        o.side[1] = {xr, ld_x, a.w.k, 0, packed_x, vt1, a.da, 1, a.w.k, static_cast<int64_t>(a.w.k) * a.w.r, nullptr};
         o.side[1].ws = parts + 2 * static_cast<size_t>(ws.chunks) * a.w.n * lora::padded(a.w.r);
         o.chunks = ws.chunks;
         e = lora::launch_outer(o, stream);

@@ -115,12 +115,12 @@ __device__ __forceinline__ void split(float v, uint32_t (&h)[PARTS]) {
 __host__ __device__ constexpr int padded(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 inline bool aligned_to(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 // Sixteen rows of 64 columns, a warp's part of a step: offset of 16-byte piece p of
-// row r in a stage of the ring.  Copied a line (or two) of a row after the other, so
+// row r.  Copied a line (or two) of a row after the other, so
 // that no sector is asked for twice; read back by the four lanes of a row, two
 // rows at a time.
 template <int PIECES>
 __device__ __forceinline__ uint32_t slot(int r, int p) {
-    return (threadIdx.x / 32 * 16 + r) * (PIECES * 16) + (p ^ (r & 7)) * 16;
+    return r * (PIECES * 16) + (p ^ (r & 7)) * 16;
 }
 
 // A thread's share of the copies of the other operand's tiles, ROWS x COLS values
@@ -193,10 +193,21 @@ struct ShrinkArgs {
     uint32_t ld_w;
     LoraWeights lw;                  // ranks
     int k;                           // the long side
+    int packed;                      // x's rows are in the plan's order
     float *out;                      // [splits][tokens in the plan's order][padded(r)]
     unsigned int *err;               // the device's error word
 };
 cudaError_t launch_shrink(const ShrinkArgs &a, bool trans, cudaStream_t stream);
+
+// Rows that TMA does not take (of a number of columns that is no multiple of 8) are
+// copied once, in the plan's order, to rows of ld_packed values: read by three
+// kernels, they would be put together from 16-byte pieces by every one of them
+// (8192 x 8961 x 3583, r 16, backward: 857 us).
+__host__ __device__ constexpr int64_t ld_packed(int64_t cols) { return (cols + 63) / 64 * 64; }
+inline size_t packed_bytes(int64_t tokens, int64_t cols) {
+    return cols % 8 ? static_cast<size_t>(tokens) * ld_packed(cols) * sizeof(uint16_t) : 0;
+}
+cudaError_t launch_pack(const LoraPlan &plan, const uint16_t *from, uint32_t ld, int cols, uint16_t *to, cudaStream_t stream);
 
 struct SumArgs {
     LoraPlan plan;
@@ -231,6 +242,7 @@ struct OuterSide {
     const uint16_t *d;               // [tokens][n]
     uint32_t ld;
     int n, blocks;                   // columns, and blocks of them
+    int packed;                      // d's rows are in the plan's order
     const uint16_t *vt;              // by 64 tokens: [parts][padded(r)][64], swizzled
     void *out;                       // [adapters] of n x r: strides
     int64_t stride_n, stride_r, stride_g;

@@ -21,7 +21,7 @@ namespace {
 constexpr int kThreads = kLoraTile / 16 * 32;
 constexpr int kCols = 64;
 
-template <int RP, bool TRANS, bool F32>
+template <int RP, bool TRANS, bool F32, bool WIDE>
 struct Shape {
     static constexpr int KS = RP / 16;
     static constexpr int PARTS = F32 ? 3 : 2;
@@ -32,13 +32,16 @@ struct Shape {
     static constexpr int ROW = TRANS ? 2 * kCols + 16 : 2 * RP + 16;
     // 32 bytes more after every 16 rows: a fragment takes two of every sixteen
     static constexpr int W = TRANS ? RP * ROW : kCols * ROW + kCols / 16 * 32;
-    static constexpr int BASE = kLoraTile * PIECES * 16;
+    // rows at odd addresses: the aligned 16-byte granules that hold them, one more than
+    // they fill, 16 rows' last ones behind the others of a warp
+    static constexpr int WARP = 16 * PIECES * 16 + (WIDE ? 0 : 16 * 16);
+    static constexpr int BASE = kLoraTile / 16 * WARP;
     static constexpr int SMEM = STAGES * (W + BASE);
 };
 
 template <int RP, bool TRANS, bool F32, bool WIDE, bool WAL>
-__global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32>::CTAS) k_lora_expand(const ExpandArgs a) {
-    using S = Shape<RP, TRANS, F32>;
+__global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k_lora_expand(const ExpandArgs a) {
+    using S = Shape<RP, TRANS, F32, WIDE>;
     extern __shared__ __align__(128) uint8_t smem[];
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * a.n);
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
@@ -62,65 +65,52 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32>::CTAS) k_lora_
             const int m = warp * 16 + i * 8 + g;
             token[i] = m < tile.count ? a.plan.words[a.plan.order() + tile.first + m] : -1;
         }
-        // the rows that the lane copies
-        constexpr int E = F32 ? 4 : 8, ES = 16 / E;      // elements of a piece, their size
+        // the rows that the lane copies: a granule of each, and the last one of a row
+        constexpr int E = F32 ? 4 : 8, ES = 16 / E;      // elements of a granule, their size
         const int64_t n0 = static_cast<int64_t>(first) * kCols;
-        const uint8_t *row[16 / S::ROWS];
-        bool have[16 / S::ROWS];
+        constexpr int COPIES = 16 / S::ROWS + (WIDE ? 0 : 1);
+        const uint8_t *row[COPIES];
+        int ahead[COPIES];      // bytes from the granule to the first column
         const bool with_base = active && a.base != nullptr;
-        if constexpr (WIDE) {
 #pragma unroll
-            for (int i = 0; i < 16 / S::ROWS; ++i) {
-                const int m = warp * 16 + i * S::ROWS + lane / S::PIECES;
-                have[i] = m < tile.count && with_base;
-                row[i] = static_cast<const uint8_t *>(a.base);
-                if (have[i]) row[i] += (row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_base) + n0) * ES + lane % S::PIECES * 16;
+        for (int i = 0; i < COPIES; ++i) {
+            const bool last = i == 16 / S::ROWS;
+            const int m = warp * 16 + (last ? lane & 15 : i * S::ROWS + lane / S::PIECES);
+            row[i] = nullptr;
+            ahead[i] = 0;
+            if (m < tile.count && with_base && (!last || lane < 16)) {
+                const uintptr_t at = reinterpret_cast<uintptr_t>(a.base) +
+                                     (row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_base) + n0) * ES;
+                const int s = WIDE ? 0 : static_cast<int>(at & 15), p = last ? S::PIECES : lane % S::PIECES;
+                row[i] = reinterpret_cast<const uint8_t *>(at - s + p * 16);
+                ahead[i] = s - p * 16;
             }
         }
         TileCopy<TRANS ? RP : kCols, TRANS ? kCols : RP, S::ROW, !TRANS, WAL> wc(w + (TRANS ? n0 : n0 * a.ld_w), a.ld_w, TRANS ? rank : kCols,
                                                                                  TRANS ? kCols : rank);
         const int64_t wstep = TRANS ? kCols : static_cast<int64_t>(kCols) * a.ld_w;
         int in_stage = 0, left = static_cast<int>(a.n - n0);      // of the next copies
-        norm::Raw<F32> late[2];      // rows at odd addresses: from load to store
         auto load = [&]() {
             if (rank > 0) wc.copy(wbase + in_stage * S::W, a.w, TRANS ? RP : left, TRANS ? left : RP, wstep);
             if (with_base) {
-                if constexpr (WIDE) {
-                    const int n = max(0, min(16, ES * (left - lane % S::PIECES * E)));
+                const int bytes = ES * min(kCols, left);
 #pragma unroll
-                    for (int i = 0; i < 16 / S::ROWS; ++i) {
-                        ptx::cp_async16(ring + in_stage * S::BASE + slot<S::PIECES>(i * S::ROWS + lane / S::PIECES, lane % S::PIECES),
-                                        have[i] && n > 0 ? row[i] : static_cast<const uint8_t *>(a.base), have[i] ? n : 0);
-                        row[i] += kCols * ES;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int n = token[i] < 0 ? 0 : left - 16 * t;
-                        if (n > 0) late[i].template load<false>(a.base, row_at(token[i], a.ld_base) + a.n - left + 16 * t, n);
-                        else late[i].zero();
-                    }
+                for (int i = 0; i < COPIES; ++i) {
+                    const bool last = i == 16 / S::ROWS;
+                    // a granule is read whole if a byte of it belongs to the row
+                    const int have = row[i] == nullptr ? 0 : bytes + ahead[i], n = WIDE ? max(0, min(16, have)) : have > 0 ? 16 : 0;
+                    const uint32_t to = ring + in_stage * S::BASE + warp * S::WARP +
+                                        (last ? 16 * S::PIECES * 16 + lane * 16
+                                              : slot<S::PIECES>(i * S::ROWS + lane / S::PIECES, lane % S::PIECES));
+                    if (!last || lane < 16) ptx::cp_async16(to, n > 0 ? row[i] : norm::base_granule(a.base), n);
+                    row[i] = row[i] == nullptr ? nullptr : row[i] + kCols * ES;
                 }
             }
             left -= kCols;
-        };
-        auto store_late = [&]() {
-            if (!WIDE && with_base) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int p = 0; p < S::PIECES / 4; ++p) {
-                        const uint32_t *v = late[i].w + 4 * p;
-                        ptx::st_shared_v4(ring + in_stage * S::BASE + slot<S::PIECES>(i * 8 + g, t * (S::PIECES / 4) + p), v[0], v[1], v[2], v[3]);
-                    }
-            }
             in_stage = in_stage + 1 == S::STAGES ? 0 : in_stage + 1;
         };
         for (int s = 0; s < S::STAGES - 1; ++s) {
-            if (s < steps) {
-                load();
-                store_late();
-            }
+            if (s < steps) load();
             ptx::cp_async_commit();
         }
 
@@ -179,8 +169,12 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32>::CTAS) k_lora_
         const uint32_t wlane = wbase + (TRANS ? 2 * t * S::ROW + 32 * (g >> 1)
                                               : (16 * (wi >> 1) + 2 * (lane >> 4) + (wi & 1)) * S::ROW + (wi >> 1) * 32 + ((lane >> 3) & 1) * 16);
         int64_t yat[2];
+        uint32_t shift[2];      // of the lane's rows of base within their granules
 #pragma unroll
-        for (int i = 0; i < 2; ++i) yat[i] = token[i] >= 0 ? row_at(token[i], a.ld_y) + n0 + 16 * t : 0;
+        for (int i = 0; i < 2; ++i) {
+            yat[i] = token[i] >= 0 ? row_at(token[i], a.ld_y) + n0 + 16 * t : 0;
+            shift[i] = static_cast<uint32_t>(norm::column_address<F32>(a.base, token[i] >= 0 ? row_at(token[i], a.ld_base) : 0)) & 15u;
+        }
         int stage = 0, out_left = static_cast<int>(a.n - n0) - 16 * t;
         for (int s = 0; s < steps; ++s) {
             ptx::cp_async_wait<S::STAGES - 2>();
@@ -196,10 +190,19 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32>::CTAS) k_lora_
                 for (int i = 0; i < 2; ++i) {
                     in[i].zero();
                     if (with_base) {
+                        const uint32_t from = ring + stage * S::BASE + warp * S::WARP;
+                        constexpr int N = S::PIECES / 4;
+                        uint32_t u[4 * (N + 1)];
 #pragma unroll
-                        for (int h = 0; h < S::PIECES / 4; ++h)
-                            ptx::ld_shared_v4(ring + stage * S::BASE + slot<S::PIECES>(i * 8 + g, t * (S::PIECES / 4) + h), in[i].w[4 * h],
-                                              in[i].w[4 * h + 1], in[i].w[4 * h + 2], in[i].w[4 * h + 3]);
+                        for (int h = 0; h < N + (WIDE ? 0 : 1); ++h) {
+                            const int p = t * N + h;
+                            const uint32_t at = p < S::PIECES ? slot<S::PIECES>(i * 8 + g, p) : 16 * S::PIECES * 16 + (i * 8 + g) * 16;
+                            ptx::ld_shared_v4(from + at, u[4 * h], u[4 * h + 1], u[4 * h + 2], u[4 * h + 3]);
+                        }
+                        if constexpr (!WIDE && F32) ragged::shift_words(u, shift[i] >> 2);
+                        else if constexpr (!WIDE) ragged::shift_down(u, shift[i]);
+#pragma unroll
+                        for (int h = 0; h < 4 * N; ++h) in[i].w[h] = u[h];
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -253,7 +256,6 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32>::CTAS) k_lora_
                 }
                 out_left -= kCols;
             }
-            if (more) store_late();
             stage = stage + 1 == S::STAGES ? 0 : stage + 1;
         }
         ptx::cp_async_wait<0>();
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32>::CTAS) k_lora_
 
 template <int RP, bool TRANS, bool F32, bool WIDE, bool WAL>
 cudaError_t run(const ExpandArgs &a, cudaStream_t stream) {
-    using S = Shape<RP, TRANS, F32>;
+    using S = Shape<RP, TRANS, F32, WIDE>;
     static unsigned long long done;
     auto *kern = &k_lora_expand<RP, TRANS, F32, WIDE, WAL>;
     const cudaError_t e = with_smem(kern, S::SMEM, S::SMEM, done);

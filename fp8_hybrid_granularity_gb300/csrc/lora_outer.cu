@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this step's tokens, a lane each; the next step's are asked for meanwhile
         auto look_up = [&](const Tile &tile, int h) {
             const int m = h * kStep + warp * (kStep / kCopyWarps) + lane;
-            return lane < kStep / kCopyWarps && m < tile.count ? order[tile.first + m] : -1;
+            return lane < kStep / kCopyWarps && m < tile.count ? (o.packed ? tile.first + m : order[tile.first + m]) : -1;
         };
         Tile tile = tile_at(a.plan, t0), next = tile_at(a.plan, min(t0 + 1, t1 - 1));
         int token = look_up(tile, 0), stage = 0, lag_stage = 0, it = 0, h = 0;
@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int LAG = WIDE ? S::STAGES - 2 : 0;
         for (int t = t0; t < t1 && ok; ++it) {
             const int now = token, t_now = t, h_now = h;
-            const int together = WIDE && tile.row >= 0 && h * kStep + kStep <= tile.count ? tile.row + h * kStep : -1;
+            const int near = o.packed ? tile.first : tile.row;
+            const int together = WIDE && near >= 0 && h * kStep + kStep <= tile.count ? near + h * kStep : -1;
             h += 1;
             if (h * kStep >= tile.count) {
                 h = 0;

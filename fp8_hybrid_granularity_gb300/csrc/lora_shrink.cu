@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     using S = Shape<RP, TRANS>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * a.k);
-    const Tile tile = tile_at(a.plan, blockIdx.x);      // its place is there, if it is a tile or not
+    Tile tile = tile_at(a.plan, blockIdx.x);      // its place is there, if it is a tile or not
+    if (a.packed) tile.row = tile.first;
     const int tiles = adapter_tiles(a.plan), splits = shrink_splits(tiles, a.k);
     if (static_cast<int>(blockIdx.x) >= tiles || static_cast<int>(blockIdx.y) >= splits) return;
     const int all = (a.k + kCols - 1) / kCols, per = (all + splits - 1) / splits;
@@ -318,6 +319,32 @@ __global__ void __launch_bounds__(256) k_lora_sum(const SumArgs a, int rp) {
 }
 
 }  // namespace
+
+namespace {
+
+// A warp 512 columns of a row at a time.
+__global__ void __launch_bounds__(256) k_lora_pack(LoraPlan plan, const uint16_t *from, uint32_t ld, int cols, uint16_t *to, uint32_t ld_to) {
+    ptx::grid_begin(static_cast<int64_t>(plan.tokens) * cols);
+    const int lane = threadIdx.x & 31, chunks = (cols + 511) / 512, rows = plan.words[plan.starts() + plan.adapters];
+    const int64_t all = static_cast<int64_t>(rows) * chunks, step = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t i = blockIdx.x * 8 + threadIdx.x / 32; i < all; i += step) {
+        const int row = static_cast<int>(i / chunks), c = static_cast<int>(i % chunks) * 512 + lane * 16;
+        if (c >= cols) continue;
+        uint32_t v[8];
+        ragged::load16<false>(from + row_at(plan.words[plan.order() + row], ld) + c, cols - c, v);
+        uint4 *p = reinterpret_cast<uint4 *>(to + row_at(row, ld_to) + c);
+        p[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        p[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_pack(const LoraPlan &plan, const uint16_t *from, uint32_t ld, int cols, uint16_t *to, cudaStream_t stream) {
+    const int64_t all = static_cast<int64_t>(plan.tokens) * ((cols + 511) / 512);
+    return launch_after(&k_lora_pack, dim3(static_cast<unsigned>(std::min<int64_t>((all + 7) / 8, 8 * kSms))), 256, 0, stream, 1, plan, from, ld, cols,
+                        to, static_cast<uint32_t>(ld_packed(cols)));
+}
 
 cudaError_t launch_sum(const SumArgs &a, cudaStream_t stream) {
     return launch_after(&k_lora_sum, dim3(a.plan.max_tiles(), kLoraTile / 32), 256, 0, stream, 1, a, padded(a.lw.r));

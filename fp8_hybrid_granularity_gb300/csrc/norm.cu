@@ -155,12 +155,12 @@ __global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr, int q_k
     }
 }
 
-// Many rows of up to 4096 columns that begin at multiples of 32 bytes: R at a time,
-// through shared memory, the next ones' copies in flight.
-constexpr int kRingCols = 4096;
-template <bool XF32, int R>
-__global__ void __launch_bounds__(256, 2) k_norm_ring(const NormArgs a, int tpr, int q_kind) {
-    constexpr int X = XF32 ? 2048 : 1024, STAGES = 2;     // bytes of a warp's columns
+// Many rows of up to 8192 columns: R at a time, through shared memory, the next ones'
+// copies in flight.
+constexpr int kRingCols = 8192;
+template <bool XF32, bool WIDE, int R>
+__global__ void __launch_bounds__(512) k_norm_ring(const NormArgs a, int tpr, int q_kind) {
+    constexpr int X = kSegment<XF32, WIDE>, STAGES = 2;     // bytes of a warp's columns
     extern __shared__ float4 params[];    // w, b, the rings
     __shared__ float red[2][32][4];
     ptx::grid_begin(static_cast<int64_t>(a.rows) * a.cols);
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(256, 2) k_norm_ring(const NormArgs a, int tpr,
     auto copy = [&](uint32_t r, int stage) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            copy_columns<XF32>(ring + (stage * R + i) * warps * X, a.x, row_at(r + i, a.ld_x) + w0, r + i < rows ? a.cols - w0 : 0);
+            copy_columns<XF32, WIDE>(ring + (stage * R + i) * warps * X, a.x, row_at(r + i, a.ld_x) + w0, r + i < rows ? a.cols - w0 : 0);
         ptx::cp_async_commit();
     };
     uint32_t r = blockIdx.x * rpb + group * R;
@@ -190,14 +190,15 @@ __global__ void __launch_bounds__(256, 2) k_norm_ring(const NormArgs a, int tpr,
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             Raw<XF32> x;
-            read_columns(ring + (stage * R + i) * warps * X, x);
+            read_columns<XF32, WIDE>(ring + (stage * R + i) * warps * X, column_address<XF32>(a.x, row_at(r + i, a.ld_x)) & 15,
+                                     r + i < rows ? a.cols - t * 16 : 0, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[i][j] = x.pair(j);
         }
         __syncwarp();
         copy(r + STAGES * step, stage);
         stage ^= 1;
-        finish<true>(a, q_kind, r, t, tpr, inv_n, row, w, b, d, mean, rstd);
+        finish<WIDE>(a, q_kind, r, t, tpr, inv_n, row, w, b, d, mean, rstd);
     }
     ptx::cp_async_wait<0>();
 }
@@ -278,14 +279,14 @@ cudaError_t run(const NormArgs &a, int q_kind, cudaStream_t stream) {
     const Shape s = shape_of(a.cols);
     const int threads = s.tpr * s.rpb;
     const size_t params = 2 * 16 * sizeof(float) * s.tpr;
-    if (WIDE && a.cols <= kRingCols && a.rows >= 4 * s.rpb * kSms) {
-        constexpr int R = XF32 ? 1 : 4, kWarpBytes = 2 * R * (XF32 ? 2048 : 1024);
+    if (a.cols <= kRingCols && a.rows >= 4 * s.rpb * kSms) {
+        constexpr int R = XF32 ? 1 : WIDE ? 4 : 2, kWarpBytes = 2 * R * kSegment<XF32, WIDE>;
         static unsigned long long done;
         const size_t smem = params + kWarpBytes * (threads / 32);
-        const cudaError_t e = with_smem(&k_norm_ring<XF32, R>, smem, 32 * 1024 + kWarpBytes * 8, done);
+        const cudaError_t e = with_smem(&k_norm_ring<XF32, WIDE, R>, smem, 64 * 1024 + kWarpBytes * 16, done);
         if (e != cudaSuccess) return e;
         const int sets = (a.rows + s.rpb * R - 1) / (s.rpb * R);
-        return launch_after(&k_norm_ring<XF32, R>, dim3(std::min(sets, 2 * kSms)), threads, smem, stream, 1, a, s.tpr, q_kind);
+        return launch_after(&k_norm_ring<XF32, WIDE, R>, dim3(std::min(sets, kSms * std::max(1, 512 / threads))), threads, smem, stream, 1, a, s.tpr, q_kind);
     }
     static unsigned long long done;
     const cudaError_t e = with_smem(&k_norm<XF32, WIDE>, params, 2 * 16 * sizeof(float) * 512, done);

@@ -192,25 +192,60 @@ __device__ __forceinline__ void kept_params(const float *at, int t, int tpr, int
 }
 
 // A warp's 512 columns of a row through shared memory: copied 16 bytes a lane next
-// to one another (no sector is asked for twice), read back 16 columns a lane.
+// to one another (no sector is asked for twice), read back 16 columns a lane.  WIDE:
+// rows that begin at multiples of 16 bytes; others come as the aligned 16-byte
+// granules that hold them, one more than they fill, and are moved into place when
+// they are read.
+template <bool F32, bool WIDE>
+constexpr int kSegment = (F32 ? 2048 : 1024) + (WIDE ? 0 : 16);
+__device__ __forceinline__ uint32_t segment_at(int p) { return (p ^ ((p >> 3) & 3)) * 16; }
+__device__ __forceinline__ const void *base_granule(const void *p) {
+    return reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(15));
+}
 template <bool F32>
+__device__ __forceinline__ uintptr_t column_address(const void *base, int64_t at) {
+    return reinterpret_cast<uintptr_t>(base) + at * (F32 ? 4 : 2);
+}
+
+template <bool F32, bool WIDE>
 __device__ __forceinline__ void copy_columns(uint32_t to, const void *base, int64_t at, int left) {
     constexpr int E = F32 ? 4 : 2;
     const int lane = threadIdx.x & 31, bytes = max(0, min(512, left)) * E;
+    const uintptr_t a = column_address<F32>(base, at), from = a & ~static_cast<uintptr_t>(15);
+    const int have = bytes > 0 ? bytes + static_cast<int>(a & 15) : 0;      // of the granules
+    auto piece = [&](int p) {
+        // a granule is read whole if a byte of it belongs to the row
+        const int n = WIDE ? max(0, min(16, have - 16 * p)) : have > 16 * p ? 16 : 0;
+        ptx::cp_async16(to + segment_at(p), n > 0 ? reinterpret_cast<const void *>(from + 16 * p) : base_granule(base), n);
+    };
 #pragma unroll
-    for (int h = 0; h < E; ++h) {
-        const int p = h * 32 + lane, n = max(0, min(16, bytes - 16 * p));
-        ptx::cp_async16(to + (p ^ ((p >> 3) & 3)) * 16,
-                        static_cast<const uint8_t *>(base) + (n > 0 ? at * E + 16 * p : 0), n);
-    }
+    for (int h = 0; h < E; ++h) piece(h * 32 + lane);
+    if (!WIDE && lane == 0) piece(32 * E);
 }
-template <bool F32>
-__device__ __forceinline__ void read_columns(uint32_t from, Raw<F32> &v) {
+template <bool F32, bool WIDE>
+__device__ __forceinline__ void read_columns(uint32_t from, uint32_t shift, int left, Raw<F32> &v) {
     constexpr int N = F32 ? 4 : 2;
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int h = 0; h < N; ++h) {
-        const int p = (threadIdx.x & 31) * N + h;
-        ptx::ld_shared_v4(from + (p ^ ((p >> 3) & 3)) * 16, v.w[4 * h], v.w[4 * h + 1], v.w[4 * h + 2], v.w[4 * h + 3]);
+        for (int h = 0; h < N; ++h)
+            ptx::ld_shared_v4(from + segment_at((threadIdx.x & 31) * N + h), v.w[4 * h], v.w[4 * h + 1], v.w[4 * h + 2], v.w[4 * h + 3]);
+    } else {
+        uint32_t w[4 * (N + 1)];
+#pragma unroll
+        for (int h = 0; h <= N; ++h)
+            ptx::ld_shared_v4(from + segment_at((threadIdx.x & 31) * N + h), w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+        if constexpr (F32) ragged::shift_words(w, shift >> 2);
+        else ragged::shift_down(w, shift);
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i) v.w[i] = w[i];
+        // the last granule also holds what is behind the row
+        if (left < 16) {
+#pragma unroll
+            for (int i = 0; i < 4 * N; ++i) {
+                if (F32) v.w[i] = i < left ? v.w[i] : 0u;
+                else v.w[i] = 2 * i + 1 < left ? v.w[i] : 2 * i < left ? v.w[i] & 0xFFFFu : 0u;
+            }
+        }
     }
 }
 

@@ -121,21 +121,20 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormBwdArgs a, int tpr) 
     for (int c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) part[c] = w[c];
 }
 
-// The same for rows of up to 4096 columns that begin at multiples of 32 bytes: R
-// rows at a time (their sums share a barrier), which come through shared memory,
-// STAGES - 1 sets of rows ahead.
+// The same for rows of up to 4096 columns: R at a time (their sums share a barrier),
+// which come through shared memory, STAGES - 1 sets of rows ahead.
 constexpr int kRingCols = 4096;
-template <bool XF32, bool DF32>
+template <bool XF32, bool DF32, bool WIDE>
 struct Ring {
-    static constexpr int R = XF32 || DF32 ? 1 : 2;
+    static constexpr int R = XF32 || DF32 || !WIDE ? 1 : 2;
     static constexpr int STAGES = R == 1 ? 3 : 2;
-    static constexpr int X = XF32 ? 2048 : 1024, D = DF32 ? 2048 : 1024;     // bytes of a warp's columns
+    static constexpr int X = kSegment<XF32, WIDE>, D = kSegment<DF32, WIDE>;     // bytes of a warp's columns
     static constexpr int bytes(int warps, bool add) { return STAGES * R * (X + D + (add ? X : 0)) * warps; }
 };
 
-template <bool XF32, bool DF32>
+template <bool XF32, bool DF32, bool WIDE>
 __global__ void __launch_bounds__(256, 2) k_norm_bwd_ring(const NormBwdArgs a, int tpr) {
-    using S = Ring<XF32, DF32>;
+    using S = Ring<XF32, DF32, WIDE>;
     constexpr int R = S::R;
     extern __shared__ float4 shared[];     // the rings, w; after the last row the sums, [2][cols], of several rows at a time
     __shared__ float red[2][32][4];
@@ -155,9 +154,9 @@ __global__ void __launch_bounds__(256, 2) k_norm_bwd_ring(const NormBwdArgs a, i
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int left = r + i < rows ? a.cols - w0 : 0;
-            copy_columns<XF32>(slot(stage, i), a.x, row_at(r + i, a.ld_x) + w0, left);
-            copy_columns<DF32>(slot(stage, i) + S::X, a.dy, row_at(r + i, a.ld_dy) + w0, left);
-            if (with_add) copy_columns<XF32>(slot(stage, i) + S::X + S::D, a.add, row_at(r + i, a.ld_add) + w0, left);
+            copy_columns<XF32, WIDE>(slot(stage, i), a.x, row_at(r + i, a.ld_x) + w0, left);
+            copy_columns<DF32, WIDE>(slot(stage, i) + S::X, a.dy, row_at(r + i, a.ld_dy) + w0, left);
+            if (with_add) copy_columns<XF32, WIDE>(slot(stage, i) + S::X + S::D, a.add, row_at(r + i, a.ld_add) + w0, left);
         }
         ptx::cp_async_commit();
     };
@@ -187,8 +186,9 @@ __global__ void __launch_bounds__(256, 2) k_norm_bwd_ring(const NormBwdArgs a, i
         float sums[2 * R], mean[R], rstd[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            read_columns(slot(stage, i), x[i]);
-            read_columns(slot(stage, i) + S::X, dy[i]);
+            const int here = r + i < rows ? cols_left : 0;
+            read_columns<XF32, WIDE>(slot(stage, i), column_address<XF32>(a.x, row_at(r + i, a.ld_x)) & 15, here, x[i]);
+            read_columns<DF32, WIDE>(slot(stage, i) + S::X, column_address<DF32>(a.dy, row_at(r + i, a.ld_dy)) & 15, here, dy[i]);
             mean[i] = st[0][i].x, rstd[i] = st[0][i].y;
         }
 #pragma unroll
@@ -224,7 +224,8 @@ __global__ void __launch_bounds__(256, 2) k_norm_bwd_ring(const NormBwdArgs a, i
             const F2 mg = f2(-sums[2 * i] * inv_n), mgx = f2(-sums[2 * i + 1] * inv_n), rs = f2(rstd[i]);
             Raw<XF32> add;
             add.zero();
-            if (with_add) read_columns(slot(stage, i) + S::X + S::D, add);
+            if (with_add)
+                read_columns<XF32, WIDE>(slot(stage, i) + S::X + S::D, column_address<XF32>(a.add, row_at(r + i, a.ld_add)) & 15, cols_left, add);
             F2 dx[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(256, 2) k_norm_bwd_ring(const NormBwdArgs a, i
                     dx[2 * j + e] = fma2(rs, fma2(xh, mgx, add2(g, mg)), add.pair(2 * j + e));
                 }
             }
-            store_values<true>(a.dx, XF32, row_at(r + i, a.ld_dx) + c0, r + i < rows ? cols_left : 0, dx);
+            store_values<WIDE>(a.dx, XF32, row_at(r + i, a.ld_dx) + c0, r + i < rows ? cols_left : 0, dx);
         }
         __syncwarp();
         copy(r + S::STAGES * step, stage);
@@ -384,6 +385,16 @@ int norm_parts(int64_t rows, int64_t cols) {
     return static_cast<int>(std::min<int64_t>((rows + s.rpb - 1) / s.rpb, kSms * std::max(1, 512 / (s.tpr * s.rpb))));
 }
 
+template <bool XF32, bool DF32, bool WIDE>
+cudaError_t run_ring(const NormBwdArgs &a, const Shape &s, int parts, size_t rest, cudaStream_t stream) {
+    using G = Ring<XF32, DF32, WIDE>;
+    static unsigned long long done;
+    const size_t smem = rest + G::bytes(s.tpr * s.rpb / 32, a.add != nullptr);
+    const cudaError_t e = with_smem(&k_norm_bwd_ring<XF32, DF32, WIDE>, smem, G::bytes(8, true) + 16 * 1024, done);
+    if (e != cudaSuccess) return e;
+    return launch_after(&k_norm_bwd_ring<XF32, DF32, WIDE>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr);
+}
+
 template <bool XF32, bool DF32>
 cudaError_t run(const NormBwdArgs &a, cudaStream_t stream) {
     const int parts = norm_parts(a.rows, a.cols);
@@ -397,13 +408,8 @@ cudaError_t run(const NormBwdArgs &a, cudaStream_t stream) {
         const bool wide = wide_rows(a.x, a.x_f32, a.ld_x) && wide_rows(a.dy, a.dy_f32, a.ld_dy) &&
                           wide_rows(a.dx, a.x_f32, a.ld_dx) && (a.add == nullptr || wide_rows(a.add, a.x_f32, a.ld_add));
         const size_t smem = (s.rpb > 1 ? 2 : 1) * 16 * sizeof(float) * s.tpr;   // at most 32 KB
-        if (wide && a.cols <= kRingCols) {
-            using G = Ring<XF32, DF32>;
-            static unsigned long long done;
-            const size_t rings = G::bytes(s.tpr * s.rpb / 32, a.add != nullptr);
-            e = with_smem(&k_norm_bwd_ring<XF32, DF32>, smem + rings, G::bytes(8, true) + 16 * 1024, done);
-            if (e == cudaSuccess)
-                e = launch_after(&k_norm_bwd_ring<XF32, DF32>, dim3(parts), s.tpr * s.rpb, smem + rings, stream, 1, a, s.tpr);
+        if (a.cols <= kRingCols) {
+            e = wide ? run_ring<XF32, DF32, true>(a, s, parts, smem, stream) : run_ring<XF32, DF32, false>(a, s, parts, smem, stream);
         } else {
             e = wide ? launch_after(&k_norm_bwd<XF32, DF32, true>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr)
                      : launch_after(&k_norm_bwd<XF32, DF32, false>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr);

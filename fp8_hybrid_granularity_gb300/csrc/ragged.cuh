@@ -122,6 +122,18 @@ __device__ __forceinline__ void store16(uint16_t *p, int left, const uint32_t (&
     }
 }
 
+// Words of an 80-byte window moved down by s words (s below 4): the first 16 are wanted.
+__device__ __forceinline__ void shift_words(uint32_t (&w)[20], uint32_t s) {
+    if (s & 2) {
+#pragma unroll
+        for (int i = 0; i < 18; ++i) w[i] = w[i + 2];
+    }
+    if (s & 1) {
+#pragma unroll
+        for (int i = 0; i < 17; ++i) w[i] = w[i + 1];
+    }
+}
+
 // Sixteen neighbouring FP32 values per thread, by the same rules: WIDE rows in
 // 32-byte accesses, others (a multiple of 4 bytes) in aligned 16-byte granules.
 template <bool WIDE>
@@ -147,14 +159,7 @@ __device__ __forceinline__ void load16(const float *p, int left, uint32_t (&v)[1
         if (s + words > 4u * i) q = ptx::ld_v4(g + i);
         w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
-    if (s & 2) {
-#pragma unroll
-        for (int i = 0; i < 18; ++i) w[i] = w[i + 2];
-    }
-    if (s & 1) {
-#pragma unroll
-        for (int i = 0; i < 17; ++i) w[i] = w[i + 1];
-    }
+    shift_words(w, s);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = i < words ? w[i] : 0u;
 }
@@ -200,14 +205,7 @@ __device__ __forceinline__ void store16(float *p, int left, const uint32_t (&v)[
             for (int i = 13; i < 16; ++i)
                 if (i >= d + 12) p[i] = __uint_as_float(w[i]);
         }
-        if (d & 2) {
-#pragma unroll
-            for (int i = 0; i < 18; ++i) w[i] = w[i + 2];
-        }
-        if (d & 1) {
-#pragma unroll
-            for (int i = 0; i < 17; ++i) w[i] = w[i + 1];
-        }
+        shift_words(w, d);
         uint4 *g = reinterpret_cast<uint4 *>(a + 4 * d);
 #pragma unroll
         for (int i = 0; i < 3; ++i) g[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
