@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
         constexpr int COPIES = 16 / S::ROWS + (WIDE ? 0 : 1);
         const uint8_t *row[COPIES];
         int ahead[COPIES];      // bytes from the granule to the first column
+        bool in[COPIES];
         const bool with_base = active && a.base != nullptr;
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
@@ -78,12 +79,14 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
             const int m = warp * 16 + (last ? lane & 15 : i * S::ROWS + lane / S::PIECES);
             row[i] = nullptr;
             ahead[i] = 0;
+            in[i] = false;
             if (m < tile.count && with_base && (!last || lane < 16)) {
                 const uintptr_t at = reinterpret_cast<uintptr_t>(a.base) +
                                      (row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_base) + n0) * ES;
                 const int s = WIDE ? 0 : static_cast<int>(at & 15), p = last ? S::PIECES : lane % S::PIECES;
                 row[i] = reinterpret_cast<const uint8_t *>(at - s + p * 16);
                 ahead[i] = s - p * 16;
+                in[i] = true;
             }
         }
         TileCopy<TRANS ? RP : kCols, TRANS ? kCols : RP, S::ROW, !TRANS, WAL> wc(w + (TRANS ? n0 : n0 * a.ld_w), a.ld_w, TRANS ? rank : kCols,
@@ -98,12 +101,13 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
                 for (int i = 0; i < COPIES; ++i) {
                     const bool last = i == 16 / S::ROWS;
                     // a granule is read whole if a byte of it belongs to the row
-                    const int have = row[i] == nullptr ? 0 : bytes + ahead[i], n = WIDE ? max(0, min(16, have)) : have > 0 ? 16 : 0;
+                    const int have = !in[i] ? 0 : WIDE ? bytes - lane % S::PIECES * 16 : bytes + ahead[i];
+                    const int n = WIDE ? max(0, min(16, have)) : have > 0 ? 16 : 0;
                     const uint32_t to = ring + in_stage * S::BASE + warp * S::WARP +
                                         (last ? 16 * S::PIECES * 16 + lane * 16
                                               : slot<S::PIECES>(i * S::ROWS + lane / S::PIECES, lane % S::PIECES));
                     if (!last || lane < 16) ptx::cp_async16(to, n > 0 ? row[i] : norm::base_granule(a.base), n);
-                    row[i] = row[i] == nullptr ? nullptr : row[i] + kCols * ES;
+                    row[i] += kCols * ES;
                 }
             }
             left -= kCols;
@@ -184,11 +188,11 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
             ptx::cp_async_commit();
             if (active) {
                 const uint32_t wat = wlane + stage * S::W;
-                norm::Raw<F32> in[2];
+                norm::Raw<F32> old[2];
                 float acc[8][4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    in[i].zero();
+                    old[i].zero();
                     if (with_base) {
                         const uint32_t from = ring + stage * S::BASE + warp * S::WARP;
                         constexpr int N = S::PIECES / 4;
@@ -202,11 +206,11 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
                         if constexpr (!WIDE && F32) ragged::shift_words(u, shift[i] >> 2);
                         else if constexpr (!WIDE) ragged::shift_down(u, shift[i]);
 #pragma unroll
-                        for (int h = 0; h < 4 * N; ++h) in[i].w[h] = u[h];
+                        for (int h = 0; h < 4 * N; ++h) old[i].w[h] = u[h];
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const F2 p = in[i].pair(j);
+                        const F2 p = old[i].pair(j);
                         acc[j][2 * i] = F32 ? 0.0f : p.lo();
                         acc[j][2 * i + 1] = F32 ? 0.0f : p.hi();
                     }
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         out[j] = f2(acc[j][2 * i], acc[j][2 * i + 1]);
-                        if constexpr (F32) out[j] = add2(in[i].pair(j), out[j]);
+                        if constexpr (F32) out[j] = add2(old[i].pair(j), out[j]);
                     }
                     norm::store_values<WIDE>(a.y, F32, yat[i], token[i] >= 0 ? out_left : 0, out);
                     yat[i] += kCols;

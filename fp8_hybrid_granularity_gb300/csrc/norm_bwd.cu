@@ -121,20 +121,19 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormBwdArgs a, int tpr) 
     for (int c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) part[c] = w[c];
 }
 
-// The same for rows of up to 4096 columns: R at a time (their sums share a barrier),
-// which come through shared memory, STAGES - 1 sets of rows ahead.
-constexpr int kRingCols = 4096;
-template <bool XF32, bool DF32, bool WIDE>
+// The same with rows that come through shared memory, STAGES - 1 sets of R ahead (the
+// sums of a set share a barrier).
+template <bool XF32, bool DF32, bool WIDE, int THREADS>
 struct Ring {
-    static constexpr int R = XF32 || DF32 || !WIDE ? 1 : 2;
-    static constexpr int STAGES = R == 1 ? 3 : 2;
+    static constexpr int R = XF32 || DF32 || !WIDE || THREADS > 256 ? 1 : 2;
+    static constexpr int STAGES = R == 1 && (THREADS == 256 || !(XF32 || DF32)) ? 3 : 2;
     static constexpr int X = kSegment<XF32, WIDE>, D = kSegment<DF32, WIDE>;     // bytes of a warp's columns
     static constexpr int bytes(int warps, bool add) { return STAGES * R * (X + D + (add ? X : 0)) * warps; }
 };
 
-template <bool XF32, bool DF32, bool WIDE>
-__global__ void __launch_bounds__(256, 2) k_norm_bwd_ring(const NormBwdArgs a, int tpr) {
-    using S = Ring<XF32, DF32, WIDE>;
+template <bool XF32, bool DF32, bool WIDE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) k_norm_bwd_ring(const NormBwdArgs a, int tpr) {
+    using S = Ring<XF32, DF32, WIDE, THREADS>;
     constexpr int R = S::R;
     extern __shared__ float4 shared[];     // the rings, w; after the last row the sums, [2][cols], of several rows at a time
     __shared__ float red[2][32][4];
@@ -385,14 +384,26 @@ int norm_parts(int64_t rows, int64_t cols) {
     return static_cast<int>(std::min<int64_t>((rows + s.rpb - 1) / s.rpb, kSms * std::max(1, 512 / (s.tpr * s.rpb))));
 }
 
-template <bool XF32, bool DF32, bool WIDE>
-cudaError_t run_ring(const NormBwdArgs &a, const Shape &s, int parts, size_t rest, cudaStream_t stream) {
-    using G = Ring<XF32, DF32, WIDE>;
+constexpr size_t kMostSmem = 226 * 1024;
+template <bool XF32, bool DF32, bool WIDE, int THREADS>
+cudaError_t run_ring(const NormBwdArgs &a, const Shape &s, int parts, size_t smem, cudaStream_t stream) {
     static unsigned long long done;
-    const size_t smem = rest + G::bytes(s.tpr * s.rpb / 32, a.add != nullptr);
-    const cudaError_t e = with_smem(&k_norm_bwd_ring<XF32, DF32, WIDE>, smem, G::bytes(8, true) + 16 * 1024, done);
+    auto *kern = &k_norm_bwd_ring<XF32, DF32, WIDE, THREADS>;
+    const cudaError_t e = with_smem(kern, smem, kMostSmem, done);
     if (e != cudaSuccess) return e;
-    return launch_after(&k_norm_bwd_ring<XF32, DF32, WIDE>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr);
+    return launch_after(kern, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr);
+}
+// Through shared memory where it holds the rows (all in FP32, with another gradient to
+// add, it does not from 6000 columns on).
+template <bool XF32, bool DF32, bool WIDE>
+cudaError_t run_rows(const NormBwdArgs &a, const Shape &s, int parts, cudaStream_t stream) {
+    const int threads = s.tpr * s.rpb, warps = threads / 32;
+    const size_t rest = (s.rpb > 1 ? 2 : 1) * 16 * sizeof(float) * s.tpr;   // at most 32 KB
+    const size_t rings = threads <= 256 ? Ring<XF32, DF32, WIDE, 256>::bytes(warps, a.add != nullptr)
+                                        : Ring<XF32, DF32, WIDE, 512>::bytes(warps, a.add != nullptr);
+    if (rest + rings > kMostSmem) return launch_after(&k_norm_bwd<XF32, DF32, WIDE>, dim3(parts), threads, rest, stream, 1, a, s.tpr);
+    return threads <= 256 ? run_ring<XF32, DF32, WIDE, 256>(a, s, parts, rest + rings, stream)
+                          : run_ring<XF32, DF32, WIDE, 512>(a, s, parts, rest + rings, stream);
 }
 
 template <bool XF32, bool DF32>
@@ -407,13 +418,7 @@ cudaError_t run(const NormBwdArgs &a, cudaStream_t stream) {
         const Shape s = shape_of(a.cols);
         const bool wide = wide_rows(a.x, a.x_f32, a.ld_x) && wide_rows(a.dy, a.dy_f32, a.ld_dy) &&
                           wide_rows(a.dx, a.x_f32, a.ld_dx) && (a.add == nullptr || wide_rows(a.add, a.x_f32, a.ld_add));
-        const size_t smem = (s.rpb > 1 ? 2 : 1) * 16 * sizeof(float) * s.tpr;   // at most 32 KB
-        if (a.cols <= kRingCols) {
-            e = wide ? run_ring<XF32, DF32, true>(a, s, parts, smem, stream) : run_ring<XF32, DF32, false>(a, s, parts, smem, stream);
-        } else {
-            e = wide ? launch_after(&k_norm_bwd<XF32, DF32, true>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr)
-                     : launch_after(&k_norm_bwd<XF32, DF32, false>, dim3(parts), s.tpr * s.rpb, smem, stream, 1, a, s.tpr);
-        }
+        e = wide ? run_rows<XF32, DF32, true>(a, s, parts, stream) : run_rows<XF32, DF32, false>(a, s, parts, stream);
     }
     if (e != cudaSuccess || a.ws == nullptr) return e;
     return launch_after(&k_norm_sums, dim3(static_cast<unsigned>((2 * static_cast<int64_t>(a.cols) + 31) / 32)), 512, 0,
