@@ -152,23 +152,23 @@ struct TileCopy {
     }
 };
 
-// The long side's splits of shrink: one round of CTAs over the plan's tiles, at
-// least 128 columns each.  On the device from the plan, on the host an upper bound.
+// The long side's splits of shrink: one round of CTAs over the plan's tiles, at least
+// 128 columns each.  On the device from the plan, on the host an upper bound: as if
+// no token were without an adapter, and the tiles full.
 constexpr int kShrinkCols = 64;
 constexpr int kMaxSplits = 16;
-__host__ __device__ inline int shrink_splits(int64_t tiles, int k) {
+__host__ __device__ inline int shrink_splits(const LoraPlan &p, int tiles, int k) {
     const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
-    int64_t n = kSms / (tiles < 1 ? 1 : tiles);
+    const int full = (p.tokens + kLoraTile - 1) / kLoraTile;
+    int64_t n = kSms / (tiles > full ? tiles : full);
     n = n < (steps + 1) / 2 ? n : (steps + 1) / 2;
     n = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
     const int64_t per = (steps + n - 1) / n;
     return static_cast<int>((steps + per - 1) / per);
 }
-// More than any number of tiles with `tokens` tokens gives.
 inline int most_splits(const LoraPlan &p, int k) {
     const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
-    const int64_t n = kSms / ((p.tokens + kLoraTile - 1) / kLoraTile);
-    const int64_t most = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
+    const int64_t n = kSms / ((p.tokens + kLoraTile - 1) / kLoraTile), most = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
     return static_cast<int>(most < steps ? most : steps);
 }
 __device__ __forceinline__ int adapter_tiles(const LoraPlan &p) { return p.words[p.tile_first() + p.adapters]; }

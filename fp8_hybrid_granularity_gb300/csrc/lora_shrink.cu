@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * a.k);
     Tile tile = tile_at(a.plan, blockIdx.x);      // its place is there, if it is a tile or not
     if (a.packed) tile.row = tile.first;
-    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(tiles, a.k);
+    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(a.plan, tiles, a.k);
     if (static_cast<int>(blockIdx.x) >= tiles || static_cast<int>(blockIdx.y) >= splits) return;
     const int all = (a.k + kCols - 1) / kCols, per = (all + splits - 1) / splits;
     const int first = blockIdx.y * per, steps = min(all - first, per);
@@ -291,7 +291,7 @@ namespace {
 __global__ void __launch_bounds__(256) k_lora_sum(const SumArgs a, int rp) {
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * rp);
     const Tile tile = tile_at(a.plan, blockIdx.x);
-    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(tiles, a.long_side), quads = rp / 4;
+    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(a.plan, tiles, a.long_side), quads = rp / 4;
     if (static_cast<int>(blockIdx.x) >= a.plan.words[0]) return;
     const int rank = tile.adapter < 0 ? 0 : rank_of(a.lw, tile.adapter);
     const int64_t next = static_cast<int64_t>(a.plan.tokens) * rp;

@@ -113,6 +113,19 @@ def test_backward(cuda_lib, size, dtype, grads):
     check_backward(s, None, v, z, None, None)
 
 
+@pytest.mark.parametrize("t,g,none", [(1000, 4, 0.6), (4001, 4, 0.12), (700, 2, 0.97), (130, 1, 0.0)])
+def test_long_sides(cuda_lib, t, g, none):
+    """Many steps of the long sides, with fewer tiles than the tokens would fill."""
+    n, k, r = 1104, 4096, 32
+    s = batch(t, n, k, r, g, none=none)
+    plan = cuda_lib.lora_plan(s["ids"], g)
+    base = rand(9, t, n).bfloat16()
+    y, v = cuda_lib.lora_add(base, s["x"], adapters(cuda_lib, s), plan, keep=True)
+    check_forward(s, base, y, v)
+    dx, da, db = cuda_lib.lora_add_bwd(s["dy"], s["x"], v, adapters(cuda_lib, s), plan)
+    check_backward(s, None, v, dx, da, db)
+
+
 def test_past_the_rank_and_without_an_adapter(cuda_lib):
     """What lies past a rank, and the rows of tokens without an adapter, may be
     anything; an adapter of rank 0 adds nothing."""
