@@ -15,6 +15,7 @@ namespace {
 constexpr int64_t kMaxDim = int64_t(1) << 30;
 constexpr int64_t kMaxLd = 0x7FFFFFFF;
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int64_t kMaxSide = int64_t(1) << 24;      // of a projection
 
 inline bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline int status_from_cuda(cudaError_t e) { return e == cudaSuccess ? FP8HG_OK : FP8HG_ERR_CUDA; }
@@ -50,6 +51,7 @@ int check_lora(const fp8hg_lora *w) {
     if (!w) return FP8HG_ERR_INVALID_ARG;
     const int st = check_dims(w->n, w->k);
     if (st != FP8HG_OK) return st;
+    if (w->n > kMaxSide || w->k > kMaxSide) return FP8HG_ERR_SHAPE;
     if (w->r < 1 || w->adapters < 1) return FP8HG_ERR_INVALID_ARG;
     if (w->r > fp8hg::kLoraMaxRank) return FP8HG_ERR_UNSUPPORTED;
     if (!w->a || !w->b || w->ld_a < w->k || w->ld_b < w->r || w->stride_a < 0 || w->stride_b < 0) return FP8HG_ERR_INVALID_ARG;
@@ -66,7 +68,7 @@ fp8hg::LoraWeights weights(const fp8hg_lora *w) {
 // Sizes for which the workspace functions have an answer.
 bool lora_sizes(int64_t tokens, int64_t adapters, int64_t r, int64_t n, int64_t k) {
     return tokens > 0 && tokens <= kMaxTokens && adapters > 0 && adapters <= fp8hg::kLoraMaxAdapters && r > 0 &&
-           r <= fp8hg::kLoraMaxRank && n > 0 && n <= kMaxDim && k > 0 && k <= kMaxDim;
+           r <= fp8hg::kLoraMaxRank && n > 0 && n <= kMaxSide && k > 0 && k <= kMaxSide;
 }
 
 }  // namespace

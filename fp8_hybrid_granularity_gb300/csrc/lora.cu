@@ -110,7 +110,7 @@ namespace {
 
 size_t partial_bytes(int64_t tokens, int adapters, int r, int64_t k) {
     const int rp = lora::padded(r);
-    return static_cast<size_t>(lora::most_splits({nullptr, static_cast<int>(tokens), adapters}, static_cast<int>(k))) * tokens * rp *
+    return static_cast<size_t>(lora::most_splits({nullptr, static_cast<int>(tokens), adapters}, static_cast<int>(k), rp)) * tokens * rp *
            sizeof(float);
 }
 
@@ -154,7 +154,7 @@ cudaError_t launch_lora_add(const LoraArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // Each CTA of a tile would add up its partial sums: left to them where there are
     // few tokens, one kernel more otherwise.
-    const bool apart = a.plan.tokens > kLoraTile && (a.v != nullptr || lora::most_splits(a.plan, a.w.k) > 1);
+    const bool apart = a.plan.tokens > kLoraTile && (a.v != nullptr || lora::most_splits(a.plan, a.w.k, lora::padded(a.w.r)) > 1);
     if (apart) {
         e = lora::launch_sum({a.plan, a.w, a.ws, a.w.k, a.v, a.ld_v}, stream);
         if (e != cudaSuccess) return e;

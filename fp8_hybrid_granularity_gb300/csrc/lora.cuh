@@ -153,23 +153,29 @@ struct TileCopy {
 };
 
 // The long side's splits of shrink: one round of CTAs over the plan's tiles, at least
-// 128 columns each.  On the device from the plan, on the host an upper bound: as if
-// no token were without an adapter, and the tiles full.
+// 128 columns each, and at most as many as keep the tensor core's sums short.  On the
+// device from the plan, on the host an upper bound: as if no token were without an
+// adapter, and the tiles full.
 constexpr int kShrinkCols = 64;
 constexpr int kMaxSplits = 16;
-__host__ __device__ inline int shrink_splits(const LoraPlan &p, int tiles, int k) {
+// Sums in tensor memory that steps take turns at, and the most steps at each: 48 sums
+// of 16, each cut off, are off by some 7e-7 of the result (64: 1e-6).
+__host__ __device__ constexpr int shrink_sums(int rp) { return rp <= 64 ? 8 : 4; }
+constexpr int kSumSteps = 12;
+__host__ __device__ inline int split_steps(int64_t steps, int ctas_a_tile, int rp) {
+    int64_t n = ctas_a_tile < (steps + 1) / 2 ? ctas_a_tile : (steps + 1) / 2;
+    n = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
+    const int64_t short_sums = (steps + shrink_sums(rp) * kSumSteps - 1) / (shrink_sums(rp) * kSumSteps);
+    return static_cast<int>(n > short_sums ? n : short_sums);
+}
+__host__ __device__ inline int shrink_splits(const LoraPlan &p, int tiles, int k, int rp) {
     const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
     const int full = (p.tokens + kLoraTile - 1) / kLoraTile;
-    int64_t n = kSms / (tiles > full ? tiles : full);
-    n = n < (steps + 1) / 2 ? n : (steps + 1) / 2;
-    n = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
-    const int64_t per = (steps + n - 1) / n;
+    const int64_t n = split_steps(steps, kSms / (tiles > full ? tiles : full), rp), per = (steps + n - 1) / n;
     return static_cast<int>((steps + per - 1) / per);
 }
-inline int most_splits(const LoraPlan &p, int k) {
-    const int64_t steps = (static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols;
-    const int64_t n = kSms / ((p.tokens + kLoraTile - 1) / kLoraTile), most = n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
-    return static_cast<int>(most < steps ? most : steps);
+inline int most_splits(const LoraPlan &p, int k, int rp) {
+    return split_steps((static_cast<int64_t>(k) + kShrinkCols - 1) / kShrinkCols, kSms / ((p.tokens + kLoraTile - 1) / kLoraTile), rp);
 }
 __device__ __forceinline__ int adapter_tiles(const LoraPlan &p) { return p.words[p.tile_first() + p.adapters]; }
 

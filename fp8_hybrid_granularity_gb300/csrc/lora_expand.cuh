@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
     const int all = (a.n + kCols - 1) / kCols;
     const int64_t total = static_cast<int64_t>(a.plan.words[0]) * all;
     const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
-    const int splits = a.long_side > 0 ? shrink_splits(a.plan, adapter_tiles(a.plan), a.long_side) : 1;
+    const int splits = a.long_side > 0 ? shrink_splits(a.plan, adapter_tiles(a.plan), a.long_side, RP) : 1;
 
     for (int64_t at = total * blockIdx.x / gridDim.x; at < end;) {
         const Tile tile = tile_at(a.plan, static_cast<int>(at / all));

@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(256) k_lora_prep(const PrepArgs a) {
     const Tile tile = tile_at(a.plan, blockIdx.x);
     const int rank = rank_of(a.lw, tile.adapter), tid = threadIdx.x, r0 = blockIdx.z * 16;
     const float scale = a.lw.scale == nullptr ? 1.0f : a.lw.scale[tile.adapter];
-    const int splits = side == 0 ? 0 : shrink_splits(a.plan, tiles, a.long_side);
+    const int splits = side == 0 ? 0 : shrink_splits(a.plan, tiles, a.long_side, RP);
 #pragma unroll
     for (int h = 0; h < kLoraTile * 4 / 256; ++h) {
         const int m = (h * 256 + tid) / 4, c = tid % 4 * 4, r = r0 + c;

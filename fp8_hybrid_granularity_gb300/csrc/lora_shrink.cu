@@ -30,8 +30,8 @@ struct Shape {
     static constexpr int N = TRANS && RP < 64 ? 64 : RP;
     static constexpr int X = kLoraTile * 128, W = TRANS ? (N / 64) * kCols * 128 : N * 128;
     static constexpr int STAGES = 216 * 1024 / (X + W) < 8 ? 216 * 1024 / (X + W) : 8;
-    static constexpr int SUMS = 512 / N < 8 ? 512 / N : 8;
-    static constexpr int TMEM = SUMS * N < 128 ? 128 : SUMS * N;
+    static constexpr int SUMS = shrink_sums(RP);
+    static constexpr int TMEM = SUMS * N;      // 128, 256 or 512 columns
     static constexpr int BARS = 8 * (2 * STAGES + 1);
     static constexpr int SMEM = 1024 + STAGES * (X + W) + BARS + 16;
     // pieces of 16 bytes of W's tile, a thread
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * a.k);
     Tile tile = tile_at(a.plan, blockIdx.x);      // its place is there, if it is a tile or not
     if (a.packed) tile.row = tile.first;
-    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(a.plan, tiles, a.k);
+    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(a.plan, tiles, a.k, RP);
     if (static_cast<int>(blockIdx.x) >= tiles || static_cast<int>(blockIdx.y) >= splits) return;
     const int all = (a.k + kCols - 1) / kCols, per = (all + splits - 1) / splits;
     const int first = blockIdx.y * per, steps = min(all - first, per);
@@ -245,7 +245,7 @@ cudaError_t run(const ShrinkArgs &a, const CUtensorMap &map_x, const CUtensorMap
     auto *kern = &k_lora_shrink<RP, TRANS, WIDE, WAL>;
     const cudaError_t e = with_smem(kern, S::SMEM, S::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, dim3(a.plan.max_tiles(), most_splits(a.plan, a.k)), kThreads, S::SMEM, stream, 1, a, map_x, map_w);
+    return launch_after(kern, dim3(a.plan.max_tiles(), most_splits(a.plan, a.k, RP)), kThreads, S::SMEM, stream, 1, a, map_x, map_w);
 }
 // W as [adapters][rows][long side], 64 values of the latter (or of a row of r) a piece.
 bool weights_map(CUtensorMap *m, const ShrinkArgs &a, int rows, int cols, int box_rows) {
@@ -291,7 +291,7 @@ namespace {
 __global__ void __launch_bounds__(256) k_lora_sum(const SumArgs a, int rp) {
     ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * rp);
     const Tile tile = tile_at(a.plan, blockIdx.x);
-    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(a.plan, tiles, a.long_side), quads = rp / 4;
+    const int tiles = adapter_tiles(a.plan), splits = shrink_splits(a.plan, tiles, a.long_side, rp), quads = rp / 4;
     if (static_cast<int>(blockIdx.x) >= a.plan.words[0]) return;
     const int rank = tile.adapter < 0 ? 0 : rank_of(a.lw, tile.adapter);
     const int64_t next = static_cast<int64_t>(a.plan.tokens) * rp;

@@ -84,12 +84,13 @@ __device__ __forceinline__ void finish(const NormArgs &a, int q_kind, uint32_t r
                                        const float *b, F2 (&d)[R][8], float (&mean)[R], float (&rstd)[R]) {
     const int c0 = t * 16, cols_left = a.cols - c0;
     const uint32_t rows = a.rows;
+    const float n = static_cast<float>(a.cols);
 #pragma unroll
     for (int i = 0; i < R; ++i) mean[i] = total(d[i]);
     row.sum(mean);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        mean[i] *= inv_n;
+        mean[i] = divide(mean[i], n, inv_n);
         const F2 m = f2(-mean[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[i][j] = add2(d[i][j], m);
@@ -106,7 +107,7 @@ __device__ __forceinline__ void finish(const NormArgs &a, int q_kind, uint32_t r
     row.sum(rstd);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        rstd[i] = rsqrtf(rstd[i] * inv_n + a.eps);
+        rstd[i] = __frsqrt_rn(divide(rstd[i], n, inv_n) + a.eps);
         if (a.stats != nullptr && t == 0 && r + i < rows) reinterpret_cast<float2 *>(a.stats)[r + i] = make_float2(mean[i], rstd[i]);
     }
 #pragma unroll
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(512) k_norm_long(const NormArgs a, int q_kind)
             piece(c0, v);
             s += total(v);
         }
-        const float mean = row.sum(s) * inv_n;
+        const float n = static_cast<float>(a.cols), mean = divide(row.sum(s), n, inv_n);
         s = 0.0f;
         for (int64_t c0 = first; c0 < a.cols; c0 += pass) {
             F2 v[8];
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(512) k_norm_long(const NormArgs a, int q_kind)
             for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], v[i]);
             s += total(v);
         }
-        const float rstd = rsqrtf(row.sum(s) * inv_n + a.eps);
+        const float rstd = __frsqrt_rn(divide(row.sum(s), n, inv_n) + a.eps);
         if (a.stats != nullptr && threadIdx.x == 0) reinterpret_cast<float2 *>(a.stats)[r] = make_float2(mean, rstd);
         auto value = [&](int64_t c0, F2 (&v)[8]) {
             const int left = static_cast<int>(a.cols - c0);

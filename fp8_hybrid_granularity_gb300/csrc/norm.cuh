@@ -77,6 +77,13 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// s / n, correctly rounded but for the last unit: a quotient that is off the same way in
+// every row shows in the codes that come out of it.
+__device__ __forceinline__ float divide(float s, float n, float inv_n) {
+    const float q = s * inv_n, e = fmaf(fmaf(-q, n, s), inv_n, q);
+    return fabsf(q) <= 3.4e38f ? e : q;
+}
+
 __device__ __forceinline__ float total(const F2 (&v)[8]) {
     const F2 a = add2(add2(v[0], v[1]), add2(v[2], v[3])), b = add2(add2(v[4], v[5]), add2(v[6], v[7]));
     const F2 s = add2(a, b);

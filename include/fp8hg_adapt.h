@@ -93,7 +93,8 @@ int fp8hg_lora_plan(const int32_t *ids, int64_t tokens, int64_t adapters, void *
 /*
  * Adapters beside one projection [n, k]: A [adapters, r, k] and B [adapters, n, r]
  * in BF16, row strides ld_a and ld_b, stride_a and stride_b elements from one
- * adapter to the next.  1 <= r <= 128 (FP8HG_ERR_UNSUPPORTED beyond).
+ * adapter to the next.  1 <= r <= 128 (FP8HG_ERR_UNSUPPORTED beyond); n and k at
+ * most 2^24.
  *
  *   scale   [adapters] floats; NULL: 1
  *   ranks   [adapters] int32: rows of A (columns of B) that an adapter has, 0 to

@@ -104,7 +104,7 @@ def lora(a=FAKE, b=FAKE, scale=None, ranks=None, g=2, r=16, n=64, k=32, sa=512, 
 BAD_LORA = [(dict(a=None), INVALID), (dict(b=None), INVALID), (dict(a=FAKE + 1), ALIGN), (dict(b=FAKE + 1), ALIGN),
             (dict(scale=FAKE + 2), ALIGN), (dict(ranks=FAKE + 2), ALIGN), (dict(r=0), INVALID), (dict(r=129, lb=129), UNSUP),
             (dict(g=0), INVALID), (dict(g=4097), SHAPE), (dict(n=-1), INVALID), (dict(n=0), SHAPE), (dict(k=0), SHAPE),
-            (dict(k=2 ** 31), SHAPE), (dict(la=31), INVALID), (dict(lb=15), INVALID), (dict(sa=-1), INVALID), (dict(la=2 ** 31), SHAPE)]
+            (dict(k=2 ** 31), SHAPE), (dict(n=2 ** 24 + 1), SHAPE), (dict(la=31), INVALID), (dict(lb=15), INVALID), (dict(sa=-1), INVALID), (dict(la=2 ** 31), SHAPE)]
 
 
 def test_lora_add_refusals(lib):
