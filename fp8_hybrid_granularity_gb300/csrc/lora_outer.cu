@@ -348,49 +348,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The adapters of several chunks, and zeros for those without a token: 32 by 32
-// values through shared memory where the result's rows run the other way.
+// values a CTA, through shared memory where the result's rows run the other way.
 __global__ void __launch_bounds__(256) k_lora_join(const OuterArgs a, int rp) {
     __shared__ float tile[32][33];
     ptx::grid_wait();
-    const OuterSide o = a.side[blockIdx.z];
+    const int parts = (a.lw.r + 31) / 32, r0 = blockIdx.z % parts * 32;
+    const OuterSide &o = a.side[blockIdx.z / parts];
     if (o.out == nullptr) return;
     const int *tile_first = a.plan.words + a.plan.tile_first();
     const int per = a.tiles(adapter_tiles(a.plan));
     const int tx = threadIdx.x & 31, ty = threadIdx.x / 32;
+    const bool along_n = o.stride_n == 1;
     for (int g = blockIdx.y; g < a.plan.adapters; g += gridDim.y) {
         const int begin = tile_first[g], end = tile_first[g + 1];
         const int c0 = begin / per, c1 = begin < end ? (end - 1) / per : c0;
         if (begin < end && c0 == c1) continue;
         for (int64_t b = static_cast<int64_t>(blockIdx.x) * 32; b < o.n; b += static_cast<int64_t>(gridDim.x) * 32) {
-            for (int r0 = 0; r0 < a.lw.r; r0 += 32) {
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (begin < end && r0 + tx < a.lw.r) {
+                const int64_t slot = static_cast<int64_t>(o.n) * rp;
+                const float *p = o.ws + (2 * static_cast<int64_t>(c0) + 1) * slot + (b + ty) * rp + r0 + tx;
+                // the first chunk's, then one of each chunk after it
+#pragma unroll 4
+                for (int c = c0; c <= c1; ++c, p += c == c0 + 1 ? slot : 2 * slot) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t n = b + ty + 8 * i;
-                    const int r = r0 + tx;
-                    float s = 0.0f;
-                    if (begin < end && n < o.n && r < a.lw.r) {
-                        const float *p = o.ws + ((2 * static_cast<int64_t>(c0) + 1) * o.n + n) * rp + r;
-                        s = ptx::ld_f32(p);
-                        p += static_cast<int64_t>(o.n) * rp;
-                        for (int c = c0 + 1; c <= c1; ++c, p += 2 * static_cast<int64_t>(o.n) * rp) s += ptx::ld_f32(p);
-                    }
-                    tile[ty + 8 * i][tx] = s;
+                    for (int i = 0; i < 4; ++i)
+                        if (b + ty + 8 * i < o.n) s[i] += ptx::ld_f32(p + static_cast<int64_t>(8 * i) * rp);
                 }
+            }
+            if (along_n) {
                 __syncthreads();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool along_n = o.stride_n == 1;
-                    const int u = ty + 8 * i;
-                    const int64_t n = b + (along_n ? tx : u);
-                    const int r = r0 + (along_n ? u : tx);
-                    if (n < o.n && r < a.lw.r) {
-                        const float s = along_n ? tile[tx][u] : tile[u][tx];
-                        const int64_t at = g * o.stride_g + n * o.stride_n + r * o.stride_r;
-                        if (a.f32) static_cast<float *>(o.out)[at] = s;
-                        else static_cast<uint16_t *>(o.out)[at] = static_cast<uint16_t>(ptx::cvt_bf16x2(s, 0.0f));
-                    }
-                }
+                for (int i = 0; i < 4; ++i) tile[ty + 8 * i][tx] = s[i];
                 __syncthreads();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] = tile[tx][ty + 8 * i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t n = b + (along_n ? tx : ty + 8 * i);
+                const int r = r0 + (along_n ? ty + 8 * i : tx);
+                if (n < o.n && r < a.lw.r) {
+                    const int64_t at = g * o.stride_g + n * o.stride_n + r * o.stride_r;
+                    if (a.f32) static_cast<float *>(o.out)[at] = s[i];
+                    else static_cast<uint16_t *>(o.out)[at] = static_cast<uint16_t>(ptx::cvt_bf16x2(s[i], 0.0f));
+                }
             }
         }
     }
@@ -456,7 +458,7 @@ cudaError_t launch_outer(OuterArgs &a, cudaStream_t stream) {
                           : rp == 64 ? pick<64>(a, wide, map, stream)
                                      : pick<128>(a, wide, map, stream);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((most + 31) / 32, 1024)), std::min(a.plan.adapters, 64), 2);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((most + 31) / 32, 1024)), std::min(a.plan.adapters, 64), 2 * ((a.lw.r + 31) / 32));
     return launch_after(&k_lora_join, grid, 256, 0, stream, 1, a, rp);
 }
 
