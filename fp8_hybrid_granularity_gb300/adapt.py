@@ -175,7 +175,8 @@ def fp8_layernorm(x, weight=None, bias=None, eps: float = 1e-5, group: int = 0, 
 @_streamed
 def layernorm_bwd(dy, x, weight, stats, add=None, out=None, params: bool = True):
     """dx (x's type), dweight and dbias (FP32) from dy, x and the forward pass's
-    stats.  add: another branch's gradient of x, added to dx (may be out).
+    stats.  add: another branch's gradient of x, added to dx.  out may be add, x
+    or dy.
     params=False: dx alone, (dx, None, None)."""
     device = lowbit._cuda_device()
     shape, ld_x, kind = _matrix(x, "x", _EITHER, device)

@@ -10,7 +10,12 @@
 // the sums for dw and db stay in registers over all rows of a CTA and leave as
 // one row of partial sums per CTA, which a second kernel adds in a fixed order:
 // results do not depend on timing.  Rows of more than 8192 columns are read twice
-// for dx and once more, by columns, for dw and db.
+// for dx and once before, by columns, for dw and db.
+//
+// 16384 x 3584, BF16 x, dy, add and dx: 93 us in a stream of calls for 470 MB, 75 % of
+// the copy rate (rows loaded into registers instead of through shared memory: 99).
+// What is left are the barrier of every pair of rows and the registers of the sums,
+// which leave room for 16 warps an SM.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -411,9 +416,9 @@ cudaError_t run(const NormBwdArgs &a, cudaStream_t stream) {
     const int parts = norm_parts(a.rows, a.cols);
     cudaError_t e;
     if (a.cols > kRegCols) {
-        e = launch_after(&k_norm_bwd_long<XF32, DF32>, dim3(std::min(a.rows, 2 * kSms)), 512, 0, stream, 1, a);
-        if (e == cudaSuccess && a.ws != nullptr)
-            e = launch_after(&k_norm_columns<XF32, DF32>, dim3((a.cols + 511) / 512, parts), 256, 0, stream, 1, a);
+        // dw and db first: dx may be dy or x
+        e = a.ws == nullptr ? cudaSuccess : launch_after(&k_norm_columns<XF32, DF32>, dim3((a.cols + 511) / 512, parts), 256, 0, stream, 1, a);
+        if (e == cudaSuccess) e = launch_after(&k_norm_bwd_long<XF32, DF32>, dim3(std::min(a.rows, 2 * kSms)), 512, 0, stream, 1, a);
     } else {
         const Shape s = shape_of(a.cols);
         const bool wide = wide_rows(a.x, a.x_f32, a.ld_x) && wide_rows(a.dy, a.dy_f32, a.ld_dy) &&

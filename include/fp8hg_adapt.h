@@ -63,7 +63,8 @@ int fp8hg_layernorm(const void *x, int x_kind, int64_t rows, int64_t cols, int64
  *
  *   dy, dy_kind      [rows, cols], row stride ld_dy
  *   x, dx, add       [rows, cols] of x_kind; add (another branch's gradient): NULL
- *                    for none, and may be dx
+ *                    for none.  dx may be add, x or dy where type and
+ *                    stride are the same
  *   dweight, dbias   [cols] floats; either or both NULL: not computed
  *   workspace        fp8hg_layernorm_bwd_workspace(rows, cols) bytes; not used if
  *                    both are NULL
@@ -119,7 +120,9 @@ typedef struct {
  *             backward pass; 0 past an adapter's rank and without one
  *   workspace fp8hg_lora_workspace(tokens, adapters, r, k) bytes
  * x A^T is summed in FP32 and enters the second product as two BF16 parts (y in
- * BF16) or three (FP32).
+ * BF16) or three (FP32).  Where an element of B is infinite, y may be a NaN instead of
+ * an infinity (a part is 0); the same holds for the backward pass and infinite
+ * elements of A, x and dy.
  */
 size_t fp8hg_lora_workspace(int64_t tokens, int64_t adapters, int64_t r, int64_t k);
 int fp8hg_lora_add(const fp8hg_lora *w, const void *plan, int64_t tokens, const uint16_t *x,

@@ -172,6 +172,22 @@ def test_backward_in_place_and_empty(cuda_lib):
     assert dx.shape == (0, 9) and (dw == 0).all() and (db == 0).all()
 
 
+@pytest.mark.parametrize("cols", [300, 4104, 5001, 8200])
+@pytest.mark.parametrize("kind", [BF16, F32])
+def test_in_place(cuda_lib, cols, kind):
+    """y over x; dx over dy and over x, with dw and db from what was there."""
+    x, dy = values(700, cols, kind), values(700, cols, kind, seed=2)
+    w, b = params(cols, F32)
+    y, stats = cuda_lib.layernorm(x, w, b)
+    over = x.clone()
+    assert torch.equal(cuda_lib.layernorm(over, w, b, out=over)[0], y)
+    want = cuda_lib.layernorm_bwd(dy, x, w, stats)
+    over = dy.clone()
+    assert all(torch.equal(p, q) for p, q in zip(cuda_lib.layernorm_bwd(over, x, w, stats, out=over), want))
+    over = x.clone()
+    assert all(torch.equal(p, q) for p, q in zip(cuda_lib.layernorm_bwd(dy, over, w, stats, out=over), want))
+
+
 def test_gradient_by_differences(cuda_lib):
     """The backward call against differences of the forward call's sum(y * c)."""
     rows, cols, h = 4, 24, 2.0 ** -6
