@@ -4,10 +4,13 @@
 // long side (partial sums in FP32; the kernels behind add them in a fixed order), 64
 // columns a step; the rows of r are its columns.  W's tile is an operand with its K
 // (A_g) or its rows (B_g, in the backward pass) next to one another.  Steps take
-// turns at the sums in tensor memory, 512 columns of it, so that a sum is cut off
-// only 4 times in as many steps as there are sums; they are added at the end.  Rows
-// past a tile's tokens, and past an adapter's rank, hold anything: they meet no
+// turns at the sums in tensor memory, up to 512 columns of it, so that a sum is cut
+// off only 4 times in as many steps as there are sums; they are added at the end.
+// Rows past a tile's tokens, and past an adapter's rank, hold anything: they meet no
 // other row's sums, and nobody reads theirs.
+//
+// Bound by HBM: 8192 x 8960, r 64, takes 29.5 us, 74 % of the copy rate (rows copied
+// by the warps: 36; mma.sync fed through registers: 52); r 16, 8192 x 3584: 16 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

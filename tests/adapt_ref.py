@@ -122,7 +122,7 @@ def lora_bwd(dy, x, v, a, b, scale, ranks, ids):
 
 # How far the adapters' results may be off, of the sum of their products'
 # magnitudes.  The tensor core cuts every product of a sum of 16 at 2^-23 of the
-# largest term, so a chain of 64 products (and their two or three parts, whose
+# largest term, so a chain of up to 48 such sums (and their two or three parts, whose
 # later ones are 2^-8 and 2^-16 of the first) is off by less than 70 * 2^-23; the
 # additions to registers add one U each (at most 300 of them here) and a factor in
 # two parts 2^-17.  Twice (two products after one another) and rounded up:
