@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libfp8hg.so")
 SOURCES = ["api.cu", "quant.cu", "quant_dual.cu", "gemm.cu", "gemm_f32s.cu", "lowbit_api.cu",
            "fp4_quant.cu", "gemm_fp4.cu", "swiglu.cu", "adapt_api.cu", "norm.cu", "norm_bwd.cu",
            "lora.cu", "lora_shrink.cu", "lora_expand.cu",
-           "lora_expand_t.cu", "lora_outer.cu"]
+           "lora_expand_t.cu", "lora_few.cu", "lora_outer.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -136,6 +136,8 @@ size_t lora_ws_bytes(int64_t tokens, int adapters, int r, int64_t k) {
 }
 
 cudaError_t launch_lora_add(const LoraArgs &a, cudaStream_t stream) {
+    const lora::FewArgs few{a.plan, a.w, a.x, a.ld_x, a.base, a.y, a.ld_base, a.ld_y, a.v, a.ld_v};
+    if (lora::few(few, a.y_f32)) return lora::launch_few(few, a.y_f32, stream);
     lora::ShrinkArgs s{};
     s.plan = a.plan;
     s.x = a.x;

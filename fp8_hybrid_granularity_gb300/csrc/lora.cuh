@@ -246,6 +246,22 @@ struct ExpandArgs {
 cudaError_t launch_expand(const ExpandArgs &a, bool f32, cudaStream_t stream);
 cudaError_t launch_expand_t(const ExpandArgs &a, bool f32, cudaStream_t stream);     // trans
 
+// Both products of at most so many tokens in one kernel.
+constexpr int kFewTokens = 64;
+struct FewArgs {
+    LoraPlan plan;
+    LoraWeights lw;
+    const uint16_t *x;
+    uint32_t ld_x;
+    const void *base;
+    void *y;
+    uint32_t ld_base, ld_y;
+    float *v_out;                    // x A^T for the backward pass, or null
+    uint32_t ld_v;
+};
+bool few(const FewArgs &a, bool f32);      // sizes and alignments that it takes
+cudaError_t launch_few(const FewArgs &a, bool f32, cudaStream_t stream);
+
 // One of the two sums over the tokens.
 struct OuterSide {
     const uint16_t *d;               // [tokens][n]

@@ -187,6 +187,37 @@ def test_strides(cuda_lib, pad, dtype):
     assert (whole == 7.0).all()
 
 
+# tokens, n, k, r, adapters: up to 16 tokens, up to 64 with many adapters, several 16s of
+# one, a long side past the one-kernel form's
+@pytest.mark.parametrize("size", [(1, 260, 72, 8, 1), (1, 4, 8, 16, 3), (2, 4100, 520, 128, 2), (5, 36, 8, 40, 2), (16, 132, 4104, 16, 1),
+                                  (17, 1028, 520, 24, 5), (48, 520, 264, 64, 24), (64, 260, 136, 32, 16), (64, 2052, 88, 128, 64),
+                                  (33, 68, 1056, 16, 9), (9, 64, 49152, 16, 2), (9, 64, 49160, 16, 2), (20, 96, 64, 8, 4096)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_few_tokens(cuda_lib, size, dtype):
+    """Decoding: what lies past a rank, and rows of tokens without an adapter, may be
+    anything; rows of wider buffers; y over base."""
+    t, n, k, r, g = size
+    s = batch(*size, seed=40, none=0.1)
+    for i, m in enumerate(s["ranks"].tolist()):
+        s["a"][i, m:], s["b"][i, :, m:] = float("nan"), float("nan")
+    none = s["ids"] < 0
+    s["x"][none] = float("nan")
+    wide = lambda x: torch.nn.functional.pad(x, (8, 8), value=float("nan"))[..., 8:8 + x.shape[-1]]  # noqa: E731
+    w = {**s, "x": wide(s["x"]), "a": wide(s["a"]), "b": wide(s["b"])}
+    plan = cuda_lib.lora_plan(s["ids"], g)
+    base, whole = wide(rand(9, t, n).to(dtype)), torch.full((t, n + 16), 7.0, dtype=dtype, device="cuda")
+    y, v = cuda_lib.lora_add(base, w["x"], adapters(cuda_lib, w), plan, out=whole[:, 8:8 + n], keep=True)
+    s["x"][none] = 0.0
+    check_forward(s, base, y, v)
+    assert torch.equal(y[none], base[none]) and (v[none] == 0).all()
+    z, _ = cuda_lib.lora_add(None, w["x"], adapters(cuda_lib, w), plan, out_dtype=dtype)
+    check_forward(s, None, z)
+    y = y.clone()
+    assert torch.equal(cuda_lib.lora_add(base, w["x"], adapters(cuda_lib, w), plan, out=base)[0], y)
+    whole[:, 8:8 + n] = 7.0
+    assert (whole == 7.0).all()
+
+
 def test_in_place_defaults_and_empty(cuda_lib):
     t, n, k, r, g = 100, 256, 128, 16, 2
     s = batch(t, n, k, r, g)
