@@ -118,15 +118,16 @@ bool rows_aligned(const uint16_t *p, uint32_t ld) { return lora::aligned_to(p, 1
 
 // Rows for the kernels that TMA feeds: as they are, or copied to `to` where that is
 // foreseen (odd strides of rows with a multiple of 8 columns are left to the kernels'
-// own copies).
-cudaError_t rows_for(const LoraPlan &plan, const uint16_t *&p, uint32_t &ld, int cols, uint8_t *to, int &packed, cudaStream_t stream) {
-    packed = !rows_aligned(p, ld) && cols % 8 != 0;
-    if (!packed) return cudaSuccess;
-    uint16_t *rows = reinterpret_cast<uint16_t *>(to);
-    const cudaError_t e = lora::launch_pack(plan, p, ld, cols, rows, stream);
-    p = rows;
+// own copies).  True if they are copied; p and ld are then the copy's.
+bool add_rows(lora::PackArgs &c, int &matrices, const uint16_t *&p, uint32_t &ld, int cols, uint8_t *to) {
+    if (rows_aligned(p, ld) || cols % 8 == 0) return false;
+    c.from[matrices] = p;
+    c.ld[matrices] = ld;
+    c.cols[matrices] = cols;
+    c.to[matrices++] = reinterpret_cast<uint16_t *>(to);
+    p = reinterpret_cast<uint16_t *>(to);
     ld = static_cast<uint32_t>(lora::ld_packed(cols));
-    return e;
+    return true;
 }
 
 }  // namespace
@@ -150,8 +151,11 @@ cudaError_t launch_lora_add(const LoraArgs &a, cudaStream_t stream) {
     s.out = a.ws;
     s.err = error_word();
     if (s.err == nullptr) return cudaErrorUnknown;
-    cudaError_t e = rows_for(a.plan, s.x, s.ld_x, a.w.k, reinterpret_cast<uint8_t *>(a.ws) + partial_bytes(a.plan.tokens, a.plan.adapters, a.w.r, a.w.k),
-                             s.packed, stream);
+    lora::PackArgs copies{};
+    copies.plan = a.plan;
+    int matrices = 0;
+    s.packed = add_rows(copies, matrices, s.x, s.ld_x, a.w.k, reinterpret_cast<uint8_t *>(a.ws) + partial_bytes(a.plan.tokens, a.plan.adapters, a.w.r, a.w.k));
+    cudaError_t e = matrices ? lora::launch_pack(copies, matrices, stream) : cudaSuccess;
     if (e == cudaSuccess) e = lora::launch_shrink(s, false, stream);
     if (e != cudaSuccess) return e;
     // Each CTA of a tile would add up its partial sums: left to them where there are
@@ -213,13 +217,15 @@ cudaError_t launch_lora_add_bwd(const LoraBwdArgs &a, cudaStream_t stream) {
     float *partial = reinterpret_cast<float *>(at), *sum = reinterpret_cast<float *>(at + ws.partial);
     uint16_t *vt0 = reinterpret_cast<uint16_t *>(at + ws.partial + ws.sum), *vt1 = vt0 + ws.vt / sizeof(uint16_t);
     float *parts = reinterpret_cast<float *>(vt1 + ws.vt / sizeof(uint16_t));
-    uint8_t *copies = reinterpret_cast<uint8_t *>(parts) + ws.outer;
-    cudaError_t e;
+    uint8_t *copied = reinterpret_cast<uint8_t *>(parts) + ws.outer;
     const uint16_t *dy = a.dy, *xr = a.x;
     uint32_t ld_dy = a.ld_dy, ld_x = a.ld_x;
-    int packed_dy = 0, packed_x = 0;
-    e = rows_for(a.plan, dy, ld_dy, a.w.n, copies, packed_dy, stream);
-    if (e == cudaSuccess && a.da != nullptr) e = rows_for(a.plan, xr, ld_x, a.w.k, copies + ws.dy, packed_x, stream);
+    lora::PackArgs copies{};
+    copies.plan = a.plan;
+    int matrices = 0;
+    const int packed_dy = add_rows(copies, matrices, dy, ld_dy, a.w.n, copied);
+    const int packed_x = a.da != nullptr && add_rows(copies, matrices, xr, ld_x, a.w.k, copied + ws.dy);
+    cudaError_t e = matrices ? lora::launch_pack(copies, matrices, stream) : cudaSuccess;
     if (e != cudaSuccess) return e;
     const bool rows = a.dx != nullptr || a.da != nullptr, outer = a.da != nullptr || a.db != nullptr;
     if (rows) {

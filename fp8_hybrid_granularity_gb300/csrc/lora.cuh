@@ -216,7 +216,14 @@ __host__ __device__ constexpr int64_t ld_packed(int64_t cols) { return (cols + 6
 inline size_t packed_bytes(int64_t tokens, int64_t cols) {
     return cols % 8 ? static_cast<size_t>(tokens) * ld_packed(cols) * sizeof(uint16_t) : 0;
 }
-cudaError_t launch_pack(const LoraPlan &plan, const uint16_t *from, uint32_t ld, int cols, uint16_t *to, cudaStream_t stream);
+struct PackArgs {
+    LoraPlan plan;
+    const uint16_t *from[2];
+    uint32_t ld[2];
+    int cols[2];
+    uint16_t *to[2];
+};
+cudaError_t launch_pack(const PackArgs &a, int matrices, cudaStream_t stream);
 
 struct SumArgs {
     LoraPlan plan;

@@ -326,15 +326,19 @@ __global__ void __launch_bounds__(256) k_lora_sum(const SumArgs a, int rp) {
 namespace {
 
 // A warp 512 columns of a row at a time.
-__global__ void __launch_bounds__(256) k_lora_pack(LoraPlan plan, const uint16_t *from, uint32_t ld, int cols, uint16_t *to, uint32_t ld_to) {
-    ptx::grid_begin(static_cast<int64_t>(plan.tokens) * cols);
-    const int lane = threadIdx.x & 31, chunks = (cols + 511) / 512, rows = plan.words[plan.starts() + plan.adapters];
+__global__ void __launch_bounds__(256) k_lora_pack(const PackArgs a) {
+    const int side = blockIdx.y, cols = side ? a.cols[1] : a.cols[0];
+    const uint16_t *from = side ? a.from[1] : a.from[0];
+    uint16_t *to = side ? a.to[1] : a.to[0];
+    const uint32_t ld = side ? a.ld[1] : a.ld[0], ld_to = static_cast<uint32_t>(ld_packed(cols));
+    ptx::grid_begin(static_cast<int64_t>(a.plan.tokens) * cols);
+    const int lane = threadIdx.x & 31, chunks = (cols + 511) / 512, rows = a.plan.words[a.plan.starts() + a.plan.adapters];
     const int64_t all = static_cast<int64_t>(rows) * chunks, step = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t i = blockIdx.x * 8 + threadIdx.x / 32; i < all; i += step) {
         const int row = static_cast<int>(i / chunks), c = static_cast<int>(i % chunks) * 512 + lane * 16;
         if (c >= cols) continue;
         uint32_t v[8];
-        ragged::load16<false>(from + row_at(plan.words[plan.order() + row], ld) + c, cols - c, v);
+        ragged::load16<false>(from + row_at(a.plan.words[a.plan.order() + row], ld) + c, cols - c, v);
         uint4 *p = reinterpret_cast<uint4 *>(to + row_at(row, ld_to) + c);
         p[0] = make_uint4(v[0], v[1], v[2], v[3]);
         p[1] = make_uint4(v[4], v[5], v[6], v[7]);
@@ -343,10 +347,9 @@ __global__ void __launch_bounds__(256) k_lora_pack(LoraPlan plan, const uint16_t
 
 }  // namespace
 
-cudaError_t launch_pack(const LoraPlan &plan, const uint16_t *from, uint32_t ld, int cols, uint16_t *to, cudaStream_t stream) {
-    const int64_t all = static_cast<int64_t>(plan.tokens) * ((cols + 511) / 512);
-    return launch_after(&k_lora_pack, dim3(static_cast<unsigned>(std::min<int64_t>((all + 7) / 8, 8 * kSms))), 256, 0, stream, 1, plan, from, ld, cols,
-                        to, static_cast<uint32_t>(ld_packed(cols)));
+cudaError_t launch_pack(const PackArgs &a, int matrices, cudaStream_t stream) {
+    const int64_t all = static_cast<int64_t>(a.plan.tokens) * ((std::max(a.cols[0], a.cols[1]) + 511) / 512);
+    return launch_after(&k_lora_pack, dim3(static_cast<unsigned>(std::min<int64_t>((all + 7) / 8, 8 * kSms)), matrices), 256, 0, stream, 1, a);
 }
 
 cudaError_t launch_sum(const SumArgs &a, cudaStream_t stream) {
