@@ -37,51 +37,66 @@ __global__ void __launch_bounds__(256) k_lora_prep(const PrepArgs a) {
     const int rank = rank_of(a.lw, tile.adapter), tid = threadIdx.x, r0 = blockIdx.z * 16;
     const float scale = a.lw.scale == nullptr ? 1.0f : a.lw.scale[tile.adapter];
     const int splits = side == 0 ? 0 : shrink_splits(a.plan, tiles, a.long_side, RP);
+    constexpr int H = kLoraTile * 4 / 256;
+    const int c = tid % 4 * 4, r = r0 + c;
+    float v[H][4];
 #pragma unroll
-    for (int h = 0; h < kLoraTile * 4 / 256; ++h) {
-        const int m = (h * 256 + tid) / 4, c = tid % 4 * 4, r = r0 + c;
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (m < tile.count) {
-            if (side == 0) {
-                const float *p = a.v + row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_v) + r;
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (r + e < rank) v[e] = p[e];
-            } else {
-                const float *p = a.dv + (tile.first + m) * static_cast<int64_t>(RP) + r;
-                const int64_t step = static_cast<int64_t>(a.plan.tokens) * RP;
+        for (int e = 0; e < 4; ++e) v[h][e] = 0.0f;
+    auto token = [&](int h) { return (h * 256 + tid) / 4; };
+    if (side == 0) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            if (token(h) >= tile.count) continue;
+            const float *p = a.v + row_at(a.plan.words[a.plan.order() + tile.first + token(h)], a.ld_v) + r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (r + e < rank) v[h][e] = p[e];
+        }
+    } else {
+        const float *p = a.dv + tile.first * static_cast<int64_t>(RP) + r;
+        const int64_t step = static_cast<int64_t>(a.plan.tokens) * RP;
 #pragma unroll 8
-                for (int s = 0; s < splits; ++s) {
-                    const uint4 q = ptx::ld_v4(p + s * step);
-                    v[0] += __uint_as_float(q.x), v[1] += __uint_as_float(q.y);
-                    v[2] += __uint_as_float(q.z), v[3] += __uint_as_float(q.w);
-                }
+        for (int s = 0; s < splits; ++s) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (r + e >= rank) v[e] = 0.0f;
-                if (a.sum != nullptr)
-                    *reinterpret_cast<float4 *>(a.sum + (tile.first + m) * static_cast<int64_t>(RP) + r) = make_float4(v[0], v[1], v[2], v[3]);
+            for (int h = 0; h < H; ++h) {
+                if (token(h) >= tile.count) continue;
+                const uint4 q = ptx::ld_v4(p + s * step + token(h) * RP);
+                v[h][0] += __uint_as_float(q.x), v[h][1] += __uint_as_float(q.y);
+                v[h][2] += __uint_as_float(q.z), v[h][3] += __uint_as_float(q.w);
             }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rows[c + e][m] = v[e] * scale;
+        for (int h = 0; h < H; ++h) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (r + e >= rank) v[h][e] = 0.0f;
+            if (a.sum != nullptr && token(h) < tile.count)
+                *reinterpret_cast<float4 *>(a.sum + (tile.first + token(h)) * static_cast<int64_t>(RP) + r) =
+                    make_float4(v[h][0], v[h][1], v[h][2], v[h][3]);
+        }
     }
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rows[c + e][token(h)] = v[h][e] * scale;
     __syncthreads();
     // eight tokens of a row of r a thread
-    const int r = tid / (kLoraTile / 8), m = tid % (kLoraTile / 8) * 8;
+    const int row = tid / (kLoraTile / 8), m = tid % (kLoraTile / 8) * 8;
     uint32_t w[PARTS][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         uint32_t lo[PARTS], hi[PARTS];
-        split<PARTS>(rows[r][m + 2 * e], lo);
-        split<PARTS>(rows[r][m + 2 * e + 1], hi);
+        split<PARTS>(rows[row][m + 2 * e], lo);
+        split<PARTS>(rows[row][m + 2 * e + 1], hi);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) w[p][e] = lo[p] | hi[p] << 16;
     }
     // as it will stand in shared memory: 64 tokens, a row of 128 bytes for each part and
     // row of r, its 16-byte pieces exchanged as the tensor core's swizzle has it
     uint8_t *to = reinterpret_cast<uint8_t *>(a.vt[side]) + (2 * static_cast<int64_t>(blockIdx.x) + m / 64) * (PARTS * RP * 128) +
-                  (r0 + r) * 128 + ((m % 64 / 8) ^ (r & 7)) * 16;
+                  (r0 + row) * 128 + ((m % 64 / 8) ^ (row & 7)) * 16;
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) *reinterpret_cast<uint4 *>(to + p * RP * 128) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
