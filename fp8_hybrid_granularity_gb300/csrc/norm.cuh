@@ -214,7 +214,7 @@ __device__ __forceinline__ uintptr_t column_address(const void *base, int64_t at
     return reinterpret_cast<uintptr_t>(base) + at * (F32 ? 4 : 2);
 }
 
-template <bool F32, bool WIDE>
+template <bool F32, bool WIDE, bool LINEAR = false>
 __device__ __forceinline__ void copy_columns(uint32_t to, const void *base, int64_t at, int left) {
     constexpr int E = F32 ? 4 : 2;
     const int lane = threadIdx.x & 31, bytes = max(0, min(512, left)) * E;
@@ -223,7 +223,7 @@ __device__ __forceinline__ void copy_columns(uint32_t to, const void *base, int6
     auto piece = [&](int p) {
         // a granule is read whole if a byte of it belongs to the row
         const int n = WIDE ? max(0, min(16, have - 16 * p)) : have > 16 * p ? 16 : 0;
-        ptx::cp_async16(to + segment_at(p), n > 0 ? reinterpret_cast<const void *>(from + 16 * p) : base_granule(base), n);
+        ptx::cp_async16(to + (LINEAR ? 16 * p : segment_at(p)), n > 0 ? reinterpret_cast<const void *>(from + 16 * p) : base_granule(base), n);
     };
 #pragma unroll
     for (int h = 0; h < E; ++h) piece(h * 32 + lane);
@@ -252,6 +252,40 @@ __device__ __forceinline__ void read_columns(uint32_t from, uint32_t shift, int 
                 if (F32) v.w[i] = i < left ? v.w[i] : 0u;
                 else v.w[i] = 2 * i + 1 < left ? v.w[i] : 2 * i < left ? v.w[i] & 0xFFFFu : 0u;
             }
+        }
+    }
+}
+
+// LINEAR granules read back as they lie, every 32nd column a lane: nothing to move into
+// place.  left: columns from the lane's first one on.
+template <bool F32>
+__device__ __forceinline__ void read_lanes(uint32_t from, uint32_t shift, int left, Raw<F32> &v) {
+    constexpr int E = F32 ? 4 : 2;
+    from += shift + (threadIdx.x & 31) * E;
+    if constexpr (F32) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v.w[j] = ptx::ld_shared_u32(from + j * 32 * E);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.w[j] = ptx::ld_shared_u16(from + 2 * j * 32 * E) | ptx::ld_shared_u16(from + (2 * j + 1) * 32 * E) << 16;
+    }
+    // the last granule also holds what is behind the row
+    if (left <= 15 * 32) {
+#pragma unroll
+        for (int j = 0; j < (F32 ? 16 : 8); ++j) {
+            if (F32) v.w[j] = j * 32 < left ? v.w[j] : 0u;
+            else v.w[j] = (2 * j + 1) * 32 < left ? v.w[j] : 2 * j * 32 < left ? v.w[j] & 0xFFFFu : 0u;
+        }
+    }
+}
+// Every 32nd column of a row from at on.
+__device__ __forceinline__ void store_lanes(void *base, int f32, int64_t at, int left, const F2 (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float u = j & 1 ? v[j / 2].hi() : v[j / 2].lo();
+        if (j * 32 < left) {
+            if (f32) static_cast<float *>(base)[at + j * 32] = u;
+            else static_cast<uint16_t *>(base)[at + j * 32] = static_cast<uint16_t>(ptx::cvt_bf16x2(u, 0.0f));
         }
     }
 }

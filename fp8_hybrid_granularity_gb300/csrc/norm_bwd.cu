@@ -29,11 +29,13 @@ namespace {
 
 using namespace norm;
 
-// Sixteen columns' sums of dw and db of one row after the other into `sums`.
+// Sixteen columns' sums of dw and db of one row after the other into `sums`: neighbours,
+// or a warp's width apart.
+template <int STEP = 1>
 __device__ __forceinline__ void gather(float *sums, int cols, int c0, bool first, const F2 (&dw)[8], const F2 (&db)[8]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const int c = c0 + i;
+        const int c = c0 + i * STEP;
         if (c < cols) {
             const float vw = i & 1 ? dw[i / 2].hi() : dw[i / 2].lo();
             const float vb = i & 1 ? db[i / 2].hi() : db[i / 2].lo();
@@ -131,13 +133,18 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormBwdArgs a, int tpr) 
 template <bool XF32, bool DF32, bool WIDE, int THREADS>
 struct Ring {
     static constexpr int R = XF32 || DF32 || !WIDE || THREADS > 256 ? 1 : 2;
-    static constexpr int STAGES = R == 1 && (THREADS == 256 || !(XF32 || DF32)) ? 3 : 2;
+    static constexpr int CTAS = THREADS <= 320 ? 2 : 1;
+    static constexpr int STAGES = R == 1 && THREADS != 320 && (THREADS == 256 || !(XF32 || DF32)) ? 3 : 2;
+    // rows at odd addresses: a lane has every 32nd of the warp's 512 columns, which need no
+    // moving into place (FP32 x, 8192 x 5001: 94 us, 133 with sixteen neighbours; BF16 71
+    // and 88)
+    static constexpr int STEP = WIDE ? 1 : 32;
     static constexpr int X = kSegment<XF32, WIDE>, D = kSegment<DF32, WIDE>;     // bytes of a warp's columns
     static constexpr int bytes(int warps, bool add) { return STAGES * R * (X + D + (add ? X : 0)) * warps; }
 };
 
 template <bool XF32, bool DF32, bool WIDE, int THREADS>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS) k_norm_bwd_ring(const NormBwdArgs a, int tpr) {
+__global__ void __launch_bounds__(THREADS, Ring<XF32, DF32, WIDE, THREADS>::CTAS) k_norm_bwd_ring(const NormBwdArgs a, int tpr) {
     using S = Ring<XF32, DF32, WIDE, THREADS>;
     constexpr int R = S::R;
     extern __shared__ float4 shared[];     // the rings, w; after the last row the sums, [2][cols], of several rows at a time
@@ -145,7 +152,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) k_norm_bwd_ring(const 
     ptx::grid_begin(static_cast<int64_t>(a.rows) * a.cols);
     RowReduce row(red, tpr);
     const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, warps = blockDim.x / 32, rpb = blockDim.x / tpr * R;
-    const int c0 = t * 16, cols_left = a.cols - c0, w0 = t / 32 * 512;
+    constexpr int STEP = S::STEP;
+    const int w0 = t / 32 * 512, c0 = STEP == 1 ? t * 16 : w0 + threadIdx.x % 32, cols_left = a.cols - c0;
     const uint32_t rows = a.rows, step = gridDim.x * rpb;
     const float inv_n = 1.0f / static_cast<float>(a.cols);
     const bool with_add = a.add != nullptr;
@@ -158,9 +166,9 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) k_norm_bwd_ring(const 
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int left = r + i < rows ? a.cols - w0 : 0;
-            copy_columns<XF32, WIDE>(slot(stage, i), a.x, row_at(r + i, a.ld_x) + w0, left);
-            copy_columns<DF32, WIDE>(slot(stage, i) + S::X, a.dy, row_at(r + i, a.ld_dy) + w0, left);
-            if (with_add) copy_columns<XF32, WIDE>(slot(stage, i) + S::X + S::D, a.add, row_at(r + i, a.ld_add) + w0, left);
+            copy_columns<XF32, WIDE, !WIDE>(slot(stage, i), a.x, row_at(r + i, a.ld_x) + w0, left);
+            copy_columns<DF32, WIDE, !WIDE>(slot(stage, i) + S::X, a.dy, row_at(r + i, a.ld_dy) + w0, left);
+            if (with_add) copy_columns<XF32, WIDE, !WIDE>(slot(stage, i) + S::X + S::D, a.add, row_at(r + i, a.ld_add) + w0, left);
         }
         ptx::cp_async_commit();
     };
@@ -174,7 +182,23 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) k_norm_bwd_ring(const 
     float *w = reinterpret_cast<float *>(shared) + S::STAGES * R * warps * set / 4;
     if (group == 0) {
         F2 v[8];
-        load_params(a.weight, a.param_f32, 1.0f, c0, cols_left, v);
+        if constexpr (STEP == 1) {
+            load_params(a.weight, a.param_f32, 1.0f, c0, cols_left, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                F2 one[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = c0 + (2 * j + e) * STEP;
+                    one[e] = f2(c >= a.cols ? 0.0f
+                                : a.weight == nullptr ? 1.0f
+                                : a.param_f32 ? static_cast<const float *>(a.weight)[c]
+                                              : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(a.weight)[c]) << 16));
+                }
+                v[j] = f2(one[0].lo(), one[1].lo());
+            }
+        }
         keep_params(w, t, tpr, v);
     }
     __syncthreads();
@@ -191,8 +215,14 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) k_norm_bwd_ring(const 
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int here = r + i < rows ? cols_left : 0;
-            read_columns<XF32, WIDE>(slot(stage, i), column_address<XF32>(a.x, row_at(r + i, a.ld_x)) & 15, here, x[i]);
-            read_columns<DF32, WIDE>(slot(stage, i) + S::X, column_address<DF32>(a.dy, row_at(r + i, a.ld_dy)) & 15, here, dy[i]);
+            const uint32_t shift_x = column_address<XF32>(a.x, row_at(r + i, a.ld_x)) & 15, shift_d = column_address<DF32>(a.dy, row_at(r + i, a.ld_dy)) & 15;
+            if constexpr (WIDE) {
+                read_columns<XF32, true>(slot(stage, i), shift_x, here, x[i]);
+                read_columns<DF32, true>(slot(stage, i) + S::X, shift_d, here, dy[i]);
+            } else {
+                read_lanes<XF32>(slot(stage, i), shift_x, here, x[i]);
+                read_lanes<DF32>(slot(stage, i) + S::X, shift_d, here, dy[i]);
+            }
             mean[i] = st[0][i].x, rstd[i] = st[0][i].y;
         }
 #pragma unroll
@@ -228,8 +258,11 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) k_norm_bwd_ring(const 
             const F2 mg = f2(-sums[2 * i] * inv_n), mgx = f2(-sums[2 * i + 1] * inv_n), rs = f2(rstd[i]);
             Raw<XF32> add;
             add.zero();
-            if (with_add)
-                read_columns<XF32, WIDE>(slot(stage, i) + S::X + S::D, column_address<XF32>(a.add, row_at(r + i, a.ld_add)) & 15, cols_left, add);
+            if (with_add) {
+                const uint32_t shift = column_address<XF32>(a.add, row_at(r + i, a.ld_add)) & 15;
+                if constexpr (WIDE) read_columns<XF32, true>(slot(stage, i) + S::X + S::D, shift, cols_left, add);
+                else read_lanes<XF32>(slot(stage, i) + S::X + S::D, shift, cols_left, add);
+            }
             F2 dx[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -241,7 +274,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) k_norm_bwd_ring(const 
                     dx[2 * j + e] = fma2(rs, fma2(xh, mgx, add2(g, mg)), add.pair(2 * j + e));
                 }
             }
-            store_values<WIDE>(a.dx, XF32, row_at(r + i, a.ld_dx) + c0, r + i < rows ? cols_left : 0, dx);
+            if constexpr (!WIDE) store_lanes(a.dx, XF32, row_at(r + i, a.ld_dx) + c0, r + i < rows ? cols_left : 0, dx);
+            else store_values<WIDE>(a.dx, XF32, row_at(r + i, a.ld_dx) + c0, r + i < rows ? cols_left : 0, dx);
         }
         __syncwarp();
         copy(r + S::STAGES * step, stage);
@@ -251,13 +285,18 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) k_norm_bwd_ring(const 
     if (a.ws == nullptr) return;
     float *part = a.ws + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
     if (blockDim.x == tpr) {
-        store_values<false>(part, 1, c0, cols_left, dw);
-        store_values<false>(part, 1, a.cols + c0, cols_left, db);
+        if constexpr (!WIDE) {
+            store_lanes(part, 1, c0, cols_left, dw);
+            store_lanes(part, 1, a.cols + c0, cols_left, db);
+        } else {
+            store_values<false>(part, 1, c0, cols_left, dw);
+            store_values<false>(part, 1, a.cols + c0, cols_left, db);
+        }
         return;
     }
     __syncthreads();
     for (int q = 0; q < static_cast<int>(blockDim.x) / tpr; ++q) {
-        if (group == q) gather(w, a.cols, c0, q == 0, dw, db);
+        if (group == q) gather<STEP>(w, a.cols, c0, q == 0, dw, db);
         __syncthreads();
     }
     for (int c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) part[c] = w[c];
@@ -382,11 +421,16 @@ __global__ void __launch_bounds__(512) k_norm_sums(const float *ws, int parts, i
     }
 }
 
+// BF16 rows of 4097 to 5120 columns: 320 threads at 96 registers, two CTAs an SM, where
+// the rows cover the second CTA's partial sums (8192 x 5008: 55 us instead of 66, 1500 x
+// 4608 21 instead of 19; FP32 spills: 92 instead of 81).
+bool pairs(int threads, int64_t rows, bool bf16) { return bf16 && threads > 256 && threads <= 320 && rows >= 2048; }
 // Rows of partial sums for dw and db: CTAs of the kernel that makes them.
-int norm_parts(int64_t rows, int64_t cols) {
+int norm_parts(int64_t rows, int64_t cols, bool bf16) {
     if (cols > kRegCols) return static_cast<int>(std::min<int64_t>((rows + kColRows - 1) / kColRows, 32));
     const Shape s = shape_of(cols);
-    return static_cast<int>(std::min<int64_t>((rows + s.rpb - 1) / s.rpb, kSms * std::max(1, 512 / (s.tpr * s.rpb))));
+    const int threads = s.tpr * s.rpb, ctas = pairs(threads, rows, bf16) ? 2 : std::max(1, 512 / threads);
+    return static_cast<int>(std::min<int64_t>((rows + s.rpb - 1) / s.rpb, kSms * ctas));
 }
 
 constexpr size_t kMostSmem = 226 * 1024;
@@ -404,6 +448,10 @@ template <bool XF32, bool DF32, bool WIDE>
 cudaError_t run_rows(const NormBwdArgs &a, const Shape &s, int parts, cudaStream_t stream) {
     const int threads = s.tpr * s.rpb, warps = threads / 32;
     const size_t rest = (s.rpb > 1 ? 2 : 1) * 16 * sizeof(float) * s.tpr;   // at most 32 KB
+    if constexpr (!XF32 && !DF32) {
+        if (pairs(threads, a.rows, true))
+            return run_ring<false, false, WIDE, 320>(a, s, parts, rest + Ring<false, false, WIDE, 320>::bytes(warps, a.add != nullptr), stream);
+    }
     const size_t rings = threads <= 256 ? Ring<XF32, DF32, WIDE, 256>::bytes(warps, a.add != nullptr)
                                         : Ring<XF32, DF32, WIDE, 512>::bytes(warps, a.add != nullptr);
     if (rest + rings > kMostSmem) return launch_after(&k_norm_bwd<XF32, DF32, WIDE>, dim3(parts), threads, rest, stream, 1, a, s.tpr);
@@ -413,7 +461,7 @@ cudaError_t run_rows(const NormBwdArgs &a, const Shape &s, int parts, cudaStream
 
 template <bool XF32, bool DF32>
 cudaError_t run(const NormBwdArgs &a, cudaStream_t stream) {
-    const int parts = norm_parts(a.rows, a.cols);
+    const int parts = norm_parts(a.rows, a.cols, !XF32 && !DF32);
     cudaError_t e;
     if (a.cols > kRegCols) {
         // dw and db first: dx may be dy or x
@@ -433,7 +481,7 @@ cudaError_t run(const NormBwdArgs &a, cudaStream_t stream) {
 }  // namespace
 
 size_t norm_bwd_ws_bytes(int64_t rows, int64_t cols) {
-    return static_cast<size_t>(norm_parts(rows, cols)) * 2 * static_cast<size_t>(cols) * sizeof(float);
+    return static_cast<size_t>(norm_parts(rows, cols, true)) * 2 * static_cast<size_t>(cols) * sizeof(float);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t stream) {

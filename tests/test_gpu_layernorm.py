@@ -147,6 +147,20 @@ def test_backward(cuda_lib, rows, cols, xt, dt, pt, with_add):
     assert torch.equal(only, dx) and none is None
 
 
+@pytest.mark.parametrize("rows,cols", [(2100, 5001), (2050, 4104), (2048, 5120), (2500, 301), (700, 5123), (1300, 1027)])
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("with_add", [False, True])
+def test_backward_of_many_rows(cuda_lib, rows, cols, kind, with_add):
+    """Many rows a CTA, even and odd ones, all of one type."""
+    x, dy = values(rows, cols, kind), values(rows, cols, kind, seed=3, shift=0.01)
+    w = params(cols, BF16)[0]
+    add = values(rows, cols, kind, seed=4) if with_add else None
+    _, stats = cuda_lib.layernorm(x, w)
+    for got, (want, tol), t, what in zip(cuda_lib.layernorm_bwd(dy, x, w, stats, add=add), ref.norm_bwd(dy, x, w, stats, add), (kind, F32, F32),
+                                         ("dx", "dw", "db")):
+        ref.close(got, want, tol + ref.half_step(t) * want.abs() * 1.01 + 1e-37, what)
+
+
 @pytest.mark.parametrize("pad", [1, 4, 8, 16, 37])
 @pytest.mark.parametrize("xt", [BF16, F32])
 def test_backward_strides(cuda_lib, xt, pad):
