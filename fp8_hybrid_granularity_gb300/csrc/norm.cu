@@ -69,13 +69,21 @@ __device__ __forceinline__ void emit(const NormArgs &a, int q_kind, uint32_t r, 
         a.s[row_at(r, a.ld_s) + (q_kind == Q_ROW ? 0 : c0 >> 7)] = static_cast<uint8_t>(byte);
 }
 
+// The first of a thread's sixteen columns: neighbours, or (LANES) every 32nd of its warp's.
+template <bool LANES>
+__device__ __forceinline__ int first_column(int t) { return LANES ? t / 32 * 512 + t % 32 : t * 16; }
+
 // The parameters to shared memory, by the first group of threads.
+template <bool LANES>
 __device__ __forceinline__ void keep_both(const NormArgs &a, int group, int t, int tpr, float *w, float *b) {
     if (group == 0) {
+        const int c0 = first_column<LANES>(t), left = a.cols - c0;
         F2 v[8];
-        load_params(a.weight, a.param_f32, 1.0f, t * 16, a.cols - t * 16, v);
+        if constexpr (LANES) load_params_lanes(a.weight, a.param_f32, 1.0f, c0, left, v);
+        else load_params(a.weight, a.param_f32, 1.0f, c0, left, v);
         keep_params(w, t, tpr, v);
-        load_params(a.bias, a.param_f32, 0.0f, t * 16, a.cols - t * 16, v);
+        if constexpr (LANES) load_params_lanes(a.bias, a.param_f32, 0.0f, c0, left, v);
+        else load_params(a.bias, a.param_f32, 0.0f, c0, left, v);
         keep_params(b, t, tpr, v);
     }
     __syncthreads();
@@ -84,10 +92,10 @@ __device__ __forceinline__ void keep_both(const NormArgs &a, int group, int t, i
 // R rows at a time from their values in registers: the mean, the differences, rstd,
 // y and where it goes.  The rows' sums share shuffles and a barrier, and their
 // parameters are read from shared memory once.
-template <bool WIDE, int R>
+template <bool WIDE, int R, bool LANES = false>
 __device__ __forceinline__ void finish(const NormArgs &a, int q_kind, uint32_t r, int t, int tpr, float inv_n, RowReduce &row, const float *w,
                                        const float *b, F2 (&d)[R][8], float (&mean)[R], float (&rstd)[R]) {
-    const int c0 = t * 16, cols_left = a.cols - c0;
+    const int c0 = first_column<LANES>(t), cols_left = a.cols - c0;
     const uint32_t rows = a.rows;
     const float n = static_cast<float>(a.cols);
 #pragma unroll
@@ -99,7 +107,8 @@ __device__ __forceinline__ void finish(const NormArgs &a, int q_kind, uint32_t r
         const F2 m = f2(-mean[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[i][j] = add2(d[i][j], m);
-        cut(d[i], cols_left);
+        if constexpr (LANES) cut_lanes(d[i], cols_left);
+        else cut(d[i], cols_left);
         F2 sq = mul2(d[i][0], d[i][0]), sp = mul2(d[i][1], d[i][1]);
 #pragma unroll
         for (int j = 2; j < 8; j += 2) {
@@ -127,12 +136,18 @@ __device__ __forceinline__ void finish(const NormArgs &a, int q_kind, uint32_t r
             d[i][2 * j + 1] = fma2(mul2(d[i][2 * j + 1], s), w1, b1);
         }
     }
-    float amax[R];
+    if constexpr (LANES) {      // y alone
 #pragma unroll
-    for (int i = 0; i < R; ++i) amax[i] = q_kind == Q_ROW ? max_of(d[i]) : 0.0f;
-    if (q_kind == Q_ROW) row.max(amax);
+        for (int i = 0; i < R; ++i)
+            if (a.y != nullptr) store_lanes(a.y, a.y_f32, row_at(r + i, a.ld_y) + c0, r + i < rows ? cols_left : 0, d[i]);
+    } else {
+        float amax[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) emit<WIDE>(a, q_kind, r + i, c0, r + i < rows ? cols_left : 0, amax[i], d[i]);
+        for (int i = 0; i < R; ++i) amax[i] = q_kind == Q_ROW ? max_of(d[i]) : 0.0f;
+        if (q_kind == Q_ROW) row.max(amax);
+#pragma unroll
+        for (int i = 0; i < R; ++i) emit<WIDE>(a, q_kind, r + i, c0, r + i < rows ? cols_left : 0, amax[i], d[i]);
+    }
 }
 
 template <bool XF32, bool WIDE>
@@ -150,7 +165,7 @@ __global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr, int q_k
     next.zero();
     if (r < rows && cols_left > 0) next.template load<WIDE>(a.x, row_at(r, a.ld_x) + c0, cols_left);
     float *w = reinterpret_cast<float *>(params), *b = w + 16 * tpr;
-    keep_both(a, group, t, tpr, w, b);
+    keep_both<false>(a, group, t, tpr, w, b);
     for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
         F2 d[1][8];
         float mean[1], rstd[1];
@@ -162,7 +177,7 @@ __global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr, int q_k
 }
 
 // Many rows: R at a time, through shared memory, the next ones' copies in flight.
-template <bool XF32, bool WIDE, int R>
+template <bool XF32, bool WIDE, int R, bool LANES>
 __global__ void __launch_bounds__(512) k_norm_ring(const NormArgs a, int tpr, int q_kind) {
     constexpr int X = kSegment<XF32, WIDE>, STAGES = 2;     // bytes of a warp's columns
     extern __shared__ float4 params[];    // w, b, the rings
@@ -178,13 +193,13 @@ __global__ void __launch_bounds__(512) k_norm_ring(const NormArgs a, int tpr, in
     auto copy = [&](uint32_t r, int stage) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            copy_columns<XF32, WIDE>(ring + (stage * R + i) * warps * X, a.x, row_at(r + i, a.ld_x) + w0, r + i < rows ? a.cols - w0 : 0);
+            copy_columns<XF32, WIDE, LANES>(ring + (stage * R + i) * warps * X, a.x, row_at(r + i, a.ld_x) + w0, r + i < rows ? a.cols - w0 : 0);
         ptx::cp_async_commit();
     };
     uint32_t r = blockIdx.x * rpb + group * R;
 #pragma unroll
     for (int k = 0; k < STAGES; ++k) copy(r + k * step, k);
-    keep_both(a, group, t, tpr, w, b);
+    keep_both<LANES>(a, group, t, tpr, w, b);
     int stage = 0;
     for (uint32_t r0 = blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
         ptx::cp_async_wait<STAGES - 1>();
@@ -194,15 +209,17 @@ __global__ void __launch_bounds__(512) k_norm_ring(const NormArgs a, int tpr, in
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             Raw<XF32> x;
-            read_columns<XF32, WIDE>(ring + (stage * R + i) * warps * X, column_address<XF32>(a.x, row_at(r + i, a.ld_x)) & 15,
-                                     r + i < rows ? a.cols - t * 16 : 0, x);
+            const uint32_t from = ring + (stage * R + i) * warps * X, shift = column_address<XF32>(a.x, row_at(r + i, a.ld_x)) & 15;
+            const int left = r + i < rows ? a.cols - first_column<LANES>(t) : 0;
+            if constexpr (LANES) read_lanes<XF32>(from, shift, left, x);
+            else read_columns<XF32, WIDE>(from, shift, left, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[i][j] = x.pair(j);
         }
         __syncwarp();
         copy(r + STAGES * step, stage);
         stage ^= 1;
-        finish<WIDE>(a, q_kind, r, t, tpr, inv_n, row, w, b, d, mean, rstd);
+        finish<WIDE, R, LANES>(a, q_kind, r, t, tpr, inv_n, row, w, b, d, mean, rstd);
     }
     ptx::cp_async_wait<0>();
 }
@@ -279,22 +296,33 @@ __global__ void __launch_bounds__(512) k_norm_long(const NormArgs a, int q_kind)
 
 // Copies ahead pay off where every CTA, two an SM, has two sets of rows at least
 // (16384 x 3584 with codes: 47 us with them, 57 without).  BF16 rows of more than 4096
-// columns would leave room for one CTA an SM (8192 x 4999: 62 us instead of 57).
+// columns would leave room for one CTA an SM (8192 x 4999 with codes: 62 us instead of
+// 57).  Rows at odd addresses without codes: every 32nd column a lane, one row at a time
+// from 4096 columns on, three CTAs an SM where it holds them (BF16, 8192 x 4999: 52 us,
+// 59 with sixteen neighbours a lane; 8192 x 7999 80 and 97; FP32 61 and 69, 109 and 125).
+template <bool XF32, bool WIDE, int R, bool LANES>
+cudaError_t run_ring(const NormArgs &a, const Shape &s, int q_kind, cudaStream_t stream) {
+    constexpr int kWarpBytes = 2 * R * kSegment<XF32, WIDE>;
+    static unsigned long long done;
+    const int threads = s.tpr * s.rpb;
+    const size_t smem = 2 * 16 * sizeof(float) * s.tpr + kWarpBytes * (threads / 32);
+    const cudaError_t e = with_smem(&k_norm_ring<XF32, WIDE, R, LANES>, smem, 64 * 1024 + kWarpBytes * 16, done);
+    if (e != cudaSuccess) return e;
+    const int sets = (a.rows + s.rpb * R - 1) / (s.rpb * R);
+    return launch_after(&k_norm_ring<XF32, WIDE, R, LANES>, dim3(std::min(sets, kSms * std::max(2, (LANES && R == 1 && !XF32 ? 1024 : 512) / threads))), threads, smem, stream, 1, a, s.tpr,
+                        q_kind);
+}
 template <bool XF32, bool WIDE>
 cudaError_t run(const NormArgs &a, int q_kind, cudaStream_t stream) {
     const Shape s = shape_of(a.cols);
     const int threads = s.tpr * s.rpb;
     const size_t params = 2 * 16 * sizeof(float) * s.tpr;
     constexpr int R = XF32 ? 1 : WIDE ? 4 : 2;
-    if (threads <= (XF32 ? 512 : 256) && a.rows >= 4 * R * s.rpb * kSms) {
-        constexpr int kWarpBytes = 2 * R * kSegment<XF32, WIDE>;
-        static unsigned long long done;
-        const size_t smem = params + kWarpBytes * (threads / 32);
-        const cudaError_t e = with_smem(&k_norm_ring<XF32, WIDE, R>, smem, 64 * 1024 + kWarpBytes * 16, done);
-        if (e != cudaSuccess) return e;
-        const int sets = (a.rows + s.rpb * R - 1) / (s.rpb * R);
-        return launch_after(&k_norm_ring<XF32, WIDE, R>, dim3(std::min(sets, 2 * kSms)), threads, smem, stream, 1, a, s.tpr, q_kind);
+    if constexpr (!WIDE) {
+        if (q_kind == Q_NONE && threads <= 256 && a.rows >= 4 * R * s.rpb * kSms) return run_ring<XF32, false, R, true>(a, s, q_kind, stream);
+        if (q_kind == Q_NONE && threads > 256 && a.rows >= 4 * kSms) return run_ring<XF32, false, 1, true>(a, s, q_kind, stream);
     }
+    if (threads <= (XF32 ? 512 : 256) && a.rows >= 4 * R * s.rpb * kSms) return run_ring<XF32, WIDE, R, false>(a, s, q_kind, stream);
     static unsigned long long done;
     const cudaError_t e = with_smem(&k_norm<XF32, WIDE>, params, 2 * 16 * sizeof(float) * 512, done);
     if (e != cudaSuccess) return e;

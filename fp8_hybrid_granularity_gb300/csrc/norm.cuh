@@ -71,6 +71,14 @@ __device__ __forceinline__ void cut(F2 (&v)[8], int left) {
     }
 }
 
+// The same of every 32nd column.
+__device__ __forceinline__ void cut_lanes(F2 (&v)[8], int left) {
+    if (left <= 15 * 32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = f2(j * 64 < left ? v[j].lo() : 0.0f, j * 64 + 32 < left ? v[j].hi() : 0.0f);
+    }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -277,6 +285,17 @@ __device__ __forceinline__ void read_lanes(uint32_t from, uint32_t shift, int le
             else v.w[j] = (2 * j + 1) * 32 < left ? v.w[j] : 2 * j * 32 < left ? v.w[j] & 0xFFFFu : 0u;
         }
     }
+}
+// Every 32nd parameter from column c0 on.
+__device__ __forceinline__ void load_params_lanes(const void *p, int f32, float none, int c0, int left, F2 (&v)[8]) {
+    auto value = [&](int j) {
+        return j * 32 >= left ? 0.0f
+               : p == nullptr ? none
+               : f32 ? static_cast<const float *>(p)[c0 + j * 32]
+                     : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[c0 + j * 32]) << 16);
+    };
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f2(value(2 * j), value(2 * j + 1));
 }
 // Every 32nd column of a row from at on.
 __device__ __forceinline__ void store_lanes(void *base, int f32, int64_t at, int left, const F2 (&v)[8]) {

@@ -182,23 +182,8 @@ __global__ void __launch_bounds__(THREADS, Ring<XF32, DF32, WIDE, THREADS>::CTAS
     float *w = reinterpret_cast<float *>(shared) + S::STAGES * R * warps * set / 4;
     if (group == 0) {
         F2 v[8];
-        if constexpr (STEP == 1) {
-            load_params(a.weight, a.param_f32, 1.0f, c0, cols_left, v);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                F2 one[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c = c0 + (2 * j + e) * STEP;
-                    one[e] = f2(c >= a.cols ? 0.0f
-                                : a.weight == nullptr ? 1.0f
-                                : a.param_f32 ? static_cast<const float *>(a.weight)[c]
-                                              : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(a.weight)[c]) << 16));
-                }
-                v[j] = f2(one[0].lo(), one[1].lo());
-            }
-        }
+        if constexpr (WIDE) load_params(a.weight, a.param_f32, 1.0f, c0, cols_left, v);
+        else load_params_lanes(a.weight, a.param_f32, 1.0f, c0, cols_left, v);
         keep_params(w, t, tpr, v);
     }
     __syncthreads();

@@ -77,6 +77,26 @@ def test_fp8(cuda_lib, rows, cols, group, fmt, with_y):
     ref.close(got, want, tol, "codes")
 
 
+MANY = [(5200, 96), (5200, 301), (1300, 1027), (2500, 2051), (2500, 3584), (700, 5001), (700, 8191)]
+
+
+@pytest.mark.parametrize("rows,cols", MANY)
+@pytest.mark.parametrize("xt,yt", [(BF16, BF16), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_many_rows(cuda_lib, rows, cols, xt, yt, pad):
+    """Many rows a CTA, whole tensors and slices."""
+    if pad:
+        test_strides(cuda_lib, rows, cols, xt, yt, pad)
+    else:
+        test_forward(cuda_lib, rows, cols, xt, yt, F32)
+
+
+@pytest.mark.parametrize("rows,cols", MANY)
+@pytest.mark.parametrize("group", [0, 128])
+def test_fp8_of_many_rows(cuda_lib, rows, cols, group):
+    test_fp8(cuda_lib, rows, cols, group, 0, True)
+
+
 def test_fp8_feeds_the_product(cuda_lib):
     """The codes are an operand of the FP8 product, as fp8_quant_token's are."""
     x = values(256, 512, BF16)
