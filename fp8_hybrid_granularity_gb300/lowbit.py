@@ -363,7 +363,7 @@ def _scratch(n, x, stream):
     third of such a call's time on the host); under stream capture, where the
     graph may outlive them, and above that they are allocated."""
     if n > _SCRATCH or torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(n, dtype=torch.uint8, device=x.device)
+        return _new((n,), (1,), torch.uint8)      # x is on the current device
     kept = _scratch_of.__dict__
     key = (x.get_device(), stream)
     t = kept.get(key)
