@@ -11,11 +11,11 @@
 
 namespace fp8hg {
 
-// Dynamic shared memory beyond 48 KB is asked for once per kernel and device, as
-// much as any of its launches takes.
+// Shared memory beyond 48 KB, a kernel's own (16 KB at most here) included, is asked for
+// once per kernel and device, as much as any of its launches takes.
 template <class K>
 cudaError_t with_smem(K kern, size_t bytes, size_t most, unsigned long long &done) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
+    if (bytes <= 32 * 1024) return cudaSuccess;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -1,4 +1,8 @@
 """Layer norm, forward and backward, against 64 bits."""
+import pathlib
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -220,6 +224,31 @@ def test_in_place(cuda_lib, cols, kind):
     assert all(torch.equal(p, q) for p, q in zip(cuda_lib.layernorm_bwd(over, x, w, stats, out=over), want))
     over = x.clone()
     assert all(torch.equal(p, q) for p, q in zip(cuda_lib.layernorm_bwd(dy, over, w, stats, out=over), want))
+
+
+def test_every_width_in_a_new_process(cuda_lib):
+    """A kernel's first call in a process asks for what its shared memory takes, whatever
+    its width: from narrow to wide, so that no wider one came before."""
+    code = """
+import torch
+import fp8_hybrid_granularity_gb300 as lib
+for cols in range(256, 8193, 256):
+    for kind in (torch.bfloat16, torch.float32):
+        for rows in (2, 5000):
+            for n in (cols - 1, cols):
+                x = torch.ones(rows, n, dtype=kind, device="cuda")
+                y, stats = lib.layernorm(x)
+                assert (y == 0).all(), (rows, n, kind)
+                if kind == torch.bfloat16:
+                    lib.fp8_layernorm(x)
+                dx, dw, db = lib.layernorm_bwd(x, x, None, stats)
+                assert (db == rows).all(), (rows, n, kind)
+                lib.layernorm_bwd(x, x, None, stats, add=x)
+torch.cuda.synchronize()
+"""
+    root = pathlib.Path(__file__).resolve().parent.parent
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_gradient_by_differences(cuda_lib):
