@@ -9,9 +9,9 @@
 //
 // 8192 x 18944, r 16, BF16: 105 us for 620 MB, 87 % of the copy rate (loads straight
 // into registers: 186 us for the whole call, now 131).  8192 x 1536, r 64: 24.5 us for
-// 50 MB: a CTA has some ten steps there, behind a chain of reads (tile, tokens, rows
-// of r) that nothing covers.  Looking the next tile up meanwhile costs registers and
-// gains 2.5 us there, but loses 2 us of 10 for one token.
+// 50 MB: a CTA has five steps of 2.5 us there, behind a chain of reads (tile, tokens, rows
+// of r) that nothing covers.  Looking the next tile up meanwhile costs registers: it
+// gains 2.5 us there, but loses 2 us of 17 in a call of 500 tokens.
 #pragma once
 #include <cuda_runtime.h>
 
