@@ -66,6 +66,22 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
         const int rank = none ? 0 : rank_of(a.lw, tile.adapter);
         const float scale = none ? 0.0f : a.lw.scale == nullptr ? 1.0f : a.lw.scale[tile.adapter];
         const uint16_t *w = a.w + (none ? 0 : tile.adapter) * a.stride_w;
+        // the rows of r, the first of their sums: asked for before the tokens are known
+        const float *vp = a.rows + (tile.first + warp * 16 + g) * static_cast<int64_t>(RP) + 2 * t;
+        const int64_t next = static_cast<int64_t>(a.plan.tokens) * RP;
+        float v[2][2 * S::KS][2];
+        bool in_v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            in_v[i] = warp * 16 + i * 8 + g < tile.count && rank > 0;
+#pragma unroll
+            for (int ks = 0; ks < 2 * S::KS; ++ks) {
+                uint2 q = make_uint2(0u, 0u);
+                if (in_v[i]) q = ptx::ld_v2(vp + i * 8 * RP + ks * 8);
+                v[i][ks][0] = __uint_as_float(q.x);
+                v[i][ks][1] = __uint_as_float(q.y);
+            }
+        }
         int token[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -126,16 +142,9 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
         }
 
         uint32_t f[S::PARTS][S::KS][4];
-        // the rows of r: partial sums in their order, U splits' loads in flight
+        // partial sums in their order, U splits' loads in flight
         constexpr int U = S::KS <= 4 ? 8 / S::KS : 1;
-        float v[2][2 * S::KS][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int ks = 0; ks < 2 * S::KS; ++ks) v[i][ks][0] = v[i][ks][1] = 0.0f;
-        const float *vp = a.rows + (tile.first + warp * 16 + g) * static_cast<int64_t>(RP) + 2 * t;
-        const int64_t next = static_cast<int64_t>(a.plan.tokens) * RP;
-        for (int s0 = 0; s0 < splits && active && rank > 0; s0 += U) {
+        for (int s0 = 1; s0 < splits && active && rank > 0; s0 += U) {
             uint2 q[U][2][2 * S::KS];
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -144,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, Shape<RP, TRANS, F32, WIDE>::CTAS) k
 #pragma unroll
                     for (int ks = 0; ks < 2 * S::KS; ++ks) {
                         q[u][i][ks] = make_uint2(0u, 0u);
-                        if (s0 + u < splits && token[i] >= 0) q[u][i][ks] = ptx::ld_v2(vp + (s0 + u) * next + i * 8 * RP + ks * 8);
+                        if (s0 + u < splits && in_v[i]) q[u][i][ks] = ptx::ld_v2(vp + (s0 + u) * next + i * 8 * RP + ks * 8);
                     }
 #pragma unroll
             for (int u = 0; u < U; ++u)
