@@ -211,7 +211,7 @@ cudaError_t launch_shrink(const ShrinkArgs &a, bool trans, cudaStream_t stream);
 // Rows that TMA does not take (of a number of columns that is no multiple of 8) are
 // copied once, in the plan's order, to rows of ld_packed values: read by three
 // kernels, they would be put together from 16-byte pieces by every one of them
-// (8192 x 8961 x 3583, r 16, backward: 857 us, with the copies 211).
+// (8192 x 8961 x 3583, r 16, backward: 857 us, with the copies 198).
 __host__ __device__ constexpr int64_t ld_packed(int64_t cols) { return (cols + 63) / 64 * 64; }
 inline size_t packed_bytes(int64_t tokens, int64_t cols) {
     return cols % 8 ? static_cast<size_t>(tokens) * ld_packed(cols) * sizeof(uint16_t) : 0;
