@@ -196,10 +196,10 @@ def layernorm_bwd(dy, x, weight, stats, add=None, out=None, params: bool = True)
         dw, db = _new((cols,), (1,), torch.float32), _new((cols,), (1,), torch.float32)
         n = _bytes("fp8hg_layernorm_bwd_workspace", rows, cols)
         if n:
-            ws = lowbit._scratch(n, x, stream).data_ptr()
+            ws = lowbit._scratch(n, x, stream)        # held until the call returns
     _check((_bound or _fns()).fp8hg_layernorm_bwd(dy.data_ptr(), kind_dy, ld_dy, x.data_ptr(), kind, ld_x, rows, cols, w, kind_p,
                                                   stats.data_ptr(), _address(add), ld_add, out.data_ptr(), ld_dx, _address(dw),
-                                                  _address(db), ws, n, stream), "layernorm_bwd")
+                                                  _address(db), _address(ws), n, stream), "layernorm_bwd")
     return out, dw, db
 
 
@@ -294,9 +294,9 @@ def lora_add(base, x, adapters: LoraAdapters, plan: LoraPlan, out=None, keep: bo
     v = _new((tokens, w.r), (w.r, 1), torch.float32) if keep else None
     stream = lowbit._raw_stream(device)
     n = _bytes("fp8hg_lora_workspace", tokens, w.adapters, w.r, w.k)
-    ws = lowbit._scratch(n, x, stream).data_ptr() if n else None
+    ws = lowbit._scratch(n, x, stream) if n else None        # held until the call returns
     _check((_bound or _fns()).fp8hg_lora_add(ctypes.byref(w), p, tokens, x.data_ptr(), ld_x, _address(base), ld_base, out.data_ptr(), ld,
-                                             kind, _address(v), w.r, ws, n, stream), "lora_add")
+                                             kind, _address(v), w.r, _address(ws), n, stream), "lora_add")
     return out, v
 
 
@@ -335,8 +335,8 @@ def lora_add_bwd(dy, x, v, adapters: LoraAdapters, plan: LoraPlan, base=None, ou
         db = _new((w.adapters, w.n, w.r), (w.n * w.r, w.r, 1), params_dtype)
     stream = lowbit._raw_stream(device)
     n = _bytes("fp8hg_lora_bwd_workspace", tokens, w.adapters, w.r, w.n, w.k)
-    ws = lowbit._scratch(n, dy, stream).data_ptr() if n else None
+    ws = lowbit._scratch(n, dy, stream) if n else None        # held until the call returns
     _check((_bound or _fns()).fp8hg_lora_add_bwd(ctypes.byref(w), p, tokens, dy.data_ptr(), ld_dy, _address(x) if params else None, ld_x,
                                                  _address(v) if params else None, ld_v, _address(base), ld_base, out.data_ptr(), ld, kind,
-                                                 _address(da), _address(db), dw_kind, ws, n, stream), "lora_add_bwd")
+                                                 _address(da), _address(db), dw_kind, _address(ws), n, stream), "lora_add_bwd")
     return out, da, db

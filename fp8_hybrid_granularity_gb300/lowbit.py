@@ -265,8 +265,8 @@ def fp4_tensor_scale(x, out=None):
     out = out if out is not None else _new((1,), (1,), torch.float32)
     n = f.fp4_tensor_scale_workspace()
     stream = _on(x)
-    _check(f.fp4_tensor_scale(x.data_ptr(), rows, cols, ld, _ts(out),
-                              _scratch(n, x, stream).data_ptr(), n, stream), "fp4_tensor_scale")
+    workspace = _scratch(n, x, stream)        # held until the call returns
+    _check(f.fp4_tensor_scale(x.data_ptr(), rows, cols, ld, _ts(out), workspace.data_ptr(), n, stream), "fp4_tensor_scale")
     return out
 
 
