@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int m = m0 + 4 * e;
-            row[e] = m < tile.count ? a.x + row_at(a.plan.words[a.plan.order() + tile.first + m], a.ld_x) + k0 + piece * 8 : nullptr;
+            const int at = tile.first + m;
+            row[e] = m < tile.count ? a.x + row_at(a.packed ? at : a.plan.words[a.plan.order() + at], a.ld_x) + k0 + piece * 8 : nullptr;
         }
         // pieces of W: rows of r, or of the long side
         const int rank = rank_of(a.lw, tile.adapter), tid = threadIdx.x, wc = tid % S::P * 8;
