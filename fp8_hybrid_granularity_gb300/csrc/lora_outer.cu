@@ -295,17 +295,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c < o.n) {
                 if (begin >= t0 && end <= t1) {
                     const int64_t to = tile.adapter * o.stride_g + c * o.stride_n + r0 * o.stride_r;
-                    const int have = a.lw.r - r0;
+                    // past the rank zeros, not products of zeros with what d holds
+                    const int have = min(S::SUMS, a.lw.r - r0), used = rank_of(a.lw, tile.adapter) - r0;
                     if (a.f32) {
                         float *p = static_cast<float *>(o.out) + to;
+                        for (int i = max(0, used); i < have; ++i) p[i * o.stride_r] = 0.0f;
 #pragma unroll
                         for (int i = 0; i < S::SUMS; ++i, p += o.stride_r)
-                            if (i < have) *p = sum[i];
+                            if (i < used) *p = sum[i];
                     } else {
                         uint16_t *p = static_cast<uint16_t *>(o.out) + to;
+                        for (int i = max(0, used); i < have; ++i) p[i * o.stride_r] = 0;
 #pragma unroll
                         for (int i = 0; i < S::SUMS; ++i, p += o.stride_r)
-                            if (i < have) *p = static_cast<uint16_t>(ptx::cvt_bf16x2(sum[i], 0.0f));
+                            if (i < used) *p = static_cast<uint16_t>(ptx::cvt_bf16x2(sum[i], 0.0f));
                     }
                 } else {
                     float *part = o.ws + ((2 * static_cast<int64_t>(blockIdx.y) + (begin < t0 ? 0 : 1)) * o.n + c) * RP + r0;
@@ -382,9 +385,10 @@ __global__ void __launch_bounds__(256) k_lora_join(const OuterArgs a, int rp) {
         const int begin = tile_first[g], end = tile_first[g + 1];
         const int c0 = begin / per, c1 = begin < end ? (end - 1) / per : c0;
         if (begin < end && c0 == c1) continue;
+        const int rank = rank_of(a.lw, g);
         for (int64_t b = static_cast<int64_t>(blockIdx.x) * 32; b < o.n; b += static_cast<int64_t>(gridDim.x) * 32) {
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (begin < end && r0 + tx < a.lw.r) {
+            if (begin < end && r0 + tx < rank) {      // zeros past the rank
                 const int64_t slot = static_cast<int64_t>(o.n) * rp;
                 const float *p = o.ws + (2 * static_cast<int64_t>(c0) + 1) * slot + (b + ty) * rp + r0 + tx;
                 // the first chunk's, then one of each chunk after it
