@@ -93,17 +93,16 @@ __device__ __forceinline__ void keep_both(const NormArgs &a, int group, int t, i
 // y and where it goes.  The rows' sums share shuffles and a barrier, and their
 // parameters are read from shared memory once.
 template <bool WIDE, int R, bool LANES = false>
-__device__ __forceinline__ void finish(const NormArgs &a, int q_kind, uint32_t r, int t, int tpr, float inv_n, RowReduce &row, const float *w,
+__device__ __forceinline__ void finish(const NormArgs &a, int q_kind, uint32_t r, int t, int tpr, RowReduce &row, const float *w,
                                        const float *b, F2 (&d)[R][8], float (&mean)[R], float (&rstd)[R]) {
     const int c0 = first_column<LANES>(t), cols_left = a.cols - c0;
     const uint32_t rows = a.rows;
     const float n = static_cast<float>(a.cols);
 #pragma unroll
     for (int i = 0; i < R; ++i) mean[i] = total(d[i]);
-    row.sum(mean);
+    row.sum(mean, [n](float s) { return s / n; });
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        mean[i] = divide(mean[i], n, inv_n);
         const F2 m = f2(-mean[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[i][j] = add2(d[i][j], m);
@@ -118,10 +117,9 @@ __device__ __forceinline__ void finish(const NormArgs &a, int q_kind, uint32_t r
         sq = add2(sq, sp);
         rstd[i] = sq.lo() + sq.hi();
     }
-    row.sum(rstd);
+    row.sum(rstd, [n, eps = a.eps](float s) { return __frsqrt_rn(s / n + eps); });
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        rstd[i] = __frsqrt_rn(divide(rstd[i], n, inv_n) + a.eps);
         if (a.stats != nullptr && t == 0 && r + i < rows) reinterpret_cast<float2 *>(a.stats)[r + i] = make_float2(mean[i], rstd[i]);
     }
 #pragma unroll
@@ -159,7 +157,6 @@ __global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr, int q_k
     const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, rpb = blockDim.x / tpr;
     const int c0 = t * 16, cols_left = a.cols - c0;
     const uint32_t rows = a.rows, step = gridDim.x * rpb;
-    const float inv_n = 1.0f / static_cast<float>(a.cols);
     uint32_t r = blockIdx.x * rpb + group;
     Raw<XF32> next;
     next.zero();
@@ -172,7 +169,7 @@ __global__ void __launch_bounds__(512) k_norm(const NormArgs a, int tpr, int q_k
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[0][j] = next.pair(j);
         if (r + step < rows && cols_left > 0) next.template load<WIDE>(a.x, row_at(r + step, a.ld_x) + c0, cols_left);
-        finish<WIDE>(a, q_kind, r, t, tpr, inv_n, row, w, b, d, mean, rstd);
+        finish<WIDE>(a, q_kind, r, t, tpr, row, w, b, d, mean, rstd);
     }
 }
 
@@ -187,7 +184,6 @@ __global__ void __launch_bounds__(512) k_norm_ring(const NormArgs a, int tpr, in
     const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, rpb = blockDim.x / tpr * R, warps = blockDim.x / 32;
     const int w0 = t / 32 * 512;
     const uint32_t rows = a.rows, step = gridDim.x * rpb;
-    const float inv_n = 1.0f / static_cast<float>(a.cols);
     float *w = reinterpret_cast<float *>(params), *b = w + 16 * tpr;
     const uint32_t ring = ptx::smem_u32(b + 16 * tpr) + threadIdx.x / 32 * X;
     auto copy = [&](uint32_t r, int stage) {
@@ -219,7 +215,7 @@ __global__ void __launch_bounds__(512) k_norm_ring(const NormArgs a, int tpr, in
         __syncwarp();
         copy(r + STAGES * step, stage);
         stage ^= 1;
-        finish<WIDE, R, LANES>(a, q_kind, r, t, tpr, inv_n, row, w, b, d, mean, rstd);
+        finish<WIDE, R, LANES>(a, q_kind, r, t, tpr, row, w, b, d, mean, rstd);
     }
     ptx::cp_async_wait<0>();
 }
@@ -232,7 +228,6 @@ __global__ void __launch_bounds__(512) k_norm_long(const NormArgs a, int q_kind)
     ptx::grid_wait();
     const int tpr = blockDim.x;
     RowReduce row(red, tpr);
-    const float inv_n = 1.0f / static_cast<float>(a.cols);
     const uint32_t rows = a.rows;
     for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const int64_t at = row_at(r, a.ld_x);
@@ -249,7 +244,7 @@ __global__ void __launch_bounds__(512) k_norm_long(const NormArgs a, int q_kind)
             piece(c0, v);
             s += total(v);
         }
-        const float n = static_cast<float>(a.cols), mean = divide(row.sum(s), n, inv_n);
+        const float n = static_cast<float>(a.cols), mean = row.sum(s) / n;
         s = 0.0f;
         for (int64_t c0 = first; c0 < a.cols; c0 += pass) {
             F2 v[8];
@@ -261,7 +256,7 @@ __global__ void __launch_bounds__(512) k_norm_long(const NormArgs a, int q_kind)
             for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], v[i]);
             s += total(v);
         }
-        const float rstd = __frsqrt_rn(divide(row.sum(s), n, inv_n) + a.eps);
+        const float rstd = __frsqrt_rn(row.sum(s) / n + a.eps);
         if (a.stats != nullptr && threadIdx.x == 0) reinterpret_cast<float2 *>(a.stats)[r] = make_float2(mean, rstd);
         auto value = [&](int64_t c0, F2 (&v)[8]) {
             const int left = static_cast<int>(a.cols - c0);

@@ -85,33 +85,33 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// s / n, correctly rounded but for the last unit: a quotient that is off the same way in
-// every row shows in the codes that come out of it.
-__device__ __forceinline__ float divide(float s, float n, float inv_n) {
-    const float q = s * inv_n, e = fmaf(fmaf(-q, n, s), inv_n, q);
-    return fabsf(q) <= 3.4e38f ? e : q;
-}
-
 __device__ __forceinline__ float total(const F2 (&v)[8]) {
     const F2 a = add2(add2(v[0], v[1]), add2(v[2], v[3])), b = add2(add2(v[4], v[5]), add2(v[6], v[7]));
     const F2 s = add2(a, b);
     return s.lo() + s.hi();
 }
 
+// A sum as it is.
+struct Same {
+    __device__ __forceinline__ float operator()(float s) const { return s; }
+};
+
 // One, two or four sums (or a maximum) over the threads of a row: `warps` whole
 // warps, at most 16.  Every thread of the CTA calls them in step; two buffers in
-// turn, so that one barrier for each set is enough.
+// turn, so that one barrier for each set is enough.  `then`: what is wanted of a sum,
+// taken once in the lanes that add it up, before all threads get it.
 struct RowReduce {
     float (*buf)[32][4];     // [2] of a warp's four values
     int warps, first, turn;
     __device__ __forceinline__ RowReduce(float (*b)[32][4], int tpr)
         : buf(b), warps(tpr / 32), first(threadIdx.x / tpr * (tpr / 32)), turn(0) {}
 
-    // The row's from the warps': lane l has value l / (32 / N) of warp l % (32 / N).
-    template <int N, bool MAX>
-    __device__ __forceinline__ void across(float (&v)[N]) {
+    // The row's from the warps': lane l has value l / (32 / N) of warp l % W, and every
+    // lane a sum that is wanted (a division by the way of zeros takes longer).
+    template <int N, bool MAX, class F = Same>
+    __device__ __forceinline__ void across(float (&v)[N], F then = F()) {
         constexpr int W = 32 / N < 16 ? 32 / N : 16;
-        const int lane = threadIdx.x & 31, at = lane % (32 / N);
+        const int lane = threadIdx.x & 31, at = lane % W;
         __syncthreads();
         const float (*t)[4] = buf[turn] + first;
         turn ^= 1;
@@ -125,14 +125,18 @@ struct RowReduce {
             const float u = __shfl_xor_sync(0xFFFFFFFFu, a, o);
             a = MAX ? max3_abs(a, a, u) : a + u;
         }
+        a = then(a);
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, a, i * (32 / N));
     }
-    __device__ __forceinline__ float sum(float a) {
+    template <class F = Same>
+    __device__ __forceinline__ float sum(float a, F then = F()) {
         float v[1] = {warp_sum(a)};
         if (warps > 1) {
             if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x / 32][0] = v[0];
-            across<1, false>(v);
+            across<1, false>(v, then);
+        } else {
+            v[0] = then(v[0]);
         }
         return v[0];
     }
@@ -144,21 +148,24 @@ struct RowReduce {
         }
         return v[0];
     }
-    __device__ __forceinline__ void sum(float (&v)[2]) {
+    template <class F = Same>
+    __device__ __forceinline__ void sum(float (&v)[2], F then = F()) {
         const bool up = threadIdx.x & 16;
         float a = (up ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[1], 16);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
         if (warps > 1) {
             if ((threadIdx.x & 15) == 0) buf[turn][threadIdx.x / 32][(threadIdx.x >> 4) & 1] = a;
-            across<2, false>(v);
+            across<2, false>(v, then);
         } else {
+            a = then(a);
             v[0] = __shfl_sync(0xFFFFFFFFu, a, 0);
             v[1] = __shfl_sync(0xFFFFFFFFu, a, 16);
         }
     }
     // four: halves, then quarters of the warp take over one value each
-    __device__ __forceinline__ void sum(float (&v)[4]) {
+    template <class F = Same>
+    __device__ __forceinline__ void sum(float (&v)[4], F then = F()) {
         const int lane = threadIdx.x & 31;
         const bool up = lane & 16, odd = lane & 8;
         float a = (up ? v[2] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
@@ -168,13 +175,17 @@ struct RowReduce {
         for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
         if (warps > 1) {
             if ((lane & 7) == 0) buf[turn][threadIdx.x / 32][lane >> 3] = a;
-            across<4, false>(v);
+            across<4, false>(v, then);
         } else {
+            a = then(a);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, a, 8 * i);
         }
     }
-    __device__ __forceinline__ void sum(float (&v)[1]) { v[0] = sum(v[0]); }
+    template <class F = Same>
+    __device__ __forceinline__ void sum(float (&v)[1], F then = F()) {
+        v[0] = sum(v[0], then);
+    }
     __device__ __forceinline__ void max(float (&v)[1]) { v[0] = max(v[0]); }
     template <int N>
     __device__ __forceinline__ void max(float (&v)[N]) {
@@ -185,7 +196,7 @@ struct RowReduce {
         }
         if (warps > 1) across<N, true>(v);
     }
-    __device__ __forceinline__ float2 sum(float a, float b) {
+    __device__ __forceinline__ float2 both(float a, float b) {
         float v[2] = {a, b};
         sum(v);
         return make_float2(v[0], v[1]);

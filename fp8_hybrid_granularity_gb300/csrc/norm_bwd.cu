@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormBwdArgs a, int tpr) 
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = mul2(g[i], xh[i]);
-        const float2 s = row.sum(total(g), total(p));
+        const float2 s = row.both(total(g), total(p));
         const F2 mg = f2(-s.x * inv_n), mgx = f2(-s.y * inv_n);
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = fma2(f2(rstd), fma2(xh[i], mgx, add2(g[i], mg)), add.pair(i));
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd_long(const NormBwdArgs a) {
             sg += total(g);
             sgx += total(p);
         }
-        const float2 s = row.sum(sg, sgx);
+        const float2 s = row.both(sg, sgx);
         const F2 mg = f2(-s.x * inv_n), mgx = f2(-s.y * inv_n);
         for (int64_t c0 = first; c0 - (threadIdx.x & 31) * 16 < a.cols; c0 += pass) {
             const int left = static_cast<int>(a.cols - c0);
