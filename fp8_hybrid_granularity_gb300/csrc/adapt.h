@@ -11,6 +11,12 @@
 
 namespace fp8hg {
 
+// The SMs that work is dealt out to: a GB300's, not the device's count, because
+// workspaces are functions of sizes alone, without a device, and because the host's
+// grids and the device's splits of the adapters' sums have to agree.  Another number of
+// SMs leaves results right and a round of CTAs less full.
+constexpr int kSms = 152;
+
 // Shared memory beyond 48 KB, a kernel's own (16 KB at most here) included, is asked for
 // once per kernel and device, as much as any of its launches takes.
 template <class K>

@@ -36,7 +36,6 @@
 namespace fp8hg {
 namespace lora {
 
-constexpr int kSms = 152;
 constexpr uint64_t kWaitNs = 2000000000ull;      // of a warp for another one of its CTA
 
 // A tile of the plan.

@@ -323,7 +323,6 @@ __device__ __forceinline__ void store_lanes(void *base, int f32, int64_t at, int
 // How a row is dealt out where it fits the registers: threads a row (whole
 // warps), rows a CTA.
 constexpr int kRegCols = 8192;
-constexpr int kSms = 152;
 struct Shape {
     int tpr, rpb;
 };
