@@ -149,7 +149,9 @@ def fp8_layernorm(x, weight=None, bias=None, eps: float = 1e-5, group: int = 0, 
     """The layer norm of x as the A operand of an FP8 product, quantized from FP32
     like fp8_quant_token: one UE8M0 scale per token (group=0) or per 128 columns
     (128; any number of columns, the last group may be shorter).  with_y=True also
-    gives y in BF16, from the same read: QTensor, y or None, stats."""
+    gives y in BF16, from the same read: QTensor, y or None, stats.  Any number of
+    rows and columns is quantized; fp8_gemm_scaled takes an operand whose rows and
+    columns are multiples of 128, so x of a batch that feeds it is padded to them."""
     device = lowbit._cuda_device()
     shape, ld, kind = _matrix(x, "x", _EITHER, device)
     rows, cols = shape

@@ -11,12 +11,12 @@
 // Tokens come in tiles of up to 128 of one adapter, gathered through the plan's
 // order.  x, dy, A and B are BF16 and their products exact; sums are FP32.  The
 // tensor core cuts its sums off instead of rounding them, which all lean the same
-// way (measured, relative to the result: 4.8e-7 after 32 sums of 16 products, 7e-7
-// after 48, 1e-6 after 64, 2.5e-6 after 148): shrink deals its steps out to several
-// sums, 48 of 16 each at most, outer takes its sums out after 32 and adds them up in
-// registers, expand's are of r <= 128 products.  v and dv, FP32 sums, enter the next
-// product as two BF16 parts (16 bits of them, for results in BF16) or three (24 bits,
-// for FP32).
+// way (measured, relative to the result, of random signs: 4.8e-7 after 32 sums of 16
+// products, 7e-7 after 48, 1e-6 after 64, 2.5e-6 after 148; of one sign 9e-7 after 32,
+// 1.2e-6 after 48): shrink deals its steps out to several sums, 48 of 16 each at most,
+// outer takes its sums out after 32 and adds them up in registers, expand's are of
+// r <= 128 products.  v and dv, FP32 sums, enter the next product as two BF16 parts (16
+// bits of them, for results in BF16) or three (24 bits, for FP32).
 //
 // 2 r operations per value of x, dy or y and r small: HBM is the bound.  Shrink and
 // outer feed tcgen05 by TMA where a tile's tokens are neighbours and by asynchronous
@@ -161,7 +161,7 @@ struct TileCopy {
 constexpr int kShrinkCols = 64;
 constexpr int kMaxSplits = 16;
 // Sums in tensor memory that steps take turns at, and the most steps at each: 48 sums
-// of 16, each cut off, are off by some 7e-7 of the result (64: 1e-6).
+// of 16, each cut off, are off by some 7e-7 of the result (64: 1e-6; of one sign 1.2e-6).
 __host__ __device__ constexpr int shrink_sums(int rp) { return rp <= 64 ? 8 : 4; }
 constexpr int kSumSteps = 12;
 __host__ __device__ inline int split_steps(int64_t steps, int ctas_a_tile, int rp) {

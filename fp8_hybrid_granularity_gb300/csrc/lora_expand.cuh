@@ -2,7 +2,7 @@
 // s_g v[t] W_g^T.
 //
 // All tiles' steps of 64 columns, dealt out evenly to one round of CTAs: a warp
-// takes 16 tokens of the tile, v's fragments in registers.  base, three or four steps
+// takes 16 tokens of the tile, v's fragments in registers.  base, two or three steps
 // ahead in shared memory, is what the products are added to (in BF16; an FP32 base is
 // added after them).  Column 16 t + 2 j + e of a step is column 2 t + e of the
 // fragment j, so that lane t of a row's four has 16 neighbouring columns to store.

@@ -13,7 +13,9 @@
 // after its start: 0.9 for the plan, 0.7 for A and x, 0.8 for the cluster's barrier, 0.2
 // for its sums, 0.9 for the fragments, 0.4 for the last products.  The first step's B and
 // base are on their way before the barrier.  32 clusters (16 of one CTA an SM) start at
-// once; of 38 the last ones wait for the first (8.5 us).
+// once; of 38 the last ones wait for the first (8.5 us).  The cluster's barrier is the
+// hardware's and has no time limit; every thread of a cluster, whose CTAs start together,
+// comes to both of its phases, whatever the plan holds.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -12,7 +12,8 @@
 //
 // 8192 tokens, 8960 + 1536 columns, r 64 in three parts: 39 us for 172 MB, 65 % of the
 // copy rate (rows copied by the warps: 58; mma.sync: 145): 41 blocks of columns by 3
-// chunks keep 123 of the 152 SMs busy.  Rows of r 7, joining 8 to 10.
+// chunks keep 123 of the 152 SMs busy.  Rows of r 7, joining 8.  13 warps leave 128
+// registers a thread: with r 64 and 128 the sums' warps spill 210 to 300 bytes.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -106,7 +107,7 @@ constexpr int kStep = 64;            // tokens
 constexpr int kCopyWarps = 4, kSumWarps = 8;
 constexpr int kThreads = (kCopyWarps + kSumWarps + 1) * 32;
 // Steps whose products stay in tensor memory before they are added up in FP32: 32
-// sums of 16, each cut off, are off by some 4e-7 of the result.
+// sums of 16, each cut off, are off by some 5e-7 of the result, of one sign 9e-7.
 constexpr int kSteps = 8;
 
 template <int RP, int PARTS>

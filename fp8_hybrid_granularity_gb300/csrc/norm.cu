@@ -14,10 +14,15 @@
 // and the parameters in shared memory, where they cost no registers.  Rows of
 // more than 8192 columns are read again for each sum (from the L2).
 //
-// 16384 x 3584, BF16 x: y in BF16 42 us (83 % of the copy rate), codes alone 49 (53 %),
-// both 54; FP32 x and y, 8192 x 3584, 39 (88 %).  With codes the latency of three
-// sums a row and 15 instructions a value bound it, not the bytes.  A warp for a whole
-// row, without any barrier, takes 40, 49 and 55 (codes by groups of 128: 52).
+// 16384 x 3584, BF16 x: y in BF16 43 us (81 % of the copy rate), codes alone 49.5 (53 %;
+// by groups of 128: 50), both 55; FP32 x and y, 8192 x 3584, 43 (81 %).  With codes
+// neither the bytes (36 % of DRAM) nor the instructions (47 % of the SM's rate) bound
+// it but the latency of three sums a row, with 14 warps an SM.  A warp for a whole row,
+// without any barrier, takes 40, 49 and 55 (codes by groups of 128: 52).  The mean and the
+// variance are plain divisions, by the lanes that add a row up: in every thread they
+// take 2 us more of these 43 (a product with 1 / n and its correction, in every
+// thread: 2 us as well).  Rows of more than 8192 columns: 4096 x 12288 164 us for 201 MB,
+// the row read three times without copies ahead.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -15,7 +15,7 @@
 // 16384 x 3584, BF16 x, dy, add and dx: 93 us in a stream of calls for 470 MB, 75 % of
 // the copy rate (rows loaded into registers instead of through shared memory: 99).
 // What is left are the barrier of every pair of rows and the registers of the sums,
-// which leave room for 16 warps an SM.
+// which leave room for 16 warps an SM.  4096 x 12288, in BF16: 230 us for 302 MB.
 #include <cuda_runtime.h>
 
 #include <algorithm>
