@@ -1,5 +1,8 @@
 """The layer norm's and adapters' calls beside one another: threads on one stream and on
-streams of their own, and graphs that share a pool."""
+streams of their own, graphs that share a pool, a first call under capture."""
+import pathlib
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -83,3 +86,38 @@ def test_graphs_of_one_pool(cuda_lib):
         torch.cuda.synchronize()
         for got, w in zip(outs, want):
             assert all(torch.equal(p, q) for p, q in zip(got, w))
+
+
+@pytest.mark.parametrize("call", ["norm", "fp8", "adapters", "few"])
+def test_first_call_of_a_process_captured(cuda_lib, call):
+    """What a kernel's first call looks up and asks for is allowed under capture."""
+    code = f"""
+import torch
+import fp8_hybrid_granularity_gb300 as lib
+x, dy = torch.randn(300, 1000, device="cuda").bfloat16(), torch.randn(300, 512, device="cuda").bfloat16()
+ids = torch.randint(-1, 3, (300,), device="cuda").int()
+w = lib.LoraAdapters(torch.randn(3, 16, 1000, device="cuda").bfloat16(), torch.randn(3, 512, 16, device="cuda").bfloat16())
+def norm():
+    y, stats = lib.layernorm(x)
+    return (y, stats) + lib.layernorm_bwd(x, x, None, stats)
+def fp8():
+    q, y, stats = lib.fp8_layernorm(x, group=128, with_y=True)
+    return q.codes, q.scales(), y, stats
+def adapters():
+    plan = lib.lora_plan(ids, 3)
+    y, v = lib.lora_add(None, x, w, plan, keep=True)
+    return (y, v) + lib.lora_add_bwd(dy, x, v, w, plan)
+def few():
+    return lib.lora_add(None, x[:4], w, lib.lora_plan(ids[:4], 3), keep=True)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = {call}()
+graph.replay()
+want = {call}()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(out, want))
+"""
+    root = pathlib.Path(__file__).resolve().parent.parent
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]

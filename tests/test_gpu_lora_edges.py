@@ -102,3 +102,33 @@ def test_adapters_far_apart(cuda_lib):
     dx, da, db = cuda_lib.lora_add_bwd(s["dy"], s["x"], v, w, plan, params_dtype=BF16)
     check_backward(s, None, v, dx, da[[0, -1]], db[[0, -1]])
     assert not da[1:-1].any() and not db[1:-1].any()
+
+
+@pytest.mark.parametrize("t,n,k,r,g", [(1 << 24, 64, 64, 16, 4096), (1 << 20, 65, 129, 24, 300), (3, 1 << 24, 64, 8, 2), (200, (1 << 21) + 1, 63, 9, 2),
+                                       (3, 64, 1 << 24, 8, 2), (200, 64, 1 << 22, 16, 2)])
+def test_largest_sizes(cuda_lib, t, n, k, r, g):
+    """As many tokens, adapters and columns as a call takes: some rows of y, v and dx, some
+    columns of three adapters' gradients."""
+    s = dict(ids=torch.randint(-1, g, (t,), device="cuda", dtype=torch.int32), ranks=torch.randint(1, r + 1, (g,), device="cuda", dtype=torch.int32),
+             scale=torch.exp(0.3 * rand(5, g)))
+    for name, shape, scale in (("x", (t, k), 1.0), ("dy", (t, n), n ** -0.5), ("a", (g, r, k), k ** -0.5), ("b", (g, n, r), 0.3)):
+        s[name] = scale * torch.randn(*shape, device="cuda", dtype=BF16)
+    plan = cuda_lib.lora_plan(s["ids"], g)
+    w = adapters(cuda_lib, s)
+    y, v = cuda_lib.lora_add(None, s["x"], w, plan, keep=True)
+    dx, da, db = cuda_lib.lora_add_bwd(s["dy"], s["x"], v, w, plan)
+    assert cuda_lib.fp8hg_get_device_error() == 0
+    some = lambda size: torch.cat([torch.arange(0, size, max(1, size // 300), device="cuda"),  # noqa: E731
+                                   torch.arange(max(0, size - 200), size, device="cuda")]).unique()
+    sel, cols, kcols = some(t), some(n), some(k)
+    p = {**s, "x": s["x"][sel], "dy": s["dy"][sel], "ids": s["ids"][sel]}
+    check_forward(p, None, y[sel], v[sel])
+    (wx, mx), _, _ = ref.lora_bwd(p["dy"], p["x"], v[sel].double(), s["a"], s["b"], s["scale"], s["ranks"], p["ids"])
+    ref.close(dx[sel], wx, ref.MMA * mx + (ref.half_step(BF16) + 2 * ref.U) * 1.01 * wx.abs(), "dx")
+    for i in {0, g // 2, g - 1}:
+        rows, m, f = (s["ids"] == i).nonzero().squeeze(1), int(s["ranks"][i]), float(s["scale"][i])
+        va, b, d = v[rows, :m].double(), s["b"][i, :, :m].double(), s["dy"][rows].double()
+        dv, dvm, x, d = f * (d @ b), f * (d.abs() @ b.abs()), s["x"][rows][:, kcols].double(), d[:, cols]
+        for got, want, mag in ((da[i, :m][:, kcols], dv.t() @ x, dvm.t() @ x.abs()), (db[i, cols, :m], f * (d.t() @ va), f * (d.abs().t() @ va.abs()))):
+            ref.close(got, want, ref.MMA * mag + ref.U * want.abs(), "dA or dB")
+        assert not da[i, m:].any() and not db[i, :, m:].any()
